@@ -16,9 +16,17 @@ Calls (same names as the C ABI, without the ``cskv_`` prefix):
     sparse_prefill_attn(...) the same attention for many prompt queries
     decode_layer(...)        one layer's decode step, host buffers in and out
     encode_rows(...)         code rows of values into a cache format
+
+and, from include/cskvx.h (prefix ``cskvx_``), attention over bounded and shared caches:
+
+    window_attn(...)         a sliding window and the first rows of each request
+    prefix_decode_attn(...)  a decode batch whose requests share their first entries
+    attn_weights(...)        each entry's accumulated attention weight
+    evict(...)               cuts each request's entries to a budget by that weight
 """
 
 import ctypes
+import functools
 import math
 
 import numpy as np
@@ -394,6 +402,233 @@ def decode_layer(jobs, q_idx, w, keys, q, main_kv, swa, swa_fmt, ctx_len, k, rat
     st = _lib.lib().cskv_decode_layer(ctypes.byref(a), _stream(stream))
     _check(st, "cskv_decode_layer")
     return out, topk_idx
+
+
+def _shaped(t, shape, name):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+
+
+def _on_stream(f):
+    """Runs f with its `stream` argument (if one is given) current, so that what f allocates for
+    the call belongs to the stream that uses it."""
+    @functools.wraps(f)
+    def g(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return f(*args, stream=stream, **kw)
+    return g
+
+
+def _launch(device, stream, tensors, call):
+    """call(stream handle) with `device` current; every tensor must live there."""
+    import torch
+    for name, t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream must be on %s, got %s" % (device, stream.device))
+    if device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        return call(torch.cuda.current_stream().cuda_stream)
+
+
+def _workspace(workspace, nbytes, device):
+    import torch
+    if workspace is None and nbytes > 0:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _need(workspace, None, "workspace")
+    return workspace, (0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def _query_args(q, out, lse, want_lse, sink, q_rope_cs):
+    """Checks the query side of an attention call; allocates out and lse."""
+    import torch
+    _need(q, torch.bfloat16, "q")
+    _need(sink, torch.float32, "sink")
+    _need(q_rope_cs, torch.float32, "q_rope_cs")
+    _need(out, torch.bfloat16, "out")
+    _need(lse, torch.float32, "lse")
+    if q.dim() != 3 or q.shape[2] != 512:
+        raise ValueError("q must have shape (rows, heads, 512), got %s" % (tuple(q.shape),))
+    T, H, _ = q.shape
+    _shaped(q_rope_cs, (T, 32, 2), "q_rope_cs")
+    _shaped(sink, (H,), "sink")
+    _shaped(out, (T, H, 512), "out")
+    _shaped(lse, (T, H), "lse")
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    return T, H, out, lse
+
+
+def window_attn_workspace_size(T, H, max_ctx_len, window, first):
+    return int(_lib.lib().cskvx_window_attn_workspace_size(T, H, max_ctx_len, window, first))
+
+
+@_on_stream
+def window_attn(q, rows, pos1, window, first, max_ctx_len, sink, softmax_scale, q_rope_cs, req_of=None, out=None,
+                lse=None, want_lse=False, workspace=None, stream=None):
+    """Attention over a sliding window and the first rows: query i (bf16 q [T, H, 512]) of
+    request req_of[i] (None: request i) at position t = pos1[i] - 1 sees the rows j <= t of
+    `rows` (a PagedCache of raw rows by position) with j < first or j > t - window; pos1[i]
+    <= 0: a padding query (out 0).  Returns (out bf16 [T, H, 512], lse fp32 [T, H] or None)."""
+    import torch
+    _need(pos1, torch.int32, "pos1")
+    _need(req_of, torch.int32, "req_of")
+    T, H, out, lse = _query_args(q, out, lse, want_lse, sink, q_rope_cs)
+    _shaped(pos1, (T,), "pos1")
+    _shaped(req_of, (T,), "req_of")
+    reqs = rows.block_table.shape[0] if rows.block_table is not None else (1 << 30)
+    L = _lib.lib()
+    need = window_attn_workspace_size(T, H, int(max_ctx_len), int(window), int(first))
+    workspace, ws_bytes = _workspace(workspace, need, q.device)
+    st = _launch(q.device, stream,
+                 (("rows", rows.pool), ("rows.block_table", rows.block_table), ("pos1", pos1), ("req_of", req_of),
+                  ("sink", sink), ("q_rope_cs", q_rope_cs), ("out", out), ("lse", lse), ("workspace", workspace)),
+                 lambda s: L.cskvx_window_attn(q.data_ptr(), rows.desc(), reqs, _ptr(req_of), pos1.data_ptr(),
+                                               int(window), int(first), int(max_ctx_len), _ptr(sink),
+                                               float(softmax_scale), q_rope_cs.data_ptr(), T, H, out.data_ptr(),
+                                               _ptr(lse), _ptr(workspace), ws_bytes, s))
+    _check(st, "cskvx_window_attn")
+    return out, lse
+
+
+def prefix_decode_attn_workspace_size(B, H, n_prefix, max_entries, with_swa):
+    return int(_lib.lib().cskvx_prefix_decode_attn_workspace_size(B, H, n_prefix, max_entries, int(bool(with_swa))))
+
+
+@_on_stream
+def prefix_decode_attn(q, main_kv, n_entries, n_prefix, max_entries, sink, softmax_scale, q_rope_cs, swa=None,
+                       swa_fmt=FMT_BF16, ctx_len=None, out=None, lse=None, want_lse=False, workspace=None, stream=None):
+    """Decode attention of a batch whose requests share entries [0, n_prefix) (read through
+    request 0's block-table row): request b sees its entries j < n_entries[b] and, with swa
+    (uint8 [B, 128, row bytes] and ctx_len int32 [B]), its window ring.  Returns (out bf16
+    [B, H, 512], lse fp32 [B, H] or None)."""
+    import torch
+    _need(n_entries, torch.int32, "n_entries")
+    _need(swa, torch.uint8, "swa")
+    _need(ctx_len, torch.int32, "ctx_len")
+    B, H, out, lse = _query_args(q, out, lse, want_lse, sink, q_rope_cs)
+    _shaped(n_entries, (B,), "n_entries")
+    if swa is not None:
+        _shaped(swa, (B, WINDOW, row_bytes(swa_fmt, 512)), "swa")
+        _shaped(ctx_len, (B,), "ctx_len")
+    _table_rows(main_kv, B, "main_kv")
+    L = _lib.lib()
+    need = prefix_decode_attn_workspace_size(B, H, int(n_prefix), int(max_entries), swa is not None)
+    workspace, ws_bytes = _workspace(workspace, need, q.device)
+    st = _launch(q.device, stream,
+                 (("main_kv", main_kv.pool), ("main_kv.block_table", main_kv.block_table), ("n_entries", n_entries),
+                  ("swa", swa), ("ctx_len", ctx_len), ("sink", sink), ("q_rope_cs", q_rope_cs), ("out", out),
+                  ("lse", lse), ("workspace", workspace)),
+                 lambda s: L.cskvx_prefix_decode_attn(q.data_ptr(), main_kv.desc(), n_entries.data_ptr(),
+                                                      int(n_prefix), int(max_entries), _ptr(swa), int(swa_fmt),
+                                                      _ptr(ctx_len), _ptr(sink), float(softmax_scale),
+                                                      q_rope_cs.data_ptr(), B, H, out.data_ptr(), _ptr(lse),
+                                                      _ptr(workspace), ws_bytes, s))
+    _check(st, "cskvx_prefix_decode_attn")
+    return out, lse
+
+
+def _table_rows(cache, B, name):
+    if cache.block_table is not None and cache.block_table.shape[0] < B:
+        raise ValueError("%s's block table has %d rows for a batch of %d" % (name, cache.block_table.shape[0], B))
+
+
+@_on_stream
+def attn_weights(q, main_kv, n_entries, max_entries, softmax_scale, q_rope_cs, lse, acc, decay=1.0, first=0,
+                 acc_out=None, stream=None):
+    """acc_out[b, j] = decay * acc[b, j] + sum over heads of exp(z - lse) for the entries
+    first <= j < n_entries[b] (lse as prefix_decode_attn gave it); acc, acc_out fp32 [B, >=
+    max_entries], acc_out None: in place.  Returns acc_out."""
+    import torch
+    _need(q, torch.bfloat16, "q")
+    _need(n_entries, torch.int32, "n_entries")
+    _need(q_rope_cs, torch.float32, "q_rope_cs")
+    _need(lse, torch.float32, "lse")
+    _need(acc, torch.float32, "acc")
+    _need(acc_out, torch.float32, "acc_out")
+    if q.dim() != 3 or q.shape[2] != 512:
+        raise ValueError("q must have shape (rows, heads, 512), got %s" % (tuple(q.shape),))
+    B, H, _ = q.shape
+    _shaped(n_entries, (B,), "n_entries")
+    _shaped(q_rope_cs, (B, 32, 2), "q_rope_cs")
+    _shaped(lse, (B, H), "lse")
+    if acc_out is None:
+        acc_out = acc
+    for t, n in ((acc, "acc"), (acc_out, "acc_out")):
+        if t.dim() != 2 or t.shape[0] != B or t.shape[1] < max_entries:
+            raise ValueError("%s must have shape (%d, at least %d), got %s" % (n, B, max_entries, tuple(t.shape)))
+    _table_rows(main_kv, B, "main_kv")
+    L = _lib.lib()
+    st = _launch(q.device, stream,
+                 (("main_kv", main_kv.pool), ("main_kv.block_table", main_kv.block_table), ("n_entries", n_entries),
+                  ("q_rope_cs", q_rope_cs), ("lse", lse), ("acc", acc), ("acc_out", acc_out)),
+                 lambda s: L.cskvx_attn_weights(q.data_ptr(), main_kv.desc(), n_entries.data_ptr(), int(first),
+                                                int(max_entries), float(softmax_scale), q_rope_cs.data_ptr(),
+                                                lse.data_ptr(), B, H, float(decay), acc.data_ptr(), acc.shape[1],
+                                                acc_out.data_ptr(), acc_out.shape[1], s))
+    _check(st, "cskvx_attn_weights")
+    return acc_out
+
+
+def evict_workspace_size(B, max_entries, budget):
+    return int(_lib.lib().cskvx_evict_workspace_size(B, max_entries, budget))
+
+
+@_on_stream
+def evict(caches, acc, n_entries, budget, fixed=0, recent=0, age=None, max_entries=None, acc_out=None, age_out=None,
+          n_out=None, src=None, workspace=None, stream=None):
+    """Cuts each request's entries to `budget` slots: the first `fixed` slots and the `recent`
+    newest ages stay, then the largest accumulated weights acc (fp32 [B, capacity]); kept
+    entries from slot `budget` on move into the given-up slots of every cache in `caches`.
+    age: int32 [B, capacity] or None (then recent is 0).  acc_out, age_out, n_out None: in
+    place.  max_entries None: acc's capacity.  Returns (src int32 [B, budget], n_out, acc_out,
+    age_out): slot i now holds the entry of slot src[:, i] (-1: none)."""
+    import torch
+    for t, dt, n in ((acc, torch.float32, "acc"), (acc_out, torch.float32, "acc_out"), (age, torch.int32, "age"),
+                     (age_out, torch.int32, "age_out"), (n_entries, torch.int32, "n_entries"),
+                     (n_out, torch.int32, "n_out"), (src, torch.int32, "src")):
+        _need(t, dt, n)
+    if acc.dim() != 2:
+        raise ValueError("acc must have shape (requests, capacity), got %s" % (tuple(acc.shape),))
+    B = acc.shape[0]
+    most = acc.shape[1] if max_entries is None else int(max_entries)
+    budget = int(budget)
+    acc_out = acc if acc_out is None else acc_out
+    age_out = age if age_out is None else age_out
+    n_out = n_entries if n_out is None else n_out
+    kept = min(most, budget)
+    for t, n, w in ((acc, "acc", most), (age, "age", most), (acc_out, "acc_out", kept), (age_out, "age_out", kept)):
+        if t is not None and (t.dim() != 2 or t.shape[0] != B or t.shape[1] < w):
+            raise ValueError("%s must have shape (%d, at least %d), got %s" % (n, B, w, tuple(t.shape)))
+    _shaped(n_entries, (B,), "n_entries")
+    _shaped(n_out, (B,), "n_out")
+    _shaped(src, (B, budget), "src")
+    for c in caches:
+        _table_rows(c, B, "a cache")
+    if src is None:
+        src = torch.empty((B, max(budget, 0)), dtype=torch.int32, device=acc.device)
+    L = _lib.lib()
+    workspace, ws_bytes = _workspace(workspace, evict_workspace_size(B, most, budget), acc.device)
+    arr = (_lib.Paged * max(1, len(caches)))(*[c.desc() for c in caches])
+    tensors = [("acc_out", acc_out), ("age", age), ("age_out", age_out), ("n_entries", n_entries), ("n_out", n_out),
+               ("src", src), ("workspace", workspace)]
+    for c in caches:
+        tensors += [("a cache", c.pool), ("a cache's block table", c.block_table)]
+    st = _launch(acc.device, stream, tensors,
+                 lambda s: L.cskvx_evict(arr, len(caches), acc.data_ptr(), acc.shape[1], _ptr(age),
+                                         0 if age is None else age.shape[1], n_entries.data_ptr(), B, most, budget,
+                                         int(fixed), int(recent), src.data_ptr(), acc_out.data_ptr(),
+                                         acc_out.shape[1], _ptr(age_out), 0 if age_out is None else age_out.shape[1],
+                                         n_out.data_ptr(), _ptr(workspace), ws_bytes, s))
+    _check(st, "cskvx_evict")
+    return src, n_out, acc_out, age_out
 
 
 DEFAULT_SCALE = 1.0 / math.sqrt(512.0)

@@ -1,4 +1,4 @@
-"""ctypes view of libcskv.so (the C ABI declared in include/cskv.h)."""
+"""ctypes view of libcskv.so (the C ABI declared in include/cskv.h and include/cskvx.h)."""
 
 import ctypes
 import os
@@ -135,6 +135,24 @@ SIGNATURES = {
     "cskv_decode_layer": (c_int32, [ctypes.POINTER(DecodeLayerArgs), c_void_p]),
 }
 
+# every symbol include/cskvx.h declares
+EXT_SIGNATURES = {
+    "cskvx_window_attn_workspace_size": (c_size_t, [c_int32, c_int32, c_int32, c_int32, c_int32]),
+    "cskvx_window_attn": (c_int32, [c_void_p, Paged, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32,
+                                    c_void_p, c_float, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                    c_size_t, c_void_p]),
+    "cskvx_prefix_decode_attn_workspace_size": (c_size_t, [c_int32, c_int32, c_int32, c_int32, c_int32]),
+    "cskvx_prefix_decode_attn": (c_int32, [c_void_p, Paged, c_void_p, c_int32, c_int32, c_void_p, c_int32,
+                                           c_void_p, c_void_p, c_float, c_void_p, c_int32, c_int32, c_void_p,
+                                           c_void_p, c_void_p, c_size_t, c_void_p]),
+    "cskvx_attn_weights": (c_int32, [c_void_p, Paged, c_void_p, c_int32, c_int32, c_float, c_void_p, c_void_p,
+                                     c_int32, c_int32, c_float, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "cskvx_evict_workspace_size": (c_size_t, [c_int32, c_int32, c_int32]),
+    "cskvx_evict": (c_int32, [ctypes.POINTER(Paged), c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                              c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_void_p,
+                              c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
+}
+
 _lib = None
 
 
@@ -148,7 +166,7 @@ def lib():
                 "`python -c 'import __graft_entry__ as g; g.build()'` "
                 "(there is no CPU fallback for the decode path)" % LIB_PATH)
         h = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in list(SIGNATURES.items()) + list(EXT_SIGNATURES.items()):
             f = getattr(h, name)
             f.restype = res
             f.argtypes = args

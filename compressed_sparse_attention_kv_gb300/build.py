@@ -11,7 +11,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcskv.so")
-SOURCES = ["cskv_api.cu", "compress.cu", "index_topk.cu", "attention.cu"]
+SOURCES = ["cskv_api.cu", "compress.cu", "index_topk.cu", "attention.cu", "cskvx_api.cu", "list_attn.cu",
+           "evict.cu"]
 HEADERS = ["common.cuh", "codec.cuh", "internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-Xcompiler", "-fvisibility=hidden",
@@ -34,7 +35,7 @@ def _stale(target, deps):
 
 def build(verbose=False, force=False):
     os.makedirs(BUILD, exist_ok=True)
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "cskv.h")]
+    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", h) for h in ("cskv.h", "cskvx.h")]
     objs = []
     jobs = []
     for src in SOURCES:

@@ -237,7 +237,8 @@ int32_t cskv_rope_table(const int64_t* positions, int32_t n, double theta, doubl
 
 int32_t cskv_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return CSKV_ERR_CUDA;
-  const unsigned int bits = take_err_compress() | take_err_index() | take_err_attention();
+  const unsigned int bits = take_err_compress() | take_err_index() | take_err_attention() |
+                            take_err_list_attn() | take_err_evict();
   if (bits & (1u << CSKV_ERR_TIMEOUT)) return CSKV_ERR_TIMEOUT;
   if (bits & (1u << CSKV_ERR_BOUNDS)) return CSKV_ERR_BOUNDS;
   if (bits) return CSKV_ERR_CUDA;

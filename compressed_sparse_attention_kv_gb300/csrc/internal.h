@@ -69,8 +69,32 @@ cudaError_t launch_sparse_prefill_attn(const void* q, const cskv_paged& kv, cons
                                        const float* q_rope, int T, int H, void* out, void* workspace,
                                        cudaStream_t stream);
 
+// include/cskvx.h
+size_t window_attn_workspace_bytes(int T, int H, int max_ctx, int window, int first);
+cudaError_t launch_window_attn(const void* q, const cskv_paged& rows, int num_reqs, const int32_t* req_of,
+                               const int32_t* pos1, int window, int first, int max_ctx, const float* sink, float scale,
+                               const float* q_rope, int T, int H, void* out, float* lse, void* workspace,
+                               cudaStream_t stream);
+size_t prefix_attn_workspace_bytes(int B, int H, int n_prefix, int max_entries, int with_swa);
+cudaError_t launch_prefix_attn(const void* q, const cskv_paged& kv, const int32_t* n_entries, int n_prefix,
+                               int max_entries, const void* swa, int swa_fmt, const int32_t* ctx_len, const float* sink,
+                               float scale, const float* q_rope, int B, int H, void* out, float* lse, void* workspace,
+                               cudaStream_t stream);
+cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32_t* n_entries, int first,
+                                int max_entries, float scale, const float* q_rope, const float* lse, int B, int H,
+                                float decay, const float* acc, long long acc_stride, float* acc_out,
+                                long long acc_out_stride, cudaStream_t stream);
+size_t evict_workspace_bytes(int B, int max_entries, int budget);
+cudaError_t launch_evict(const cskv_paged* caches, int ncaches, const float* acc, long long acc_stride,
+                         const int32_t* age, long long age_stride, const int32_t* n_entries, int B, int max_entries,
+                         int budget, int fixed, int recent, int32_t* src, float* acc_out, long long acc_out_stride,
+                         int32_t* age_out, long long age_out_stride, int32_t* n_out, void* workspace,
+                         cudaStream_t stream);
+
 unsigned int take_err_compress();
 unsigned int take_err_index();
 unsigned int take_err_attention();
+unsigned int take_err_list_attn();
+unsigned int take_err_evict();
 
 }  // namespace cskv
