@@ -14,6 +14,7 @@ int32_t cuda_status(cudaError_t e) { return e == cudaSuccess ? CSKV_OK : CSKV_ER
 
 constexpr unsigned kRowFormats =
     (1u << CSKV_FMT_BF16) | (1u << CSKV_FMT_FP8_E4M3_E8M0_B32) | (1u << CSKV_FMT_FP4_E2M1_E4M3_B16);
+constexpr int kMaxRows = 1 << 30;  // (query, head) rows of a call
 constexpr int kMaxLen = 1 << 30;   // positions and entries: sums of two stay within 32 bits
 
 bool cache_ok(const cskv_paged& c, unsigned formats) {
@@ -31,7 +32,8 @@ bool rows_ok(const cskv_paged& c) { return cache_ok(c, kRowFormats) && c.dim == 
 
 // what the three attention calls share; rows = queries
 int32_t query_check(const void* q, const cskv_paged& kv, float scale, const float* q_rope_cs, int32_t rows, int32_t H) {
-  if (q == nullptr || q_rope_cs == nullptr || rows < 1 || rows > (1 << 24) || H < 1 || H > 128) return CSKV_ERR_INVALID;
+  if (q == nullptr || q_rope_cs == nullptr || rows < 1 || rows > kMaxRows / 128 || H < 1 || H > 128)
+    return CSKV_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(q_rope_cs, 16)) return CSKV_ERR_INVALID;
   if (!(scale > 0.0f) || std::isinf(scale) || !rows_ok(kv)) return CSKV_ERR_INVALID;
   return CSKV_OK;
@@ -46,7 +48,7 @@ bool workspace_ok(const void* w, size_t have, size_t need) {
 extern "C" {
 
 size_t cskvx_window_attn_workspace_size(int32_t T, int32_t H, int32_t max_ctx_len, int32_t window, int32_t first) {
-  if (T < 1 || T > (1 << 24) || H < 1 || H > 128 || max_ctx_len < 0 || window < 1 || first < 0) return 0;
+  if (T < 1 || T > kMaxRows / 128 || H < 1 || H > 128 || max_ctx_len < 0 || window < 1 || first < 0) return 0;
   return window_attn_workspace_bytes(T, H, max_ctx_len, window, first);
 }
 
@@ -68,7 +70,7 @@ int32_t cskvx_window_attn(const void* q, cskv_paged rows, int32_t num_reqs, cons
 
 size_t cskvx_prefix_decode_attn_workspace_size(int32_t B, int32_t H, int32_t n_prefix, int32_t max_entries,
                                                int32_t with_swa) {
-  if (B < 1 || B > (1 << 24) || H < 1 || H > 128 || n_prefix < 0 || max_entries < n_prefix) return 0;
+  if (B < 1 || B > kMaxRows / 128 || H < 1 || H > 128 || n_prefix < 0 || max_entries < n_prefix) return 0;
   return prefix_attn_workspace_bytes(B, H, n_prefix, max_entries, with_swa != 0);
 }
 

@@ -2,8 +2,42 @@
 // accumulated attention weights (cskvx_window_attn, cskvx_prefix_decode_attn,
 // cskvx_attn_weights).
 //
-// One warp per (query, head) row, 16 dims per lane, one pass over the row's keys with
-// a running maximum and sum.
+// The mathematics.  A key row c_j is key and value of every head.  For a (query, head)
+// row r with rotated query q'_r: z_rj = (q'_r . c_j) * scale over the keys the row sees,
+// and out_r = rot^-1(sum_j exp(z_rj) c_j / (sum_j exp(z_rj) + exp(sink))).  The keys are
+// taken in tiles of 128; a running reference m_r (base 2) stands for the maximum, and
+//   l_r <- l_r 2^(m - m') + sum_j 2^(z_rj - m'),  O_r <- O_r 2^(m - m') + sum_j 2^(z_rj - m') c_j
+// where m moves only when a logit exceeds it by more than kSlack: until then the weights
+// stay below 2^kSlack, and O need not be touched.  Parts of a row's keys that different
+// blocks take are joined by attn_join_kernel in a fixed order.
+//
+// What bounds it.  A tile of 128 keys for 64 rows is 33.5 MFLOP on 67 KB of FP8 rows: the
+// tensor core and the shared-memory reads of its operands, with the dequantisation of the
+// tile (65,536 values) beside it; short windows are bound by the queries and outputs.
+//
+// The tiling.  One block holds 64 rows: 64 / H queries of a request (or one query's heads),
+// or 64 consecutive (request, head) rows over a shared prefix.  Both products run with the
+// keys or the dims as the 128 MMA rows and the 64 query rows as the MMA columns:
+//   S^T = K Q^T    (128 keys x 64, K = 512 dims, K-major operands), 64 TMEM columns,
+//   O^T += V^T P^T (4 blocks of 128 dims x 64, K = 128 keys, MN-major operands; V is the
+//                   same shared-memory tile as K), 4 x 64 TMEM columns,
+// since a 512-d fp32 output of 128 rows would take the whole tensor memory.  Few rows need
+// no padding to 128.  The tile lives in eight 16 KiB chunks of 64 dims.  Roles:
+//   warps 0-7   load and rotate the queries, then softmax: a thread has one key and up to
+//               32 rows, straight from TMEM; P^T to shared memory as bf16; the epilogue;
+//   warps 8-15  load rows (several chunks ahead, in registers), dequantise exactly to bf16
+//               and fill a chunk as soon as the O product has released it;
+//   warp 16     one thread issues the MMAs of a chunk as soon as it is full.
+// So a tile's dequantisation overlaps the O product of the tile before it, and S follows
+// chunk by chunk.
+//
+// Roundings: the rotated query is kept as hi + lo, two bf16 numbers (the lo part of the 64
+// rotated dims is a ninth chunk of Q), so that logits and log-sum-exp are fp32-accurate;
+// P is rounded to bf16 (2^-8 relative at most, the operand type of the product); partial
+// outputs, sums and maxima stay fp32.
+#include <algorithm>
+#include <cmath>
+
 #include "codec.cuh"
 #include "internal.h"
 
@@ -12,8 +46,19 @@ namespace cskv {
 namespace {
 
 constexpr int kD = 512;
+constexpr int kKeys = 128;
+constexpr int kRows = 64;
+constexpr int kChunk = kKeys * 128;      // bytes of 64 dims of a tile
+constexpr int kSoftThreads = 256;
+constexpr int kLoadThreads = 256;
+constexpr int kThreads = kSoftThreads + kLoadThreads + 32;
+constexpr int kSoftBarrier = 1;          // named barrier of warps 0-7
+constexpr uint32_t kTmemS = 256;         // TMEM columns: O 0..255, S from here
+constexpr float kSlack = 8.0f;           // base 2: weights stay below 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+enum Kind { kWindowRows, kPrefixEntries, kOwnEntries, kRing };
 
 struct ListArgs {
   const uint8_t* q;
@@ -22,7 +67,7 @@ struct ListArgs {
   const float* sink;
   float scale_log2;
   const float* q_rope;
-  int T, H;
+  int T, H;                  // queries (requests) and heads
   uint8_t* out;
   float* lse;
   // window: queries of requests, raw rows by position
@@ -42,148 +87,1071 @@ struct ListArgs {
   float* acc_out;
   long long acc_out_stride;
   float decay;
+  // the grid's work: row blocks of per-query items, and how often each key list is split
+  int group;                 // queries per block (H <= 64)
+  int head_blocks, heads_per_block;
+  int split, prefix_split, prefix_blocks, own_blocks;
+  int parts;                 // partial outputs of a row (1: written straight to out)
+  float* opart;              // [row][part][512]
+  float* ml;                 // [row][part][2]: m (base 2) and l
+  unsigned long long spin;
 };
 
-// dims 16 l .. 16 l + 15 of a row
-__device__ __forceinline__ void row16(int fmt, const uint8_t* p, int l, float (&v)[16]) {
-  if (fmt == CSKV_FMT_BF16) {
-    for (int i = 0; i < 4; ++i) {
-      const float4 x = load_bf16x4(p + 32 * l + 8 * i);
-      v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+// A stretch of keys that rows of one request share: positions 0 .. f1-1, then base, base+1, ...
+struct Run {
+  int req, f1, base, nkeys, tile0;
+  int q0, q1;                // the block's queries [q0, q1) that belong to it
+  int whole;                 // every row of the block belongs to it
+  int min_f, max_lo, min_hi; // over its rows: positions that all of them see
+};
+
+struct __align__(16) RowSees {   // position p is seen when p < f or lo <= p <= hi
+  int f, lo, hi, run;
+};
+
+struct ListSmem {
+  uint64_t full[8], free_[8], bar_s[2], bar_p[2], bar_q;
+  uint32_t tmem;
+  int abort;
+  int nruns, ntiles;
+  Run runs[kRows];
+  RowSees sees[kRows];
+  __align__(16) float m[kRows];      // running reference, -inf: no key yet
+  __align__(16) float msub[kRows];   // the same, 0 for -inf
+  __align__(16) float fac[kRows];
+  float part[4][2 * kRows];
+  uint32_t kstate[2][kKeys];         // by tile parity; a byte per loading thread: 1 the row exists, 2 it is not finite
+};
+
+// ---------------------------------------------------------------------------
+// small wrappers
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool wait_bar(ListSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(&sm->abort)) return false;
+    if (clock64() - t0 > limit) {   // gave up: every role leaves its loop
+      set_err(CSKV_ERR_TIMEOUT);
+      *reinterpret_cast<volatile int*>(&sm->abort) = 1;
+      return false;
     }
-  } else if (fmt == CSKV_FMT_FP8_E4M3_E8M0_B32) {
-    const float s = exp2i(static_cast<int>(p[kD + (l >> 1)]) - 127);
-    for (int i = 0; i < 16; ++i) v[i] = e4m3_to_f32(p[16 * l + i]) * s;
+  }
+  return true;
+}
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(kSoftBarrier), "n"(kSoftThreads) : "memory");
+}
+__device__ __forceinline__ bool soft_any(bool p) {
+  int r;
+  asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbar.red.or.pred b, %2, %3, a;\n\tselp.s32 %0, 1, 0, b;\n\t}"
+               : "=r"(r) : "r"(static_cast<int>(p)), "n"(kSoftBarrier), "n"(kSoftThreads) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// `count` (16 or 32) columns into v[0..count)
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, int count, float (&v)[32]) {
+  if (count > 16) tmem_ld32(taddr, v);
+  else tmem_ld16(taddr, *reinterpret_cast<float(*)[16]>(v));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+// x * y on two bf16 (rounded to nearest, subnormals kept)
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// rows: 16 dims of a row from its bytes to bf16, exactly
+// ---------------------------------------------------------------------------
+template <int FMT>
+struct Raw;
+template <>
+struct Raw<CSKV_FMT_FP8_E4M3_E8M0_B32> {
+  uint4 c;
+  uint32_t s;
+};
+template <>
+struct Raw<CSKV_FMT_FP4_E2M1_E4M3_B16> {
+  uint2 c;
+  uint32_t s;
+};
+template <>
+struct Raw<CSKV_FMT_BF16> {
+  uint4 a, b;
+};
+
+// 16-dim group g (0..31) of the row at p (nullptr: zeros)
+__device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_FP8_E4M3_E8M0_B32>& r) {
+  r.c = make_uint4(0u, 0u, 0u, 0u);
+  r.s = 127u;
+  if (p != nullptr) {
+    r.c = __ldg(reinterpret_cast<const uint4*>(p + 16 * g));
+    r.s = __ldg(p + kD + (g >> 1));
+  }
+}
+__device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r) {
+  r.c = make_uint2(0u, 0u);
+  r.s = 0u;
+  if (p != nullptr) {
+    r.c = __ldg(reinterpret_cast<const uint2*>(p + 8 * g));
+    r.s = __ldg(p + kD / 2 + g);
+  }
+}
+__device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_BF16>& r) {
+  r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
+  if (p != nullptr) {
+    r.a = __ldg(reinterpret_cast<const uint4*>(p + 32 * g));
+    r.b = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 16));
+  }
+}
+
+// nonzero if one of the two bf16 of w is infinite or NaN (an exponent of all ones carries
+// into the sign bit when its lowest bit is added)
+__device__ __forceinline__ uint32_t unfit_bf16(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// to 8 words of two bf16; returns nonzero if a value is not finite
+__device__ __forceinline__ uint32_t convert(const Raw<CSKV_FMT_BF16>& r, uint32_t (&w)[8]) {
+  w[0] = r.a.x; w[1] = r.a.y; w[2] = r.a.z; w[3] = r.a.w;
+  w[4] = r.b.x; w[5] = r.b.y; w[6] = r.b.z; w[7] = r.b.w;
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bad |= unfit_bf16(w[i]);
+  return bad;
+}
+// e4m3 s.eeee.mmm placed at bf16 bits 15 and 10..4 is the value times 2^-120 (subnormal codes
+// too), so one product by 2^(120 + e) of the block's scale 2^e dequantises; the result has
+// 4 significant bits.  Scales beyond 2^7 take the product in two steps.
+__device__ __forceinline__ uint32_t convert(const Raw<CSKV_FMT_FP8_E4M3_E8M0_B32>& r, uint32_t (&w)[8]) {
+  const uint32_t c[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bad |= ((c[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // a code of S.1111.111
+    const uint32_t lo = __byte_perm(c[i], 0u, 0x1404), hi = __byte_perm(c[i], 0u, 0x3424);
+    w[2 * i] = ((lo >> 4) & 0x07F007F0u) | (lo & 0x80008000u);
+    w[2 * i + 1] = ((hi >> 4) & 0x07F007F0u) | (hi & 0x80008000u);
+  }
+  if (r.s <= 134u) {
+    const uint32_t f = (r.s + 120u) << 7, ff = f | (f << 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], ff);
   } else {
-    const float s = e4m3_to_f32(p[kD / 2 + l]);
+    const uint32_t f = r.s << 7, ff = f | (f << 16);   // 2^(s - 127), infinite for s = 255
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t h;
-      asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-          : "=r"(h) : "r"(static_cast<uint32_t>(p[8 * l + i])));
-      v[2 * i] = __half2float(__ushort_as_half(h & 0xFFFF)) * s;
-      v[2 * i + 1] = __half2float(__ushort_as_half(h >> 16)) * s;
+      w[i] = mul_bf16x2(mul_bf16x2(w[i], 0x7B807B80u), ff);
+      bad |= unfit_bf16(w[i]);
     }
   }
+  return bad;
+}
+// e2m1 times the e4m3 scale is exact in fp16 (6 significant bits, 2^-10 .. 2688); fp16
+// s.eeeee.m(10) moved down three bits is a bf16 of the value times 2^-112.
+__device__ __forceinline__ uint32_t convert(const Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r, uint32_t (&w)[8]) {
+  uint32_t s2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(static_cast<uint16_t>(r.s | (r.s << 8))));
+  const uint32_t c[2] = {r.c.x, r.c.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h;
+      asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(c[i] >> (8 * j)));
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(s2));
+      w[4 * i + j] = mul_bf16x2(((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u), 0x77807780u);
+    }
+  }
+  return (r.s & 0x7Fu) == 0x7Fu ? 1u : 0u;
 }
 
-struct RowState {
-  float q[16], o[16], m, l;
+// ---------------------------------------------------------------------------
+// a block's work
+// ---------------------------------------------------------------------------
+struct Item {
+  int kind;
+  int fmt, row_bytes;
+  cskv_paged pages;
+  int r0, nr;            // rows [r0, r0 + nr) of the [T * H] rows
+  int split, nsplit;     // this block takes the split-th of nsplit shares of the tiles
+  int part;              // its partial output
 };
 
-__device__ __forceinline__ void rotate16(const float* cs, int lane, float sign, float (&v)[16]) {
-  if (lane < 28) return;
-  for (int i = 0; i < 8; ++i) {
-    const int k = 8 * (lane - 28) + i;
-    const float c = cs[2 * k], s = sign * cs[2 * k + 1];
-    const float y0 = v[2 * i], y1 = v[2 * i + 1];
-    v[2 * i] = y0 * c - y1 * s;
-    v[2 * i + 1] = y0 * s + y1 * c;
+__device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
+  Item it;
+  it.fmt = a.kv.fmt;
+  it.row_bytes = a.row_bytes;
+  it.pages = a.kv;
+  it.split = 0;
+  it.nsplit = 1;
+  it.part = 0;
+  const int rows = a.T * a.H;
+  if (a.pos1 != nullptr) {
+    it.kind = kWindowRows;
+    it.nsplit = a.split;
+    it.split = it.part = x % a.split;
+    x /= a.split;
+  } else if (x < a.prefix_blocks * a.prefix_split) {
+    it.kind = kPrefixEntries;
+    it.nsplit = a.prefix_split;
+    it.split = it.part = x % a.prefix_split;
+    it.r0 = x / a.prefix_split * kRows;
+    it.nr = min(kRows, rows - it.r0);
+    return it;
+  } else {
+    x -= a.prefix_blocks * a.prefix_split;
+    const int psplit = a.prefix_blocks > 0 ? a.prefix_split : 0;
+    if (x < a.own_blocks * a.split) {
+      it.kind = kOwnEntries;
+      it.nsplit = a.split;
+      it.split = x % a.split;
+      it.part = psplit + it.split;
+      x /= a.split;
+    } else {
+      x -= a.own_blocks * a.split;
+      it.kind = kRing;
+      it.part = a.parts - 1;
+      it.fmt = a.swa_fmt;
+      it.row_bytes = a.swa_row_bytes;
+    }
   }
+  if (a.head_blocks == 1) {
+    it.r0 = x * a.group * a.H;
+    it.nr = min(a.group * a.H, rows - it.r0);
+  } else {
+    const int h0 = x % a.head_blocks * a.heads_per_block;
+    it.r0 = x / a.head_blocks * a.H + h0;
+    it.nr = min(a.heads_per_block, a.H - h0);
+  }
+  if (it.kind == kRing) {   // the request's ring as a flat array of two pages
+    it.pages.pool = const_cast<uint8_t*>(a.swa) + static_cast<size_t>(it.r0 / a.H) * kWindow * it.row_bytes;
+    it.pages.block_table = nullptr;
+    it.pages.page_bytes = 64 * it.row_bytes;
+    it.pages.num_pages = 2;
+    it.pages.fmt = it.fmt;
+  }
+  return it;
 }
 
-// the key's logit in base 2 (all lanes), its values in v
-__device__ __forceinline__ float logit(const ListArgs& a, int fmt, const uint8_t* p, int lane, const float (&q)[16],
-                                       float (&v)[16]) {
-  row16(fmt, p, lane, v);
-  float z = 0.f;
-  for (int i = 0; i < 16; ++i) z += q[i] * v[i];
-  for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-  bool fine = true;   // a row that is not finite makes its logits NaN
-  for (int i = 0; i < 16; ++i) fine = fine && fabsf(v[i]) < INFINITY;
-  if (!__all_sync(0xFFFFFFFFu, fine)) return __int_as_float(0x7FC00000);
-  return z * a.scale_log2;
-}
-
-__device__ __forceinline__ void attend(const ListArgs& a, int fmt, const uint8_t* p, int lane, RowState& r) {
-  if (p == nullptr) return;
-  float v[16];
-  const float z = logit(a, fmt, p, lane, r.q, v);
-  const float m = fmaxf(r.m, z);
-  const float f = r.m == -INFINITY ? 0.f : exp2f(r.m - m);
-  const float e = exp2f(z - m);
-  r.l = r.l * f + e;
-  for (int i = 0; i < 16; ++i) r.o[i] = r.o[i] * f + e * v[i];
-  r.m = m;
-}
-
-__device__ __forceinline__ void load_query(const ListArgs& a, int t, int h, int lane, float (&q)[16]) {
-  row16(CSKV_FMT_BF16, a.q + (size_t(t) * a.H + h) * kD * 2, lane, q);
-  rotate16(a.q_rope + size_t(t) * 64, lane, 1.f, q);
-}
-
-__device__ __forceinline__ int cut(int n, int most) {
-  if (n > most) { set_err(CSKV_ERR_BOUNDS); n = most; }
+__device__ __forceinline__ int entries_of(const ListArgs& a, int b) {
+  int n = a.n_entries[b];
+  if (n < 0 || n > a.max_entries) {
+    set_err(CSKV_ERR_BOUNDS);
+    n = max(0, min(n, a.max_entries));
+  }
   return n;
 }
 
-__global__ void __launch_bounds__(256) list_attn_kernel(const ListArgs a) {
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)a.T * a.H) return;
-  const int t = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H);
-  RowState r;
-  load_query(a, t, h, lane, r.q);
-  for (int i = 0; i < 16; ++i) r.o[i] = 0.f;
-  r.m = -INFINITY;
-  r.l = 0.f;
-  if (a.pos1 != nullptr) {
-    const int pos = cut(a.pos1[t], a.max_ctx) - 1;
-    const int req = a.req_of ? a.req_of[t] : t;
-    if (pos >= 0 && (req < 0 || req >= a.num_reqs)) {
-      set_err(CSKV_ERR_BOUNDS);
+// What the block's queries see, and the runs of keys: all threads of the block call this.
+__device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
+  const int tid = threadIdx.x;
+  const int t0 = it.r0 / a.H;
+  if (tid < kRows) {
+    RowSees s{0, 1, 0, -1};   // nothing
+    if (tid < it.nr) {
+      const int t = (it.r0 + tid) / a.H;
+      if (it.kind == kWindowRows) {
+        int p1 = a.pos1[t];
+        const int req = a.req_of ? a.req_of[t] : t;
+        if (p1 > a.max_ctx) { set_err(CSKV_ERR_BOUNDS); p1 = a.max_ctx; }
+        if (p1 > 0 && (req < 0 || req >= a.num_reqs)) { set_err(CSKV_ERR_BOUNDS); p1 = 0; }
+        if (p1 > 0) s = RowSees{min(a.first, p1), max(0, p1 - a.window), p1 - 1, req};
+      } else if (it.kind == kRing) {
+        s = RowSees{max(0, min(a.ctx_len[t], kWindow)), 1, 0, t};
+      } else {
+        const int n = entries_of(a, t);
+        s = RowSees{it.kind == kPrefixEntries ? min(n, a.n_prefix) : n, 1, 0, it.kind == kPrefixEntries ? 0 : t};
+      }
+    }
+    sm->sees[tid] = s;   // .run holds the request until the runs are built
+    sm->m[tid] = -INFINITY;
+    sm->msub[tid] = 0.f;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int nruns = 0, tiles = 0;
+    if (it.kind != kWindowRows) {
+      int f = 0, minf = 0x7FFFFFFF;
+      for (int r = 0; r < it.nr; ++r) {
+        f = max(f, sm->sees[r].f);
+        minf = min(minf, sm->sees[r].f);
+      }
+      const int from = it.kind == kOwnEntries ? a.n_prefix : 0;
+      Run u{sm->sees[0].run, 0, from, max(0, f - from), 0, 0, it.nr, 1, minf, 1, 0};
+      if (it.kind == kPrefixEntries) u.req = 0;
+      sm->runs[0] = u;
+      nruns = u.nkeys > 0 ? 1 : 0;
+      tiles = (u.nkeys + kKeys - 1) / kKeys;
     } else {
-      const int lo = max(0, pos - a.window + 1);
-      for (int j = 0; j < min(a.first, lo); ++j) attend(a, a.kv.fmt, paged_row(a.kv, req, j, a.row_bytes).data, lane, r);
-      for (int j = lo; j <= pos; ++j) attend(a, a.kv.fmt, paged_row(a.kv, req, j, a.row_bytes).data, lane, r);
+      // neighbouring queries of one request at neighbouring positions share a run
+      const int nq = (it.r0 + it.nr - 1) / a.H - t0 + 1;
+      int q = 0;
+      while (q < nq) {
+        const RowSees first = sm->sees[q * a.H < it.nr ? q * a.H : 0];
+        if (first.run < 0) { ++q; continue; }
+        int lo = first.lo, hi = first.hi, f = first.f, last = first.hi;
+        int minf = first.f, maxlo = first.lo, minhi = first.hi;
+        int e = q + 1;
+        for (; e < nq; ++e) {
+          const RowSees s = sm->sees[e * a.H];
+          if (s.run != first.run || s.hi > last + 64 || s.hi < last - 64) break;
+          last = s.hi;
+          lo = min(lo, s.lo); hi = max(hi, s.hi); f = max(f, s.f);
+          minf = min(minf, s.f); maxlo = max(maxlo, s.lo); minhi = min(minhi, s.hi);
+        }
+        const int f1 = min(f, lo);        // first rows before the windows; the rest of them lie inside
+        Run u{first.run, f1, lo, f1 + hi - lo + 1, tiles, q, e, q == 0 && e == nq, minf, maxlo, minhi};
+        sm->runs[nruns++] = u;
+        tiles += (u.nkeys + kKeys - 1) / kKeys;
+        q = e;
+      }
     }
-  } else {
-    int n = a.n_entries[t];
-    if (n < 0) { set_err(CSKV_ERR_BOUNDS); n = 0; }
-    n = cut(n, a.max_entries);
-    for (int j = 0; j < n; ++j)
-      attend(a, a.kv.fmt, paged_row(a.kv, j < a.n_prefix ? 0 : t, j, a.row_bytes).data, lane, r);
-    if (a.swa != nullptr) {
-      const int w = min(a.ctx_len[t], kWindow);
-      for (int j = 0; j < w; ++j)
-        attend(a, a.swa_fmt, a.swa + (size_t(t) * kWindow + j) * a.swa_row_bytes, lane, r);
-    }
+    sm->nruns = nruns;
+    sm->ntiles = tiles;
   }
-  const bool empty = r.l == 0.f;   // no key: out 0, lse the sink itself
-  if (a.sink != nullptr) {
-    const float s = a.sink[h] * kLog2e, m = fmaxf(r.m, s);
-    if (m > -INFINITY) {
-      const float f = r.m == -INFINITY ? 0.f : exp2f(r.m - m);
-      r.l = r.l * f + exp2f(s - m);
-      for (int i = 0; i < 16; ++i) r.o[i] *= f;
-      r.m = m;
+  __syncthreads();
+  if (tid < it.nr) {
+    int run = -1;
+    if (it.kind != kWindowRows) {
+      run = 0;
+    } else {
+      const int q = (it.r0 + tid) / a.H - t0;
+      for (int i = 0; i < sm->nruns; ++i)
+        if (q >= sm->runs[i].q0 && q < sm->runs[i].q1) run = i;
     }
+    sm->sees[tid].run = run;
   }
-  const float inv = r.l == 0.f ? 0.f : 1.0f / r.l;
-  for (int i = 0; i < 16; ++i) r.o[i] *= inv;
-  rotate16(a.q_rope + size_t(t) * 64, lane, -1.f, r.o);
-  __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(a.out + (size_t(row) * kD + 16 * lane) * 2);
-  for (int i = 0; i < 8; ++i) o[i] = __floats2bfloat162_rn(r.o[2 * i], r.o[2 * i + 1]);
-  if (a.lse != nullptr && lane == 0) a.lse[row] = empty ? (a.sink ? a.sink[h] : -INFINITY) : (r.m + log2f(r.l)) * kLn2;
+  __syncthreads();
 }
 
-// one warp per (request, entry)
-__global__ void __launch_bounds__(256) weights_kernel(const ListArgs a) {
-  const int b = blockIdx.y;
-  const int j = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  int n = a.n_entries[b];
-  if (n < 0) { set_err(CSKV_ERR_BOUNDS); n = 0; }
-  n = cut(n, a.max_entries);
-  if (j < a.first || j >= n) return;
-  const uint8_t* p = paged_row(a.kv, b, j, a.row_bytes).data;
-  float w = 0.f;
-  for (int h = 0; h < a.H && p != nullptr; ++h) {
-    float q[16], v[16];
-    load_query(a, b, h, lane, q);
-    const float z = logit(a, a.kv.fmt, p, lane, q, v);
-    const float l = a.lse_in[size_t(b) * a.H + h];
-    if (l != -INFINITY) w += exp2f(z - l * kLog2e);
+// Walks a block's tiles in order.
+struct TileWalk {
+  const ListSmem* sm;
+  int run = 0;
+  __device__ __forceinline__ explicit TileWalk(const ListSmem* s) : sm(s) {}
+  // key index of the tile's first key within its run, and the number of keys it holds
+  __device__ __forceinline__ void seek(int tile, int* k0, int* n) {
+    while (run + 1 < sm->nruns && tile >= sm->runs[run + 1].tile0) ++run;
+    *k0 = (tile - sm->runs[run].tile0) * kKeys;
+    *n = min(kKeys, sm->runs[run].nkeys - *k0);
   }
-  if (lane == 0) a.acc_out[b * a.acc_out_stride + j] = a.decay * a.acc[b * a.acc_stride + j] + w;
+  __device__ __forceinline__ int position(int key) const {
+    const Run& u = sm->runs[run];
+    return key < u.f1 ? key : u.base + (key - u.f1);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// loading warps.  Thread lt has dims 16 (lt & 3) .. + 15 of every chunk, of rows lt / 4 and
+// lt / 4 + 64 of every tile.  NS chunk slots; slot users in order: fill f of a slot waits
+// for release f - 1 (released in pairs of chunks when NS == 8: the O product's dim blocks).
+// ---------------------------------------------------------------------------
+template <int FMT, int NS>
+__device__ void load_tiles(const Item& it, ListSmem* sm, uint8_t* slots, int tile_begin, int tile_end,
+                           unsigned long long spin) {
+  constexpr int kAhead = FMT == CSKV_FMT_BF16 ? 2 : 4;   // chunks in registers
+  const int lt = threadIdx.x - kSoftThreads;
+  const int row = lt >> 2, grp = lt & 3;
+  TileWalk walk(sm);
+  const uint8_t* cur[2];
+  const uint8_t* nxt[2] = {nullptr, nullptr};
+  int keys = 0, nkeys = 0;
+  auto resolve = [&](int tile, const uint8_t* (&p)[2], int* n) {
+    int k0;
+    walk.seek(tile, &k0, n);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = row + 64 * u;
+      p[u] = r < *n ? paged_row(it.pages, sm->runs[walk.run].req, walk.position(k0 + r), it.row_bytes).data : nullptr;
+    }
+  };
+  Raw<FMT> raw[kAhead][2];
+  resolve(tile_begin, cur, &keys);
+#pragma unroll
+  for (int c = 0; c < kAhead; ++c)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_raw(cur[u], 4 * c + grp, raw[c][u]);
+  for (int tile = tile_begin; tile < tile_end; ++tile) {
+    const int i = tile - tile_begin;
+    const bool more = tile + 1 < tile_end;
+    if (more) resolve(tile + 1, nxt, &nkeys);
+    const int used = (keys + 15) & ~15;   // rows that the O product reads
+    uint32_t bad = 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int fill = i * (8 / NS) + c / NS;
+      if (fill > 0 && (NS != 8 || (c & 1) == 0))
+        if (!wait_bar(sm, &sm->free_[NS == 8 ? c >> 1 : c % NS], (fill - 1) & 1, spin)) return;
+      uint8_t* slot = slots + (c % NS) * kChunk;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = row + 64 * u;
+        uint32_t w[8];
+        const uint32_t b = convert(raw[c % kAhead][u], w);
+        if (b != 0) {   // kept out of both products; the softmax makes the key's logits NaN
+          bad |= 1u << u;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] = 0u;
+        }
+        if (r < used) {
+          *reinterpret_cast<uint4*>(slot + sw128_offset(r, 2 * grp)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(slot + sw128_offset(r, 2 * grp + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        if (c + kAhead < 8) load_raw(cur[u], 4 * (c + kAhead) + grp, raw[c % kAhead][u]);
+        else if (more) load_raw(nxt[u], 4 * (c + kAhead - 8) + grp, raw[c % kAhead][u]);
+      }
+      if (c == 7) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          reinterpret_cast<uint8_t*>(&sm->kstate[i & 1][row + 64 * u])[grp] =
+              static_cast<uint8_t>((cur[u] != nullptr ? 1 : 0) | ((bad >> u) & 1) << 1);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->full[c % NS]);
+    }
+    cur[0] = nxt[0];
+    cur[1] = nxt[1];
+    keys = nkeys;
+  }
+}
+
+template <int NS>
+__device__ __forceinline__ void load_role(const Item& it, ListSmem* sm, uint8_t* slots, int b, int e,
+                                          unsigned long long spin) {
+  if (it.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32) load_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32, NS>(it, sm, slots, b, e, spin);
+  else if (it.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16) load_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16, NS>(it, sm, slots, b, e, spin);
+  else load_tiles<CSKV_FMT_BF16, NS>(it, sm, slots, b, e, spin);
+}
+
+// The block's query rows, rotated, into the K-major chunks of Q (rows nq apart; chunk 8 holds
+// the second bf16 of the rotated dims); warps 0-7.
+__device__ __forceinline__ void load_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
+#pragma unroll 4
+  for (int x = threadIdx.x; x < nq * 64; x += kSoftThreads) {
+    const int r = x >> 6, c = x & 63;   // dims 8c .. 8c + 7
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r < nr) v = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(r0 + r) * kD + c * 8) * 2));
+    uint8_t* dst = qtile + (c >> 3) * (nq * 128) + sw128_offset(r, c & 7);
+    if (c >= 56) {
+      uint4 lo = make_uint4(0u, 0u, 0u, 0u);
+      if (r < nr) {
+        const float* cs = a.q_rope + static_cast<size_t>((r0 + r) / a.H) * 64 + (c - 56) * 8;
+        const float4 t0 = __ldg(reinterpret_cast<const float4*>(cs)), t1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
+        const float co[4] = {t0.x, t0.z, t1.x, t1.z}, si[4] = {t0.y, t0.w, t1.y, t1.w};
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+        uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
+          const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
+          w[k] = pack_bf16(z0, z1);
+          l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
+        }
+      }
+      *reinterpret_cast<uint4*>(qtile + 8 * (nq * 128) + sw128_offset(r, c & 7)) = lo;
+    }
+    *reinterpret_cast<uint4*>(dst) = v;
+  }
+}
+
+// S^T of one chunk: 128 keys x nq rows (TMEM d), K = 64 dims
+__device__ __forceinline__ void issue_s_chunk(uint32_t d, uint32_t kslot, uint32_t qtile, int c, int nq, uint32_t id) {
+  const uint64_t dk = smem_desc_sw128(kslot, 16, 1024);
+  const uint64_t dq = smem_desc_sw128(qtile + c * (nq * 128), 16, 1024);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mma_f16(d, dk + 2 * k, dq + 2 * k, id, c > 0 || k > 0);
+  if (c == 7) {   // the query's second halves on the same keys' rotated dims
+    const uint64_t dl = smem_desc_sw128(qtile + 8 * (nq * 128), 16, 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_f16(d, dk + 2 * k, dl + 2 * k, id, 1);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the attention kernel
+// ---------------------------------------------------------------------------
+// softmax of one key's logits z (nc rows from column cb), and the epilogue's helpers
+__device__ __forceinline__ void mask_logits(const ListSmem* sm, int run, int pos, uint32_t state, int cb, int nc,
+                                            float scale, float (&z)[32]) {
+  const bool exists = (state & 0x01010101u) == 0x01010101u;
+  const bool fine = (state & 0x02020202u) == 0u;
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    if (c < nc) {
+      const RowSees s = sm->sees[cb + c];
+      const bool see = exists && s.run == run && (pos < s.f || (pos >= s.lo && pos <= s.hi));
+      z[c] = see ? (fine ? z[c] * scale : __int_as_float(0x7FC00000)) : -INFINITY;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_constant__ ListArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* ktile = base;                              // 8 chunks of 128 rows x 128 B
+  uint8_t* qtile = ktile + 8 * kChunk;                // 9 chunks of nq rows x 128 B
+  uint8_t* ptile = qtile + 9 * kRows * 128;           // 128 keys x 128 B
+  ListSmem* sm = reinterpret_cast<ListSmem*>(ptile + kChunk);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Item it = item_of(a, blockIdx.x);
+  const int nq = (it.nr + 15) & ~15;
+
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) mbar_init(&sm->full[i], kLoadThreads / 32);
+    for (int i = 0; i < 4; ++i) mbar_init(&sm->free_[i], 1);
+    mbar_init(&sm->bar_s[0], 2);
+    mbar_init(&sm->bar_p[0], kSoftThreads / 32);
+    mbar_init(&sm->bar_q, kSoftThreads / 32);
+    sm->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 16) tmem_alloc(&sm->tmem, 512);
+  tc_fence_before();
+  plan_block(a, it, sm);
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+  const int begin = static_cast<int>(static_cast<long long>(sm->ntiles) * it.split / it.nsplit);
+  const int end = static_cast<int>(static_cast<long long>(sm->ntiles) * (it.split + 1) / it.nsplit);
+  const int nt = end - begin;
+
+  if (warp >= 8 && warp < 16) {
+    if (nt > 0) load_role<8>(it, sm, ktile, begin, end, a.spin);
+  } else if (warp == 16) {
+    if (lane == 0 && nt > 0) {
+      const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
+      const uint32_t ido = make_idesc(1, 1, 1, 1, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
+      const uint64_t dv = smem_desc_sw128(smem_u32(ktile), kChunk, 1024);
+      const uint64_t dp = smem_desc_sw128(smem_u32(ptile), kChunk, 1024);
+      TileWalk walk(sm);
+      bool ok = wait_bar(sm, &sm->bar_q, 0, a.spin);
+      for (int i = 0; i < nt && ok; ++i) {
+        for (int c = 0; c < 8 && ok; ++c) {
+          ok = wait_bar(sm, &sm->full[c], i & 1, a.spin);
+          tc_fence_after();
+          if (ok) issue_s_chunk(tmem + kTmemS, smem_u32(ktile) + c * kChunk, smem_u32(qtile), c, nq, ids);
+        }
+        mma_commit(&sm->bar_s[0]);
+        mbar_arrive(&sm->bar_s[0]);   // hands on what the loading warps wrote (kstate)
+        ok = ok && wait_bar(sm, &sm->bar_p[0], i & 1, a.spin);
+        if (!ok) break;
+        tc_fence_after();
+        int k0, n;
+        walk.seek(begin + i, &k0, &n);
+        const int ks = (n + 15) >> 4;
+#pragma unroll 1
+        for (int mb = 0; mb < 4; ++mb) {
+          for (int k = 0; k < ks; ++k)
+            mma_f16(tmem + mb * kRows, dv + mb * (kChunk >> 3) + k * 128, dp + k * 128, ido, i > 0 || k > 0);
+          mma_commit(&sm->free_[mb]);
+        }
+      }
+    }
+  } else {
+    load_queries(a, it.r0, it.nr, nq, qtile);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm->bar_q);
+    const int quarter = warp & 3, half = warp >> 2;
+    const int cb = half * 32, nc = max(0, min(32, nq - cb));
+    const int key = quarter * 32 + lane;
+    const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
+    float l[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) l[c] = 0.f;
+    TileWalk walk(sm);
+    bool ok = true;
+    for (int i = 0; i < nt; ++i) {
+      if (ok) ok = wait_bar(sm, &sm->bar_s[0], i & 1, a.spin);
+      __syncwarp();
+      tc_fence_after();
+      float z[32];
+      if (nc > 0) {
+        tmem_ld_cols(tmem + kTmemS + tlane + cb, nc, z);
+        tmem_wait_ld();
+      }
+      int k0, n;
+      walk.seek(begin + i, &k0, &n);
+      const Run& u = sm->runs[walk.run];
+      const uint32_t state = key < n ? sm->kstate[i & 1][key] : 0u;
+      // all 128 keys seen by all rows: inside every window, or all first rows
+      const int pa = walk.position(k0), pb = walk.position(k0 + n - 1);
+      const bool plain = u.whole && n == kKeys && ((pb < u.min_f) || (pa >= u.max_lo && pb <= u.min_hi && pb - pa == kKeys - 1));
+      if (plain && state == 0x01010101u) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) z[c] *= a.scale_log2;
+      } else {
+        mask_logits(sm, walk.run, walk.position(k0 + key), state, cb, nc, a.scale_log2, z);
+      }
+      bool above = false;
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        if (c < nc) {
+          const float4 m = *reinterpret_cast<const float4*>(&sm->m[cb + c]);
+          above = above || z[c] > m.x + kSlack || z[c + 1] > m.y + kSlack || z[c + 2] > m.z + kSlack || z[c + 3] > m.w + kSlack;
+        }
+      }
+      if (soft_any(above)) {   // some row's reference moves: the tile's maxima, exactly
+        float mine = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          if (c < nc) {
+            const float v = warp_max(z[c]);
+            if (lane == c) mine = v;
+          }
+        }
+        if (lane < nc) sm->part[quarter][cb + lane] = mine;
+        soft_sync();
+        if (tid < nq) {
+          const float old = sm->m[tid];
+          const float now = fmaxf(fmaxf(fmaxf(sm->part[0][tid], sm->part[1][tid]), fmaxf(sm->part[2][tid], sm->part[3][tid])), old);
+          sm->fac[tid] = old == -INFINITY ? 0.f : exp2f(old - now);
+          sm->m[tid] = now;
+          sm->msub[tid] = now == -INFINITY ? 0.f : now;
+        }
+        soft_sync();
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c < nc) l[c] *= sm->fac[cb + c];
+        if (i > 0) {   // the S commit says that the O products so far are complete
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll 1
+            for (int g = 0; g < nq; g += 32) {
+              float o[32];
+              const uint32_t at = tmem + tlane + (half * 2 + x) * kRows + g;
+              tmem_ld32(at, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= sm->fac[g + c];
+              tmem_st32(at, o);
+              tmem_wait_st();
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (8 * g < nc) {
+          const float4 m0 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * g]);
+          const float4 m1 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * g + 4]);
+          const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+          float p[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            p[c] = exp2f(z[8 * g + c] - mm[c]);
+            l[8 * g + c] += p[c];
+          }
+          *reinterpret_cast<uint4*>(ptile + sw128_offset(key, half * 4 + g)) =
+              make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->bar_p[0]);
+    }
+    if (nt > 0 && ok) wait_bar(sm, &sm->free_[3], (nt - 1) & 1, a.spin);
+    __syncwarp();
+    tc_fence_after();
+    // ---- the rows' sums over the 128 keys: lane c ends with row cb + c
+    {
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) {
+        const bool hi = (lane & w) != 0;
+#pragma unroll
+        for (int j = 0; j < w; ++j) {
+          const float send = hi ? l[j] : l[j + w];
+          const float keep = hi ? l[j + w] : l[j];
+          l[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
+        }
+      }
+      if (lane < nc) sm->part[quarter][cb + lane] = l[0];
+    }
+    soft_sync();
+    if (tid < nq) {
+      const float sum = ((sm->part[0][tid] + sm->part[1][tid]) + sm->part[2][tid]) + sm->part[3][tid];
+      const float m = sm->m[tid];
+      float f = 0.f;
+      if (tid < it.nr) {
+        const size_t row = static_cast<size_t>(it.r0) + tid;
+        if (a.parts > 1) {
+          *reinterpret_cast<float2*>(a.ml + (row * a.parts + it.part) * 2) = make_float2(m, sum);
+          f = 1.f;
+        } else {
+          const float sink = a.sink ? a.sink[row % a.H] : -INFINITY;
+          const float s2 = sink * kLog2e;
+          const float M = fmaxf(m, s2);
+          const float e = exp2f(m - M);
+          const float total = sum * e + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));
+          const bool none = sum == 0.f;   // no key: out 0, lse the sink itself
+          f = none ? 0.f : e / total;
+          if (sum != sum) f = sum;
+          if (a.lse != nullptr) a.lse[row] = none ? sink : sum != sum ? sum : (M + log2f(total)) * kLn2;
+        }
+      }
+      sm->fac[tid] = f;
+    }
+    soft_sync();
+    // ---- O^T out: a thread has dim d of up to 32 rows at a time
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+      const int mb = half * 2 + x;
+      const int d = mb * 128 + quarter * 32 + lane;
+#pragma unroll 1
+      for (int g = 0; g < nq; g += 32) {
+        const int cols = min(32, nq - g);
+        float o[32];
+        if (nt > 0) {
+          tmem_ld_cols(tmem + tlane + mb * kRows + g, cols, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = 0.f;
+        }
+        if (a.parts > 1) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (g + c < it.nr)
+              a.opart[((static_cast<size_t>(it.r0) + g + c) * a.parts + it.part) * kD + d] = o[c];
+        } else {
+          const bool turn = mb == 3 && quarter >= 2;   // dims 448..511
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            if (g + c < it.nr) {
+              float v0 = o[c] * sm->fac[g + c], v1 = o[c + 1] * sm->fac[g + c + 1];
+              if (turn) {
+                const int k = (d - (kD - 64)) >> 1;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  float& v = y == 0 ? v0 : v1;
+                  const int r = min(it.r0 + g + c + y, it.r0 + it.nr - 1);
+                  const float2 cs = __ldg(reinterpret_cast<const float2*>(a.q_rope + static_cast<size_t>(r / a.H) * 64) + k);
+                  const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                  v = (lane & 1) ? v * cs.x - w * cs.y : v * cs.x + w * cs.y;
+                }
+              }
+              // even lanes store dims d, d + 1 of row c, odd lanes dims d - 1, d of row c + 1
+              const float other = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? v0 : v1, 1);
+              const uint32_t w = (lane & 1) ? pack_bf16(other, v1) : pack_bf16(v0, other);
+              const int r = g + c + (lane & 1);
+              if (r < it.nr)
+                *reinterpret_cast<uint32_t*>(a.out + ((static_cast<size_t>(it.r0) + r) * kD + (d & ~1)) * 2) = w;
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins a row's partial outputs in order, adds the sink, turns the output back: 64 threads of
+// 8 dims per row.
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ ListArgs a) {
+  const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= static_cast<size_t>(a.T) * a.H) return;
+  const int d = (threadIdx.x & 63) * 8;
+  const float* ml = a.ml + row * a.parts * 2;
+  const float sink = a.sink ? a.sink[row % a.H] : -INFINITY;
+  const float s2 = sink * kLog2e;
+  float M = s2;
+  for (int p = 0; p < a.parts; ++p)
+    if (ml[2 * p + 1] != 0.f) M = fmaxf(M, ml[2 * p]);
+  float total = 0.f, o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p) {
+    const float l = ml[2 * p + 1];
+    if (l == 0.f) continue;
+    const float e = l != l ? l : exp2f(ml[2 * p] - M);
+    total += l * e;
+    const float4* v = reinterpret_cast<const float4*>(a.opart + (row * a.parts + p) * kD + d);
+    const float4 v0 = __ldg(v), v1 = __ldg(v + 1);
+    o[0] += e * v0.x; o[1] += e * v0.y; o[2] += e * v0.z; o[3] += e * v0.w;
+    o[4] += e * v1.x; o[5] += e * v1.y; o[6] += e * v1.z; o[7] += e * v1.w;
+  }
+  const bool none = total == 0.f;
+  if (s2 != -INFINITY) total += exp2f(s2 - M);
+  const float inv = none ? 0.f : 1.0f / total;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] *= inv;
+  if (d >= kD - 64) {
+    const float* cs = a.q_rope + row / a.H * 64 + (d - (kD - 64));
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float c = cs[i], s = cs[i + 1], y0 = o[i], y1 = o[i + 1];
+      o[i] = y0 * c + y1 * s;
+      o[i + 1] = y1 * c - y0 * s;
+    }
+  }
+  *reinterpret_cast<uint4*>(a.out + (row * kD + d) * 2) =
+      make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+  if (a.lse != nullptr && d == 0) a.lse[row] = none ? sink : (M + log2f(total)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// accumulated weights: S^T of every tile, then a thread sums its key's weights over the
+// heads.  Up to 128 heads are the MMA columns, two S buffers in TMEM, four chunk slots
+// (released as soon as the chunk's products are complete).
+// ---------------------------------------------------------------------------
+constexpr int kWeightSlots = 4;
+
+__global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ ListArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* slots = base;
+  const int nq = (a.H + 15) & ~15;
+  uint8_t* qtile = slots + kWeightSlots * kChunk;
+  ListSmem* sm = reinterpret_cast<ListSmem*>(qtile + 9 * nq * 128);
+  float* lse = reinterpret_cast<float*>(sm + 1);   // [128] base 2, +inf: adds nothing
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / a.split, split = blockIdx.x % a.split;
+
+  if (tid == 0) {
+    for (int i = 0; i < kWeightSlots; ++i) {
+      mbar_init(&sm->full[i], kLoadThreads / 32);
+      mbar_init(&sm->free_[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->bar_s[i], 2);
+      mbar_init(&sm->bar_p[i], kSoftThreads / 32);
+    }
+    mbar_init(&sm->bar_q, kSoftThreads / 32);
+    sm->abort = 0;
+    fence_mbar_init();
+    const int n = entries_of(a, b);
+    sm->runs[0] = Run{b, 0, a.first, max(0, n - a.first), 0, 0, 1, 1, 0, 0, 0};
+    sm->nruns = 1;
+    sm->ntiles = (sm->runs[0].nkeys + kKeys - 1) / kKeys;
+  }
+  if (tid < 128) {
+    const float v = tid < a.H ? a.lse_in[static_cast<size_t>(b) * a.H + tid] : -INFINITY;
+    lse[tid] = v == -INFINITY ? INFINITY : v * kLog2e;
+  }
+  if (warp == 16) tmem_alloc(&sm->tmem, 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+  const int begin = static_cast<int>(static_cast<long long>(sm->ntiles) * split / a.split);
+  const int end = static_cast<int>(static_cast<long long>(sm->ntiles) * (split + 1) / a.split);
+  const int nt = end - begin;
+
+  if (nt > 0) {
+    if (warp >= 8 && warp < 16) {
+      Item it;
+      it.fmt = a.kv.fmt;
+      it.row_bytes = a.row_bytes;
+      it.pages = a.kv;
+      load_role<kWeightSlots>(it, sm, slots, begin, end, a.spin);
+    } else if (warp == 16) {
+      if (lane == 0) {
+        const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
+        bool ok = wait_bar(sm, &sm->bar_q, 0, a.spin);
+        for (int i = 0; i < nt && ok; ++i) {
+          const int buf = i & 1;
+          if (i >= 2) ok = wait_bar(sm, &sm->bar_p[buf], ((i >> 1) - 1) & 1, a.spin);
+          tc_fence_after();
+          for (int c = 0; c < 8 && ok; ++c) {
+            const int fill = i * 2 + (c >> 2);
+            ok = wait_bar(sm, &sm->full[c & 3], fill & 1, a.spin);
+            tc_fence_after();
+            if (ok) issue_s_chunk(tmem + buf * 128, smem_u32(slots) + (c & 3) * kChunk, smem_u32(qtile), c, nq, ids);
+            mma_commit(&sm->free_[c & 3]);
+          }
+          mma_commit(&sm->bar_s[buf]);
+          mbar_arrive(&sm->bar_s[buf]);   // hands on what the loading warps wrote (kstate)
+        }
+      }
+    } else {
+      load_queries(a, b * a.H, a.H, nq, qtile);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->bar_q);
+      const int quarter = warp & 3, half = warp >> 2;
+      const int key = quarter * 32 + lane;
+      const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
+      // columns [c0, c1) of this warp: the 16-column groups of Q cut in two halves
+      const int groups = nq >> 4;
+      const int c0 = half == 0 ? 0 : ((groups + 1) >> 1) * 16, c1 = half == 0 ? ((groups + 1) >> 1) * 16 : nq;
+      bool ok = true;
+      for (int i = 0; i < nt; ++i) {
+        const int buf = i & 1;
+        if (ok) ok = wait_bar(sm, &sm->bar_s[buf], (i >> 1) & 1, a.spin);
+        __syncwarp();
+        tc_fence_after();
+        float w = 0.f;
+        for (int c = c0; c < c1; c += 16) {
+          float z[16];
+          tmem_ld16(tmem + tlane + buf * 128 + c, z);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            const float4 s = *reinterpret_cast<const float4*>(&lse[c + k]);
+            w += (exp2f(z[k] * a.scale_log2 - s.x) + exp2f(z[k + 1] * a.scale_log2 - s.y)) +
+                 (exp2f(z[k + 2] * a.scale_log2 - s.z) + exp2f(z[k + 3] * a.scale_log2 - s.w));
+          }
+        }
+        tc_fence_before();
+        // (the state of tile i + 2 is written after its S product, so after this release)
+        const int k = (begin + i) * kKeys + key;
+        const uint32_t state = sm->kstate[buf][key];
+        if (half == 1) sm->part[buf][key] = w;
+        soft_sync();
+        if (lane == 0) mbar_arrive(&sm->bar_p[buf]);
+        if (half == 0 && k < sm->runs[0].nkeys) {
+          if (groups > 1) w += sm->part[buf][key];
+          const bool exists = (state & 0x01010101u) == 0x01010101u;
+          if (!exists) w = 0.f;
+          else if (state & 0x02020202u) w = __int_as_float(0x7FC00000);
+          const long long j = a.first + k;
+          a.acc_out[b * a.acc_out_stride + j] = a.decay * a.acc[b * a.acc_stride + j] + w;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+constexpr size_t kAttnSmem = 1024 + 9 * size_t(kChunk) + 9 * kRows * 128 + sizeof(ListSmem);
+static_assert(kAttnSmem <= 227 * 1024, "one block per SM");
+
+size_t weights_smem(int H) {
+  const int nq = (H + 15) & ~15;
+  return 1024 + kWeightSlots * size_t(kChunk) + 9 * size_t(nq) * 128 + sizeof(ListSmem) + 128 * sizeof(float);
+}
+
+__host__ __device__ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// How blocks, splits and partial outputs follow from the sizes alone (so that a workspace of
+// the size that was asked for always fits).  Lengths and costs are in tiles of 128 keys.
+struct ListPlan {
+  int group, head_blocks, heads_per_block, blocks;   // per-query blocks
+  int split, prefix_blocks, prefix_split, own_blocks, ring_blocks, parts;
+};
+
+constexpr int kSmsPlanned = 152;
+constexpr double kBlockCost = 2.0;   // a block's set-up and epilogue
+
+// The time of groups of equal blocks started one after the other on all SMs.
+struct Schedule {
+  double time = 0, idle = 0;
+  void add(double n, double length) {
+    const double work = n * length;
+    if (work <= idle) {
+      idle -= work;
+      return;
+    }
+    const double left = work - idle, waves = std::ceil(left / length / kSmsPlanned);
+    time += waves * length;
+    idle = waves * length * kSmsPlanned - left;
+  }
+};
+
+// writing and reading partial outputs: 4 KB a row and part at about 2.5 MB per tile's time
+double join_cost(double rows, int parts) { return parts <= 1 ? 0.0 : 1.5 + rows * parts * 4096.0 / 10e6; }
+
+int tiles_of(long long keys) { return static_cast<int>((keys + kKeys - 1) / kKeys); }
+int shares(int tiles, int len) { return len > 0 ? (tiles + len - 1) / len : 0; }
+
+// the share length of least cost among tiles, tiles / 2, ... (every count to 16, then in steps of an eighth)
+template <class Cost>
+int best_length(int tiles, Cost&& cost) {
+  int best_len = tiles;
+  double best = cost(tiles);
+  for (int n = 2; n <= tiles && n <= 4 * kSmsPlanned; n += n < 16 ? 1 : n / 8) {
+    const int len = (tiles + n - 1) / n;
+    const double c = cost(len);
+    if (c < best) {
+      best = c;
+      best_len = len;
+    }
+  }
+  return best_len;
+}
+
+ListPlan base_plan(int T, int H, bool grouped) {
+  ListPlan p = {};
+  p.head_blocks = (H + kRows - 1) / kRows;
+  p.heads_per_block = (H + p.head_blocks - 1) / p.head_blocks;
+  p.group = p.head_blocks == 1 && grouped ? kRows / H : 1;
+  p.blocks = (T + p.group - 1) / p.group * p.head_blocks;
+  p.split = p.prefix_split = 1;
+  return p;
+}
+
+ListPlan window_plan(int T, int H, bool grouped, int max_ctx, int window, int first) {
+  ListPlan p = base_plan(T, H, grouped);
+  const long long keys = std::min<long long>(max_ctx, static_cast<long long>(window) + first + p.group - 1);
+  const int tiles = std::max(1, tiles_of(keys));
+  const int len = best_length(tiles, [&](int l) {
+    Schedule s;
+    s.add(double(p.blocks) * shares(tiles, l), l + kBlockCost);
+    return s.time + join_cost(double(T) * H, shares(tiles, l));
+  });
+  p.split = p.parts = shares(tiles, len);
+  return p;
+}
+
+ListPlan prefix_plan(int B, int H, int n_prefix, int max_entries, bool ring) {
+  ListPlan p = base_plan(B, H, false);
+  const int rows = B * H;
+  const int ptiles = tiles_of(n_prefix), otiles = tiles_of(max_entries - n_prefix);
+  p.prefix_blocks = ptiles > 0 ? (rows + kRows - 1) / kRows : 0;
+  p.ring_blocks = ring ? p.blocks : 0;
+  p.own_blocks = otiles > 0 || (ptiles == 0 && !ring) ? p.blocks : 0;
+  const int len = best_length(std::max(1, std::max(ptiles, otiles)), [&](int l) {
+    Schedule s;
+    if (ptiles > 0) s.add(double(p.prefix_blocks) * shares(ptiles, l), std::min(l, ptiles) + kBlockCost);
+    if (otiles > 0) s.add(double(p.own_blocks) * shares(otiles, l), std::min(l, otiles) + kBlockCost);
+    if (ring) s.add(p.ring_blocks, 1 + kBlockCost);
+    return s.time + join_cost(rows, shares(ptiles, l) + shares(otiles, l) + (ring ? 1 : 0));
+  });
+  p.prefix_split = std::max(1, shares(ptiles, len));
+  p.split = std::max(1, shares(otiles, len));
+  p.parts = (p.prefix_blocks > 0 ? p.prefix_split : 0) + (p.own_blocks > 0 ? p.split : 0) + (ring ? 1 : 0);
+  return p;
+}
+
+size_t plan_workspace(const ListPlan& p, int T, int H) {
+  if (p.parts <= 1) return 0;
+  const size_t n = static_cast<size_t>(T) * H * p.parts;
+  return a256(n * kD * 4) + a256(n * 2 * 4);
 }
 
 ListArgs common_args(const void* q, const cskv_paged& kv, const float* sink, float scale, const float* q_rope, int T,
@@ -199,23 +1167,51 @@ ListArgs common_args(const void* q, const cskv_paged& kv, const float* sink, flo
   a.H = H;
   a.out = static_cast<uint8_t*>(out);
   a.lse = lse;
+  a.spin = spin_limit();
   return a;
 }
 
-cudaError_t launch_list(const ListArgs& a, cudaStream_t stream) {
-  const long long rows = (long long)a.T * a.H;
-  list_attn_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
+cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStream_t stream) {
+  a.group = p.group;
+  a.head_blocks = p.head_blocks;
+  a.heads_per_block = p.heads_per_block;
+  a.split = p.split;
+  a.prefix_split = p.prefix_split;
+  a.prefix_blocks = p.prefix_blocks;
+  a.own_blocks = p.own_blocks;
+  a.parts = p.parts;
+  const size_t rows = static_cast<size_t>(a.T) * a.H;
+  a.opart = static_cast<float*>(workspace);
+  a.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a256(rows * p.parts * kD * 4));
+  const unsigned grid = a.pos1 != nullptr
+                            ? static_cast<unsigned>(p.blocks) * p.split
+                            : static_cast<unsigned>(p.prefix_blocks) * p.prefix_split + p.own_blocks * p.split + p.ring_blocks;
+  cudaError_t e = cudaFuncSetAttribute(list_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kAttnSmem));
+  if (e != cudaSuccess) return e;
+  list_attn_kernel<<<grid, kThreads, kAttnSmem, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.parts <= 1) return e;
+  attn_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t window_attn_workspace_bytes(int, int, int, int, int) { return 0; }
-size_t prefix_attn_workspace_bytes(int, int, int, int, int) { return 0; }
+size_t window_attn_workspace_bytes(int T, int H, int max_ctx, int window, int first) {
+  // one query per request or queries of prompts: the larger of the two
+  return std::max(plan_workspace(window_plan(T, H, false, max_ctx, window, first), T, H),
+                  plan_workspace(window_plan(T, H, true, max_ctx, window, first), T, H));
+}
+
+size_t prefix_attn_workspace_bytes(int B, int H, int n_prefix, int max_entries, int with_swa) {
+  return plan_workspace(prefix_plan(B, H, n_prefix, max_entries, with_swa != 0), B, H);
+}
 
 cudaError_t launch_window_attn(const void* q, const cskv_paged& rows, int num_reqs, const int32_t* req_of,
                                const int32_t* pos1, int window, int first, int max_ctx, const float* sink, float scale,
-                               const float* q_rope, int T, int H, void* out, float* lse, void*, cudaStream_t stream) {
+                               const float* q_rope, int T, int H, void* out, float* lse, void* workspace,
+                               cudaStream_t stream) {
   ListArgs a = common_args(q, rows, sink, scale, q_rope, T, H, out, lse);
   a.req_of = req_of;
   a.pos1 = pos1;
@@ -223,12 +1219,13 @@ cudaError_t launch_window_attn(const void* q, const cskv_paged& rows, int num_re
   a.window = window;
   a.first = first;
   a.max_ctx = max_ctx;
-  return launch_list(a, stream);
+  // without req_of every query is a request of its own: no two share keys
+  return launch_list(a, window_plan(T, H, req_of != nullptr, max_ctx, window, first), workspace, stream);
 }
 
 cudaError_t launch_prefix_attn(const void* q, const cskv_paged& kv, const int32_t* n_entries, int n_prefix,
                                int max_entries, const void* swa, int swa_fmt, const int32_t* ctx_len, const float* sink,
-                               float scale, const float* q_rope, int B, int H, void* out, float* lse, void*,
+                               float scale, const float* q_rope, int B, int H, void* out, float* lse, void* workspace,
                                cudaStream_t stream) {
   ListArgs a = common_args(q, kv, sink, scale, q_rope, B, H, out, lse);
   a.n_entries = n_entries;
@@ -236,9 +1233,9 @@ cudaError_t launch_prefix_attn(const void* q, const cskv_paged& kv, const int32_
   a.max_entries = max_entries;
   a.swa = static_cast<const uint8_t*>(swa);
   a.swa_fmt = swa_fmt;
-  a.swa_row_bytes = static_cast<int>(cskv_row_bytes(swa_fmt, kD));
+  a.swa_row_bytes = swa != nullptr ? static_cast<int>(cskv_row_bytes(swa_fmt, kD)) : 0;
   a.ctx_len = ctx_len;
-  return launch_list(a, stream);
+  return launch_list(a, prefix_plan(B, H, n_prefix, max_entries, swa != nullptr), workspace, stream);
 }
 
 cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32_t* n_entries, int first,
@@ -256,7 +1253,18 @@ cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32
   a.acc_stride = acc_stride;
   a.acc_out = acc_out;
   a.acc_out_stride = acc_out_stride;
-  weights_kernel<<<dim3((max_entries + 7) / 8, B), 256, 0, stream>>>(a);
+  const int tiles = tiles_of(max_entries - first);
+  const int len = best_length(tiles, [&](int l) {
+    Schedule s;
+    s.add(double(B) * shares(tiles, l), l + kBlockCost);
+    return s.time;
+  });
+  a.split = shares(tiles, len);
+  const size_t smem = weights_smem(H);
+  const cudaError_t e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  weights_kernel<<<static_cast<unsigned>(B) * a.split, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
