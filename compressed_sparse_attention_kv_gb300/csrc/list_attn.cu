@@ -25,11 +25,14 @@
 // no padding to 128.  The tile lives in eight 16 KiB chunks of 64 dims.  Roles:
 //   warps 0-7   load and rotate the queries, then softmax: a thread has one key and up to
 //               32 rows, straight from TMEM; P^T to shared memory as bf16; the epilogue;
-//   warps 8-15  load rows (several chunks ahead, in registers), dequantise exactly to bf16
-//               and fill a chunk as soon as the O product has released it;
+//   warps 8-15  one chunk of every tile each: load its 64 dims of the rows (four rows ahead
+//               in registers), dequantise exactly to bf16, fill the chunk as soon as the O
+//               product has released it; one fence a tile and warp makes it visible to the
+//               tensor core (a fence per chunk by all warps made them wait for each other);
 //   warp 16     one thread issues the MMAs of a chunk as soon as it is full.
 // So a tile's dequantisation overlaps the O product of the tile before it, and S follows
-// chunk by chunk.
+// chunk by chunk.  The roles run different code at the same time: their loops stay short
+// enough for the instruction cache.
 //
 // Roundings: the rotated query is kept as hi + lo, two bf16 numbers (the lo part of the 64
 // rotated dims is a ninth chunk of Q), so that logits and log-sum-exp are fp32-accurate;
@@ -94,6 +97,7 @@ struct ListArgs {
   int parts;                 // partial outputs of a row (1: written straight to out)
   float* opart;              // [row][part][512]
   float* ml;                 // [row][part][2]: m (base 2) and l
+  float slack;               // kSlack in units of q'.c
   unsigned long long spin;
 };
 
@@ -116,11 +120,15 @@ struct ListSmem {
   int nruns, ntiles;
   Run runs[kRows];
   RowSees sees[kRows];
-  __align__(16) float m[kRows];      // running reference, -inf: no key yet
-  __align__(16) float msub[kRows];   // the same, 0 for -inf
+  __align__(16) float m[kRows];      // running reference in units of q'.c, -inf: no key yet
+  __align__(16) float limit[kRows];  // a logit above it moves the reference
+  __align__(16) float msub[kRows];   // the reference in base 2, 0 for none
   __align__(16) float fac[kRows];
   float part[4][2 * kRows];
-  uint32_t kstate[2][kKeys];         // by tile parity; a byte per loading thread: 1 the row exists, 2 it is not finite
+  // rows of tile i that do not exist: bit r & 31 of word [i & 3][r >> 5], set by the loading
+  // warps, cleared by the softmax that has read it (weights_kernel's loads run up to three
+  // tiles ahead of it)
+  uint32_t none[4][4];
 };
 
 // ---------------------------------------------------------------------------
@@ -148,23 +156,57 @@ __device__ __forceinline__ bool soft_any(bool p) {
                : "=r"(r) : "r"(static_cast<int>(p)), "n"(kSoftBarrier), "n"(kSoftThreads) : "memory");
   return r != 0;
 }
-__device__ __forceinline__ float warp_max(float v) {
+__device__ __forceinline__ float exp2_fast(float x) {
   float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+// Transposing butterfly: lanes 2c and 2c + 1 end with op over the warp's lanes of their v[c]
+// (v is spent).
+template <class Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[16], Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int w = 8; w >= 1; w >>= 1) {
+    const bool hi = (lane & (2 * w)) != 0;
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const float send = hi ? v[j] : v[j + w];
+      const float keep = hi ? v[j + w] : v[j];
+      v[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, 2 * w));
+    }
+  }
+  return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The issuing lane's MMAs are unrolled with constant descriptor offsets and constant
+// accumulate flags: about 40 cycles each, near what a 128 x 64 x 16 product takes; computed
+// in a rolled loop, descriptors cost 100 to 190 cycles per MMA whatever its size.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void mma_add(uint32_t d, uint64_t da, uint64_t db, uint32_t id) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(id)
+      : "memory");
+}
+__device__ __forceinline__ void mma_set(uint32_t d, uint64_t da, uint64_t db, uint32_t id) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(id)
+      : "memory");
+}
 // `count` (16 or 32) columns into v[0..count)
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, int count, float (&v)[32]) {
   if (count > 16) tmem_ld32(taddr, v);
@@ -201,88 +243,51 @@ struct Raw<CSKV_FMT_BF16> {
   uint4 a, b;
 };
 
-// 16-dim group g (0..31) of the row at p (nullptr: zeros)
+// Rows that do not exist read as zeros from here, so that loads and conversions have no branch.
+__device__ uint4 g_zero_row[64];
+
+// 16-dim group g (0..31) of the row at p
 __device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_FP8_E4M3_E8M0_B32>& r) {
-  r.c = make_uint4(0u, 0u, 0u, 0u);
-  r.s = 127u;
-  if (p != nullptr) {
-    r.c = __ldg(reinterpret_cast<const uint4*>(p + 16 * g));
-    r.s = __ldg(p + kD + (g >> 1));
-  }
+  r.c = __ldg(reinterpret_cast<const uint4*>(p + 16 * g));
+  r.s = __ldg(p + kD + (g >> 1));
 }
 __device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r) {
-  r.c = make_uint2(0u, 0u);
-  r.s = 0u;
-  if (p != nullptr) {
-    r.c = __ldg(reinterpret_cast<const uint2*>(p + 8 * g));
-    r.s = __ldg(p + kD / 2 + g);
-  }
+  r.c = __ldg(reinterpret_cast<const uint2*>(p + 8 * g));
+  r.s = __ldg(p + kD / 2 + g);
 }
 __device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_BF16>& r) {
-  r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
-  if (p != nullptr) {
-    r.a = __ldg(reinterpret_cast<const uint4*>(p + 32 * g));
-    r.b = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 16));
-  }
+  r.a = __ldg(reinterpret_cast<const uint4*>(p + 32 * g));
+  r.b = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 16));
 }
 
-// nonzero if one of the two bf16 of w is infinite or NaN (an exponent of all ones carries
-// into the sign bit when its lowest bit is added)
-__device__ __forceinline__ uint32_t unfit_bf16(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
-
-// to 8 words of two bf16; returns nonzero if a value is not finite
-__device__ __forceinline__ uint32_t convert(const Raw<CSKV_FMT_BF16>& r, uint32_t (&w)[8]) {
+// to 8 words of two bf16
+__device__ __forceinline__ void convert(const Raw<CSKV_FMT_BF16>& r, uint32_t (&w)[8]) {
   w[0] = r.a.x; w[1] = r.a.y; w[2] = r.a.z; w[3] = r.a.w;
   w[4] = r.b.x; w[5] = r.b.y; w[6] = r.b.z; w[7] = r.b.w;
-  uint32_t bad = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) bad |= unfit_bf16(w[i]);
-  return bad;
 }
-// e4m3 s.eeee.mmm placed at bf16 bits 15 and 10..4 is the value times 2^-120 (subnormal codes
-// too), so one product by 2^(120 + e) of the block's scale 2^e dequantises; the result has
-// 4 significant bits.  Scales beyond 2^7 take the product in two steps.
-__device__ __forceinline__ uint32_t convert(const Raw<CSKV_FMT_FP8_E4M3_E8M0_B32>& r, uint32_t (&w)[8]) {
+// e4m3 pairs to fp16 (exact), times the block's scale 2^e in fp32, rounded to bf16 (4
+// significant bits: exact where bf16 holds the value)
+__device__ __forceinline__ void convert(const Raw<CSKV_FMT_FP8_E4M3_E8M0_B32>& r, uint32_t (&w)[8]) {
+  const float s = exp2i(static_cast<int>(r.s) - 127);   // infinite for a scale byte of 255
   const uint32_t c[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
-  uint32_t bad = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bad |= ((c[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // a code of S.1111.111
-    const uint32_t lo = __byte_perm(c[i], 0u, 0x1404), hi = __byte_perm(c[i], 0u, 0x3424);
-    w[2 * i] = ((lo >> 4) & 0x07F007F0u) | (lo & 0x80008000u);
-    w[2 * i + 1] = ((hi >> 4) & 0x07F007F0u) | (hi & 0x80008000u);
+  for (int i = 0; i < 8; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c[i >> 1] >> (16 * (i & 1)))));
+    w[i] = pack_bf16(__half2float(__ushort_as_half(h & 0xFFFF)) * s, __half2float(__ushort_as_half(h >> 16)) * s);
   }
-  if (r.s <= 134u) {
-    const uint32_t f = (r.s + 120u) << 7, ff = f | (f << 16);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], ff);
-  } else {
-    const uint32_t f = r.s << 7, ff = f | (f << 16);   // 2^(s - 127), infinite for s = 255
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = mul_bf16x2(mul_bf16x2(w[i], 0x7B807B80u), ff);
-      bad |= unfit_bf16(w[i]);
-    }
-  }
-  return bad;
 }
-// e2m1 times the e4m3 scale is exact in fp16 (6 significant bits, 2^-10 .. 2688); fp16
-// s.eeeee.m(10) moved down three bits is a bf16 of the value times 2^-112.
-__device__ __forceinline__ uint32_t convert(const Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r, uint32_t (&w)[8]) {
-  uint32_t s2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(static_cast<uint16_t>(r.s | (r.s << 8))));
+// e2m1 pairs to fp16, times the e4m3 scale (6 significant bits: exact in fp32 and bf16)
+__device__ __forceinline__ void convert(const Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r, uint32_t (&w)[8]) {
+  const float s = e4m3_to_f32(r.s);
   const uint32_t c[2] = {r.c.x, r.c.y};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t h;
-      asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(c[i] >> (8 * j)));
-      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(s2));
-      w[4 * i + j] = mul_bf16x2(((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u), 0x77807780u);
-    }
+  for (int i = 0; i < 8; ++i) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+        : "=r"(h) : "r"(c[i >> 2] >> (8 * (i & 3))));
+    w[i] = pack_bf16(__half2float(__ushort_as_half(h & 0xFFFF)) * s, __half2float(__ushort_as_half(h >> 16)) * s);
   }
-  return (r.s & 0x7Fu) == 0x7Fu ? 1u : 0u;
 }
 
 // ---------------------------------------------------------------------------
@@ -384,18 +389,20 @@ __device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
       }
     }
     sm->sees[tid] = s;   // .run holds the request until the runs are built
-    sm->m[tid] = -INFINITY;
+    sm->m[tid] = sm->limit[tid] = -INFINITY;
     sm->msub[tid] = 0.f;
   }
+  if (tid < 16) (&sm->none[0][0])[tid] = 0u;
   __syncthreads();
+  int f = 0, minf = 0;
+  if (it.kind != kWindowRows && tid < 32) {
+    const int f0 = tid < it.nr ? sm->sees[tid].f : -1, f1 = tid + 32 < it.nr ? sm->sees[tid + 32].f : -1;
+    f = __reduce_max_sync(0xFFFFFFFFu, max(f0, f1));
+    minf = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, min(static_cast<unsigned>(f0), static_cast<unsigned>(f1))));
+  }
   if (tid == 0) {
     int nruns = 0, tiles = 0;
     if (it.kind != kWindowRows) {
-      int f = 0, minf = 0x7FFFFFFF;
-      for (int r = 0; r < it.nr; ++r) {
-        f = max(f, sm->sees[r].f);
-        minf = min(minf, sm->sees[r].f);
-      }
       const int from = it.kind == kOwnEntries ? a.n_prefix : 0;
       Run u{sm->sees[0].run, 0, from, max(0, f - from), 0, 0, it.nr, 1, minf, 1, 0};
       if (it.kind == kPrefixEntries) u.req = 0;
@@ -462,148 +469,198 @@ struct TileWalk {
 };
 
 // ---------------------------------------------------------------------------
-// loading warps.  Thread lt has dims 16 (lt & 3) .. + 15 of every chunk, of rows lt / 4 and
-// lt / 4 + 64 of every tile.  NS chunk slots; slot users in order: fill f of a slot waits
-// for release f - 1 (released in pairs of chunks when NS == 8: the O product's dim blocks).
+// loading warps: warp c of them has chunk c (dims 64c .. 64c + 63) of every tile, lane l the
+// 16-dim group l & 3 of rows l / 4, l / 4 + 8, ...  NS chunk slots; the fills of a slot wait
+// for its release (kPairs: chunks are released in pairs, the O product's blocks of 128 dims).
 // ---------------------------------------------------------------------------
-template <int FMT, int NS>
+template <int FMT, int NS, bool kPairs>
 __device__ void load_tiles(const Item& it, ListSmem* sm, uint8_t* slots, int tile_begin, int tile_end,
                            unsigned long long spin) {
-  constexpr int kAhead = FMT == CSKV_FMT_BF16 ? 2 : 4;   // chunks in registers
-  const int lt = threadIdx.x - kSoftThreads;
-  const int row = lt >> 2, grp = lt & 3;
+  constexpr int kBatch = FMT == CSKV_FMT_BF16 ? 2 : 4;   // rows of a lane in flight beside those converted
+  const int chunk = (threadIdx.x >> 5) - kSoftThreads / 32, lane = threadIdx.x & 31;
+  const int sub = lane >> 2, grp = lane & 3;
+  uint8_t* slot = slots + (chunk % NS) * kChunk;
+  uint64_t* full = &sm->full[chunk % NS];
+  uint64_t* free_bar = &sm->free_[kPairs ? chunk >> 1 : chunk % NS];
   TileWalk walk(sm);
-  const uint8_t* cur[2];
-  const uint8_t* nxt[2] = {nullptr, nullptr};
-  int keys = 0, nkeys = 0;
-  auto resolve = [&](int tile, const uint8_t* (&p)[2], int* n) {
+  // the addresses of a tile's rows: row 32 u + lane in p[u]
+  unsigned long long p[4];
+  int keys = 0;
+  auto resolve = [&](int tile) {
     int k0;
-    walk.seek(tile, &k0, n);
+    walk.seek(tile, &k0, &keys);
+    const int req = sm->runs[walk.run].req;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = row + 64 * u;
-      p[u] = r < *n ? paged_row(it.pages, sm->runs[walk.run].req, walk.position(k0 + r), it.row_bytes).data : nullptr;
+    for (int u = 0; u < 4; ++u) {
+      const int r = 32 * u + lane;
+      const uint8_t* x = reinterpret_cast<const uint8_t*>(g_zero_row);
+      if (r < keys) {
+        const uint8_t* y = paged_row(it.pages, req, walk.position(k0 + r), it.row_bytes).data;
+        if (y != nullptr) x = y;
+        else if (chunk == 0) atomicOr(&sm->none[(tile - tile_begin) & 3][u], 1u << lane);
+      }
+      p[u] = reinterpret_cast<unsigned long long>(x);
     }
   };
-  Raw<FMT> raw[kAhead][2];
-  resolve(tile_begin, cur, &keys);
+  // two batches of raw rows take turns: one is converted while the other is in flight
+  // (copying one to the other would wait for the loads)
+  Raw<FMT> raw0[kBatch], raw1[kBatch];
+  // batch j: rows 8k + sub for k in [j * kBatch, (j + 1) * kBatch)
+  auto load = [&](int j, Raw<FMT> (&r)[kBatch]) {
+    const int pu = (j * kBatch) >> 2;
+    const unsigned long long q = pu == 0 ? p[0] : pu == 1 ? p[1] : pu == 2 ? p[2] : p[3];
 #pragma unroll
-  for (int c = 0; c < kAhead; ++c)
+    for (int u = 0; u < kBatch; ++u) {
+      const unsigned long long x = __shfl_sync(0xFFFFFFFFu, q, ((j * kBatch + u) & 3) * 8 + sub);
+      load_raw(reinterpret_cast<const uint8_t*>(x), 4 * chunk + grp, r[u]);
+    }
+  };
+  auto store = [&](int j, const Raw<FMT> (&r)[kBatch]) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) load_raw(cur[u], 4 * c + grp, raw[c][u]);
+    for (int u = 0; u < kBatch; ++u) {
+      const int row = 8 * (j * kBatch + u) + sub;
+      uint32_t w[8];
+      convert(r[u], w);
+      *reinterpret_cast<uint4*>(slot + sw128_offset(row, 2 * grp)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(slot + sw128_offset(row, 2 * grp + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  };
+  constexpr int kBatches = 16 / kBatch;
+  resolve(tile_begin);
+  load(0, raw0);
   for (int tile = tile_begin; tile < tile_end; ++tile) {
     const int i = tile - tile_begin;
-    const bool more = tile + 1 < tile_end;
-    if (more) resolve(tile + 1, nxt, &nkeys);
-    const int used = (keys + 15) & ~15;   // rows that the O product reads
-    uint32_t bad = 0;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int fill = i * (8 / NS) + c / NS;
-      if (fill > 0 && (NS != 8 || (c & 1) == 0))
-        if (!wait_bar(sm, &sm->free_[NS == 8 ? c >> 1 : c % NS], (fill - 1) & 1, spin)) return;
-      uint8_t* slot = slots + (c % NS) * kChunk;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int r = row + 64 * u;
-        uint32_t w[8];
-        const uint32_t b = convert(raw[c % kAhead][u], w);
-        if (b != 0) {   // kept out of both products; the softmax makes the key's logits NaN
-          bad |= 1u << u;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) w[x] = 0u;
-        }
-        if (r < used) {
-          *reinterpret_cast<uint4*>(slot + sw128_offset(r, 2 * grp)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(slot + sw128_offset(r, 2 * grp + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-        if (c + kAhead < 8) load_raw(cur[u], 4 * (c + kAhead) + grp, raw[c % kAhead][u]);
-        else if (more) load_raw(nxt[u], 4 * (c + kAhead - 8) + grp, raw[c % kAhead][u]);
+    const int fill = kPairs ? i : i * (8 / NS) + chunk / NS;
+    load(1, raw1);
+    if (fill > 0 && !wait_bar(sm, free_bar, (fill - 1) & 1, spin)) return;
+    __syncwarp();
+#pragma unroll 1
+    for (int j = 0; j < kBatches; j += 2) {
+      store(j, raw0);
+      if (j + 2 < kBatches) {
+        load(j + 2, raw0);
+      } else if (tile + 1 < tile_end) {
+        resolve(tile + 1);
+        load(0, raw0);
       }
-      if (c == 7) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          reinterpret_cast<uint8_t*>(&sm->kstate[i & 1][row + 64 * u])[grp] =
-              static_cast<uint8_t>((cur[u] != nullptr ? 1 : 0) | ((bad >> u) & 1) << 1);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->full[c % NS]);
+      store(j + 1, raw1);
+      if (j + 3 < kBatches) load(j + 3, raw1);
     }
-    cur[0] = nxt[0];
-    cur[1] = nxt[1];
-    keys = nkeys;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);
   }
 }
 
-template <int NS>
+template <int NS, bool kPairs>
 __device__ __forceinline__ void load_role(const Item& it, ListSmem* sm, uint8_t* slots, int b, int e,
                                           unsigned long long spin) {
-  if (it.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32) load_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32, NS>(it, sm, slots, b, e, spin);
-  else if (it.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16) load_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16, NS>(it, sm, slots, b, e, spin);
-  else load_tiles<CSKV_FMT_BF16, NS>(it, sm, slots, b, e, spin);
+  if (it.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32) load_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32, NS, kPairs>(it, sm, slots, b, e, spin);
+  else if (it.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16) load_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16, NS, kPairs>(it, sm, slots, b, e, spin);
+  else load_tiles<CSKV_FMT_BF16, NS, kPairs>(it, sm, slots, b, e, spin);
 }
 
-// The block's query rows, rotated, into the K-major chunks of Q (rows nq apart; chunk 8 holds
-// the second bf16 of the rotated dims); warps 0-7.
-__device__ __forceinline__ void load_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
-#pragma unroll 4
+// The block's query rows into the K-major chunks of Q (rows nq apart); warps 0-7.  The rows
+// come in by asynchronous copies; the last 64 dims are then rotated in place, chunk 8 holds
+// the second bf16 of each rotated value.
+__device__ __forceinline__ void request_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
+  const uint8_t* q = a.q + static_cast<size_t>(r0) * kD * 2;
+#pragma unroll 1
   for (int x = threadIdx.x; x < nq * 64; x += kSoftThreads) {
     const int r = x >> 6, c = x & 63;   // dims 8c .. 8c + 7
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < nr) v = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(r0 + r) * kD + c * 8) * 2));
     uint8_t* dst = qtile + (c >> 3) * (nq * 128) + sw128_offset(r, c & 7);
-    if (c >= 56) {
-      uint4 lo = make_uint4(0u, 0u, 0u, 0u);
-      if (r < nr) {
-        const float* cs = a.q_rope + static_cast<size_t>((r0 + r) / a.H) * 64 + (c - 56) * 8;
-        const float4 t0 = __ldg(reinterpret_cast<const float4*>(cs)), t1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
-        const float co[4] = {t0.x, t0.z, t1.x, t1.z}, si[4] = {t0.y, t0.w, t1.y, t1.w};
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-        uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
-          const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
-          w[k] = pack_bf16(z0, z1);
-          l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
-        }
-      }
-      *reinterpret_cast<uint4*>(qtile + 8 * (nq * 128) + sw128_offset(r, c & 7)) = lo;
-    }
-    *reinterpret_cast<uint4*>(dst) = v;
+    if (r < nr) cp_async16(dst, q + static_cast<size_t>(x) * 16);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
+__device__ __forceinline__ void rotate_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
+  cp_async_wait_all();
+  soft_sync();
+#pragma unroll 1
+  for (int x = threadIdx.x; x < nq * 8; x += kSoftThreads) {
+    const int r = x >> 3, c = x & 7;
+    uint4* hi = reinterpret_cast<uint4*>(qtile + 7 * (nq * 128) + sw128_offset(r, c));
+    uint4 v = *hi, lo = make_uint4(0u, 0u, 0u, 0u);
+    if (r < nr) {
+      const float* cs = a.q_rope + static_cast<size_t>((r0 + r) / a.H) * 64 + c * 8;
+      const float4 t0 = __ldg(reinterpret_cast<const float4*>(cs)), t1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
+      const float co[4] = {t0.x, t0.z, t1.x, t1.z}, si[4] = {t0.y, t0.w, t1.y, t1.w};
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+      uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
+        const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
+        w[k] = pack_bf16(z0, z1);
+        l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
+      }
+      *hi = v;
+    }
+    *reinterpret_cast<uint4*>(qtile + 8 * (nq * 128) + sw128_offset(r, c)) = lo;
+  }
+  fence_proxy_async_smem();
+}
 
-// S^T of one chunk: 128 keys x nq rows (TMEM d), K = 64 dims
-__device__ __forceinline__ void issue_s_chunk(uint32_t d, uint32_t kslot, uint32_t qtile, int c, int nq, uint32_t id) {
-  const uint64_t dk = smem_desc_sw128(kslot, 16, 1024);
-  const uint64_t dq = smem_desc_sw128(qtile + c * (nq * 128), 16, 1024);
+// S^T of chunk c: 128 keys x nq rows (TMEM d), K = 64 dims; dk, dq: the chunk's descriptors,
+// dl: those of the query's second halves, on the same keys' rotated dims
+__device__ __forceinline__ void issue_s_chunk(uint32_t d, uint64_t dk, uint64_t dq, uint64_t dl, int c, uint32_t id) {
+  if (c == 0) mma_set(d, dk, dq, id);
+  else mma_add(d, dk, dq, id);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) mma_f16(d, dk + 2 * k, dq + 2 * k, id, c > 0 || k > 0);
-  if (c == 7) {   // the query's second halves on the same keys' rotated dims
-    const uint64_t dl = smem_desc_sw128(qtile + 8 * (nq * 128), 16, 1024);
+  for (int k = 1; k < 4; ++k) mma_add(d, dk + 2 * k, dq + 2 * k, id);
+  if (c == 7) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mma_f16(d, dk + 2 * k, dl + 2 * k, id, 1);
+    for (int k = 0; k < 4; ++k) mma_add(d, dk + 2 * k, dl + 2 * k, id);
   }
 }
 
 // ---------------------------------------------------------------------------
 // the attention kernel
 // ---------------------------------------------------------------------------
-// softmax of one key's logits z (nc rows from column cb), and the epilogue's helpers
-__device__ __forceinline__ void mask_logits(const ListSmem* sm, int run, int pos, uint32_t state, int cb, int nc,
-                                            float scale, float (&z)[32]) {
-  const bool exists = (state & 0x01010101u) == 0x01010101u;
-  const bool fine = (state & 0x02020202u) == 0u;
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    if (c < nc) {
-      const RowSees s = sm->sees[cb + c];
-      const bool see = exists && s.run == run && (pos < s.f || (pos >= s.lo && pos <= s.hi));
-      z[c] = see ? (fine ? z[c] * scale : __int_as_float(0x7FC00000)) : -INFINITY;
-    }
+// Bits [0, n) of a word, for n of any size.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// Which of a warp's 32 rows see which of its 32 keys: the lane with column c makes row cb + c's
+// bits over the keys k0 .. k0 + 31 of the run (the seen positions are at most three stretches
+// of key indices), then the 32 x 32 bit matrix is transposed; lane k ends with key k0 + k's
+// bits over the rows.
+__device__ __forceinline__ uint32_t seen_by(const ListSmem* sm, int run, int k0, int col) {
+  const int lane = threadIdx.x & 31;
+  const RowSees s = sm->sees[col];
+  const Run& u = sm->runs[run];
+  uint32_t x = 0;
+  if (s.run == run) {
+    const int shift = u.f1 - u.base - k0;   // bit of a position in the second stretch
+    const uint32_t second = ~low_bits(u.f1 - k0);
+    x = low_bits(min(s.f, u.f1) - k0);
+    x |= second & low_bits(s.f + shift);
+    x |= second & low_bits(s.hi + 1 + shift) & ~low_bits(s.lo + shift);
   }
+#pragma unroll
+  for (int j = 16; j >= 1; j >>= 1) {
+    const uint32_t m = j == 16 ? 0x0000FFFFu : j == 8 ? 0x00FF00FFu : j == 4 ? 0x0F0F0F0Fu : j == 2 ? 0x33333333u : 0x55555555u;
+    const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, x, j);
+    x = (lane & j) ? (x & ~m) | ((y & ~m) >> j) : (x & m) | ((y & m) << j);
+  }
+  return x;
+}
+
+// A key row with a value that is not finite makes every logit of its key not finite, so one
+// column is looked at, and only then the row.  Such a row leaves the tile (zeros, for the O
+// product) and the key's logits become NaN.
+__device__ __noinline__ bool unfit_row(const uint8_t* ktile, int key) {
+  uint32_t bad = 0;
+  for (int x = 0; x < 64; ++x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(ktile + (x >> 3) * kChunk + sw128_offset(key, x & 7));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // an exponent of all ones carries into the sign bit when its lowest bit is added
+    for (int i = 0; i < 4; ++i) bad |= ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+  }
+  return bad != 0u;
+}
+__device__ __noinline__ void clear_row(uint8_t* ktile, int key) {
+  for (int x = 0; x < 64; ++x)
+    *reinterpret_cast<uint4*>(ktile + (x >> 3) * kChunk + sw128_offset(key, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_constant__ ListArgs a) {
@@ -618,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
   const int nq = (it.nr + 15) & ~15;
 
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(&sm->full[i], kLoadThreads / 32);
+    for (int i = 0; i < 8; ++i) mbar_init(&sm->full[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&sm->free_[i], 1);
     mbar_init(&sm->bar_s[0], 2);
     mbar_init(&sm->bar_p[0], kSoftThreads / 32);
@@ -627,49 +684,62 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
     fence_mbar_init();
   }
   if (warp == 16) tmem_alloc(&sm->tmem, 512);
+  if (warp < 8) request_queries(a, it.r0, it.nr, nq, qtile);
   tc_fence_before();
   plan_block(a, it, sm);
   tc_fence_after();
-  const uint32_t tmem = sm->tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
   const int begin = static_cast<int>(static_cast<long long>(sm->ntiles) * it.split / it.nsplit);
   const int end = static_cast<int>(static_cast<long long>(sm->ntiles) * (it.split + 1) / it.nsplit);
   const int nt = end - begin;
 
   if (warp >= 8 && warp < 16) {
-    if (nt > 0) load_role<8>(it, sm, ktile, begin, end, a.spin);
+    if (nt > 0) load_role<8, true>(it, sm, ktile, begin, end, a.spin);
   } else if (warp == 16) {
-    if (lane == 0 && nt > 0) {
+    if (nt > 0 && elect_lane()) {
       const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
       const uint32_t ido = make_idesc(1, 1, 1, 1, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
+      const uint64_t dk = smem_desc_sw128(smem_u32(ktile), 16, 1024);
+      const uint64_t dq = smem_desc_sw128(smem_u32(qtile), 16, 1024);
       const uint64_t dv = smem_desc_sw128(smem_u32(ktile), kChunk, 1024);
       const uint64_t dp = smem_desc_sw128(smem_u32(ptile), kChunk, 1024);
+      const uint32_t qstep = nq * 8;   // a chunk of Q, in the descriptors' 16-byte units
       TileWalk walk(sm);
       bool ok = wait_bar(sm, &sm->bar_q, 0, a.spin);
       for (int i = 0; i < nt && ok; ++i) {
-        for (int c = 0; c < 8 && ok; ++c) {
-          ok = wait_bar(sm, &sm->full[c], i & 1, a.spin);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          ok = ok && wait_bar(sm, &sm->full[c], i & 1, a.spin);
           tc_fence_after();
-          if (ok) issue_s_chunk(tmem + kTmemS, smem_u32(ktile) + c * kChunk, smem_u32(qtile), c, nq, ids);
+          if (ok) issue_s_chunk(tmem + kTmemS, dk + c * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
         }
         mma_commit(&sm->bar_s[0]);
-        mbar_arrive(&sm->bar_s[0]);   // hands on what the loading warps wrote (kstate)
+        mbar_arrive(&sm->bar_s[0]);   // hands on what the loading warps wrote (none)
         ok = ok && wait_bar(sm, &sm->bar_p[0], i & 1, a.spin);
         if (!ok) break;
         tc_fence_after();
         int k0, n;
         walk.seek(begin + i, &k0, &n);
         const int ks = (n + 15) >> 4;
-#pragma unroll 1
+#pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
-          for (int k = 0; k < ks; ++k)
-            mma_f16(tmem + mb * kRows, dv + mb * (kChunk >> 3) + k * 128, dp + k * 128, ido, i > 0 || k > 0);
+          const uint64_t dvb = dv + mb * (kChunk >> 3);
+          if (i == 0) mma_set(tmem + mb * kRows, dvb, dp, ido);
+          else mma_add(tmem + mb * kRows, dvb, dp, ido);
+          if (ks == 8) {
+#pragma unroll
+            for (int k = 1; k < 8; ++k) mma_add(tmem + mb * kRows, dvb + k * 128, dp + k * 128, ido);
+          } else {
+#pragma unroll 1
+            for (int k = 1; k < ks; ++k) mma_add(tmem + mb * kRows, dvb + k * 128, dp + k * 128, ido);
+          }
           mma_commit(&sm->free_[mb]);
         }
       }
     }
+    __syncwarp();
   } else {
-    load_queries(a, it.r0, it.nr, nq, qtile);
-    fence_proxy_async_smem();
+    rotate_queries(a, it.r0, it.nr, nq, qtile);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm->bar_q);
     const int quarter = warp & 3, half = warp >> 2;
@@ -693,63 +763,86 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
       int k0, n;
       walk.seek(begin + i, &k0, &n);
       const Run& u = sm->runs[walk.run];
-      const uint32_t state = key < n ? sm->kstate[i & 1][key] : 0u;
       // all 128 keys seen by all rows: inside every window, or all first rows
       const int pa = walk.position(k0), pb = walk.position(k0 + n - 1);
-      const bool plain = u.whole && n == kKeys && ((pb < u.min_f) || (pa >= u.max_lo && pb <= u.min_hi && pb - pa == kKeys - 1));
-      if (plain && state == 0x01010101u) {
+      const uint32_t none = sm->none[i & 3][quarter];
+      const bool plain = u.whole && n == kKeys && none == 0u &&
+                         ((pb < u.min_f) || (pa >= u.max_lo && pb <= u.min_hi && pb - pa == kKeys - 1));
+      bool unfit = false;
+      if (nc > 0 && key < n && !(fabsf(z[0]) < INFINITY)) {
+        unfit = unfit_row(ktile, key);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) z[c] *= a.scale_log2;
-      } else {
-        mask_logits(sm, walk.run, walk.position(k0 + key), state, cb, nc, a.scale_log2, z);
+        for (int c = 0; c < 32; ++c)
+          if (unfit) z[c] = __int_as_float(0x7FC00000);
+      }
+      __syncwarp();
+      if (!plain && nc > 0) {
+        uint32_t bits = seen_by(sm, walk.run, k0 + quarter * 32, cb + lane);
+        if (key >= n || ((none >> lane) & 1u) != 0u) bits = 0u;
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (((bits >> c) & 1u) == 0u) z[c] = -INFINITY;
       }
       bool above = false;
 #pragma unroll
       for (int c = 0; c < 32; c += 4) {
         if (c < nc) {
-          const float4 m = *reinterpret_cast<const float4*>(&sm->m[cb + c]);
-          above = above || z[c] > m.x + kSlack || z[c + 1] > m.y + kSlack || z[c + 2] > m.z + kSlack || z[c + 3] > m.w + kSlack;
+          const float4 m = *reinterpret_cast<const float4*>(&sm->limit[cb + c]);
+          above |= (z[c] > m.x) | (z[c + 1] > m.y) | (z[c + 2] > m.z) | (z[c + 3] > m.w);
         }
       }
-      if (soft_any(above)) {   // some row's reference moves: the tile's maxima, exactly
-        float mine = -INFINITY;
+      const bool moves = soft_any(above);
+      if (unfit && half == 0) clear_row(ktile, key);   // both halves have looked at it
+      if (moves) {   // some row's reference moves: the tile's maxima, exactly
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          if (c < nc) {
-            const float v = warp_max(z[c]);
-            if (lane == c) mine = v;
+        for (int g = 0; g < 32; g += 16) {
+          if (g < nc) {
+            float t[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) t[c] = z[g + c];
+            const float mine = reduce_columns(t, [](float x, float y) { return fmaxf(x, y); });
+            if ((lane & 1) == 0) sm->part[quarter][cb + g + (lane >> 1)] = mine;
           }
         }
-        if (lane < nc) sm->part[quarter][cb + lane] = mine;
         soft_sync();
         if (tid < nq) {
-          const float old = sm->m[tid];
+          const float old = sm->m[tid], old_sub = sm->msub[tid];
           const float now = fmaxf(fmaxf(fmaxf(sm->part[0][tid], sm->part[1][tid]), fmaxf(sm->part[2][tid], sm->part[3][tid])), old);
-          sm->fac[tid] = old == -INFINITY ? 0.f : exp2f(old - now);
+          const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
+          sm->fac[tid] = old == -INFINITY ? 0.f : exp2f(old_sub - sub);
           sm->m[tid] = now;
-          sm->msub[tid] = now == -INFINITY ? 0.f : now;
+          sm->limit[tid] = now + a.slack;
+          sm->msub[tid] = sub;
         }
         soft_sync();
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (c < nc) l[c] *= sm->fac[cb + c];
-        if (i > 0) {   // the S commit says that the O products so far are complete
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-#pragma unroll 1
-            for (int g = 0; g < nq; g += 32) {
-              float o[32];
-              const uint32_t at = tmem + tlane + (half * 2 + x) * kRows + g;
-              tmem_ld32(at, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] *= sm->fac[g + c];
-              tmem_st32(at, o);
-              tmem_wait_st();
-            }
+        for (int c = 0; c < 32; c += 4) {
+          if (c < nc) {
+            const float4 f = *reinterpret_cast<const float4*>(&sm->fac[cb + c]);
+            l[c] *= f.x;
+            l[c + 1] *= f.y;
+            l[c + 2] *= f.z;
+            l[c + 3] *= f.w;
           }
         }
+        if (i > 0) {   // the S commit says that the O products so far are complete
+#pragma unroll 1
+          for (int x = 0; x < 8; ++x) {   // this warp's two blocks of dims, 16 rows at a time
+            const int g = (x & 3) * 16;
+            if (g < nq) {
+              float o[16];
+              const uint32_t at = tmem + tlane + (half * 2 + (x >> 2)) * kRows + g;
+              tmem_ld16(at, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 16; ++c) o[c] *= sm->fac[g + c];
+              tmem_st16(at, o);
+            }
+          }
+          tmem_wait_st();
+        }
       }
+      if (lane == 0 && none != 0u && half == 0) sm->none[i & 3][quarter] = 0u;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         if (8 * g < nc) {
@@ -759,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
           float p[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            p[c] = exp2f(z[8 * g + c] - mm[c]);
+            p[c] = exp2_fast(fmaf(z[8 * g + c], a.scale_log2, -mm[c]));
             l[8 * g + c] += p[c];
           }
           *reinterpret_cast<uint4*>(ptile + sw128_offset(key, half * 4 + g)) =
@@ -774,24 +867,21 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
     if (nt > 0 && ok) wait_bar(sm, &sm->free_[3], (nt - 1) & 1, a.spin);
     __syncwarp();
     tc_fence_after();
-    // ---- the rows' sums over the 128 keys: lane c ends with row cb + c
-    {
+    // ---- the rows' sums over the 128 keys: lanes 2c and 2c + 1 end with row cb + g + c
 #pragma unroll
-      for (int w = 16; w >= 1; w >>= 1) {
-        const bool hi = (lane & w) != 0;
+    for (int g = 0; g < 32; g += 16) {
+      if (g < nc) {
+        float t[16];
 #pragma unroll
-        for (int j = 0; j < w; ++j) {
-          const float send = hi ? l[j] : l[j + w];
-          const float keep = hi ? l[j + w] : l[j];
-          l[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
-        }
+        for (int c = 0; c < 16; ++c) t[c] = l[g + c];
+        const float mine = reduce_columns(t, [](float x, float y) { return x + y; });
+        if ((lane & 1) == 0) sm->part[quarter][cb + g + (lane >> 1)] = mine;
       }
-      if (lane < nc) sm->part[quarter][cb + lane] = l[0];
     }
     soft_sync();
     if (tid < nq) {
       const float sum = ((sm->part[0][tid] + sm->part[1][tid]) + sm->part[2][tid]) + sm->part[3][tid];
-      const float m = sm->m[tid];
+      const float m = sm->m[tid] == -INFINITY ? -INFINITY : sm->msub[tid];
       float f = 0.f;
       if (tid < it.nr) {
         const size_t row = static_cast<size_t>(it.r0) + tid;
@@ -813,53 +903,53 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
       sm->fac[tid] = f;
     }
     soft_sync();
-    // ---- O^T out: a thread has dim d of up to 32 rows at a time
+    // ---- O^T out: a thread has dim d of 16 rows at a time
 #pragma unroll 1
-    for (int x = 0; x < 2; ++x) {
-      const int mb = half * 2 + x;
+    for (int x = 0; x < 8; ++x) {
+      const int mb = half * 2 + (x >> 2), g = (x & 3) * 16;
+      if (g >= it.nr) continue;
       const int d = mb * 128 + quarter * 32 + lane;
-#pragma unroll 1
-      for (int g = 0; g < nq; g += 32) {
-        const int cols = min(32, nq - g);
-        float o[32];
-        if (nt > 0) {
-          tmem_ld_cols(tmem + tlane + mb * kRows + g, cols, o);
-          tmem_wait_ld();
-        } else {
+      float o[16];
+      if (nt > 0) {
+        tmem_ld16(tmem + tlane + mb * kRows + g, o);
+        tmem_wait_ld();
+      } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0.f;
+        for (int c = 0; c < 16; ++c) o[c] = 0.f;
+      }
+      if (a.parts > 1) {
+        float* to = a.opart + ((static_cast<size_t>(it.r0) + g) * a.parts + it.part) * kD + d;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          if (g + c < it.nr) to[static_cast<size_t>(c) * a.parts * kD] = o[c];
+        continue;
+      }
+#pragma unroll
+      for (int c = 0; c < 16; c += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&sm->fac[g + c]);
+        o[c] *= f.x;
+        o[c + 1] *= f.y;
+        o[c + 2] *= f.z;
+        o[c + 3] *= f.w;
+      }
+      if (mb == 3 && quarter >= 2) {   // dims 448..511, turned back
+        const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
+        const int t0 = (it.r0 + g) / a.H, t1 = (it.r0 + min(g + 16, it.nr) - 1) / a.H;
+        float2 w = __ldg(cs + static_cast<size_t>(t0) * 32);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          if (t1 != t0) w = __ldg(cs + static_cast<size_t>((it.r0 + min(g + c, it.nr - 1)) / a.H) * 32);
+          const float y = __shfl_xor_sync(0xFFFFFFFFu, o[c], 1);
+          o[c] = (lane & 1) ? o[c] * w.x - y * w.y : o[c] * w.x + y * w.y;
         }
-        if (a.parts > 1) {
+      }
+      // even lanes store dims d, d + 1 of row c, odd lanes dims d - 1, d of row c + 1
+      uint8_t* to = a.out + ((static_cast<size_t>(it.r0) + g + (lane & 1)) * kD + (d & ~1)) * 2;
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (g + c < it.nr)
-              a.opart[((static_cast<size_t>(it.r0) + g + c) * a.parts + it.part) * kD + d] = o[c];
-        } else {
-          const bool turn = mb == 3 && quarter >= 2;   // dims 448..511
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            if (g + c < it.nr) {
-              float v0 = o[c] * sm->fac[g + c], v1 = o[c + 1] * sm->fac[g + c + 1];
-              if (turn) {
-                const int k = (d - (kD - 64)) >> 1;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  float& v = y == 0 ? v0 : v1;
-                  const int r = min(it.r0 + g + c + y, it.r0 + it.nr - 1);
-                  const float2 cs = __ldg(reinterpret_cast<const float2*>(a.q_rope + static_cast<size_t>(r / a.H) * 64) + k);
-                  const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-                  v = (lane & 1) ? v * cs.x - w * cs.y : v * cs.x + w * cs.y;
-                }
-              }
-              // even lanes store dims d, d + 1 of row c, odd lanes dims d - 1, d of row c + 1
-              const float other = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? v0 : v1, 1);
-              const uint32_t w = (lane & 1) ? pack_bf16(other, v1) : pack_bf16(v0, other);
-              const int r = g + c + (lane & 1);
-              if (r < it.nr)
-                *reinterpret_cast<uint32_t*>(a.out + ((static_cast<size_t>(it.r0) + r) * kD + (d & ~1)) * 2) = w;
-            }
-          }
-        }
+      for (int c = 0; c < 16; c += 2) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? o[c] : o[c + 1], 1);
+        const uint32_t w = (lane & 1) ? pack_bf16(other, o[c + 1]) : pack_bf16(o[c], other);
+        if (g + c + (lane & 1) < it.nr) *reinterpret_cast<uint32_t*>(to + c * (kD * 2)) = w;
       }
     }
   }
@@ -921,8 +1011,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // heads.  Up to 128 heads are the MMA columns, two S buffers in TMEM, four chunk slots
 // (released as soon as the chunk's products are complete).
 // ---------------------------------------------------------------------------
-constexpr int kWeightSlots = 4;
-
+template <int kWeightSlots>
 __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ ListArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -936,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 
   if (tid == 0) {
     for (int i = 0; i < kWeightSlots; ++i) {
-      mbar_init(&sm->full[i], kLoadThreads / 32);
+      mbar_init(&sm->full[i], 1);
       mbar_init(&sm->free_[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -955,11 +1044,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     const float v = tid < a.H ? a.lse_in[static_cast<size_t>(b) * a.H + tid] : -INFINITY;
     lse[tid] = v == -INFINITY ? INFINITY : v * kLog2e;
   }
+  if (tid < 16) (&sm->none[0][0])[tid] = 0u;
   if (warp == 16) tmem_alloc(&sm->tmem, 256);
+  if (warp < 8) request_queries(a, b * a.H, a.H, nq, qtile);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm->tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
   const int begin = static_cast<int>(static_cast<long long>(sm->ntiles) * split / a.split);
   const int end = static_cast<int>(static_cast<long long>(sm->ntiles) * (split + 1) / a.split);
   const int nt = end - begin;
@@ -970,29 +1061,33 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       it.fmt = a.kv.fmt;
       it.row_bytes = a.row_bytes;
       it.pages = a.kv;
-      load_role<kWeightSlots>(it, sm, slots, begin, end, a.spin);
+      load_role<kWeightSlots, false>(it, sm, slots, begin, end, a.spin);
     } else if (warp == 16) {
-      if (lane == 0) {
+      if (elect_lane()) {
         const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
+        const uint64_t dk = smem_desc_sw128(smem_u32(slots), 16, 1024);
+        const uint64_t dq = smem_desc_sw128(smem_u32(qtile), 16, 1024);
+        const uint32_t qstep = nq * 8;
         bool ok = wait_bar(sm, &sm->bar_q, 0, a.spin);
         for (int i = 0; i < nt && ok; ++i) {
           const int buf = i & 1;
           if (i >= 2) ok = wait_bar(sm, &sm->bar_p[buf], ((i >> 1) - 1) & 1, a.spin);
           tc_fence_after();
-          for (int c = 0; c < 8 && ok; ++c) {
-            const int fill = i * 2 + (c >> 2);
-            ok = wait_bar(sm, &sm->full[c & 3], fill & 1, a.spin);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int slot = c % kWeightSlots, fill = i * (8 / kWeightSlots) + c / kWeightSlots;
+            ok = ok && wait_bar(sm, &sm->full[slot], fill & 1, a.spin);
             tc_fence_after();
-            if (ok) issue_s_chunk(tmem + buf * 128, smem_u32(slots) + (c & 3) * kChunk, smem_u32(qtile), c, nq, ids);
-            mma_commit(&sm->free_[c & 3]);
+            if (ok) issue_s_chunk(tmem + buf * 128, dk + slot * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
+            mma_commit(&sm->free_[slot]);
           }
           mma_commit(&sm->bar_s[buf]);
-          mbar_arrive(&sm->bar_s[buf]);   // hands on what the loading warps wrote (kstate)
+          mbar_arrive(&sm->bar_s[buf]);   // hands on what the loading warps wrote (none)
         }
       }
+      __syncwarp();
     } else {
-      load_queries(a, b * a.H, a.H, nq, qtile);
-      fence_proxy_async_smem();
+      rotate_queries(a, b * a.H, a.H, nq, qtile);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->bar_q);
       const int quarter = warp & 3, half = warp >> 2;
@@ -1015,22 +1110,20 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 #pragma unroll
           for (int k = 0; k < 16; k += 4) {
             const float4 s = *reinterpret_cast<const float4*>(&lse[c + k]);
-            w += (exp2f(z[k] * a.scale_log2 - s.x) + exp2f(z[k + 1] * a.scale_log2 - s.y)) +
-                 (exp2f(z[k + 2] * a.scale_log2 - s.z) + exp2f(z[k + 3] * a.scale_log2 - s.w));
+            w += (exp2_fast(fmaf(z[k], a.scale_log2, -s.x)) + exp2_fast(fmaf(z[k + 1], a.scale_log2, -s.y))) +
+                 (exp2_fast(fmaf(z[k + 2], a.scale_log2, -s.z)) + exp2_fast(fmaf(z[k + 3], a.scale_log2, -s.w)));
           }
         }
         tc_fence_before();
-        // (the state of tile i + 2 is written after its S product, so after this release)
         const int k = (begin + i) * kKeys + key;
-        const uint32_t state = sm->kstate[buf][key];
+        const uint32_t none = sm->none[i & 3][quarter];
         if (half == 1) sm->part[buf][key] = w;
         soft_sync();
+        if (half == 0 && lane == 0 && none != 0u) sm->none[i & 3][quarter] = 0u;
         if (lane == 0) mbar_arrive(&sm->bar_p[buf]);
         if (half == 0 && k < sm->runs[0].nkeys) {
           if (groups > 1) w += sm->part[buf][key];
-          const bool exists = (state & 0x01010101u) == 0x01010101u;
-          if (!exists) w = 0.f;
-          else if (state & 0x02020202u) w = __int_as_float(0x7FC00000);
+          if ((none >> lane) & 1u) w = 0.f;
           const long long j = a.first + k;
           a.acc_out[b * a.acc_out_stride + j] = a.decay * a.acc[b * a.acc_stride + j] + w;
         }
@@ -1051,9 +1144,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 constexpr size_t kAttnSmem = 1024 + 9 * size_t(kChunk) + 9 * kRows * 128 + sizeof(ListSmem);
 static_assert(kAttnSmem <= 227 * 1024, "one block per SM");
 
+// eight chunk slots where the queries leave room for them (H <= 64)
+int weight_slots(int H) { return H <= kRows ? 8 : 4; }
+
 size_t weights_smem(int H) {
   const int nq = (H + 15) & ~15;
-  return 1024 + kWeightSlots * size_t(kChunk) + 9 * size_t(nq) * 128 + sizeof(ListSmem) + 128 * sizeof(float);
+  return 1024 + weight_slots(H) * size_t(kChunk) + 9 * size_t(nq) * 128 + sizeof(ListSmem) + 128 * sizeof(float);
 }
 
 __host__ __device__ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1167,6 +1263,7 @@ ListArgs common_args(const void* q, const cskv_paged& kv, const float* sink, flo
   a.H = H;
   a.out = static_cast<uint8_t*>(out);
   a.lse = lse;
+  a.slack = kSlack / a.scale_log2;
   a.spin = spin_limit();
   return a;
 }
@@ -1261,10 +1358,10 @@ cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32
   });
   a.split = shares(tiles, len);
   const size_t smem = weights_smem(H);
-  const cudaError_t e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+  auto kernel = weight_slots(H) == 8 ? weights_kernel<8> : weights_kernel<4>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  weights_kernel<<<static_cast<unsigned>(B) * a.split, kThreads, smem, stream>>>(a);
+  kernel<<<static_cast<unsigned>(B) * a.split, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
