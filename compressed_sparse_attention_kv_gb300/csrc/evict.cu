@@ -1,18 +1,41 @@
 // Eviction of cache entries by accumulated attention weight (cskvx_evict).
 //
-// Per request: the budget-th largest key (protected entries above every weight), by a
-// radix select over order-preserving 32-bit keys, ties to the lower slot; then one
-// ordered scan that lists the given-up slots below m (holes) and the kept slots from m
-// on (movers), pairwise; then the movers' rows are copied into the holes.  A mover's
-// slot is at least m and a hole's below m, so no copy reads what another one writes.
+// Per request: the m-th largest key, m the budget (order-preserving 32-bit keys of the
+// weights, protected entries above every weight), by a radix select of three digits
+// (11 + 11 + 10 bits); ties go to the lower slot; then an ordered pass pairs the given-up
+// slots below m (holes) with the kept slots from m on (movers), both ascending; then the
+// movers' rows are copied into the holes.  A mover's slot is at least m and a hole's below m,
+// so no copy reads what another one writes, and the order of the copies does not matter.
+//
+// What it needs: a weight and an age read per entry (8 bytes) and two row copies per evicted
+// entry of the head; the selection is latency-bound (a request's 65,536 entries are 0.5 MB),
+// the copies are bound by HBM.
+//
+// A request is selected by one cluster of 1, 2, 4 or 8 blocks, each with a slice of the
+// entries whose keys it keeps in shared memory (a slice too large for it is read again, from
+// L2, for every digit).  Histograms of the blocks are added up through distributed shared
+// memory; every block takes the same decision.  Warps walk contiguous stretches with
+// ballots, so that ranks need one scan over the warps' counts.  Few pairs are copied by the
+// cluster itself; many by a second kernel over the whole device.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace cskv {
 
 namespace {
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kSliceTarget = 4096;       // entries per block before a request takes another block
+constexpr int kKeysInSmem = 48 * 1024;   // entries of a slice whose keys fit in shared memory
+constexpr int kFusedPairs = 512;         // pairs that the selecting cluster copies itself
 
 struct EvictArgs {
   cskv_paged cache[4];
@@ -33,7 +56,7 @@ struct EvictArgs {
   int32_t* npairs;   // [B]
   int32_t* hole;     // [B, max_pairs]
   int32_t* mover;    // [B, max_pairs]
-  int max_pairs;
+  int max_pairs, fused, cached;
 };
 
 __host__ __device__ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -46,31 +69,46 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// inclusive scan of one value per thread over the block; *total = the sum
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xFFFFFFFFu, v, o);
-    if (lane >= o) v += x;
+struct SelSmem {
+  int hist[2048];
+  int sums[kSelWarps];
+  int warp_a[kSelWarps], warp_b[kSelWarps];
+  int newest;                // of the slice, then of the request
+  int digit, need;
+  int total_a, total_b;      // of the slice
+};
+
+// Copies the rows of pair (to, from) of request b in every cache; one warp.
+__device__ __forceinline__ void move_pair(const EvictArgs& a, int b, int to, int from, int lane) {
+  for (int c = 0; c < a.ncaches; ++c) {
+    const cskv_paged& p = a.cache[c];
+    const RowPtr d = paged_row(p, b, to, a.row_bytes[c]), s = paged_row(p, b, from, a.row_bytes[c]);
+    if (d.data == nullptr || s.data == nullptr) continue;
+    const bool split = p.fmt == CSKV_FMT_FP8_E4M3_ROWSCALE_PAGESPLIT || p.fmt == CSKV_FMT_FP4_E2M1_E8M0_HADAMARD_PAGESPLIT;
+    const int bytes = split ? a.row_bytes[c] - 4 : a.row_bytes[c];
+    if ((bytes & 15) == 0) {   // rows start on 16 bytes then (128 and 64 bytes of page-split codes too)
+      uint4 v[2];
+      const int n = bytes >> 4;   // at most 64
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (lane + 32 * u < n) v[u] = reinterpret_cast<const uint4*>(s.data)[lane + 32 * u];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (lane + 32 * u < n) reinterpret_cast<uint4*>(d.data)[lane + 32 * u] = v[u];
+    } else {                   // 132 or 72 bytes
+      for (int x = lane; x < bytes >> 2; x += 32)
+        reinterpret_cast<uint32_t*>(d.data)[x] = reinterpret_cast<const uint32_t*>(s.data)[x];
+    }
+    if (split && lane == 0) *reinterpret_cast<uint32_t*>(d.scale) = *reinterpret_cast<const uint32_t*>(s.scale);
   }
-  if (lane == 31) warp_sums[w] = v;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) {
-    if (i < w) before += warp_sums[i];
-    all += warp_sums[i];
-  }
-  *total = all;
-  __syncthreads();
-  return v + before;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[32];
-  __shared__ int s_newest, s_need;
-  __shared__ uint32_t s_prefix;
-  const int b = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ uint32_t keys[];   // the slice's keys, if they fit
+  __shared__ SelSmem sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
+  const int b = blockIdx.x / blocks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int n = a.n_entries[b];
   if (n < 0 || n > a.max_entries) {
     if (tid == 0) set_err(CSKV_ERR_BOUNDS);
@@ -82,96 +120,193 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   int32_t* src = a.src + (long long)b * a.budget;
   int32_t* hole = a.hole + (long long)b * a.max_pairs;
   int32_t* mover = a.mover + (long long)b * a.max_pairs;
-  if (n <= a.budget) {
-    for (int i = tid; i < a.budget; i += blockDim.x) src[i] = i < n ? i : -1;
-    if (tid == 0) a.npairs[b] = 0;
-  } else {
-    // newest age
-    if (tid == 0) { s_newest = INT32_MIN; s_prefix = 0; s_need = m; }
+  // the blocks' slices: contiguous, whole warp stretches of 32
+  const int per_warp = (((n + blocks - 1) / blocks + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int slice0 = min(n, rank * per_warp * kSelWarps), slice1 = min(n, (rank + 1) * per_warp * kSelWarps);
+  const int w0 = min(slice1, slice0 + warp * per_warp), w1 = min(slice1, w0 + per_warp);
+  const bool acc_in_place = a.acc_out == a.acc, age_in_place = a.age_out == a.age;
+  int pairs = 0;
+
+  if (n > a.budget) {
+    const bool aged = age != nullptr && a.recent > 0;
+    if (tid == 0) sm.newest = INT32_MIN;
     __syncthreads();
-    if (age != nullptr && a.recent > 0) {
+    if (aged) {   // the newest age of the request
       int mx = INT32_MIN;
-      for (int i = tid; i < n; i += blockDim.x) mx = max(mx, age[i]);
+      for (int i = slice0 + tid; i < slice1; i += kSelThreads) mx = max(mx, age[i]);
       mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-      if ((tid & 31) == 0) atomicMax(&s_newest, mx);
+      if (lane == 0) atomicMax(&sm.newest, mx);
+      cluster.sync();
+      mx = INT32_MIN;
+      for (int r = 0; r < blocks; ++r) mx = max(mx, *cluster.map_shared_rank(&sm.newest, r));
+      cluster.sync();
+      if (tid == 0) sm.newest = mx;
       __syncthreads();
     }
-    const long long bar = static_cast<long long>(s_newest) - a.recent;
-    auto key_of = [&](int i) -> uint32_t {
-      if (i < a.fixed || (age != nullptr && a.recent > 0 && age[i] > bar)) return 0xFFFFFFFFu;
+    const long long bar = static_cast<long long>(sm.newest) - a.recent;
+    auto make_key = [&](int i) -> uint32_t {
+      if (i < a.fixed || (aged && age[i] > bar)) return 0xFFFFFFFFu;
       return weight_key(acc[i]);
     };
-    // the m-th largest key, eight bits at a time from the top
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      const uint32_t prefix = s_prefix;
-      for (int i = tid; i < n; i += blockDim.x) {
-        const uint32_t k = key_of(i);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int need = s_need, d = 255;
-        while (hist[d] < need) need -= hist[d--];
-        s_need = need;
-        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
-      }
+    const bool cached = a.cached != 0;
+    if (cached) {
+      for (int i = slice0 + tid; i < slice1; i += kSelThreads) keys[i - slice0] = make_key(i);
       __syncthreads();
     }
-    const uint32_t T = s_prefix;
-    const int ties = s_need;   // of the keys equal to T, this many (the lowest slots) stay
-    int ties_before = 0, holes = 0, movers = 0;
-    for (int i0 = 0; i0 < n; i0 += blockDim.x) {
-      const int i = i0 + tid;
-      const uint32_t k = i < n ? key_of(i) : 0u;
-      int total;
-      const int tie = i < n && k == T ? 1 : 0;
-      const int tr = block_scan(tie, warp_sums, &total) + ties_before;
-      ties_before += total;
-      const bool keep = i < n && (k > T || (tie && tr <= ties));
-      const int is_hole = i < m && !keep ? 1 : 0;
-      const int hr = block_scan(is_hole, warp_sums, &total) + holes;
-      holes += total;
-      const int is_mover = i >= m && keep ? 1 : 0;
-      const int mr = block_scan(is_mover, warp_sums, &total) + movers;
-      movers += total;
-      if (is_hole) hole[hr - 1] = i;
-      else if (i < m) src[i] = i;
-      if (is_mover) mover[mr - 1] = i;
+    auto key_of = [&](int i) -> uint32_t { return cached ? keys[i - slice0] : make_key(i); };
+    // the m-th largest key, digit by digit from the top
+    uint32_t prefix = 0, mask = 0;
+    int need = m;
+#pragma unroll 1
+    for (int d = 0; d < 3; ++d) {
+      const int bits = d == 2 ? 10 : 11, shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+      const int bins = 1 << bits;
+      for (int x = tid; x < bins; x += kSelThreads) sm.hist[x] = 0;
+      __syncthreads();
+      for (int i = slice0 + tid; i < slice1; i += kSelThreads) {
+        const uint32_t k = key_of(i);
+        if ((k & mask) == prefix) atomicAdd(&sm.hist[(k >> shift) & (bins - 1)], 1);
+      }
+      cluster.sync();
+      // this thread's two bins (from the top), over all blocks
+      int c[2] = {0, 0};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int bin = bins - 1 - (2 * tid + u);
+        if (bin >= 0)
+          for (int r = 0; r < blocks; ++r) c[u] += *cluster.map_shared_rank(&sm.hist[bin], r);
+      }
+      int v = c[0] + c[1];   // inclusive scan over the threads
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += x;
+      }
+      if (lane == 31) sm.sums[warp] = v;
+      __syncthreads();
+      int before = 0;
+      {
+        int x = lane < warp ? sm.sums[lane] : 0;
+        before = __reduce_add_sync(0xFFFFFFFFu, x);
+      }
+      const int upto = before + v, above = upto - c[0] - c[1];
+      if (above < need && upto >= need) {   // the digit lies in one of this thread's bins
+        const bool second = above + c[0] < need;
+        sm.digit = bins - 1 - (2 * tid + (second ? 1 : 0));
+        sm.need = need - above - (second ? c[0] : 0);
+      }
+      cluster.sync();   // the decision, and every block is done with the histograms
+      prefix |= static_cast<uint32_t>(sm.digit) << shift;
+      mask |= static_cast<uint32_t>(bins - 1) << shift;
+      need = sm.need;
+    }
+    // keys above `prefix` stay, and the first `need` of those equal to it
+    // ---- ranks of the equal ones
+    int count = 0;
+    for (int i = w0 + lane; i - lane < w1; i += 32) count += __popc(__ballot_sync(0xFFFFFFFFu, i < w1 && key_of(i) == prefix));
+    if (lane == 0) sm.warp_a[warp] = count;
+    __syncthreads();
+    if (warp == 0) {
+      const int x = sm.warp_a[lane];
+      const int t = __reduce_add_sync(0xFFFFFFFFu, x);
+      if (lane == 0) sm.total_a = t;
+    }
+    cluster.sync();
+    int ties = 0;   // equal keys before this warp's stretch
+    for (int r = 0; r < rank; ++r) ties += *cluster.map_shared_rank(&sm.total_a, r);
+    ties += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sm.warp_a[lane] : 0);
+    cluster.sync();
+    // ---- holes and movers of this warp's stretch
+    auto walk = [&](auto&& visit) {
+      int t = ties;
+      for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < w1 ? key_of(i) : 0u;
+        const uint32_t eq = __ballot_sync(0xFFFFFFFFu, i < w1 && k == prefix);
+        const bool keep = i < w1 && (k > prefix || (k == prefix && t + __popc(eq & ((1u << lane) - 1u)) < need));
+        t += __popc(eq);
+        visit(i, __ballot_sync(0xFFFFFFFFu, i < w1 && i < m && !keep), __ballot_sync(0xFFFFFFFFu, i < w1 && i >= m && keep));
+      }
+    };
+    int holes = 0, movers = 0;
+    walk([&](int, uint32_t h, uint32_t v) {
+      holes += __popc(h);
+      movers += __popc(v);
+    });
+    if (lane == 0) {
+      sm.warp_a[warp] = holes;
+      sm.warp_b[warp] = movers;
     }
     __syncthreads();
-    for (int i = tid; i < holes; i += blockDim.x) src[hole[i]] = mover[i];
-    if (tid == 0) a.npairs[b] = holes;
+    if (warp == 0) {
+      const int x = __reduce_add_sync(0xFFFFFFFFu, sm.warp_a[lane]), y = __reduce_add_sync(0xFFFFFFFFu, sm.warp_b[lane]);
+      if (lane == 0) {
+        sm.total_a = x;
+        sm.total_b = y;
+      }
+    }
+    cluster.sync();
+    int h0 = 0, v0 = 0;
+    for (int r = 0; r < blocks; ++r) {
+      const int x = *cluster.map_shared_rank(&sm.total_a, r);
+      if (r < rank) {
+        h0 += x;
+        v0 += *cluster.map_shared_rank(&sm.total_b, r);
+      }
+      pairs += x;
+    }
+    h0 += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sm.warp_a[lane] : 0);
+    v0 += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sm.warp_b[lane] : 0);
+    walk([&](int i, uint32_t h, uint32_t v) {
+      const uint32_t below = (1u << lane) - 1u;
+      if ((h >> lane) & 1u) {
+        hole[h0 + __popc(h & below)] = i;
+      } else if (i < min(m, w1)) {   // keeps its entry
+        src[i] = i;
+        if (!acc_in_place) a.acc_out[b * a.acc_out_stride + i] = acc[i];
+        if (age != nullptr && !age_in_place) a.age_out[b * a.age_out_stride + i] = age[i];
+      }
+      if ((v >> lane) & 1u) mover[v0 + __popc(v & below)] = i;
+      h0 += __popc(h);
+      v0 += __popc(v);
+    });
+    __threadfence();
+    cluster.sync();   // the lists are complete, and no block reads another's shared memory any more
+    for (int i = rank * kSelThreads + tid; i < pairs; i += blocks * kSelThreads) src[hole[i]] = mover[i];
+  } else {
+    for (int i = rank * kSelThreads + tid; i < a.budget; i += blocks * kSelThreads) {
+      src[i] = i < n ? i : -1;
+      if (i < n && !acc_in_place) a.acc_out[b * a.acc_out_stride + i] = acc[i];
+      if (i < n && age != nullptr && !age_in_place) a.age_out[b * a.age_out_stride + i] = age[i];
+    }
   }
-  __syncthreads();
-  if (tid == 0) a.n_out[b] = m;
-  // weights and ages follow their entries; in place only the holes change
-  for (int i = tid; i < m; i += blockDim.x) {
-    const int s = src[i];
-    if (s != i || a.acc_out != a.acc) a.acc_out[b * a.acc_out_stride + i] = acc[s];
-    if (age != nullptr && (s != i || a.age_out != a.age)) a.age_out[b * a.age_out_stride + i] = age[s];
+  // the movers' weights and ages (those of the slots that keep their entry: above, unless in place)
+  for (int i = rank * kSelThreads + tid; i < pairs; i += blocks * kSelThreads) {
+    const int to = hole[i], from = mover[i];
+    a.acc_out[b * a.acc_out_stride + to] = acc[from];
+    if (age != nullptr) a.age_out[b * a.age_out_stride + to] = age[from];
+  }
+  if (rank == 0 && tid == 0) {
+    a.npairs[b] = pairs;
+    if (a.n_out != a.n_entries) a.n_out[b] = m;
+  }
+  if (a.fused) {
+    for (int i = rank * kSelWarps + warp; i < pairs; i += blocks * kSelWarps) move_pair(a, b, hole[i], mover[i], lane);
+  }
+  if (a.n_out == a.n_entries) {   // every block has read n_entries
+    cluster.sync();
+    if (rank == 0 && tid == 0) a.n_out[b] = m;
   }
 }
 
-// one warp per (request, pair): the rows of every cache, 4 bytes a lane
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
+// The rows of many pairs: a warp per pair, four pairs at a time per block and warp.
+__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+  grid_dep_wait();
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int np = a.npairs[b];
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < np; i += gridDim.x * 8) {
-    const int to = a.hole[(long long)b * a.max_pairs + i], from = a.mover[(long long)b * a.max_pairs + i];
-    for (int c = 0; c < a.ncaches; ++c) {
-      const cskv_paged& p = a.cache[c];
-      const RowPtr d = paged_row(p, b, to, a.row_bytes[c]), s = paged_row(p, b, from, a.row_bytes[c]);
-      if (d.data == nullptr || s.data == nullptr) continue;
-      const bool split = p.fmt == CSKV_FMT_FP8_E4M3_ROWSCALE_PAGESPLIT || p.fmt == CSKV_FMT_FP4_E2M1_E8M0_HADAMARD_PAGESPLIT;
-      const int words = (split ? a.row_bytes[c] - 4 : a.row_bytes[c]) / 4;
-      for (int x = lane; x < words; x += 32)
-        reinterpret_cast<uint32_t*>(d.data)[x] = reinterpret_cast<const uint32_t*>(s.data)[x];
-      if (split && lane == 0) *reinterpret_cast<uint32_t*>(d.scale) = *reinterpret_cast<const uint32_t*>(s.scale);
-    }
-  }
+  const int i0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4;
+#pragma unroll 1
+  for (int i = i0; i < min(i0 + 4, np); ++i)
+    move_pair(a, b, a.hole[(long long)b * a.max_pairs + i], a.mover[(long long)b * a.max_pairs + i], lane);
 }
 
 int max_pairs_of(int max_entries, int budget) {
@@ -213,18 +348,41 @@ cudaError_t launch_evict(const cskv_paged* caches, int ncaches, const float* acc
   a.age_out_stride = age_out_stride;
   a.n_out = n_out;
   a.max_pairs = max_pairs_of(max_entries, budget);
+  a.fused = a.max_pairs <= kFusedPairs;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.npairs = reinterpret_cast<int32_t*>(w);
   w += a256(size_t(B) * 4);
   a.hole = reinterpret_cast<int32_t*>(w);
   w += a256(size_t(B) * a.max_pairs * 4);
   a.mover = reinterpret_cast<int32_t*>(w);
-  evict_select_kernel<<<B, kSelThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.max_pairs == 0) return e;
-  const int blocks = (a.max_pairs + 7) / 8;
-  evict_move_kernel<<<dim3(blocks, B), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  int blocks = 1;
+  while (blocks < kMaxCluster && static_cast<long long>(blocks) * kSliceTarget < max_entries) blocks *= 2;
+  // the largest slice: whole warp stretches of 32
+  const int slice = ((((max_entries + blocks - 1) / blocks + kSelWarps - 1) / kSelWarps + 31) & ~31) * kSelWarps;
+  a.cached = slice <= kKeysInSmem;
+  const size_t smem = a.cached ? size_t(slice) * 4 : 0;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysInSmem * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B) * blocks);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+  if (e != cudaSuccess || a.max_pairs == 0 || a.fused) return e;
+  // starts while the selection ends; waits for it before it reads the pairs
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((a.max_pairs + 31) / 32), B);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a);
 }
 
 unsigned int take_err_evict() { return take_dev_err(); }

@@ -23,16 +23,14 @@
 //                   same shared-memory tile as K), 4 x 64 TMEM columns,
 // since a 512-d fp32 output of 128 rows would take the whole tensor memory.  Few rows need
 // no padding to 128.  The tile lives in eight 16 KiB chunks of 64 dims.  Roles:
-//   warps 0-7   load and rotate the queries, then softmax: a thread has one key and up to
-//               32 rows, straight from TMEM; P^T to shared memory as bf16; the epilogue;
-//   warps 8-15  one chunk of every tile each: load its 64 dims of the rows (four rows ahead
-//               in registers), dequantise exactly to bf16, fill the chunk as soon as the O
-//               product has released it; one fence a tile and warp makes it visible to the
-//               tensor core (a fence per chunk by all warps made them wait for each other);
+//   warps 0-15  load and rotate the queries; then for each tile: dequantise the tile's rows
+//               exactly to bf16 into the two chunks that four warps share, as soon as the O product
+//               has released it (the rows' bytes have been on their way since the tile
+//               before); then softmax: a thread has one key and 16 rows, straight from TMEM;
+//               P^T to shared memory as bf16; at the end the epilogue;
 //   warp 16     one thread issues the MMAs of a chunk as soon as it is full.
-// So a tile's dequantisation overlaps the O product of the tile before it, and S follows
-// chunk by chunk.  The roles run different code at the same time: their loops stay short
-// enough for the instruction cache.
+// Loading and softmax take turns in the same warps: a tile's products wait for both anyway,
+// and sixteen warps hide the latency of either better than eight warps for each.
 //
 // Roundings: the rotated query is kept as hi + lo, two bf16 numbers (the lo part of the 64
 // rotated dims is a ninth chunk of Q), so that logits and log-sum-exp are fp32-accurate;
@@ -52,10 +50,10 @@ constexpr int kD = 512;
 constexpr int kKeys = 128;
 constexpr int kRows = 64;
 constexpr int kChunk = kKeys * 128;      // bytes of 64 dims of a tile
-constexpr int kSoftThreads = 256;
-constexpr int kLoadThreads = 256;
-constexpr int kThreads = kSoftThreads + kLoadThreads + 32;
-constexpr int kSoftBarrier = 1;          // named barrier of warps 0-7
+constexpr int kWorkWarps = 16;
+constexpr int kWorkThreads = kWorkWarps * 32;
+constexpr int kThreads = kWorkThreads + 32;
+constexpr int kWorkBarrier = 1;          // named barrier of warps 0-15
 constexpr uint32_t kTmemS = 256;         // TMEM columns: O 0..255, S from here
 constexpr float kSlack = 8.0f;           // base 2: weights stay below 2^8
 constexpr float kLog2e = 1.4426950408889634f;
@@ -113,8 +111,19 @@ struct __align__(16) RowSees {   // position p is seen when p < f or lo <= p <= 
   int f, lo, hi, run;
 };
 
+struct Item {
+  int kind;
+  int fmt, row_bytes;
+  cskv_paged pages;
+  int r0, nr;            // rows [r0, r0 + nr) of the [T * H] rows
+  int split, nsplit;     // this block takes the split-th of nsplit shares of the tiles
+  int part;              // its partial output
+};
+
 struct ListSmem {
-  uint64_t full[8], free_[8], bar_s[2], bar_p[2], bar_q;
+  Item item;                 // the block's, read from here where registers are short
+  uint64_t full[4], free_[4],   // of a pair of chunk slots
+       bar_s[2], bar_p[2], bar_q;
   uint32_t tmem;
   int abort;
   int nruns, ntiles;
@@ -124,7 +133,7 @@ struct ListSmem {
   __align__(16) float limit[kRows];  // a logit above it moves the reference
   __align__(16) float msub[kRows];   // the reference in base 2, 0 for none
   __align__(16) float fac[kRows];
-  float part[4][2 * kRows];
+  float part[6][2 * kRows];
   // rows of tile i that do not exist: bit r & 31 of word [i & 3][r >> 5], set by the loading
   // warps, cleared by the softmax that has read it (weights_kernel's loads run up to three
   // tiles ahead of it)
@@ -147,13 +156,13 @@ __device__ __forceinline__ bool wait_bar(ListSmem* sm, uint64_t* bar, uint32_t p
   }
   return true;
 }
-__device__ __forceinline__ void soft_sync() {
-  asm volatile("bar.sync %0, %1;" ::"n"(kSoftBarrier), "n"(kSoftThreads) : "memory");
+__device__ __forceinline__ void work_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(kWorkBarrier), "n"(kWorkThreads) : "memory");
 }
-__device__ __forceinline__ bool soft_any(bool p) {
+__device__ __forceinline__ bool work_any(bool p) {
   int r;
   asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbar.red.or.pred b, %2, %3, a;\n\tselp.s32 %0, 1, 0, b;\n\t}"
-               : "=r"(r) : "r"(static_cast<int>(p)), "n"(kSoftBarrier), "n"(kSoftThreads) : "memory");
+               : "=r"(r) : "r"(static_cast<int>(p)), "n"(kWorkBarrier), "n"(kWorkThreads) : "memory");
   return r != 0;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -239,9 +248,7 @@ struct Raw<CSKV_FMT_FP4_E2M1_E4M3_B16> {
   uint32_t s;
 };
 template <>
-struct Raw<CSKV_FMT_BF16> {
-  uint4 a, b;
-};
+struct Raw<CSKV_FMT_BF16> {};   // copied straight into the chunk
 
 // Rows that do not exist read as zeros from here, so that loads and conversions have no branch.
 __device__ uint4 g_zero_row[64];
@@ -254,16 +261,6 @@ __device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_F
 __device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r) {
   r.c = __ldg(reinterpret_cast<const uint2*>(p + 8 * g));
   r.s = __ldg(p + kD / 2 + g);
-}
-__device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_BF16>& r) {
-  r.a = __ldg(reinterpret_cast<const uint4*>(p + 32 * g));
-  r.b = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 16));
-}
-
-// to 8 words of two bf16
-__device__ __forceinline__ void convert(const Raw<CSKV_FMT_BF16>& r, uint32_t (&w)[8]) {
-  w[0] = r.a.x; w[1] = r.a.y; w[2] = r.a.z; w[3] = r.a.w;
-  w[4] = r.b.x; w[5] = r.b.y; w[6] = r.b.z; w[7] = r.b.w;
 }
 // e4m3 pairs to fp16 (exact), times the block's scale 2^e in fp32, rounded to bf16 (4
 // significant bits: exact where bf16 holds the value)
@@ -293,15 +290,6 @@ __device__ __forceinline__ void convert(const Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r
 // ---------------------------------------------------------------------------
 // a block's work
 // ---------------------------------------------------------------------------
-struct Item {
-  int kind;
-  int fmt, row_bytes;
-  cskv_paged pages;
-  int r0, nr;            // rows [r0, r0 + nr) of the [T * H] rows
-  int split, nsplit;     // this block takes the split-th of nsplit shares of the tiles
-  int part;              // its partial output
-};
-
 __device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
   Item it;
   it.fmt = a.kv.fmt;
@@ -469,96 +457,113 @@ struct TileWalk {
 };
 
 // ---------------------------------------------------------------------------
-// loading warps: warp c of them has chunk c (dims 64c .. 64c + 63) of every tile, lane l the
-// 16-dim group l & 3 of rows l / 4, l / 4 + 8, ...  NS chunk slots; the fills of a slot wait
-// for its release (kPairs: chunks are released in pairs, the O product's blocks of 128 dims).
+// loading.  Warps 4m .. 4m + 3 have the dims 128 m .. 128 m + 127 (two chunks, one block of
+// the O product) of every tile, 32 rows each; lane l the 16-dim group l & 7 of the rows
+// l / 8, l / 8 + 4, ...: an instruction reads 128 bytes of four rows (whole sectors, few
+// cache lines).  NS chunk slots; the fills of a pair of slots wait for its release.
 // ---------------------------------------------------------------------------
-template <int FMT, int NS, bool kPairs>
-__device__ void load_tiles(const Item& it, ListSmem* sm, uint8_t* slots, int tile_begin, int tile_end,
-                           unsigned long long spin) {
-  constexpr int kBatch = FMT == CSKV_FMT_BF16 ? 2 : 4;   // rows of a lane in flight beside those converted
-  const int chunk = (threadIdx.x >> 5) - kSoftThreads / 32, lane = threadIdx.x & 31;
-  const int sub = lane >> 2, grp = lane & 3;
-  uint8_t* slot = slots + (chunk % NS) * kChunk;
-  uint64_t* full = &sm->full[chunk % NS];
-  uint64_t* free_bar = &sm->free_[kPairs ? chunk >> 1 : chunk % NS];
-  TileWalk walk(sm);
-  // the addresses of a tile's rows: row 32 u + lane in p[u]
-  unsigned long long p[4];
-  int keys = 0;
-  auto resolve = [&](int tile) {
-    int k0;
-    walk.seek(tile, &k0, &keys);
-    const int req = sm->runs[walk.run].req;
+template <int FMT, int NS>
+struct RowLoader {
+  // batches of four items a lane whose bytes are requested a tile ahead; the rest while the
+  // tile's turn is awaited; the pages of a tile are looked up two tiles ahead
+  static constexpr int kEarly = 2;
+  ListSmem* sm;
+  uint8_t* slot;
+  TileWalk walk;
+  unsigned long long p;      // the address of the tile's row 32 (warp & 3) + lane
+  int page, row;             // of the tile after it: physical page and logical row (-1: no such key)
+  Raw<FMT> raw[2][4];
+  int block, row0, lane;
+
+  __device__ __forceinline__ RowLoader(ListSmem* s, uint8_t* slots) : sm(s), walk(s) {
+    const int warp = threadIdx.x >> 5;
+    block = warp >> 2;
+    row0 = 32 * (warp & 3);
+    lane = threadIdx.x & 31;
+    slot = slots + (2 * block % NS + ((lane >> 2) & 1)) * kChunk + (row0 + (lane >> 3)) * 128;
+  }
+  __device__ __forceinline__ const uint8_t* row_of(int j, int u) const {
+    return reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, p, 16 * j + 4 * u + (lane >> 3)));
+  }
+  __device__ __forceinline__ void load(int j) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int r = 32 * u + lane;
-      const uint8_t* x = reinterpret_cast<const uint8_t*>(g_zero_row);
-      if (r < keys) {
-        const uint8_t* y = paged_row(it.pages, req, walk.position(k0 + r), it.row_bytes).data;
-        if (y != nullptr) x = y;
-        else if (chunk == 0) atomicOr(&sm->none[(tile - tile_begin) & 3][u], 1u << lane);
+      const uint8_t* from = row_of(j, u);
+      if constexpr (FMT == CSKV_FMT_BF16) {   // the block's 256 bytes of the row: into L2, until the chunks are free
+        if ((lane & 3) == 0) prefetch_l2(from + 256 * block + 128 * ((lane >> 2) & 1));
+      } else {
+        load_raw(from, 8 * block + (lane & 7), raw[j][u]);
       }
-      p[u] = reinterpret_cast<unsigned long long>(x);
     }
-  };
-  // two batches of raw rows take turns: one is converted while the other is in flight
-  // (copying one to the other would wait for the loads)
-  Raw<FMT> raw0[kBatch], raw1[kBatch];
-  // batch j: rows 8k + sub for k in [j * kBatch, (j + 1) * kBatch)
-  auto load = [&](int j, Raw<FMT> (&r)[kBatch]) {
-    const int pu = (j * kBatch) >> 2;
-    const unsigned long long q = pu == 0 ? p[0] : pu == 1 ? p[1] : pu == 2 ? p[2] : p[3];
+  }
+  __device__ __forceinline__ void store(int j) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const unsigned long long x = __shfl_sync(0xFFFFFFFFu, q, ((j * kBatch + u) & 3) * 8 + sub);
-      load_raw(reinterpret_cast<const uint8_t*>(x), 4 * chunk + grp, r[u]);
+    for (int u = 0; u < 4; ++u) {
+      const int r = 16 * j + 4 * u;                  // rows r + (lane >> 3) of the warp's 32
+      const int swz = (r + (lane >> 3)) & 7;         // row0 is a multiple of 8
+      const int g = 2 * (lane & 3), odd = (lane >> 2) & 1;
+      // the two chunks' lanes store their two pieces in opposite order: no bank conflict
+      uint8_t* first = slot + r * 128 + (((g + odd) ^ swz) << 4);
+      uint8_t* second = slot + r * 128 + (((g + 1 - odd) ^ swz) << 4);
+      if constexpr (FMT == CSKV_FMT_BF16) {
+        const uint8_t* from = row_of(j, u) + 256 * block + 32 * (lane & 7);
+        cp_async16(first, from + 16 * odd);
+        cp_async16(second, from + 16 * (1 - odd));
+      } else {
+        uint32_t w[8];
+        convert(raw[j][u], w);
+        const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(first) = odd ? hi : lo;
+        *reinterpret_cast<uint4*>(second) = odd ? lo : hi;
+      }
     }
-  };
-  auto store = [&](int j, const Raw<FMT> (&r)[kBatch]) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int row = 8 * (j * kBatch + u) + sub;
-      uint32_t w[8];
-      convert(r[u], w);
-      *reinterpret_cast<uint4*>(slot + sw128_offset(row, 2 * grp)) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(slot + sw128_offset(row, 2 * grp + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  // looks tile `tile` of the item up in the block table
+  __device__ __forceinline__ void look_up(int tile, int end) {
+    row = -1;
+    if (tile >= end) return;
+    int k0, n;
+    walk.seek(tile, &k0, &n);
+    if (row0 + lane < n) {
+      row = walk.position(k0 + row0 + lane);
+      page = row / kPageRows;
+      if (sm->item.pages.block_table != nullptr)
+        page = page < sm->item.pages.max_pages
+                   ? __ldg(sm->item.pages.block_table + static_cast<long long>(sm->runs[walk.run].req) * sm->item.pages.max_pages + page)
+                   : -1;
     }
-  };
-  constexpr int kBatches = 16 / kBatch;
-  resolve(tile_begin);
-  load(0, raw0);
-  for (int tile = tile_begin; tile < tile_end; ++tile) {
-    const int i = tile - tile_begin;
-    const int fill = kPairs ? i : i * (8 / NS) + chunk / NS;
-    load(1, raw1);
-    if (fill > 0 && !wait_bar(sm, free_bar, (fill - 1) & 1, spin)) return;
+  }
+  // requests the first bytes of the tile that was looked up (tile i of the block), looks the next one up
+  __device__ __forceinline__ void request(int tile, int i, int end) {
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(g_zero_row);
+    if (row >= 0) {
+      if (page >= 0 && page < sm->item.pages.num_pages) {
+        x = page_row(sm->item.pages, page, row % kPageRows, sm->item.row_bytes).data;
+      } else {
+        set_err(CSKV_ERR_BOUNDS);
+        if (block == 0) atomicOr(&sm->none[i & 3][row0 >> 5], 1u << lane);
+      }
+    }
+    p = reinterpret_cast<unsigned long long>(x);
+    load(0);
+    if (kEarly == 2) load(1);
+    look_up(tile + 1, end);
+  }
+  // the tile's rows into the chunks once they are free
+  __device__ __forceinline__ bool fill(int i, unsigned long long spin) {
+    const int n = i * (8 / NS) + 2 * block / NS;
+    if (kEarly == 1) load(1);
+    const bool ok = n == 0 || wait_bar(sm, &sm->free_[block % (NS / 2)], (n - 1) & 1, spin);
     __syncwarp();
-#pragma unroll 1
-    for (int j = 0; j < kBatches; j += 2) {
-      store(j, raw0);
-      if (j + 2 < kBatches) {
-        load(j + 2, raw0);
-      } else if (tile + 1 < tile_end) {
-        resolve(tile + 1);
-        load(0, raw0);
-      }
-      store(j + 1, raw1);
-      if (j + 3 < kBatches) load(j + 3, raw1);
-    }
+    store(0);
+    store(1);
+    if (FMT == CSKV_FMT_BF16) cp_async_wait_all();
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(full);
+    if (lane == 0) mbar_arrive(&sm->full[block % (NS / 2)]);
+    return ok;
   }
-}
-
-template <int NS, bool kPairs>
-__device__ __forceinline__ void load_role(const Item& it, ListSmem* sm, uint8_t* slots, int b, int e,
-                                          unsigned long long spin) {
-  if (it.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32) load_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32, NS, kPairs>(it, sm, slots, b, e, spin);
-  else if (it.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16) load_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16, NS, kPairs>(it, sm, slots, b, e, spin);
-  else load_tiles<CSKV_FMT_BF16, NS, kPairs>(it, sm, slots, b, e, spin);
-}
+};
 
 // The block's query rows into the K-major chunks of Q (rows nq apart); warps 0-7.  The rows
 // come in by asynchronous copies; the last 64 dims are then rotated in place, chunk 8 holds
@@ -566,7 +571,7 @@ __device__ __forceinline__ void load_role(const Item& it, ListSmem* sm, uint8_t*
 __device__ __forceinline__ void request_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
   const uint8_t* q = a.q + static_cast<size_t>(r0) * kD * 2;
 #pragma unroll 1
-  for (int x = threadIdx.x; x < nq * 64; x += kSoftThreads) {
+  for (int x = threadIdx.x; x < nq * 64; x += kWorkThreads) {
     const int r = x >> 6, c = x & 63;   // dims 8c .. 8c + 7
     uint8_t* dst = qtile + (c >> 3) * (nq * 128) + sw128_offset(r, c & 7);
     if (r < nr) cp_async16(dst, q + static_cast<size_t>(x) * 16);
@@ -575,9 +580,9 @@ __device__ __forceinline__ void request_queries(const ListArgs& a, int r0, int n
 }
 __device__ __forceinline__ void rotate_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
   cp_async_wait_all();
-  soft_sync();
+  work_sync();
 #pragma unroll 1
-  for (int x = threadIdx.x; x < nq * 8; x += kSoftThreads) {
+  for (int x = threadIdx.x; x < nq * 8; x += kWorkThreads) {
     const int r = x >> 3, c = x & 7;
     uint4* hi = reinterpret_cast<uint4*>(qtile + 7 * (nq * 128) + sw128_offset(r, c));
     uint4 v = *hi, lo = make_uint4(0u, 0u, 0u, 0u);
@@ -623,7 +628,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 // Which of a warp's 32 rows see which of its 32 keys: the lane with column c makes row cb + c's
 // bits over the keys k0 .. k0 + 31 of the run (the seen positions are at most three stretches
 // of key indices), then the 32 x 32 bit matrix is transposed; lane k ends with key k0 + k's
-// bits over the rows.
+// bits over the rows.  (16 rows: lanes c and c + 16 make the same row's bits.)
 __device__ __forceinline__ uint32_t seen_by(const ListSmem* sm, int run, int k0, int col) {
   const int lane = threadIdx.x & 31;
   const RowSees s = sm->sees[col];
@@ -663,6 +668,141 @@ __device__ __noinline__ void clear_row(uint8_t* ktile, int key) {
     *reinterpret_cast<uint4*>(ktile + (x >> 3) * kChunk + sw128_offset(key, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// The tiles [begin, end) of a block: l accumulates this thread's key's weights of its 16 rows.
+template <int FMT>
+__device__ __forceinline__ bool attend_tiles(const ListArgs& a, ListSmem* sm, uint8_t* ktile,
+                                             uint8_t* ptile, uint32_t tmem, int nq, int begin, int end,
+                                             float (&l)[16]) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int quarter = warp & 3, group = warp >> 2;
+  const int cb = group * 16;        // this thread's rows (columns of S^T)
+  const bool has = cb < nq;
+  const int key = quarter * 32 + lane;
+  const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
+  RowLoader<FMT, 8> rows(sm, ktile);
+  TileWalk walk(sm);
+  bool ok = true;
+  rows.look_up(begin, end);
+  rows.request(begin, 0, end);
+  for (int i = 0; i < end - begin; ++i) {
+    ok = rows.fill(i, a.spin) && ok;
+    if (begin + i + 1 < end) rows.request(begin + i + 1, i + 1, end);
+    int k0, n;
+    walk.seek(begin + i, &k0, &n);
+    const Run& u = sm->runs[walk.run];
+    // all 128 keys seen by all rows: inside every window, or all first rows
+    const int pa = walk.position(k0), pb = walk.position(k0 + n - 1);
+    bool plain = u.whole && n == kKeys &&
+                 ((pb < u.min_f) || (pa >= u.max_lo && pb <= u.min_hi && pb - pa == kKeys - 1));
+    uint32_t bits = 0xFFFFu;
+    if (!plain && has) {   // before S is complete
+      bits = seen_by(sm, walk.run, k0 + quarter * 32, cb + (lane & 15));
+      if (key >= n) bits = 0u;
+    }
+    ok = wait_bar(sm, &sm->bar_s[0], i & 1, a.spin) && ok;
+    __syncwarp();
+    tc_fence_after();
+    float z[16];
+    if (has) {
+      tmem_ld16(tmem + kTmemS + tlane + cb, z);
+      tmem_wait_ld();
+    }
+    const uint32_t none = sm->none[i & 3][quarter];
+    if (none != 0u) {
+      plain = false;
+      if ((none >> lane) & 1u) bits = 0u;
+    }
+    bool unfit = false;
+    if (has && key < n && !(fabsf(z[0]) < INFINITY)) {
+      unfit = unfit_row(ktile, key);
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        if (unfit) z[c] = __int_as_float(0x7FC00000);
+    }
+    __syncwarp();
+    if (!plain) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        if (((bits >> c) & 1u) == 0u) z[c] = -INFINITY;
+    }
+    bool above = false;
+    if (has) {
+#pragma unroll
+      for (int c = 0; c < 16; c += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(&sm->limit[cb + c]);
+        above |= (z[c] > m.x) | (z[c + 1] > m.y) | (z[c + 2] > m.z) | (z[c + 3] > m.w);
+      }
+    }
+    const bool moves = work_any(above);
+    if (unfit && group == 0) clear_row(ktile, key);   // every group has looked at it
+    if (moves) {   // some row's reference moves: the tile's maxima, exactly
+      if (has) {
+        float t[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) t[c] = z[c];
+        const float mine = reduce_columns(t, [](float x, float y) { return fmaxf(x, y); });
+        if ((lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = mine;
+      }
+      work_sync();
+      if (tid < nq) {
+        const float old = sm->m[tid], old_sub = sm->msub[tid];
+        const float now = fmaxf(fmaxf(fmaxf(sm->part[0][tid], sm->part[1][tid]), fmaxf(sm->part[2][tid], sm->part[3][tid])), old);
+        const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
+        sm->fac[tid] = old == -INFINITY ? 0.f : exp2f(old_sub - sub);
+        sm->m[tid] = now;
+        sm->limit[tid] = now + a.slack;
+        sm->msub[tid] = sub;
+      }
+      work_sync();
+      if (has) {
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm->fac[cb + c]);
+          l[c] *= f.x;
+          l[c + 1] *= f.y;
+          l[c + 2] *= f.z;
+          l[c + 3] *= f.w;
+        }
+      }
+      if (i > 0) {   // the S commit says that the O products so far are complete
+#pragma unroll 1
+        for (int g = 0; g < nq; g += 16) {   // this warp's 32 dims of block `group`, 16 rows at a time
+          float o[16];
+          const uint32_t at = tmem + tlane + group * kRows + g;
+          tmem_ld16(at, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) o[c] *= sm->fac[g + c];
+          tmem_st16(at, o);
+        }
+        tmem_wait_st();
+      }
+    }
+    if (lane == 0 && none != 0u && group == 0) sm->none[i & 3][quarter] = 0u;
+    if (has) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float4 m0 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * g]);
+        const float4 m1 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * g + 4]);
+        const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+        float p[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          p[c] = exp2_fast(fmaf(z[8 * g + c], a.scale_log2, -mm[c]));
+          l[8 * g + c] += p[c];
+        }
+        *reinterpret_cast<uint4*>(ptile + sw128_offset(key, group * 2 + g)) =
+            make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm->bar_p[0]);
+  }
+  return ok;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_constant__ ListArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -675,16 +815,19 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
   const int nq = (it.nr + 15) & ~15;
 
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(&sm->full[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&sm->free_[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm->full[i], 4);
+      mbar_init(&sm->free_[i], 1);
+    }
     mbar_init(&sm->bar_s[0], 2);
-    mbar_init(&sm->bar_p[0], kSoftThreads / 32);
-    mbar_init(&sm->bar_q, kSoftThreads / 32);
+    mbar_init(&sm->bar_p[0], kWorkWarps);
+    mbar_init(&sm->bar_q, kWorkWarps);
     sm->abort = 0;
+    sm->item = it;
     fence_mbar_init();
   }
-  if (warp == 16) tmem_alloc(&sm->tmem, 512);
-  if (warp < 8) request_queries(a, it.r0, it.nr, nq, qtile);
+  if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 512);
+  if (warp < kWorkWarps) request_queries(a, it.r0, it.nr, nq, qtile);
   tc_fence_before();
   plan_block(a, it, sm);
   tc_fence_after();
@@ -693,9 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
   const int end = static_cast<int>(static_cast<long long>(sm->ntiles) * (it.split + 1) / it.nsplit);
   const int nt = end - begin;
 
-  if (warp >= 8 && warp < 16) {
-    if (nt > 0) load_role<8, true>(it, sm, ktile, begin, end, a.spin);
-  } else if (warp == 16) {
+  if (warp == kWorkWarps) {
     if (nt > 0 && elect_lane()) {
       const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
       const uint32_t ido = make_idesc(1, 1, 1, 1, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
@@ -709,8 +850,10 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
       for (int i = 0; i < nt && ok; ++i) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          ok = ok && wait_bar(sm, &sm->full[c], i & 1, a.spin);
-          tc_fence_after();
+          if ((c & 1) == 0) {
+            ok = ok && wait_bar(sm, &sm->full[c >> 1], i & 1, a.spin);
+            tc_fence_after();
+          }
           if (ok) issue_s_chunk(tmem + kTmemS, dk + c * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
         }
         mma_commit(&sm->bar_s[0]);
@@ -742,143 +885,31 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
     rotate_queries(a, it.r0, it.nr, nq, qtile);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm->bar_q);
-    const int quarter = warp & 3, half = warp >> 2;
-    const int cb = half * 32, nc = max(0, min(32, nq - cb));
-    const int key = quarter * 32 + lane;
+    const int quarter = warp & 3, group = warp >> 2;
+    const int cb = group * 16;
+    const bool has = cb < nq;
     const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
-    float l[32];
+    float l[16];
 #pragma unroll
-    for (int c = 0; c < 32; ++c) l[c] = 0.f;
-    TileWalk walk(sm);
-    bool ok = true;
-    for (int i = 0; i < nt; ++i) {
-      if (ok) ok = wait_bar(sm, &sm->bar_s[0], i & 1, a.spin);
-      __syncwarp();
-      tc_fence_after();
-      float z[32];
-      if (nc > 0) {
-        tmem_ld_cols(tmem + kTmemS + tlane + cb, nc, z);
-        tmem_wait_ld();
-      }
-      int k0, n;
-      walk.seek(begin + i, &k0, &n);
-      const Run& u = sm->runs[walk.run];
-      // all 128 keys seen by all rows: inside every window, or all first rows
-      const int pa = walk.position(k0), pb = walk.position(k0 + n - 1);
-      const uint32_t none = sm->none[i & 3][quarter];
-      const bool plain = u.whole && n == kKeys && none == 0u &&
-                         ((pb < u.min_f) || (pa >= u.max_lo && pb <= u.min_hi && pb - pa == kKeys - 1));
-      bool unfit = false;
-      if (nc > 0 && key < n && !(fabsf(z[0]) < INFINITY)) {
-        unfit = unfit_row(ktile, key);
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (unfit) z[c] = __int_as_float(0x7FC00000);
-      }
-      __syncwarp();
-      if (!plain && nc > 0) {
-        uint32_t bits = seen_by(sm, walk.run, k0 + quarter * 32, cb + lane);
-        if (key >= n || ((none >> lane) & 1u) != 0u) bits = 0u;
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (((bits >> c) & 1u) == 0u) z[c] = -INFINITY;
-      }
-      bool above = false;
-#pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        if (c < nc) {
-          const float4 m = *reinterpret_cast<const float4*>(&sm->limit[cb + c]);
-          above |= (z[c] > m.x) | (z[c + 1] > m.y) | (z[c + 2] > m.z) | (z[c + 3] > m.w);
-        }
-      }
-      const bool moves = soft_any(above);
-      if (unfit && half == 0) clear_row(ktile, key);   // both halves have looked at it
-      if (moves) {   // some row's reference moves: the tile's maxima, exactly
-#pragma unroll
-        for (int g = 0; g < 32; g += 16) {
-          if (g < nc) {
-            float t[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) t[c] = z[g + c];
-            const float mine = reduce_columns(t, [](float x, float y) { return fmaxf(x, y); });
-            if ((lane & 1) == 0) sm->part[quarter][cb + g + (lane >> 1)] = mine;
-          }
-        }
-        soft_sync();
-        if (tid < nq) {
-          const float old = sm->m[tid], old_sub = sm->msub[tid];
-          const float now = fmaxf(fmaxf(fmaxf(sm->part[0][tid], sm->part[1][tid]), fmaxf(sm->part[2][tid], sm->part[3][tid])), old);
-          const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
-          sm->fac[tid] = old == -INFINITY ? 0.f : exp2f(old_sub - sub);
-          sm->m[tid] = now;
-          sm->limit[tid] = now + a.slack;
-          sm->msub[tid] = sub;
-        }
-        soft_sync();
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          if (c < nc) {
-            const float4 f = *reinterpret_cast<const float4*>(&sm->fac[cb + c]);
-            l[c] *= f.x;
-            l[c + 1] *= f.y;
-            l[c + 2] *= f.z;
-            l[c + 3] *= f.w;
-          }
-        }
-        if (i > 0) {   // the S commit says that the O products so far are complete
-#pragma unroll 1
-          for (int x = 0; x < 8; ++x) {   // this warp's two blocks of dims, 16 rows at a time
-            const int g = (x & 3) * 16;
-            if (g < nq) {
-              float o[16];
-              const uint32_t at = tmem + tlane + (half * 2 + (x >> 2)) * kRows + g;
-              tmem_ld16(at, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 16; ++c) o[c] *= sm->fac[g + c];
-              tmem_st16(at, o);
-            }
-          }
-          tmem_wait_st();
-        }
-      }
-      if (lane == 0 && none != 0u && half == 0) sm->none[i & 3][quarter] = 0u;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (8 * g < nc) {
-          const float4 m0 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * g]);
-          const float4 m1 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * g + 4]);
-          const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-          float p[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            p[c] = exp2_fast(fmaf(z[8 * g + c], a.scale_log2, -mm[c]));
-            l[8 * g + c] += p[c];
-          }
-          *reinterpret_cast<uint4*>(ptile + sw128_offset(key, half * 4 + g)) =
-              make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
-        }
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->bar_p[0]);
+    for (int c = 0; c < 16; ++c) l[c] = 0.f;
+    if (nt > 0) {
+      bool ok;
+      if (it.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32)
+        ok = attend_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32>(a, sm, ktile, ptile, tmem, nq, begin, end, l);
+      else if (it.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16)
+        ok = attend_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16>(a, sm, ktile, ptile, tmem, nq, begin, end, l);
+      else
+        ok = attend_tiles<CSKV_FMT_BF16>(a, sm, ktile, ptile, tmem, nq, begin, end, l);
+      if (ok) wait_bar(sm, &sm->free_[3], (nt - 1) & 1, a.spin);
     }
-    if (nt > 0 && ok) wait_bar(sm, &sm->free_[3], (nt - 1) & 1, a.spin);
     __syncwarp();
     tc_fence_after();
-    // ---- the rows' sums over the 128 keys: lanes 2c and 2c + 1 end with row cb + g + c
-#pragma unroll
-    for (int g = 0; g < 32; g += 16) {
-      if (g < nc) {
-        float t[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) t[c] = l[g + c];
-        const float mine = reduce_columns(t, [](float x, float y) { return x + y; });
-        if ((lane & 1) == 0) sm->part[quarter][cb + g + (lane >> 1)] = mine;
-      }
+    // ---- the rows' sums over the 128 keys
+    if (has) {
+      const float mine = reduce_columns(l, [](float x, float y) { return x + y; });
+      if ((lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = mine;
     }
-    soft_sync();
+    work_sync();
     if (tid < nq) {
       const float sum = ((sm->part[0][tid] + sm->part[1][tid]) + sm->part[2][tid]) + sm->part[3][tid];
       const float m = sm->m[tid] == -INFINITY ? -INFINITY : sm->msub[tid];
@@ -902,16 +933,20 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
       }
       sm->fac[tid] = f;
     }
-    soft_sync();
+    work_sync();
     // ---- O^T out: a thread has dim d of 16 rows at a time
+    const int d = group * 128 + quarter * 32 + lane;
+    const bool turn = group == 3 && quarter >= 2;   // dims 448..511, turned back
+    const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
+    const int t0 = it.r0 / a.H;
+    const bool one = (it.r0 + it.nr - 1) / a.H == t0;   // the rows of one query
+    float2 w = make_float2(1.f, 0.f);
+    if (turn && one && a.parts == 1) w = __ldg(cs + static_cast<size_t>(t0) * 32);
 #pragma unroll 1
-    for (int x = 0; x < 8; ++x) {
-      const int mb = half * 2 + (x >> 2), g = (x & 3) * 16;
-      if (g >= it.nr) continue;
-      const int d = mb * 128 + quarter * 32 + lane;
+    for (int g = 0; g < it.nr; g += 16) {
       float o[16];
       if (nt > 0) {
-        tmem_ld16(tmem + tlane + mb * kRows + g, o);
+        tmem_ld16(tmem + tlane + group * kRows + g, o);
         tmem_wait_ld();
       } else {
 #pragma unroll
@@ -932,13 +967,10 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
         o[c + 2] *= f.z;
         o[c + 3] *= f.w;
       }
-      if (mb == 3 && quarter >= 2) {   // dims 448..511, turned back
-        const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
-        const int t0 = (it.r0 + g) / a.H, t1 = (it.r0 + min(g + 16, it.nr) - 1) / a.H;
-        float2 w = __ldg(cs + static_cast<size_t>(t0) * 32);
+      if (turn) {
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          if (t1 != t0) w = __ldg(cs + static_cast<size_t>((it.r0 + min(g + c, it.nr - 1)) / a.H) * 32);
+          if (!one) w = __ldg(cs + static_cast<size_t>((it.r0 + min(g + c, it.nr - 1)) / a.H) * 32);
           const float y = __shfl_xor_sync(0xFFFFFFFFu, o[c], 1);
           o[c] = (lane & 1) ? o[c] * w.x - y * w.y : o[c] * w.x + y * w.y;
         }
@@ -948,14 +980,14 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
 #pragma unroll
       for (int c = 0; c < 16; c += 2) {
         const float other = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? o[c] : o[c + 1], 1);
-        const uint32_t w = (lane & 1) ? pack_bf16(other, o[c + 1]) : pack_bf16(o[c], other);
-        if (g + c + (lane & 1) < it.nr) *reinterpret_cast<uint32_t*>(to + c * (kD * 2)) = w;
+        const uint32_t v = (lane & 1) ? pack_bf16(other, o[c + 1]) : pack_bf16(o[c], other);
+        if (g + c + (lane & 1) < it.nr) *reinterpret_cast<uint32_t*>(to + c * (kD * 2)) = v;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kWorkWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1011,6 +1043,59 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // heads.  Up to 128 heads are the MMA columns, two S buffers in TMEM, four chunk slots
 // (released as soon as the chunk's products are complete).
 // ---------------------------------------------------------------------------
+// The tiles [begin, end) of request b: while the S product of a tile runs, the tile before it
+// is weighed.
+template <int FMT, int NS>
+__device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uint8_t* slots,
+                                            const float* lse, uint32_t tmem, int nq, int b, int begin, int end) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, group = warp >> 2;
+  const int key = quarter * 32 + lane;
+  const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
+  RowLoader<FMT, NS> rows(sm, slots);
+  const int nt = end - begin;
+  rows.look_up(begin, end);
+  rows.request(begin, 0, end);
+  for (int i = 0; i <= nt; ++i) {
+    if (i < nt) {
+      rows.fill(i, a.spin);
+      if (i + 1 < nt) rows.request(begin + i + 1, i + 1, end);
+    }
+    if (i == 0) continue;
+    const int t = i - 1, buf = t & 1;
+    wait_bar(sm, &sm->bar_s[buf], (t >> 1) & 1, a.spin);
+    __syncwarp();
+    tc_fence_after();
+    // columns group * 16, group * 16 + 64, ...: this warp's share of the heads
+    float w = 0.f;
+    for (int c = group * 16; c < nq; c += 64) {
+      float z[16];
+      tmem_ld16(tmem + tlane + buf * 128 + c, z);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(&lse[c + k]);
+        w += (exp2_fast(fmaf(z[k], a.scale_log2, -s.x)) + exp2_fast(fmaf(z[k + 1], a.scale_log2, -s.y))) +
+             (exp2_fast(fmaf(z[k + 2], a.scale_log2, -s.z)) + exp2_fast(fmaf(z[k + 3], a.scale_log2, -s.w)));
+      }
+    }
+    tc_fence_before();
+    const int k = (begin + t) * kKeys + key;
+    const uint32_t none = sm->none[t & 3][quarter];
+    float* part = &sm->part[0][0] + buf * (3 * kKeys);   // three groups' shares, two tiles in turn
+    if (group > 0) part[(group - 1) * kKeys + key] = w;
+    work_sync();
+    if (group == 0 && lane == 0 && none != 0u) sm->none[t & 3][quarter] = 0u;
+    if (lane == 0) mbar_arrive(&sm->bar_p[buf]);
+    if (group == 0 && k < sm->runs[0].nkeys) {
+      w = (w + part[key]) + (part[kKeys + key] + part[2 * kKeys + key]);
+      if ((none >> lane) & 1u) w = 0.f;
+      const long long j = a.first + k;
+      a.acc_out[b * a.acc_out_stride + j] = a.decay * a.acc[b * a.acc_stride + j] + w;
+    }
+  }
+}
+
 template <int kWeightSlots>
 __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ ListArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1024,18 +1109,20 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   const int b = blockIdx.x / a.split, split = blockIdx.x % a.split;
 
   if (tid == 0) {
-    for (int i = 0; i < kWeightSlots; ++i) {
-      mbar_init(&sm->full[i], 1);
+    for (int i = 0; i < kWeightSlots / 2; ++i) {
+      mbar_init(&sm->full[i], 4);
       mbar_init(&sm->free_[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->bar_s[i], 2);
-      mbar_init(&sm->bar_p[i], kSoftThreads / 32);
+      mbar_init(&sm->bar_p[i], kWorkWarps);
     }
-    mbar_init(&sm->bar_q, kSoftThreads / 32);
+    mbar_init(&sm->bar_q, kWorkWarps);
     sm->abort = 0;
     fence_mbar_init();
     const int n = entries_of(a, b);
+    sm->item.row_bytes = a.row_bytes;
+    sm->item.pages = a.kv;
     sm->runs[0] = Run{b, 0, a.first, max(0, n - a.first), 0, 0, 1, 1, 0, 0, 0};
     sm->nruns = 1;
     sm->ntiles = (sm->runs[0].nkeys + kKeys - 1) / kKeys;
@@ -1045,8 +1132,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     lse[tid] = v == -INFINITY ? INFINITY : v * kLog2e;
   }
   if (tid < 16) (&sm->none[0][0])[tid] = 0u;
-  if (warp == 16) tmem_alloc(&sm->tmem, 256);
-  if (warp < 8) request_queries(a, b * a.H, a.H, nq, qtile);
+  if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 256);
+  if (warp < kWorkWarps) request_queries(a, b * a.H, a.H, nq, qtile);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1056,13 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   const int nt = end - begin;
 
   if (nt > 0) {
-    if (warp >= 8 && warp < 16) {
-      Item it;
-      it.fmt = a.kv.fmt;
-      it.row_bytes = a.row_bytes;
-      it.pages = a.kv;
-      load_role<kWeightSlots, false>(it, sm, slots, begin, end, a.spin);
-    } else if (warp == 16) {
+    if (warp == kWorkWarps) {
       if (elect_lane()) {
         const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
         const uint64_t dk = smem_desc_sw128(smem_u32(slots), 16, 1024);
@@ -1076,10 +1157,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const int slot = c % kWeightSlots, fill = i * (8 / kWeightSlots) + c / kWeightSlots;
-            ok = ok && wait_bar(sm, &sm->full[slot], fill & 1, a.spin);
-            tc_fence_after();
+            if ((c & 1) == 0) {
+              ok = ok && wait_bar(sm, &sm->full[slot >> 1], fill & 1, a.spin);
+              tc_fence_after();
+            }
             if (ok) issue_s_chunk(tmem + buf * 128, dk + slot * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
-            mma_commit(&sm->free_[slot]);
+            if (c & 1) mma_commit(&sm->free_[slot >> 1]);
           }
           mma_commit(&sm->bar_s[buf]);
           mbar_arrive(&sm->bar_s[buf]);   // hands on what the loading warps wrote (none)
@@ -1090,49 +1173,17 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       rotate_queries(a, b * a.H, a.H, nq, qtile);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->bar_q);
-      const int quarter = warp & 3, half = warp >> 2;
-      const int key = quarter * 32 + lane;
-      const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
-      // columns [c0, c1) of this warp: the 16-column groups of Q cut in two halves
-      const int groups = nq >> 4;
-      const int c0 = half == 0 ? 0 : ((groups + 1) >> 1) * 16, c1 = half == 0 ? ((groups + 1) >> 1) * 16 : nq;
-      bool ok = true;
-      for (int i = 0; i < nt; ++i) {
-        const int buf = i & 1;
-        if (ok) ok = wait_bar(sm, &sm->bar_s[buf], (i >> 1) & 1, a.spin);
-        __syncwarp();
-        tc_fence_after();
-        float w = 0.f;
-        for (int c = c0; c < c1; c += 16) {
-          float z[16];
-          tmem_ld16(tmem + tlane + buf * 128 + c, z);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(&lse[c + k]);
-            w += (exp2_fast(fmaf(z[k], a.scale_log2, -s.x)) + exp2_fast(fmaf(z[k + 1], a.scale_log2, -s.y))) +
-                 (exp2_fast(fmaf(z[k + 2], a.scale_log2, -s.z)) + exp2_fast(fmaf(z[k + 3], a.scale_log2, -s.w)));
-          }
-        }
-        tc_fence_before();
-        const int k = (begin + i) * kKeys + key;
-        const uint32_t none = sm->none[i & 3][quarter];
-        if (half == 1) sm->part[buf][key] = w;
-        soft_sync();
-        if (half == 0 && lane == 0 && none != 0u) sm->none[i & 3][quarter] = 0u;
-        if (lane == 0) mbar_arrive(&sm->bar_p[buf]);
-        if (half == 0 && k < sm->runs[0].nkeys) {
-          if (groups > 1) w += sm->part[buf][key];
-          if ((none >> lane) & 1u) w = 0.f;
-          const long long j = a.first + k;
-          a.acc_out[b * a.acc_out_stride + j] = a.decay * a.acc[b * a.acc_stride + j] + w;
-        }
-      }
+      if (a.kv.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32)
+        weigh_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32, kWeightSlots>(a, sm, slots, lse, tmem, nq, b, begin, end);
+      else if (a.kv.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16)
+        weigh_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16, kWeightSlots>(a, sm, slots, lse, tmem, nq, b, begin, end);
+      else
+        weigh_tiles<CSKV_FMT_BF16, kWeightSlots>(a, sm, slots, lse, tmem, nq, b, begin, end);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kWorkWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
