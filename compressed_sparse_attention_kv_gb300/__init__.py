@@ -404,66 +404,102 @@ def decode_layer(jobs, q_idx, w, keys, q, main_kv, swa, swa_fmt, ctx_len, k, rat
     return out, topk_idx
 
 
-def _shaped(t, shape, name):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+def _refuse(name, t, dtype, shape, device):
+    """Says what is wrong with an argument that _take did not accept."""
+    _need(t, dtype, name)
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _take(name, t, dtype, shape, device):
+    """The address of a contiguous tensor of this type, shape and device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _cache_on(name, cache, rows, device):
+    """A cache whose pool and table (of at least `rows` requests) are on the device."""
+    bt = cache.block_table
+    if cache.pool.device != device or (bt is not None and bt.device != device):
+        raise ValueError("%s must be on %s" % (name, device))
+    if bt is not None and bt.shape[0] < rows:
+        raise ValueError("%s's block table has %d rows for a batch of %d" % (name, bt.shape[0], rows))
+    return cache.desc()
 
 
 def _on_stream(f):
     """Runs f with its `stream` argument (if one is given) current, so that what f allocates for
-    the call belongs to the stream that uses it."""
+    the call belongs to the stream that uses it, and with the first tensor's device current."""
     @functools.wraps(f)
     def g(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
         import torch
-        with torch.cuda.stream(stream):
-            return f(*args, stream=stream, **kw)
+        first = args[0] if args else kw.get("q", kw.get("acc"))
+        if type(first) is not torch.Tensor:
+            first = kw["acc"] if len(args) < 2 else args[1]
+        device = first.device
+        if stream is not None:
+            if device.type == "cuda" and stream.device != device:
+                raise ValueError("the stream must be on %s, got %s" % (device, stream.device))
+            with torch.cuda.stream(stream):
+                return f(*args, **kw)
+        if device.type == "cuda" and device.index != torch._C._cuda_getDevice():
+            with torch.cuda.device(device):
+                return f(*args, **kw)
+        return f(*args, **kw)
     return g
 
 
-def _launch(device, stream, tensors, call):
-    """call(stream handle) with `device` current; every tensor must live there."""
+def _raw_stream(device):
+    """The current stream of the (current) device, as the library takes it."""
     import torch
-    for name, t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    if stream is not None and stream.device != device:
-        raise ValueError("the stream must be on %s, got %s" % (device, stream.device))
-    if device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
-        return call(torch.cuda.current_stream().cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _workspace(workspace, nbytes, device):
-    import torch
-    if workspace is None and nbytes > 0:
+    """(tensor, address, bytes) of the caller's workspace, or of one of nbytes."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        import torch
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
     _need(workspace, None, "workspace")
-    return workspace, (0 if workspace is None else workspace.numel() * workspace.element_size())
+    if workspace.device != device:
+        raise ValueError("workspace must be on %s, got %s" % (device, workspace.device))
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _query_args(q, out, lse, want_lse, sink, q_rope_cs):
-    """Checks the query side of an attention call; allocates out and lse."""
+def _query(q):
+    """(rows, heads, device, address) of the queries."""
     import torch
-    _need(q, torch.bfloat16, "q")
-    _need(sink, torch.float32, "sink")
-    _need(q_rope_cs, torch.float32, "q_rope_cs")
-    _need(out, torch.bfloat16, "out")
-    _need(lse, torch.float32, "lse")
+    if q.dtype is not torch.bfloat16 or not q.is_cuda or not q.is_contiguous():
+        _need(q, torch.bfloat16, "q")
     if q.dim() != 3 or q.shape[2] != 512:
         raise ValueError("q must have shape (rows, heads, 512), got %s" % (tuple(q.shape),))
     T, H, _ = q.shape
-    _shaped(q_rope_cs, (T, 32, 2), "q_rope_cs")
-    _shaped(sink, (H,), "sink")
-    _shaped(out, (T, H, 512), "out")
-    _shaped(lse, (T, H), "lse")
+    return T, H, q.device, q.data_ptr()
+
+
+def _outputs(q, T, H, device, out, lse, want_lse):
+    """(out, lse, their addresses); allocates what is not given."""
+    import torch
     if out is None:
-        out = torch.empty_like(q)
-    if lse is None and want_lse:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    return T, H, out, lse
+        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=device)
+        po = out.data_ptr()
+    else:
+        po = _take("out", out, torch.bfloat16, (T, H, 512), device)
+    if lse is not None:
+        pl = _take("lse", lse, torch.float32, (T, H), device)
+    elif want_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=device)
+        pl = lse.data_ptr()
+    else:
+        pl = None
+    return out, lse, po, pl
 
 
 def window_attn_workspace_size(T, H, max_ctx_len, window, first):
@@ -478,23 +514,20 @@ def window_attn(q, rows, pos1, window, first, max_ctx_len, sink, softmax_scale, 
     `rows` (a PagedCache of raw rows by position) with j < first or j > t - window; pos1[i]
     <= 0: a padding query (out 0).  Returns (out bf16 [T, H, 512], lse fp32 [T, H] or None)."""
     import torch
-    _need(pos1, torch.int32, "pos1")
-    _need(req_of, torch.int32, "req_of")
-    T, H, out, lse = _query_args(q, out, lse, want_lse, sink, q_rope_cs)
-    _shaped(pos1, (T,), "pos1")
-    _shaped(req_of, (T,), "req_of")
-    reqs = rows.block_table.shape[0] if rows.block_table is not None else (1 << 30)
+    T, H, dev, pq = _query(q)
+    i32, f32 = torch.int32, torch.float32
+    pp = _take("pos1", pos1, i32, (T,), dev)
+    pr = _take("req_of", req_of, i32, (T,), dev)
+    ps = _take("sink", sink, f32, (H,), dev)
+    pc = _take("q_rope_cs", q_rope_cs, f32, (T, 32, 2), dev)
+    desc = _cache_on("rows", rows, T if req_of is None else 1, dev)
+    reqs = rows.block_table.shape[0] if rows.block_table is not None else 1 << 30
+    out, lse, po, pl = _outputs(q, T, H, dev, out, lse, want_lse)
     L = _lib.lib()
-    need = window_attn_workspace_size(T, H, int(max_ctx_len), int(window), int(first))
-    workspace, ws_bytes = _workspace(workspace, need, q.device)
-    st = _launch(q.device, stream,
-                 (("rows", rows.pool), ("rows.block_table", rows.block_table), ("pos1", pos1), ("req_of", req_of),
-                  ("sink", sink), ("q_rope_cs", q_rope_cs), ("out", out), ("lse", lse), ("workspace", workspace)),
-                 lambda s: L.cskvx_window_attn(q.data_ptr(), rows.desc(), reqs, _ptr(req_of), pos1.data_ptr(),
-                                               int(window), int(first), int(max_ctx_len), _ptr(sink),
-                                               float(softmax_scale), q_rope_cs.data_ptr(), T, H, out.data_ptr(),
-                                               _ptr(lse), _ptr(workspace), ws_bytes, s))
-    _check(st, "cskvx_window_attn")
+    need = 0 if workspace is not None else L.cskvx_window_attn_workspace_size(T, H, max_ctx_len, window, first)
+    workspace, pw, nw = _workspace(workspace, need, dev)
+    _check(L.cskvx_window_attn(pq, desc, reqs, pr, pp, window, first, max_ctx_len, ps, softmax_scale, pc, T, H, po, pl,
+                               pw, nw, _raw_stream(dev)), "cskvx_window_attn")
     return out, lse
 
 
@@ -510,34 +543,26 @@ def prefix_decode_attn(q, main_kv, n_entries, n_prefix, max_entries, sink, softm
     (uint8 [B, 128, row bytes] and ctx_len int32 [B]), its window ring.  Returns (out bf16
     [B, H, 512], lse fp32 [B, H] or None)."""
     import torch
-    _need(n_entries, torch.int32, "n_entries")
-    _need(swa, torch.uint8, "swa")
-    _need(ctx_len, torch.int32, "ctx_len")
-    B, H, out, lse = _query_args(q, out, lse, want_lse, sink, q_rope_cs)
-    _shaped(n_entries, (B,), "n_entries")
+    B, H, dev, pq = _query(q)
+    i32, f32 = torch.int32, torch.float32
+    pn = _take("n_entries", n_entries, i32, (B,), dev)
+    ps = _take("sink", sink, f32, (H,), dev)
+    pc = _take("q_rope_cs", q_rope_cs, f32, (B, 32, 2), dev)
+    pr = px = None
     if swa is not None:
-        _shaped(swa, (B, WINDOW, row_bytes(swa_fmt, 512)), "swa")
-        _shaped(ctx_len, (B,), "ctx_len")
-    _table_rows(main_kv, B, "main_kv")
+        pr = _take("swa", swa, torch.uint8, (B, WINDOW, row_bytes(swa_fmt, 512)), dev)
+        if ctx_len is None:
+            raise ValueError("swa needs ctx_len")
+        px = _take("ctx_len", ctx_len, i32, (B,), dev)
+    desc = _cache_on("main_kv", main_kv, B, dev)
+    out, lse, po, pl = _outputs(q, B, H, dev, out, lse, want_lse)
     L = _lib.lib()
-    need = prefix_decode_attn_workspace_size(B, H, int(n_prefix), int(max_entries), swa is not None)
-    workspace, ws_bytes = _workspace(workspace, need, q.device)
-    st = _launch(q.device, stream,
-                 (("main_kv", main_kv.pool), ("main_kv.block_table", main_kv.block_table), ("n_entries", n_entries),
-                  ("swa", swa), ("ctx_len", ctx_len), ("sink", sink), ("q_rope_cs", q_rope_cs), ("out", out),
-                  ("lse", lse), ("workspace", workspace)),
-                 lambda s: L.cskvx_prefix_decode_attn(q.data_ptr(), main_kv.desc(), n_entries.data_ptr(),
-                                                      int(n_prefix), int(max_entries), _ptr(swa), int(swa_fmt),
-                                                      _ptr(ctx_len), _ptr(sink), float(softmax_scale),
-                                                      q_rope_cs.data_ptr(), B, H, out.data_ptr(), _ptr(lse),
-                                                      _ptr(workspace), ws_bytes, s))
-    _check(st, "cskvx_prefix_decode_attn")
+    need = 0 if workspace is not None else L.cskvx_prefix_decode_attn_workspace_size(B, H, n_prefix, max_entries,
+                                                                                     swa is not None)
+    workspace, pw, nw = _workspace(workspace, need, dev)
+    _check(L.cskvx_prefix_decode_attn(pq, desc, pn, n_prefix, max_entries, pr, swa_fmt, px, ps, softmax_scale, pc, B, H,
+                                      po, pl, pw, nw, _raw_stream(dev)), "cskvx_prefix_decode_attn")
     return out, lse
-
-
-def _table_rows(cache, B, name):
-    if cache.block_table is not None and cache.block_table.shape[0] < B:
-        raise ValueError("%s's block table has %d rows for a batch of %d" % (name, cache.block_table.shape[0], B))
 
 
 @_on_stream
@@ -547,34 +572,29 @@ def attn_weights(q, main_kv, n_entries, max_entries, softmax_scale, q_rope_cs, l
     first <= j < n_entries[b] (lse as prefix_decode_attn gave it); acc, acc_out fp32 [B, >=
     max_entries], acc_out None: in place.  Returns acc_out."""
     import torch
-    _need(q, torch.bfloat16, "q")
-    _need(n_entries, torch.int32, "n_entries")
-    _need(q_rope_cs, torch.float32, "q_rope_cs")
-    _need(lse, torch.float32, "lse")
-    _need(acc, torch.float32, "acc")
-    _need(acc_out, torch.float32, "acc_out")
-    if q.dim() != 3 or q.shape[2] != 512:
-        raise ValueError("q must have shape (rows, heads, 512), got %s" % (tuple(q.shape),))
-    B, H, _ = q.shape
-    _shaped(n_entries, (B,), "n_entries")
-    _shaped(q_rope_cs, (B, 32, 2), "q_rope_cs")
-    _shaped(lse, (B, H), "lse")
+    B, H, dev, pq = _query(q)
+    f32 = torch.float32
+    pn = _take("n_entries", n_entries, torch.int32, (B,), dev)
+    pc = _take("q_rope_cs", q_rope_cs, f32, (B, 32, 2), dev)
+    pl = _take("lse", lse, f32, (B, H), dev)
     if acc_out is None:
         acc_out = acc
-    for t, n in ((acc, "acc"), (acc_out, "acc_out")):
-        if t.dim() != 2 or t.shape[0] != B or t.shape[1] < max_entries:
-            raise ValueError("%s must have shape (%d, at least %d), got %s" % (n, B, max_entries, tuple(t.shape)))
-    _table_rows(main_kv, B, "main_kv")
-    L = _lib.lib()
-    st = _launch(q.device, stream,
-                 (("main_kv", main_kv.pool), ("main_kv.block_table", main_kv.block_table), ("n_entries", n_entries),
-                  ("q_rope_cs", q_rope_cs), ("lse", lse), ("acc", acc), ("acc_out", acc_out)),
-                 lambda s: L.cskvx_attn_weights(q.data_ptr(), main_kv.desc(), n_entries.data_ptr(), int(first),
-                                                int(max_entries), float(softmax_scale), q_rope_cs.data_ptr(),
-                                                lse.data_ptr(), B, H, float(decay), acc.data_ptr(), acc.shape[1],
-                                                acc_out.data_ptr(), acc_out.shape[1], s))
-    _check(st, "cskvx_attn_weights")
+    pa, wa = _table("acc", acc, f32, B, max_entries, dev)
+    pb, wb = _table("acc_out", acc_out, f32, B, max_entries, dev)
+    desc = _cache_on("main_kv", main_kv, B, dev)
+    _check(_lib.lib().cskvx_attn_weights(pq, desc, pn, first, max_entries, softmax_scale, pc, pl, B, H, decay, pa, wa,
+                                         pb, wb, _raw_stream(dev)), "cskvx_attn_weights")
     return acc_out
+
+
+def _table(name, t, dtype, rows, least, device):
+    """(address, columns) of a [rows, at least `least`] table (None: (None, 0))."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < least:
+        _need(t, dtype, name)
+        raise ValueError("%s must have shape (%d, at least %d), got %s" % (name, rows, least, tuple(t.shape)))
+    return _take(name, t, dtype, t.shape, device), t.shape[1]
 
 
 def evict_workspace_size(B, max_entries, budget):
@@ -591,43 +611,31 @@ def evict(caches, acc, n_entries, budget, fixed=0, recent=0, age=None, max_entri
     place.  max_entries None: acc's capacity.  Returns (src int32 [B, budget], n_out, acc_out,
     age_out): slot i now holds the entry of slot src[:, i] (-1: none)."""
     import torch
-    for t, dt, n in ((acc, torch.float32, "acc"), (acc_out, torch.float32, "acc_out"), (age, torch.int32, "age"),
-                     (age_out, torch.int32, "age_out"), (n_entries, torch.int32, "n_entries"),
-                     (n_out, torch.int32, "n_out"), (src, torch.int32, "src")):
-        _need(t, dt, n)
-    if acc.dim() != 2:
+    i32, f32 = torch.int32, torch.float32
+    if acc.dim() != 2 or not acc.is_cuda:
+        _need(acc, f32, "acc")
         raise ValueError("acc must have shape (requests, capacity), got %s" % (tuple(acc.shape),))
-    B = acc.shape[0]
-    most = acc.shape[1] if max_entries is None else int(max_entries)
-    budget = int(budget)
+    B, dev = acc.shape[0], acc.device
+    most = acc.shape[1] if max_entries is None else max_entries
+    kept = min(most, budget)
     acc_out = acc if acc_out is None else acc_out
     age_out = age if age_out is None else age_out
     n_out = n_entries if n_out is None else n_out
-    kept = min(most, budget)
-    for t, n, w in ((acc, "acc", most), (age, "age", most), (acc_out, "acc_out", kept), (age_out, "age_out", kept)):
-        if t is not None and (t.dim() != 2 or t.shape[0] != B or t.shape[1] < w):
-            raise ValueError("%s must have shape (%d, at least %d), got %s" % (n, B, w, tuple(t.shape)))
-    _shaped(n_entries, (B,), "n_entries")
-    _shaped(n_out, (B,), "n_out")
-    _shaped(src, (B, budget), "src")
-    for c in caches:
-        _table_rows(c, B, "a cache")
+    pa, wa = _table("acc", acc, f32, B, most, dev)
+    pg, wg = _table("age", age, i32, B, most, dev)
+    pb, wb = _table("acc_out", acc_out, f32, B, kept, dev)
+    ph, wh = _table("age_out", age_out, i32, B, kept, dev)
+    pn = _take("n_entries", n_entries, i32, (B,), dev)
+    pm = _take("n_out", n_out, i32, (B,), dev)
+    arr = (_lib.Paged * max(1, len(caches)))(*[_cache_on("a cache", c, B, dev) for c in caches])
     if src is None:
-        src = torch.empty((B, max(budget, 0)), dtype=torch.int32, device=acc.device)
+        src = torch.empty((B, max(budget, 0)), dtype=i32, device=dev)
+    px = _take("src", src, i32, (B, max(budget, 0)), dev)
     L = _lib.lib()
-    workspace, ws_bytes = _workspace(workspace, evict_workspace_size(B, most, budget), acc.device)
-    arr = (_lib.Paged * max(1, len(caches)))(*[c.desc() for c in caches])
-    tensors = [("acc_out", acc_out), ("age", age), ("age_out", age_out), ("n_entries", n_entries), ("n_out", n_out),
-               ("src", src), ("workspace", workspace)]
-    for c in caches:
-        tensors += [("a cache", c.pool), ("a cache's block table", c.block_table)]
-    st = _launch(acc.device, stream, tensors,
-                 lambda s: L.cskvx_evict(arr, len(caches), acc.data_ptr(), acc.shape[1], _ptr(age),
-                                         0 if age is None else age.shape[1], n_entries.data_ptr(), B, most, budget,
-                                         int(fixed), int(recent), src.data_ptr(), acc_out.data_ptr(),
-                                         acc_out.shape[1], _ptr(age_out), 0 if age_out is None else age_out.shape[1],
-                                         n_out.data_ptr(), _ptr(workspace), ws_bytes, s))
-    _check(st, "cskvx_evict")
+    need = 0 if workspace is not None else L.cskvx_evict_workspace_size(B, most, budget)
+    workspace, pw, nw = _workspace(workspace, need, dev)
+    _check(L.cskvx_evict(arr, len(caches), pa, wa, pg, wg, pn, B, most, budget, fixed, recent, px, pb, wb, ph, wh, pm,
+                         pw, nw, _raw_stream(dev)), "cskvx_evict")
     return src, n_out, acc_out, age_out
 
 

@@ -88,10 +88,12 @@ struct ListArgs {
   float* acc_out;
   long long acc_out_stride;
   float decay;
+  int balanced;              // the blocks share all requests' tiles evenly
   // the grid's work: row blocks of per-query items, and how often each key list is split
   int group;                 // queries per block (H <= 64)
   int head_blocks, heads_per_block;
   int split, prefix_split, prefix_blocks, own_blocks;
+  int prefix_in_own, ring_in_own;   // the prefix, the ring belong to each request's own list
   int parts;                 // partial outputs of a row (1: written straight to out)
   float* opart;              // [row][part][512]
   float* ml;                 // [row][part][2]: m (base 2) and l
@@ -103,18 +105,21 @@ struct ListArgs {
 struct Run {
   int req, f1, base, nkeys, tile0;
   int q0, q1;                // the block's queries [q0, q1) that belong to it
+  int ring;                  // the keys are slots of request req's window ring, not of the cache
   int whole;                 // every row of the block belongs to it
   int min_f, max_lo, min_hi; // over its rows: positions that all of them see
 };
 
-struct __align__(16) RowSees {   // position p is seen when p < f or lo <= p <= hi
-  int f, lo, hi, run;
+struct __align__(16) RowSees {   // position p of run `run` is seen when p < f or lo <= p <= hi;
+  int f, lo, hi, run;            // entries: hi = -1, and lo is the number of ring slots
 };
 
 struct Item {
   int kind;
   int fmt, row_bytes;
   cskv_paged pages;
+  const uint8_t* ring;   // rings of all requests, for runs of ring slots
+  int n_prefix;          // positions below it are looked up in request 0's row
   int r0, nr;            // rows [r0, r0 + nr) of the [T * H] rows
   int split, nsplit;     // this block takes the split-th of nsplit shares of the tiles
   int part;              // its partial output
@@ -139,6 +144,8 @@ struct ListSmem {
   // tiles ahead of it)
   uint32_t none[4][4];
 };
+
+__host__ __device__ inline int tiles_of(long long keys) { return static_cast<int>((keys + kKeys - 1) / kKeys); }
 
 // ---------------------------------------------------------------------------
 // small wrappers
@@ -295,6 +302,8 @@ __device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
   it.fmt = a.kv.fmt;
   it.row_bytes = a.row_bytes;
   it.pages = a.kv;
+  it.ring = a.swa;
+  it.n_prefix = a.pos1 == nullptr && a.prefix_in_own ? a.n_prefix : 0;
   it.split = 0;
   it.nsplit = 1;
   it.part = 0;
@@ -336,13 +345,6 @@ __device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
     it.r0 = x / a.head_blocks * a.H + h0;
     it.nr = min(a.heads_per_block, a.H - h0);
   }
-  if (it.kind == kRing) {   // the request's ring as a flat array of two pages
-    it.pages.pool = const_cast<uint8_t*>(a.swa) + static_cast<size_t>(it.r0 / a.H) * kWindow * it.row_bytes;
-    it.pages.block_table = nullptr;
-    it.pages.page_bytes = 64 * it.row_bytes;
-    it.pages.num_pages = 2;
-    it.pages.fmt = it.fmt;
-  }
   return it;
 }
 
@@ -360,7 +362,7 @@ __device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
   const int tid = threadIdx.x;
   const int t0 = it.r0 / a.H;
   if (tid < kRows) {
-    RowSees s{0, 1, 0, -1};   // nothing
+    RowSees s{0, 0, -1, -1};   // nothing
     if (tid < it.nr) {
       const int t = (it.r0 + tid) / a.H;
       if (it.kind == kWindowRows) {
@@ -369,11 +371,10 @@ __device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
         if (p1 > a.max_ctx) { set_err(CSKV_ERR_BOUNDS); p1 = a.max_ctx; }
         if (p1 > 0 && (req < 0 || req >= a.num_reqs)) { set_err(CSKV_ERR_BOUNDS); p1 = 0; }
         if (p1 > 0) s = RowSees{min(a.first, p1), max(0, p1 - a.window), p1 - 1, req};
-      } else if (it.kind == kRing) {
-        s = RowSees{max(0, min(a.ctx_len[t], kWindow)), 1, 0, t};
       } else {
-        const int n = entries_of(a, t);
-        s = RowSees{it.kind == kPrefixEntries ? min(n, a.n_prefix) : n, 1, 0, it.kind == kPrefixEntries ? 0 : t};
+        const int ring = a.swa != nullptr ? max(0, min(a.ctx_len[t], kWindow)) : 0;
+        const int n = it.kind == kRing ? 0 : entries_of(a, t);
+        s = RowSees{it.kind == kPrefixEntries ? min(n, a.n_prefix) : n, ring, -1, it.kind == kPrefixEntries ? 0 : t};
       }
     }
     sm->sees[tid] = s;   // .run holds the request until the runs are built
@@ -391,12 +392,17 @@ __device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
   if (tid == 0) {
     int nruns = 0, tiles = 0;
     if (it.kind != kWindowRows) {
-      const int from = it.kind == kOwnEntries ? a.n_prefix : 0;
-      Run u{sm->sees[0].run, 0, from, max(0, f - from), 0, 0, it.nr, 1, minf, 1, 0};
-      if (it.kind == kPrefixEntries) u.req = 0;
-      sm->runs[0] = u;
-      nruns = u.nkeys > 0 ? 1 : 0;
-      tiles = (u.nkeys + kKeys - 1) / kKeys;
+      const int from = it.kind == kOwnEntries && !a.prefix_in_own ? a.n_prefix : 0;
+      const int req = it.kind == kPrefixEntries ? 0 : t0;
+      if (f > from && it.kind != kRing) {
+        sm->runs[nruns++] = Run{req, 0, from, f - from, 0, 0, it.nr, 0, 1, minf, 1, 0};
+        tiles = tiles_of(f - from);
+      }
+      const int ring = sm->sees[0].lo;   // one request's rows
+      if ((it.kind == kRing || (it.kind == kOwnEntries && a.ring_in_own)) && ring > 0) {
+        sm->runs[nruns++] = Run{req, 0, 0, ring, tiles, 0, it.nr, 1, 1, ring, 1, 0};
+        ++tiles;
+      }
     } else {
       // neighbouring queries of one request at neighbouring positions share a run
       const int nq = (it.r0 + it.nr - 1) / a.H - t0 + 1;
@@ -415,7 +421,7 @@ __device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
           minf = min(minf, s.f); maxlo = max(maxlo, s.lo); minhi = min(minhi, s.hi);
         }
         const int f1 = min(f, lo);        // first rows before the windows; the rest of them lie inside
-        Run u{first.run, f1, lo, f1 + hi - lo + 1, tiles, q, e, q == 0 && e == nq, minf, maxlo, minhi};
+        Run u{first.run, f1, lo, f1 + hi - lo + 1, tiles, q, e, 0, q == 0 && e == nq, minf, maxlo, minhi};
         sm->runs[nruns++] = u;
         tiles += (u.nkeys + kKeys - 1) / kKeys;
         q = e;
@@ -467,6 +473,7 @@ struct RowLoader {
   // batches of four items a lane whose bytes are requested a tile ahead; the rest while the
   // tile's turn is awaited; the pages of a tile are looked up two tiles ahead
   static constexpr int kEarly = 2;
+  static constexpr int kRingPage = -2;
   ListSmem* sm;
   uint8_t* slot;
   TileWalk walk;
@@ -525,12 +532,17 @@ struct RowLoader {
     int k0, n;
     walk.seek(tile, &k0, &n);
     if (row0 + lane < n) {
+      const Run& u = sm->runs[walk.run];
       row = walk.position(k0 + row0 + lane);
       page = row / kPageRows;
-      if (sm->item.pages.block_table != nullptr)
+      if (u.ring) {
+        row += u.req * kWindow;
+        page = kRingPage;
+      } else if (sm->item.pages.block_table != nullptr) {
+        const int req = row < sm->item.n_prefix ? 0 : u.req;
         page = page < sm->item.pages.max_pages
-                   ? __ldg(sm->item.pages.block_table + static_cast<long long>(sm->runs[walk.run].req) * sm->item.pages.max_pages + page)
-                   : -1;
+                   ? __ldg(sm->item.pages.block_table + static_cast<long long>(req) * sm->item.pages.max_pages + page) : -1;
+      }
     }
   }
   // requests the first bytes of the tile that was looked up (tile i of the block), looks the next one up
@@ -539,6 +551,8 @@ struct RowLoader {
     if (row >= 0) {
       if (page >= 0 && page < sm->item.pages.num_pages) {
         x = page_row(sm->item.pages, page, row % kPageRows, sm->item.row_bytes).data;
+      } else if (page == kRingPage) {
+        x = sm->item.ring + static_cast<long long>(row) * sm->item.row_bytes;
       } else {
         set_err(CSKV_ERR_BOUNDS);
         if (block == 0) atomicOr(&sm->none[i & 3][row0 >> 5], 1u << lane);
@@ -634,7 +648,9 @@ __device__ __forceinline__ uint32_t seen_by(const ListSmem* sm, int run, int k0,
   const RowSees s = sm->sees[col];
   const Run& u = sm->runs[run];
   uint32_t x = 0;
-  if (s.run == run) {
+  if (u.ring) {
+    x = s.run >= 0 ? low_bits(s.lo - k0) : 0u;
+  } else if (s.run == run) {
     const int shift = u.f1 - u.base - k0;   // bit of a position in the second stretch
     const uint32_t second = ~low_bits(u.f1 - k0);
     x = low_bits(min(s.f, u.f1) - k0);
@@ -996,6 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
 // Joins a row's partial outputs in order, adds the sink, turns the output back: 64 threads of
 // 8 dims per row.
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ ListArgs a) {
+  grid_dep_wait();
   const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (row >= static_cast<size_t>(a.T) * a.H) return;
   const int d = (threadIdx.x & 63) * 8;
@@ -1043,26 +1060,104 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // heads.  Up to 128 heads are the MMA columns, two S buffers in TMEM, four chunk slots
 // (released as soon as the chunk's products are complete).
 // ---------------------------------------------------------------------------
-// The tiles [begin, end) of request b: while the S product of a tile runs, the tile before it
-// is weighed.
+// Request b's queries and log-sum-exps (base 2; +inf: adds nothing); warps 0-15.
+__device__ __forceinline__ void load_request(const ListArgs& a, ListSmem* sm, int b, int nq, uint8_t* qtile, float* lse) {
+  work_sync();   // the request before it is weighed
+  request_queries(a, b * a.H, a.H, nq, qtile);
+  if (threadIdx.x < 128) {
+    const float v = threadIdx.x < a.H ? a.lse_in[static_cast<size_t>(b) * a.H + threadIdx.x] : -INFINITY;
+    lse[threadIdx.x] = v == -INFINITY ? INFINITY : v * kLog2e;
+  }
+  rotate_queries(a, b * a.H, a.H, nq, qtile);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->bar_q);
+}
+
+// The block's runs: an even share of all requests' tiles (up to 64 requests), or of one
+// request's.  One warp calls this.
+__device__ __forceinline__ void plan_weights(const ListArgs& a, ListSmem* sm) {
+  const int lane = threadIdx.x & 31;
+  int keys[2] = {0, 0}, before[2];
+  long long lo, hi;
+  int req[2];
+  if (a.balanced) {
+    int sum = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      req[u] = 2 * lane + u;
+      if (req[u] < a.T) keys[u] = max(0, entries_of(a, req[u]) - a.first);
+      before[u] = sum;
+      sum += tiles_of(keys[u]);
+    }
+    int upto = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const long long total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    before[0] += upto - sum;
+    before[1] += upto - sum;
+    lo = total * blockIdx.x / gridDim.x;
+    hi = total * (blockIdx.x + 1) / gridDim.x;
+  } else {
+    req[0] = blockIdx.x / a.split;
+    req[1] = 0;
+    before[0] = before[1] = 0;
+    if (lane == 0) keys[0] = max(0, entries_of(a, req[0]) - a.first);
+    const long long total = __shfl_sync(0xFFFFFFFFu, tiles_of(keys[0]), 0);
+    lo = total * (blockIdx.x % a.split) / a.split;
+    hi = total * (blockIdx.x % a.split + 1) / a.split;
+  }
+  int nruns = 0;
+  uint32_t have[2];
+  long long from[2], to[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    from[u] = max(lo, static_cast<long long>(before[u]));
+    to[u] = min(hi, static_cast<long long>(before[u]) + tiles_of(keys[u]));
+    have[u] = __ballot_sync(0xFFFFFFFFu, from[u] < to[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if (from[u] < to[u]) {
+      const uint32_t below = (1u << lane) - 1u;
+      const int at = __popc(have[0] & below) + __popc(have[1] & below) + (u == 1 ? (have[0] >> lane) & 1 : 0);
+      const long long k0 = (from[u] - before[u]) * kKeys, k1 = min(static_cast<long long>(keys[u]), (to[u] - before[u]) * kKeys);
+      sm->runs[at] = Run{req[u], 0, static_cast<int>(a.first + k0), static_cast<int>(k1 - k0),
+                         static_cast<int>(from[u] - lo), 0, 1, 0, 1, 0, 0, 0};
+    }
+  }
+  nruns = __popc(have[0]) + __popc(have[1]);
+  if (lane == 0) {
+    sm->nruns = nruns;
+    sm->ntiles = static_cast<int>(hi - lo);
+  }
+}
+
+// The block's nt tiles (runs of one or several requests): while the S product of a tile runs,
+// the tile before it is weighed.  Where a run of another request begins, its queries replace
+// the ones before as soon as their last product is complete.
 template <int FMT, int NS>
-__device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uint8_t* slots,
-                                            const float* lse, uint32_t tmem, int nq, int b, int begin, int end) {
+__device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uint8_t* slots, uint8_t* qtile,
+                                            float* lse, uint32_t tmem, int nq, int nt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, group = warp >> 2;
   const int key = quarter * 32 + lane;
   const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
   RowLoader<FMT, NS> rows(sm, slots);
-  const int nt = end - begin;
-  rows.look_up(begin, end);
-  rows.request(begin, 0, end);
+  TileWalk walk(sm);
+  rows.look_up(0, nt);
+  rows.request(0, 0, nt);
   for (int i = 0; i <= nt; ++i) {
     if (i < nt) {
       rows.fill(i, a.spin);
-      if (i + 1 < nt) rows.request(begin + i + 1, i + 1, end);
+      if (i + 1 < nt) rows.request(i + 1, i + 1, nt);
     }
     if (i == 0) continue;
     const int t = i - 1, buf = t & 1;
+    int k0, n;
+    walk.seek(t, &k0, &n);
+    const Run& u = sm->runs[walk.run];
     wait_bar(sm, &sm->bar_s[buf], (t >> 1) & 1, a.spin);
     __syncwarp();
     tc_fence_after();
@@ -1080,19 +1175,20 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
       }
     }
     tc_fence_before();
-    const int k = (begin + t) * kKeys + key;
     const uint32_t none = sm->none[t & 3][quarter];
     float* part = &sm->part[0][0] + buf * (3 * kKeys);   // three groups' shares, two tiles in turn
     if (group > 0) part[(group - 1) * kKeys + key] = w;
     work_sync();
     if (group == 0 && lane == 0 && none != 0u) sm->none[t & 3][quarter] = 0u;
     if (lane == 0) mbar_arrive(&sm->bar_p[buf]);
-    if (group == 0 && k < sm->runs[0].nkeys) {
+    if (group == 0 && key < n) {
       w = (w + part[key]) + (part[kKeys + key] + part[2 * kKeys + key]);
       if ((none >> lane) & 1u) w = 0.f;
-      const long long j = a.first + k;
+      const long long b = u.req, j = walk.position(k0 + key);
       a.acc_out[b * a.acc_out_stride + j] = a.decay * a.acc[b * a.acc_stride + j] + w;
     }
+    if (i < nt && walk.run + 1 < sm->nruns && i == sm->runs[walk.run + 1].tile0)
+      load_request(a, sm, sm->runs[walk.run + 1].req, nq, qtile, lse);
   }
 }
 
@@ -1104,9 +1200,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   const int nq = (a.H + 15) & ~15;
   uint8_t* qtile = slots + kWeightSlots * kChunk;
   ListSmem* sm = reinterpret_cast<ListSmem*>(qtile + 9 * nq * 128);
-  float* lse = reinterpret_cast<float*>(sm + 1);   // [128] base 2, +inf: adds nothing
+  float* lse = reinterpret_cast<float*>(sm + 1);   // [128]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.x / a.split, split = blockIdx.x % a.split;
 
   if (tid == 0) {
     for (int i = 0; i < kWeightSlots / 2; ++i) {
@@ -1120,27 +1215,18 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     mbar_init(&sm->bar_q, kWorkWarps);
     sm->abort = 0;
     fence_mbar_init();
-    const int n = entries_of(a, b);
     sm->item.row_bytes = a.row_bytes;
     sm->item.pages = a.kv;
-    sm->runs[0] = Run{b, 0, a.first, max(0, n - a.first), 0, 0, 1, 1, 0, 0, 0};
-    sm->nruns = 1;
-    sm->ntiles = (sm->runs[0].nkeys + kKeys - 1) / kKeys;
+    sm->item.n_prefix = 0;
   }
-  if (tid < 128) {
-    const float v = tid < a.H ? a.lse_in[static_cast<size_t>(b) * a.H + tid] : -INFINITY;
-    lse[tid] = v == -INFINITY ? INFINITY : v * kLog2e;
-  }
-  if (tid < 16) (&sm->none[0][0])[tid] = 0u;
+  if (warp == 1) plan_weights(a, sm);
+  if (tid >= 64 && tid < 80) (&sm->none[0][0])[tid - 64] = 0u;
   if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 256);
-  if (warp < kWorkWarps) request_queries(a, b * a.H, a.H, nq, qtile);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
-  const int begin = static_cast<int>(static_cast<long long>(sm->ntiles) * split / a.split);
-  const int end = static_cast<int>(static_cast<long long>(sm->ntiles) * (split + 1) / a.split);
-  const int nt = end - begin;
+  const int nt = sm->ntiles;
 
   if (nt > 0) {
     if (warp == kWorkWarps) {
@@ -1149,10 +1235,15 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         const uint64_t dk = smem_desc_sw128(smem_u32(slots), 16, 1024);
         const uint64_t dq = smem_desc_sw128(smem_u32(qtile), 16, 1024);
         const uint32_t qstep = nq * 8;
-        bool ok = wait_bar(sm, &sm->bar_q, 0, a.spin);
+        bool ok = true;
+        int run = -1;
         for (int i = 0; i < nt && ok; ++i) {
           const int buf = i & 1;
-          if (i >= 2) ok = wait_bar(sm, &sm->bar_p[buf], ((i >> 1) - 1) & 1, a.spin);
+          if (run + 1 < sm->nruns && i == sm->runs[run + 1].tile0) {
+            ++run;
+            ok = wait_bar(sm, &sm->bar_q, run & 1, a.spin);
+          }
+          if (i >= 2) ok = ok && wait_bar(sm, &sm->bar_p[buf], ((i >> 1) - 1) & 1, a.spin);
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -1170,15 +1261,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       }
       __syncwarp();
     } else {
-      rotate_queries(a, b * a.H, a.H, nq, qtile);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->bar_q);
+      load_request(a, sm, sm->runs[0].req, nq, qtile, lse);
       if (a.kv.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32)
-        weigh_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32, kWeightSlots>(a, sm, slots, lse, tmem, nq, b, begin, end);
+        weigh_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32, kWeightSlots>(a, sm, slots, qtile, lse, tmem, nq, nt);
       else if (a.kv.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16)
-        weigh_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16, kWeightSlots>(a, sm, slots, lse, tmem, nq, b, begin, end);
+        weigh_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16, kWeightSlots>(a, sm, slots, qtile, lse, tmem, nq, nt);
       else
-        weigh_tiles<CSKV_FMT_BF16, kWeightSlots>(a, sm, slots, lse, tmem, nq, b, begin, end);
+        weigh_tiles<CSKV_FMT_BF16, kWeightSlots>(a, sm, slots, qtile, lse, tmem, nq, nt);
     }
   }
   tc_fence_before();
@@ -1210,6 +1299,7 @@ __host__ __device__ inline size_t a256(size_t x) { return (x + 255) & ~size_t(25
 struct ListPlan {
   int group, head_blocks, heads_per_block, blocks;   // per-query blocks
   int split, prefix_blocks, prefix_split, own_blocks, ring_blocks, parts;
+  int prefix_in_own, ring_in_own;
 };
 
 constexpr int kSmsPlanned = 152;
@@ -1230,10 +1320,9 @@ struct Schedule {
   }
 };
 
-// writing and reading partial outputs: 4 KB a row and part at about 2.5 MB per tile's time
-double join_cost(double rows, int parts) { return parts <= 1 ? 0.0 : 1.5 + rows * parts * 4096.0 / 10e6; }
+// the join's launch, and writing and reading partial outputs: 4 KB a row and part
+double join_cost(double rows, int parts) { return parts <= 1 ? 0.0 : 0.8 + rows * parts * 4096.0 / 15e6; }
 
-int tiles_of(long long keys) { return static_cast<int>((keys + kKeys - 1) / kKeys); }
 int shares(int tiles, int len) { return len > 0 ? (tiles + len - 1) / len : 0; }
 
 // the share length of least cost among tiles, tiles / 2, ... (every count to 16, then in steps of an eighth)
@@ -1275,24 +1364,42 @@ ListPlan window_plan(int T, int H, bool grouped, int max_ctx, int window, int fi
   return p;
 }
 
-ListPlan prefix_plan(int B, int H, int n_prefix, int max_entries, bool ring) {
-  ListPlan p = base_plan(B, H, false);
+// The prefix once for blocks of 64 (request, head) rows beside each request's own list, or as
+// the first part of every request's list (the better one when a block's 64 rows are one
+// request's heads anyway, or when there is little of it: fewer partial outputs); the ring in
+// the request's list when its rows have the cache's format (`merge`), else as a block of its own.
+ListPlan prefix_plan(int B, int H, int n_prefix, int max_entries, bool ring, bool merge) {
+  ListPlan best = {};
+  double best_cost = -1;
   const int rows = B * H;
-  const int ptiles = tiles_of(n_prefix), otiles = tiles_of(max_entries - n_prefix);
-  p.prefix_blocks = ptiles > 0 ? (rows + kRows - 1) / kRows : 0;
-  p.ring_blocks = ring ? p.blocks : 0;
-  p.own_blocks = otiles > 0 || (ptiles == 0 && !ring) ? p.blocks : 0;
-  const int len = best_length(std::max(1, std::max(ptiles, otiles)), [&](int l) {
-    Schedule s;
-    if (ptiles > 0) s.add(double(p.prefix_blocks) * shares(ptiles, l), std::min(l, ptiles) + kBlockCost);
-    if (otiles > 0) s.add(double(p.own_blocks) * shares(otiles, l), std::min(l, otiles) + kBlockCost);
-    if (ring) s.add(p.ring_blocks, 1 + kBlockCost);
-    return s.time + join_cost(rows, shares(ptiles, l) + shares(otiles, l) + (ring ? 1 : 0));
-  });
-  p.prefix_split = std::max(1, shares(ptiles, len));
-  p.split = std::max(1, shares(otiles, len));
-  p.parts = (p.prefix_blocks > 0 ? p.prefix_split : 0) + (p.own_blocks > 0 ? p.split : 0) + (ring ? 1 : 0);
-  return p;
+  for (int in_own = n_prefix > 0 ? 0 : 1; in_own < 2; ++in_own) {
+    ListPlan p = base_plan(B, H, false);
+    const int ptiles = in_own ? 0 : tiles_of(n_prefix);
+    const int entries = in_own ? max_entries : max_entries - n_prefix;
+    p.prefix_in_own = in_own;
+    p.own_blocks = entries > 0 || (ptiles == 0 && !ring) ? p.blocks : 0;
+    p.ring_in_own = ring && merge && p.own_blocks > 0;
+    p.ring_blocks = ring && !p.ring_in_own ? p.blocks : 0;
+    p.prefix_blocks = ptiles > 0 ? (rows + kRows - 1) / kRows : 0;
+    const int otiles = p.own_blocks > 0 ? tiles_of(entries) + p.ring_in_own : 0;
+    auto cost = [&](int l) {
+      Schedule s;
+      if (ptiles > 0) s.add(double(p.prefix_blocks) * shares(ptiles, l), std::min(l, ptiles) + kBlockCost);
+      if (otiles > 0) s.add(double(p.own_blocks) * shares(otiles, l), std::min(l, otiles) + kBlockCost);
+      if (p.ring_blocks > 0) s.add(p.ring_blocks, 1 + kBlockCost);
+      return s.time + join_cost(rows, shares(ptiles, l) + shares(otiles, l) + (p.ring_blocks > 0));
+    };
+    const int len = best_length(std::max(1, std::max(ptiles, otiles)), cost);
+    p.prefix_split = std::max(1, shares(ptiles, len));
+    p.split = std::max(1, shares(otiles, len));
+    p.parts = (p.prefix_blocks > 0 ? p.prefix_split : 0) + (p.own_blocks > 0 ? p.split : 0) + (p.ring_blocks > 0);
+    const double c = cost(len);
+    if (best_cost < 0 || c < best_cost) {
+      best_cost = c;
+      best = p;
+    }
+  }
+  return best;
 }
 
 size_t plan_workspace(const ListPlan& p, int T, int H) {
@@ -1327,6 +1434,8 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
   a.prefix_split = p.prefix_split;
   a.prefix_blocks = p.prefix_blocks;
   a.own_blocks = p.own_blocks;
+  a.prefix_in_own = p.prefix_in_own;
+  a.ring_in_own = p.ring_in_own;
   a.parts = p.parts;
   const size_t rows = static_cast<size_t>(a.T) * a.H;
   a.opart = static_cast<float*>(workspace);
@@ -1340,8 +1449,17 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
   list_attn_kernel<<<grid, kThreads, kAttnSmem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.parts <= 1) return e;
-  attn_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  // launched while the kernel before it ends; waits for it before it reads anything
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel, a);
 }
 
 }  // namespace
@@ -1353,7 +1471,9 @@ size_t window_attn_workspace_bytes(int T, int H, int max_ctx, int window, int fi
 }
 
 size_t prefix_attn_workspace_bytes(int B, int H, int n_prefix, int max_entries, int with_swa) {
-  return plan_workspace(prefix_plan(B, H, n_prefix, max_entries, with_swa != 0), B, H);
+  // with a ring of the cache's format or of another: the larger of the two
+  return std::max(plan_workspace(prefix_plan(B, H, n_prefix, max_entries, with_swa != 0, false), B, H),
+                  plan_workspace(prefix_plan(B, H, n_prefix, max_entries, with_swa != 0, true), B, H));
 }
 
 cudaError_t launch_window_attn(const void* q, const cskv_paged& rows, int num_reqs, const int32_t* req_of,
@@ -1383,7 +1503,7 @@ cudaError_t launch_prefix_attn(const void* q, const cskv_paged& kv, const int32_
   a.swa_fmt = swa_fmt;
   a.swa_row_bytes = swa != nullptr ? static_cast<int>(cskv_row_bytes(swa_fmt, kD)) : 0;
   a.ctx_len = ctx_len;
-  return launch_list(a, prefix_plan(B, H, n_prefix, max_entries, swa != nullptr), workspace, stream);
+  return launch_list(a, prefix_plan(B, H, n_prefix, max_entries, swa != nullptr, swa_fmt == kv.fmt), workspace, stream);
 }
 
 cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32_t* n_entries, int first,
@@ -1401,18 +1521,24 @@ cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32
   a.acc_stride = acc_stride;
   a.acc_out = acc_out;
   a.acc_out_stride = acc_out_stride;
+  // up to 64 requests: the blocks, one per SM, share all their tiles evenly, whatever their
+  // lengths; more requests: blocks of one request's tiles each
   const int tiles = tiles_of(max_entries - first);
-  const int len = best_length(tiles, [&](int l) {
-    Schedule s;
-    s.add(double(B) * shares(tiles, l), l + kBlockCost);
-    return s.time;
-  });
-  a.split = shares(tiles, len);
+  a.balanced = B <= kRows;
+  unsigned grid = static_cast<unsigned>(std::min<long long>(kSmsPlanned, static_cast<long long>(B) * tiles));
+  if (!a.balanced) {
+    a.split = shares(tiles, best_length(tiles, [&](int l) {
+      Schedule s;
+      s.add(double(B) * shares(tiles, l), l + kBlockCost);
+      return s.time;
+    }));
+    grid = static_cast<unsigned>(B) * a.split;
+  }
   const size_t smem = weights_smem(H);
   auto kernel = weight_slots(H) == 8 ? weights_kernel<8> : weights_kernel<4>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(B) * a.split, kThreads, smem, stream>>>(a);
+  kernel<<<grid, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
