@@ -94,6 +94,8 @@ struct ListArgs {
   int head_blocks, heads_per_block;
   int split, prefix_split, prefix_blocks, own_blocks;
   int prefix_in_own, ring_in_own;   // the prefix, the ring belong to each request's own list
+  int rings_only, after_rings;      // the call's launch for the rings; the one after it
+  int prefetch;                     // no other block reads this block's keys: send for them early
   int parts;                 // partial outputs of a row (1: written straight to out)
   float* opart;              // [row][part][512]
   float* ml;                 // [row][part][2]: m (base 2) and l
@@ -116,7 +118,7 @@ struct __align__(16) RowSees {   // position p of run `run` is seen when p < f o
 
 struct Item {
   int kind;
-  int fmt, row_bytes;
+  int row_bytes;
   cskv_paged pages;
   const uint8_t* ring;   // rings of all requests, for runs of ring slots
   int n_prefix;          // positions below it are looked up in request 0's row
@@ -242,38 +244,35 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
 // ---------------------------------------------------------------------------
 // rows: 16 dims of a row from its bytes to bf16, exactly
 // ---------------------------------------------------------------------------
+// a lane's share of a row: the codes of 16 dims; and the scales of a row's block of 128 dims
 template <int FMT>
 struct Raw;
 template <>
 struct Raw<CSKV_FMT_FP8_E4M3_E8M0_B32> {
-  uint4 c;
-  uint32_t s;
+  using Codes = uint4;
+  using Scales = uint32_t;   // four e8m0
 };
 template <>
 struct Raw<CSKV_FMT_FP4_E2M1_E4M3_B16> {
-  uint2 c;
-  uint32_t s;
+  using Codes = uint2;
+  using Scales = uint2;      // eight e4m3
 };
 template <>
-struct Raw<CSKV_FMT_BF16> {};   // copied straight into the chunk
+struct Raw<CSKV_FMT_BF16> {   // copied straight into the chunk
+  using Codes = char;
+  using Scales = char;
+};
 
 // Rows that do not exist read as zeros from here, so that loads and conversions have no branch.
 __device__ uint4 g_zero_row[64];
 
-// 16-dim group g (0..31) of the row at p
-__device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_FP8_E4M3_E8M0_B32>& r) {
-  r.c = __ldg(reinterpret_cast<const uint4*>(p + 16 * g));
-  r.s = __ldg(p + kD + (g >> 1));
-}
-__device__ __forceinline__ void load_raw(const uint8_t* p, int g, Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r) {
-  r.c = __ldg(reinterpret_cast<const uint2*>(p + 8 * g));
-  r.s = __ldg(p + kD / 2 + g);
-}
+__device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
+
 // e4m3 pairs to fp16 (exact), times the block's scale 2^e in fp32, rounded to bf16 (4
 // significant bits: exact where bf16 holds the value)
-__device__ __forceinline__ void convert(const Raw<CSKV_FMT_FP8_E4M3_E8M0_B32>& r, uint32_t (&w)[8]) {
-  const float s = exp2i(static_cast<int>(r.s) - 127);   // infinite for a scale byte of 255
-  const uint32_t c[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
+__device__ __forceinline__ void convert(const uint4& r, uint32_t scale, uint32_t (&w)[8]) {
+  const float s = exp2i(static_cast<int>(scale) - 127);   // infinite for a scale byte of 255
+  const uint32_t c[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t h;
@@ -282,9 +281,9 @@ __device__ __forceinline__ void convert(const Raw<CSKV_FMT_FP8_E4M3_E8M0_B32>& r
   }
 }
 // e2m1 pairs to fp16, times the e4m3 scale (6 significant bits: exact in fp32 and bf16)
-__device__ __forceinline__ void convert(const Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r, uint32_t (&w)[8]) {
-  const float s = e4m3_to_f32(r.s);
-  const uint32_t c[2] = {r.c.x, r.c.y};
+__device__ __forceinline__ void convert(const uint2& r, uint32_t scale, uint32_t (&w)[8]) {
+  const float s = e4m3_to_f32(scale);
+  const uint32_t c[2] = {r.x, r.y};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t h;
@@ -299,7 +298,6 @@ __device__ __forceinline__ void convert(const Raw<CSKV_FMT_FP4_E2M1_E4M3_B16>& r
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
   Item it;
-  it.fmt = a.kv.fmt;
   it.row_bytes = a.row_bytes;
   it.pages = a.kv;
   it.ring = a.swa;
@@ -313,6 +311,10 @@ __device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
     it.nsplit = a.split;
     it.split = it.part = x % a.split;
     x /= a.split;
+  } else if (a.rings_only) {
+    it.kind = kRing;
+    it.part = a.parts - 1;
+    it.row_bytes = a.swa_row_bytes;
   } else if (x < a.prefix_blocks * a.prefix_split) {
     it.kind = kPrefixEntries;
     it.nsplit = a.prefix_split;
@@ -322,20 +324,11 @@ __device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
     return it;
   } else {
     x -= a.prefix_blocks * a.prefix_split;
-    const int psplit = a.prefix_blocks > 0 ? a.prefix_split : 0;
-    if (x < a.own_blocks * a.split) {
-      it.kind = kOwnEntries;
-      it.nsplit = a.split;
-      it.split = x % a.split;
-      it.part = psplit + it.split;
-      x /= a.split;
-    } else {
-      x -= a.own_blocks * a.split;
-      it.kind = kRing;
-      it.part = a.parts - 1;
-      it.fmt = a.swa_fmt;
-      it.row_bytes = a.swa_row_bytes;
-    }
+    it.kind = kOwnEntries;
+    it.nsplit = a.split;
+    it.split = x % a.split;
+    it.part = (a.prefix_blocks > 0 ? a.prefix_split : 0) + it.split;
+    x /= a.split;
   }
   if (a.head_blocks == 1) {
     it.r0 = x * a.group * a.H;
@@ -470,16 +463,16 @@ struct TileWalk {
 // ---------------------------------------------------------------------------
 template <int FMT, int NS>
 struct RowLoader {
-  // batches of four items a lane whose bytes are requested a tile ahead; the rest while the
-  // tile's turn is awaited; the pages of a tile are looked up two tiles ahead
-  static constexpr int kEarly = 2;
+  // a tile's bytes are requested while the tile before it is in its products (and sent for
+  // into L2 while that one's weights are computed), its pages looked up a tile earlier
   static constexpr int kRingPage = -2;
   ListSmem* sm;
   uint8_t* slot;
   TileWalk walk;
   unsigned long long p;      // the address of the tile's row 32 (warp & 3) + lane
   int page, row;             // of the tile after it: physical page and logical row (-1: no such key)
-  Raw<FMT> raw[2][4];
+  typename Raw<FMT>::Codes raw[2][4];
+  typename Raw<FMT>::Scales scales;   // of this lane's row
   int block, row0, lane;
 
   __device__ __forceinline__ RowLoader(ListSmem* s, uint8_t* slots) : sm(s), walk(s) {
@@ -499,7 +492,8 @@ struct RowLoader {
       if constexpr (FMT == CSKV_FMT_BF16) {   // the block's 256 bytes of the row: into L2, until the chunks are free
         if ((lane & 3) == 0) prefetch_l2(from + 256 * block + 128 * ((lane >> 2) & 1));
       } else {
-        load_raw(from, 8 * block + (lane & 7), raw[j][u]);
+        using C = typename Raw<FMT>::Codes;
+        raw[j][u] = __ldg(reinterpret_cast<const C*>(from) + 8 * block + (lane & 7));
       }
     }
   }
@@ -517,8 +511,15 @@ struct RowLoader {
         cp_async16(first, from + 16 * odd);
         cp_async16(second, from + 16 * (1 - odd));
       } else {
-        uint32_t w[8];
-        convert(raw[j][u], w);
+        uint32_t scale, w[8];
+        const int src = r + (lane >> 3);
+        if constexpr (FMT == CSKV_FMT_FP8_E4M3_E8M0_B32) {
+          scale = byte_of(__shfl_sync(0xFFFFFFFFu, scales, src), (lane & 7) >> 1);
+        } else {
+          const uint32_t s0 = __shfl_sync(0xFFFFFFFFu, scales.x, src), s1 = __shfl_sync(0xFFFFFFFFu, scales.y, src);
+          scale = byte_of((lane & 4) ? s1 : s0, lane & 3);
+        }
+        convert(raw[j][u], scale, w);
         const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
         *reinterpret_cast<uint4*>(first) = odd ? hi : lo;
         *reinterpret_cast<uint4*>(second) = odd ? lo : hi;
@@ -545,7 +546,14 @@ struct RowLoader {
       }
     }
   }
-  // requests the first bytes of the tile that was looked up (tile i of the block), looks the next one up
+  // sends the rows of the tile that was looked up into L2
+  __device__ __forceinline__ void prefetch() const {
+    if (block == 0 && row >= 0 && page >= 0 && page < sm->item.pages.num_pages)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                       page_row(sm->item.pages, page, row % kPageRows, sm->item.row_bytes).data),
+                   "r"(sm->item.row_bytes));
+  }
+  // requests the bytes of the tile that was looked up (tile i of the block), looks the next one up
   __device__ __forceinline__ void request(int tile, int i, int end) {
     const uint8_t* x = reinterpret_cast<const uint8_t*>(g_zero_row);
     if (row >= 0) {
@@ -559,14 +567,15 @@ struct RowLoader {
       }
     }
     p = reinterpret_cast<unsigned long long>(x);
+    if constexpr (FMT == CSKV_FMT_FP8_E4M3_E8M0_B32) scales = __ldg(reinterpret_cast<const uint32_t*>(x + kD) + block);
+    if constexpr (FMT == CSKV_FMT_FP4_E2M1_E4M3_B16) scales = __ldg(reinterpret_cast<const uint2*>(x + kD / 2) + block);
     load(0);
-    if (kEarly == 2) load(1);
+    load(1);
     look_up(tile + 1, end);
   }
   // the tile's rows into the chunks once they are free
   __device__ __forceinline__ bool fill(int i, unsigned long long spin) {
     const int n = i * (8 / NS) + 2 * block / NS;
-    if (kEarly == 1) load(1);
     const bool ok = n == 0 || wait_bar(sm, &sm->free_[block % (NS / 2)], (n - 1) & 1, spin);
     __syncwarp();
     store(0);
@@ -815,11 +824,16 @@ __device__ __forceinline__ bool attend_tiles(const ListArgs& a, ListSmem* sm, ui
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm->bar_p[0]);
+    if (a.prefetch) rows.prefetch();
   }
   return ok;
 }
 
+// One kernel per row format: a call whose rings have another format than its cache launches two
+// (a block's code stays within its registers and the instruction cache).
+template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_constant__ ListArgs a) {
+  if (a.rings_only) grid_dep_launch();   // the other kernel of the call may start
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* ktile = base;                              // 8 chunks of 128 rows x 128 B
@@ -909,13 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
 #pragma unroll
     for (int c = 0; c < 16; ++c) l[c] = 0.f;
     if (nt > 0) {
-      bool ok;
-      if (it.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32)
-        ok = attend_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32>(a, sm, ktile, ptile, tmem, nq, begin, end, l);
-      else if (it.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16)
-        ok = attend_tiles<CSKV_FMT_FP4_E2M1_E4M3_B16>(a, sm, ktile, ptile, tmem, nq, begin, end, l);
-      else
-        ok = attend_tiles<CSKV_FMT_BF16>(a, sm, ktile, ptile, tmem, nq, begin, end, l);
+      const bool ok = attend_tiles<FMT>(a, sm, ktile, ptile, tmem, nq, begin, end, l);
       if (ok) wait_bar(sm, &sm->free_[3], (nt - 1) & 1, a.spin);
     }
     __syncwarp();
@@ -1007,6 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (a.after_rings) grid_dep_wait();   // this grid completes after the rings' one
 }
 
 // Joins a row's partial outputs in order, adds the sink, turns the output back: 64 threads of
@@ -1181,6 +1190,7 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
     work_sync();
     if (group == 0 && lane == 0 && none != 0u) sm->none[t & 3][quarter] = 0u;
     if (lane == 0) mbar_arrive(&sm->bar_p[buf]);
+    rows.prefetch();
     if (group == 0 && key < n) {
       w = (w + part[key]) + (part[kKeys + key] + part[2 * kKeys + key]);
       if ((none >> lane) & 1u) w = 0.f;
@@ -1426,6 +1436,27 @@ ListArgs common_args(const void* q, const cskv_paged& kv, const float* sink, flo
   return a;
 }
 
+// One launch of list_attn_kernel for rows of format fmt; `beside`: it may start while the
+// launch before it runs.
+cudaError_t launch_kind(const ListArgs& a, int fmt, unsigned grid, bool beside, cudaStream_t stream) {
+  auto kernel = fmt == CSKV_FMT_FP8_E4M3_E8M0_B32 ? list_attn_kernel<CSKV_FMT_FP8_E4M3_E8M0_B32>
+                : fmt == CSKV_FMT_FP4_E2M1_E4M3_B16 ? list_attn_kernel<CSKV_FMT_FP4_E2M1_E4M3_B16>
+                                                    : list_attn_kernel<CSKV_FMT_BF16>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kAttnSmem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kAttnSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStream_t stream) {
   a.group = p.group;
   a.head_blocks = p.head_blocks;
@@ -1440,14 +1471,22 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
   const size_t rows = static_cast<size_t>(a.T) * a.H;
   a.opart = static_cast<float*>(workspace);
   a.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a256(rows * p.parts * kD * 4));
-  const unsigned grid = a.pos1 != nullptr
-                            ? static_cast<unsigned>(p.blocks) * p.split
-                            : static_cast<unsigned>(p.prefix_blocks) * p.prefix_split + p.own_blocks * p.split + p.ring_blocks;
-  cudaError_t e = cudaFuncSetAttribute(list_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kAttnSmem));
-  if (e != cudaSuccess) return e;
-  list_attn_kernel<<<grid, kThreads, kAttnSmem, stream>>>(a);
-  e = cudaGetLastError();
+  a.rings_only = a.after_rings = 0;
+  // few blocks: a request's keys come from HBM; many blocks read them again and again from L2
+  a.prefetch = a.req_of == nullptr && p.prefix_blocks == 0 && p.head_blocks == 1;
+  cudaError_t e = cudaSuccess;
+  if (p.ring_blocks > 0) {
+    ListArgs r = a;
+    r.rings_only = 1;
+    e = launch_kind(r, a.swa_fmt, p.ring_blocks, false, stream);
+    if (e != cudaSuccess) return e;
+  }
+  const unsigned grid = static_cast<unsigned>(p.prefix_blocks) * p.prefix_split +
+                        static_cast<unsigned>(a.pos1 != nullptr ? p.blocks : p.own_blocks) * p.split;
+  if (grid > 0) {
+    a.after_rings = p.ring_blocks > 0;
+    e = launch_kind(a, a.kv.fmt, grid, a.after_rings != 0, stream);
+  }
   if (e != cudaSuccess || p.parts <= 1) return e;
   // launched while the kernel before it ends; waits for it before it reads anything
   cudaLaunchAttribute attr[1];
