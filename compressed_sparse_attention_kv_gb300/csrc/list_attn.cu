@@ -28,7 +28,12 @@
 //               has released it (the rows' bytes have been on their way since the tile
 //               before); then softmax: a thread has one key and 16 rows, straight from TMEM;
 //               P^T to shared memory as bf16; at the end the epilogue;
-//   warp 16     one thread issues the MMAs of a chunk as soon as it is full.
+//   warp 16     one thread issues the MMAs of a chunk as soon as it is full;
+//   warp 17     finds what the block's next 64 rows see (their runs of keys) and, a tile or two
+//               ahead of the others, looks the addresses of a tile's rows up.
+// A block takes one row block after the other (prompts have many more of them than the device
+// has SMs): the queries and the first keys of the next one are on their way while the last
+// products and the epilogue of this one run.
 // Loading and softmax take turns in the same warps: a tile's products wait for both anyway,
 // and sixteen warps hide the latency of either better than eight warps for each.
 //
@@ -49,10 +54,11 @@ namespace {
 constexpr int kD = 512;
 constexpr int kKeys = 128;
 constexpr int kRows = 64;
+constexpr int kRuns = 32;                // runs of keys of a row block (of one query each at most)
 constexpr int kChunk = kKeys * 128;      // bytes of 64 dims of a tile
 constexpr int kWorkWarps = 16;
 constexpr int kWorkThreads = kWorkWarps * 32;
-constexpr int kThreads = kWorkThreads + 32;
+constexpr int kThreads = kWorkThreads + 64;
 constexpr int kWorkBarrier = 1;          // named barrier of warps 0-15
 constexpr uint32_t kTmemS = 256;         // TMEM columns: O 0..255, S from here
 constexpr float kSlack = 8.0f;           // base 2: weights stay below 2^8
@@ -94,7 +100,8 @@ struct ListArgs {
   int head_blocks, heads_per_block;
   int split, prefix_split, prefix_blocks, own_blocks;
   int prefix_in_own, ring_in_own;   // the prefix, the ring belong to each request's own list
-  int rings_only, after_rings;      // the call's launch for the rings; the one after it
+  int rings_only, lead, beside;     // the call's launch for the rings; before it; beside another
+  int items;                        // row blocks of the launch
   int prefetch;                     // no other block reads this block's keys: send for them early
   int parts;                 // partial outputs of a row (1: written straight to out)
   float* opart;              // [row][part][512]
@@ -127,23 +134,34 @@ struct Item {
   int part;              // its partial output
 };
 
+// A row block's work, made by the planning warp.
+struct Plan {
+  Item item;
+  int nruns, begin, nt, nq;          // runs; its tiles [begin, begin + nt); rows padded to 16
+  Run runs[kRuns];
+  RowSees sees[kRows];
+};
+
+struct TileInfo {
+  int n, k0, run;                    // keys; key index of the first one within the run
+  int plain;                         // every row sees every one of 128 keys
+};
+
 struct ListSmem {
-  Item item;                 // the block's, read from here where registers are short
-  uint64_t full[4], free_[4],   // of a pair of chunk slots
-       bar_s[2], bar_p[2], bar_q;
+  unsigned long long rowp[2][kKeys]; // addresses of a tile's rows (g_zero_row: no such row), by tile parity
+  TileInfo info[2];
+  Plan plan[2];                      // of the row block at hand and of the next one
+  uint64_t full[4], free_[4],        // of a pair of chunk slots
+      bar_s[2], bar_p[2], bar_q, plan_full[2], plan_free[2], rows_full[2], rows_free[2], drained;
   uint32_t tmem;
   int abort;
-  int nruns, ntiles;
-  Run runs[kRows];
-  RowSees sees[kRows];
   __align__(16) float m[kRows];      // running reference in units of q'.c, -inf: no key yet
   __align__(16) float limit[kRows];  // a logit above it moves the reference
   __align__(16) float msub[kRows];   // the reference in base 2, 0 for none
   __align__(16) float fac[kRows];
-  float part[6][2 * kRows];
-  // rows of tile i that do not exist: bit r & 31 of word [i & 3][r >> 5], set by the loading
-  // warps, cleared by the softmax that has read it (weights_kernel's loads run up to three
-  // tiles ahead of it)
+  float part[4][kRows];
+  // rows of tile i that could not be read: bit r & 31 of word [i & 3][r >> 5] (four tiles:
+  // weights_kernel's loads run ahead of its weights)
   uint32_t none[4][4];
 };
 
@@ -152,10 +170,18 @@ __host__ __device__ inline int tiles_of(long long keys) { return static_cast<int
 // ---------------------------------------------------------------------------
 // small wrappers
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ bool wait_bar(ListSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
-  if (mbar_try_wait(bar, parity)) return true;
+// The hardware suspends a waiting thread for up to about 4 us at a time: a waiting warp takes no
+// issue slots from the working ones.
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 4000;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool wait_on(ListSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
   const unsigned long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!try_wait_long(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&sm->abort)) return false;
     if (clock64() - t0 > limit) {   // gave up: every role leaves its loop
       set_err(CSKV_ERR_TIMEOUT);
@@ -165,6 +191,22 @@ __device__ __forceinline__ bool wait_bar(ListSmem* sm, uint64_t* bar, uint32_t p
   }
   return true;
 }
+__device__ __forceinline__ bool wait_bar(ListSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
+  return try_wait_long(bar, parity) || wait_on(sm, bar, parity, limit);
+}
+// wait_bar for a whole warp: all lanes take the same decision
+__device__ __forceinline__ bool wait_warp(ListSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
+  return __all_sync(0xFFFFFFFFu, wait_bar(sm, bar, parity, limit)) != 0;
+}
+// Before the tensor memory is given back: the issuing lane's products are complete (at once,
+// unless a wait gave up while some were in flight).
+__device__ __forceinline__ void drain_products(ListSmem* sm) {
+  mma_commit(&sm->drained);
+  mbar_wait(&sm->drained, 0, kDefaultSpinLimit);
+}
+// The named barrier of the working warps has no limit: every one of them reaches each of its
+// uses, because they all take the same loops (a plan is accepted by all or by none, and after a
+// wait that gave up they go on through the same tiles without waiting).
 __device__ __forceinline__ void work_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(kWorkBarrier), "n"(kWorkThreads) : "memory");
 }
@@ -234,12 +276,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-// x * y on two bf16 (rounded to nearest, subnormals kept)
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
 
 // ---------------------------------------------------------------------------
 // rows: 16 dims of a row from its bytes to bf16, exactly
@@ -268,28 +304,48 @@ __device__ uint4 g_zero_row[64];
 
 __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
 
-// e4m3 pairs to fp16 (exact), times the block's scale 2^e in fp32, rounded to bf16 (4
-// significant bits: exact where bf16 holds the value)
+// x * y on two bf16 (rounded to nearest, subnormals kept)
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// two fp16 to two bf16 (through fp32)
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16(f.x, f.y);
+}
+// e4m3 pairs to fp16 and to bf16 (4 significant bits: exact), times the block's scale 2^e
+// (one rounding, where bf16 does not hold the value)
 __device__ __forceinline__ void convert(const uint4& r, uint32_t scale, uint32_t (&w)[8]) {
-  const float s = exp2i(static_cast<int>(scale) - 127);   // infinite for a scale byte of 255
+  const uint32_t f = scale == 0u ? 0x0040u : scale << 7, ff = f | (f << 16);   // 255: infinite
   const uint32_t c[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c[i >> 1] >> (16 * (i & 1)))));
-    w[i] = pack_bf16(__half2float(__ushort_as_half(h & 0xFFFF)) * s, __half2float(__ushort_as_half(h >> 16)) * s);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(c[i]));
+    w[2 * i] = mul_bf16x2(f16x2_to_bf16x2(lo), ff);
+    w[2 * i + 1] = mul_bf16x2(f16x2_to_bf16x2(hi), ff);
   }
 }
-// e2m1 pairs to fp16, times the e4m3 scale (6 significant bits: exact in fp32 and bf16)
+// e2m1 pairs to fp16, times the e4m3 scale (6 significant bits, 2^-10 .. 2688: exact in fp16
+// and in bf16)
 __device__ __forceinline__ void convert(const uint2& r, uint32_t scale, uint32_t (&w)[8]) {
-  const float s = e4m3_to_f32(scale);
+  uint32_t s2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(static_cast<uint16_t>(scale * 0x0101u)));
   const uint32_t c[2] = {r.x, r.y};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t h;
-    asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
-        : "=r"(h) : "r"(c[i >> 2] >> (8 * (i & 3))));
-    w[i] = pack_bf16(__half2float(__ushort_as_half(h & 0xFFFF)) * s, __half2float(__ushort_as_half(h >> 16)) * s);
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\tcvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(c[i]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(h[j]), "r"(s2));
+      w[4 * i + j] = f16x2_to_bf16x2(h[j]);
+    }
   }
 }
 
@@ -350,14 +406,19 @@ __device__ __forceinline__ int entries_of(const ListArgs& a, int b) {
   return n;
 }
 
-// What the block's queries see, and the runs of keys: all threads of the block call this.
-__device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
-  const int tid = threadIdx.x;
+// What the rows of row block x see, and their runs of keys; one warp.
+__device__ void make_plan(const ListArgs& a, int x, Plan* pl) {
+  const int lane = threadIdx.x & 31;
+  const Item it = item_of(a, x);
   const int t0 = it.r0 / a.H;
-  if (tid < kRows) {
+  int fmax = -1;
+  unsigned fmin = 0xFFFFFFFFu;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = lane + 32 * u;
     RowSees s{0, 0, -1, -1};   // nothing
-    if (tid < it.nr) {
-      const int t = (it.r0 + tid) / a.H;
+    if (r < it.nr) {
+      const int t = (it.r0 + r) / a.H;
       if (it.kind == kWindowRows) {
         int p1 = a.pos1[t];
         const int req = a.req_of ? a.req_of[t] : t;
@@ -367,33 +428,28 @@ __device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
       } else {
         const int ring = a.swa != nullptr ? max(0, min(a.ctx_len[t], kWindow)) : 0;
         const int n = it.kind == kRing ? 0 : entries_of(a, t);
-        s = RowSees{it.kind == kPrefixEntries ? min(n, a.n_prefix) : n, ring, -1, it.kind == kPrefixEntries ? 0 : t};
+        s = RowSees{it.kind == kPrefixEntries ? min(n, a.n_prefix) : n, ring, -1, 0};
+        fmax = max(fmax, s.f);
+        fmin = min(fmin, static_cast<unsigned>(s.f));
       }
     }
-    sm->sees[tid] = s;   // .run holds the request until the runs are built
-    sm->m[tid] = sm->limit[tid] = -INFINITY;
-    sm->msub[tid] = 0.f;
+    pl->sees[r] = s;   // window: .run holds the request until the runs are built
   }
-  if (tid < 16) (&sm->none[0][0])[tid] = 0u;
-  __syncthreads();
-  int f = 0, minf = 0;
-  if (it.kind != kWindowRows && tid < 32) {
-    const int f0 = tid < it.nr ? sm->sees[tid].f : -1, f1 = tid + 32 < it.nr ? sm->sees[tid + 32].f : -1;
-    f = __reduce_max_sync(0xFFFFFFFFu, max(f0, f1));
-    minf = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, min(static_cast<unsigned>(f0), static_cast<unsigned>(f1))));
-  }
-  if (tid == 0) {
+  fmax = __reduce_max_sync(0xFFFFFFFFu, fmax);
+  fmin = __reduce_min_sync(0xFFFFFFFFu, fmin);
+  __syncwarp();
+  if (lane == 0) {
     int nruns = 0, tiles = 0;
     if (it.kind != kWindowRows) {
       const int from = it.kind == kOwnEntries && !a.prefix_in_own ? a.n_prefix : 0;
       const int req = it.kind == kPrefixEntries ? 0 : t0;
-      if (f > from && it.kind != kRing) {
-        sm->runs[nruns++] = Run{req, 0, from, f - from, 0, 0, it.nr, 0, 1, minf, 1, 0};
-        tiles = tiles_of(f - from);
+      if (fmax > from && it.kind != kRing) {
+        pl->runs[nruns++] = Run{req, 0, from, fmax - from, 0, 0, it.nr, 0, 1, static_cast<int>(fmin), 1, 0};
+        tiles = tiles_of(fmax - from);
       }
-      const int ring = sm->sees[0].lo;   // one request's rows
+      const int ring = pl->sees[0].lo;   // one request's rows
       if ((it.kind == kRing || (it.kind == kOwnEntries && a.ring_in_own)) && ring > 0) {
-        sm->runs[nruns++] = Run{req, 0, 0, ring, tiles, 0, it.nr, 1, 1, ring, 1, 0};
+        pl->runs[nruns++] = Run{req, 0, 0, ring, tiles, 0, it.nr, 1, 1, ring, 1, 0};
         ++tiles;
       }
     } else {
@@ -401,185 +457,147 @@ __device__ void plan_block(const ListArgs& a, const Item& it, ListSmem* sm) {
       const int nq = (it.r0 + it.nr - 1) / a.H - t0 + 1;
       int q = 0;
       while (q < nq) {
-        const RowSees first = sm->sees[q * a.H < it.nr ? q * a.H : 0];
+        const RowSees first = pl->sees[q * a.H < it.nr ? q * a.H : 0];
         if (first.run < 0) { ++q; continue; }
         int lo = first.lo, hi = first.hi, f = first.f, last = first.hi;
         int minf = first.f, maxlo = first.lo, minhi = first.hi;
         int e = q + 1;
         for (; e < nq; ++e) {
-          const RowSees s = sm->sees[e * a.H];
+          const RowSees s = pl->sees[e * a.H];
           if (s.run != first.run || s.hi > last + 64 || s.hi < last - 64) break;
           last = s.hi;
           lo = min(lo, s.lo); hi = max(hi, s.hi); f = max(f, s.f);
           minf = min(minf, s.f); maxlo = max(maxlo, s.lo); minhi = min(minhi, s.hi);
         }
         const int f1 = min(f, lo);        // first rows before the windows; the rest of them lie inside
-        Run u{first.run, f1, lo, f1 + hi - lo + 1, tiles, q, e, 0, q == 0 && e == nq, minf, maxlo, minhi};
-        sm->runs[nruns++] = u;
-        tiles += (u.nkeys + kKeys - 1) / kKeys;
+        pl->runs[nruns++] = Run{first.run, f1, lo, f1 + hi - lo + 1, tiles, q, e, 0, q == 0 && e == nq, minf, maxlo, minhi};
+        tiles += tiles_of(f1 + hi - lo + 1);
         q = e;
       }
     }
-    sm->nruns = nruns;
-    sm->ntiles = tiles;
+    pl->item = it;
+    pl->nruns = nruns;
+    pl->nq = (it.nr + 15) & ~15;
+    pl->begin = static_cast<int>(static_cast<long long>(tiles) * it.split / it.nsplit);
+    pl->nt = static_cast<int>(static_cast<long long>(tiles) * (it.split + 1) / it.nsplit) - pl->begin;
   }
-  __syncthreads();
-  if (tid < it.nr) {
-    int run = -1;
-    if (it.kind != kWindowRows) {
-      run = 0;
-    } else {
-      const int q = (it.r0 + tid) / a.H - t0;
-      for (int i = 0; i < sm->nruns; ++i)
-        if (q >= sm->runs[i].q0 && q < sm->runs[i].q1) run = i;
+  __syncwarp();
+  if (it.kind == kWindowRows) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = lane + 32 * u;
+      int run = -1;
+      const int q = (it.r0 + r) / a.H - t0;
+      for (int i = 0; i < pl->nruns; ++i)
+        if (r < it.nr && q >= pl->runs[i].q0 && q < pl->runs[i].q1) run = i;
+      pl->sees[r].run = run;
     }
-    sm->sees[tid].run = run;
   }
-  __syncthreads();
 }
 
 // Walks a block's tiles in order.
 struct TileWalk {
-  const ListSmem* sm;
+  const Plan* pl;
   int run = 0;
-  __device__ __forceinline__ explicit TileWalk(const ListSmem* s) : sm(s) {}
+  __device__ __forceinline__ explicit TileWalk(const Plan* p) : pl(p) {}
   // key index of the tile's first key within its run, and the number of keys it holds
   __device__ __forceinline__ void seek(int tile, int* k0, int* n) {
-    while (run + 1 < sm->nruns && tile >= sm->runs[run + 1].tile0) ++run;
-    *k0 = (tile - sm->runs[run].tile0) * kKeys;
-    *n = min(kKeys, sm->runs[run].nkeys - *k0);
+    while (run + 1 < pl->nruns && tile >= pl->runs[run + 1].tile0) ++run;
+    *k0 = (tile - pl->runs[run].tile0) * kKeys;
+    *n = min(kKeys, pl->runs[run].nkeys - *k0);
   }
   __device__ __forceinline__ int position(int key) const {
-    const Run& u = sm->runs[run];
+    const Run& u = pl->runs[run];
     return key < u.f1 ? key : u.base + (key - u.f1);
   }
 };
 
 // ---------------------------------------------------------------------------
 // loading.  Warps 4m .. 4m + 3 have the dims 128 m .. 128 m + 127 (two chunks, one block of
-// the O product) of every tile, 32 rows each; lane l the 16-dim group l & 7 of the rows
-// l / 8, l / 8 + 4, ...: an instruction reads 128 bytes of four rows (whole sectors, few
-// cache lines).  NS chunk slots; the fills of a pair of slots wait for its release.
+// the O product) of every tile, 32 rows each; lane l the 16-dim group l & 3 of chunk l / 16 of
+// the rows (l / 4) & 3, + 4, ...: an instruction reads 128 bytes of four rows (whole sectors,
+// few cache lines), and eight neighbouring lanes store to different banks.  A tile's bytes are
+// requested while the tile before it is in its products.  NS chunk slots; the fills of a pair of
+// slots wait for its release.
 // ---------------------------------------------------------------------------
 template <int FMT, int NS>
 struct RowLoader {
-  // a tile's bytes are requested while the tile before it is in its products (and sent for
-  // into L2 while that one's weights are computed), its pages looked up a tile earlier
-  static constexpr int kRingPage = -2;
   ListSmem* sm;
   uint8_t* slot;
-  TileWalk walk;
-  unsigned long long p;      // the address of the tile's row 32 (warp & 3) + lane
-  int page, row;             // of the tile after it: physical page and logical row (-1: no such key)
   typename Raw<FMT>::Codes raw[2][4];
-  typename Raw<FMT>::Scales scales;   // of this lane's row
-  int block, row0, lane;
+  typename Raw<FMT>::Scales scales;   // of row row0 + lane
+  int block, row0, lane, group;       // group: of 16 dims
+  int keys;                           // of the tile requested
 
-  __device__ __forceinline__ RowLoader(ListSmem* s, uint8_t* slots) : sm(s), walk(s) {
+  __device__ __forceinline__ RowLoader(ListSmem* s, uint8_t* slots) : sm(s) {
     const int warp = threadIdx.x >> 5;
     block = warp >> 2;
     row0 = 32 * (warp & 3);
     lane = threadIdx.x & 31;
-    slot = slots + (2 * block % NS + ((lane >> 2) & 1)) * kChunk + (row0 + (lane >> 3)) * 128;
+    slot = slots + (2 * block % NS + (lane >> 4)) * kChunk + (row0 + ((lane >> 2) & 3)) * 128;
+    group = 8 * block + 4 * (lane >> 4) + (lane & 3);
   }
-  __device__ __forceinline__ const uint8_t* row_of(int j, int u) const {
-    return reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, p, 16 * j + 4 * u + (lane >> 3)));
+  __device__ __forceinline__ const uint8_t* row_of(int g, int j, int u) const {
+    return reinterpret_cast<const uint8_t*>(sm->rowp[g & 1][row0 + 16 * j + 4 * u + ((lane >> 2) & 3)]);
   }
-  __device__ __forceinline__ void load(int j) {
+  __device__ __forceinline__ void load(int g, int j) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const uint8_t* from = row_of(j, u);
+      const uint8_t* from = row_of(g, j, u);
       if constexpr (FMT == CSKV_FMT_BF16) {   // the block's 256 bytes of the row: into L2, until the chunks are free
-        if ((lane & 3) == 0) prefetch_l2(from + 256 * block + 128 * ((lane >> 2) & 1));
+        if ((lane & 3) == 0) prefetch_l2(from + 32 * group);
       } else {
         using C = typename Raw<FMT>::Codes;
-        raw[j][u] = __ldg(reinterpret_cast<const C*>(from) + 8 * block + (lane & 7));
+        raw[j][u] = __ldg(reinterpret_cast<const C*>(from) + group);
       }
     }
   }
-  __device__ __forceinline__ void store(int j) {
+  __device__ __forceinline__ void store(int g, int j) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int r = 16 * j + 4 * u;                  // rows r + (lane >> 3) of the warp's 32
-      const int swz = (r + (lane >> 3)) & 7;         // row0 is a multiple of 8
-      const int g = 2 * (lane & 3), odd = (lane >> 2) & 1;
-      // the two chunks' lanes store their two pieces in opposite order: no bank conflict
-      uint8_t* first = slot + r * 128 + (((g + odd) ^ swz) << 4);
-      uint8_t* second = slot + r * 128 + (((g + 1 - odd) ^ swz) << 4);
+      const int r = 16 * j + 4 * u, src = r + ((lane >> 2) & 3);   // of the warp's 32 rows
+      const int swz = src & 7, c = 2 * (lane & 3);                // row0 is a multiple of 8
+      uint8_t* first = slot + r * 128 + ((c ^ swz) << 4);
+      uint8_t* second = slot + r * 128 + (((c + 1) ^ swz) << 4);
       if constexpr (FMT == CSKV_FMT_BF16) {
-        const uint8_t* from = row_of(j, u) + 256 * block + 32 * (lane & 7);
-        cp_async16(first, from + 16 * odd);
-        cp_async16(second, from + 16 * (1 - odd));
+        const uint8_t* from = row_of(g, j, u) + 32 * group;
+        cp_async16(first, from);
+        cp_async16(second, from + 16);
       } else {
         uint32_t scale, w[8];
-        const int src = r + (lane >> 3);
         if constexpr (FMT == CSKV_FMT_FP8_E4M3_E8M0_B32) {
-          scale = byte_of(__shfl_sync(0xFFFFFFFFu, scales, src), (lane & 7) >> 1);
+          scale = byte_of(__shfl_sync(0xFFFFFFFFu, scales, src), (group >> 1) & 3);
         } else {
           const uint32_t s0 = __shfl_sync(0xFFFFFFFFu, scales.x, src), s1 = __shfl_sync(0xFFFFFFFFu, scales.y, src);
-          scale = byte_of((lane & 4) ? s1 : s0, lane & 3);
+          scale = byte_of((lane & 16) ? s1 : s0, lane & 3);
         }
         convert(raw[j][u], scale, w);
-        const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
-        *reinterpret_cast<uint4*>(first) = odd ? hi : lo;
-        *reinterpret_cast<uint4*>(second) = odd ? lo : hi;
+        *reinterpret_cast<uint4*>(first) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(second) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
   }
-  // looks tile `tile` of the item up in the block table
-  __device__ __forceinline__ void look_up(int tile, int end) {
-    row = -1;
-    if (tile >= end) return;
-    int k0, n;
-    walk.seek(tile, &k0, &n);
-    if (row0 + lane < n) {
-      const Run& u = sm->runs[walk.run];
-      row = walk.position(k0 + row0 + lane);
-      page = row / kPageRows;
-      if (u.ring) {
-        row += u.req * kWindow;
-        page = kRingPage;
-      } else if (sm->item.pages.block_table != nullptr) {
-        const int req = row < sm->item.n_prefix ? 0 : u.req;
-        page = page < sm->item.pages.max_pages
-                   ? __ldg(sm->item.pages.block_table + static_cast<long long>(req) * sm->item.pages.max_pages + page) : -1;
-      }
-    }
-  }
-  // sends the rows of the tile that was looked up into L2
-  __device__ __forceinline__ void prefetch() const {
-    if (block == 0 && row >= 0 && page >= 0 && page < sm->item.pages.num_pages)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                       page_row(sm->item.pages, page, row % kPageRows, sm->item.row_bytes).data),
-                   "r"(sm->item.row_bytes));
-  }
-  // requests the bytes of the tile that was looked up (tile i of the block), looks the next one up
-  __device__ __forceinline__ void request(int tile, int i, int end) {
-    const uint8_t* x = reinterpret_cast<const uint8_t*>(g_zero_row);
-    if (row >= 0) {
-      if (page >= 0 && page < sm->item.pages.num_pages) {
-        x = page_row(sm->item.pages, page, row % kPageRows, sm->item.row_bytes).data;
-      } else if (page == kRingPage) {
-        x = sm->item.ring + static_cast<long long>(row) * sm->item.row_bytes;
-      } else {
-        set_err(CSKV_ERR_BOUNDS);
-        if (block == 0) atomicOr(&sm->none[i & 3][row0 >> 5], 1u << lane);
-      }
-    }
-    p = reinterpret_cast<unsigned long long>(x);
+  // requests the bytes of the block's tile g, whose addresses have been looked up
+  __device__ __forceinline__ bool request(int g, unsigned long long spin) {
+    const bool ok = wait_warp(sm, &sm->rows_full[g & 1], (g >> 1) & 1, spin);
+    keys = ok ? sm->info[g & 1].n : 0;
+    if (row0 >= keys) return ok;   // none of this warp's rows
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(sm->rowp[g & 1][row0 + lane]);
     if constexpr (FMT == CSKV_FMT_FP8_E4M3_E8M0_B32) scales = __ldg(reinterpret_cast<const uint32_t*>(x + kD) + block);
     if constexpr (FMT == CSKV_FMT_FP4_E2M1_E4M3_B16) scales = __ldg(reinterpret_cast<const uint2*>(x + kD / 2) + block);
-    load(0);
-    load(1);
-    look_up(tile + 1, end);
+    load(g, 0);
+    load(g, 1);
+    return ok;
   }
   // the tile's rows into the chunks once they are free
-  __device__ __forceinline__ bool fill(int i, unsigned long long spin) {
-    const int n = i * (8 / NS) + 2 * block / NS;
+  __device__ __forceinline__ bool fill(int g, unsigned long long spin) {
+    const int n = g * (8 / NS) + 2 * block / NS;
     const bool ok = n == 0 || wait_bar(sm, &sm->free_[block % (NS / 2)], (n - 1) & 1, spin);
     __syncwarp();
-    store(0);
-    store(1);
+    if (row0 < keys) {   // (rows behind the last key: zeros up to this warp's 32, beyond them nothing is read)
+      store(g, 0);
+      store(g, 1);
+    }
     if (FMT == CSKV_FMT_BF16) cp_async_wait_all();
     fence_proxy_async_smem();
     __syncwarp();
@@ -587,6 +605,65 @@ struct RowLoader {
     return ok;
   }
 };
+
+// Tile `tile` of a plan, the block's tile g: looks its rows up in the block table and hands their
+// addresses on, once the tile two before it has been used; one warp.
+__device__ __forceinline__ bool look_up_tile(const ListArgs& a, ListSmem* sm, const Plan* pl, TileWalk& walk, int tile,
+                                             int g) {
+  const int lane = threadIdx.x & 31;
+  const Item& it = pl->item;
+  int k0, n;
+  walk.seek(tile, &k0, &n);
+  const Run& u = pl->runs[walk.run];
+  int row[4], page[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = 32 * j + lane;
+    row[j] = page[j] = -1;
+    if (r < n) {
+      row[j] = walk.position(k0 + r);
+      page[j] = row[j] / kPageRows;
+      if (!u.ring && it.pages.block_table != nullptr) {
+        const int req = row[j] < it.n_prefix ? 0 : u.req;
+        page[j] = page[j] < it.pages.max_pages
+                      ? __ldg(it.pages.block_table + static_cast<long long>(req) * it.pages.max_pages + page[j]) : -1;
+      }
+    }
+  }
+  const uint8_t* x[4];
+  uint32_t none[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[j] = reinterpret_cast<const uint8_t*>(g_zero_row);
+    bool bad = false;
+    if (row[j] >= 0) {
+      if (u.ring) x[j] = it.ring + (static_cast<long long>(u.req) * kWindow + row[j]) * it.row_bytes;
+      else if (page[j] >= 0 && page[j] < it.pages.num_pages)
+        x[j] = page_row(it.pages, page[j], row[j] % kPageRows, it.row_bytes).data;
+      else bad = true;
+    }
+    if (bad) set_err(CSKV_ERR_BOUNDS);
+    none[j] = __ballot_sync(0xFFFFFFFFu, bad);
+  }
+  if (a.prefetch) {   // into L2, until the loading warps have registers for them
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (row[j] >= 0)
+        for (int o = 0; o < it.row_bytes; o += 128) prefetch_l2(x[j] + o);
+  }
+  // all 128 keys seen by all rows: inside every window, or all first rows
+  const int pa = walk.position(k0), pb = walk.position(k0 + n - 1);
+  const int plain = u.whole && n == kKeys && (none[0] | none[1] | none[2] | none[3]) == 0u &&
+                    ((pb < u.min_f) || (pa >= u.max_lo && pb <= u.min_hi && pb - pa == kKeys - 1));
+  if (g >= 2 && !wait_warp(sm, &sm->rows_free[g & 1], ((g >> 1) - 1) & 1, a.spin)) return false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sm->rowp[g & 1][32 * j + lane] = reinterpret_cast<unsigned long long>(x[j]);
+  if (lane < 4) sm->none[g & 3][lane] = lane == 0 ? none[0] : lane == 1 ? none[1] : lane == 2 ? none[2] : none[3];
+  if (lane == 0) sm->info[g & 1] = TileInfo{n, k0, walk.run, plain};
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm->rows_full[g & 1]);
+  return true;
+}
 
 // The block's query rows into the K-major chunks of Q (rows nq apart); warps 0-7.  The rows
 // come in by asynchronous copies; the last 64 dims are then rotated in place, chunk 8 holds
@@ -652,10 +729,10 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 // bits over the keys k0 .. k0 + 31 of the run (the seen positions are at most three stretches
 // of key indices), then the 32 x 32 bit matrix is transposed; lane k ends with key k0 + k's
 // bits over the rows.  (16 rows: lanes c and c + 16 make the same row's bits.)
-__device__ __forceinline__ uint32_t seen_by(const ListSmem* sm, int run, int k0, int col) {
+__device__ __forceinline__ uint32_t seen_by(const Plan* pl, int run, int k0, int col) {
   const int lane = threadIdx.x & 31;
-  const RowSees s = sm->sees[col];
-  const Run& u = sm->runs[run];
+  const RowSees s = pl->sees[col];
+  const Run& u = pl->runs[run];
   uint32_t x = 0;
   if (u.ring) {
     x = s.run >= 0 ? low_bits(s.lo - k0) : 0u;
@@ -693,246 +770,128 @@ __device__ __noinline__ void clear_row(uint8_t* ktile, int key) {
     *reinterpret_cast<uint4*>(ktile + (x >> 3) * kChunk + sw128_offset(key, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// The tiles [begin, end) of a block: l accumulates this thread's key's weights of its 16 rows.
-template <int FMT>
-__device__ __forceinline__ bool attend_tiles(const ListArgs& a, ListSmem* sm, uint8_t* ktile,
-                                             uint8_t* ptile, uint32_t tmem, int nq, int begin, int end,
-                                             float (&l)[16]) {
+// The softmax of the block's tile g (`first`: no tile of these rows before it): l accumulates the warp's keys' weights of row cb + lane / 2.  after_s() runs once the tile's
+// S product is complete.
+template <class AfterS>
+__device__ __forceinline__ bool weigh_tile(const ListArgs& a, const Plan* pl, ListSmem* sm, uint8_t* ktile,
+                                           uint8_t* ptile, uint32_t tmem, int g, bool first, float& l,
+                                           AfterS&& after_s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarter = warp & 3, group = warp >> 2;
   const int cb = group * 16;        // this thread's rows (columns of S^T)
+  const int nq = pl->nq;
   const bool has = cb < nq;
   const int key = quarter * 32 + lane;
   const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
-  RowLoader<FMT, 8> rows(sm, ktile);
-  TileWalk walk(sm);
-  bool ok = true;
-  rows.look_up(begin, end);
-  rows.request(begin, 0, end);
-  for (int i = 0; i < end - begin; ++i) {
-    ok = rows.fill(i, a.spin) && ok;
-    if (begin + i + 1 < end) rows.request(begin + i + 1, i + 1, end);
-    int k0, n;
-    walk.seek(begin + i, &k0, &n);
-    const Run& u = sm->runs[walk.run];
-    // all 128 keys seen by all rows: inside every window, or all first rows
-    const int pa = walk.position(k0), pb = walk.position(k0 + n - 1);
-    bool plain = u.whole && n == kKeys &&
-                 ((pb < u.min_f) || (pa >= u.max_lo && pb <= u.min_hi && pb - pa == kKeys - 1));
-    uint32_t bits = 0xFFFFu;
-    if (!plain && has) {   // before S is complete
-      bits = seen_by(sm, walk.run, k0 + quarter * 32, cb + (lane & 15));
-      if (key >= n) bits = 0u;
-    }
-    ok = wait_bar(sm, &sm->bar_s[0], i & 1, a.spin) && ok;
-    __syncwarp();
-    tc_fence_after();
-    float z[16];
-    if (has) {
-      tmem_ld16(tmem + kTmemS + tlane + cb, z);
-      tmem_wait_ld();
-    }
-    const uint32_t none = sm->none[i & 3][quarter];
-    if (none != 0u) {
-      plain = false;
-      if ((none >> lane) & 1u) bits = 0u;
-    }
-    bool unfit = false;
-    if (has && key < n && !(fabsf(z[0]) < INFINITY)) {
-      unfit = unfit_row(ktile, key);
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (unfit) z[c] = __int_as_float(0x7FC00000);
-    }
-    __syncwarp();
-    if (!plain) {
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (((bits >> c) & 1u) == 0u) z[c] = -INFINITY;
-    }
-    bool above = false;
-    if (has) {
-#pragma unroll
-      for (int c = 0; c < 16; c += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(&sm->limit[cb + c]);
-        above |= (z[c] > m.x) | (z[c + 1] > m.y) | (z[c + 2] > m.z) | (z[c + 3] > m.w);
-      }
-    }
-    const bool moves = work_any(above);
-    if (unfit && group == 0) clear_row(ktile, key);   // every group has looked at it
-    if (moves) {   // some row's reference moves: the tile's maxima, exactly
-      if (has) {
-        float t[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) t[c] = z[c];
-        const float mine = reduce_columns(t, [](float x, float y) { return fmaxf(x, y); });
-        if ((lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = mine;
-      }
-      work_sync();
-      if (tid < nq) {
-        const float old = sm->m[tid], old_sub = sm->msub[tid];
-        const float now = fmaxf(fmaxf(fmaxf(sm->part[0][tid], sm->part[1][tid]), fmaxf(sm->part[2][tid], sm->part[3][tid])), old);
-        const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
-        sm->fac[tid] = old == -INFINITY ? 0.f : exp2f(old_sub - sub);
-        sm->m[tid] = now;
-        sm->limit[tid] = now + a.slack;
-        sm->msub[tid] = sub;
-      }
-      work_sync();
-      if (has) {
-#pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm->fac[cb + c]);
-          l[c] *= f.x;
-          l[c + 1] *= f.y;
-          l[c + 2] *= f.z;
-          l[c + 3] *= f.w;
-        }
-      }
-      if (i > 0) {   // the S commit says that the O products so far are complete
-#pragma unroll 1
-        for (int g = 0; g < nq; g += 16) {   // this warp's 32 dims of block `group`, 16 rows at a time
-          float o[16];
-          const uint32_t at = tmem + tlane + group * kRows + g;
-          tmem_ld16(at, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] *= sm->fac[g + c];
-          tmem_st16(at, o);
-        }
-        tmem_wait_st();
-      }
-    }
-    if (lane == 0 && none != 0u && group == 0) sm->none[i & 3][quarter] = 0u;
-    if (has) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float4 m0 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * g]);
-        const float4 m1 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * g + 4]);
-        const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-        float p[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          p[c] = exp2_fast(fmaf(z[8 * g + c], a.scale_log2, -mm[c]));
-          l[8 * g + c] += p[c];
-        }
-        *reinterpret_cast<uint4*>(ptile + sw128_offset(key, group * 2 + g)) =
-            make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
-      }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm->bar_p[0]);
-    if (a.prefetch) rows.prefetch();
+  const TileInfo t = sm->info[g & 1];
+  const int n = t.n;
+  uint32_t bits = 0xFFFFu;
+  if (t.plain == 0 && has) {   // before S is complete
+    bits = seen_by(pl, t.run, t.k0 + quarter * 32, cb + (lane & 15));
+    if (key >= n || ((sm->none[g & 3][quarter] >> lane) & 1u) != 0u) bits = 0u;
   }
+  const bool ok = wait_bar(sm, &sm->bar_s[0], g & 1, a.spin);
+  __syncwarp();
+  tc_fence_after();
+  float z[16];
+  if (has) {
+    tmem_ld16(tmem + kTmemS + tlane + cb, z);
+    tmem_wait_ld();
+  }
+  after_s();
+  bool unfit = false;
+  if (has && key < n && !(fabsf(z[0]) < INFINITY)) {
+    unfit = unfit_row(ktile, key);
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (unfit) z[c] = __int_as_float(0x7FC00000);
+  }
+  __syncwarp();
+  if (t.plain == 0) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (((bits >> c) & 1u) == 0u) z[c] = -INFINITY;
+  }
+  bool above = false;
+  if (has) {
+#pragma unroll
+    for (int c = 0; c < 16; c += 4) {
+      const float4 m = *reinterpret_cast<const float4*>(&sm->limit[cb + c]);
+      above |= (z[c] > m.x) | (z[c + 1] > m.y) | (z[c + 2] > m.z) | (z[c + 3] > m.w);
+    }
+  }
+  const bool moves = work_any(above);
+  if (unfit && group == 0) clear_row(ktile, key);   // every group has looked at it
+  if (moves) {   // some row's reference moves: the tile's maxima, exactly
+    if (has) {
+      float t[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) t[c] = z[c];
+      const float mine = reduce_columns(t, [](float x, float y) { return fmaxf(x, y); });
+      if ((lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = mine;
+    }
+    work_sync();
+    if (tid < nq) {
+      const float old = sm->m[tid], old_sub = sm->msub[tid];
+      const float now = fmaxf(fmaxf(fmaxf(sm->part[0][tid], sm->part[1][tid]), fmaxf(sm->part[2][tid], sm->part[3][tid])), old);
+      const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
+      sm->fac[tid] = old == -INFINITY ? 0.f : exp2f(old_sub - sub);
+      sm->m[tid] = now;
+      sm->limit[tid] = now + a.slack;
+      sm->msub[tid] = sub;
+    }
+    work_sync();
+    if (has) l *= sm->fac[cb + (lane >> 1)];
+    if (!first) {   // the S commit says that the O products so far are complete
+#pragma unroll 1
+      for (int r = 0; r < nq; r += 16) {   // this warp's 32 dims of block `group`, 16 rows at a time
+        float o[16];
+        const uint32_t at = tmem + tlane + group * kRows + r;
+        tmem_ld16(at, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) o[c] *= sm->fac[r + c];
+        tmem_st16(at, o);
+      }
+      tmem_wait_st();
+    }
+  }
+  if (has) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 m0 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * h]);
+      const float4 m1 = *reinterpret_cast<const float4*>(&sm->msub[cb + 8 * h + 4]);
+      const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) z[8 * h + c] = exp2_fast(fmaf(z[8 * h + c], a.scale_log2, -mm[c]));
+      const float* p = z + 8 * h;
+      *reinterpret_cast<uint4*>(ptile + sw128_offset(key, group * 2 + h)) =
+          make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm->bar_p[0]);
+  if (lane == 0) mbar_arrive(&sm->rows_free[g & 1]);
+  // while the O product starts: lanes 2c and 2c + 1 keep the sum of the warp's keys for row cb + c
+  if (has) l += reduce_columns(z, [](float x, float y) { return x + y; });
   return ok;
 }
 
-// One kernel per row format: a call whose rings have another format than its cache launches two
-// (a block's code stays within its registers and the instruction cache).
-template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_constant__ ListArgs a) {
-  if (a.rings_only) grid_dep_launch();   // the other kernel of the call may start
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* ktile = base;                              // 8 chunks of 128 rows x 128 B
-  uint8_t* qtile = ktile + 8 * kChunk;                // 9 chunks of nq rows x 128 B
-  uint8_t* ptile = qtile + 9 * kRows * 128;           // 128 keys x 128 B
-  ListSmem* sm = reinterpret_cast<ListSmem*>(ptile + kChunk);
+
+// The epilogue of a row block of nt tiles: the rows' sums, then O^T out.
+__device__ __forceinline__ void write_rows(const ListArgs& a, const Plan* pl, ListSmem* sm, uint32_t tmem, int nt,
+                                           float l) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Item it = item_of(a, blockIdx.x);
-  const int nq = (it.nr + 15) & ~15;
-
-  if (tid == 0) {
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm->full[i], 4);
-      mbar_init(&sm->free_[i], 1);
-    }
-    mbar_init(&sm->bar_s[0], 2);
-    mbar_init(&sm->bar_p[0], kWorkWarps);
-    mbar_init(&sm->bar_q, kWorkWarps);
-    sm->abort = 0;
-    sm->item = it;
-    fence_mbar_init();
-  }
-  if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 512);
-  if (warp < kWorkWarps) request_queries(a, it.r0, it.nr, nq, qtile);
-  tc_fence_before();
-  plan_block(a, it, sm);
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
-  const int begin = static_cast<int>(static_cast<long long>(sm->ntiles) * it.split / it.nsplit);
-  const int end = static_cast<int>(static_cast<long long>(sm->ntiles) * (it.split + 1) / it.nsplit);
-  const int nt = end - begin;
-
-  if (warp == kWorkWarps) {
-    if (nt > 0 && elect_lane()) {
-      const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
-      const uint32_t ido = make_idesc(1, 1, 1, 1, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
-      const uint64_t dk = smem_desc_sw128(smem_u32(ktile), 16, 1024);
-      const uint64_t dq = smem_desc_sw128(smem_u32(qtile), 16, 1024);
-      const uint64_t dv = smem_desc_sw128(smem_u32(ktile), kChunk, 1024);
-      const uint64_t dp = smem_desc_sw128(smem_u32(ptile), kChunk, 1024);
-      const uint32_t qstep = nq * 8;   // a chunk of Q, in the descriptors' 16-byte units
-      TileWalk walk(sm);
-      bool ok = wait_bar(sm, &sm->bar_q, 0, a.spin);
-      for (int i = 0; i < nt && ok; ++i) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if ((c & 1) == 0) {
-            ok = ok && wait_bar(sm, &sm->full[c >> 1], i & 1, a.spin);
-            tc_fence_after();
-          }
-          if (ok) issue_s_chunk(tmem + kTmemS, dk + c * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
-        }
-        mma_commit(&sm->bar_s[0]);
-        mbar_arrive(&sm->bar_s[0]);   // hands on what the loading warps wrote (none)
-        ok = ok && wait_bar(sm, &sm->bar_p[0], i & 1, a.spin);
-        if (!ok) break;
-        tc_fence_after();
-        int k0, n;
-        walk.seek(begin + i, &k0, &n);
-        const int ks = (n + 15) >> 4;
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-          const uint64_t dvb = dv + mb * (kChunk >> 3);
-          if (i == 0) mma_set(tmem + mb * kRows, dvb, dp, ido);
-          else mma_add(tmem + mb * kRows, dvb, dp, ido);
-          if (ks == 8) {
-#pragma unroll
-            for (int k = 1; k < 8; ++k) mma_add(tmem + mb * kRows, dvb + k * 128, dp + k * 128, ido);
-          } else {
-#pragma unroll 1
-            for (int k = 1; k < ks; ++k) mma_add(tmem + mb * kRows, dvb + k * 128, dp + k * 128, ido);
-          }
-          mma_commit(&sm->free_[mb]);
-        }
-      }
-    }
-    __syncwarp();
-  } else {
-    rotate_queries(a, it.r0, it.nr, nq, qtile);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm->bar_q);
-    const int quarter = warp & 3, group = warp >> 2;
-    const int cb = group * 16;
-    const bool has = cb < nq;
-    const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
-    float l[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) l[c] = 0.f;
-    if (nt > 0) {
-      const bool ok = attend_tiles<FMT>(a, sm, ktile, ptile, tmem, nq, begin, end, l);
-      if (ok) wait_bar(sm, &sm->free_[3], (nt - 1) & 1, a.spin);
-    }
-    __syncwarp();
-    tc_fence_after();
+  const int quarter = warp & 3, group = warp >> 2;
+  const Item& it = pl->item;
+  const int nq = pl->nq;
+  const int cb = group * 16;
+  const bool has = cb < nq;
+  const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
     // ---- the rows' sums over the 128 keys
-    if (has) {
-      const float mine = reduce_columns(l, [](float x, float y) { return x + y; });
-      if ((lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = mine;
-    }
+    if (has && (lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = l;
     work_sync();
     if (tid < nq) {
       const float sum = ((sm->part[0][tid] + sm->part[1][tid]) + sm->part[2][tid]) + sm->part[3][tid];
@@ -956,6 +915,10 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
         }
       }
       sm->fac[tid] = f;
+    }
+    if (tid < kRows) {   // for the next rows
+      sm->m[tid] = sm->limit[tid] = -INFINITY;
+      sm->msub[tid] = 0.f;
     }
     work_sync();
     // ---- O^T out: a thread has dim d of 16 rows at a time
@@ -1008,6 +971,162 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
         if (g + c + (lane & 1) < it.nr) *reinterpret_cast<uint32_t*>(to + c * (kD * 2)) = v;
       }
     }
+}
+
+// One kernel per row format: a call whose rings have another format than its cache launches two
+// (a block's code stays within its registers and the instruction cache).
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_constant__ ListArgs a) {
+  if (a.lead) grid_dep_launch();   // the call's launch for the rings may start
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* ktile = base;                              // 8 chunks of 128 rows x 128 B
+  uint8_t* qtile = ktile + 8 * kChunk;                // 9 chunks of nq rows x 128 B
+  uint8_t* ptile = qtile + 9 * kRows * 128;           // 128 keys x 128 B
+  ListSmem* sm = reinterpret_cast<ListSmem*>(ptile + kChunk);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // this block's row blocks: blockIdx.x, + gridDim.x, ...
+  const int items = (a.items - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm->full[i], 4);
+      mbar_init(&sm->free_[i], 1);
+    }
+    mbar_init(&sm->bar_s[0], 2);
+    mbar_init(&sm->bar_p[0], kWorkWarps);
+    mbar_init(&sm->bar_q, kWorkWarps);
+    mbar_init(&sm->drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->plan_full[i], 1);
+      mbar_init(&sm->plan_free[i], kWorkWarps + 1);
+      mbar_init(&sm->rows_full[i], 1);
+      mbar_init(&sm->rows_free[i], kWorkWarps);
+    }
+    sm->abort = 0;
+    fence_mbar_init();
+  }
+  if (tid < kRows) {
+    sm->m[tid] = sm->limit[tid] = -INFINITY;
+    sm->msub[tid] = 0.f;
+  }
+  if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 512);
+  if (warp < kWorkWarps) {
+    const Item it = item_of(a, blockIdx.x);
+    request_queries(a, it.r0, it.nr, (it.nr + 15) & ~15, qtile);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
+
+  if (warp == kWorkWarps + 1) {          // ---- plans and addresses
+    bool ok = true;
+    int g = 0;
+    for (int e = 0; e < items && ok; ++e) {
+      if (e >= 2) ok = wait_warp(sm, &sm->plan_free[e & 1], ((e >> 1) - 1) & 1, a.spin);
+      if (!ok) break;
+      Plan* pl = &sm->plan[e & 1];
+      make_plan(a, blockIdx.x + e * gridDim.x, pl);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->plan_full[e & 1]);
+      TileWalk walk(pl);
+      for (int i = 0; i < pl->nt && ok; ++i, ++g) ok = look_up_tile(a, sm, pl, walk, pl->begin + i, g);
+    }
+  } else if (warp == kWorkWarps) {       // ---- products
+    if (elect_lane()) {
+      const uint64_t dk = smem_desc_sw128(smem_u32(ktile), 16, 1024);
+      const uint64_t dq = smem_desc_sw128(smem_u32(qtile), 16, 1024);
+      const uint64_t dv = smem_desc_sw128(smem_u32(ktile), kChunk, 1024);
+      const uint64_t dp = smem_desc_sw128(smem_u32(ptile), kChunk, 1024);
+      bool ok = true;
+      int g = 0;
+      for (int e = 0; e < items && ok; ++e) {
+        ok = wait_bar(sm, &sm->plan_full[e & 1], (e >> 1) & 1, a.spin);
+        if (!ok) break;
+        const Plan* pl = &sm->plan[e & 1];
+        const int nt = pl->nt, nq = pl->nq;
+        const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
+        const uint32_t ido = make_idesc(1, 1, 1, 1, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
+        const uint32_t qstep = nq * 8;   // a chunk of Q, in the descriptors' 16-byte units
+        ok = wait_bar(sm, &sm->bar_q, e & 1, a.spin);
+        for (int i = 0; i < nt && ok; ++i, ++g) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if ((c & 1) == 0) {
+              ok = ok && wait_bar(sm, &sm->full[c >> 1], g & 1, a.spin);
+              tc_fence_after();
+            }
+            if (ok) issue_s_chunk(tmem + kTmemS, dk + c * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
+          }
+          const int ks = (sm->info[g & 1].n + 15) >> 4;   // (the tile's, until its weights are there)
+          mma_commit(&sm->bar_s[0]);
+          mbar_arrive(&sm->bar_s[0]);   // hands on what the loading warps wrote (none)
+          ok = ok && wait_bar(sm, &sm->bar_p[0], g & 1, a.spin);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb) {
+            const uint64_t dvb = dv + mb * (kChunk >> 3);
+            if (i == 0) mma_set(tmem + mb * kRows, dvb, dp, ido);
+            else mma_add(tmem + mb * kRows, dvb, dp, ido);
+            if (ks == 8) {
+#pragma unroll
+              for (int k = 1; k < 8; ++k) mma_add(tmem + mb * kRows, dvb + k * 128, dp + k * 128, ido);
+            } else {
+#pragma unroll 1
+              for (int k = 1; k < ks; ++k) mma_add(tmem + mb * kRows, dvb + k * 128, dp + k * 128, ido);
+            }
+            mma_commit(&sm->free_[mb]);
+          }
+        }
+        mbar_arrive(&sm->plan_free[e & 1]);
+      }
+      drain_products(sm);
+    }
+    __syncwarp();
+  } else {                               // ---- loads, softmax, epilogue
+    RowLoader<FMT, 8> rows(sm, ktile);
+    bool ok = true, requested = false;
+    int g = 0;
+    auto plan_of = [&](int e) -> const Plan* {   // nullptr: not there in time
+      return wait_warp(sm, &sm->plan_full[e & 1], (e >> 1) & 1, a.spin) ? &sm->plan[e & 1] : nullptr;
+    };
+    for (int e = 0; e < items; ++e) {
+      const Plan* pl = plan_of(e);
+      if (work_any(pl == nullptr)) break;
+      rotate_queries(a, pl->item.r0, pl->item.nr, pl->nq, qtile);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->bar_q);
+      float l = 0.f;
+      const int nt = pl->nt;
+      if (nt > 0 && !requested) ok = rows.request(g, a.spin) && ok;
+      for (int i = 0; i < nt; ++i, ++g) {
+        ok = rows.fill(g, a.spin) && ok;
+        // the next tile's bytes, this row block's or the next one's
+        const bool last = i + 1 == nt;
+        const Plan* np = !last ? pl : e + 1 < items ? plan_of(e + 1) : nullptr;
+        requested = np != nullptr && (!last || np->nt > 0);
+        if (requested) ok = rows.request(g + 1, a.spin) && ok;
+        ok = weigh_tile(a, pl, sm, ktile, ptile, tmem, g, i == 0, l, [&]() {
+          // the last product on these queries is complete: the next ones may come
+          if (last && np != nullptr) request_queries(a, np->item.r0, np->item.nr, np->nq, qtile);
+        }) && ok;
+      }
+      if (nt > 0 && ok) wait_bar(sm, &sm->free_[3], (g - 1) & 1, a.spin);
+      if (nt == 0 && e + 1 < items) {
+        const Plan* np = plan_of(e + 1);
+        work_sync();   // everybody has rotated these rows
+        if (np != nullptr) request_queries(a, np->item.r0, np->item.nr, np->nq, qtile);
+      }
+      __syncwarp();
+      tc_fence_after();
+      write_rows(a, pl, sm, tmem, nt, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->plan_free[e & 1]);
+    }
+    cp_async_wait_all();   // (queries on their way, if a wait gave up)
   }
   tc_fence_before();
   __syncthreads();
@@ -1015,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (a.after_rings) grid_dep_wait();   // this grid completes after the rings' one
+  if (a.rings_only && a.beside) grid_dep_wait();   // this grid completes after the one it runs beside
 }
 
 // Joins a row's partial outputs in order, adds the sink, turns the output back: 64 threads of
@@ -1082,7 +1201,7 @@ __device__ __forceinline__ void load_request(const ListArgs& a, ListSmem* sm, in
   if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->bar_q);
 }
 
-// The block's runs: an even share of all requests' tiles (up to 64 requests), or of one
+// The block's runs: an even share of all requests' tiles (up to kRuns requests), or of one
 // request's.  One warp calls this.
 __device__ __forceinline__ void plan_weights(const ListArgs& a, ListSmem* sm) {
   const int lane = threadIdx.x & 31;
@@ -1132,14 +1251,15 @@ __device__ __forceinline__ void plan_weights(const ListArgs& a, ListSmem* sm) {
       const uint32_t below = (1u << lane) - 1u;
       const int at = __popc(have[0] & below) + __popc(have[1] & below) + (u == 1 ? (have[0] >> lane) & 1 : 0);
       const long long k0 = (from[u] - before[u]) * kKeys, k1 = min(static_cast<long long>(keys[u]), (to[u] - before[u]) * kKeys);
-      sm->runs[at] = Run{req[u], 0, static_cast<int>(a.first + k0), static_cast<int>(k1 - k0),
+      sm->plan[0].runs[at] = Run{req[u], 0, static_cast<int>(a.first + k0), static_cast<int>(k1 - k0),
                          static_cast<int>(from[u] - lo), 0, 1, 0, 1, 0, 0, 0};
     }
   }
   nruns = __popc(have[0]) + __popc(have[1]);
   if (lane == 0) {
-    sm->nruns = nruns;
-    sm->ntiles = static_cast<int>(hi - lo);
+    sm->plan[0].nruns = nruns;
+    sm->plan[0].begin = 0;
+    sm->plan[0].nt = static_cast<int>(hi - lo);
   }
 }
 
@@ -1154,19 +1274,20 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
   const int key = quarter * 32 + lane;
   const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
   RowLoader<FMT, NS> rows(sm, slots);
-  TileWalk walk(sm);
-  rows.look_up(0, nt);
-  rows.request(0, 0, nt);
+  const Plan* pl = &sm->plan[0];
+  TileWalk walk(pl);
+  rows.request(0, a.spin);
   for (int i = 0; i <= nt; ++i) {
     if (i < nt) {
       rows.fill(i, a.spin);
-      if (i + 1 < nt) rows.request(i + 1, i + 1, nt);
+      if (lane == 0) mbar_arrive(&sm->rows_free[i & 1]);
+      if (i + 1 < nt) rows.request(i + 1, a.spin);
     }
     if (i == 0) continue;
     const int t = i - 1, buf = t & 1;
     int k0, n;
     walk.seek(t, &k0, &n);
-    const Run& u = sm->runs[walk.run];
+    const Run& u = pl->runs[walk.run];
     wait_bar(sm, &sm->bar_s[buf], (t >> 1) & 1, a.spin);
     __syncwarp();
     tc_fence_after();
@@ -1185,20 +1306,18 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
     }
     tc_fence_before();
     const uint32_t none = sm->none[t & 3][quarter];
-    float* part = &sm->part[0][0] + buf * (3 * kKeys);   // three groups' shares, two tiles in turn
+    float* part = lse + 128 + buf * (3 * kKeys);   // three groups' shares, two tiles in turn
     if (group > 0) part[(group - 1) * kKeys + key] = w;
     work_sync();
-    if (group == 0 && lane == 0 && none != 0u) sm->none[t & 3][quarter] = 0u;
     if (lane == 0) mbar_arrive(&sm->bar_p[buf]);
-    rows.prefetch();
     if (group == 0 && key < n) {
       w = (w + part[key]) + (part[kKeys + key] + part[2 * kKeys + key]);
       if ((none >> lane) & 1u) w = 0.f;
       const long long b = u.req, j = walk.position(k0 + key);
       a.acc_out[b * a.acc_out_stride + j] = a.decay * a.acc[b * a.acc_stride + j] + w;
     }
-    if (i < nt && walk.run + 1 < sm->nruns && i == sm->runs[walk.run + 1].tile0)
-      load_request(a, sm, sm->runs[walk.run + 1].req, nq, qtile, lse);
+    if (i < nt && walk.run + 1 < pl->nruns && i == pl->runs[walk.run + 1].tile0)
+      load_request(a, sm, pl->runs[walk.run + 1].req, nq, qtile, lse);
   }
 }
 
@@ -1210,7 +1329,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   const int nq = (a.H + 15) & ~15;
   uint8_t* qtile = slots + kWeightSlots * kChunk;
   ListSmem* sm = reinterpret_cast<ListSmem*>(qtile + 9 * nq * 128);
-  float* lse = reinterpret_cast<float*>(sm + 1);   // [128]
+  float* lse = reinterpret_cast<float*>(sm + 1);   // [128], then the groups' shares of two tiles
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -1219,27 +1338,33 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       mbar_init(&sm->free_[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->rows_full[i], 1);
+      mbar_init(&sm->rows_free[i], kWorkWarps);
       mbar_init(&sm->bar_s[i], 2);
       mbar_init(&sm->bar_p[i], kWorkWarps);
     }
     mbar_init(&sm->bar_q, kWorkWarps);
+    mbar_init(&sm->drained, 1);
     sm->abort = 0;
     fence_mbar_init();
-    sm->item.row_bytes = a.row_bytes;
-    sm->item.pages = a.kv;
-    sm->item.n_prefix = 0;
+    sm->plan[0].item.row_bytes = a.row_bytes;
+    sm->plan[0].item.pages = a.kv;
+    sm->plan[0].item.n_prefix = 0;
   }
   if (warp == 1) plan_weights(a, sm);
-  if (tid >= 64 && tid < 80) (&sm->none[0][0])[tid - 64] = 0u;
   if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
-  const int nt = sm->ntiles;
+  const int nt = sm->plan[0].nt;
 
   if (nt > 0) {
-    if (warp == kWorkWarps) {
+    if (warp == kWorkWarps + 1) {
+      TileWalk walk(&sm->plan[0]);
+      bool ok = true;
+      for (int g = 0; g < nt && ok; ++g) ok = look_up_tile(a, sm, &sm->plan[0], walk, g, g);
+    } else if (warp == kWorkWarps) {
       if (elect_lane()) {
         const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
         const uint64_t dk = smem_desc_sw128(smem_u32(slots), 16, 1024);
@@ -1249,7 +1374,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         int run = -1;
         for (int i = 0; i < nt && ok; ++i) {
           const int buf = i & 1;
-          if (run + 1 < sm->nruns && i == sm->runs[run + 1].tile0) {
+          if (run + 1 < sm->plan[0].nruns && i == sm->plan[0].runs[run + 1].tile0) {
             ++run;
             ok = wait_bar(sm, &sm->bar_q, run & 1, a.spin);
           }
@@ -1268,10 +1393,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           mma_commit(&sm->bar_s[buf]);
           mbar_arrive(&sm->bar_s[buf]);   // hands on what the loading warps wrote (none)
         }
+        drain_products(sm);
       }
       __syncwarp();
     } else {
-      load_request(a, sm, sm->runs[0].req, nq, qtile, lse);
+      load_request(a, sm, sm->plan[0].runs[0].req, nq, qtile, lse);
       if (a.kv.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32)
         weigh_tiles<CSKV_FMT_FP8_E4M3_E8M0_B32, kWeightSlots>(a, sm, slots, qtile, lse, tmem, nq, nt);
       else if (a.kv.fmt == CSKV_FMT_FP4_E2M1_E4M3_B16)
@@ -1299,7 +1425,7 @@ int weight_slots(int H) { return H <= kRows ? 8 : 4; }
 
 size_t weights_smem(int H) {
   const int nq = (H + 15) & ~15;
-  return 1024 + weight_slots(H) * size_t(kChunk) + 9 * size_t(nq) * 128 + sizeof(ListSmem) + 128 * sizeof(float);
+  return 1024 + weight_slots(H) * size_t(kChunk) + 9 * size_t(nq) * 128 + sizeof(ListSmem) + (128 + 6 * kKeys) * sizeof(float);
 }
 
 __host__ __device__ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1355,7 +1481,7 @@ ListPlan base_plan(int T, int H, bool grouped) {
   ListPlan p = {};
   p.head_blocks = (H + kRows - 1) / kRows;
   p.heads_per_block = (H + p.head_blocks - 1) / p.head_blocks;
-  p.group = p.head_blocks == 1 && grouped ? kRows / H : 1;
+  p.group = p.head_blocks == 1 && grouped ? std::min(kRuns, kRows / H) : 1;
   p.blocks = (T + p.group - 1) / p.group * p.head_blocks;
   p.split = p.prefix_split = 1;
   return p;
@@ -1471,21 +1597,26 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
   const size_t rows = static_cast<size_t>(a.T) * a.H;
   a.opart = static_cast<float*>(workspace);
   a.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a256(rows * p.parts * kD * 4));
-  a.rings_only = a.after_rings = 0;
   // few blocks: a request's keys come from HBM; many blocks read them again and again from L2
   a.prefetch = a.req_of == nullptr && p.prefix_blocks == 0 && p.head_blocks == 1;
+  a.rings_only = a.lead = a.beside = 0;
+  const int blocks = p.prefix_blocks * p.prefix_split + (a.pos1 != nullptr ? p.blocks : p.own_blocks) * p.split;
   cudaError_t e = cudaSuccess;
+  if (blocks > 0) {
+    a.items = blocks;
+    a.lead = p.ring_blocks > 0;
+    // prompts: one block per SM, each with several row blocks; otherwise the row blocks differ
+    // in length, and the hardware's order balances them better
+    e = launch_kind(a, a.kv.fmt, a.pos1 != nullptr ? std::min(blocks, kSmsPlanned) : blocks, false, stream);
+    if (e != cudaSuccess) return e;
+  }
   if (p.ring_blocks > 0) {
     ListArgs r = a;
     r.rings_only = 1;
-    e = launch_kind(r, a.swa_fmt, p.ring_blocks, false, stream);
-    if (e != cudaSuccess) return e;
-  }
-  const unsigned grid = static_cast<unsigned>(p.prefix_blocks) * p.prefix_split +
-                        static_cast<unsigned>(a.pos1 != nullptr ? p.blocks : p.own_blocks) * p.split;
-  if (grid > 0) {
-    a.after_rings = p.ring_blocks > 0;
-    e = launch_kind(a, a.kv.fmt, grid, a.after_rings != 0, stream);
+    r.lead = 0;
+    r.beside = blocks > 0;
+    r.items = p.ring_blocks;
+    e = launch_kind(r, a.swa_fmt, p.ring_blocks, r.beside != 0, stream);
   }
   if (e != cudaSuccess || p.parts <= 1) return e;
   // launched while the kernel before it ends; waits for it before it reads anything
@@ -1560,10 +1691,11 @@ cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32
   a.acc_stride = acc_stride;
   a.acc_out = acc_out;
   a.acc_out_stride = acc_out_stride;
-  // up to 64 requests: the blocks, one per SM, share all their tiles evenly, whatever their
+  a.prefetch = 1;
+  // up to kRuns requests: the blocks, one per SM, share all their tiles evenly, whatever their
   // lengths; more requests: blocks of one request's tiles each
   const int tiles = tiles_of(max_entries - first);
-  a.balanced = B <= kRows;
+  a.balanced = B <= kRuns;
   unsigned grid = static_cast<unsigned>(std::min<long long>(kSmsPlanned, static_cast<long long>(B) * tiles));
   if (!a.balanced) {
     a.split = shares(tiles, best_length(tiles, [&](int l) {
