@@ -361,8 +361,6 @@ cudaError_t launch_evict(const cskv_paged* caches, int ncaches, const float* acc
   const int slice = ((((max_entries + blocks - 1) / blocks + kSelWarps - 1) / kSelWarps + 31) & ~31) * kSelWarps;
   a.cached = slice <= kKeysInSmem;
   const size_t smem = a.cached ? size_t(slice) * 4 : 0;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysInSmem * 4);
-  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = blocks;
@@ -374,7 +372,8 @@ cudaError_t launch_evict(const cskv_paged* caches, int ncaches, const float* acc
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+  static std::atomic<uint64_t> allowed;
+  const cudaError_t e = launch_with_shared_memory(cfg, evict_select_kernel, allowed, kKeysInSmem * 4, a);
   if (e != cudaSuccess || a.max_pairs == 0 || a.fused) return e;
   // starts while the selection ends; waits for it before it reads the pairs
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -2,6 +2,7 @@
 // front end (cskv_api.cu) and the kernel files.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -68,6 +69,31 @@ cudaError_t launch_sparse_prefill_attn(const void* q, const cskv_paged& kv, cons
                                        int ratio, int max_ctx, const float* sink, float softmax_scale,
                                        const float* q_rope, int T, int H, void* out, void* workspace,
                                        cudaStream_t stream);
+
+// Lets `kernel` use `bytes` of dynamic shared memory, asked of the driver once per device (a
+// request costs as much as a third of a launch); `again` asks in any case, after a launch that
+// failed (a device reset forgets it).
+inline cudaError_t allow_shared_memory(const void* kernel, std::atomic<uint64_t>& done, size_t bytes, bool again) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!again && (done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+// A launch of a kernel whose shared memory was allowed before (at most max_bytes of it).
+template <class Kernel, class... Args>
+inline cudaError_t launch_with_shared_memory(const cudaLaunchConfig_t& cfg, Kernel kernel, std::atomic<uint64_t>& done,
+                                             size_t max_bytes, const Args&... args) {
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel), done, max_bytes, false);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaErrorInvalidValue) return e;
+  cudaGetLastError();
+  e = allow_shared_memory(reinterpret_cast<const void*>(kernel), done, max_bytes, true);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // include/cskvx.h
 size_t window_attn_workspace_bytes(int T, int H, int max_ctx, int window, int first);

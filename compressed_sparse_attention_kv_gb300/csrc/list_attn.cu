@@ -130,6 +130,7 @@ struct Item {
   const uint8_t* ring;   // rings of all requests, for runs of ring slots
   int n_prefix;          // positions below it are looked up in request 0's row
   int r0, nr;            // rows [r0, r0 + nr) of the [T * H] rows
+  int t0, one;           // the first row's query; all rows are that query's
   int split, nsplit;     // this block takes the split-th of nsplit shares of the tiles
   int part;              // its partial output
 };
@@ -377,6 +378,8 @@ __device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
     it.split = it.part = x % a.prefix_split;
     it.r0 = x / a.prefix_split * kRows;
     it.nr = min(kRows, rows - it.r0);
+    it.t0 = it.r0 / a.H;
+    it.one = (it.r0 + it.nr - 1) / a.H == it.t0;
     return it;
   } else {
     x -= a.prefix_blocks * a.prefix_split;
@@ -386,12 +389,15 @@ __device__ __forceinline__ Item item_of(const ListArgs& a, int x) {
     it.part = (a.prefix_blocks > 0 ? a.prefix_split : 0) + it.split;
     x /= a.split;
   }
+  it.t0 = x * a.group;
+  it.one = a.group == 1;
   if (a.head_blocks == 1) {
-    it.r0 = x * a.group * a.H;
+    it.r0 = it.t0 * a.H;
     it.nr = min(a.group * a.H, rows - it.r0);
   } else {
-    const int h0 = x % a.head_blocks * a.heads_per_block;
-    it.r0 = x / a.head_blocks * a.H + h0;
+    const int q = x / a.head_blocks, h0 = (x - q * a.head_blocks) * a.heads_per_block;
+    it.t0 = q;
+    it.r0 = q * a.H + h0;
     it.nr = min(a.heads_per_block, a.H - h0);
   }
   return it;
@@ -410,7 +416,7 @@ __device__ __forceinline__ int entries_of(const ListArgs& a, int b) {
 __device__ void make_plan(const ListArgs& a, int x, Plan* pl) {
   const int lane = threadIdx.x & 31;
   const Item it = item_of(a, x);
-  const int t0 = it.r0 / a.H;
+  const int t0 = it.t0;
   int fmax = -1;
   unsigned fmin = 0xFFFFFFFFu;
 #pragma unroll
@@ -418,7 +424,7 @@ __device__ void make_plan(const ListArgs& a, int x, Plan* pl) {
     const int r = lane + 32 * u;
     RowSees s{0, 0, -1, -1};   // nothing
     if (r < it.nr) {
-      const int t = (it.r0 + r) / a.H;
+      const int t = it.one ? t0 : (it.r0 + r) / a.H;
       if (it.kind == kWindowRows) {
         int p1 = a.pos1[t];
         const int req = a.req_of ? a.req_of[t] : t;
@@ -454,7 +460,7 @@ __device__ void make_plan(const ListArgs& a, int x, Plan* pl) {
       }
     } else {
       // neighbouring queries of one request at neighbouring positions share a run
-      const int nq = (it.r0 + it.nr - 1) / a.H - t0 + 1;
+      const int nq = it.one ? 1 : (it.r0 + it.nr - 1) / a.H - t0 + 1;
       int q = 0;
       while (q < nq) {
         const RowSees first = pl->sees[q * a.H < it.nr ? q * a.H : 0];
@@ -487,7 +493,7 @@ __device__ void make_plan(const ListArgs& a, int x, Plan* pl) {
     for (int u = 0; u < 2; ++u) {
       const int r = lane + 32 * u;
       int run = -1;
-      const int q = (it.r0 + r) / a.H - t0;
+      const int q = it.one ? 0 : (it.r0 + r) / a.H - t0;
       for (int i = 0; i < pl->nruns; ++i)
         if (r < it.nr && q >= pl->runs[i].q0 && q < pl->runs[i].q1) run = i;
       pl->sees[r].run = run;
@@ -679,29 +685,38 @@ __device__ __forceinline__ void request_queries(const ListArgs& a, int r0, int n
   }
 }
 __device__ __forceinline__ void rotate_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
-  cp_async_wait_all();
-  work_sync();
+  static_assert(kRows * 8 <= kWorkThreads, "a thread per 8 dims of 64 rows, two passes for 128");
 #pragma unroll 1
-  for (int x = threadIdx.x; x < nq * 8; x += kWorkThreads) {
+  for (int x = threadIdx.x; x - static_cast<int>(threadIdx.x) < nq * 8; x += kWorkThreads) {
     const int r = x >> 3, c = x & 7;
-    uint4* hi = reinterpret_cast<uint4*>(qtile + 7 * (nq * 128) + sw128_offset(r, c));
-    uint4 v = *hi, lo = make_uint4(0u, 0u, 0u, 0u);
-    if (r < nr) {
-      const float* cs = a.q_rope + static_cast<size_t>((r0 + r) / a.H) * 64 + c * 8;
-      const float4 t0 = __ldg(reinterpret_cast<const float4*>(cs)), t1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
-      const float co[4] = {t0.x, t0.z, t1.x, t1.z}, si[4] = {t0.y, t0.w, t1.y, t1.w};
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-      uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
-        const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
-        w[k] = pack_bf16(z0, z1);
-        l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
-      }
-      *hi = v;
+    float4 t0 = make_float4(1.f, 0.f, 1.f, 0.f), t1 = t0;
+    if (r < nr) {   // on their way while the queries are awaited
+      const float* cs = a.q_rope + static_cast<size_t>(static_cast<unsigned>(r0 + r) / static_cast<unsigned>(a.H)) * 64 + c * 8;
+      t0 = __ldg(reinterpret_cast<const float4*>(cs));
+      t1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
     }
-    *reinterpret_cast<uint4*>(qtile + 8 * (nq * 128) + sw128_offset(r, c)) = lo;
+    if (x < kWorkThreads) {
+      cp_async_wait_all();
+      work_sync();
+    }
+    if (r < nq) {
+      uint4* hi = reinterpret_cast<uint4*>(qtile + 7 * (nq * 128) + sw128_offset(r, c));
+      uint4 v = *hi, lo = make_uint4(0u, 0u, 0u, 0u);
+      if (r < nr) {
+        const float co[4] = {t0.x, t0.z, t1.x, t1.z}, si[4] = {t0.y, t0.w, t1.y, t1.w};
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+        uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
+          const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
+          w[k] = pack_bf16(z0, z1);
+          l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
+        }
+        *hi = v;
+      }
+      *reinterpret_cast<uint4*>(qtile + 8 * (nq * 128) + sw128_offset(r, c)) = lo;
+    }
   }
   fence_proxy_async_smem();
 }
@@ -770,12 +785,9 @@ __device__ __noinline__ void clear_row(uint8_t* ktile, int key) {
     *reinterpret_cast<uint4*>(ktile + (x >> 3) * kChunk + sw128_offset(key, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// The softmax of the block's tile g (`first`: no tile of these rows before it): l accumulates the warp's keys' weights of row cb + lane / 2.  after_s() runs once the tile's
-// S product is complete.
-template <class AfterS>
+// The softmax of the block's tile g (`first`: no tile of these rows before it): l accumulates the warp's keys' weights of row cb + lane / 2.
 __device__ __forceinline__ bool weigh_tile(const ListArgs& a, const Plan* pl, ListSmem* sm, uint8_t* ktile,
-                                           uint8_t* ptile, uint32_t tmem, int g, bool first, float& l,
-                                           AfterS&& after_s) {
+                                           uint8_t* ptile, uint32_t tmem, int g, bool first, float& l) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarter = warp & 3, group = warp >> 2;
   const int cb = group * 16;        // this thread's rows (columns of S^T)
@@ -798,7 +810,6 @@ __device__ __forceinline__ bool weigh_tile(const ListArgs& a, const Plan* pl, Li
     tmem_ld16(tmem + kTmemS + tlane + cb, z);
     tmem_wait_ld();
   }
-  after_s();
   bool unfit = false;
   if (has && key < n && !(fabsf(z[0]) < INFINITY)) {
     unfit = unfit_row(ktile, key);
@@ -880,97 +891,106 @@ __device__ __forceinline__ bool weigh_tile(const ListArgs& a, const Plan* pl, Li
 }
 
 
-// The epilogue of a row block of nt tiles: the rows' sums, then O^T out.
-__device__ __forceinline__ void write_rows(const ListArgs& a, const Plan* pl, ListSmem* sm, uint32_t tmem, int nt,
-                                           float l) {
+// The epilogue of a row block, first part (while its last O product runs): the rows' sums, their
+// log-sum-exps, and the factors that their outputs take.
+__device__ __forceinline__ void finish_sums(const ListArgs& a, const Plan* pl, ListSmem* sm, float l) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quarter = warp & 3, group = warp >> 2;
+  const int quarter = warp & 3, cb = (warp >> 2) * 16;
   const Item& it = pl->item;
-  const int nq = pl->nq;
-  const int cb = group * 16;
-  const bool has = cb < nq;
-  const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
-    // ---- the rows' sums over the 128 keys
-    if (has && (lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = l;
-    work_sync();
-    if (tid < nq) {
+  const unsigned r = it.r0 + tid;
+  float sink = -INFINITY;
+  if (a.sink != nullptr && tid < it.nr) sink = __ldg(a.sink + r % static_cast<unsigned>(a.H));
+  if (cb < pl->nq && (lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = l;
+  work_sync();
+  if (tid < kRows) {
+    float f = 0.f;
+    if (tid < it.nr) {
       const float sum = ((sm->part[0][tid] + sm->part[1][tid]) + sm->part[2][tid]) + sm->part[3][tid];
       const float m = sm->m[tid] == -INFINITY ? -INFINITY : sm->msub[tid];
-      float f = 0.f;
-      if (tid < it.nr) {
-        const size_t row = static_cast<size_t>(it.r0) + tid;
-        if (a.parts > 1) {
-          *reinterpret_cast<float2*>(a.ml + (row * a.parts + it.part) * 2) = make_float2(m, sum);
-          f = 1.f;
-        } else {
-          const float sink = a.sink ? a.sink[row % a.H] : -INFINITY;
-          const float s2 = sink * kLog2e;
-          const float M = fmaxf(m, s2);
-          const float e = exp2f(m - M);
-          const float total = sum * e + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));
-          const bool none = sum == 0.f;   // no key: out 0, lse the sink itself
-          f = none ? 0.f : e / total;
-          if (sum != sum) f = sum;
-          if (a.lse != nullptr) a.lse[row] = none ? sink : sum != sum ? sum : (M + log2f(total)) * kLn2;
-        }
-      }
-      sm->fac[tid] = f;
-    }
-    if (tid < kRows) {   // for the next rows
-      sm->m[tid] = sm->limit[tid] = -INFINITY;
-      sm->msub[tid] = 0.f;
-    }
-    work_sync();
-    // ---- O^T out: a thread has dim d of 16 rows at a time
-    const int d = group * 128 + quarter * 32 + lane;
-    const bool turn = group == 3 && quarter >= 2;   // dims 448..511, turned back
-    const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
-    const int t0 = it.r0 / a.H;
-    const bool one = (it.r0 + it.nr - 1) / a.H == t0;   // the rows of one query
-    float2 w = make_float2(1.f, 0.f);
-    if (turn && one && a.parts == 1) w = __ldg(cs + static_cast<size_t>(t0) * 32);
-#pragma unroll 1
-    for (int g = 0; g < it.nr; g += 16) {
-      float o[16];
-      if (nt > 0) {
-        tmem_ld16(tmem + tlane + group * kRows + g, o);
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] = 0.f;
-      }
       if (a.parts > 1) {
-        float* to = a.opart + ((static_cast<size_t>(it.r0) + g) * a.parts + it.part) * kD + d;
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (g + c < it.nr) to[static_cast<size_t>(c) * a.parts * kD] = o[c];
-        continue;
+        *reinterpret_cast<float2*>(a.ml + (static_cast<size_t>(r) * a.parts + it.part) * 2) = make_float2(m, sum);
+        f = 1.f;
+      } else {
+        const float s2 = sink * kLog2e;
+        const float M = fmaxf(m, s2);
+        const float e = exp2f(m - M);
+        const float total = sum * e + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));
+        const bool none = sum == 0.f;   // no key: out 0, lse the sink itself
+        f = none ? 0.f : e / total;
+        if (sum != sum) f = sum;
+        if (a.lse != nullptr) a.lse[r] = none ? sink : sum != sum ? sum : (M + log2f(total)) * kLn2;
       }
+    }
+    sm->fac[tid] = f;
+    sm->m[tid] = sm->limit[tid] = -INFINITY;   // for the next rows
+    sm->msub[tid] = 0.f;
+  }
+  work_sync();
+}
+
+// Second part: O^T out.  A thread has dim d of 16 rows at a time (the next tile's bytes hold most registers); each row's 32 dims of a warp are
+// one 64-byte run.
+__device__ __forceinline__ void write_rows(const ListArgs& a, const Plan* pl, ListSmem* sm, uint32_t tmem, int nt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, group = warp >> 2;
+  const int r0 = pl->item.r0, nr = pl->item.nr;
+  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * kRows;
+  const int d = group * 128 + quarter * 32 + lane;
+  const bool turn = group == 3 && quarter >= 2 && a.parts == 1;   // dims 448..511, turned back
+  const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
+  const unsigned H = a.H, t0 = r0 / H;
+  const bool one = pl->item.one;   // the rows of one query
+  float2 w = make_float2(1.f, 0.f);
+  if (turn && one) w = __ldg(cs + static_cast<size_t>(t0) * 32);
+#pragma unroll 1
+  for (int g = 0; g < nr; g += 16) {
+    float o[16];
+    if (nt > 0) {
+      tmem_ld16(from + g, o);   // (columns behind the last row hold nothing of use)
+      tmem_wait_ld();
+    } else {
 #pragma unroll
-      for (int c = 0; c < 16; c += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&sm->fac[g + c]);
-        o[c] *= f.x;
-        o[c + 1] *= f.y;
-        o[c + 2] *= f.z;
-        o[c + 3] *= f.w;
-      }
-      if (turn) {
+      for (int c = 0; c < 16; ++c) o[c] = 0.f;
+    }
+    if (a.parts > 1) {
+      float* to = a.opart + ((static_cast<size_t>(r0) + g) * a.parts + pl->item.part) * kD + d;
+      const size_t step = static_cast<size_t>(a.parts) * kD;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          if (!one) w = __ldg(cs + static_cast<size_t>((it.r0 + min(g + c, it.nr - 1)) / a.H) * 32);
-          const float y = __shfl_xor_sync(0xFFFFFFFFu, o[c], 1);
-          o[c] = (lane & 1) ? o[c] * w.x - y * w.y : o[c] * w.x + y * w.y;
-        }
-      }
-      // even lanes store dims d, d + 1 of row c, odd lanes dims d - 1, d of row c + 1
-      uint8_t* to = a.out + ((static_cast<size_t>(it.r0) + g + (lane & 1)) * kD + (d & ~1)) * 2;
+      for (int c = 0; c < 16; ++c)
+        if (g + c < nr) to[c * step] = o[c];
+      continue;
+    }
+#pragma unroll
+    for (int c = 0; c < 16; c += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&sm->fac[g + c]);   // 0 behind the last row
+      o[c] *= f.x;
+      o[c + 1] *= f.y;
+      o[c + 2] *= f.z;
+      o[c + 3] *= f.w;
+    }
+    if (turn) {
+      // even lanes turn and store the pair of dims (d, d + 1) of row c, odd lanes (d - 1, d) of row c + 1
+      const bool odd = (lane & 1) != 0;
 #pragma unroll
       for (int c = 0; c < 16; c += 2) {
-        const float other = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? o[c] : o[c + 1], 1);
-        const uint32_t v = (lane & 1) ? pack_bf16(other, o[c + 1]) : pack_bf16(o[c], other);
-        if (g + c + (lane & 1) < it.nr) *reinterpret_cast<uint32_t*>(to + c * (kD * 2)) = v;
+        const int r = g + c + (odd ? 1 : 0);
+        if (!one) w = __ldg(cs + static_cast<size_t>((r0 + min(r, nr - 1)) / H) * 32);
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[c] : o[c + 1], 1);
+        const float y0 = odd ? other : o[c], y1 = odd ? o[c + 1] : other;
+        const uint32_t v = pack_bf16(y0 * w.x + y1 * w.y, y1 * w.x - y0 * w.y);
+        if (r < nr)
+          *reinterpret_cast<uint32_t*>(a.out + ((static_cast<size_t>(r0) + r) * kD + (d & ~1)) * 2) = v;
       }
+      continue;
     }
+    uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + (static_cast<size_t>(r0) + g) * kD + d;
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      const uint32_t v = pack_bf16(o[c], o[c + 1]);
+      if (g + c < nr) to[c * kD] = static_cast<uint16_t>(v);
+      if (g + c + 1 < nr) to[(c + 1) * kD] = static_cast<uint16_t>(v >> 16);
+    }
+  }
 }
 
 // One kernel per row format: a call whose rings have another format than its cache launches two
@@ -1011,6 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
     sm->msub[tid] = 0.f;
   }
   if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 512);
+  if (warp == kWorkWarps + 1) make_plan(a, blockIdx.x, &sm->plan[0]);
   if (warp < kWorkWarps) {
     const Item it = item_of(a, blockIdx.x);
     request_queries(a, it.r0, it.nr, (it.nr + 15) & ~15, qtile);
@@ -1027,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
       if (e >= 2) ok = wait_warp(sm, &sm->plan_free[e & 1], ((e >> 1) - 1) & 1, a.spin);
       if (!ok) break;
       Plan* pl = &sm->plan[e & 1];
-      make_plan(a, blockIdx.x + e * gridDim.x, pl);
+      if (e > 0) make_plan(a, blockIdx.x + e * gridDim.x, pl);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->plan_full[e & 1]);
       TileWalk walk(pl);
@@ -1109,11 +1130,11 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
         const Plan* np = !last ? pl : e + 1 < items ? plan_of(e + 1) : nullptr;
         requested = np != nullptr && (!last || np->nt > 0);
         if (requested) ok = rows.request(g + 1, a.spin) && ok;
-        ok = weigh_tile(a, pl, sm, ktile, ptile, tmem, g, i == 0, l, [&]() {
-          // the last product on these queries is complete: the next ones may come
-          if (last && np != nullptr) request_queries(a, np->item.r0, np->item.nr, np->nq, qtile);
-        }) && ok;
+        ok = weigh_tile(a, pl, sm, ktile, ptile, tmem, g, i == 0, l) && ok;
+        // the last S product on these queries is complete: the next ones may come
+        if (last && np != nullptr) request_queries(a, np->item.r0, np->item.nr, np->nq, qtile);
       }
+      finish_sums(a, pl, sm, l);
       if (nt > 0 && ok) wait_bar(sm, &sm->free_[3], (g - 1) & 1, a.spin);
       if (nt == 0 && e + 1 < items) {
         const Plan* np = plan_of(e + 1);
@@ -1122,7 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
       }
       __syncwarp();
       tc_fence_after();
-      write_rows(a, pl, sm, tmem, nt, l);
+      write_rows(a, pl, sm, tmem, nt);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->plan_free[e & 1]);
     }
@@ -1456,8 +1477,9 @@ struct Schedule {
   }
 };
 
-// the join's launch, and writing and reading partial outputs: 4 KB a row and part
-double join_cost(double rows, int parts) { return parts <= 1 ? 0.0 : 0.8 + rows * parts * 4096.0 / 15e6; }
+// The join's launch (on the host too: two tiles of one row block in two blocks and a join took
+// 26 us a call, in one block 20 us), and writing and reading partial outputs: 4 KB a row and part.
+double join_cost(double rows, int parts) { return parts <= 1 ? 0.0 : 2.0 + rows * parts * 4096.0 / 15e6; }
 
 int shares(int tiles, int len) { return len > 0 ? (tiles + len - 1) / len : 0; }
 
@@ -1565,11 +1587,10 @@ ListArgs common_args(const void* q, const cskv_paged& kv, const float* sink, flo
 // One launch of list_attn_kernel for rows of format fmt; `beside`: it may start while the
 // launch before it runs.
 cudaError_t launch_kind(const ListArgs& a, int fmt, unsigned grid, bool beside, cudaStream_t stream) {
+  static std::atomic<uint64_t> allowed[3];
   auto kernel = fmt == CSKV_FMT_FP8_E4M3_E8M0_B32 ? list_attn_kernel<CSKV_FMT_FP8_E4M3_E8M0_B32>
                 : fmt == CSKV_FMT_FP4_E2M1_E4M3_B16 ? list_attn_kernel<CSKV_FMT_FP4_E2M1_E4M3_B16>
                                                     : list_attn_kernel<CSKV_FMT_BF16>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kAttnSmem));
-  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1580,7 +1601,8 @@ cudaError_t launch_kind(const ListArgs& a, int fmt, unsigned grid, bool beside, 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = beside ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  static_assert(CSKV_FMT_BF16 == 0 && CSKV_FMT_FP8_E4M3_E8M0_B32 == 1 && CSKV_FMT_FP4_E2M1_E4M3_B16 == 2, "an index");
+  return launch_with_shared_memory(cfg, kernel, allowed[fmt], kAttnSmem, a);
 }
 
 cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStream_t stream) {
@@ -1706,11 +1728,15 @@ cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32
     grid = static_cast<unsigned>(B) * a.split;
   }
   const size_t smem = weights_smem(H);
-  auto kernel = weight_slots(H) == 8 ? weights_kernel<8> : weights_kernel<4>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  static std::atomic<uint64_t> allowed[2];
+  const bool wide = weight_slots(H) == 4;
+  auto kernel = wide ? weights_kernel<4> : weights_kernel<8>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  return launch_with_shared_memory(cfg, kernel, allowed[wide], weights_smem(wide ? 128 : kRows), a);
 }
 
 unsigned int take_err_list_attn() { return take_dev_err(); }
