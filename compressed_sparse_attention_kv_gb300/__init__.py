@@ -591,10 +591,16 @@ def _table(name, t, dtype, rows, least, device):
     """(address, columns) of a [rows, at least `least`] table (None: (None, 0))."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < least:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < least:
         _need(t, dtype, name)
-        raise ValueError("%s must have shape (%d, at least %d), got %s" % (name, rows, least, tuple(t.shape)))
-    return _take(name, t, dtype, t.shape, device), t.shape[1]
+        raise ValueError("%s must have shape (%d, at least %d), got %s" % (name, rows, least, tuple(shape)))
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, device)
+    return t.data_ptr(), shape[1]
+
+
+_PAGED_ARRAYS = [_lib.Paged * max(1, n) for n in range(5)]
 
 
 def evict_workspace_size(B, max_entries, budget):
@@ -627,7 +633,8 @@ def evict(caches, acc, n_entries, budget, fixed=0, recent=0, age=None, max_entri
     ph, wh = _table("age_out", age_out, i32, B, kept, dev)
     pn = _take("n_entries", n_entries, i32, (B,), dev)
     pm = _take("n_out", n_out, i32, (B,), dev)
-    arr = (_lib.Paged * max(1, len(caches)))(*[_cache_on("a cache", c, B, dev) for c in caches])
+    arr = _PAGED_ARRAYS[len(caches)] if len(caches) < 5 else _lib.Paged * len(caches)
+    arr = arr(*[_cache_on("a cache", c, B, dev) for c in caches])
     if src is None:
         src = torch.empty((B, max(budget, 0)), dtype=i32, device=dev)
     px = _take("src", src, i32, (B, max(budget, 0)), dev)

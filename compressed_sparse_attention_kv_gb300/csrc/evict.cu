@@ -108,6 +108,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   __shared__ SelSmem sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
+  auto sync_all = [&]() {   // a cluster of one block needs its block's barrier only
+    if (blocks == 1) __syncthreads();
+    else cluster.sync();
+  };
   const int b = blockIdx.x / blocks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int n = a.n_entries[b];
   if (n < 0 || n > a.max_entries) {
@@ -136,10 +140,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       for (int i = slice0 + tid; i < slice1; i += kSelThreads) mx = max(mx, age[i]);
       mx = __reduce_max_sync(0xFFFFFFFFu, mx);
       if (lane == 0) atomicMax(&sm.newest, mx);
-      cluster.sync();
+      sync_all();
       mx = INT32_MIN;
       for (int r = 0; r < blocks; ++r) mx = max(mx, *cluster.map_shared_rank(&sm.newest, r));
-      cluster.sync();
+      sync_all();
       if (tid == 0) sm.newest = mx;
       __syncthreads();
     }
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         const uint32_t k = key_of(i);
         if ((k & mask) == prefix) atomicAdd(&sm.hist[(k >> shift) & (bins - 1)], 1);
       }
-      cluster.sync();
+      sync_all();
       // this thread's two bins (from the top), over all blocks
       int c[2] = {0, 0};
 #pragma unroll
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         sm.digit = bins - 1 - (2 * tid + (second ? 1 : 0));
         sm.need = need - above - (second ? c[0] : 0);
       }
-      cluster.sync();   // the decision, and every block is done with the histograms
+      sync_all();   // the decision, and every block is done with the histograms
       prefix |= static_cast<uint32_t>(sm.digit) << shift;
       mask |= static_cast<uint32_t>(bins - 1) << shift;
       need = sm.need;
@@ -210,11 +214,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       const int t = __reduce_add_sync(0xFFFFFFFFu, x);
       if (lane == 0) sm.total_a = t;
     }
-    cluster.sync();
+    sync_all();
     int ties = 0;   // equal keys before this warp's stretch
     for (int r = 0; r < rank; ++r) ties += *cluster.map_shared_rank(&sm.total_a, r);
     ties += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sm.warp_a[lane] : 0);
-    cluster.sync();
+    sync_all();
     // ---- holes and movers of this warp's stretch
     auto walk = [&](auto&& visit) {
       int t = ties;
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         sm.total_b = y;
       }
     }
-    cluster.sync();
+    sync_all();
     int h0 = 0, v0 = 0;
     for (int r = 0; r < blocks; ++r) {
       const int x = *cluster.map_shared_rank(&sm.total_a, r);
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       v0 += __popc(v);
     });
     __threadfence();
-    cluster.sync();   // the lists are complete, and no block reads another's shared memory any more
+    sync_all();   // the lists are complete, and no block reads another's shared memory any more
     for (int i = rank * kSelThreads + tid; i < pairs; i += blocks * kSelThreads) src[hole[i]] = mover[i];
   } else {
     for (int i = rank * kSelThreads + tid; i < a.budget; i += blocks * kSelThreads) {
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     for (int i = rank * kSelWarps + warp; i < pairs; i += blocks * kSelWarps) move_pair(a, b, hole[i], mover[i], lane);
   }
   if (a.n_out == a.n_entries) {   // every block has read n_entries
-    cluster.sync();
+    sync_all();
     if (rank == 0 && tid == 0) a.n_out[b] = m;
   }
 }
