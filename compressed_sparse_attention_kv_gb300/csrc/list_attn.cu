@@ -533,7 +533,9 @@ struct RowLoader {
   typename Raw<FMT>::Codes raw[2][4];
   typename Raw<FMT>::Scales scales;   // of row row0 + lane
   int block, row0, lane, group;       // group: of 16 dims
-  int keys;                           // of the tile requested
+  // of the tile requested; -1 for good after a wait that gave up (a later wait might pass by its
+  // parity, before there are addresses)
+  int keys = 0;
 
   __device__ __forceinline__ RowLoader(ListSmem* s, uint8_t* slots) : sm(s) {
     const int warp = threadIdx.x >> 5;
@@ -585,8 +587,8 @@ struct RowLoader {
   }
   // requests the bytes of the block's tile g, whose addresses have been looked up
   __device__ __forceinline__ bool request(int g, unsigned long long spin) {
-    const bool ok = wait_warp(sm, &sm->rows_full[g & 1], (g >> 1) & 1, spin);
-    keys = ok ? sm->info[g & 1].n : 0;
+    const bool ok = keys >= 0 && wait_warp(sm, &sm->rows_full[g & 1], (g >> 1) & 1, spin);
+    keys = ok ? sm->info[g & 1].n : -1;
     if (row0 >= keys) return ok;   // none of this warp's rows
     const uint8_t* x = reinterpret_cast<const uint8_t*>(sm->rowp[g & 1][row0 + lane]);
     if constexpr (FMT == CSKV_FMT_FP8_E4M3_E8M0_B32) scales = __ldg(reinterpret_cast<const uint32_t*>(x + kD) + block);
@@ -1024,6 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
       mbar_init(&sm->rows_free[i], kWorkWarps);
     }
     sm->abort = 0;
+    sm->info[0] = sm->info[1] = TileInfo{0, 0, 0, 0};   // (what a wait that gave up leaves is never wild)
     fence_mbar_init();
   }
   if (tid < kRows) {
@@ -1080,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
             }
             if (ok) issue_s_chunk(tmem + kTmemS, dk + c * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
           }
-          const int ks = (sm->info[g & 1].n + 15) >> 4;   // (the tile's, until its weights are there)
+          const int ks = (min(sm->info[g & 1].n, kKeys) + 15) >> 4;   // (the tile's, until its weights are there)
           mma_commit(&sm->bar_s[0]);
           mbar_arrive(&sm->bar_s[0]);   // hands on what the loading warps wrote (none)
           ok = ok && wait_bar(sm, &sm->bar_p[0], g & 1, a.spin);

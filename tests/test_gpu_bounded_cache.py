@@ -617,3 +617,151 @@ def test_wrong_shapes_are_refused():
         cskv.evict([], acc, i, 50)
     with pytest.raises(cskv.CskvError):
         cskv.window_attn(q, dev, i, 0, 0, 100, None, SCALE, cs)
+
+
+@pytest.mark.parametrize("limit", [1, 2000, 20000])
+def test_waits_that_run_out_end_their_kernels(limit):
+    """With a limit far below a tile's time the kernels give up, report it and return; after it the
+    same calls are exact."""
+    pos1 = [3000, 2000, 1500]
+    cache = _cache(FP8, pos1, seed=740)
+    q = _queries(3, 16, 741)
+    c = _prefix_case(3, 16, 500, [900, 800, 700], FP8, FP8, seed=742)
+    prompt = _queries(600, 16, 743)
+    long = _cache(FP8, [600], seed=744)
+    lse = torch.zeros((3, 16), device="cuda")
+    acc = torch.zeros((3, 900), device="cuda")
+    good = [x.clone() for x in _window(cache, q, pos1, 2000, 4, None, None)]
+    assert cskv.device_status() == 0
+    cskv.set_spin_limit(limit)
+    try:
+        _window(cache, q, pos1, 2000, 4, None, None)
+        _window(long, prompt, np.arange(1, 601), 128, 4, np.zeros(600, np.int64), None)
+        _prefix_run(c)
+        cskv.attn_weights(c["q"][0].cuda(), c["cache"].to_device(), _i32(c["n"]), 900, SCALE, _cs(c["ctx"]), lse, acc)
+        assert cskv.device_status() in ((4,) if limit == 1 else (0, 4))
+    finally:
+        cskv.set_spin_limit(0)
+    again = _window(cache, q, pos1, 2000, 4, None, None)
+    assert cskv.device_status() == 0
+    assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
+    _prefix_all(c, *_prefix_run(c))
+
+
+def test_caches_beyond_four_gigabytes():
+    """Pages at the end of a pool of more than 2^32 bytes."""
+    page = 64 * 1024
+    pages = (1 << 32) // page + 40
+    pool = torch.zeros((pages, page), dtype=torch.uint8, device="cuda")
+    L = 700
+    small = _cache(BF16, [L], seed=750)
+    per = small.max_pages
+    bt = np.arange(pages - per, pages, dtype=np.int32)[None]
+    for p in range(per):
+        pool[int(bt[0, p])] = cuda(small.pool[small.block_table[0, p]])
+    big = cskv.PagedCache(pool, cuda(bt), BF16, 512)
+    q = _queries(1, 16, 751)
+    args = (_i32([L]), 600, 4, L, None, SCALE, _cs([L]))
+    a, la = cskv.window_attn(q[0].cuda(), big, *args, want_lse=True)
+    b, lb = cskv.window_attn(q[0].cuda(), small.to_device(), *args, want_lse=True)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    acc = torch.rand((1, L), device="cuda")
+    before = pool[int(bt[0, 0]):].clone()
+    src, n, _, _ = cskv.evict([big], acc, _i32([L]), 300)
+    src = src[0].long()
+    rows = before.view(-1, 1024)
+    assert torch.equal(pool[int(bt[0, 0]):].view(-1, 1024)[:300], rows[src])
+    assert cskv.device_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """The same operators at the same time on two streams, each with its own workspace."""
+    c = [_prefix_case(4, 32, 1000, [1500, 1400, 1300, 1200], FP8, FP8, seed=760 + k) for k in range(2)]
+    want = [_prefix_run(x) for x in c]
+    torch.cuda.synchronize()
+    args = []
+    for x in c:
+        args.append(((x["q"][0].cuda(), x["cache"].to_device(), _i32(x["n"]), x["P"], 1500, cuda(x["sink"]), SCALE,
+                      _cs(x["ctx"])), dict(swa=cuda(x["ring"][0]), swa_fmt=FP8, ctx_len=_i32(x["ctx"]), want_lse=True)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for k in range(2):
+            got[k].append(cskv.prefix_decode_attn(*args[k][0], stream=streams[k], **args[k][1]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for out, lse in got[k]:
+            assert torch.equal(out, want[k][0]) and torch.equal(lse, want[k][1])
+    assert cskv.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", [FP8, FP4])
+def test_every_code_and_scale_is_read_exactly(fmt):
+    """A query that sees one row gives that row back: every code under many scales, bit for bit
+    (bf16 holds every such value except where the largest scales overflow it)."""
+    rb = codecs.row_bytes(fmt, 512)
+    if fmt == FP8:
+        codes = np.concatenate([np.arange(256), np.arange(256)]).astype(np.uint8)
+        codes[(codes & 0x7F) == 0x7F] = 0x40
+        scales = [0, 1, 7, 100, 119, 127, 134, 135, 140, 200, 245]
+        rows = np.stack([np.concatenate([codes, np.full(16, s, np.uint8)]) for s in scales])
+    else:
+        packed = np.tile(np.arange(256).astype(np.uint8), 1)
+        scales = [s for s in range(256) if (s & 0x7F) != 0x7F][::5]
+        rows = np.stack([np.concatenate([packed, np.full(32, s, np.uint8)]) for s in scales])
+    n = len(rows)
+    cache = HostPaged(fmt, 512, [1] * n, seed=770)
+    for b in range(n):
+        cache.pool[cache.block_table[b, 0], :rb] = rows[b]
+    want = codecs.decode_rows(rows, fmt, 512)
+    cs = torch.zeros((n, 32, 2), device="cuda")
+    cs[..., 0] = 1.0
+    out, _ = cskv.window_attn(torch.zeros((n, 1, 512), dtype=torch.bfloat16, device="cuda"), cache.to_device(),
+                              _i32([1] * n), 4, 0, 1, None, SCALE, cs)
+    assert cskv.device_status() == 0
+    assert np.array_equal(out[:, 0].float().cpu().numpy().astype(np.float64),
+                          torch.from_numpy(want).to(torch.bfloat16).double().numpy())
+
+
+def test_evict_with_one_table_in_place_and_one_apart():
+    e = _evict_case(2, 500, [500, 300], [(FP8, 512)], seed=780)
+    dev = [c.to_device() for c in e["caches"]]
+    acc, age, n = cuda(e["acc"]), cuda(e["age"]), _i32(e["n"])
+    age_out = torch.full((2, 400), -5, dtype=torch.int32, device="cuda")
+    src, n_out, acc_out, _ = cskv.evict(dev, acc, n, 400, fixed=3, recent=40, age=age, age_out=age_out)
+    assert acc_out is acc and n_out is n and cskv.device_status() == 0
+    for b in range(2):
+        ref, m = bounded.evict(e["acc"][b], e["age"][b], int(e["n"][b]), 400, 3, 40)
+        assert np.array_equal(src[b].cpu().numpy(), ref) and int(n_out[b]) == m
+        assert np.array_equal(acc_out[b, :m].cpu().numpy(), e["acc"][b][ref[:m]])
+        assert np.array_equal(acc_out[b, m:].cpu().numpy(), e["acc"][b][m:])
+        assert np.array_equal(age_out[b, :m].cpu().numpy(), e["age"][b][ref[:m]])
+        assert (age_out[b, m:] == -5).all()
+        assert np.array_equal(age[b].cpu().numpy(), e["age"][b])
+
+
+def test_weights_of_many_requests():
+    """More requests than share their tiles evenly (a block per request), some empty."""
+    B, H = 70, 8
+    n = [(37 * b) % 300 for b in range(B)]
+    c = _prefix_case(B, H, 0, n, BF16, None, seed=790)
+    lse = torch.full((B, H), 5.0, device="cuda")
+    acc = torch.zeros((B, 300), device="cuda")
+    cskv.attn_weights(c["q"][0].cuda(), c["cache"].to_device(), _i32(n), 300, SCALE, _cs(c["ctx"]), lse, acc)
+    assert cskv.device_status() == 0
+    got = acc.cpu().numpy()
+    for b in range(B):
+        w, bound = bounded.weights(c["q"][1][b], int(c["ctx"][b]) - 1, c["cache"].decoded[b][:n[b]], np.full(H, 5.0), SCALE)
+        assert np.all(np.abs(got[b, :n[b]] - w) <= bound + 2.0 ** -24 * np.abs(w)) and not got[b, n[b]:].any()
+
+
+def test_window_many_heads_of_one_query_group():
+    """One head: 32 queries to a row block, several runs in it; and a prompt whose last block is short."""
+    L = [97, 3, 200]
+    cache = _cache(FP8, L, seed=800)
+    req = np.repeat(np.arange(3), L)
+    pos1 = np.concatenate([np.arange(1, n + 1) for n in L])
+    for H in (1, 2, 63):
+        _window_all(cache, _queries(len(req), H, 801), pos1, 33, 2, req, None,
+                    pick=list(range(0, len(req), 7)) + [96, 97, 99, 100, len(req) - 1])
