@@ -180,7 +180,7 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
       : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool wait_on(ListSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
+__device__ __forceinline__ bool wait_on(ListSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
   const unsigned long long t0 = clock64();
   while (!try_wait_long(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&sm->abort)) return false;
@@ -222,22 +222,25 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Transposing butterfly: lanes 2c and 2c + 1 end with op over the warp's lanes of their v[c]
-// (v is spent).
-template <class Op>
-__device__ __forceinline__ float reduce_columns(float (&v)[16], Op op) {
+// Transposing butterfly: of N columns, lanes (32 / N) c to (32 / N) (c + 1) - 1 end with op over the
+// warp's lanes of their v[c] (v is spent).
+template <int N, class Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[N], Op op) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int w = 8; w >= 1; w >>= 1) {
-    const bool hi = (lane & (2 * w)) != 0;
+  for (int w = N / 2; w >= 1; w >>= 1) {
+    const int bit = w * (32 / N);
+    const bool hi = (lane & bit) != 0;
 #pragma unroll
     for (int j = 0; j < w; ++j) {
       const float send = hi ? v[j] : v[j + w];
       const float keep = hi ? v[j + w] : v[j];
-      v[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, 2 * w));
+      v[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, bit));
     }
   }
-  return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
+#pragma unroll
+  for (int bit = 16 / N; bit >= 1; bit >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], bit));
+  return v[0];
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
@@ -246,6 +249,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // The issuing lane's MMAs are unrolled with constant descriptor offsets and constant
@@ -267,11 +276,6 @@ __device__ __forceinline__ void mma_set(uint32_t d, uint64_t da, uint64_t db, ui
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(da), "l"(db), "r"(id)
       : "memory");
-}
-// `count` (16 or 32) columns into v[0..count)
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, int count, float (&v)[32]) {
-  if (count > 16) tmem_ld32(taddr, v);
-  else tmem_ld16(taddr, *reinterpret_cast<float(*)[16]>(v));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -772,8 +776,9 @@ __device__ __forceinline__ uint32_t seen_by(const Plan* pl, int run, int k0, int
 // A key row with a value that is not finite makes every logit of its key not finite, so one
 // column is looked at, and only then the row.  Such a row leaves the tile (zeros, for the O
 // product) and the key's logits become NaN.
-__device__ __noinline__ bool unfit_row(const uint8_t* ktile, int key) {
+__device__ __forceinline__ bool unfit_row(const uint8_t* ktile, int key) {
   uint32_t bad = 0;
+#pragma unroll 1
   for (int x = 0; x < 64; ++x) {
     const uint4 v = *reinterpret_cast<const uint4*>(ktile + (x >> 3) * kChunk + sw128_offset(key, x & 7));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -782,7 +787,8 @@ __device__ __noinline__ bool unfit_row(const uint8_t* ktile, int key) {
   }
   return bad != 0u;
 }
-__device__ __noinline__ void clear_row(uint8_t* ktile, int key) {
+__device__ __forceinline__ void clear_row(uint8_t* ktile, int key) {
+#pragma unroll 1
   for (int x = 0; x < 64; ++x)
     *reinterpret_cast<uint4*>(ktile + (x >> 3) * kChunk + sw128_offset(key, x & 7)) = make_uint4(0u, 0u, 0u, 0u);
 }
@@ -837,11 +843,14 @@ __device__ __forceinline__ bool weigh_tile(const ListArgs& a, const Plan* pl, Li
   if (unfit && group == 0) clear_row(ktile, key);   // every group has looked at it
   if (moves) {   // some row's reference moves: the tile's maxima, exactly
     if (has) {
-      float t[16];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) t[c] = z[c];
-      const float mine = reduce_columns(t, [](float x, float y) { return fmaxf(x, y); });
-      if ((lane & 1) == 0) sm->part[quarter][cb + (lane >> 1)] = mine;
+      for (int h = 0; h < 16; h += 8) {   // (in halves: registers)
+        float t[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) t[c] = z[h + c];
+        const float mine = reduce_columns(t, [](float x, float y) { return fmaxf(x, y); });
+        if ((lane & 3) == 0) sm->part[quarter][cb + h + (lane >> 2)] = mine;
+      }
     }
     work_sync();
     if (tid < nq) {
@@ -930,40 +939,44 @@ __device__ __forceinline__ void finish_sums(const ListArgs& a, const Plan* pl, L
   work_sync();
 }
 
-// Second part: O^T out.  A thread has dim d of 16 rows at a time (the next tile's bytes hold most registers); each row's 32 dims of a warp are
-// one 64-byte run.
+// Second part: O^T out, in units of 8 rows of a block of 128 dims (the next tile's bytes hold
+// most registers); a thread has one dim of them,
+// a row's 32 dims of a warp are one 64-byte run.  With 64 rows a warp has 16 rows of every
+// block, so that the turned dims (twice the instructions) are spread over eight warps.
 __device__ __forceinline__ void write_rows(const ListArgs& a, const Plan* pl, ListSmem* sm, uint32_t tmem, int nt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, group = warp >> 2;
+  const int quarter = warp & 3;
   const int r0 = pl->item.r0, nr = pl->item.nr;
-  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * kRows;
-  const int d = group * 128 + quarter * 32 + lane;
-  const bool turn = group == 3 && quarter >= 2 && a.parts == 1;   // dims 448..511, turned back
-  const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
+  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const unsigned H = a.H, t0 = r0 / H;
   const bool one = pl->item.one;   // the rows of one query
-  float2 w = make_float2(1.f, 0.f);
-  if (turn && one) w = __ldg(cs + static_cast<size_t>(t0) * 32);
+  const int sets = (nr + 7) >> 3;
 #pragma unroll 1
-  for (int g = 0; g < nr; g += 16) {
-    float o[16];
+  for (int x = warp >> 2; x < 4 * sets; x += 4) {
+    const int block = x / sets, g = (x - block * sets) * 8;
+    const int d = block * 128 + quarter * 32 + lane;
+    const bool turn = block == 3 && quarter >= 2 && a.parts == 1;   // dims 448..511, turned back
+    const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
+    float2 w = make_float2(1.f, 0.f);
+    if (turn && one) w = __ldg(cs + static_cast<size_t>(t0) * 32);
+    float o[8];
     if (nt > 0) {
-      tmem_ld16(from + g, o);   // (columns behind the last row hold nothing of use)
+      tmem_ld8(from + block * kRows + g, o);   // (columns behind the last row hold nothing of use)
       tmem_wait_ld();
     } else {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) o[c] = 0.f;
+      for (int c = 0; c < 8; ++c) o[c] = 0.f;
     }
     if (a.parts > 1) {
       float* to = a.opart + ((static_cast<size_t>(r0) + g) * a.parts + pl->item.part) * kD + d;
       const size_t step = static_cast<size_t>(a.parts) * kD;
 #pragma unroll
-      for (int c = 0; c < 16; ++c)
+      for (int c = 0; c < 8; ++c)
         if (g + c < nr) to[c * step] = o[c];
       continue;
     }
 #pragma unroll
-    for (int c = 0; c < 16; c += 4) {
+    for (int c = 0; c < 8; c += 4) {
       const float4 f = *reinterpret_cast<const float4*>(&sm->fac[g + c]);   // 0 behind the last row
       o[c] *= f.x;
       o[c + 1] *= f.y;
@@ -974,7 +987,7 @@ __device__ __forceinline__ void write_rows(const ListArgs& a, const Plan* pl, Li
       // even lanes turn and store the pair of dims (d, d + 1) of row c, odd lanes (d - 1, d) of row c + 1
       const bool odd = (lane & 1) != 0;
 #pragma unroll
-      for (int c = 0; c < 16; c += 2) {
+      for (int c = 0; c < 8; c += 2) {
         const int r = g + c + (odd ? 1 : 0);
         if (!one) w = __ldg(cs + static_cast<size_t>((r0 + min(r, nr - 1)) / H) * 32);
         const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[c] : o[c + 1], 1);
@@ -987,7 +1000,7 @@ __device__ __forceinline__ void write_rows(const ListArgs& a, const Plan* pl, Li
     }
     uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + (static_cast<size_t>(r0) + g) * kD + d;
 #pragma unroll
-    for (int c = 0; c < 16; c += 2) {
+    for (int c = 0; c < 8; c += 2) {
       const uint32_t v = pack_bf16(o[c], o[c + 1]);
       if (g + c < nr) to[c * kD] = static_cast<uint16_t>(v);
       if (g + c + 1 < nr) to[(c + 1) * kD] = static_cast<uint16_t>(v >> 16);
