@@ -152,7 +152,7 @@ struct ListSmem {
   unsigned long long rowp[2][kKeys]; // addresses of a tile's rows (g_zero_row: no such row), by tile parity
   TileInfo info[2];
   Plan plan[2];                      // of the row block at hand and of the next one
-  uint64_t full[4], free_[4],        // of a pair of chunk slots
+  uint64_t full[4], free_[4],        // of a pair of chunk slots; of a block of 128 dims
       bar_s[2], bar_p[2], bar_q, plan_full[2], plan_free[2], rows_full[2], rows_free[2], drained;
   uint32_t tmem;
   int abort;
@@ -530,6 +530,16 @@ struct TileWalk {
 // requested while the tile before it is in its products.  NS chunk slots; the fills of a pair of
 // slots wait for its release.
 // ---------------------------------------------------------------------------
+// Waits until the slots of a block of dims are free for tile g: the block that had them last has
+// been used.  (A release barrier per block of dims, not per pair of slots: a wait sees every phase
+// of its barrier, so that none is mistaken for another by its parity.)
+template <int NS>
+__device__ __forceinline__ bool wait_released(ListSmem* sm, int block, int g, unsigned long long spin) {
+  constexpr int kAtOnce = NS / 2;   // blocks of dims in the slots
+  const int last = (block + 4 - kAtOnce) & 3, tile = block < kAtOnce ? g - 1 : g;   // kAtOnce blocks before it
+  return tile < 0 || wait_bar(sm, &sm->free_[last], tile & 1, spin);
+}
+
 template <int FMT, int NS>
 struct RowLoader {
   ListSmem* sm;
@@ -603,8 +613,7 @@ struct RowLoader {
   }
   // the tile's rows into the chunks once they are free
   __device__ __forceinline__ bool fill(int g, unsigned long long spin) {
-    const int n = g * (8 / NS) + 2 * block / NS;
-    const bool ok = n == 0 || wait_bar(sm, &sm->free_[block % (NS / 2)], (n - 1) & 1, spin);
+    const bool ok = wait_released<NS>(sm, block, g, spin);
     __syncwarp();
     if (row0 < keys) {   // (rows behind the last key: zeros up to this warp's 32, beyond them nothing is read)
       store(g, 0);
@@ -1301,8 +1310,7 @@ __device__ __forceinline__ void plan_weights(const ListArgs& a, ListSmem* sm) {
 }
 
 // The block's nt tiles (runs of one or several requests): while the S product of a tile runs,
-// the tile before it is weighed.  Where a run of another request begins, its queries replace
-// the ones before as soon as their last product is complete.
+// the tile before it is weighed.
 template <int FMT, int NS>
 __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uint8_t* slots, uint8_t* qtile,
                                             float* lse, uint32_t tmem, int nq, int nt) {
@@ -1314,14 +1322,21 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
   const Plan* pl = &sm->plan[0];
   TileWalk walk(pl);
   rows.request(0, a.spin);
-  for (int i = 0; i <= nt; ++i) {
-    if (i < nt) {
+  int next_run = 1, i = 0, t = 0;   // tiles to fill and to weigh next
+  while (t < nt) {
+    // The first tile of another request's run is filled after the tile before it has been weighed
+    // and the queries replaced: with four slots its first chunks have to be used before the last
+    // ones can be filled.
+    const bool turn = next_run < pl->nruns && i == pl->runs[next_run].tile0;
+    if (i < nt && (i == t || !turn)) {
+      if (turn) load_request(a, sm, pl->runs[next_run++].req, nq, qtile, lse);
       rows.fill(i, a.spin);
       if (lane == 0) mbar_arrive(&sm->rows_free[i & 1]);
-      if (i + 1 < nt) rows.request(i + 1, a.spin);
+      ++i;
+      if (i < nt) rows.request(i, a.spin);
+      if (i < nt && i - t < 2) continue;
     }
-    if (i == 0) continue;
-    const int t = i - 1, buf = t & 1;
+    const int buf = t & 1;
     int k0, n;
     walk.seek(t, &k0, &n);
     const Run& u = pl->runs[walk.run];
@@ -1353,8 +1368,7 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
       const long long b = u.req, j = walk.position(k0 + key);
       a.acc_out[b * a.acc_out_stride + j] = a.decay * a.acc[b * a.acc_stride + j] + w;
     }
-    if (i < nt && walk.run + 1 < pl->nruns && i == pl->runs[walk.run + 1].tile0)
-      load_request(a, sm, pl->runs[walk.run + 1].req, nq, qtile, lse);
+    ++t;
   }
 }
 
@@ -1370,7 +1384,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < kWeightSlots / 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sm->full[i], 4);
       mbar_init(&sm->free_[i], 1);
     }
@@ -1425,7 +1439,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
               tc_fence_after();
             }
             if (ok) issue_s_chunk(tmem + buf * 128, dk + slot * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
-            if (c & 1) mma_commit(&sm->free_[slot >> 1]);
+            if (c & 1) mma_commit(&sm->free_[c >> 1]);
           }
           mma_commit(&sm->bar_s[buf]);
           mbar_arrive(&sm->bar_s[buf]);   // hands on what the loading warps wrote (none)

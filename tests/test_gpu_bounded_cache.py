@@ -765,3 +765,20 @@ def test_window_many_heads_of_one_query_group():
     for H in (1, 2, 63):
         _window_all(cache, _queries(len(req), H, 801), pos1, 33, 2, req, None,
                     pick=list(range(0, len(req), 7)) + [96, 97, 99, 100, len(req) - 1])
+
+
+@pytest.mark.parametrize("H", [16, 64, 65, 96, 128])
+@pytest.mark.parametrize("fmt", [BF16, FP8, FP4])
+def test_weights_shares_that_span_requests(H, fmt):
+    """More tiles than blocks: a block's share goes from one request to the next."""
+    B = 24
+    n = [1500 - 37 * b for b in range(B)]
+    c = _prefix_case(B, H, 0, n, fmt, None, seed=810 + H)
+    lse = torch.full((B, H), 5.0, device="cuda")
+    acc = torch.zeros((B, 1500), device="cuda")
+    cskv.attn_weights(c["q"][0].cuda(), c["cache"].to_device(), _i32(n), 1500, SCALE, _cs(c["ctx"]), lse, acc)
+    assert cskv.device_status() == 0
+    got = acc.cpu().numpy()
+    for b in range(B):
+        w, bound = bounded.weights(c["q"][1][b], int(c["ctx"][b]) - 1, c["cache"].decoded[b][:n[b]], np.full(H, 5.0), SCALE)
+        assert np.all(np.abs(got[b, :n[b]] - w) <= bound + 2.0 ** -24 * np.abs(w)) and not got[b, n[b]:].any()
