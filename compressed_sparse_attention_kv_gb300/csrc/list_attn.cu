@@ -59,6 +59,7 @@ constexpr int kChunk = kKeys * 128;      // bytes of 64 dims of a tile
 constexpr int kWorkWarps = 16;
 constexpr int kWorkThreads = kWorkWarps * 32;
 constexpr int kThreads = kWorkThreads + 64;
+constexpr int kWeightSlots = 4;          // of weights_kernel
 constexpr int kWorkBarrier = 1;          // named barrier of warps 0-15
 constexpr uint32_t kTmemS = 256;         // TMEM columns: O 0..255, S from here
 constexpr float kSlack = 8.0f;           // base 2: weights stay below 2^8
@@ -102,6 +103,7 @@ struct ListArgs {
   int prefix_in_own, ring_in_own;   // the prefix, the ring belong to each request's own list
   int rings_only, lead, beside;     // the call's launch for the rings; before it; beside another
   int items;                        // row blocks of the launch
+  int q_rows;                       // rows of its largest one, padded to 16
   int prefetch;                     // no other block reads this block's keys: send for them early
   int parts;                 // partial outputs of a row (1: written straight to out)
   float* opart;              // [row][part][512]
@@ -1026,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* ktile = base;                              // 8 chunks of 128 rows x 128 B
   uint8_t* qtile = ktile + 8 * kChunk;                // 9 chunks of nq rows x 128 B
-  uint8_t* ptile = qtile + 9 * kRows * 128;           // 128 keys x 128 B
+  uint8_t* ptile = qtile + 9 * a.q_rows * 128;        // 128 keys x 128 B
   ListSmem* sm = reinterpret_cast<ListSmem*>(ptile + kChunk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // this block's row blocks: blockIdx.x, + gridDim.x, ...
@@ -1184,31 +1186,60 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
 }
 
 // Joins a row's partial outputs in order, adds the sink, turns the output back: 64 threads of
-// 8 dims per row.
+// 8 dims, and where there are many parts four times as many, each with every fourth part (128
+// parts of 8 rows took 45 us longer with 64 threads that read them one after the other).
+constexpr int kFewParts = 8;
+template <int kShares>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ ListArgs a) {
+  __shared__ float shares[kShares > 1 ? kShares - 1 : 1][kD];
   grid_dep_wait();
-  const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (row >= static_cast<size_t>(a.T) * a.H) return;
+  const int sub = threadIdx.x >> 6, share = kShares > 1 ? sub : 0, lane = threadIdx.x & 31;
+  const size_t row = kShares > 1 ? blockIdx.x : static_cast<size_t>(blockIdx.x) * 4 + sub;
+  if (row >= static_cast<size_t>(a.T) * a.H) return;   // (one row per block: never)
   const int d = (threadIdx.x & 63) * 8;
-  const float* ml = a.ml + row * a.parts * 2;
+  const float2* ml = reinterpret_cast<const float2*>(a.ml) + row * a.parts;
   const float sink = a.sink ? a.sink[row % a.H] : -INFINITY;
   const float s2 = sink * kLog2e;
-  float M = s2;
-  for (int p = 0; p < a.parts; ++p)
-    if (ml[2 * p + 1] != 0.f) M = fmaxf(M, ml[2 * p]);
-  float total = 0.f, o[8];
+  auto weight = [&](float2 x, float M) { return x.y == 0.f ? 0.f : x.y != x.y ? x.y : exp2f(x.x - M); };
+  // the maximum and the sum: each thread by itself, or a part per lane
+  const int first = kShares > 1 ? lane : 0, step = kShares > 1 ? 32 : 1;
+  float M = s2, total = 0.f, o[8];
+#pragma unroll 4
+  for (int p = first; p < a.parts; p += step) {
+    const float2 x = __ldg(ml + p);
+    if (x.y != 0.f) M = fmaxf(M, x.x);
+  }
+  if constexpr (kShares > 1) {
+    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, w));
+    for (int p = lane; p < a.parts; p += 32) {
+      const float2 x = __ldg(ml + p);
+      total += x.y * weight(x, M);
+    }
+    for (int w = 16; w >= 1; w >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, w);
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
 #pragma unroll 4
-  for (int p = 0; p < a.parts; ++p) {
-    const float l = ml[2 * p + 1];
-    if (l == 0.f) continue;
-    const float e = l != l ? l : exp2f(ml[2 * p] - M);
-    total += l * e;
+  for (int p = share; p < a.parts; p += kShares) {
+    const float2 x = __ldg(ml + p);
+    const float e = weight(x, M);   // 0: a part without keys, whose output is 0
+    if constexpr (kShares == 1) total += x.y * e;
     const float4* v = reinterpret_cast<const float4*>(a.opart + (row * a.parts + p) * kD + d);
     const float4 v0 = __ldg(v), v1 = __ldg(v + 1);
     o[0] += e * v0.x; o[1] += e * v0.y; o[2] += e * v0.z; o[3] += e * v0.w;
     o[4] += e * v1.x; o[5] += e * v1.y; o[6] += e * v1.z; o[7] += e * v1.w;
+  }
+  if constexpr (kShares > 1) {
+    if (share > 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) shares[share - 1][d + i] = o[i];
+    }
+    __syncthreads();
+    if (share > 0) return;
+    for (int x = 0; x < kShares - 1; ++x) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] += shares[x][d + i];
+    }
   }
   const bool none = total == 0.f;
   if (s2 != -INFINITY) total += exp2f(s2 - M);
@@ -1232,7 +1263,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // accumulated weights: S^T of every tile, then a thread sums its key's weights over the
 // heads.  Up to 128 heads are the MMA columns, two S buffers in TMEM, four chunk slots
-// (released as soon as the chunk's products are complete).
+// (released as soon as the chunk's products are complete).  Eight slots would hold a tile, but the
+// rows' bytes on their way wait for lines of what shared memory leaves of L1: 32 x 8192 FP8 entries
+// of 64 heads took 52 us with eight slots (28 KB of L1) and 43 us with four (64 KB).
 // ---------------------------------------------------------------------------
 // Request b's queries and log-sum-exps (base 2; +inf: adds nothing); warps 0-15.
 __device__ __forceinline__ void load_request(const ListArgs& a, ListSmem* sm, int b, int nq, uint8_t* qtile, float* lse) {
@@ -1372,7 +1405,6 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
   }
 }
 
-template <int kWeightSlots>
 __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ ListArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -1381,7 +1413,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   uint8_t* qtile = slots + kWeightSlots * kChunk;
   ListSmem* sm = reinterpret_cast<ListSmem*>(qtile + 9 * nq * 128);
   float* lse = reinterpret_cast<float*>(sm + 1);   // [128], then the groups' shares of two tiles
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -1468,15 +1500,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-constexpr size_t kAttnSmem = 1024 + 9 * size_t(kChunk) + 9 * kRows * 128 + sizeof(ListSmem);
-static_assert(kAttnSmem <= 227 * 1024, "one block per SM");
-
-// eight chunk slots where the queries leave room for them (H <= 64)
-int weight_slots(int H) { return H <= kRows ? 8 : 4; }
+// Only as much as the rows need: the rest is L1, which the keys on their way wait for.
+constexpr size_t attn_smem(int q_rows) { return 1024 + 9 * size_t(kChunk) + 9 * size_t(q_rows) * 128 + sizeof(ListSmem); }
+static_assert(attn_smem(kRows) <= 227 * 1024, "one block per SM");
 
 size_t weights_smem(int H) {
   const int nq = (H + 15) & ~15;
-  return 1024 + weight_slots(H) * size_t(kChunk) + 9 * size_t(nq) * 128 + sizeof(ListSmem) + (128 + 6 * kKeys) * sizeof(float);
+  return 1024 + kWeightSlots * size_t(kChunk) + 9 * size_t(nq) * 128 + sizeof(ListSmem) + (128 + 6 * kKeys) * sizeof(float);
 }
 
 __host__ __device__ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1627,12 +1657,12 @@ cudaError_t launch_kind(const ListArgs& a, int fmt, unsigned grid, bool beside, 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kAttnSmem;
+  cfg.dynamicSmemBytes = attn_smem(a.q_rows);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = beside ? 1 : 0;
   static_assert(CSKV_FMT_BF16 == 0 && CSKV_FMT_FP8_E4M3_E8M0_B32 == 1 && CSKV_FMT_FP4_E2M1_E4M3_B16 == 2, "an index");
-  return launch_with_shared_memory(cfg, kernel, allowed[fmt], kAttnSmem, a);
+  return launch_with_shared_memory(cfg, kernel, allowed[fmt], attn_smem(kRows), a);
 }
 
 cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStream_t stream) {
@@ -1652,6 +1682,7 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
   // few blocks: a request's keys come from HBM; many blocks read them again and again from L2
   a.prefetch = a.req_of == nullptr && p.prefix_blocks == 0 && p.head_blocks == 1;
   a.rings_only = a.lead = a.beside = 0;
+  a.q_rows = p.prefix_blocks > 0 ? kRows : (p.group * p.heads_per_block + 15) & ~15;
   const int blocks = p.prefix_blocks * p.prefix_split + (a.pos1 != nullptr ? p.blocks : p.own_blocks) * p.split;
   cudaError_t e = cudaSuccess;
   if (blocks > 0) {
@@ -1676,12 +1707,13 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  const bool many = p.parts > kFewParts;
+  cfg.gridDim = dim3(static_cast<unsigned>(many ? rows : (rows + 3) / 4));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel, a);
+  return cudaLaunchKernelEx(&cfg, many ? attn_join_kernel<4> : attn_join_kernel<1>, a);
 }
 
 }  // namespace
@@ -1757,16 +1789,13 @@ cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32
     }));
     grid = static_cast<unsigned>(B) * a.split;
   }
-  const size_t smem = weights_smem(H);
-  static std::atomic<uint64_t> allowed[2];
-  const bool wide = weight_slots(H) == 4;
-  auto kernel = wide ? weights_kernel<4> : weights_kernel<8>;
+  static std::atomic<uint64_t> allowed;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = weights_smem(H);
   cfg.stream = stream;
-  return launch_with_shared_memory(cfg, kernel, allowed[wide], weights_smem(wide ? 128 : kRows), a);
+  return launch_with_shared_memory(cfg, weights_kernel, allowed, weights_smem(2 * kRows), a);
 }
 
 unsigned int take_err_list_attn() { return take_dev_err(); }

@@ -782,3 +782,12 @@ def test_weights_shares_that_span_requests(H, fmt):
     for b in range(B):
         w, bound = bounded.weights(c["q"][1][b], int(c["ctx"][b]) - 1, c["cache"].decoded[b][:n[b]], np.full(H, 5.0), SCALE)
         assert np.all(np.abs(got[b, :n[b]] - w) <= bound + 2.0 ** -24 * np.abs(w)) and not got[b, n[b]:].any()
+
+
+@pytest.mark.parametrize("H", [3, 64])
+def test_window_of_many_parts(H):
+    """A long window of one request: more parts than one thread per 8 dims joins, some rows of a
+    second request without any key."""
+    pos1 = [20000, 0, 17]
+    cache = _cache(FP8, pos1, seed=820)
+    _window_all(cache, _queries(3, H, 821), pos1, 20000, 3, None, np.linspace(-2, 3, H).astype(np.float32))
