@@ -59,7 +59,6 @@ constexpr int kChunk = kKeys * 128;      // bytes of 64 dims of a tile
 constexpr int kWorkWarps = 16;
 constexpr int kWorkThreads = kWorkWarps * 32;
 constexpr int kThreads = kWorkThreads + 64;
-constexpr int kWeightSlots = 4;          // of weights_kernel
 constexpr int kWorkBarrier = 1;          // named barrier of warps 0-15
 constexpr uint32_t kTmemS = 256;         // TMEM columns: O 0..255, S from here
 constexpr float kSlack = 8.0f;           // base 2: weights stay below 2^8
@@ -277,6 +276,12 @@ __device__ __forceinline__ void mma_set(uint32_t d, uint64_t da, uint64_t db, ui
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(da), "l"(db), "r"(id)
+      : "memory");
+}
+__device__ __forceinline__ void mma_if(uint32_t d, uint64_t da, uint64_t db, uint32_t id, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(id), "r"(add)
       : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -701,6 +706,8 @@ __device__ __forceinline__ void request_queries(const ListArgs& a, int r0, int n
     else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
+// kTerms: bf16 numbers that a rotated value is kept as (the third one in chunk 9).
+template <int kTerms>
 __device__ __forceinline__ void rotate_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
   static_assert(kRows * 8 <= kWorkThreads, "a thread per 8 dims of 64 rows, two passes for 128");
 #pragma unroll 1
@@ -718,21 +725,25 @@ __device__ __forceinline__ void rotate_queries(const ListArgs& a, int r0, int nr
     }
     if (r < nq) {
       uint4* hi = reinterpret_cast<uint4*>(qtile + 7 * (nq * 128) + sw128_offset(r, c));
-      uint4 v = *hi, lo = make_uint4(0u, 0u, 0u, 0u);
+      uint4 v = *hi, lo = make_uint4(0u, 0u, 0u, 0u), rest = lo;
       if (r < nr) {
         const float co[4] = {t0.x, t0.z, t1.x, t1.z}, si[4] = {t0.y, t0.w, t1.y, t1.w};
         uint32_t* w = reinterpret_cast<uint32_t*>(&v);
         uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+        uint32_t* e = reinterpret_cast<uint32_t*>(&rest);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
           const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
           w[k] = pack_bf16(z0, z1);
-          l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
+          const float l0 = z0 - bf16lo(w[k]), l1 = z1 - bf16hi(w[k]);   // (exact)
+          l[k] = pack_bf16(l0, l1);
+          if (kTerms == 3) e[k] = pack_bf16(l0 - bf16lo(l[k]), l1 - bf16hi(l[k]));
         }
         *hi = v;
       }
       *reinterpret_cast<uint4*>(qtile + 8 * (nq * 128) + sw128_offset(r, c)) = lo;
+      if (kTerms == 3) *reinterpret_cast<uint4*>(qtile + 9 * (nq * 128) + sw128_offset(r, c)) = rest;
     }
   }
   fence_proxy_async_smem();
@@ -749,6 +760,26 @@ __device__ __forceinline__ void issue_s_chunk(uint32_t d, uint64_t dk, uint64_t 
 #pragma unroll
     for (int k = 0; k < 4; ++k) mma_add(d, dk + 2 * k, dl + 2 * k, id);
   }
+}
+
+// For the weights, which are fp32: block m of 128 dims (chunks 2m, 2m + 1; dk, dq: its first chunk's
+// descriptors) into a sum of its own, or on top of the block before it (`add`).  The tensor core
+// cuts the low bits off at every step, so short sums are more exact, and the small terms of the
+// rotated dims (dl: the query's second and third) come before the large ones.
+__device__ __forceinline__ void issue_s_block(uint32_t d, uint64_t dk, uint64_t dq, uint64_t dl, uint32_t qstep, int m,
+                                              uint32_t add, uint32_t id) {
+  if (m == 3) {
+    mma_if(d, dk + (kChunk >> 4), dl + qstep, id, add);
+#pragma unroll
+    for (int k = 1; k < 8; ++k) mma_add(d, dk + (kChunk >> 4) + 2 * (k & 3), dl + (k < 4 ? qstep : 0u) + 2 * (k & 3), id);
+    mma_add(d, dk, dq, id);
+  } else {
+    mma_if(d, dk, dq, id, add);
+  }
+#pragma unroll
+  for (int k = 1; k < 4; ++k) mma_add(d, dk + 2 * k, dq + 2 * k, id);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mma_add(d, dk + (kChunk >> 4) + 2 * k, dq + qstep + 2 * k, id);
 }
 
 // ---------------------------------------------------------------------------
@@ -1143,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
     for (int e = 0; e < items; ++e) {
       const Plan* pl = plan_of(e);
       if (work_any(pl == nullptr)) break;
-      rotate_queries(a, pl->item.r0, pl->item.nr, pl->nq, qtile);
+      rotate_queries<2>(a, pl->item.r0, pl->item.nr, pl->nq, qtile);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->bar_q);
@@ -1265,8 +1296,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // heads.  Up to 128 heads are the MMA columns, two S buffers in TMEM, four chunk slots
 // (released as soon as the chunk's products are complete).  Eight slots would hold a tile, but the
 // rows' bytes on their way wait for lines of what shared memory leaves of L1: 32 x 8192 FP8 entries
-// of 64 heads took 52 us with eight slots (28 KB of L1) and 43 us with four (64 KB).
+// of 64 heads took 52 us with eight slots (28 KB of L1) and 45 us with four (64 KB).
+// Two, where the queries of more than 112 heads leave room for no more.  The weights are fp32: with
+// a rotated query in three bf16 numbers and the S product in four sums (two above 64 heads) logits
+// of N(0, 2) are off by 2.3e-7 (rms); in two numbers and one sum they were off by 2.2e-6, and no faster.
 // ---------------------------------------------------------------------------
+constexpr int kTileSums = 256;   // TMEM columns of a tile: 4 sums of up to 64 columns, or 2 of up to 128
+__device__ __forceinline__ int tile_sums(int nq) { return nq <= 64 ? 4 : 2; }
+
 // Request b's queries and log-sum-exps (base 2; +inf: adds nothing); warps 0-15.
 __device__ __forceinline__ void load_request(const ListArgs& a, ListSmem* sm, int b, int nq, uint8_t* qtile, float* lse) {
   work_sync();   // the request before it is weighed
@@ -1275,7 +1312,7 @@ __device__ __forceinline__ void load_request(const ListArgs& a, ListSmem* sm, in
     const float v = threadIdx.x < a.H ? a.lse_in[static_cast<size_t>(b) * a.H + threadIdx.x] : -INFINITY;
     lse[threadIdx.x] = v == -INFINITY ? INFINITY : v * kLog2e;
   }
-  rotate_queries(a, b * a.H, a.H, nq, qtile);
+  rotate_queries<3>(a, b * a.H, a.H, nq, qtile);
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->bar_q);
 }
@@ -1353,6 +1390,7 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
   const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
   RowLoader<FMT, NS> rows(sm, slots);
   const Plan* pl = &sm->plan[0];
+  const int sums = tile_sums(nq);
   TileWalk walk(pl);
   rows.request(0, a.spin);
   int next_run = 1, i = 0, t = 0;   // tiles to fill and to weigh next
@@ -1379,9 +1417,15 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
     // columns group * 16, group * 16 + 64, ...: this warp's share of the heads
     float w = 0.f;
     for (int c = group * 16; c < nq; c += 64) {
-      float z[16];
-      tmem_ld16(tmem + tlane + buf * 128 + c, z);
-      tmem_wait_ld();
+      float z[16], more[16];
+      const uint32_t at = tmem + tlane + buf * kTileSums + c;
+      tmem_ld16(at, z);
+      for (int x = kTileSums / sums; x < kTileSums; x += kTileSums / sums) {
+        tmem_ld16(at + x, more);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) z[k] += more[k];
+      }
 #pragma unroll
       for (int k = 0; k < 16; k += 4) {
         const float4 s = *reinterpret_cast<const float4*>(&lse[c + k]);
@@ -1405,13 +1449,14 @@ __device__ __forceinline__ void weigh_tiles(const ListArgs& a, ListSmem* sm, uin
   }
 }
 
+template <int kWeightSlots>
 __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ ListArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* slots = base;
   const int nq = (a.H + 15) & ~15;
   uint8_t* qtile = slots + kWeightSlots * kChunk;
-  ListSmem* sm = reinterpret_cast<ListSmem*>(qtile + 9 * nq * 128);
+  ListSmem* sm = reinterpret_cast<ListSmem*>(qtile + 10 * nq * 128);
   float* lse = reinterpret_cast<float*>(sm + 1);   // [128], then the groups' shares of two tiles
   const int tid = threadIdx.x, warp = tid >> 5;
 
@@ -1435,7 +1480,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     sm->plan[0].item.n_prefix = 0;
   }
   if (warp == 1) plan_weights(a, sm);
-  if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 256);
+  if (warp == kWorkWarps) tmem_alloc(&sm->tmem, 2 * kTileSums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1453,6 +1498,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         const uint64_t dk = smem_desc_sw128(smem_u32(slots), 16, 1024);
         const uint64_t dq = smem_desc_sw128(smem_u32(qtile), 16, 1024);
         const uint32_t qstep = nq * 8;
+        const int sums = tile_sums(nq);
         bool ok = true;
         int run = -1;
         for (int i = 0; i < nt && ok; ++i) {
@@ -1464,14 +1510,14 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           if (i >= 2) ok = ok && wait_bar(sm, &sm->bar_p[buf], ((i >> 1) - 1) & 1, a.spin);
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int slot = c % kWeightSlots, fill = i * (8 / kWeightSlots) + c / kWeightSlots;
-            if ((c & 1) == 0) {
-              ok = ok && wait_bar(sm, &sm->full[slot >> 1], fill & 1, a.spin);
-              tc_fence_after();
-            }
-            if (ok) issue_s_chunk(tmem + buf * 128, dk + slot * (kChunk >> 4), dq + c * qstep, dq + 8 * qstep, c, ids);
-            if (c & 1) mma_commit(&sm->free_[c >> 1]);
+          for (int m = 0; m < 4; ++m) {
+            const int slot = 2 * m % kWeightSlots, fill = i * (8 / kWeightSlots) + 2 * m / kWeightSlots;
+            ok = ok && wait_bar(sm, &sm->full[slot >> 1], fill & 1, a.spin);
+            tc_fence_after();
+            if (ok)
+              issue_s_block(tmem + buf * kTileSums + (m * sums >> 2) * (kTileSums / sums), dk + slot * (kChunk >> 4),
+                            dq + 2 * m * qstep, dq + 8 * qstep, qstep, m, (m & 1) != 0 && sums == 2, ids);
+            mma_commit(&sm->free_[m]);
           }
           mma_commit(&sm->bar_s[buf]);
           mbar_arrive(&sm->bar_s[buf]);   // hands on what the loading warps wrote (none)
@@ -1493,7 +1539,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   __syncthreads();
   if (warp == kWorkWarps) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 2 * kTileSums);
   }
 }
 
@@ -1504,10 +1550,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 constexpr size_t attn_smem(int q_rows) { return 1024 + 9 * size_t(kChunk) + 9 * size_t(q_rows) * 128 + sizeof(ListSmem); }
 static_assert(attn_smem(kRows) <= 227 * 1024, "one block per SM");
 
-size_t weights_smem(int H) {
-  const int nq = (H + 15) & ~15;
-  return 1024 + kWeightSlots * size_t(kChunk) + 9 * size_t(nq) * 128 + sizeof(ListSmem) + (128 + 6 * kKeys) * sizeof(float);
+constexpr size_t weights_smem(int H, int slots) {
+  return 1024 + slots * size_t(kChunk) + 10 * size_t((H + 15) & ~15) * 128 + sizeof(ListSmem) + (128 + 6 * kKeys) * sizeof(float);
 }
+constexpr int kMostHeads = 112;   // with four slots
+static_assert(weights_smem(kMostHeads, 4) <= 227 * 1024 && weights_smem(128, 2) <= 227 * 1024, "one block per SM");
 
 __host__ __device__ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -1789,13 +1836,15 @@ cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32
     }));
     grid = static_cast<unsigned>(B) * a.split;
   }
-  static std::atomic<uint64_t> allowed;
+  static std::atomic<uint64_t> allowed[2];
+  const bool most = H > kMostHeads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = weights_smem(H);
+  cfg.dynamicSmemBytes = weights_smem(H, most ? 2 : 4);
   cfg.stream = stream;
-  return launch_with_shared_memory(cfg, weights_kernel, allowed, weights_smem(2 * kRows), a);
+  return launch_with_shared_memory(cfg, most ? weights_kernel<2> : weights_kernel<4>, allowed[most],
+                                   most ? weights_smem(128, 2) : weights_smem(kMostHeads, 4), a);
 }
 
 unsigned int take_err_list_attn() { return take_dev_err(); }
