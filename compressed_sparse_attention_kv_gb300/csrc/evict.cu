@@ -16,7 +16,7 @@
 // L2, for every digit).  Histograms of the blocks are added up through distributed shared
 // memory; every block takes the same decision.  Warps walk contiguous stretches with
 // ballots, so that ranks need one scan over the warps' counts.  Few pairs are copied by the
-// cluster itself (up to 512 a request: the second launch costs more); many by a second kernel
+// cluster itself; many by a second kernel
 // over the whole device.  The counts of kept entries on either side of slot m give every warp
 // its place in both lists in one exchange between the blocks.
 //
@@ -39,9 +39,15 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kSliceTarget = 4096;       // entries per block before a request takes another block
-constexpr int kKeysInSmem = 48 * 1024;   // entries of a slice whose keys fit in shared memory
-constexpr int kFusedPairs = 512;         // pairs that the selecting cluster copies itself
+// Entries per block before a request takes another block: 65,536 entries took 112 us in one block
+// and 30 in eight, 16,384 took 26 in one and 20 in four; 4,096 took 15 in one and 18 in four.
+constexpr int kSliceTarget = 4096;
+// Entries of a slice whose keys fit in shared memory (4 requests of 65,536: 49 us, read again for
+// every digit 56).
+constexpr int kKeysInSmem = 48 * 1024;
+// Pairs that the selecting cluster copies itself: 64, 512 and 1,024 pairs of one request took 16, 20
+// and 25 us, by a second kernel 19 each; of 32 requests 17, 21 and 27 us, by a second kernel 20, 22 and 26.
+constexpr int kFusedPairs = 512;
 
 struct EvictArgs {
   cskv_paged cache[4];

@@ -1219,6 +1219,8 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
 // Joins a row's partial outputs in order, adds the sink, turns the output back: 64 threads of
 // 8 dims, and where there are many parts four times as many, each with every fourth part (128
 // parts of 8 rows took 45 us longer with 64 threads that read them one after the other).
+// Up to 8 parts one share: four take longer where there are many rows (16 requests of 64 heads and
+// 4 parts: 31.2 us, with four shares 32.6); beyond, 30.6 us against 18.3 (16 heads, 8,192 keys).
 constexpr int kFewParts = 8;
 template <int kShares>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ ListArgs a) {
@@ -1576,11 +1578,15 @@ struct Schedule {
     const double work = n * length;
     if (work <= idle) {
       idle -= work;
-      return;
+    } else {
+      const double left = work - idle, waves = std::ceil(left / length / kSmsPlanned);
+      time += waves * length;
+      idle = waves * length * kSmsPlanned - left;
     }
-    const double left = work - idle, waves = std::ceil(left / length / kSmsPlanned);
-    time += waves * length;
-    idle = waves * length * kSmsPlanned - left;
+    if (time < length) {   // blocks beside shorter ones
+      idle += (length - time) * kSmsPlanned;
+      time = length;
+    }
   }
 };
 
@@ -1631,8 +1637,11 @@ ListPlan window_plan(int T, int H, bool grouped, int max_ctx, int window, int fi
 
 // The prefix once for blocks of 64 (request, head) rows beside each request's own list, or as
 // the first part of every request's list (the better one when a block's 64 rows are one
-// request's heads anyway, or when there is little of it: fewer partial outputs); the ring in
-// the request's list when its rows have the cache's format (`merge`), else as a block of its own.
+// request's heads anyway, or when there is little of it: fewer partial outputs).  Apart and in the
+// lists: 64 requests of 64 heads and 8,192 + 512 entries 133 and 152 us, of 16 heads and 1,024 + 64
+// 22 and 28 us, 32 requests of 896 + 128 the same 26.  The ring in the request's list when its rows
+// have the cache's format (`merge`; those 32 requests: 26 us, as blocks of their own 35), else as a
+// block of its own.
 ListPlan prefix_plan(int B, int H, int n_prefix, int max_entries, bool ring, bool merge) {
   ListPlan best = {};
   double best_cost = -1;
@@ -1726,7 +1735,8 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
   const size_t rows = static_cast<size_t>(a.T) * a.H;
   a.opart = static_cast<float*>(workspace);
   a.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a256(rows * p.parts * kD * 4));
-  // few blocks: a request's keys come from HBM; many blocks read them again and again from L2
+  // few blocks: a request's keys come from HBM (32 requests of 4,160 keys: 52 us, without it 56); many
+  // blocks read them again and again from L2 (a prefix of 896 entries: 26.0 us, without it 25.2)
   a.prefetch = a.req_of == nullptr && p.prefix_blocks == 0 && p.head_blocks == 1;
   a.rings_only = a.lead = a.beside = 0;
   a.q_rows = p.prefix_blocks > 0 ? kRows : (p.group * p.heads_per_block + 15) & ~15;
@@ -1735,8 +1745,9 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
   if (blocks > 0) {
     a.items = blocks;
     a.lead = p.ring_blocks > 0;
-    // prompts: one block per SM, each with several row blocks; otherwise the row blocks differ
-    // in length, and the hardware's order balances them better
+    // prompts: one block per SM, each with several row blocks (8,192 tokens of 16 heads, a window of
+    // 128: 212 us, with a block each 253); otherwise the row blocks differ in length, and the
+    // hardware's order balances them better
     e = launch_kind(a, a.kv.fmt, a.pos1 != nullptr ? std::min(blocks, kSmsPlanned) : blocks, false, stream);
     if (e != cudaSuccess) return e;
   }
@@ -1824,7 +1835,8 @@ cudaError_t launch_attn_weights(const void* q, const cskv_paged& kv, const int32
   a.acc_out_stride = acc_out_stride;
   a.prefetch = 1;
   // up to kRuns requests: the blocks, one per SM, share all their tiles evenly, whatever their
-  // lengths; more requests: blocks of one request's tiles each
+  // lengths (32 requests of 256 to 8,192 entries: 33 us; 58 in blocks of one request's tiles each,
+  // as more requests are)
   const int tiles = tiles_of(max_entries - first);
   a.balanced = B <= kRuns;
   unsigned grid = static_cast<unsigned>(std::min<long long>(kSmsPlanned, static_cast<long long>(B) * tiles));
