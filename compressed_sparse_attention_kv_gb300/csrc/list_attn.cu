@@ -1622,13 +1622,15 @@ ListPlan base_plan(int T, int H, bool grouped) {
   return p;
 }
 
-ListPlan window_plan(int T, int H, bool grouped, int max_ctx, int window, int first) {
+// `several`: the queries are of more than one request, so that a row block may see two lists.
+ListPlan window_plan(int T, int H, bool grouped, bool several, int max_ctx, int window, int first) {
   ListPlan p = base_plan(T, H, grouped);
   const long long keys = std::min<long long>(max_ctx, static_cast<long long>(window) + first + p.group - 1);
   const int tiles = std::max(1, tiles_of(keys));
   const int len = best_length(tiles, [&](int l) {
     Schedule s;
     s.add(double(p.blocks) * shares(tiles, l), l + kBlockCost);
+    if (several && p.group > 1) s.time = std::max(s.time, 2 * l + kBlockCost);
     return s.time + join_cost(double(T) * H, shares(tiles, l));
   });
   p.split = p.parts = shares(tiles, len);
@@ -1777,9 +1779,10 @@ cudaError_t launch_list(ListArgs& a, const ListPlan& p, void* workspace, cudaStr
 }  // namespace
 
 size_t window_attn_workspace_bytes(int T, int H, int max_ctx, int window, int first) {
-  // one query per request or queries of prompts: the larger of the two
-  return std::max(plan_workspace(window_plan(T, H, false, max_ctx, window, first), T, H),
-                  plan_workspace(window_plan(T, H, true, max_ctx, window, first), T, H));
+  // one query per request, queries of one prompt or of several: the largest
+  return std::max({plan_workspace(window_plan(T, H, false, false, max_ctx, window, first), T, H),
+                   plan_workspace(window_plan(T, H, true, false, max_ctx, window, first), T, H),
+                   plan_workspace(window_plan(T, H, true, true, max_ctx, window, first), T, H)});
 }
 
 size_t prefix_attn_workspace_bytes(int B, int H, int n_prefix, int max_entries, int with_swa) {
@@ -1800,7 +1803,7 @@ cudaError_t launch_window_attn(const void* q, const cskv_paged& rows, int num_re
   a.first = first;
   a.max_ctx = max_ctx;
   // without req_of every query is a request of its own: no two share keys
-  return launch_list(a, window_plan(T, H, req_of != nullptr, max_ctx, window, first), workspace, stream);
+  return launch_list(a, window_plan(T, H, req_of != nullptr, num_reqs > 1, max_ctx, window, first), workspace, stream);
 }
 
 cudaError_t launch_prefix_attn(const void* q, const cskv_paged& kv, const int32_t* n_entries, int n_prefix,
