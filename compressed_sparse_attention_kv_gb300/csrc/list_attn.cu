@@ -842,11 +842,12 @@ __device__ __forceinline__ bool weigh_tile(const ListArgs& a, const Plan* pl, Li
   const int quarter = warp & 3, group = warp >> 2;
   const int cb = group * 16;        // this thread's rows (columns of S^T)
   const int nq = pl->nq;
-  const bool has = cb < nq;
   const int key = quarter * 32 + lane;
   const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
   const TileInfo t = sm->info[g & 1];
   const int n = t.n;
+  // whether the warp has rows and keys: a short tile's weights behind its last key are not read
+  const bool rows = cb < nq, has = rows && quarter * 32 < n;
   uint32_t bits = 0xFFFFu;
   if (t.plain == 0 && has) {   // before S is complete
     bits = seen_by(pl, t.run, t.k0 + quarter * 32, cb + (lane & 15));
@@ -893,6 +894,8 @@ __device__ __forceinline__ bool weigh_tile(const ListArgs& a, const Plan* pl, Li
         const float mine = reduce_columns(t, [](float x, float y) { return fmaxf(x, y); });
         if ((lane & 3) == 0) sm->part[quarter][cb + h + (lane >> 2)] = mine;
       }
+    } else if (rows && lane < 16) {
+      sm->part[quarter][cb + lane] = -INFINITY;
     }
     work_sync();
     if (tid < nq) {
@@ -905,7 +908,7 @@ __device__ __forceinline__ bool weigh_tile(const ListArgs& a, const Plan* pl, Li
       sm->msub[tid] = sub;
     }
     work_sync();
-    if (has) l *= sm->fac[cb + (lane >> 1)];
+    if (rows) l *= sm->fac[cb + (lane >> 1)];
     if (!first) {   // the S commit says that the O products so far are complete
 #pragma unroll 1
       for (int r = 0; r < nq; r += 16) {   // this warp's 32 dims of block `group`, 16 rows at a time
