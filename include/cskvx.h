@@ -20,6 +20,10 @@
  * host before anything is launched (CSKV_ERR_INVALID).  A length beyond the host's
  * bound is cut to it, an index outside its table or pool is skipped; both set
  * CSKV_ERR_BOUNDS on the device.  A workspace belongs to one call at a time.
+ * Limits: 2^23 queries or requests of a call (65,535 requests in attn_weights and
+ * evict), lengths and positions up to 2^30; softmax_scale is finite and above 0.
+ * A wait inside a kernel that runs out (cskv_set_spin_limit) ends the kernel with
+ * CSKV_ERR_TIMEOUT on the device; its outputs are then not defined.
  */
 #ifndef CSKVX_H
 #define CSKVX_H
@@ -53,8 +57,9 @@ extern "C" {
  * the queries that see it NaN, and no others.
  * The query is kept as the sum of two bf16 numbers after its rotation, products run
  * as bf16 tensor-core MMAs with fp32 accumulation, weights enter the second product
- * as bf16; sums, maxima and partial outputs are fp32.  The same call gives the same
- * bits each time.
+ * as bf16 and the output is divided by the sum of the rounded ones; lse is made of the
+ * fp32 weights; sums, maxima and partial outputs are fp32.  The same call gives the
+ * same bits each time.
  * ------------------------------------------------------------------------ */
 CSKV_API size_t cskvx_window_attn_workspace_size(int32_t T, int32_t H, int32_t max_ctx_len, int32_t window,
                                                  int32_t first);
@@ -98,7 +103,9 @@ CSKV_API int32_t cskvx_prefix_decode_attn(const void* q, cskv_paged main_kv, con
  * z as in cskvx_prefix_decode_attn, lse what that call gave (a row whose lse is -inf
  * adds nothing); other elements of acc_out are left as they are.  acc, acc_out:
  * fp32 [B, stride], stride >= max_entries; acc_out may be acc itself.  first: e.g.
- * the shared prefix, which is not evicted.  decay finite.  H in [1, 128].
+ * the shared prefix, which is not evicted.  decay finite.  H in [1, 128].  The rotated
+ * query is kept as three bf16 numbers and a logit summed in four parts (two above 64 heads),
+ * so that logits are exact to about 2e-7 of N(0, 2).
  * ------------------------------------------------------------------------ */
 CSKV_API int32_t cskvx_attn_weights(const void* q, cskv_paged main_kv, const int32_t* n_entries, int32_t first,
                                     int32_t max_entries, float softmax_scale, const float* q_rope_cs,

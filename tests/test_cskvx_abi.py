@@ -158,3 +158,26 @@ def test_oracle_evict_follows_the_definition(seed):
                 continue
             assert np.isnan(acc[g]) and not np.isnan(acc[k]) or value(k) > value(g) or (
                 value(k) == value(g) and np.isnan(acc[k]) == np.isnan(acc[g]) and k < g)
+
+
+@pytest.mark.parametrize("what, change", [
+    ("window", {"T": (1 << 23) + 1, "num_reqs": 1 << 24}), ("prefix", {"B": (1 << 23) + 1}),
+    ("weights", {"B": 65536}), ("evict", {"B": 65536}), ("evict", {"max_entries": (1 << 30) + 1}),
+    ("evict", {"budget": (1 << 30) + 1}), ("weights", {"max_entries": (1 << 30) + 1}),
+])
+def test_sizes_beyond_the_limits_are_refused(lib, what, change):
+    test_bad_arguments_are_refused_before_any_launch(lib, what, change)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_workspaces_of_any_size_are_finite(lib, seed):
+    """A list is cut into 4 x 152 shares at most, a row sees a prefix, its own list and a ring: up to
+    2 x 608 + 1 parts of 2 KB and 8 bytes a row."""
+    rng = np.random.default_rng(900 + seed)
+    for _ in range(500):
+        T, H = int(2 ** rng.uniform(0, 14)), int(rng.integers(1, 129))
+        ctx, window, first = (int(2 ** rng.uniform(0, 30)) for _ in range(3))
+        w = lib.cskvx_window_attn_workspace_size(T, H, ctx, window, first)
+        p = lib.cskvx_prefix_decode_attn_workspace_size(T, H, min(window, ctx), ctx, int(rng.integers(0, 2)))
+        for need in (w, p):
+            assert need % 256 == 0 and need <= T * H * (2 * 608 + 1) * (2048 + 8) + 512
