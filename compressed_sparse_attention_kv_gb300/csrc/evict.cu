@@ -20,8 +20,8 @@
 // over the whole device.  The counts of kept entries on either side of slot m give every warp
 // its place in both lists in one exchange between the blocks.
 //
-// Measured: 8 requests of 65,536 entries cut to half (1 KB rows) 78 us, 30 of them the
-// selection and 46 the copies (5.8 TB/s); 32 requests of 4,160 cut by a page 16 us, one
+// Measured: 8 requests of 65,536 entries cut to half (1 KB rows) 78 us, 29 of them the
+// selection and 48 the copies (5.7 TB/s); 32 requests of 4,160 cut by a page 16 us, one
 // request of 333 entries 12 us, both the chain of barriers and memory latencies of a selection.
 #include <algorithm>
 
