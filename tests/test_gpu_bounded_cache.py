@@ -791,3 +791,32 @@ def test_window_of_many_parts(H):
     pos1 = [20000, 0, 17]
     cache = _cache(FP8, pos1, seed=820)
     _window_all(cache, _queries(3, H, 821), pos1, 20000, 3, None, np.linspace(-2, 3, H).astype(np.float32))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_of_slices_beyond_shared_memory(in_place):
+    """Longer slices than the shared memory has keys for: they are read again for every digit."""
+    cap, n, budget, fixed, recent = 450001, 449999, 300000, 100, 20000
+    pages = (cap + 63) // 64
+    rs = np.random.default_rng(830)
+    acc = np.exp(rs.standard_normal((1, cap))).astype(np.float32)
+    acc[0, ::5] = 0.25
+    age = rs.permutation(cap).astype(np.int32)[None]
+    pool = torch.randint(0, 256, (pages, 64 * 256), dtype=torch.uint8, device="cuda",
+                         generator=torch.Generator(device="cuda").manual_seed(831))
+    bt = cuda(rs.permutation(pages).astype(np.int32)[None])
+    rows = lambda: pool.view(pages, 64, 256)[bt[0].long()].view(-1, 256)
+    before = rows().clone()
+    a, g, nn = cuda(acc), cuda(age), _i32([n])
+    kw = {} if in_place else dict(acc_out=torch.full((1, budget), -5.0, device="cuda"), n_out=_i32([0]),
+                                  age_out=torch.full((1, budget), -5, dtype=torch.int32, device="cuda"))
+    src, n_out, acc_out, age_out = cskv.evict([cskv.PagedCache(pool, bt, BF16, 128)], a, nn, budget, fixed=fixed,
+                                              recent=recent, age=g, **kw)
+    assert cskv.device_status() == 0
+    ref, m = bounded.evict(acc[0], age[0], n, budget, fixed, recent)
+    assert int(n_out[0]) == m and np.array_equal(src[0].cpu().numpy(), ref)
+    assert np.array_equal(acc_out[0, :m].cpu().numpy(), acc[0][ref[:m]])
+    assert np.array_equal(age_out[0, :m].cpu().numpy(), age[0][ref[:m]])
+    after = rows()
+    assert torch.equal(after[:m], before[torch.from_numpy(ref[:m]).long().cuda()])
+    assert torch.equal(after[m:], before[m:])
