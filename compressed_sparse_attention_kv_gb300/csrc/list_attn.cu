@@ -164,7 +164,7 @@ struct ListSmem {
   TileInfo info[2];
   Plan plan[2];                      // of the row block at hand and of the next one
   uint64_t full[4], free_[4],        // of a pair of chunk slots; of a block of 128 dims
-      bar_s[2], bar_p[2], bar_q, plan_full[2], plan_free[2], rows_full[2], rows_free[2], drained;
+      bar_s[2], bar_p[2], bar_q[2], plan_full[2], plan_free[2], rows_full[2], rows_free[2], drained;
   uint32_t tmem;
   int abort;
   __align__(16) float m[kRows];      // running reference in units of q'.c, -inf: no key yet
@@ -1130,9 +1130,9 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
     }
     mbar_init(&sm->bar_s[0], 2);
     mbar_init(&sm->bar_p[0], kWorkWarps);
-    mbar_init(&sm->bar_q, kWorkWarps);
     mbar_init(&sm->drained, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->bar_q[i], kWorkWarps);
       mbar_init(&sm->plan_full[i], 1);
       mbar_init(&sm->plan_free[i], kWorkWarps + 1);
       mbar_init(&sm->rows_full[i], 1);
@@ -1186,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
         const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
         const uint32_t ido = make_idesc(1, 1, 1, 1, 128, 0) | (static_cast<uint32_t>(nq >> 3) << 17);
         const uint32_t qstep = nq * 8;   // a chunk of Q, in the descriptors' 16-byte units
-        ok = wait_bar(sm, &sm->bar_q, e & 1, a.spin);
+        ok = wait_bar(sm, &sm->bar_q[e & 1], (e >> 1) & 1, a.spin);
         for (int i = 0; i < nt && ok; ++i, ++g) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -1235,7 +1235,9 @@ __global__ void __launch_bounds__(kThreads, 1) list_attn_kernel(const __grid_con
       rotate_queries<2>(a, pl->item.r0, pl->item.nr, pl->nq, qtile);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->bar_q);
+      // (a barrier per plan slot: nothing else keeps these warps from completing the phase of the row
+      // block behind one without tiles before the issuing thread has seen this one)
+      if (lane == 0) mbar_arrive(&sm->bar_q[e & 1]);
       float l = 0.f, hat[4] = {0.f, 0.f, 0.f, 0.f};   // sums of the weights, and of the rounded ones
       const int nt = pl->nt;
       if (nt > 0 && !requested) ok = rows.request(g, a.spin) && ok;
@@ -1374,7 +1376,7 @@ __device__ __forceinline__ void load_request(const ListArgs& a, ListSmem* sm, in
   }
   rotate_queries<3>(a, b * a.H, a.H, nq, qtile);
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->bar_q);
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->bar_q[0]);   // (every run has a tile: one barrier does)
 }
 
 // The block's runs: an even share of all requests' tiles (up to kRuns requests), or of one
@@ -1531,7 +1533,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       mbar_init(&sm->bar_s[i], 2);
       mbar_init(&sm->bar_p[i], kWorkWarps);
     }
-    mbar_init(&sm->bar_q, kWorkWarps);
+    mbar_init(&sm->bar_q[0], kWorkWarps);
     mbar_init(&sm->drained, 1);
     sm->abort = 0;
     fence_mbar_init();
@@ -1565,7 +1567,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           const int buf = i & 1;
           if (run + 1 < sm->plan[0].nruns && i == sm->plan[0].runs[run + 1].tile0) {
             ++run;
-            ok = wait_bar(sm, &sm->bar_q, run & 1, a.spin);
+            ok = wait_bar(sm, &sm->bar_q[0], run & 1, a.spin);
           }
           if (i >= 2) ok = ok && wait_bar(sm, &sm->bar_p[buf], ((i >> 1) - 1) & 1, a.spin);
           tc_fence_after();

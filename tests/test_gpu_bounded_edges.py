@@ -1,0 +1,41 @@
+"""window_attn, prefix_decode_attn, attn_weights and evict where a call is unusual: prompts of
+many row blocks with padding, tables and pages of other shapes, extreme sinks and scales.  The
+bounds are those of test_gpu_bounded_cache.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import compressed_sparse_attention_kv_gb300 as cskv
+from oracle import bounded, codecs
+
+from cases import cuda
+from test_gpu_bounded_cache import (BF16, FP4, FP8, SCALE, _cache, _check, _cs, _i32, _prefix_all, _prefix_case,
+                                    _prefix_run, _queries, _window, _window_all, _window_ref)
+
+pytestmark = pytest.mark.gpu
+
+
+# --- row blocks without any tile ---------------------------------------------------------------
+
+@pytest.mark.parametrize("where", ["first", "last", "between", "stretches", "alternating", "all"])
+@pytest.mark.parametrize("H", [64, 100])
+def test_window_padding_in_prompts_of_many_row_blocks(where, H):
+    """A prompt of 1,000 queries is several row blocks to each SM; those of padding have no tile."""
+    T, L = 1000, 400
+    cache = _cache(FP8, [L], seed=900 + H)
+    pos1 = np.arange(T) % L + 1
+    i = np.arange(T)
+    empty = {"first": i < 500, "last": i >= 500, "between": (i > 150) & (i < 700),
+             "stretches": (i // 152) % 2 == 0, "alternating": (i // 7) % 2 == 0, "all": i >= 0}[where]
+    pos1 = np.where(empty, 0, pos1)
+    q = _queries(T, H, 901)
+    req = np.zeros(T, np.int64)
+    sink = np.random.default_rng(902).standard_normal(H).astype(np.float32)
+    for _ in range(3):
+        out, lse = _window(cache, q, pos1, 128, 4, req, sink, max_ctx=L)
+        assert cskv.device_status() == 0
+        assert not out[cuda(empty)].any() and torch.equal(lse[cuda(empty)], cuda(sink).expand(int(empty.sum()), H))
+    real = np.flatnonzero(~empty)
+    for k in real[::max(1, len(real) // 12)]:
+        _check(out[k], lse[k], _window_ref(cache, q, k, pos1, 128, 4, req, sink), "query %d" % k)
