@@ -1026,7 +1026,8 @@ __device__ __forceinline__ void finish_sums(const ListArgs& a, const Plan* pl, L
         const float M = fmaxf(m, s2);
         const float e = exp2f(m - M);
         const float total = sum * e + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));
-        const bool none = sum == 0.f;   // no key: out 0, lse the sink itself
+        // no key, or a sink above fp32 in base 2 (which leaves the keys nothing): out 0, lse the sink itself
+        const bool none = sum == 0.f || s2 == INFINITY;
         f = none ? 0.f : e / total * ratio;
         if (sum != sum) f = sum;
         if (a.lse != nullptr) a.lse[r] = none ? sink : sum != sum ? sum : (M + log2f(total)) * kLn2;
@@ -1334,7 +1335,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       for (int i = 0; i < 8; ++i) o[i] += shares[x][d + i];
     }
   }
-  const bool none = total == 0.f;
+  const bool none = total == 0.f;   // no key that counts beside the sink
   if (s2 != -INFINITY) total += exp2f(s2 - M);
   const float inv = none ? 0.f : 1.0f / total;
 #pragma unroll

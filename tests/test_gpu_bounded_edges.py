@@ -39,3 +39,42 @@ def test_window_padding_in_prompts_of_many_row_blocks(where, H):
     real = np.flatnonzero(~empty)
     for k in real[::max(1, len(real) // 12)]:
         _check(out[k], lse[k], _window_ref(cache, q, k, pos1, 128, 4, req, sink), "query %d" % k)
+
+
+# --- sinks ---------------------------------------------------------------------------------------
+
+def _check_with_sinks(out, lse, ref, sink):
+    """A head whose sink is +inf: out 0, lse +inf; the others against the definition."""
+    top = np.isposinf(sink)
+    assert not out[cuda(top)].any() and torch.isposinf(lse[cuda(top)]).all()
+    keep = cuda(~top)
+    o, l, bo, bl = ref
+    _check(out[keep], lse[keep], (o[~top], l[~top], bo[~top], bl[~top]))
+
+
+SINKS = np.array([np.inf, np.finfo(np.float32).max, 3e38, 1e38, 200.0, -np.inf, 0.0], np.float32)
+
+
+@pytest.mark.parametrize("pos1,window", [([200, 0, 60], 128), ([20000], 20000)])
+def test_window_sinks_up_to_infinity(pos1, window):
+    """Sinks above any logit, some beyond fp32 in base 2; one list and a split one."""
+    cache = _cache(FP8, pos1, seed=920)
+    q = _queries(len(pos1), len(SINKS), 921)
+    out, lse = _window(cache, q, pos1, window, 4, None, SINKS)
+    assert cskv.device_status() == 0
+    finite = np.where(np.isposinf(SINKS), 0.0, SINKS)
+    for i in range(len(pos1)):
+        _check_with_sinks(out[i], lse[i], _window_ref(cache, q, i, pos1, window, 4, None, finite), SINKS)
+
+
+@pytest.mark.parametrize("swa_fmt", [None, FP8, BF16])
+def test_prefix_sinks_up_to_infinity(swa_fmt):
+    c = _prefix_case(3, len(SINKS), 100, [300, 100, 0], FP8, swa_fmt, seed=922, ctx=[500, 20, 0])
+    c["sink"] = SINKS
+    out, lse = _prefix_run(c)
+    assert cskv.device_status() == 0
+    from test_gpu_bounded_cache import _prefix_keys
+    finite = np.where(np.isposinf(SINKS), 0.0, SINKS)
+    for b in range(3):
+        ref = bounded.attend(c["q"][1][b], max(0, int(c["ctx"][b]) - 1), _prefix_keys(c, b), finite, SCALE)
+        _check_with_sinks(out[b], lse[b], ref, SINKS)
