@@ -16,6 +16,7 @@ constexpr unsigned kRowFormats =
     (1u << CSKV_FMT_BF16) | (1u << CSKV_FMT_FP8_E4M3_E8M0_B32) | (1u << CSKV_FMT_FP4_E2M1_E4M3_B16);
 constexpr int kMaxRows = 1 << 30;  // (query, head) rows of a call
 constexpr int kMaxLen = 1 << 30;   // positions and entries: sums of two stay within 32 bits
+constexpr float kMaxScale = 1e38f; // finite in base 2 (times 1.4427) as well
 
 bool cache_ok(const cskv_paged& c, unsigned formats) {
   if (c.pool == nullptr || !aligned(c.pool, 16)) return false;
@@ -35,7 +36,7 @@ int32_t query_check(const void* q, const cskv_paged& kv, float scale, const floa
   if (q == nullptr || q_rope_cs == nullptr || rows < 1 || rows > kMaxRows / 128 || H < 1 || H > 128)
     return CSKV_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(q_rope_cs, 16)) return CSKV_ERR_INVALID;
-  if (!(scale > 0.0f) || std::isinf(scale) || !rows_ok(kv)) return CSKV_ERR_INVALID;
+  if (!(scale > 0.0f && scale <= kMaxScale) || !rows_ok(kv)) return CSKV_ERR_INVALID;
   return CSKV_OK;
 }
 

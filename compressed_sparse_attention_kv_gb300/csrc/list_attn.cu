@@ -52,6 +52,7 @@
 // warp instructions), the softmax and the barriers between them follow one another, and one block's
 // tile, queries and weights fill the shared memory of an SM.  A row block of one short tile takes 10 us.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "codec.cuh"
@@ -1758,7 +1759,8 @@ ListArgs common_args(const void* q, const cskv_paged& kv, const float* sink, flo
   a.H = H;
   a.out = static_cast<uint8_t*>(out);
   a.lse = lse;
-  a.slack = kSlack / a.scale_log2;
+  // finite for the smallest scales too: the reference of a row without keys is -inf, and has to stay so
+  a.slack = std::min(kSlack / a.scale_log2, FLT_MAX);
   a.spin = spin_limit();
   return a;
 }

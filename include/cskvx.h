@@ -21,7 +21,7 @@
  * bound is cut to it, an index outside its table or pool is skipped; both set
  * CSKV_ERR_BOUNDS on the device.  A workspace belongs to one call at a time.
  * Limits: 2^23 queries or requests of a call (65,535 requests in attn_weights and
- * evict), lengths and positions up to 2^30; softmax_scale is finite and above 0.
+ * evict), lengths and positions up to 2^30; softmax_scale is above 0, 1e38 at most.
  * A wait inside a kernel that runs out (cskv_set_spin_limit) ends the kernel with
  * CSKV_ERR_TIMEOUT on the device; its outputs are then not defined.
  */

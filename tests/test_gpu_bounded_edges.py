@@ -78,3 +78,31 @@ def test_prefix_sinks_up_to_infinity(swa_fmt):
     for b in range(3):
         ref = bounded.attend(c["q"][1][b], max(0, int(c["ctx"][b]) - 1), _prefix_keys(c, b), finite, SCALE)
         _check_with_sinks(out[b], lse[b], ref, SINKS)
+
+
+# --- scales --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale", [1e-45, 1e-40, 1e-38, 2e-38, 1e-30, 1e-3])
+def test_window_smallest_scales(scale):
+    """Logits near 0, whatever the keys: the mean of the visible rows.  The first query's keys are all in
+    the row block's first tile, the last one's all in its second."""
+    L, H = 300, 16
+    cache = _cache(FP8, [L], seed=930)
+    pos1 = np.array([100, 160, 220, 280])
+    q = _queries(4, H, 931)
+    out, lse = cskv.window_attn(q[0].cuda(), cache.to_device(), _i32(pos1), 10, 0, L, None, scale, _cs(pos1),
+                                req_of=_i32([0] * 4), want_lse=True)
+    assert cskv.device_status() == 0
+    for i in range(4):
+        keys = cache.decoded[0][bounded.visible(pos1[i] - 1, 10, 0)]
+        _check(out[i], lse[i], bounded.attend(q[1][i], pos1[i] - 1, keys, None, float(np.float32(scale))))
+
+
+def test_largest_scale():
+    """With zero queries every logit is 0 under the largest scale too."""
+    cache = _cache(BF16, [200], seed=932)
+    q = torch.zeros((1, 4, 512), dtype=torch.bfloat16, device="cuda")
+    out, lse = cskv.window_attn(q, cache.to_device(), _i32([200]), 50, 2, 200, None, 1e38, _cs([200]), want_lse=True)
+    assert cskv.device_status() == 0
+    keys = cache.decoded[0][bounded.visible(199, 50, 2)]
+    _check(out[0], lse[0], bounded.attend(np.zeros((4, 512)), 199, keys, None, 1e38))
