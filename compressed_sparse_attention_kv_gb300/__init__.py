@@ -612,7 +612,9 @@ def evict(caches, acc, n_entries, budget, fixed=0, recent=0, age=None, max_entri
           n_out=None, src=None, workspace=None, stream=None):
     """Cuts each request's entries to `budget` slots: the first `fixed` slots and the `recent`
     newest ages stay, then the largest accumulated weights acc (fp32 [B, capacity]); kept
-    entries from slot `budget` on move into the given-up slots of every cache in `caches`.
+    entries from slot `budget` on move into the given-up slots of every cache in `caches` (with
+    a block table each, unless there is one request; pages that requests share hold slots below
+    `fixed` alone).
     age: int32 [B, capacity] or None (then recent is 0).  acc_out, age_out, n_out None: in
     place.  max_entries None: acc's capacity.  Returns (src int32 [B, budget], n_out, acc_out,
     age_out): slot i now holds the entry of slot src[:, i] (-1: none)."""

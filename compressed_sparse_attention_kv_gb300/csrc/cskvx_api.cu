@@ -126,6 +126,8 @@ int32_t cskvx_evict(const cskv_paged* caches, int32_t ncaches, const float* acc,
     if (!cache_ok(caches[c], 0x1Fu)) return CSKV_ERR_INVALID;
   if (src == nullptr || acc_out == nullptr || n_out == nullptr) return CSKV_ERR_INVALID;
   if (B < 1 || B > 65535 || max_entries < 0 || max_entries > kMaxLen) return CSKV_ERR_INVALID;
+  for (int32_t c = 0; c < ncaches; ++c)   // without a table all requests would move the same rows
+    if (caches[c].block_table == nullptr && B > 1) return CSKV_ERR_INVALID;
   if (budget < 1 || budget > kMaxLen || fixed < 0 || recent < 0 || fixed > budget || recent > budget - fixed)
     return CSKV_ERR_INVALID;
   if (age == nullptr ? (recent != 0 || age_out != nullptr) : (age_out == nullptr || age_stride < max_entries))

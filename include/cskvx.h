@@ -121,8 +121,11 @@ CSKV_API int32_t cskvx_attn_weights(const void* q, cskv_paged main_kv, const int
  * equal, NaN is below everything).  With m = min(n, budget) entries kept, a kept
  * slot below m stays where it is; the kept slots from m on move, in ascending
  * order, into the slots below m that were given up, in ascending order: the fewest
- * rows move, and slots below `fixed` (a shared prefix) are not written.
- * The rows of all `ncaches` caches (1..4; any format, tables of their own) move, and
+ * rows move, and slots below `fixed` are not written: pages that requests share hold slots
+ * below `fixed` alone (a shared prefix of n_prefix entries: fixed >= n_prefix, and the slots
+ * from `fixed` on in pages of the request's own).
+ * The rows of all `ncaches` caches (1..4; any format, tables of their own, NULL only with
+ * B = 1) move, and
  *   src[b, i]      = the slot whose entry slot i now holds (i < m), -1 for m <= i < budget,
  *   acc_out[b, i]  = acc[b, src[b, i]],  age_out likewise, for i < m,
  *   n_out[b]       = m.
