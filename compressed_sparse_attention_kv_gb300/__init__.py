@@ -438,8 +438,10 @@ def _on_stream(f):
     def g(*args, stream=None, **kw):
         import torch
         first = args[0] if args else kw.get("q", kw.get("acc"))
-        if type(first) is not torch.Tensor:
-            first = kw["acc"] if len(args) < 2 else args[1]
+        if not isinstance(first, torch.Tensor):   # evict: its caches
+            first = args[1] if len(args) > 1 else kw.get("acc")
+            if not isinstance(first, torch.Tensor):
+                return f(*args, **kw)             # which says what is missing
         device = first.device
         if stream is not None:
             if device.type == "cuda" and stream.device != device:

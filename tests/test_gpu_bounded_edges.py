@@ -106,3 +106,20 @@ def test_largest_scale():
     assert cskv.device_status() == 0
     keys = cache.decoded[0][bounded.visible(199, 50, 2)]
     _check(out[0], lse[0], bounded.attend(np.zeros((4, 512)), 199, keys, None, 1e38))
+
+
+# --- what a tensor, a cache and a workspace may be ------------------------------------------------
+
+def test_a_parameter_as_queries_and_on_a_stream():
+    pos1 = [300, 70]
+    cache = _cache(FP8, pos1, seed=940)
+    q = _queries(2, 16, 941)
+    a, la = _window(cache, q, pos1, 128, 4, None, None)
+    p = torch.nn.Parameter(q[0].cuda(), requires_grad=False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    args = (cache.to_device(), _i32(pos1), 128, 4, 300, None, SCALE, _cs(pos1))
+    torch.cuda.synchronize()
+    b, lb = cskv.window_attn(p, *args, want_lse=True, stream=side)
+    side.synchronize()
+    assert torch.equal(a, b) and torch.equal(la, lb)
