@@ -47,16 +47,20 @@ extern "C" {
  * One query per request is the decode step; the queries of prompts may come in any
  * order and from any requests (neighbours of one request at neighbouring positions
  * share their keys' loads).  pos1[i] <= 0 marks a padding query: no key, out 0,
- * lse the sink (-inf without one).  A row outside the window and the first rows is
- * never read: its pages may be reused, with any table entry left behind.
+ * lse the sink (-inf without one).  A row that no query sees never counts, whatever it
+ * holds, and no page without a visible row is looked up: pages wholly behind the window
+ * may be reused, with any table entry left behind.  (Where queries of one request lie up
+ * to 64 positions apart, the rows between their windows may be read; they share pages with
+ * visible ones.)
  * q, out: bf16 [T, H, 512]; rows: 512-d, format BF16, FP8 or FP4, its block table
  * [num_reqs, max_pages] (NULL: one flat array of rows for every request);
  * pos1, req_of: int32 [T]; sink: fp32 [H] or NULL; q_rope_cs: fp32 [T, 32, 2];
  * lse: fp32 [T, H] or NULL.  window >= 1, first >= 0, H in [1, 128], every pos1[i]
  * <= max_ctx_len.  A key row with a value that is not finite makes the outputs of
  * the queries that see it NaN, and no others.
- * The query is kept as the sum of two bf16 numbers after its rotation, products run
- * as bf16 tensor-core MMAs with fp32 accumulation, weights enter the second product
+ * The query is kept as the sum of two bf16 numbers after its rotation (logits of N(0, 2)
+ * are exact to about 2e-6, rms), products run as bf16 tensor-core MMAs with fp32
+ * accumulation, weights enter the second product
  * as bf16 and the output is divided by the sum of the rounded ones; lse is made of the
  * fp32 weights; sums, maxima and partial outputs are fp32.  The same call gives the
  * same bits each time.
@@ -75,11 +79,12 @@ CSKV_API int32_t cskvx_window_attn(const void* q, cskv_paged rows, int32_t num_r
  * Request b's keys are its entries j < n_entries[b] of main_kv and, with swa, the
  * rows of its 128-slot window ring (slot r holds a key when r < ctx_len[b]); one
  * softmax with the sink, rotations, out and lse as in cskvx_window_attn.  The
- * entries j < n_prefix are read through request 0's block-table row, once for
- * blocks of up to 64 (request, head) rows; the entries from n_prefix on through
- * the request's own row.  n_prefix need not be a multiple of the page: rows
- * of request 0 stand for everybody's below it.  A request with fewer than n_prefix
- * entries sees those it has.  n_prefix = 0: nothing is shared.  Unlike
+ * entries j < n_prefix are read through request 0's block-table row, once for blocks of
+ * 64 (request, head) rows, or with each request's own entries where that takes less
+ * time; the entries from n_prefix on through the request's own row.  n_prefix need not
+ * be a multiple of the page: rows of request 0 stand for everybody's below it.  A
+ * request with fewer than n_prefix entries sees those it has (request 0's pages hold
+ * all n_prefix of them in any case).  n_prefix = 0: nothing is shared.  Unlike
  * cskv_sparse_decode_attn the number of entries does not follow from a context
  * length, so a cache that cskvx_evict has cut is read as it is.
  * n_entries: int32 [B], 0 .. max_entries (0: none); ctx_len: int32 [B], <= 0: empty

@@ -123,3 +123,32 @@ def test_a_parameter_as_queries_and_on_a_stream():
     b, lb = cskv.window_attn(p, *args, want_lse=True, stream=side)
     side.synchronize()
     assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+# --- what is read ----------------------------------------------------------------------------------
+
+def _rubbish(cache, b, keep):
+    """Rows of request b that are not in `keep` become NaN codes and scales; entries of pages without
+    a row to keep point nowhere."""
+    rb = codecs.row_bytes(cache.fmt, cache.dim)
+    keep = set(int(j) for j in keep)
+    for p in range(cache.max_pages):
+        rows = [s for s in range(64) if 64 * p + s in keep]
+        page = cache.pool[cache.block_table[b, p]]
+        for s in set(range(64)) - set(rows):
+            page[s * rb:(s + 1) * rb] = 0xFF
+        if not rows:
+            cache.block_table[b, p] = -77 if p % 2 else cache.num_pages + 5
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP8, FP4])
+@pytest.mark.parametrize("window,first,H", [(1, 0, 16), (1, 3, 16), (10, 0, 4), (20, 70, 32), (1, 0, 64)])
+def test_window_rows_between_neighbouring_windows_never_count(fmt, window, first, H):
+    """Queries of one request up to 64 positions apart, in either order and with jumps: the rows in
+    the gaps hold NaN, and no page without a visible row is looked up."""
+    L = 1500
+    cache = _cache(fmt, [L], seed=950)
+    pos1 = np.concatenate([100 + 64 * np.arange(5), 1500 - 64 * np.arange(4), [700, 640, 760, 701], [90]])
+    see = set(j for p in pos1 for j in bounded.visible(p - 1, window, first).tolist())
+    _rubbish(cache, 0, see)
+    _window_all(cache, _queries(len(pos1), H, 951), pos1, window, first, np.zeros(len(pos1), np.int64), None)
