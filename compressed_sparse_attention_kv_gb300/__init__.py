@@ -571,8 +571,9 @@ def prefix_decode_attn(q, main_kv, n_entries, n_prefix, max_entries, sink, softm
 def attn_weights(q, main_kv, n_entries, max_entries, softmax_scale, q_rope_cs, lse, acc, decay=1.0, first=0,
                  acc_out=None, stream=None):
     """acc_out[b, j] = decay * acc[b, j] + sum over heads of exp(z - lse) for the entries
-    first <= j < n_entries[b] (lse as prefix_decode_attn gave it); acc, acc_out fp32 [B, >=
-    max_entries], acc_out None: in place.  Returns acc_out."""
+    first <= j < n_entries[b] (lse as prefix_decode_attn gave it), read through each request's
+    own block-table row: first >= that call's n_prefix, unless every request's pages hold the
+    prefix.  acc, acc_out fp32 [B, >= max_entries], acc_out None: in place.  Returns acc_out."""
     import torch
     B, H, dev, pq = _query(q)
     f32 = torch.float32

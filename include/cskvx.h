@@ -105,12 +105,14 @@ CSKV_API int32_t cskvx_prefix_decode_attn(const void* q, cskv_paged main_kv, con
  * cskvx_attn_weights: accumulated attention weights.  For every request b and
  * entry j with first <= j < n_entries[b]:
  *   acc_out[b, j] = decay * acc[b, j] + sum_h exp(z_{b,h,j} - lse[b, h]),
- * z as in cskvx_prefix_decode_attn, lse what that call gave (a row whose lse is -inf
- * adds nothing); other elements of acc_out are left as they are.  acc, acc_out:
- * fp32 [B, stride], stride >= max_entries; acc_out may be acc itself.  first: e.g.
- * the shared prefix, which is not evicted.  decay finite.  H in [1, 128].  The rotated
- * query is kept as three bf16 numbers and a logit summed in four parts (two above 64 heads),
- * so that logits are exact to about 2e-7 of N(0, 2).
+ * z of the entry's row in request b's own pages, lse what cskvx_prefix_decode_attn gave (a
+ * row whose lse is -inf adds nothing); other elements of acc_out are left as they are.
+ * After a call with n_prefix > 0 take first >= n_prefix: entries below n_prefix were
+ * attended to in request 0's pages, and have their weights here only where every
+ * request's table row and pages hold the prefix too.  acc, acc_out: fp32 [B, stride],
+ * stride >= max_entries; acc_out may be acc itself.  decay finite.  H in [1, 128].  The
+ * rotated query is kept as three bf16 numbers and a logit summed in four parts (two above
+ * 64 heads), so that logits of N(0, 2) are exact to about 2e-7 (rms).
  * ------------------------------------------------------------------------ */
 CSKV_API int32_t cskvx_attn_weights(const void* q, cskv_paged main_kv, const int32_t* n_entries, int32_t first,
                                     int32_t max_entries, float softmax_scale, const float* q_rope_cs,

@@ -152,3 +152,28 @@ def test_window_rows_between_neighbouring_windows_never_count(fmt, window, first
     see = set(j for p in pos1 for j in bounded.visible(p - 1, window, first).tolist())
     _rubbish(cache, 0, see)
     _window_all(cache, _queries(len(pos1), H, 951), pos1, window, first, np.zeros(len(pos1), np.int64), None)
+
+
+@pytest.mark.parametrize("B,H,P,n", [(3, 16, 70, 200), (3, 64, 200, 330), (2, 128, 1, 140), (5, 8, 1000, 1064)])
+def test_weights_behind_a_prefix_that_ends_inside_a_page(B, H, P, n):
+    """The prefix lies in request 0's pages alone: the other requests' rows below it hold NaN, their table
+    entries of whole prefix pages point nowhere.  The attention and the weights from n_prefix on are
+    the same as with rows everywhere; the weights below it would be of each request's own rows."""
+    c = _prefix_case(B, H, P, [n - 13 * b if n - 13 * b > P else P for b in range(B)], FP8, None, seed=960 + P)
+    cache = c["cache"]
+    for b in range(1, B):      # not the pages of request 0: rows below P of the page the prefix ends in
+        edge = cache.block_table[b, P // 64]
+        cache.pool[edge, :P % 64 * 528] = 0xFF
+        cache.block_table[b, :P // 64] = -5
+    out, lse = _prefix_run(c)
+    _prefix_all(c, out, lse)
+    acc = torch.full((B, n), 0.5, device="cuda")
+    got = cskv.attn_weights(c["q"][0].cuda(), cache.to_device(), _i32(c["n"]), n, SCALE, _cs(c["ctx"]), lse, acc,
+                            decay=0.5, first=P).cpu().numpy().astype(np.float64)
+    assert cskv.device_status() == 0
+    l = lse.cpu().numpy()
+    for b in range(B):
+        m = int(c["n"][b])
+        w, bound = bounded.weights(c["q"][1][b], int(c["ctx"][b]) - 1, cache.decoded[b][P:m], l[b], SCALE)
+        assert np.all(np.abs(got[b, P:m] - 0.25 - w) <= bound + 3 * 2.0 ** -24 * (0.25 + w))
+        assert np.all(got[b, :P] == 0.5) and np.all(got[b, m:] == 0.5)
