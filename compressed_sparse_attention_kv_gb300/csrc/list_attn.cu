@@ -1362,8 +1362,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // rows' bytes on their way wait for lines of what shared memory leaves of L1: 32 x 8192 FP8 entries
 // of 64 heads took 52 us with eight slots (28 KB of L1) and 45 us with four (64 KB).
 // Two, where the queries of more than 112 heads leave room for no more.  The weights are fp32: with
-// a rotated query in three bf16 numbers and the S product in four sums (two above 64 heads) logits
-// of N(0, 2) are off by 2.3e-7 (rms); in two numbers and one sum they were off by 2.2e-6, and no faster.
+// a rotated query in three bf16 numbers and the S product in four sums logits of N(0, 2) are off by
+// 2.3e-7 (rms), in the two sums that 128 columns leave room for by 6.4e-7; in two numbers and one sum
+// they were off by 2.1e-6, and no faster.
 // ---------------------------------------------------------------------------
 constexpr int kTileSums = 256;   // TMEM columns of a tile: 4 sums of up to 64 columns, or 2 of up to 128
 __device__ __forceinline__ int tile_sums(int nq) { return nq <= 64 ? 4 : 2; }

@@ -112,7 +112,7 @@ CSKV_API int32_t cskvx_prefix_decode_attn(const void* q, cskv_paged main_kv, con
  * request's table row and pages hold the prefix too.  acc, acc_out: fp32 [B, stride],
  * stride >= max_entries; acc_out may be acc itself.  decay finite.  H in [1, 128].  The
  * rotated query is kept as three bf16 numbers and a logit summed in four parts (two above
- * 64 heads), so that logits of N(0, 2) are exact to about 2e-7 (rms).
+ * 64 heads), so that logits of N(0, 2) are exact to about 2e-7 (rms; 6e-7 above 64 heads).
  * ------------------------------------------------------------------------ */
 CSKV_API int32_t cskvx_attn_weights(const void* q, cskv_paged main_kv, const int32_t* n_entries, int32_t first,
                                     int32_t max_entries, float softmax_scale, const float* q_rope_cs,
