@@ -177,3 +177,111 @@ def test_weights_behind_a_prefix_that_ends_inside_a_page(B, H, P, n):
         w, bound = bounded.weights(c["q"][1][b], int(c["ctx"][b]) - 1, cache.decoded[b][P:m], l[b], SCALE)
         assert np.all(np.abs(got[b, P:m] - 0.25 - w) <= bound + 3 * 2.0 ** -24 * (0.25 + w))
         assert np.all(got[b, :P] == 0.5) and np.all(got[b, m:] == 0.5)
+
+
+def _flat(cache):
+    """Request 0's pages in order as a cache without a table."""
+    pool = cache.pool[cache.block_table[0]]
+    return cskv.PagedCache(cuda(pool), None, cache.fmt, cache.dim)
+
+
+def _long_pages(cache, extra=48 + 16 * 1024):
+    """The same cache with pages further apart, NaN codes between them."""
+    pool = np.full((cache.num_pages, cache.page_bytes + extra), 0xFF, np.uint8)
+    pool[:, :cache.page_bytes] = cache.pool
+    return cskv.PagedCache(cuda(pool), cuda(cache.block_table), cache.fmt, cache.dim)
+
+
+@pytest.mark.parametrize("other", [_flat, _long_pages])
+@pytest.mark.parametrize("fmt", [BF16, FP8, FP4])
+def test_caches_without_a_table_and_with_long_pages(other, fmt):
+    """The same bits as with one table and 64-row pages, from all four calls (one request's rows)."""
+    L, T, H = 700, 90, 16
+    cache = _cache(fmt, [L], seed=970)
+    a, b = cache.to_device(), other(cache)
+    q = _queries(T, H, 971)[0].cuda()
+    pos1 = np.random.default_rng(972).integers(1, L + 1, T)
+    w = [cskv.window_attn(q, x, _i32(pos1), 100, 5, L, None, SCALE, _cs(pos1), req_of=_i32([0] * T), want_lse=True)
+         for x in (a, b)]
+    p = [cskv.prefix_decode_attn(q[:1], x, _i32([L]), 130, L, None, SCALE, _cs(pos1[:1]), want_lse=True) for x in (a, b)]
+    acc = [cskv.attn_weights(q[:1], x, _i32([L]), L, SCALE, _cs(pos1[:1]), p[0][1], torch.zeros((1, L), device="cuda"))
+           for x in (a, b)]
+    for x in (w, p):
+        assert torch.equal(x[0][0], x[1][0]) and torch.equal(x[0][1], x[1][1])
+    assert torch.equal(acc[0], acc[1]) and (acc[0] > 0).all()
+    for i in range(0, T, 9):
+        _check(w[1][0][i], w[1][1][i], _window_ref(cache, (None, q.float().cpu().numpy().astype(np.float64)), i, pos1,
+                                                   100, 5, [0] * T, None))
+    before = b.pool.clone()
+    src = [cskv.evict([x], acc[0].clone(), _i32([L]), 300, fixed=10)[0] for x in (a, b)]
+    assert torch.equal(src[0], src[1]) and cskv.device_status() == 0
+    rows = lambda c, pool: pool[:, :cache.page_bytes].reshape(pool.shape[0], 64, -1)[
+        c.block_table[0].long() if c.block_table is not None else torch.arange(pool.shape[0], device="cuda")].flatten(0, 1)
+    assert torch.equal(rows(a, a.pool), rows(b, b.pool))
+    assert torch.equal(rows(b, b.pool)[:300], rows(b, before)[src[1][0].long()])
+    assert torch.equal(b.pool[:, cache.page_bytes:], before[:, cache.page_bytes:])
+
+
+def test_a_flat_cache_of_several_requests():
+    """Without a table every request of a batch attends to the same rows."""
+    cache = _cache(FP8, [500], seed=975)
+    flat, n = _flat(cache), np.array([500, 3, 0, 257])
+    q = _queries(4, 64, 976)
+    out, lse = cskv.prefix_decode_attn(q[0].cuda(), flat, _i32(n), 100, 500, None, SCALE, _cs(n), want_lse=True)
+    wo, wl = cskv.window_attn(q[0].cuda(), flat, _i32(n), 5000, 0, 500, None, SCALE, _cs(n), want_lse=True)
+    acc = cskv.attn_weights(q[0].cuda(), flat, _i32(n), 500, SCALE, _cs(n), lse, torch.zeros((4, 500), device="cuda"))
+    assert cskv.device_status() == 0
+    for b in range(4):
+        ref = bounded.attend(q[1][b], max(0, n[b] - 1), cache.decoded[0][:n[b]], None, SCALE)
+        _check(out[b], lse[b], ref)
+        _check(wo[b], wl[b], ref)
+        if n[b]:
+            w, bound = bounded.weights(q[1][b], int(n[b]) - 1, cache.decoded[0][:n[b]], lse[b].cpu().numpy(), SCALE)
+            assert np.all(np.abs(acc[b, :n[b]].cpu().numpy() - w) <= bound + 2.0 ** -24 * w)
+        assert not acc[b, n[b]:].any()
+
+
+def test_workspaces_of_the_caller():
+    """Of the stated size inside a larger buffer, full of NaN: the same results, nothing beyond it written."""
+    c = _prefix_case(3, 16, 500, [3000, 2800, 600], FP8, BF16, seed=980)
+    pos1 = [20000, 300]
+    cache = _cache(FP8, pos1, seed=981)
+    q = _queries(2, 16, 982)
+    e_acc = torch.rand((2, 3000), device="cuda")
+    e_cache = _cache(FP8, [3000, 3000], seed=983)
+
+    def calls(ws):
+        o = [_prefix_run(c, **ws(cskv.prefix_decode_attn_workspace_size(3, 16, 500, 3000, True))),
+             _window(cache, q, pos1, 20000, 4, None, None, **ws(cskv.window_attn_workspace_size(2, 16, 20000, 20000, 4)))]
+        d = e_cache.to_device()
+        o.append(cskv.evict([d], e_acc.clone(), _i32([3000, 2500]), 1400, fixed=3,
+                            **ws(cskv.evict_workspace_size(2, 3000, 1400)))[:3] + (d.pool,))
+        return [t for x in o for t in x]
+
+    guards = []
+
+    def mine(nbytes):
+        assert nbytes > 0
+        buf = torch.full((nbytes + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+        guards.append((buf, nbytes))
+        return dict(workspace=buf[256:256 + nbytes])
+
+    want, got = calls(lambda nbytes: {}), calls(mine)
+    assert cskv.device_status() == 0 and len(guards) == 3
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    for buf, nbytes in guards:
+        assert (buf[:256] == 0xFF).all() and (buf[256 + nbytes:] == 0xFF).all()
+    with pytest.raises(cskv.CskvError):
+        _prefix_run(c, workspace=guards[0][0][256:256 + guards[0][1] - 256])
+    with pytest.raises(cskv.CskvError):
+        _prefix_run(c, workspace=guards[0][0][128:])
+
+
+@pytest.mark.parametrize("B,H", [(3, 16), (3, 64), (33, 8)])
+def test_prefix_longer_than_the_first_request(B, H):
+    """Request 0's pages hold the prefix, though it sees a part of it (or nothing) itself."""
+    c = _prefix_case(B, H, 200, [50] + [300 - b for b in range(1, B)], FP8, FP8, seed=985)
+    _prefix_all(c, *_prefix_run(c))
+    c["n"][0] = 0
+    _prefix_all(c, *_prefix_run(c))
