@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   }
 }
 
-// The rows of many pairs: a warp per pair, four pairs at a time per block and warp.
+// The rows of many pairs: a warp moves four pairs, one after the other.
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictArgs a) {
   grid_dep_wait();
   const int b = blockIdx.y, lane = threadIdx.x & 31;

@@ -11,9 +11,10 @@
 // stay below 2^kSlack, and O need not be touched.  Parts of a row's keys that different
 // blocks take are joined by attn_join_kernel in a fixed order.
 //
-// What bounds it.  A tile of 128 keys for 64 rows is 33.5 MFLOP on 67 KB of FP8 rows: the
-// tensor core and the shared-memory reads of its operands, with the dequantisation of the
-// tile (65,536 values) beside it; short windows are bound by the queries and outputs.
+// What bounds it.  A tile of 128 keys for 64 rows is 16.8 MFLOP (1.3 us of one SM's tensor core) on
+// 67 KB of FP8 rows (1.5 us of an SM's share of HBM, where no other block reads them): either, with
+// the dequantisation of the tile (65,536 values) and the softmax of 8,192 logits beside them, which
+// take longer than both; short windows are bound by the queries and outputs.
 //
 // The tiling.  One block holds 64 rows: 64 / H queries of a request (or one query's heads),
 // or 64 consecutive (request, head) rows over a shared prefix.  Both products run with the
@@ -38,12 +39,15 @@
 // and sixteen warps hide the latency of either better than eight warps for each.
 //
 // Roundings: the rotated query is kept as hi + lo, two bf16 numbers (the lo part of the 64
-// rotated dims is a ninth chunk of Q), so that logits and log-sum-exp are fp32-accurate;
-// P is rounded to bf16 (2^-9 relative at most, the operand type of the product), and the output
+// rotated dims is a ninth chunk of Q), so that logits of N(0, 2) and the log-sum-exp are off by
+// 2.1e-6 (rms: 1.7e-6 the two numbers, the rest the tensor core's sums; one number 1.2e-3);
+// P is rounded to bf16 (2^-8 relative at most, the operand type of the product), and the output
 // divided by the sum of the rounded weights, so that the roundings of a few large ones cancel
 // (outputs of 237 keys and N(0, 2) logits are off by 1.9e-3 after their own rounding to bf16, by
-// 2.1e-3 over the exact sum, up to 2.6e-3 in single requests; plain fp32 1.7e-3); the log-sum-exp
-// has the exact weights' sum; partial outputs, sums and maxima stay fp32.
+// 2.1e-3 over the exact sum, up to 2.6e-3 in single requests; plain fp32 1.7e-3; the second sum costs
+// a prompt chunk 5 %, 732 us without it); the log-sum-exp has the exact weights' sum; what the
+// rounding took from a sum, 2^-8 of it at most, is handed on as bf16 (2^-16 of the sum); partial
+// outputs, sums and maxima stay fp32.
 //
 // Measured: a prompt chunk of 8,192 tokens, 64 heads, a window of 128 and 4 first rows (FP8)
 // 768 us; 32 single tokens over 4,160 FP8 keys, 64 heads, 56 us (1.3 TB/s); 64 requests of 64 heads
@@ -729,7 +733,7 @@ __device__ __forceinline__ bool look_up_tile(const ListArgs& a, ListSmem* sm, co
   return true;
 }
 
-// The block's query rows into the K-major chunks of Q (rows nq apart); warps 0-7.  The rows
+// The block's query rows into the K-major chunks of Q (rows nq apart); warps 0-15.  The rows
 // come in by asynchronous copies; the last 64 dims are then rotated in place, chunk 8 holds
 // the second bf16 of each rotated value.
 __device__ __forceinline__ void request_queries(const ListArgs& a, int r0, int nr, int nq, uint8_t* qtile) {
