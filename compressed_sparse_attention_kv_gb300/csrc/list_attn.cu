@@ -51,7 +51,7 @@
 //
 // Measured: a prompt chunk of 8,192 tokens, 64 heads, a window of 128 and 4 first rows (FP8)
 // 768 us; 32 single tokens over 4,160 FP8 keys, 64 heads, 56 us (1.3 TB/s); 64 requests of 64 heads
-// over a prefix of 8,192 FP4 entries and 512 of their own 138 us (0.53 PFLOP/s).  A tile takes 3.5
+// over a prefix of 8,192 FP4 entries and 512 of their own 142 us (0.51 PFLOP/s).  A tile takes 3.5
 // to 4 us, of which the products are 1.5: its rows' loads, their conversion (about 7,000
 // warp instructions), the softmax and the barriers between them follow one another, and one block's
 // tile, queries and weights fill the shared memory of an SM.  A row block of one short tile takes 10 us.
