@@ -285,3 +285,31 @@ def test_prefix_longer_than_the_first_request(B, H):
     _prefix_all(c, *_prefix_run(c))
     c["n"][0] = 0
     _prefix_all(c, *_prefix_run(c))
+
+
+def test_weights_of_heads_whose_sink_takes_everything():
+    """A log-sum-exp of +inf or far above the logits adds nothing, as the formula says."""
+    c = _prefix_case(2, 4, 0, [300, 20], FP8, None, seed=990, with_sink=False)
+    lse = np.array([[np.inf, 3e38, -np.inf, 2.0], [-np.inf, np.inf, 5.0, 6.0]], np.float32)
+    acc = torch.zeros((2, 300), device="cuda")
+    cskv.attn_weights(c["q"][0].cuda(), c["cache"].to_device(), _i32(c["n"]), 300, SCALE, _cs(c["ctx"]), cuda(lse), acc)
+    assert cskv.device_status() == 0
+    got = acc.cpu().numpy()
+    for b, heads in ((0, [3]), (1, [2, 3])):
+        m = int(c["n"][b])
+        w, bound = bounded.weights(c["q"][1][b][heads], int(c["ctx"][b]) - 1, c["cache"].decoded[b][:m], lse[b, heads], SCALE)
+        assert np.all(np.abs(got[b, :m] - w) <= bound + 2.0 ** -24 * w) and not got[b, m:].any()
+
+
+def test_calls_whose_bounds_are_zero():
+    """No position and no entry at all: outputs 0, log-sum-exps the sinks, nothing accumulated or moved."""
+    cache = _cache(FP8, [64, 64], seed=991).to_device()
+    q, z, sink = _queries(2, 16, 992)[0].cuda(), _i32([0, 0]), torch.arange(16, device="cuda", dtype=torch.float32)
+    acc = torch.full((2, 8), 3.0, device="cuda")
+    for out, lse in (cskv.window_attn(q, cache, z, 5, 0, 0, sink, SCALE, _cs([1, 1]), want_lse=True),
+                     cskv.prefix_decode_attn(q, cache, z, 0, 0, sink, SCALE, _cs([1, 1]), want_lse=True)):
+        assert not out.any() and torch.equal(lse, sink.expand(2, 16))
+    cskv.attn_weights(q, cache, z, 0, SCALE, _cs([1, 1]), lse, acc)
+    src, n, _, _ = cskv.evict([cache], acc, z, 4, max_entries=0)
+    assert cskv.device_status() == 0
+    assert (acc == 3.0).all() and (src == -1).all() and n.tolist() == [0, 0]
