@@ -23,6 +23,13 @@ and, from include/cskvx.h (prefix ``cskvx_``), attention over bounded and shared
     prefix_decode_attn(...)  a decode batch whose requests share their first entries
     attn_weights(...)        each entry's accumulated attention weight
     evict(...)               cuts each request's entries to a budget by that weight
+
+and, from include/cskvs.h (prefix ``cskvs_``), one step of a server, from lengths to attention:
+
+    plan_step(...)           block tables, slots and positions of a step's tokens, from lengths
+    rope_cs(...)             the (cos, sin) table of positions on the GPU, one axis or several
+    norm_rope(...)           norms of queries and rows with the rotation, rows coded into a cache
+    chunk_attn(...)          new tokens' attention over all visible entries and a window
 """
 
 import ctypes
@@ -437,7 +444,9 @@ def _on_stream(f):
     @functools.wraps(f)
     def g(*args, stream=None, **kw):
         import torch
-        first = args[0] if args else kw.get("q", kw.get("acc"))
+        first = args[0] if args else kw.get("q", kw.get("acc", kw.get("ctx_len", kw.get("positions", kw.get("jobs")))))
+        if isinstance(first, (list, tuple)) and first and isinstance(first[0], dict):   # norm_rope: its jobs
+            first = first[0].get("x")
         if not isinstance(first, torch.Tensor):   # evict: its caches
             first = args[1] if len(args) > 1 else kw.get("acc")
             if not isinstance(first, torch.Tensor):
@@ -649,6 +658,251 @@ def evict(caches, acc, n_entries, budget, fixed=0, recent=0, age=None, max_entri
     _check(L.cskvx_evict(arr, len(caches), pa, wa, pg, wg, pn, B, most, budget, fixed, recent, px, pb, wb, ph, wh, pm,
                          pw, nw, _raw_stream(dev)), "cskvx_evict")
     return src, n_out, acc_out, age_out
+
+
+class PageTable:
+    """The pages of a batch and the free ones: `block_table` int32 [B, max_pages]; `free_pages`
+    int32 [capacity], a ring of free pages' ids; `state` int32 [4]: where the ring starts, how
+    many ids it holds, and (written by plan_step) how many pages a step lacked, 0."""
+
+    def __init__(self, block_table, free_pages, state):
+        import torch
+        for t, n in ((block_table, "block_table"), (free_pages, "free_pages"), (state, "state")):
+            _need(t, torch.int32, n)
+        if block_table.dim() != 2 or free_pages.dim() != 1 or tuple(state.shape) != (4,):
+            raise ValueError("block_table, free_pages and state must have shapes (B, max_pages), (capacity,) and (4,)")
+        if free_pages.device != block_table.device or state.device != block_table.device:
+            raise ValueError("free_pages and state must be on %s" % block_table.device)
+        self.block_table = block_table
+        self.free_pages = free_pages
+        self.state = state
+
+    @classmethod
+    def allocate(cls, B, max_pages, num_pages, device="cuda"):
+        """No request has a page, all num_pages are free."""
+        import torch
+        i32 = torch.int32
+        state = torch.zeros(4, dtype=i32, device=device)
+        state[1] = num_pages
+        return cls(torch.full((B, max_pages), -1, dtype=i32, device=device),
+                   torch.arange(num_pages, dtype=i32, device=device), state)
+
+
+class StepMaps:
+    """What plan_step writes, for B requests and T places for tokens: cu_new int32 [B + 1],
+    new_len, first_row, n_rows int32 [B], req_of, pos1 int32 [T], slot int64 [T] (None without
+    pages), ring_slot int64 [T] (None without a ring).  Made once, it may serve every step."""
+
+    def __init__(self, B, T, pages=True, ring=False, device="cuda"):
+        import torch
+        i32, i64 = torch.int32, torch.int64
+        # one allocation, the 64-bit maps first
+        n64 = (T if pages else 0) + (T if ring else 0)
+        buf = torch.empty(8 * n64 + 4 * (4 * B + 1 + 2 * T), dtype=torch.uint8, device=device)
+        wide = buf[:8 * n64].view(i64)
+        self.slot = wide[:T] if pages else None
+        self.ring_slot = wide[n64 - T:] if ring else None
+        self.cu_new, self.new_len, self.first_row, self.n_rows, self.req_of, self.pos1 = \
+            buf[8 * n64:].view(i32).split((B + 1, B, B, B, T, T))
+        self.B, self.T, self.device = B, T, buf.device
+
+
+@_on_stream
+def plan_step(ctx_len, n_new, T, pages=None, ratio=1, ring_rows=0, shared_pages=None, state_out=None, out=None,
+              workspace=None, stream=None):
+    """Block tables and slot maps of a step on the GPU: request b has ctx_len[b] tokens (int32 [B])
+    and gets n_new[b] more (0: none, < 0: the request ends and gives its pages back).  T: places
+    for tokens; those behind the last one are padding (pos1 0, req_of and slots -1).  pages (a
+    PageTable) gets pages from its ring for the rows floor(length / ratio) that its requests come
+    to have; state_out int32 [4]: its state after the step (None: in place).  ring_rows > 0: the
+    rows of a window ring per request.  shared_pages int32 [B]: leading pages that a request
+    does not give back.  Returns the StepMaps (`out`, or a new one)."""
+    import torch
+    i32 = torch.int32
+    if ctx_len.dim() != 1 or not ctx_len.is_cuda:
+        _need(ctx_len, i32, "ctx_len")
+        raise ValueError("ctx_len must have shape (requests,), got %s" % (tuple(ctx_len.shape),))
+    B, dev = ctx_len.shape[0], ctx_len.device
+    pc = _take("ctx_len", ctx_len, i32, (B,), dev)
+    pn = _take("n_new", n_new, i32, (B,), dev)
+    psh = _take("shared_pages", shared_pages, i32, (B,), dev)
+    pt = pf = ps = po = None
+    per = cap = 0
+    if pages is not None:
+        bt = pages.block_table
+        per, cap = bt.shape[1], pages.free_pages.shape[0]
+        pt = _take("block_table", bt, i32, (B, per), dev)
+        pf, ps = pages.free_pages.data_ptr(), pages.state.data_ptr()
+        po = ps if state_out is None else _take("state_out", state_out, i32, (4,), dev)
+    elif shared_pages is not None or state_out is not None:
+        raise ValueError("shared_pages and state_out need pages")
+    if out is None:
+        out = StepMaps(B, T, pages is not None, ring_rows > 0, dev)
+    elif out.B != B or out.T != T or out.device != dev or (out.slot is None) != (pages is None) or \
+            (out.ring_slot is None) != (ring_rows <= 0):
+        raise ValueError("out must be a StepMaps of %d requests and %d tokens on %s, with slots as pages and ring_rows "
+                         "say" % (B, T, dev))
+    L = _lib.lib()
+    need = 0 if workspace is not None else L.cskvs_plan_step_workspace_size(B)
+    workspace, pw, nw = _workspace(workspace, need, dev)
+    _check(L.cskvs_plan_step(pc, pn, B, ratio, T, ring_rows, pt, per, psh, pf, cap, ps, po, out.cu_new.data_ptr(),
+                             out.new_len.data_ptr(), out.first_row.data_ptr(), out.n_rows.data_ptr(),
+                             out.req_of.data_ptr(), out.pos1.data_ptr(), _ptr(out.slot), _ptr(out.ring_slot), pw, nw,
+                             _raw_stream(dev)), "cskvs_plan_step")
+    return out
+
+
+class RopePlan:
+    """Speeds of the 32 rotated pairs (theta, yarn as in rope_table) and the axis of positions
+    that each follows: sections (n_0, n_1, ...), pairs of axis 0 first, then of axis 1, ...
+    (32 in all), or axis_of, 32 axes, pair by pair; neither: one axis.  Made once and kept."""
+
+    def __init__(self, theta=160000.0, yarn=None, sections=None, axis_of=None):
+        if sections is not None:
+            if axis_of is not None:
+                raise ValueError("sections and axis_of say the same")
+            if any(n < 0 for n in sections) or sum(sections) != 32:
+                raise ValueError("sections must add up to 32 pairs, got %s" % (tuple(sections),))
+            axis_of = [a for a, n in enumerate(sections) for _ in range(n)]
+        self.axes = 1 if axis_of is None else len(sections) if sections is not None else max(axis_of) + 1
+        if axis_of is not None and (len(axis_of) != 32 or min(axis_of) < 0 or self.axes > 4):
+            raise ValueError("axis_of must be 32 axes of at most four, got %s" % (axis_of,))
+        y = yarn or {}
+        self.struct = _lib.RopePlan()
+        axis = None if axis_of is None else (ctypes.c_uint8 * 32)(*axis_of)
+        st = _lib.lib().cskvs_rope_init(ctypes.byref(self.struct), float(theta), float(y.get("factor", 1.0)),
+                                        float(y.get("original", 1.0)), float(y.get("beta_fast", 1.0)),
+                                        float(y.get("beta_slow", 1.0)), self.axes,
+                                        None if axis is None else ctypes.addressof(axis))
+        _check(st, "cskvs_rope_init")
+        self.ref = ctypes.byref(self.struct)
+
+
+@_on_stream
+def rope_cs(positions, plan, shift=0, out=None, stream=None):
+    """fp32 [T, 32, 2] (cos, sin) of positions + shift on the GPU (int32 [T], or [axes, T] for a
+    RopePlan of several axes): the table that compress, norm_rope and the attention calls take."""
+    import torch
+    shape = positions.shape
+    if len(shape) == 1 and plan.axes == 1:
+        T = shape[0]
+    elif len(shape) == 2 and shape[0] == plan.axes:
+        T = shape[1]
+    else:
+        raise ValueError("positions must have shape (%d, T), got %s" % (plan.axes, tuple(shape)))
+    if positions.dtype is not torch.int32 or not positions.is_cuda or not positions.is_contiguous():
+        _need(positions, torch.int32, "positions")
+    dev = positions.device
+    if out is None:
+        out = torch.empty((T, 32, 2), dtype=torch.float32, device=dev)
+        po = out.data_ptr()
+    else:
+        po = _take("out", out, torch.float32, (T, 32, 2), dev)
+    _check(_lib.lib().cskvs_rope_cs(plan.ref, positions.data_ptr(), T, shift, T, po, _raw_stream(dev)), "cskvs_rope_cs")
+    return out
+
+
+def _heads(name, t, T, device):
+    """(address, stride between tokens) of a bf16 [T, H, dim] tensor whose heads are contiguous."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype is not torch.bfloat16:
+        raise ValueError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if t.device != device or t.dim() != 3 or t.shape[0] != T:
+        raise ValueError("%s must have shape (%d, heads, dim) on %s, got %s on %s"
+                         % (name, T, device, tuple(t.shape), t.device))
+    s = t.stride()
+    H, dim = t.shape[1], t.shape[2]
+    if (s[2] != 1 and dim > 1) or (s[1] != dim and H > 1):
+        raise ValueError("%s's heads must be contiguous, got strides %s" % (name, s))
+    return t.data_ptr(), s[0] if T > 1 else H * dim
+
+
+_NORM_ARRAYS = [_lib.NormJob * max(1, n) for n in range(5)]
+
+
+@_on_stream
+def norm_rope(jobs, rope_cs=None, stream=None):
+    """Norms, rotation and coding of a step's queries and rows in one launch.  jobs: up to four
+    dicts of x (bf16 [T, H, dim], dim 128 or 512, tokens any stride apart), norm (False), norm_w
+    (fp32 [dim] or None), eps (1e-6), rotate (False), and either out (bf16 [T, H, dim], None: a
+    new tensor; may be x) or cache (a PagedCache of that dim, H = 1) with slot (int64 [T],
+    physical rows, < 0: skipped).  rope_cs: fp32 [T, 32, 2] (needed where a job rotates).
+    Returns the list of outs (None for jobs with a cache)."""
+    import torch
+    if not 1 <= len(jobs) <= 4:
+        raise ValueError("1 to 4 jobs, got %d" % len(jobs))
+    x = jobs[0]["x"]
+    T, dev = x.shape[0], x.device
+    pc = _take("rope_cs", rope_cs, torch.float32, (T, 32, 2), dev)
+    arr, outs = _NORM_ARRAYS[len(jobs)](), []
+    for a, j in zip(arr, jobs):
+        x = j["x"]
+        a.x, a.x_stride = _heads("x", x, T, dev)
+        a.H, a.dim = x.shape[1], x.shape[2]
+        w = j.get("norm_w")
+        a.norm, a.eps, a.rotate = bool(j.get("norm", w is not None)), j.get("eps", 1e-6), bool(j.get("rotate"))
+        a.norm_w = _take("norm_w", w, torch.float32, (a.dim,), dev)
+        cache, out = j.get("cache"), j.get("out")
+        if cache is not None:
+            if out is not None:
+                raise ValueError("a job has out or cache")
+            if j.get("slot") is None:
+                raise ValueError("cache needs slot")
+            a.slot = _take("slot", j["slot"], torch.int64, (T,), dev)
+            a.cache = _cache_on("cache", cache, 0, dev)
+        else:
+            if out is None:
+                out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+            elif out.shape != x.shape:
+                raise ValueError("out must have shape %s, got %s" % (tuple(x.shape), tuple(out.shape)))
+            a.out, a.out_stride = _heads("out", out, T, dev)
+        outs.append(out)
+    _check(_lib.lib().cskvs_norm_rope(arr, len(jobs), pc, T, _raw_stream(dev)), "cskvs_norm_rope")
+    return outs
+
+
+def chunk_attn_max_keys(R, T, max_entries, window, max_ctx_len):
+    """A bound of the keys that chunk_attn decodes, whatever the lengths."""
+    return int(_lib.lib().cskvs_chunk_attn_max_keys(R, T, max_entries, window, max_ctx_len))
+
+
+def chunk_attn_workspace_size(R, T, H, max_keys):
+    return int(_lib.lib().cskvs_chunk_attn_workspace_size(R, T, H, max_keys))
+
+
+@_on_stream
+def chunk_attn(q, cu_q, ctx_len, entries, ratio, max_entries, max_ctx_len, sink, softmax_scale, q_rope_cs,
+               n_entries=None, rows=None, window=0, max_keys=None, out=None, lse=None, want_lse=False, workspace=None,
+               stream=None):
+    """Attention of chunks of new tokens: the queries cu_q[r] .. cu_q[r + 1] - 1 of q (bf16
+    [T, H, 512]) are the last tokens of request r, whose length is ctx_len[r]; the one at position
+    t sees the entries j < floor((t + 1) / ratio) of `entries` (a PagedCache; ratio 0: all
+    n_entries[r]; never more than n_entries[r], if given) and, with rows (a PagedCache of raw
+    rows by position), the last `window` rows up to its own.  max_keys: a tighter bound than
+    chunk_attn_max_keys (the workspace holds 1 KB for each).  Returns (out bf16 [T, H, 512], lse
+    fp32 [T, H] or None)."""
+    import torch
+    T, H, dev, pq = _query(q)
+    i32, f32 = torch.int32, torch.float32
+    R = cu_q.shape[0] - 1
+    pu = _take("cu_q", cu_q, i32, (R + 1,), dev)
+    px = _take("ctx_len", ctx_len, i32, (R,), dev)
+    pn = _take("n_entries", n_entries, i32, (R,), dev)
+    ps = _take("sink", sink, f32, (H,), dev)
+    pc = _take("q_rope_cs", q_rope_cs, f32, (T, 32, 2), dev)
+    de = None if entries is None else ctypes.byref(_cache_on("entries", entries, R, dev))
+    dr = None if rows is None else ctypes.byref(_cache_on("rows", rows, R, dev))
+    out, lse, po, pl = _outputs(q, T, H, dev, out, lse, want_lse)
+    L = _lib.lib()
+    if max_keys is None:
+        max_keys = L.cskvs_chunk_attn_max_keys(R, T, max_entries if entries is not None else 0, window, max_ctx_len)
+    need = 0 if workspace is not None else L.cskvs_chunk_attn_workspace_size(R, T, H, max_keys)
+    workspace, pw, nw = _workspace(workspace, need, dev)
+    _check(L.cskvs_chunk_attn(pq, pu, px, R, T, H, de, ratio, pn, max_entries, dr, window, max_ctx_len, ps,
+                              softmax_scale, pc, po, pl, max_keys, pw, nw, _raw_stream(dev)), "cskvs_chunk_attn")
+    return out, lse
 
 
 DEFAULT_SCALE = 1.0 / math.sqrt(512.0)

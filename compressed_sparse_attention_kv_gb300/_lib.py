@@ -1,4 +1,5 @@
-"""ctypes view of libcskv.so (the C ABI declared in include/cskv.h and include/cskvx.h)."""
+"""ctypes view of libcskv.so (the C ABI declared in include/cskv.h, include/cskvx.h and
+include/cskvs.h)."""
 
 import ctypes
 import os
@@ -103,6 +104,33 @@ class DecodeLayerArgs(ctypes.Structure):
     ]
 
 
+class RopePlan(ctypes.Structure):
+    """struct cskvs_rope_plan."""
+    _fields_ = [
+        ("speed", (ctypes.c_uint32 * 3) * 32),
+        ("axis", ctypes.c_uint8 * 32),
+        ("axes", c_int32),
+    ]
+
+
+class NormJob(ctypes.Structure):
+    """struct cskvs_norm_job."""
+    _fields_ = [
+        ("x", c_void_p),
+        ("x_stride", c_int64),
+        ("H", c_int32),
+        ("dim", c_int32),
+        ("norm", c_int32),
+        ("norm_w", c_void_p),
+        ("eps", c_float),
+        ("rotate", c_int32),
+        ("out", c_void_p),
+        ("out_stride", c_int64),
+        ("cache", Paged),
+        ("slot", c_void_p),
+    ]
+
+
 # name -> (restype, argtypes); every symbol include/cskv.h declares
 SIGNATURES = {
     "cskv_row_bytes": (c_size_t, [c_int32, c_int32]),
@@ -153,6 +181,23 @@ EXT_SIGNATURES = {
                               c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
 }
 
+# every symbol include/cskvs.h declares
+STEP_SIGNATURES = {
+    "cskvs_plan_step_workspace_size": (c_size_t, [c_int32]),
+    "cskvs_plan_step": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int32, c_void_p,
+                                  c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "cskvs_rope_init": (c_int32, [ctypes.POINTER(RopePlan), ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                  ctypes.c_double, ctypes.c_double, c_int32, c_void_p]),
+    "cskvs_rope_cs": (c_int32, [ctypes.POINTER(RopePlan), c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p]),
+    "cskvs_norm_rope": (c_int32, [ctypes.POINTER(NormJob), c_int32, c_void_p, c_int32, c_void_p]),
+    "cskvs_chunk_attn_max_keys": (c_int64, [c_int32, c_int32, c_int32, c_int32, c_int32]),
+    "cskvs_chunk_attn_workspace_size": (c_size_t, [c_int32, c_int32, c_int32, c_int64]),
+    "cskvs_chunk_attn": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, ctypes.POINTER(Paged),
+                                   c_int32, c_void_p, c_int32, ctypes.POINTER(Paged), c_int32, c_int32, c_void_p,
+                                   c_float, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+}
+
 _lib = None
 
 
@@ -166,7 +211,7 @@ def lib():
                 "`python -c 'import __graft_entry__ as g; g.build()'` "
                 "(there is no CPU fallback for the decode path)" % LIB_PATH)
         h = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in list(SIGNATURES.items()) + list(EXT_SIGNATURES.items()):
+        for name, (res, args) in list(SIGNATURES.items()) + list(EXT_SIGNATURES.items()) + list(STEP_SIGNATURES.items()):
             f = getattr(h, name)
             f.restype = res
             f.argtypes = args

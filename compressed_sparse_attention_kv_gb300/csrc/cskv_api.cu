@@ -159,6 +159,31 @@ static cudaError_t stage_copy(void* dst, const void* src, size_t n, bool to_devi
 
 using namespace cskv;
 
+namespace cskv {
+bool rope_speeds(double theta, double yarn_factor, double yarn_original, double beta_fast, double beta_slow,
+                 double (&f)[32]) {
+  if (!(theta > 1.0)) return false;
+  const bool yarn = yarn_factor > 1.0;
+  if (yarn && !(yarn_original > 0.0 && beta_fast > 0.0 && beta_slow > 0.0)) return false;
+  constexpr int kPairs = 32, kRopeDim = 64;
+  for (int k = 0; k < kPairs; ++k) f[k] = std::pow(theta, -2.0 * k / kRopeDim);
+  if (yarn) {
+    // the pair that turns `beta` times over the original length (the YaRN correction range)
+    auto kb = [&](double beta) {
+      return kRopeDim * std::log(yarn_original / (2.0 * M_PI * beta)) / (2.0 * std::log(theta));
+    };
+    const int lo = std::max(static_cast<int>(std::floor(kb(beta_fast))), 0);
+    const int hi = std::min(static_cast<int>(std::ceil(kb(beta_slow))), kPairs - 1);
+    const double span = std::max(static_cast<double>(hi - lo), 1e-3);
+    for (int k = 0; k < kPairs; ++k) {
+      const double ramp = std::min(std::max((k - lo) / span, 0.0), 1.0);
+      f[k] = f[k] / yarn_factor * ramp + f[k] * (1.0 - ramp);
+    }
+  }
+  return true;
+}
+}  // namespace cskv
+
 extern "C" {
 
 size_t cskv_row_bytes(int32_t fmt, int32_t dim) {
@@ -205,25 +230,9 @@ void cskv_set_timing_events(void* begin, void* end) {
 int32_t cskv_rope_table(const int64_t* positions, int32_t n, double theta, double yarn_factor,
                         double yarn_original, double beta_fast, double beta_slow, float* out) {
   if (n < 0 || (n > 0 && (positions == nullptr || out == nullptr))) return CSKV_ERR_INVALID;
-  if (!(theta > 1.0)) return CSKV_ERR_INVALID;
-  const bool yarn = yarn_factor > 1.0;
-  if (yarn && !(yarn_original > 0.0 && beta_fast > 0.0 && beta_slow > 0.0)) return CSKV_ERR_INVALID;
-  constexpr int kPairs = 32, kRopeDim = 64;
+  constexpr int kPairs = 32;
   double f[kPairs];
-  for (int k = 0; k < kPairs; ++k) f[k] = std::pow(theta, -2.0 * k / kRopeDim);
-  if (yarn) {
-    // the pair that turns `beta` times over the original length (the YaRN correction range)
-    auto kb = [&](double beta) {
-      return kRopeDim * std::log(yarn_original / (2.0 * M_PI * beta)) / (2.0 * std::log(theta));
-    };
-    const int lo = std::max(static_cast<int>(std::floor(kb(beta_fast))), 0);
-    const int hi = std::min(static_cast<int>(std::ceil(kb(beta_slow))), kPairs - 1);
-    const double span = std::max(static_cast<double>(hi - lo), 1e-3);
-    for (int k = 0; k < kPairs; ++k) {
-      const double ramp = std::min(std::max((k - lo) / span, 0.0), 1.0);
-      f[k] = f[k] / yarn_factor * ramp + f[k] * (1.0 - ramp);
-    }
-  }
+  if (!rope_speeds(theta, yarn_factor, yarn_original, beta_fast, beta_slow, f)) return CSKV_ERR_INVALID;
   for (int32_t i = 0; i < n; ++i) {
     const double p = static_cast<double>(positions[i]);
     for (int k = 0; k < kPairs; ++k) {
@@ -238,7 +247,7 @@ int32_t cskv_rope_table(const int64_t* positions, int32_t n, double theta, doubl
 int32_t cskv_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return CSKV_ERR_CUDA;
   const unsigned int bits = take_err_compress() | take_err_index() | take_err_attention() |
-                            take_err_list_attn() | take_err_evict();
+                            take_err_list_attn() | take_err_evict() | take_err_step() | take_err_chunk_attn();
   if (bits & (1u << CSKV_ERR_TIMEOUT)) return CSKV_ERR_TIMEOUT;
   if (bits & (1u << CSKV_ERR_BOUNDS)) return CSKV_ERR_BOUNDS;
   if (bits) return CSKV_ERR_CUDA;

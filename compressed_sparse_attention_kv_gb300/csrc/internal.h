@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/cskv.h"
+#include "../../include/cskvs.h"
 
 namespace cskv {
 
@@ -117,10 +118,32 @@ cudaError_t launch_evict(const cskv_paged* caches, int ncaches, const float* acc
                          int32_t* age_out, long long age_out_stride, int32_t* n_out, void* workspace,
                          cudaStream_t stream);
 
+// include/cskvs.h
+// the pairs' angles per position, as cskv_rope_table has them; false: bad arguments
+bool rope_speeds(double theta, double yarn_factor, double yarn_original, double beta_fast, double beta_slow,
+                 double (&f)[32]);
+size_t plan_step_workspace_bytes(int B);
+cudaError_t launch_plan_step(const int32_t* ctx_len, const int32_t* n_new, int B, int ratio, int T, int ring_rows,
+                             int32_t* table, int max_pages, const int32_t* shared, int32_t* free_pages, int capacity,
+                             const int32_t* state, int32_t* state_out, int32_t* cu_new, int32_t* new_len,
+                             int32_t* first_row, int32_t* n_rows, int32_t* req_of, int32_t* pos1, int64_t* slot,
+                             int64_t* ring_slot, void* workspace, cudaStream_t stream);
+cudaError_t launch_rope_cs(const cskvs_rope_plan& plan, const int32_t* pos, int64_t axis_stride, int shift, int T,
+                           float* out, cudaStream_t stream);
+cudaError_t launch_norm_rope(const cskvs_norm_job* jobs, int njobs, const float* rope_cs, int T, cudaStream_t stream);
+size_t chunk_attn_workspace_bytes(int R, int T, int H, int64_t max_keys);
+cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t* ctx_len, int R, int T, int H,
+                              const cskv_paged* entries, int ratio, const int32_t* n_entries, int max_entries,
+                              const cskv_paged* rows, int window, int max_ctx, const float* sink, float scale,
+                              const float* q_rope, void* out, float* lse, int64_t max_keys, void* workspace,
+                              cudaStream_t stream);
+
 unsigned int take_err_compress();
 unsigned int take_err_index();
 unsigned int take_err_attention();
 unsigned int take_err_list_attn();
 unsigned int take_err_evict();
+unsigned int take_err_step();
+unsigned int take_err_chunk_attn();
 
 }  // namespace cskv

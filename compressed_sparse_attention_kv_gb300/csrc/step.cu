@@ -1,0 +1,618 @@
+// What a step of new tokens needs before its attention (include/cskvs.h): block tables and slot
+// maps from the requests' lengths, the (cos, sin) table of positions on the device, and the
+// norms of queries and rows with the rotation and the coding in the same pass.
+#include <algorithm>
+#include <cmath>
+
+#include "codec.cuh"
+#include "internal.h"
+
+namespace cskv {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// cskvs_plan_step.  Three prefix sums over the requests (their new tokens, the pages they need,
+// the pages they give back), then every token finds its request among the sums and every new
+// page its place in the ring of free pages.  Nothing is carried between blocks but the sums, so
+// a page's place follows from its number alone: the k-th new page of the step is the k-th of the
+// ring, and the j-th page given back goes j places behind the ring's last one.  The two stretches
+// do not meet, so that blocks read and write the ring without waiting for one another.
+// Bound: latency (24 bytes a token).  One block does a small step in one launch; beyond
+// that one block makes the sums and a launch of many blocks the maps.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+constexpr int kMapThreads = 256;
+constexpr int kStaged = 2048;            // requests of a block's tokens that fit into shared memory
+constexpr int kMaxLen = 1 << 30;
+
+struct PlanRecord {        // of a request
+  int tok0;                // its first token
+  int ctx;                 // its length before the step
+  int first, last;         // its pages before and after the step
+  int used, own;           // a request that ends: pages [own, used) are given back
+  long long take, give;    // the number of its first new page, and of its first page given back
+};
+struct PlanHead {
+  int tokens;              // new tokens of the step
+  int head, count;         // the ring before the step
+  int pad;
+};
+
+struct PlanArgs {
+  const int32_t* ctx_len;
+  const int32_t* n_new;
+  int B, ratio, T, ring_rows;
+  int32_t* table;
+  int max_pages;
+  const int32_t* shared;
+  int32_t* free_pages;
+  int capacity;
+  const int32_t* state;
+  int32_t* state_out;
+  int32_t* cu_new;
+  int32_t* new_len;
+  int32_t* first_row;
+  int32_t* n_rows;
+  int32_t* req_of;
+  int32_t* pos1;
+  long long* slot;
+  long long* ring_slot;
+  PlanHead* head;
+  PlanRecord* rec;
+};
+
+__device__ __forceinline__ int pages_of(int rows) { return (rows + kPageRows - 1) / kPageRows; }
+
+// Inclusive sums of a block's values; `total` gets the last one.
+__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    long long x = lane < warps ? part[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    part[lane] = x;
+  }
+  __syncthreads();
+  if (warp > 0) v += part[warp - 1];
+  *total = part[warps - 1];
+  __syncthreads();   // part is used again
+  return v;
+}
+
+__device__ __forceinline__ int bounded_len(int n) {
+  if (n >= 0 && n <= kMaxLen) return n;
+  set_err(CSKV_ERR_BOUNDS);
+  return n < 0 ? 0 : kMaxLen;
+}
+
+// The sums, the lengths and the ring's new state; one block.
+__device__ void plan_sums(const PlanArgs& a) {
+  __shared__ long long part[32];
+  long long tok = 0, take = 0, give = 0;   // before this round of requests
+  int head = a.state != nullptr ? a.state[0] : 0, count = a.state != nullptr ? a.state[1] : 0;
+  if (a.state != nullptr && (head < 0 || head >= a.capacity || count < 0 || count > a.capacity)) {
+    if (threadIdx.x == 0) set_err(CSKV_ERR_BOUNDS);
+    head = head < 0 || head >= a.capacity ? 0 : head;
+    count = max(0, min(count, a.capacity));
+  }
+  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    const bool there = b < a.B;
+    int ctx = 0, n = 0;
+    bool ends = false;
+    if (there) {
+      ctx = bounded_len(a.ctx_len[b]);
+      n = a.n_new[b];
+      ends = n < 0;
+      n = ends ? 0 : n;
+      if (n > kMaxLen - ctx) { set_err(CSKV_ERR_BOUNDS); n = kMaxLen - ctx; }
+    }
+    long long total;
+    const long long upto = tok + block_scan(n, part, &total);
+    const int tok0 = static_cast<int>(min(upto - n, static_cast<long long>(a.T)));
+    if (upto > a.T && n > 0) { set_err(CSKV_ERR_BOUNDS); n = min(n, a.T - tok0); }
+    tok += total;
+    const int len = ends ? 0 : ctx + n;
+    const int row0 = ends ? 0 : ctx / a.ratio, row1 = len / a.ratio;
+    PlanRecord r;
+    r.tok0 = tok0;
+    r.ctx = ctx;
+    r.first = pages_of(row0);
+    r.last = pages_of(row1);
+    r.used = ends ? pages_of(ctx / a.ratio) : 0;
+    if (a.table != nullptr && max(r.last, r.used) > a.max_pages) {
+      set_err(CSKV_ERR_BOUNDS);
+      r.first = min(r.first, a.max_pages);
+      r.last = min(r.last, a.max_pages);
+      r.used = min(r.used, a.max_pages);
+    }
+    r.own = there && ends && a.shared != nullptr ? max(0, min(a.shared[b], r.used)) : 0;
+    const int need = there && a.table != nullptr ? r.last - r.first : 0;
+    const int back = there && a.table != nullptr ? r.used - r.own : 0;
+    r.take = take + block_scan(need, part, &total) - need;
+    take += total;
+    r.give = give + block_scan(back, part, &total) - back;
+    give += total;
+    if (there) {
+      a.rec[b] = r;
+      a.cu_new[b] = tok0;
+      a.new_len[b] = len;
+      a.first_row[b] = row0;
+      a.n_rows[b] = row1;
+    }
+  }
+  if (threadIdx.x == 0) {
+    const int tokens = static_cast<int>(min(tok, static_cast<long long>(a.T)));
+    a.cu_new[a.B] = tokens;
+    *a.head = PlanHead{tokens, head, count, 0};
+    if (a.table != nullptr) {
+      const int taken = static_cast<int>(min(take, static_cast<long long>(count)));
+      if (give > a.capacity - count) { set_err(CSKV_ERR_BOUNDS); give = a.capacity - count; }
+      a.state_out[0] = static_cast<int>((static_cast<long long>(head) + taken) % a.capacity);
+      a.state_out[1] = static_cast<int>(count - taken + give);
+      a.state_out[2] = static_cast<int>(min(take - taken, static_cast<long long>(INT32_MAX)));
+      a.state_out[3] = 0;
+    }
+  }
+}
+
+// The id of the step's k-th new page, -1: none is left.
+__device__ __forceinline__ int new_page(const PlanArgs& a, const PlanHead& h, long long k) {
+  return k < h.count ? a.free_pages[(h.head + k) % a.capacity] : -1;
+}
+
+// The maps of tokens [i0, i0 + stride * ...) and the pages of requests w0, w0 + warps, ...
+__device__ void plan_tokens(const PlanArgs& a, const PlanHead& h, int block, int blocks, int* staged) {
+  for (long long base = static_cast<long long>(block) * blockDim.x; base < a.T;
+       base += static_cast<long long>(blocks) * blockDim.x) {
+    const int i0 = static_cast<int>(base), i = i0 + threadIdx.x;
+    // the requests of the block's tokens: [lo, hi], the last ones whose first token is not behind them
+    const int end = min(i0 + static_cast<int>(blockDim.x), h.tokens) - 1;
+    int lo = 0, hi = 0;
+    if (i0 < h.tokens) {
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {   // 32 places at a time; every warp for itself
+        const int key = side == 0 ? i0 : end;
+        int from = 0, n = a.B;                 // the last b in [from, from + n) with tok0 <= key
+        while (n > 1) {
+          const int step = (n + 31) / 32, at = from + static_cast<int>(threadIdx.x & 31) * step;
+          const bool le = at < from + n && a.cu_new[at] <= key;
+          const int k = __popc(__ballot_sync(0xFFFFFFFFu, le)) - 1;   // (from itself is one)
+          const int next = from + k * step;
+          n = min(step, from + n - next);
+          from = next;
+        }
+        (side == 0 ? lo : hi) = from;
+      }
+    }
+    const bool stage = hi - lo < kStaged && hi > lo;
+    __syncthreads();   // the tokens before are mapped
+    if (stage)
+      for (int x = threadIdx.x; x <= hi - lo; x += blockDim.x) staged[x] = a.cu_new[lo + x];
+    __syncthreads();
+    if (i >= a.T) continue;
+    int req = -1, p1 = 0;
+    long long slot = -1, ring = -1;
+    if (i < h.tokens) {
+      int b = lo, n = hi - lo + 1;
+      while (n > 1) {
+        const int half = n / 2, at = b + half;
+        const bool le = (stage ? staged[at - lo] : a.cu_new[at]) <= i;
+        b = le ? at : b;
+        n = le ? n - half : half;
+      }
+      const PlanRecord r = a.rec[b];
+      const int next = b + 1 <= hi && stage ? staged[b + 1 - lo] : a.cu_new[b + 1];
+      const int p = r.ctx + (i - r.tok0);
+      req = b;
+      p1 = p + 1;
+      if (a.table != nullptr && p1 % a.ratio == 0) {
+        const int row = p1 / a.ratio - 1, lp = row / kPageRows;
+        int page = -1;
+        if (lp < a.max_pages)
+          page = lp < r.first ? a.table[static_cast<long long>(b) * a.max_pages + lp] : new_page(a, h, r.take + lp - r.first);
+        if (page >= 0) slot = static_cast<long long>(page) * kPageRows + row % kPageRows;
+      }
+      if (a.ring_rows > 0 && next - i <= a.ring_rows) ring = static_cast<long long>(b) * a.ring_rows + p % a.ring_rows;
+    }
+    a.req_of[i] = req;
+    a.pos1[i] = p1;
+    if (a.slot != nullptr) a.slot[i] = slot;
+    if (a.ring_slot != nullptr) a.ring_slot[i] = ring;
+  }
+}
+
+__device__ void plan_pages(const PlanArgs& a, const PlanHead& h, int warp, int warps) {
+  if (a.table == nullptr) return;
+  const int lane = threadIdx.x & 31;
+  for (int b = warp; b < a.B; b += warps) {
+    const PlanRecord r = a.rec[b];
+    int32_t* line = a.table + static_cast<long long>(b) * a.max_pages;
+    for (int lp = r.first + lane; lp < r.last; lp += 32) line[lp] = new_page(a, h, r.take + lp - r.first);
+    for (int lp = r.own + lane; lp < r.used; lp += 32) {
+      const long long j = r.give + lp - r.own;
+      if (j < a.capacity - h.count) a.free_pages[(static_cast<long long>(h.head) + h.count + j) % a.capacity] = line[lp];
+    }
+  }
+}
+
+template <bool kWhole>   // kWhole: the maps too
+__global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const __grid_constant__ PlanArgs a) {
+  grid_dep_launch();
+  plan_sums(a);
+  if constexpr (kWhole) {
+    __shared__ int staged[kStaged];
+    __syncthreads();   // (the records are this block's own writes)
+    const PlanHead h = *a.head;
+    plan_pages(a, h, threadIdx.x >> 5, kPlanThreads / 32);
+    plan_tokens(a, h, 0, 1, staged);
+  }
+}
+
+__global__ void __launch_bounds__(kMapThreads) plan_maps_kernel(const __grid_constant__ PlanArgs a) {
+  __shared__ int staged[kStaged];
+  grid_dep_wait();
+  const PlanHead h = *a.head;
+  plan_pages(a, h, (blockIdx.x * kMapThreads + threadIdx.x) >> 5, gridDim.x * (kMapThreads / 32));
+  plan_tokens(a, h, blockIdx.x, gridDim.x, staged);
+}
+
+// ---------------------------------------------------------------------------
+// cskvs_rope_cs.  The angle in turns is position * (f / 2 pi), of which the fraction alone
+// matters: a 32-bit position times a 96-bit fraction, kept to 64 bits, is exact to 2^-63 turns at
+// any position, in two integer products (double precision has a 64th of the fp32 rate here, and
+// its reduction by 2 pi would take most of it).  What is left of the nearest quarter turn, in
+// [-1/8, 1/8], becomes two floats; times 2 pi that is the angle t + d, |t| <= pi / 4, and
+//   sin = t + (t^3 (-1/6 + t^2/120 - ...) + d),  cos = (1 - t^2/2) + (t^4 (1/24 - ...) - t d + what
+// the rounding of 1 - t^2/2 lost): Taylor polynomials to t^11 and t^12 (remainders 7e-12 and
+// 1e-12), the error below one ulp of the result.
+// Bound: writes, 256 bytes a position, beside about 50 instructions a pair.
+// ---------------------------------------------------------------------------
+constexpr int kRopeThreads = 256;
+constexpr int kRopeAtOnce = kRopeThreads / 16;   // positions of a block at a time: a thread has two pairs
+
+struct RopeArgs {
+  cskvs_rope_plan plan;
+  const int32_t* pos;
+  long long axis_stride;
+  int shift, T;
+  float* out;
+};
+
+__device__ __forceinline__ float2 cos_sin_of_turns(uint64_t t) {
+  const uint32_t q = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
+  const int64_t r = static_cast<int64_t>(t - (static_cast<uint64_t>(q) << 62));   // [-2^61, 2^61) of 2^64
+  const float rh = __ll2float_rn(r);
+  const float rl = __ll2float_rn(r - static_cast<int64_t>(rh));   // (rh is a whole number below 2^62)
+  constexpr float kTurn = 0x1.921fb6p-62f, kTurnLow = -0x1.777a5cp-87f;   // 2 pi / 2^64
+  const float x = rh * kTurn;
+  const float d = fmaf(rh, kTurn, -x) + fmaf(rh, kTurnLow, rl * kTurn);
+  const float s = x * x, sl = fmaf(x, x, -s);
+  float p = -1.0f / 39916800.0f;
+  p = fmaf(p, s, 1.0f / 362880.0f);
+  p = fmaf(p, s, -1.0f / 5040.0f);
+  p = fmaf(p, s, 1.0f / 120.0f);
+  p = fmaf(p, s, -1.0f / 6.0f);
+  const float sn = x + fmaf(x * s, p, d);
+  float c = 1.0f / 479001600.0f;
+  c = fmaf(c, s, -1.0f / 3628800.0f);
+  c = fmaf(c, s, 1.0f / 40320.0f);
+  c = fmaf(c, s, -1.0f / 720.0f);
+  c = fmaf(c, s, 1.0f / 24.0f);
+  const float w = fmaf(-0.5f, s, 1.0f);
+  const float lost = fmaf(-0.5f, s, 1.0f - w) - fmaf(x, d, 0.5f * sl);
+  const float cs = w + fmaf(s * s, c, lost);
+  const float a = (q & 1) ? sn : cs, b = (q & 1) ? cs : sn;
+  return make_float2(((q + 1) & 2) ? -a : a, (q & 2) ? -b : b);
+}
+
+__global__ void __launch_bounds__(kRopeThreads) rope_cs_kernel(const __grid_constant__ RopeArgs a) {
+  const int two = threadIdx.x & 15;
+  uint64_t speed[2];
+  uint32_t low[2];
+  const int32_t* pos[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint32_t* w = a.plan.speed[2 * two + u];
+    speed[u] = static_cast<uint64_t>(w[0]) << 32 | w[1];
+    low[u] = w[2];
+    pos[u] = a.pos + a.plan.axis[2 * two + u] * a.axis_stride;
+  }
+  for (long long i = static_cast<long long>(blockIdx.x) * kRopeAtOnce + (threadIdx.x >> 4); i < a.T;
+       i += static_cast<long long>(gridDim.x) * kRopeAtOnce) {
+    float2 r[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const long long p = static_cast<long long>(__ldg(pos[u] + i)) + a.shift;
+      const uint64_t m = static_cast<uint64_t>(p < 0 ? -p : p);
+      uint64_t t = m * speed[u] + ((m * low[u]) >> 32);
+      r[u] = cos_sin_of_turns(p < 0 ? 0 - t : t);
+    }
+    reinterpret_cast<float4*>(a.out)[i * 16 + two] = make_float4(r[0].x, r[0].y, r[1].x, r[1].y);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// cskvs_norm_rope
+// ---------------------------------------------------------------------------
+constexpr int kNormThreads = 256;
+constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kMaxNormJobs = 4;
+
+struct NormJob {
+  const uint8_t* x;
+  long long x_stride;   // bytes
+  int H, dim, norm, rotate;
+  const float* norm_w;
+  float eps;
+  uint8_t* out;
+  long long out_stride;
+  cskv_paged cache;
+  int row_bytes;
+  const long long* slot;
+  int per_token;        // warps of a token
+};
+struct NormArgs {
+  NormJob job[kMaxNormJobs];
+  long long first[kMaxNormJobs + 1];   // warps of the jobs before
+  int njobs;
+  int T;
+  const float* rope_cs;
+};
+
+__device__ __forceinline__ void norm16(const NormJob& j, float (&y)[16], int c0, int lanes) {
+  // the sum of squares: neighbours first, then the lanes of the head
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(__fmul_rn(y[2 * i], y[2 * i]), __fmul_rn(y[2 * i + 1], y[2 * i + 1]));
+#pragma unroll
+  for (int w = 4; w >= 1; w >>= 1)
+#pragma unroll
+    for (int i = 0; i < w; ++i) v[i] = __fadd_rn(v[2 * i], v[2 * i + 1]);
+  float ss = v[0];
+  for (int o = 1; o < lanes; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
+  const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(j.dim)), j.eps)));
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (j.norm_w != nullptr) w = __ldg(reinterpret_cast<const float4*>(j.norm_w + c0 + i));
+    y[i] = __fmul_rn(__fmul_rn(y[i], r), w.x);
+    y[i + 1] = __fmul_rn(__fmul_rn(y[i + 1], r), w.y);
+    y[i + 2] = __fmul_rn(__fmul_rn(y[i + 2], r), w.z);
+    y[i + 3] = __fmul_rn(__fmul_rn(y[i + 3], r), w.w);
+  }
+}
+
+__device__ __forceinline__ void turn2(float& y0, float& y1, float c, float s) {
+  const float z0 = __fsub_rn(__fmul_rn(y0, c), __fmul_rn(y1, s));
+  y1 = __fadd_rn(__fmul_rn(y0, s), __fmul_rn(y1, c));
+  y0 = z0;
+}
+
+// Heads of one token: a lane has 16 dims of a head, 32 lanes (dim 512) or 8 (dim 128) a head.
+__device__ __forceinline__ void norm_heads(const NormArgs& a, const NormJob& j, long long w) {
+  const int lane = threadIdx.x & 31;
+  const long long t = w / j.per_token;
+  const int lanes = j.dim / 16, at_once = 32 / lanes;
+  const int c0 = (lane & (lanes - 1)) * 16;
+  const int h = static_cast<int>(w - t * j.per_token) * at_once + lane / lanes;
+  const bool there = h < j.H;
+  float y[16];
+  uint4 v[2] = {};
+  if (there) {
+    const uint4* from = reinterpret_cast<const uint4*>(j.x + t * j.x_stride + (static_cast<long long>(h) * j.dim + c0) * 2);
+    v[0] = from[0];
+    v[1] = from[1];
+  }
+  const bool turn = j.rotate && c0 >= j.dim - 64;
+  float4 cs[4];
+  if (turn) {
+    const float4* from = reinterpret_cast<const float4*>(a.rope_cs + t * 64 + (c0 - (j.dim - 64)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = __ldg(from + i);
+  }
+  const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[2 * i] = bf16lo(u[i]);
+    y[2 * i + 1] = bf16hi(u[i]);
+  }
+  if (j.norm) norm16(j, y, c0, lanes);
+  if (turn) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn2(y[4 * i], y[4 * i + 1], cs[i].x, cs[i].y);
+      turn2(y[4 * i + 2], y[4 * i + 3], cs[i].z, cs[i].w);
+    }
+  }
+  if (there) {
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+      o[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    uint4* to = reinterpret_cast<uint4*>(j.out + t * j.out_stride + (static_cast<long long>(h) * j.dim + c0) * 2);
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// A row of D dims into the cache: a lane has four neighbouring dims of every 128.
+template <int D>
+__device__ __forceinline__ void norm_row(const NormArgs& a, const NormJob& j, long long t) {
+  constexpr int N = D / 128;
+  const int lane = threadIdx.x & 31;
+  const long long slot = j.slot[t];
+  if (slot < 0) return;   // (the whole warp)
+  const long long page = slot / kPageRows;
+  if (page >= j.cache.num_pages) {
+    if (lane == 0) set_err(CSKV_ERR_BOUNDS);
+    return;
+  }
+  const RowPtr dst = page_row(j.cache, page, static_cast<int>(slot % kPageRows), j.row_bytes);
+  float4 y[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = load_bf16x4(j.x + t * j.x_stride + (128 * i + 4 * lane) * 2);
+  if (j.norm) {
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = __fadd_rn(__fadd_rn(__fmul_rn(y[i].x, y[i].x), __fmul_rn(y[i].y, y[i].y)),
+                       __fadd_rn(__fmul_rn(y[i].z, y[i].z), __fmul_rn(y[i].w, y[i].w)));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], o));
+    }
+    float ss = v[0];
+    if constexpr (N == 4) ss = __fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3]));
+    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(D)), j.eps)));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (j.norm_w != nullptr) w = __ldg(reinterpret_cast<const float4*>(j.norm_w + 128 * i + 4 * lane));
+      y[i].x = __fmul_rn(__fmul_rn(y[i].x, r), w.x);
+      y[i].y = __fmul_rn(__fmul_rn(y[i].y, r), w.y);
+      y[i].z = __fmul_rn(__fmul_rn(y[i].z, r), w.z);
+      y[i].w = __fmul_rn(__fmul_rn(y[i].w, r), w.w);
+    }
+  }
+  if (j.rotate && lane >= 16) {   // dims 64 .. 127 of the last 128
+    const float4 cs = __ldg(reinterpret_cast<const float4*>(a.rope_cs + t * 64) + (lane - 16));
+    turn2(y[N - 1].x, y[N - 1].y, cs.x, cs.y);
+    turn2(y[N - 1].z, y[N - 1].w, cs.z, cs.w);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) store_row_values(y[i], 32 * i + lane, j.cache.fmt, D, dst, true);
+}
+
+__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
+  const long long w = static_cast<long long>(blockIdx.x) * kNormWarps + (threadIdx.x >> 5);
+  int k = 0;
+  while (k + 1 < a.njobs && w >= a.first[k + 1]) ++k;
+  if (w >= a.first[a.njobs]) return;
+  const NormJob& j = a.job[k];
+  if (j.slot == nullptr) norm_heads(a, j, w - a.first[k]);
+  else if (j.dim == 512) norm_row<512>(a, j, w - a.first[k]);
+  else norm_row<128>(a, j, w - a.first[k]);
+}
+
+inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t plan_step_workspace_bytes(int B) { return 256 + a256(sizeof(PlanRecord) * static_cast<size_t>(B)); }
+
+cudaError_t launch_plan_step(const int32_t* ctx_len, const int32_t* n_new, int B, int ratio, int T, int ring_rows,
+                             int32_t* table, int max_pages, const int32_t* shared, int32_t* free_pages, int capacity,
+                             const int32_t* state, int32_t* state_out, int32_t* cu_new, int32_t* new_len,
+                             int32_t* first_row, int32_t* n_rows, int32_t* req_of, int32_t* pos1, int64_t* slot,
+                             int64_t* ring_slot, void* workspace, cudaStream_t stream) {
+  PlanArgs a = {};
+  a.ctx_len = ctx_len;
+  a.n_new = n_new;
+  a.B = B;
+  a.ratio = ratio;
+  a.T = T;
+  a.ring_rows = ring_slot != nullptr ? ring_rows : 0;
+  a.table = table;
+  a.max_pages = max_pages;
+  a.shared = shared;
+  a.free_pages = free_pages;
+  a.capacity = capacity;
+  a.state = table != nullptr ? state : nullptr;
+  a.state_out = state_out;
+  a.cu_new = cu_new;
+  a.new_len = new_len;
+  a.first_row = first_row;
+  a.n_rows = n_rows;
+  a.req_of = req_of;
+  a.pos1 = pos1;
+  a.slot = reinterpret_cast<long long*>(slot);
+  a.ring_slot = reinterpret_cast<long long*>(ring_slot);
+  a.head = static_cast<PlanHead*>(workspace);
+  a.rec = reinterpret_cast<PlanRecord*>(static_cast<uint8_t*>(workspace) + 256);
+  const bool whole = T <= 2048 && B <= 1024;
+  if (whole) {
+    plan_sums_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  plan_sums_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int blocks = std::max((T + kMapThreads - 1) / kMapThreads, (B + kMapThreads / 32 - 1) / (kMapThreads / 32));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(std::max(blocks, 1), 152 * 8)));
+  cfg.blockDim = dim3(kMapThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, plan_maps_kernel, a);
+}
+
+cudaError_t launch_rope_cs(const cskvs_rope_plan& plan, const int32_t* pos, int64_t axis_stride, int shift, int T,
+                           float* out, cudaStream_t stream) {
+  if (T == 0) return cudaSuccess;
+  RopeArgs a;
+  a.plan = plan;
+  a.pos = pos;
+  a.axis_stride = axis_stride;
+  a.shift = shift;
+  a.T = T;
+  a.out = out;
+  const int blocks = std::min((T + kRopeAtOnce - 1) / kRopeAtOnce, 152 * 8);
+  rope_cs_kernel<<<blocks, kRopeThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_norm_rope(const cskvs_norm_job* jobs, int njobs, const float* rope_cs, int T, cudaStream_t stream) {
+  if (T == 0) return cudaSuccess;
+  NormArgs a = {};
+  a.njobs = njobs;
+  a.T = T;
+  a.rope_cs = rope_cs;
+  for (int i = 0; i < njobs; ++i) {
+    const cskvs_norm_job& s = jobs[i];
+    NormJob& j = a.job[i];
+    j.x = static_cast<const uint8_t*>(s.x);
+    j.x_stride = s.x_stride * 2;
+    j.H = s.H;
+    j.dim = s.dim;
+    j.norm = s.norm != 0;
+    j.norm_w = s.norm_w;
+    j.eps = s.eps;
+    j.rotate = s.rotate != 0;
+    j.slot = reinterpret_cast<const long long*>(s.slot);
+    j.per_token = 1;
+    if (s.slot != nullptr) {
+      j.cache = s.cache;
+      j.row_bytes = static_cast<int>(cskv_row_bytes(s.cache.fmt, s.cache.dim));
+    } else {
+      j.out = static_cast<uint8_t*>(s.out);
+      j.out_stride = s.out_stride * 2;
+      j.per_token = s.dim == 512 ? s.H : (s.H + 3) / 4;
+    }
+    a.first[i + 1] = a.first[i] + static_cast<long long>(T) * j.per_token;
+  }
+  const long long blocks = (a.first[njobs] + kNormWarps - 1) / kNormWarps;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  norm_rope_kernel<<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+unsigned int take_err_step() { return take_dev_err(); }
+
+}  // namespace cskv
