@@ -13,7 +13,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcskv.so")
 SOURCES = ["cskv_api.cu", "compress.cu", "index_topk.cu", "attention.cu", "cskvx_api.cu", "list_attn.cu",
            "evict.cu", "cskvs_api.cu", "step.cu", "chunk_attn.cu"]
-HEADERS = ["common.cuh", "codec.cuh", "internal.h"]
+HEADERS = ["common.cuh", "codec.cuh", "attn.cuh", "internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-Xcompiler", "-fvisibility=hidden",
          "-diag-suppress", "177"]

@@ -341,6 +341,18 @@ def test_a_graph_and_a_stream_and_a_workspace_of_the_callers():
     assert cskv.device_status() == 0
 
 
+def test_a_tighter_bound_of_keys_and_one_too_tight():
+    c = Case([10, 10], [1000, 200], 16, 1, FP8, window=20, seed=22)
+    up = lambda n: (n + 15) // 16 * 16
+    need = [up(1000) + up(29), up(200) + up(29)]
+    a = c.run(max_keys=sum(need))
+    c.check(*a, pick=[0, 9, 10, 19])
+    b = c.run(max_keys=sum(need) - 1)      # no room for the second request: no keys
+    assert cskv.device_status() == ERR_BOUNDS
+    c.check(*b, pick=[0, 9])               # (not the same bits: the row blocks' shares are others)
+    assert not b[0][10:].any() and torch.isneginf(b[1][10:]).all()
+
+
 def test_calls_that_are_refused():
     c = Case([3], [100], 16, 1, FP8, window=20, seed=23)
     a = c.args()
