@@ -26,13 +26,14 @@
 // heads.  Its keys come in tiles of 64, two tiles in shared memory; P is one of two buffers; tensor
 // memory holds the output (4 blocks of 128 dims x 64 rows, dims as lanes) and two tiles' logits
 // (rows as lanes: a row's sums stay within four threads).  Roles:
-//   warps 0-3    softmax of a tile, 16 rows each: logits from tensor memory, P to shared memory;
-//   warps 4-11   the next row block's queries (loaded and rotated while the last products of this one
+//   warps 0-7    softmax of a tile, 16 rows and 32 keys each: logits from tensor memory, P to shared
+//                memory (four warps of 64 keys each took 2,000 cycles a tile: 5.76 ms);
+//   warps 8-15   the next row block's queries (loaded and rotated while the last products of this one
 //                run), and the outputs;
-//   warp 12      one thread issues the products: S S O O of two tiles in turn, so that the softmax of
+//   warp 16      one thread issues the products: S S O O of two tiles in turn, so that the softmax of
 //                one runs beside the products of the other, and the next two tiles' keys come while
 //                the O products run;
-//   warp 13      plans row blocks and sends for their keys (bulk copies, a pair of chunks of 64 dims
+//   warp 17      plans row blocks and sends for their keys (bulk copies, a pair of chunks of 64 dims
 //                at a time, as soon as the O product on the pair two tiles before is complete).
 // Roundings as in list_attn.cu: the rotated query as two bf16 numbers, P in bf16 over the sum of the
 // rounded weights, all sums, references and partial outputs fp32.
@@ -51,8 +52,9 @@ constexpr int kD = 512;
 constexpr int kTile = 64;                 // keys of a tile
 constexpr int kRows = 64;                 // rows of a row block
 constexpr int kChunk = kTile * 128;       // bytes of 64 dims of a tile
-constexpr int kStage = 8 * kChunk;
-constexpr int kSoftWarps = 4, kOutWarps = 8;
+constexpr int kPair = 2 * kChunk;         // of 128 dims: groups of 8 keys, each [64 dims][8 keys][128 B] twice
+constexpr int kStage = 4 * kPair;
+constexpr int kSoftWarps = 8, kOutWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kOutWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kOutThreads = kOutWarps * 32;
@@ -105,7 +107,7 @@ struct ChunkArgs {
   long long* unit0;         // [items + 1]
   SplitPlan* split;         // [most_blocks]
   uint8_t* flags;           // of every decoded row: 0, kNone, kUnfit
-  uint8_t* images;          // decoded rows: of each request 8 chunks of 64 dims, [row][128 bytes], swizzled
+  uint8_t* images;          // decoded rows: of each request 4 blocks of 128 dims as they lie in a stage
   float* opart;             // [2 * most_blocks][kRows][512]
   float2* ml;               // [2 * most_blocks][kRows]: m (base 2) and l
   unsigned long long spin;
@@ -345,7 +347,8 @@ __global__ void __launch_bounds__(kDecodeThreads) chunk_decode_kernel(const __gr
     const uint8_t* mine = nullptr;
     if (lane < kDecodeRows && k0 + lane < have)
       mine = paged_row(c, r, (raw ? p.row0 : 0) + static_cast<long long>(k0) + lane, row_bytes).data;
-    uint8_t* image = a.images + p.base * (2 * kD) + (lane >> 2) * (rows * 128) + static_cast<long long>(first) * 128;
+    uint8_t* image = a.images + p.base * (2 * kD) + (lane >> 3) * (rows * 256) + static_cast<long long>(first) * 256 +
+                     ((lane >> 2) & 1) * 1024;
     uint32_t unfit = 0;
 #pragma unroll 4
     for (int i = 0; i < kDecodeRows; ++i) {
@@ -364,8 +367,9 @@ __global__ void __launch_bounds__(kDecodeThreads) chunk_decode_kernel(const __gr
         }
       }
       const int swz = i & 7, at = 2 * (lane & 3);
-      *reinterpret_cast<uint4*>(image + i * 128 + ((at ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(image + i * 128 + (((at + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+      uint8_t* to = image + (i >> 3) * 2048 + swz * 128;
+      *reinterpret_cast<uint4*>(to + ((at ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(to + (((at + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
     }
     const uint32_t none = __ballot_sync(0xFFFFFFFFu, lane < kDecodeRows && mine == nullptr);
     if (lane < kDecodeRows) a.flags[x + lane] = (none >> lane) & 1u ? kNone : (unfit >> lane) & 1u ? kUnfit : 0;
@@ -390,7 +394,7 @@ struct Item {
   int plain;                     // keys below it are seen by every row
   int bad;
   int part;                      // partial output, -1: none
-  long long base, stride;        // the request's first decoded row, bytes between its chunks
+  long long base, stride;        // the request's first decoded row, bytes between its blocks of dims
   RowSees sees[kRows];
 };
 
@@ -402,7 +406,8 @@ struct ChunkSmem {
   uint32_t tmem;
   int abort;
   __align__(16) float fac[kRows];          // a moved reference's factors
-  float4 sums[2][kRows];                   // m (base 2), l, sum of the rounded weights, of a row block
+  float top[2][kRows];                     // a tile's largest logits, of either half of its keys
+  float4 sums[2][2][kRows];                // of a row block and a half: m (base 2), l, sum of the rounded weights
   __align__(16) float out_fac[kRows];
 };
 
@@ -440,17 +445,14 @@ __device__ __forceinline__ bool role_any(bool p) {
 }
 constexpr int kSoftId = 1, kOutId = 2;
 
-// 16 lanes x 64 columns: thread l has columns 8 j + 2 (l & 3) and + 1 of lane l / 4 in v[4 j], v[4 j + 1],
+// 16 lanes x 32 columns: thread l has columns 8 j + 2 (l & 3) and + 1 of lane l / 4 in v[4 j], v[4 j + 1],
 // of lane l / 4 + 8 in v[4 j + 2], v[4 j + 3].
-__device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, float (&v)[32]) {
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float (&v)[16]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 
@@ -490,7 +492,7 @@ __device__ void make_item(const ChunkArgs& a, Item* it, int e, long long units, 
     it->plain = least;
     it->bad = p.bad;
     it->base = p.base;
-    it->stride = static_cast<long long>(p.entries16 + p.rows16) * 128;
+    it->stride = static_cast<long long>(p.entries16 + p.rows16) * 256;
     // its tiles between the share's borders
     const long long u0 = a.unit0[e];
     const int tiles = tiles_of(k.keys);
@@ -558,7 +560,7 @@ __device__ __forceinline__ void rotate_queries(const ChunkArgs& a, const Item* i
   fence_proxy_async_smem();
 }
 
-// The softmax warps' state of two rows: r = 16 * warp + lane / 4, and r + 8.
+// The softmax warps' state of two rows: r = 16 * (warp & 3) + lane / 4, and r + 8.
 struct RowState {
   float m[2], limit[2], msub[2];   // reference in units of q'.c; a logit above limit moves it; in base 2
   float l[2], hat[2];              // this thread's sums of the weights, and of the rounded ones
@@ -571,11 +573,11 @@ struct RowState {
   }
 };
 
-// Logits of tile k0 / kTile that a row does not see become -inf, those of unfit rows NaN.
-__device__ __forceinline__ void mask_tile(const ChunkArgs& a, const Item* it, int k0, const RowSees (&sees)[2], float (&z)[32]) {
+// Logits of the keys k0 .. k0 + 31 that a row does not see become -inf, those of unfit rows NaN.
+__device__ __forceinline__ void mask_keys(const ChunkArgs& a, const Item* it, int k0, const RowSees (&sees)[2], float (&z)[16]) {
   const int c = 2 * (threadIdx.x & 3);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int k = k0 + 8 * j + c + u;
@@ -594,30 +596,35 @@ __device__ __forceinline__ void mask_tile(const ChunkArgs& a, const Item* it, in
   }
 }
 
-// The softmax of the block's tile g, the row block's tile t.
+// The softmax of the block's tile g, the row block's tile t: this warp's 16 rows and 32 keys.
 __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, const Item* it, uint8_t* ptile, uint32_t tmem,
                                            int g, int t, bool first, const RowSees (&sees)[2], RowState& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t tlane = static_cast<uint32_t>(warp * 32) << 16;
-  const int buf = g & 1, k0 = t * kTile;
+  const int quarter = warp & 3, half = warp >> 2;
+  const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
+  const int buf = g & 1, k0 = t * kTile + 32 * half, r = 16 * quarter + (lane >> 2);
   wait_warp(sm, &sm->s_full[buf], (g >> 1) & 1, a.spin);
   tc_fence_after();
-  float z[32];
-  tmem_ld16x64(tmem + kTmemS + 64 * buf + tlane, z);
+  float z[16];
+  tmem_ld16x32(tmem + kTmemS + 64 * buf + 32 * half + tlane, z);
   tmem_wait_ld();
-  if (k0 + kTile > it->plain || it->bad) mask_tile(a, it, k0, sees, z);
-  float top[2] = {z[0], z[2]};
+  if (k0 + 32 > it->plain || it->bad) mask_keys(a, it, k0, sees, z);
+  float top[2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    top[0] = fmaxf(top[0], fmaxf(z[4 * j], z[4 * j + 1]));
-    top[1] = fmaxf(top[1], fmaxf(z[4 * j + 2], z[4 * j + 3]));
-  }
+  for (int i = 0; i < 2; ++i)
+    top[i] = fmaxf(fmaxf(fmaxf(z[2 * i], z[2 * i + 1]), fmaxf(z[4 + 2 * i], z[4 + 2 * i + 1])),
+                   fmaxf(fmaxf(z[8 + 2 * i], z[8 + 2 * i + 1]), fmaxf(z[12 + 2 * i], z[12 + 2 * i + 1])));
   if (role_any<kSoftId, kSoftWarps * 32>(top[0] > s.limit[0] || top[1] > s.limit[1])) {   // some row's reference moves
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
       top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
-      const float now = fmaxf(top[i], s.m[i]);
+      if ((lane & 3) == 0) sm->top[half][r + 8 * i] = top[i];
+    }
+    role_sync<kSoftId, kSoftWarps * 32>();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float now = fmaxf(fmaxf(top[i], sm->top[half ^ 1][r + 8 * i]), s.m[i]);
       const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
       const float f = s.m[i] == -INFINITY ? 0.f : exp2f(s.msub[i] - sub);
       s.m[i] = now;
@@ -625,30 +632,32 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
       s.msub[i] = sub;
       s.l[i] *= f;
       s.hat[i] *= f;
-      if ((lane & 3) == 0) sm->fac[16 * warp + (lane >> 2) + 8 * i] = f;
+      if (half == 0 && (lane & 3) == 0) sm->fac[r + 8 * i] = f;
     }
     if (!first) {
       role_sync<kSoftId, kSoftWarps * 32>();
       wait_warp(sm, &sm->free_[(g - 1) & 1][3], ((g - 1) >> 1) & 1, a.spin);   // the O product before is complete
       tc_fence_after();
 #pragma unroll 1
-      for (int x = 0; x < 4 * it->nq; x += 16) {   // this warp's 32 dims of the four blocks, 16 rows at a time
-        const int block = x / it->nq, r = x - block * it->nq;
-        float o[16];
-        const uint32_t at = tmem + tlane + block * kRows + r;
-        tmem_ld16(at, o);
-        tmem_wait_ld();
+      for (int block = 2 * half; block < 2 * half + 2; ++block) {   // this warp's 32 dims of two blocks, 16 rows at a time
+#pragma unroll 1
+        for (int x = 0; x < it->nq; x += 16) {
+          float o[16];
+          const uint32_t at = tmem + tlane + block * kRows + x;
+          tmem_ld16(at, o);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] *= sm->fac[r + c];
-        tmem_st16(at, o);
+          for (int c = 0; c < 16; ++c) o[c] *= sm->fac[x + c];
+          tmem_st16(at, o);
+        }
       }
       tmem_wait_st();
     }
   }
-  uint8_t* to = ptile + buf * kChunk + (16 * warp + (lane >> 2)) * 128 + 4 * (lane & 3);
+  uint8_t* to = ptile + buf * kChunk + r * 128 + 4 * (lane & 3);
   const int swz = lane >> 2;   // of both rows
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float x = exp2_fast(fmaf(z[4 * j + 2 * i], a.scale_log2, -s.msub[i]));
@@ -656,7 +665,7 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
       const uint32_t w = pack_bf16(x, y);
       s.l[i] += x + y;
       s.hat[i] += bf16lo(w) + bf16hi(w);
-      *reinterpret_cast<uint32_t*>(to + i * 1024 + ((j ^ swz) << 4)) = w;
+      *reinterpret_cast<uint32_t*>(to + i * 1024 + (((4 * half + j) ^ swz) << 4)) = w;
     }
   }
   fence_proxy_async_smem();
@@ -736,7 +745,10 @@ __device__ __forceinline__ void finish_sums(const ChunkArgs& a, const Item* it, 
   if (r >= kRows) return;
   float f = 0.f;
   if (r < it->nr) {
-    const float4 s = sm->sums[e & 1][r];   // m, l, sum of the rounded weights
+    float4 s = sm->sums[e & 1][0][r];   // m, l, sum of the rounded weights
+    const float4 more = sm->sums[e & 1][1][r];
+    s.y += more.y;
+    s.z += more.z;
     const unsigned row = it->r0 + r;
     // the output is made of rounded weights: over their own sum a few large ones' roundings cancel
     const float ratio = s.y == 0.f ? 1.f : s.y / s.z;
@@ -761,7 +773,7 @@ __device__ __forceinline__ void finish_sums(const ChunkArgs& a, const Item* it, 
 
 // S of a tile: 64 rows x 64 keys, K = 512 dims and the second halves of the 64 rotated ones
 __device__ __forceinline__ void issue_s_chunk(uint32_t d, uint64_t dq, uint64_t dk, int c, uint32_t id) {
-  const uint64_t q = dq + c * (kChunk >> 4), k = dk + c * (kChunk >> 4);
+  const uint64_t q = dq + c * (kChunk >> 4), k = dk + (c >> 1) * (kPair >> 4) + (c & 1) * (1024 >> 4);
   if (c == 0) mma_set(d, q, k, id);
   else mma_add(d, q, k, id);
 #pragma unroll
@@ -777,7 +789,7 @@ static_assert(kChunkSmemBytes <= 227 * 1024, "one block per SM");
 
 __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* ktile = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // 2 stages of 8 chunks of 64 rows x 128 B
+  uint8_t* ktile = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // 2 stages of 64 keys
   uint8_t* qtile = ktile + 2 * kStage;                                            // 9 chunks
   uint8_t* ptile = qtile + 9 * kChunk;                                            // 2 of 64 rows x 64 keys
   ChunkSmem* sm = reinterpret_cast<ChunkSmem*>(ptile + 2 * kChunk);
@@ -825,28 +837,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       make_item(a, it, first + e, head.units, head.blocks);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->item_full[e & 1]);
-      // lane c sends for chunk c
-      const uint8_t* image = a.images + it->base * (2 * kD) + (lane & 7) * it->stride;
-      for (int t = 0; t < it->nt && ok; ++t) {
-        const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0);
-        const int ne = max(0, min(n, it->seen16 - k0)), nr = n - ne;   // entries, raw rows (whole 16s)
-        const int stage = g & 1;
-        uint8_t* to = ktile + stage * kStage + (lane & 7) * kChunk;
-#pragma unroll 1
-        for (int m = 0; m < 4 && ok; ++m) {
-          if (g >= 2) ok = wait_warp(sm, &sm->free_[stage][m], ((g >> 1) - 1) & 1, a.spin);
-          if (!ok) { pairs = m; break; }
-          if (lane == 2 * m) mbar_expect_tx(&sm->full[stage][m], 2 * n * 128);
-          __syncwarp();
-          if ((lane >> 1) == m) {
-            if (ne > 0) bulk_g2s(to, image + static_cast<long long>(k0) * 128, ne * 128, &sm->full[stage][m]);
-            if (nr > 0)
-              bulk_g2s(to + ne * 128, image + static_cast<long long>(it->raw0 + k0 + ne - it->seen16) * 128, nr * 128,
-                       &sm->full[stage][m]);
+      if (lane == 0) {
+        const uint8_t* image = a.images + it->base * (2 * kD);
+        const long long stride = it->stride;
+        const int nt = it->nt, keys = it->keys, seen16 = it->seen16, raw0 = it->raw0;
+        for (int t = 0; t < nt && ok; ++t) {
+          const int k0 = (it->begin + t) * kTile, n = min(kTile, keys - k0);
+          const int ne = max(0, min(n, seen16 - k0)), nr = n - ne;   // entries, raw rows (whole 16s)
+          const uint8_t* from = image + static_cast<long long>(ne > 0 ? k0 : raw0 + k0 - seen16) * 256;
+          const int stage = g & 1;
+          uint8_t* to = ktile + stage * kStage;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            uint64_t* full = &sm->full[stage][m];
+            if (g >= 2) ok = ok && wait_bar(sm, &sm->free_[stage][m], ((g >> 1) - 1) & 1, a.spin);
+            if (ok) {
+              mbar_expect_tx(full, n * 256);
+              bulk_g2s(to + m * kPair, from + m * stride, (ne > 0 ? ne : nr) * 256, full);
+              if (ne > 0 && nr > 0)
+                bulk_g2s(to + m * kPair + ne * 256, image + m * stride + static_cast<long long>(raw0) * 256, nr * 256, full);
+              pairs = m + 1;
+            }
           }
+          if (ok) { ++g; pairs = 0; }
         }
-        if (ok) ++g;
       }
+      g = __shfl_sync(0xFFFFFFFFu, g, 0);
+      pairs = __shfl_sync(0xFFFFFFFFu, pairs, 0);
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
     }
     // copies in flight (there are none, unless a wait gave up): the last ones to each pair of chunks
     if (lane == 0) {
@@ -861,8 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     if (elect_lane()) {
       const uint32_t ids = make_idesc(1, 1, 0, 0, 64, 64);
       const uint64_t dq = smem_desc_sw128(smem_u32(qtile), 16, 1024);
-      const uint64_t dk = smem_desc_sw128(smem_u32(ktile), 16, 1024);
-      const uint64_t dv = smem_desc_sw128(smem_u32(ktile), kChunk, 1024);
+      const uint64_t dk = smem_desc_sw128(smem_u32(ktile), 16, 2048);
+      const uint64_t dv = smem_desc_sw128(smem_u32(ktile), 1024, 2048);
       const uint64_t dp = smem_desc_sw128(smem_u32(ptile), 16, 1024);
       bool ok = true;
       int g = 0;
@@ -915,15 +933,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             const uint64_t v = dv + stage * (kStage >> 4), p = dp + stage * (kChunk >> 4);
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb) {
-              const uint64_t vb = v + mb * (kChunk >> 3);
+              const uint64_t vb = v + mb * (kPair >> 4);
               if (t + u == 0) mma_set(tmem + mb * kRows, vb, p, ido);
               else mma_add(tmem + mb * kRows, vb, p, ido);
               if (ks == 4) {
 #pragma unroll
-                for (int k = 1; k < 4; ++k) mma_add(tmem + mb * kRows, vb + k * 128, p + 2 * k, ido);
+                for (int k = 1; k < 4; ++k) mma_add(tmem + mb * kRows, vb + k * 256, p + 2 * k, ido);
               } else {
 #pragma unroll 1
-                for (int k = 1; k < ks; ++k) mma_add(tmem + mb * kRows, vb + k * 128, p + 2 * k, ido);
+                for (int k = 1; k < ks; ++k) mma_add(tmem + mb * kRows, vb + k * 256, p + 2 * k, ido);
               }
               mma_commit(&sm->free_[stage][mb]);
             }
@@ -942,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       const bool there = wait_warp(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
       if (role_any<kSoftId, kSoftWarps * 32>(!there)) break;
       const Item* it = &sm->item[e & 1];
-      const int r = 16 * warp + (lane >> 2);
+      const int r = 16 * (warp & 3) + (lane >> 2);
       const RowSees sees[2] = {it->sees[r], it->sees[r + 8]};
       RowState s;
       s.reset();
@@ -956,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
           s.hat[i] += __shfl_xor_sync(0xFFFFFFFFu, s.hat[i], o);
         }
         if ((lane & 3) == 0)
-          sm->sums[e & 1][r + 8 * i] = make_float4(s.m[i] == -INFINITY ? -INFINITY : s.msub[i], s.l[i], s.hat[i], 0.f);
+          sm->sums[e & 1][warp >> 2][r + 8 * i] = make_float4(s.m[i] == -INFINITY ? -INFINITY : s.msub[i], s.l[i], s.hat[i], 0.f);
       }
       __syncwarp();
       if (lane == 0) {
