@@ -696,14 +696,15 @@ class StepMaps:
     def __init__(self, B, T, pages=True, ring=False, device="cuda"):
         import torch
         i32, i64 = torch.int32, torch.int64
-        # one allocation, the 64-bit maps first
-        n64 = (T if pages else 0) + (T if ring else 0)
-        buf = torch.empty(8 * n64 + 4 * (4 * B + 1 + 2 * T), dtype=torch.uint8, device=device)
-        wide = buf[:8 * n64].view(i64)
-        self.slot = wide[:T] if pages else None
-        self.ring_slot = wide[n64 - T:] if ring else None
-        self.cu_new, self.new_len, self.first_row, self.n_rows, self.req_of, self.pos1 = \
-            buf[8 * n64:].view(i32).split((B + 1, B, B, B, T, T))
+        buf = torch.empty(4 * B + 1 + 2 * T, dtype=i32, device=device)
+        self.cu_new, self.new_len, self.first_row, self.n_rows, self.req_of, self.pos1 = buf.split((B + 1, B, B, B, T, T))
+        self.slot = self.ring_slot = None
+        if pages and ring:
+            self.slot, self.ring_slot = torch.empty((2, T), dtype=i64, device=device).unbind()
+        elif pages:
+            self.slot = torch.empty(T, dtype=i64, device=device)
+        elif ring:
+            self.ring_slot = torch.empty(T, dtype=i64, device=device)
         self.B, self.T, self.device = B, T, buf.device
 
 

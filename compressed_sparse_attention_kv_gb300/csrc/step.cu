@@ -96,8 +96,9 @@ __device__ __forceinline__ int bounded_len(int n) {
   return n < 0 ? 0 : kMaxLen;
 }
 
-// The sums, the lengths and the ring's new state; one block.
-__device__ void plan_sums(const PlanArgs& a) {
+// The sums, the lengths and the ring's new state; one block.  first_tokens (shared memory, may be
+// null): the requests' first tokens once more.
+__device__ void plan_sums(const PlanArgs& a, int* first_tokens) {
   __shared__ long long part[32];
   long long tok = 0, take = 0, give = 0;   // before this round of requests
   int head = a.state != nullptr ? a.state[0] : 0, count = a.state != nullptr ? a.state[1] : 0;
@@ -147,6 +148,7 @@ __device__ void plan_sums(const PlanArgs& a) {
     if (there) {
       a.rec[b] = r;
       a.cu_new[b] = tok0;
+      if (first_tokens != nullptr) first_tokens[b] = tok0;
       a.new_len[b] = len;
       a.first_row[b] = row0;
       a.n_rows[b] = row1;
@@ -167,40 +169,50 @@ __device__ void plan_sums(const PlanArgs& a) {
   }
 }
 
+// The ring's place k behind its first one (k up to its capacity).
+__device__ __forceinline__ int32_t* ring_place(const PlanArgs& a, const PlanHead& h, long long k) {
+  const long long at = h.head + k;
+  return a.free_pages + (at >= a.capacity ? at - a.capacity : at);
+}
 // The id of the step's k-th new page, -1: none is left.
 __device__ __forceinline__ int new_page(const PlanArgs& a, const PlanHead& h, long long k) {
-  return k < h.count ? a.free_pages[(h.head + k) % a.capacity] : -1;
+  return k < h.count ? *ring_place(a, h, k) : -1;
 }
 
-// The maps of tokens [i0, i0 + stride * ...) and the pages of requests w0, w0 + warps, ...
+// The maps of the tokens of blocks block, block + blocks, ...; staged: shared memory, which holds the
+// requests' first tokens already (kWhole) or gets those of the block's tokens.
+template <bool kWhole>
 __device__ void plan_tokens(const PlanArgs& a, const PlanHead& h, int block, int blocks, int* staged) {
   for (long long base = static_cast<long long>(block) * blockDim.x; base < a.T;
        base += static_cast<long long>(blocks) * blockDim.x) {
     const int i0 = static_cast<int>(base), i = i0 + threadIdx.x;
     // the requests of the block's tokens: [lo, hi], the last ones whose first token is not behind them
-    const int end = min(i0 + static_cast<int>(blockDim.x), h.tokens) - 1;
-    int lo = 0, hi = 0;
-    if (i0 < h.tokens) {
+    int lo = 0, hi = kWhole ? a.B - 1 : 0;
+    bool stage = kWhole;
+    if constexpr (!kWhole) {
+      const int end = min(i0 + static_cast<int>(blockDim.x), h.tokens) - 1;
+      if (i0 < h.tokens) {
 #pragma unroll
-      for (int side = 0; side < 2; ++side) {   // 32 places at a time; every warp for itself
-        const int key = side == 0 ? i0 : end;
-        int from = 0, n = a.B;                 // the last b in [from, from + n) with tok0 <= key
-        while (n > 1) {
-          const int step = (n + 31) / 32, at = from + static_cast<int>(threadIdx.x & 31) * step;
-          const bool le = at < from + n && a.cu_new[at] <= key;
-          const int k = __popc(__ballot_sync(0xFFFFFFFFu, le)) - 1;   // (from itself is one)
-          const int next = from + k * step;
-          n = min(step, from + n - next);
-          from = next;
+        for (int side = 0; side < 2; ++side) {   // 32 places at a time; every warp for itself
+          const int key = side == 0 ? i0 : end;
+          int from = 0, n = a.B;                 // the last b in [from, from + n) with a first token <= key
+          while (n > 1) {
+            const int step = (n + 31) / 32, at = from + static_cast<int>(threadIdx.x & 31) * step;
+            const bool le = at < from + n && a.cu_new[at] <= key;
+            const int k = __popc(__ballot_sync(0xFFFFFFFFu, le)) - 1;   // (from itself is one)
+            const int next = from + k * step;
+            n = min(step, from + n - next);
+            from = next;
+          }
+          (side == 0 ? lo : hi) = from;
         }
-        (side == 0 ? lo : hi) = from;
       }
+      stage = hi - lo < kStaged && hi > lo;
+      __syncthreads();   // the tokens before are mapped
+      if (stage)
+        for (int x = threadIdx.x; x <= hi - lo; x += blockDim.x) staged[x] = a.cu_new[lo + x];
+      __syncthreads();
     }
-    const bool stage = hi - lo < kStaged && hi > lo;
-    __syncthreads();   // the tokens before are mapped
-    if (stage)
-      for (int x = threadIdx.x; x <= hi - lo; x += blockDim.x) staged[x] = a.cu_new[lo + x];
-    __syncthreads();
     if (i >= a.T) continue;
     int req = -1, p1 = 0;
     long long slot = -1, ring = -1;
@@ -213,8 +225,7 @@ __device__ void plan_tokens(const PlanArgs& a, const PlanHead& h, int block, int
         n = le ? n - half : half;
       }
       const PlanRecord r = a.rec[b];
-      const int next = b + 1 <= hi && stage ? staged[b + 1 - lo] : a.cu_new[b + 1];
-      const int p = r.ctx + (i - r.tok0);
+      const int p = r.ctx + (i - r.tok0), len = a.new_len[b];
       req = b;
       p1 = p + 1;
       if (a.table != nullptr && p1 % a.ratio == 0) {
@@ -224,7 +235,7 @@ __device__ void plan_tokens(const PlanArgs& a, const PlanHead& h, int block, int
           page = lp < r.first ? a.table[static_cast<long long>(b) * a.max_pages + lp] : new_page(a, h, r.take + lp - r.first);
         if (page >= 0) slot = static_cast<long long>(page) * kPageRows + row % kPageRows;
       }
-      if (a.ring_rows > 0 && next - i <= a.ring_rows) ring = static_cast<long long>(b) * a.ring_rows + p % a.ring_rows;
+      if (a.ring_rows > 0 && len - p <= a.ring_rows) ring = static_cast<long long>(b) * a.ring_rows + p % a.ring_rows;
     }
     a.req_of[i] = req;
     a.pos1[i] = p1;
@@ -242,7 +253,7 @@ __device__ void plan_pages(const PlanArgs& a, const PlanHead& h, int warp, int w
     for (int lp = r.first + lane; lp < r.last; lp += 32) line[lp] = new_page(a, h, r.take + lp - r.first);
     for (int lp = r.own + lane; lp < r.used; lp += 32) {
       const long long j = r.give + lp - r.own;
-      if (j < a.capacity - h.count) a.free_pages[(static_cast<long long>(h.head) + h.count + j) % a.capacity] = line[lp];
+      if (j < a.capacity - h.count) *ring_place(a, h, h.count + j) = line[lp];
     }
   }
 }
@@ -250,13 +261,15 @@ __device__ void plan_pages(const PlanArgs& a, const PlanHead& h, int warp, int w
 template <bool kWhole>   // kWhole: the maps too
 __global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const __grid_constant__ PlanArgs a) {
   grid_dep_launch();
-  plan_sums(a);
   if constexpr (kWhole) {
-    __shared__ int staged[kStaged];
+    __shared__ int first_tokens[kPlanThreads];
+    plan_sums(a, first_tokens);
     __syncthreads();   // (the records are this block's own writes)
     const PlanHead h = *a.head;
+    plan_tokens<true>(a, h, 0, 1, first_tokens);
     plan_pages(a, h, threadIdx.x >> 5, kPlanThreads / 32);
-    plan_tokens(a, h, 0, 1, staged);
+  } else {
+    plan_sums(a, nullptr);
   }
 }
 
@@ -265,7 +278,7 @@ __global__ void __launch_bounds__(kMapThreads) plan_maps_kernel(const __grid_con
   grid_dep_wait();
   const PlanHead h = *a.head;
   plan_pages(a, h, (blockIdx.x * kMapThreads + threadIdx.x) >> 5, gridDim.x * (kMapThreads / 32));
-  plan_tokens(a, h, blockIdx.x, gridDim.x, staged);
+  plan_tokens<false>(a, h, blockIdx.x, gridDim.x, staged);
 }
 
 // ---------------------------------------------------------------------------
@@ -290,11 +303,19 @@ struct RopeArgs {
   float* out;
 };
 
+// a number below 2^23 as a float: the last bits of 2^23 + n
+__device__ __forceinline__ float float23(uint32_t n) { return __uint_as_float(0x4B000000u | n) - 8388608.0f; }
+
 __device__ __forceinline__ float2 cos_sin_of_turns(uint64_t t) {
   const uint32_t q = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
   const int64_t r = static_cast<int64_t>(t - (static_cast<uint64_t>(q) << 62));   // [-2^61, 2^61) of 2^64
-  const float rh = __ll2float_rn(r);
-  const float rl = __ll2float_rn(r - static_cast<int64_t>(rh));   // (rh is a whole number below 2^62)
+  // in three pieces, each a float without rounding, then in two (conversions of 64 bits run at a
+  // quarter of the rate: 25.5 us for the 131,071 positions that take 9)
+  const float r2 = static_cast<float>(static_cast<int>(r >> 46)) * 0x1p46f;
+  const float r1 = float23(static_cast<uint32_t>(r >> 23) & 0x7FFFFFu) * 0x1p23f;
+  const float r0 = float23(static_cast<uint32_t>(r) & 0x7FFFFFu);
+  const float rh = r2 + r1;
+  const float rl = (r1 - (rh - r2)) + r0;
   constexpr float kTurn = 0x1.921fb6p-62f, kTurnLow = -0x1.777a5cp-87f;   // 2 pi / 2^64
   const float x = rh * kTurn;
   const float d = fmaf(rh, kTurn, -x) + fmaf(rh, kTurnLow, rl * kTurn);
@@ -349,6 +370,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cs_kernel(const __grid_cons
 constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kMaxNormJobs = 4;
+constexpr long long kManyHeads = 4 * 152 * 32;   // of 512 dims
 
 struct NormJob {
   const uint8_t* x;
@@ -371,81 +393,120 @@ struct NormArgs {
   const float* rope_cs;
 };
 
-__device__ __forceinline__ void norm16(const NormJob& j, float (&y)[16], int c0, int lanes) {
-  // the sum of squares: neighbours first, then the lanes of the head
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(__fmul_rn(y[2 * i], y[2 * i]), __fmul_rn(y[2 * i + 1], y[2 * i + 1]));
-#pragma unroll
-  for (int w = 4; w >= 1; w >>= 1)
-#pragma unroll
-    for (int i = 0; i < w; ++i) v[i] = __fadd_rn(v[2 * i], v[2 * i + 1]);
-  float ss = v[0];
-  for (int o = 1; o < lanes; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
-  const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(j.dim)), j.eps)));
-#pragma unroll
-  for (int i = 0; i < 16; i += 4) {
-    float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-    if (j.norm_w != nullptr) w = __ldg(reinterpret_cast<const float4*>(j.norm_w + c0 + i));
-    y[i] = __fmul_rn(__fmul_rn(y[i], r), w.x);
-    y[i + 1] = __fmul_rn(__fmul_rn(y[i + 1], r), w.y);
-    y[i + 2] = __fmul_rn(__fmul_rn(y[i + 2], r), w.z);
-    y[i + 3] = __fmul_rn(__fmul_rn(y[i + 3], r), w.w);
-  }
-}
-
 __device__ __forceinline__ void turn2(float& y0, float& y1, float c, float s) {
   const float z0 = __fsub_rn(__fmul_rn(y0, c), __fmul_rn(y1, s));
   y1 = __fadd_rn(__fmul_rn(y0, s), __fmul_rn(y1, c));
   y0 = z0;
 }
 
-// Heads of one token: a lane has 16 dims of a head, 32 lanes (dim 512) or 8 (dim 128) a head.
-__device__ __forceinline__ void norm_heads(const NormArgs& a, const NormJob& j, long long w) {
-  const int lane = threadIdx.x & 31;
-  const long long t = w / j.per_token;
-  const int lanes = j.dim / 16, at_once = 32 / lanes;
-  const int c0 = (lane & (lanes - 1)) * 16;
-  const int h = static_cast<int>(w - t * j.per_token) * at_once + lane / lanes;
-  const bool there = h < j.H;
-  float y[16];
-  uint4 v[2] = {};
-  if (there) {
-    const uint4* from = reinterpret_cast<const uint4*>(j.x + t * j.x_stride + (static_cast<long long>(h) * j.dim + c0) * 2);
-    v[0] = from[0];
-    v[1] = from[1];
-  }
-  const bool turn = j.rotate && c0 >= j.dim - 64;
-  float4 cs[4];
-  if (turn) {
-    const float4* from = reinterpret_cast<const float4*>(a.rope_cs + t * 64 + (c0 - (j.dim - 64)));
+// N heads of one token (dim 512) or 4 N (dim 128).  A lane has pieces of 8 neighbouring dims: of a head
+// of 512 the pieces lane and lane + 32; of a head of 128 piece lane % 16 of head lane / 16 and of
+// head lane / 16 + 2, so that every access of a warp is 512 contiguous bytes.  All of a warp's
+// loads are on their way before the first is used.
+__device__ __forceinline__ void unpack8(const uint4& v, float (&y)[8]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = __ldg(from + i);
-  }
-  const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     y[2 * i] = bf16lo(u[i]);
     y[2 * i + 1] = bf16hi(u[i]);
   }
-  if (j.norm) norm16(j, y, c0, lanes);
-  if (turn) {
+}
+__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
+  uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      turn2(y[4 * i], y[4 * i + 1], cs[i].x, cs[i].y);
-      turn2(y[4 * i + 2], y[4 * i + 3], cs[i].z, cs[i].w);
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+    o[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// neighbours first
+__device__ __forceinline__ float squares8(const float (&y)[8]) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __fadd_rn(__fmul_rn(y[2 * i], y[2 * i]), __fmul_rn(y[2 * i + 1], y[2 * i + 1]));
+  return __fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3]));
+}
+__device__ __forceinline__ void scale8(float (&y)[8], float r, const float4& w0, const float4& w1) {
+  const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fmul_rn(y[i], r), w[i]);
+}
+__device__ __forceinline__ void turn8(float (&y)[8], const float4& c0, const float4& c1) {
+  turn2(y[0], y[1], c0.x, c0.y);
+  turn2(y[2], y[3], c0.z, c0.w);
+  turn2(y[4], y[5], c1.x, c1.y);
+  turn2(y[6], y[7], c1.z, c1.w);
+}
+
+template <int D, int N>
+__device__ __forceinline__ void norm_heads(const NormArgs& a, const NormJob& j, long long w) {
+  constexpr int kLanes = D == 512 ? 32 : 16;            // of a piece of a head
+  constexpr int kStep = D == 512 ? 1 : 4;               // heads of two pieces of a warp
+  const int lane = threadIdx.x & 31;
+  const long long t = w / j.per_token;
+  const int h0 = static_cast<int>(w - t * j.per_token) * (N * kStep);
+  const int at = (lane & (kLanes - 1)) * 8;             // the first piece's first dim
+  const uint8_t* from = j.x + t * j.x_stride;
+  uint8_t* to = j.out + t * j.out_stride;
+  // piece p of head group n: its head, its byte
+  auto head = [&](int n, int p) { return D == 512 ? h0 + n : h0 + 4 * n + 2 * p + lane / 16; };
+  auto byte = [&](int n, int p) {
+    return (static_cast<long long>(head(n, p)) * D + at + (D == 512 ? 256 * p : 0)) * 2;
+  };
+  uint4 v[N][2];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      v[n][p] = make_uint4(0u, 0u, 0u, 0u);
+      if (head(n, p) < j.H) v[n][p] = *reinterpret_cast<const uint4*>(from + byte(n, p));
+    }
+  const bool turn = j.rotate && at >= (D == 512 ? 192 : 64);   // of the last piece (512), of either (128)
+  float4 c0 = make_float4(1.f, 0.f, 1.f, 0.f), c1 = c0;
+  if (turn) {
+    const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + t * 64 + (at - (D == 512 ? 192 : 64)));
+    c0 = __ldg(cs);
+    c1 = __ldg(cs + 1);
+  }
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+  float4 g[2][2] = {{one, one}, {one, one}};
+  if (j.norm_w != nullptr) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float4* wp = reinterpret_cast<const float4*>(j.norm_w + at + (D == 512 ? 256 * p : 0));
+      g[p][0] = __ldg(wp);
+      g[p][1] = __ldg(wp + 1);
     }
   }
-  if (there) {
-    uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-      o[i] = *reinterpret_cast<const uint32_t*>(&p);
+  for (int n = 0; n < N; ++n) {
+    float y[2][8];
+    unpack8(v[n][0], y[0]);
+    unpack8(v[n][1], y[1]);
+    if (j.norm) {
+      float ss[2] = {squares8(y[0]), squares8(y[1])};
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) {
+        ss[0] = __fadd_rn(ss[0], __shfl_xor_sync(0xFFFFFFFFu, ss[0], o));
+        ss[1] = __fadd_rn(ss[1], __shfl_xor_sync(0xFFFFFFFFu, ss[1], o));
+      }
+      if (D == 512) ss[0] = ss[1] = __fadd_rn(ss[0], ss[1]);
+      // one square root and division for all pieces of a head: lane-wise they are the same numbers
+#pragma unroll
+      for (int p = 0; p < (D == 512 ? 1 : 2); ++p)
+        ss[p] = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss[p], static_cast<float>(D)), j.eps)));
+      if (D == 512) ss[1] = ss[0];
+      scale8(y[0], ss[0], g[0][0], g[0][1]);
+      scale8(y[1], ss[1], g[1][0], g[1][1]);
     }
-    uint4* to = reinterpret_cast<uint4*>(j.out + t * j.out_stride + (static_cast<long long>(h) * j.dim + c0) * 2);
-    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    if (turn) {
+      if (D == 128) turn8(y[0], c0, c1);
+      turn8(y[1], c0, c1);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      if (head(n, p) < j.H) *reinterpret_cast<uint4*>(to + byte(n, p)) = pack8(y[p]);
   }
 }
 
@@ -496,15 +557,22 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const NormJob& j, lo
   for (int i = 0; i < N; ++i) store_row_values(y[i], 32 * i + lane, j.cache.fmt, D, dst, true);
 }
 
+// N: heads of 512 dims a warp has at a time
+template <int N>
 __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   const long long w = static_cast<long long>(blockIdx.x) * kNormWarps + (threadIdx.x >> 5);
   int k = 0;
   while (k + 1 < a.njobs && w >= a.first[k + 1]) ++k;
   if (w >= a.first[a.njobs]) return;
   const NormJob& j = a.job[k];
-  if (j.slot == nullptr) norm_heads(a, j, w - a.first[k]);
-  else if (j.dim == 512) norm_row<512>(a, j, w - a.first[k]);
-  else norm_row<128>(a, j, w - a.first[k]);
+  if (j.slot == nullptr) {
+    if (j.dim == 512) norm_heads<512, N>(a, j, w - a.first[k]);
+    else norm_heads<128, N>(a, j, w - a.first[k]);
+  } else if (j.dim == 512) {
+    norm_row<512>(a, j, w - a.first[k]);
+  } else {
+    norm_row<128>(a, j, w - a.first[k]);
+  }
 }
 
 inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -542,7 +610,7 @@ cudaError_t launch_plan_step(const int32_t* ctx_len, const int32_t* n_new, int B
   a.ring_slot = reinterpret_cast<long long*>(ring_slot);
   a.head = static_cast<PlanHead*>(workspace);
   a.rec = reinterpret_cast<PlanRecord*>(static_cast<uint8_t*>(workspace) + 256);
-  const bool whole = T <= 2048 && B <= 1024;
+  const bool whole = T <= 2048 && B <= kPlanThreads;
   if (whole) {
     plan_sums_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
     return cudaGetLastError();
@@ -584,6 +652,12 @@ cudaError_t launch_norm_rope(const cskvs_norm_job* jobs, int njobs, const float*
   a.njobs = njobs;
   a.T = T;
   a.rope_cs = rope_cs;
+  // four heads a warp where that leaves every SM its warps, else one: the loads on their way hide the
+  // memory's latency in long calls, the warps in short ones
+  long long heads = 0;
+  for (int i = 0; i < njobs; ++i)
+    if (jobs[i].slot == nullptr) heads += static_cast<long long>(T) * jobs[i].H * jobs[i].dim / 512;
+  const int n = heads >= kManyHeads ? 4 : 1;
   for (int i = 0; i < njobs; ++i) {
     const cskvs_norm_job& s = jobs[i];
     NormJob& j = a.job[i];
@@ -603,13 +677,15 @@ cudaError_t launch_norm_rope(const cskvs_norm_job* jobs, int njobs, const float*
     } else {
       j.out = static_cast<uint8_t*>(s.out);
       j.out_stride = s.out_stride * 2;
-      j.per_token = s.dim == 512 ? s.H : (s.H + 3) / 4;
+      const int step = s.dim == 512 ? n : 4 * n;
+      j.per_token = (s.H + step - 1) / step;
     }
     a.first[i + 1] = a.first[i] + static_cast<long long>(T) * j.per_token;
   }
   const long long blocks = (a.first[njobs] + kNormWarps - 1) / kNormWarps;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  norm_rope_kernel<<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(a);
+  if (n == 4) norm_rope_kernel<4><<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(a);
+  else norm_rope_kernel<1><<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
