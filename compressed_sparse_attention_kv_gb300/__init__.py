@@ -691,20 +691,21 @@ class PageTable:
 class StepMaps:
     """What plan_step writes, for B requests and T places for tokens: cu_new int32 [B + 1],
     new_len, first_row, n_rows int32 [B], req_of, pos1 int32 [T], slot int64 [T] (None without
-    pages), ring_slot int64 [T] (None without a ring).  Made once, it may serve every step."""
+    pages), ring_slot int64 [T] (None without a ring), and the call's workspace beside them.
+    Made once, it may serve every step, one at a time."""
 
     def __init__(self, B, T, pages=True, ring=False, device="cuda"):
         import torch
-        i32, i64 = torch.int32, torch.int64
-        buf = torch.empty(4 * B + 1 + 2 * T, dtype=i32, device=device)
-        self.cu_new, self.new_len, self.first_row, self.n_rows, self.req_of, self.pos1 = buf.split((B + 1, B, B, B, T, T))
-        self.slot = self.ring_slot = None
-        if pages and ring:
-            self.slot, self.ring_slot = torch.empty((2, T), dtype=i64, device=device).unbind()
-        elif pages:
-            self.slot = torch.empty(T, dtype=i64, device=device)
-        elif ring:
-            self.ring_slot = torch.empty(T, dtype=i64, device=device)
+        # one allocation: the step's workspace, the 64-bit maps, the others
+        self.workspace_bytes = _lib.lib().cskvs_plan_step_workspace_size(B)
+        wide = (self.workspace_bytes // 8,) + ((T,) if pages else ()) + ((T,) if ring else ())
+        buf = torch.empty(sum(wide) + (4 * B + 2 + 2 * T) // 2, dtype=torch.int64, device=device)
+        _, *slots, rest = buf.split_with_sizes(wide + (buf.shape[0] - sum(wide),))
+        self.slot = slots[0] if pages else None
+        self.ring_slot = slots[-1] if ring else None
+        self.cu_new, self.new_len, self.first_row, self.n_rows, self.req_of, self.pos1, _ = \
+            rest.view(torch.int32).split_with_sizes((B + 1, B, B, B, T, T, 1))
+        self.workspace = buf.data_ptr()
         self.B, self.T, self.device = B, T, buf.device
 
 
@@ -743,13 +744,14 @@ def plan_step(ctx_len, n_new, T, pages=None, ratio=1, ring_rows=0, shared_pages=
             (out.ring_slot is None) != (ring_rows <= 0):
         raise ValueError("out must be a StepMaps of %d requests and %d tokens on %s, with slots as pages and ring_rows "
                          "say" % (B, T, dev))
-    L = _lib.lib()
-    need = 0 if workspace is not None else L.cskvs_plan_step_workspace_size(B)
-    workspace, pw, nw = _workspace(workspace, need, dev)
-    _check(L.cskvs_plan_step(pc, pn, B, ratio, T, ring_rows, pt, per, psh, pf, cap, ps, po, out.cu_new.data_ptr(),
-                             out.new_len.data_ptr(), out.first_row.data_ptr(), out.n_rows.data_ptr(),
-                             out.req_of.data_ptr(), out.pos1.data_ptr(), _ptr(out.slot), _ptr(out.ring_slot), pw, nw,
-                             _raw_stream(dev)), "cskvs_plan_step")
+    if workspace is None:
+        pw, nw = out.workspace, out.workspace_bytes
+    else:
+        workspace, pw, nw = _workspace(workspace, 0, dev)
+    _check(_lib.lib().cskvs_plan_step(pc, pn, B, ratio, T, ring_rows, pt, per, psh, pf, cap, ps, po,
+                                      out.cu_new.data_ptr(), out.new_len.data_ptr(), out.first_row.data_ptr(),
+                                      out.n_rows.data_ptr(), out.req_of.data_ptr(), out.pos1.data_ptr(), _ptr(out.slot),
+                                      _ptr(out.ring_slot), pw, nw, _raw_stream(dev)), "cskvs_plan_step")
     return out
 
 

@@ -306,61 +306,107 @@ struct RopeArgs {
 // a number below 2^23 as a float: the last bits of 2^23 + n
 __device__ __forceinline__ float float23(uint32_t n) { return __uint_as_float(0x4B000000u | n) - 8388608.0f; }
 
-__device__ __forceinline__ float2 cos_sin_of_turns(uint64_t t) {
-  const uint32_t q = static_cast<uint32_t>((t + (1ull << 61)) >> 62);
-  const int64_t r = static_cast<int64_t>(t - (static_cast<uint64_t>(q) << 62));   // [-2^61, 2^61) of 2^64
-  // in three pieces, each a float without rounding, then in two (conversions of 64 bits run at a
-  // quarter of the rate: 25.5 us for the 131,071 positions that take 9)
-  const float r2 = static_cast<float>(static_cast<int>(r >> 46)) * 0x1p46f;
-  const float r1 = float23(static_cast<uint32_t>(r >> 23) & 0x7FFFFFu) * 0x1p23f;
-  const float r0 = float23(static_cast<uint32_t>(r) & 0x7FFFFFu);
-  const float rh = r2 + r1;
-  const float rl = (r1 - (rh - r2)) + r0;
+// Two numbers in one register pair, and the fp32 operations on both at once (each rounded as alone).
+struct Two {
+  float a, b;
+};
+__device__ __forceinline__ Two both(float x) { return Two{x, x}; }
+__device__ __forceinline__ Two mul(const Two& x, const Two& y) {
+  Two r;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.a), "=f"(r.b) : "f"(x.a), "f"(x.b), "f"(y.a), "f"(y.b));
+  return r;
+}
+__device__ __forceinline__ Two add(const Two& x, const Two& y) {
+  Two r;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.a), "=f"(r.b) : "f"(x.a), "f"(x.b), "f"(y.a), "f"(y.b));
+  return r;
+}
+__device__ __forceinline__ Two fma(const Two& x, const Two& y, const Two& z) {
+  Two r = z;
+  fma2(r.a, r.b, x.a, x.b, y.a, y.b);
+  return r;
+}
+__device__ __forceinline__ Two neg(const Two& x) { return Two{-x.a, -x.b}; }
+
+// (cos, sin) of two angles in turns of 2^64
+__device__ __forceinline__ float4 cos_sin_of_turns(const uint64_t (&t)[2]) {
+  uint32_t q[2];
+  float part[2][3];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    q[u] = static_cast<uint32_t>((t[u] + (1ull << 61)) >> 62);
+    const int64_t r = static_cast<int64_t>(t[u] - (static_cast<uint64_t>(q[u]) << 62));   // [-2^61, 2^61)
+    // in three pieces, each a float without rounding (conversions of 64 bits run at a quarter of the
+    // rate: 25.5 us instead of 16)
+    part[u][0] = static_cast<float>(static_cast<int>(r >> 46));
+    part[u][1] = float23(static_cast<uint32_t>(r >> 23) & 0x7FFFFFu);
+    part[u][2] = float23(static_cast<uint32_t>(r) & 0x7FFFFFu);
+  }
+  const Two r2 = mul(Two{part[0][0], part[1][0]}, both(0x1p46f)), r1 = mul(Two{part[0][1], part[1][1]}, both(0x1p23f));
+  const Two rh = add(r2, r1);
+  const Two rl = add(add(r1, neg(add(rh, neg(r2)))), Two{part[0][2], part[1][2]});
   constexpr float kTurn = 0x1.921fb6p-62f, kTurnLow = -0x1.777a5cp-87f;   // 2 pi / 2^64
-  const float x = rh * kTurn;
-  const float d = fmaf(rh, kTurn, -x) + fmaf(rh, kTurnLow, rl * kTurn);
-  const float s = x * x, sl = fmaf(x, x, -s);
-  float p = -1.0f / 39916800.0f;
-  p = fmaf(p, s, 1.0f / 362880.0f);
-  p = fmaf(p, s, -1.0f / 5040.0f);
-  p = fmaf(p, s, 1.0f / 120.0f);
-  p = fmaf(p, s, -1.0f / 6.0f);
-  const float sn = x + fmaf(x * s, p, d);
-  float c = 1.0f / 479001600.0f;
-  c = fmaf(c, s, -1.0f / 3628800.0f);
-  c = fmaf(c, s, 1.0f / 40320.0f);
-  c = fmaf(c, s, -1.0f / 720.0f);
-  c = fmaf(c, s, 1.0f / 24.0f);
-  const float w = fmaf(-0.5f, s, 1.0f);
-  const float lost = fmaf(-0.5f, s, 1.0f - w) - fmaf(x, d, 0.5f * sl);
-  const float cs = w + fmaf(s * s, c, lost);
-  const float a = (q & 1) ? sn : cs, b = (q & 1) ? cs : sn;
-  return make_float2(((q + 1) & 2) ? -a : a, (q & 2) ? -b : b);
+  const Two x = mul(rh, both(kTurn));
+  const Two d = add(fma(rh, both(kTurn), neg(x)), fma(rh, both(kTurnLow), mul(rl, both(kTurn))));
+  const Two s = mul(x, x), sl = fma(x, x, neg(s));
+  Two p = fma(both(-1.0f / 39916800.0f), s, both(1.0f / 362880.0f));
+  p = fma(p, s, both(-1.0f / 5040.0f));
+  p = fma(p, s, both(1.0f / 120.0f));
+  p = fma(p, s, both(-1.0f / 6.0f));
+  const Two sn = add(x, fma(mul(x, s), p, d));
+  Two c = fma(both(1.0f / 479001600.0f), s, both(-1.0f / 3628800.0f));
+  c = fma(c, s, both(1.0f / 40320.0f));
+  c = fma(c, s, both(-1.0f / 720.0f));
+  c = fma(c, s, both(1.0f / 24.0f));
+  const Two w = fma(both(-0.5f), s, both(1.0f));
+  const Two lost = add(fma(both(-0.5f), s, add(both(1.0f), neg(w))), neg(fma(x, d, mul(both(0.5f), sl))));
+  const Two cs = add(w, fma(mul(s, s), c, lost));
+  float o[4];
+  const float cc[2] = {cs.a, cs.b}, ss[2] = {sn.a, sn.b};
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float a = (q[u] & 1) ? ss[u] : cc[u], b = (q[u] & 1) ? cc[u] : ss[u];
+    o[2 * u] = __uint_as_float(__float_as_uint(a) ^ (((q[u] + 1) & 2) << 30));
+    o[2 * u + 1] = __uint_as_float(__float_as_uint(b) ^ ((q[u] & 2) << 30));
+  }
+  return make_float4(o[0], o[1], o[2], o[3]);
 }
 
 __global__ void __launch_bounds__(kRopeThreads) rope_cs_kernel(const __grid_constant__ RopeArgs a) {
   const int two = threadIdx.x & 15;
-  uint64_t speed[2];
-  uint32_t low[2];
+  uint64_t speed[2], more[2];   // bits 2^-1 .. 2^-64 of a turn; 2^-33 .. 2^-96
   const int32_t* pos[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const uint32_t* w = a.plan.speed[2 * two + u];
     speed[u] = static_cast<uint64_t>(w[0]) << 32 | w[1];
-    low[u] = w[2];
+    more[u] = static_cast<uint64_t>(w[1]) << 32 | w[2];
     pos[u] = a.pos + a.plan.axis[2 * two + u] * a.axis_stride;
   }
-  for (long long i = static_cast<long long>(blockIdx.x) * kRopeAtOnce + (threadIdx.x >> 4); i < a.T;
-       i += static_cast<long long>(gridDim.x) * kRopeAtOnce) {
-    float2 r[2];
+  const long long step = static_cast<long long>(gridDim.x) * kRopeAtOnce;
+  long long i = static_cast<long long>(blockIdx.x) * kRopeAtOnce + (threadIdx.x >> 4);
+  int next[2] = {0, 0};
+  if (i < a.T) {
+    next[0] = __ldg(pos[0] + i);
+    next[1] = __ldg(pos[1] + i);
+  }
+  for (; i < a.T; i += step) {
+    const int now[2] = {next[0], next[1]};
+    if (i + step < a.T) {
+      next[0] = __ldg(pos[0] + i + step);
+      next[1] = __ldg(pos[1] + i + step);
+    }
+    uint64_t t[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const long long p = static_cast<long long>(__ldg(pos[u] + i)) + a.shift;
-      const uint64_t m = static_cast<uint64_t>(p < 0 ? -p : p);
-      uint64_t t = m * speed[u] + ((m * low[u]) >> 32);
-      r[u] = cos_sin_of_turns(p < 0 ? 0 - t : t);
+      // position p = low - (p < 0) 2^32, in [-2^32, 2^32)
+      const long long p = static_cast<long long>(now[u]) + a.shift;
+      const uint32_t low = static_cast<uint32_t>(p);
+      t[u] = speed[u] * low + __umulhi(low, static_cast<uint32_t>(more[u])) - (p < 0 ? more[u] : 0);
     }
-    reinterpret_cast<float4*>(a.out)[i * 16 + two] = make_float4(r[0].x, r[0].y, r[1].x, r[1].y);
+    reinterpret_cast<float4*>(a.out)[i * 16 + two] = cos_sin_of_turns(t);
   }
 }
 
