@@ -8,10 +8,12 @@
 // moves only when a logit exceeds it by more than kSlack (weights stay below 2^kSlack).
 //
 // What bounds it.  Every key is read by all the queries of its chunk, so the products: 4 * 512
-// flops for each (query, head, key).  On an SM a 128 x 64 x 16 product takes 50 cycles and a
-// 64 x 64 x 16 one 35 (operands from shared memory, measured), so that 64 rows on 64 keys cost
-// 36 * 35 + 16 * 51 = 2,060 cycles, half of the tensor core's peak rate; a 512-d fp32 output of more
-// than 64 rows and the logits beside it do not fit the tensor memory.
+// flops for each (query, head, key).  A 512-d fp32 output of more than 64 rows and the logits beside
+// it do not fit an SM's tensor memory, and products of 64 rows are bound by shared memory (128
+// bytes a cycle for operands): on one SM 36 products of 64 x 64 x 16 and 16 of 128 x 64 x 16 for 64 rows on
+// 64 keys take 2,060 cycles (measured: 35 and 51 each), half of the tensor core's peak rate, and the
+// copies' writes come on top.  Two SMs that share 128 rows and their keys read half of it:
+// 36 products of 128 x 128 x 16 (34 cycles) and 16 of 256 x 128 x 16 (69) for 128 rows on 128 keys.
 //
 // Four kernels, each started while the one before it ends:
 //   chunk_plan_kernel    the requests' key lists, the row blocks and their tiles as one line of
@@ -19,22 +21,28 @@
 //   chunk_decode_kernel  every key that some query sees, once, from its paged row to bf16 in the
 //                        order that the tensor core reads (the same rows are read by hundreds of row
 //                        blocks: decoding a tile takes longer than its products);
-//   chunk_attn_kernel    one block per SM, its share of the work;
+//   chunk_attn_kernel    one pair of blocks (a cluster) per two SMs, its share of the work;
 //   chunk_join_kernel    the row blocks that a share's border cuts in two or more.
 //
-// chunk_attn_kernel.  A row block is up to 64 rows of one request: 64 / H queries, or one query's
-// heads.  Its keys come in tiles of 64, two tiles in shared memory; P is one of two buffers; tensor
-// memory holds the output (4 blocks of 128 dims x 64 rows, dims as lanes) and two tiles' logits
-// (rows as lanes: a row's sums stay within four threads).  Roles:
-//   warps 0-7    softmax of a tile, 16 rows and 32 keys each: logits from tensor memory, P to shared
-//                memory (four warps of 64 keys each took 2,000 cycles a tile: 5.76 ms);
+// chunk_attn_kernel.  A row block is up to 128 rows of one request, 128 / H queries; the even block of
+// the pair has the first half of its rows, the odd one the second.  The keys come in tiles of 128.
+//   S  = Q K^T     each block gets its own rows x 128 keys; it holds its rows of Q and half of the
+//                  tile's keys, all dims (64 KB);
+//   O^T += V^T P^T each block gets all rows x two of the four blocks of 128 dims; it holds these dims of
+//                  all the tile's keys (64 KB) and its own rows of P (16 KB).
+// The products are issued for both by the even block.  Tensor memory: O in columns 0..255 (dims as
+// lanes), the logits of two tiles behind it (rows as lanes, 64 to 127 with the second half of
+// the keys).  Roles in each block:
+//   warps 0-7    softmax of a tile: a thread has one row and 32 keys; P to shared memory;
 //   warps 8-15   the next row block's queries (loaded and rotated while the last products of this one
 //                run), and the outputs;
-//   warp 16      one thread issues the products: S S O O of two tiles in turn, so that the softmax of
-//                one runs beside the products of the other, and the next two tiles' keys come while
-//                the O products run;
-//   warp 17      plans row blocks and sends for their keys (bulk copies, a pair of chunks of 64 dims
-//                at a time, as soon as the O product on the pair two tiles before is complete).
+//   warp 16      in the even block one thread issues the products, S of the next tile before O of this
+//                one, so that the softmax runs beside products; in the odd block one thread tells the
+//                even one which copies have arrived;
+//   warp 17      plans row blocks and sends for their keys (bulk copies of a block of 128 dims), as soon
+//                as the product on the same place's keys before is complete.
+// A row's reference belongs to its block, its output's columns to both: when a reference moves, the
+// factors go to the other block's shared memory, and a flag for every tile says whether they did.
 // Roundings as in list_attn.cu: the rotated query as two bf16 numbers, P in bf16 over the sum of the
 // rounded weights, all sums, references and partial outputs fp32.
 #include <algorithm>
@@ -49,18 +57,18 @@ namespace cskv {
 namespace {
 
 constexpr int kD = 512;
-constexpr int kTile = 64;                 // keys of a tile
-constexpr int kRows = 64;                 // rows of a row block
-constexpr int kChunk = kTile * 128;       // bytes of 64 dims of a tile
-constexpr int kPair = 2 * kChunk;         // of 128 dims: groups of 8 keys, each [64 dims][8 keys][128 B] twice
-constexpr int kStage = 4 * kPair;
+constexpr int kTile = 128;                // keys of a tile
+constexpr int kRows = 64;                 // rows of a block, at most; a row block has twice as many
+constexpr int kChunk = kRows * 128;       // bytes of 64 dims of the queries, of 64 keys of P
+constexpr int kKeyPart = 64 * 256;        // bytes of 128 dims of half a tile: groups of 8 keys, each [64 dims][8 keys][128 B] twice
+constexpr int kDimPart = kTile * 256;     // of a tile
 constexpr int kSoftWarps = 8, kOutWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kOutWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kOutThreads = kOutWarps * 32;
 constexpr uint32_t kTmemS = 256;          // TMEM columns: O 0..255, S from here, 64 for each tile
 constexpr float kSlack = 8.0f;            // base 2
-constexpr int kSms = 152;
+constexpr int kPairs = 76;                // of SMs
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanItems = 4;             // row blocks of a thread at a time
 constexpr int kItemUnits = 3;             // a row block's cost beside its tiles, a tile being 2
@@ -75,7 +83,7 @@ struct ReqPlan {
   int bad;                  // a row of it could not be read or is not finite
 };
 struct SplitPlan {
-  int item, b0, b1, pad;    // a row block that blocks b0 .. b1 share
+  int item, b0, b1, pad;    // a row block that pairs b0 .. b1 share
 };
 struct ChunkHead {
   int items, blocks, splits, pad;
@@ -99,7 +107,7 @@ struct ChunkArgs {
   uint8_t* out;
   float* lse;
   long long max_keys;
-  int group, head_blocks, heads_per_block;
+  int group;                // queries of a row block
   int most_blocks;          // shares at most
   // workspace
   ChunkHead* head;
@@ -108,13 +116,16 @@ struct ChunkArgs {
   SplitPlan* split;         // [most_blocks]
   uint8_t* flags;           // of every decoded row: 0, kNone, kUnfit
   uint8_t* images;          // decoded rows: of each request 4 blocks of 128 dims as they lie in a stage
-  float* opart;             // [2 * most_blocks][kRows][512]
-  float2* ml;               // [2 * most_blocks][kRows]: m (base 2) and l
+  float* opart;             // [2 * most_blocks][2 * kRows][512]
+  float2* ml;               // [2 * most_blocks][2 * kRows]: m (base 2) and l
   unsigned long long spin;
 };
 constexpr uint8_t kNone = 1, kUnfit = 2;
 
 __host__ __device__ inline int up16(int n) { return (n + 15) & ~15; }
+// Products of a pair of blocks have whole 32s of columns: each block has half of a tile's keys, rounded
+// up to 16 (columns behind the last key are seen by nobody).
+__device__ __forceinline__ int half_keys(int n) { return up16((n + 1) / 2); }
 
 // ---------------------------------------------------------------------------
 // row blocks
@@ -143,8 +154,7 @@ __device__ __forceinline__ int seen_entries(const ChunkArgs& a, const ReqPlan& p
 }
 __device__ __forceinline__ BlockKeys block_keys(const ChunkArgs& a, const ReqPlan& p, int x) {
   BlockKeys k;
-  const int g = a.head_blocks == 1 ? x : x / a.head_blocks;
-  k.i0 = g * a.group;
+  k.i0 = x * a.group;
   k.i1 = min(p.nq, k.i0 + a.group);
   const int p0 = p.len - p.nq + k.i0 + 1, p1 = p.len - p.nq + k.i1;   // position + 1 of the first and last one
   k.seen16 = up16(seen_entries(a, p, p1));
@@ -160,8 +170,8 @@ __device__ __forceinline__ BlockKeys block_keys(const ChunkArgs& a, const ReqPla
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 __device__ __forceinline__ int units_of(int tiles) { return 2 * max(tiles, 1) + kItemUnits; }
 
-// Shares: block b has the units [units * b / blocks, units * (b + 1) / blocks); tile t of a row block
-// begins at its unit 2 t and belongs to the block that has this unit.
+// Shares: pair b has the units [units * b / blocks, units * (b + 1) / blocks); tile t of a row block
+// begins at its unit 2 t and belongs to the pair that has this unit.
 __device__ __forceinline__ long long share_begin(long long units, int blocks, int b) { return units * b / blocks; }
 __device__ __forceinline__ int block_of_unit(long long units, int blocks, long long u) {
   return static_cast<int>(((u + 1) * blocks - 1) / units);
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       set_err(CSKV_ERR_BOUNDS);
       p.entries = p.entries16 = p.rows = p.rows16 = 0;
     }
-    const int blocks = (p.nq + a.group - 1) / a.group * a.head_blocks;
+    const int blocks = (p.nq + a.group - 1) / a.group;
     p.item0 = static_cast<int>(items + block_scan(blocks, part, &total) - blocks);
     items += total;
     if (r < a.R) a.req[r] = p;
@@ -387,10 +397,12 @@ struct __align__(16) RowSees {   // key k of the block's list is seen when k < s
 };
 
 struct Item {
-  int r0, nr, nq;                // rows [r0, r0 + nr) of the [T * H] rows; padded to 16
+  int row0, rows, half;          // rows [row0, row0 + rows) of the [T * H] rows, the first `half` of them in the even block
+  int r0, nr;                    // this block's
+  int nq;                        // columns of O for a block's rows: half, rounded up to 16
   int t0, one;                   // the first row's query; all rows are that query's
   int seen16, raw0, keys;        // the list (BlockKeys); raw0 counted among all decoded rows of the request
-  int begin, nt;                 // this block's tiles
+  int begin, nt;                 // this pair's tiles
   int plain;                     // keys below it are seen by every row
   int bad;
   int part;                      // partial output, -1: none
@@ -400,17 +412,65 @@ struct Item {
 
 struct ChunkSmem {
   Item item[2];
-  uint64_t full[2][4], free_[2][4];        // of a stage's pairs of chunks
-  uint64_t s_full[2], p_full[2];
-  uint64_t q_full, q_free, o_free, l_full[2], item_full[2], item_free[2], drained;
+  uint64_t k_full[4], k_free[4];           // keys: blocks of 128 dims
+  uint64_t v_full[2], v_free[2];           // this block's dims
+  uint64_t s_full[2], moved[2], p_full, q_full, q_free, o_free, l_full[2], f_full[2], item_full[2], item_free[2], drained;
   uint32_t tmem;
   int abort;
-  __align__(16) float fac[kRows];          // a moved reference's factors
-  float top[2][kRows];                     // a tile's largest logits, of either half of its keys
-  float4 sums[2][2][kRows];                // of a row block and a half: m (base 2), l, sum of the rounded weights
-  __align__(16) float out_fac[kRows];
+  int flag[2];                             // by tile: the other block's references moved
+  __align__(16) float fac[2][2 * kRows];   // by tile: a moved reference's factors, by columns of O
+  float top[4][kRows];                     // a tile's largest logits, of each quarter of its keys
+  float ref[2][kRows];                     // of a row block: m (base 2)
+  float2 sums[2][4][kRows];                // and of a quarter of its keys: l, the sum of the rounded weights
+  __align__(16) float out_fac[2][2 * kRows];   // of a row block, by columns of O
 };
 
+// Another block of the cluster's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void store_to(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void store_to(uint32_t at, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_release_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Products for both blocks of the pair (issued by the even one) and their completion, on the barrier
+// of both.
+__device__ __forceinline__ void mma2_add(uint32_t d, uint64_t da, uint64_t db, uint32_t id) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(id)
+      : "memory");
+}
+__device__ __forceinline__ void mma2_set(uint32_t d, uint64_t da, uint64_t db, uint32_t id) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(id)
+      : "memory");
+}
+__device__ __forceinline__ void mma2_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
 __device__ __forceinline__ bool wait_on(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
   const unsigned long long t0 = clock64();
   while (!try_wait_long(bar, parity)) {
@@ -445,31 +505,19 @@ __device__ __forceinline__ bool role_any(bool p) {
 }
 constexpr int kSoftId = 1, kOutId = 2;
 
-// 16 lanes x 32 columns: thread l has columns 8 j + 2 (l & 3) and + 1 of lane l / 4 in v[4 j], v[4 j + 1],
-// of lane l / 4 + 8 in v[4 j + 2], v[4 j + 3].
-__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float (&v)[16]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
-// Row block e of this block's share; one warp.
-__device__ void make_item(const ChunkArgs& a, Item* it, int e, long long units, int blocks) {
+// Row block e of this pair's share, and this block's rows of it; one warp.
+__device__ void make_item(const ChunkArgs& a, Item* it, int e, long long units, int blocks, int pair, int rank) {
   const int lane = threadIdx.x & 31;
   const ReqPlan p = a.req[request_of_item(a, e)];
-  const int x = e - p.item0;
-  const BlockKeys k = block_keys(a, p, x);
-  const int h0 = a.head_blocks == 1 ? 0 : (x % a.head_blocks) * a.heads_per_block;
-  const int nr = a.head_blocks == 1 ? (k.i1 - k.i0) * a.H : min(a.heads_per_block, a.H - h0);
+  const BlockKeys k = block_keys(a, p, e - p.item0);
+  const int rows = (k.i1 - k.i0) * a.H, half = (rows + 1) / 2;
+  const int at = rank == 0 ? 0 : half, nr = rank == 0 ? half : rows - half;   // of the row block
   const int raw0 = k.raw0 + p.row0;   // position of the list's first raw row
   int least = INT32_MAX;
   for (int r = lane; r < kRows; r += 32) {
     RowSees s{0, 0, -1, 0};
     if (r < nr) {
-      const int pos1 = p.len - p.nq + k.i0 + (a.head_blocks == 1 ? r / a.H : 0) + 1;
+      const int pos1 = p.len - p.nq + k.i0 + (at + r) / a.H + 1;
       s.seen = seen_entries(a, p, pos1);
       if (p.rows > 0 && pos1 > 0) {
         s.lo = k.seen16 + max(0, pos1 - a.window) - raw0;
@@ -482,10 +530,13 @@ __device__ void make_item(const ChunkArgs& a, Item* it, int e, long long units, 
   least = __reduce_min_sync(0xFFFFFFFFu, least);
   if (lane == 0) {
     it->t0 = p.q0 + k.i0;
-    it->one = a.head_blocks != 1 || a.group == 1;
-    it->r0 = it->t0 * a.H + h0;
+    it->one = k.i1 - k.i0 == 1;
+    it->row0 = it->t0 * a.H;
+    it->rows = rows;
+    it->half = half;
+    it->r0 = it->row0 + at;
     it->nr = nr;
-    it->nq = up16(nr);
+    it->nq = up16(half);
     it->seen16 = k.seen16;
     it->raw0 = p.entries16 + k.raw0;
     it->keys = k.keys;
@@ -496,18 +547,18 @@ __device__ void make_item(const ChunkArgs& a, Item* it, int e, long long units, 
     // its tiles between the share's borders
     const long long u0 = a.unit0[e];
     const int tiles = tiles_of(k.keys);
-    const long long lo = share_begin(units, blocks, blockIdx.x), hi = share_begin(units, blocks, blockIdx.x + 1);
+    const long long lo = share_begin(units, blocks, pair), hi = share_begin(units, blocks, pair + 1);
     const int begin = static_cast<int>(min(static_cast<long long>(tiles), max(0ll, (lo - u0 + 1) / 2)));
     const int end = static_cast<int>(min(static_cast<long long>(tiles), max(0ll, (hi - u0 + 1) / 2)));
     it->begin = begin;
     it->nt = end - begin;
-    it->part = begin > 0 || end < tiles ? 2 * blockIdx.x + (u0 > lo) : -1;
+    it->part = begin > 0 || end < tiles ? 2 * pair + (u0 > lo) : -1;
   }
 }
 
-// The row blocks of this block's share: [first, last].
-__device__ __forceinline__ void share_items(const ChunkArgs& a, const ChunkHead& h, int* first, int* last) {
-  const long long lo = share_begin(h.units, h.blocks, blockIdx.x), hi = share_begin(h.units, h.blocks, blockIdx.x + 1);
+// The row blocks of a pair's share: [first, last].
+__device__ __forceinline__ void share_items(const ChunkArgs& a, const ChunkHead& h, int pair, int* first, int* last) {
+  const long long lo = share_begin(h.units, h.blocks, pair), hi = share_begin(h.units, h.blocks, pair + 1);
   int e = item_of_unit(a.unit0, h.items, lo);
   const int tiles = (static_cast<int>(a.unit0[e + 1] - a.unit0[e]) - kItemUnits) / 2;
   if (a.unit0[e] + 2ll * (tiles - 1) < lo) ++e;   // its tiles are all before the border
@@ -560,140 +611,171 @@ __device__ __forceinline__ void rotate_queries(const ChunkArgs& a, const Item* i
   fence_proxy_async_smem();
 }
 
-// The softmax warps' state of two rows: r = 16 * (warp & 3) + lane / 4, and r + 8.
+// A softmax thread's state of its row.
 struct RowState {
-  float m[2], limit[2], msub[2];   // reference in units of q'.c; a logit above limit moves it; in base 2
-  float l[2], hat[2];              // this thread's sums of the weights, and of the rounded ones
+  float m, limit, msub;   // reference in units of q'.c; a logit above limit moves it; in base 2
+  float l, hat;           // this thread's sums of the weights, and of the rounded ones
   __device__ __forceinline__ void reset() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      m[i] = limit[i] = -INFINITY;
-      msub[i] = l[i] = hat[i] = 0.f;
-    }
+    m = limit = -INFINITY;
+    msub = l = hat = 0.f;
   }
 };
 
-// Logits of the keys k0 .. k0 + 31 that a row does not see become -inf, those of unfit rows NaN.
-__device__ __forceinline__ void mask_keys(const ChunkArgs& a, const Item* it, int k0, const RowSees (&sees)[2], float (&z)[16]) {
-  const int c = 2 * (threadIdx.x & 3);
+// Logits of the keys k0 .. k0 + 31 that the row does not see become -inf, those of unfit rows NaN.
+__device__ __forceinline__ void mask_keys(const ChunkArgs& a, const Item* it, int k0, const RowSees& s, float (&z)[32]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 32; ++j) {
+    const int k = k0 + j;
+    if (!(k < s.seen || (k >= s.lo && k <= s.hi))) z[j] = -INFINITY;
+  }
+  if (it->bad) {
+#pragma unroll 1
+    for (int j0 = 0; j0 < 32; j0 += 8) {   // eight rows' flags lie together (k0 and the list's parts are whole 8s)
+      const int k = k0 + j0;
+      if (k >= it->keys) break;
+      const uint8_t* at = a.flags + it->base + (k < it->seen16 ? k : it->raw0 + k - it->seen16);
+      const uint2 f = *reinterpret_cast<const uint2*>(at);
+      if ((f.x | f.y) == 0u) continue;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = k0 + 8 * j + c + u;
-      int flag = 0;
-      if (it->bad && k < it->keys) {
-        const int row = k < it->seen16 ? k : it->raw0 + k - it->seen16;
-        flag = a.flags[it->base + row];
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool see = (k < sees[i].seen || (k >= sees[i].lo && k <= sees[i].hi)) && flag != kNone;
-        float& x = z[4 * j + 2 * i + u];
-        x = !see ? -INFINITY : flag == kUnfit ? __int_as_float(0x7FC00000) : x;
+      for (int j = 0; j < 32; ++j) {
+        if ((j & ~7) != j0) continue;
+        const uint32_t x = byte_of((j & 4) ? f.y : f.x, j & 3);
+        if (x == kNone) z[j] = -INFINITY;
+        if (x == kUnfit && z[j] != -INFINITY) z[j] = __int_as_float(0x7FC00000);
       }
     }
   }
 }
 
-// The softmax of the block's tile g, the row block's tile t: this warp's 16 rows and 32 keys.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// The softmax of the pair's tile g, the row block's tile t: this thread's row and 32 keys.
 __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, const Item* it, uint8_t* ptile, uint32_t tmem,
-                                           int g, int t, bool first, const RowSees (&sees)[2], RowState& s) {
+                                           int rank, int g, int t, bool first, const RowSees& sees, RowState& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, half = warp >> 2;
+  const int quarter = warp & 3, side = warp >> 2;        // lanes of tensor memory; columns 32 side .. + 31
+  const int r = 32 * (quarter & 1) + lane;
   const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
-  const int buf = g & 1, k0 = t * kTile + 32 * half, r = 16 * quarter + (lane >> 2);
+  const int buf = g & 1;
+  const int n2 = half_keys(min(kTile, it->keys - t * kTile));
+  const int c0 = 32 * side;                              // the thread's first key within its half
+  const int k0 = (quarter >> 1) * n2 + c0;               // within the tile
+  const bool has = c0 < n2;
   wait_warp(sm, &sm->s_full[buf], (g >> 1) & 1, a.spin);
   tc_fence_after();
-  float z[16];
-  tmem_ld16x32(tmem + kTmemS + 64 * buf + 32 * half + tlane, z);
-  tmem_wait_ld();
-  if (k0 + 32 > it->plain || it->bad) mask_keys(a, it, k0, sees, z);
-  float top[2];
+  float z[32];
+  if (has) {
+    tmem_ld32(tmem + kTmemS + 64 * buf + c0 + tlane, z);
+    tmem_wait_ld();
+    if (n2 - c0 < 32) {   // a short tile: columns behind its last key
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    top[i] = fmaxf(fmaxf(fmaxf(z[2 * i], z[2 * i + 1]), fmaxf(z[4 + 2 * i], z[4 + 2 * i + 1])),
-                   fmaxf(fmaxf(z[8 + 2 * i], z[8 + 2 * i + 1]), fmaxf(z[12 + 2 * i], z[12 + 2 * i + 1])));
-  if (role_any<kSoftId, kSoftWarps * 32>(top[0] > s.limit[0] || top[1] > s.limit[1])) {   // some row's reference moves
+      for (int j = 0; j < 32; ++j)
+        if (c0 + j >= n2) z[j] = -INFINITY;
+    }
+    if (t * kTile + k0 + 32 > it->plain || it->bad) mask_keys(a, it, t * kTile + k0, sees, z);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
-      top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
-      if ((lane & 3) == 0) sm->top[half][r + 8 * i] = top[i];
+    for (int j = 0; j < 32; ++j) z[j] = -INFINITY;
+  }
+  float top = z[0];
+#pragma unroll
+  for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j]);
+  const bool moves = role_any<kSoftId, kSoftWarps * 32>(top > s.limit);
+  if (moves) {   // some row's reference moves
+    sm->top[2 * side + (quarter >> 1)][r] = top;
+    role_sync<kSoftId, kSoftWarps * 32>();
+    const float now = fmaxf(fmaxf(fmaxf(sm->top[0][r], sm->top[1][r]), fmaxf(sm->top[2][r], sm->top[3][r])), s.m);
+    const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
+    const float f = s.m == -INFINITY ? 0.f : exp2f(s.msub - sub);
+    s.m = now;
+    s.limit = now + a.slack;
+    s.msub = sub;
+    s.l *= f;
+    s.hat *= f;
+    if (!first && side == 0 && quarter < 2 && r < it->nq) {
+      float* to = &sm->fac[buf][rank * it->nq + r];
+      *to = f;
+      store_to(of_block(to, rank ^ 1), f);
     }
     role_sync<kSoftId, kSoftWarps * 32>();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float now = fmaxf(fmaxf(top[i], sm->top[half ^ 1][r + 8 * i]), s.m[i]);
-      const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
-      const float f = s.m[i] == -INFINITY ? 0.f : exp2f(s.msub[i] - sub);
-      s.m[i] = now;
-      s.limit[i] = now + a.slack;
-      s.msub[i] = sub;
-      s.l[i] *= f;
-      s.hat[i] *= f;
-      if (half == 0 && (lane & 3) == 0) sm->fac[r + 8 * i] = f;
-    }
-    if (!first) {
-      role_sync<kSoftId, kSoftWarps * 32>();
-      wait_warp(sm, &sm->free_[(g - 1) & 1][3], ((g - 1) >> 1) & 1, a.spin);   // the O product before is complete
-      tc_fence_after();
-#pragma unroll 1
-      for (int block = 2 * half; block < 2 * half + 2; ++block) {   // this warp's 32 dims of two blocks, 16 rows at a time
-#pragma unroll 1
-        for (int x = 0; x < it->nq; x += 16) {
-          float o[16];
-          const uint32_t at = tmem + tlane + block * kRows + x;
-          tmem_ld16(at, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] *= sm->fac[x + c];
-          tmem_st16(at, o);
-        }
-      }
-      tmem_wait_st();
-    }
   }
-  uint8_t* to = ptile + buf * kChunk + r * 128 + 4 * (lane & 3);
-  const int swz = lane >> 2;   // of both rows
+  if (threadIdx.x == 0) {   // (the barriers above order the warps' factors before it)
+    store_to(of_block(&sm->flag[buf], rank ^ 1), static_cast<int>(moves));
+    arrive_release_at(of_block(&sm->moved[buf], rank ^ 1));
+  }
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float x = exp2_fast(fmaf(z[2 * j], a.scale_log2, -s.msub));
+    const float y = exp2_fast(fmaf(z[2 * j + 1], a.scale_log2, -s.msub));
+    w[j] = pack_bf16(x, y);
+    s.l += x + y;
+    s.hat += bf16lo(w[j]) + bf16hi(w[j]);
+  }
+  // the O product before has read P, and its output may be rescaled
+  if (g > 0) {
+    wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
+    tc_fence_after();
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    const int k = k0 + 8 * j;
+    if (c0 + 8 * j < n2)
+      *reinterpret_cast<uint4*>(ptile + (k >> 6) * kChunk + r * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4)) =
+          make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+  wait_warp(sm, &sm->moved[buf], (g >> 1) & 1, a.spin);
+  if (!first) {
+    const bool theirs = *reinterpret_cast<volatile int*>(&sm->flag[buf]) != 0;
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+      if (!(u == rank ? moves : theirs)) continue;
+#pragma unroll 1
+      for (int x = u * it->nq; x < (u + 1) * it->nq; x += 8) {   // 32 dims of block `side`, 8 rows at a time
+        float o[8];
+        const uint32_t at = tmem + tlane + side * (2 * kRows) + x;
+        tmem_ld8(at, o);
+        tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float x = exp2_fast(fmaf(z[4 * j + 2 * i], a.scale_log2, -s.msub[i]));
-      const float y = exp2_fast(fmaf(z[4 * j + 2 * i + 1], a.scale_log2, -s.msub[i]));
-      const uint32_t w = pack_bf16(x, y);
-      s.l[i] += x + y;
-      s.hat[i] += bf16lo(w) + bf16hi(w);
-      *reinterpret_cast<uint32_t*>(to + i * 1024 + (((4 * half + j) ^ swz) << 4)) = w;
+        for (int c = 0; c < 8; ++c) o[c] *= sm->fac[buf][x + c];
+        tmem_st8(at, o);
+      }
+      tmem_wait_st();
     }
   }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncwarp();
-  if (lane == 0) mbar_arrive(&sm->p_full[buf]);
+  if (lane == 0) arrive_at(of_block(&sm->p_full, 0));
 }
 
 // O^T out, in units of 8 rows of a block of 128 dims: a thread has one dim of them, a row's 32 dims
-// of a warp are one 64-byte run.
-__device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem) {
+// of a warp are one 64-byte run.  All rows of the row block, this block's dims.
+__device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem, int rank, int e) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;
-  const int r0 = it->r0, nr = it->nr;
   const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const unsigned H = a.H;
-  const int sets = (nr + 7) >> 3;
+  const int sets = it->nq >> 3;   // of each half of the rows
 #pragma unroll 1
   for (int x = (warp - kSoftWarps) >> 2; x < 4 * sets; x += kOutWarps / 4) {
-    const int block = x / sets, g = (x - block * sets) * 8;
+    const int which = x / sets, j = which >> 1, u = which & 1, g = (x - which * sets) * 8;   // block of dims, half of the rows, row
+    const int block = 2 * j + rank;
     const int d = block * 128 + quarter * 32 + lane;
+    const int r0 = it->row0 + (u == 0 ? 0 : it->half), nr = u == 0 ? it->half : it->rows - it->half;
+    if (g >= nr) continue;
     const bool turn = block == 3 && quarter >= 2 && it->part < 0;   // dims 448..511, turned back
     const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
     float2 w = make_float2(1.f, 0.f);
     if (turn && it->one) w = __ldg(cs + static_cast<size_t>(it->t0) * 32);
     float o[8];
     if (it->nt > 0) {
-      tmem_ld8(from + block * kRows + g, o);   // (columns behind the last row hold nothing of use)
+      tmem_ld8(from + j * (2 * kRows) + u * it->nq + g, o);   // (columns behind the last row hold nothing of use)
       tmem_wait_ld();
     } else {
 #pragma unroll
@@ -701,14 +783,14 @@ __device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, C
     }
 #pragma unroll
     for (int c = 0; c < 8; c += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[g + c]);
+      const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[e & 1][u * it->nq + g + c]);
       o[c] *= f.x;
       o[c + 1] *= f.y;
       o[c + 2] *= f.z;
       o[c + 3] *= f.w;
     }
     if (it->part >= 0) {
-      float* to = a.opart + (static_cast<size_t>(it->part) * kRows + g) * kD + d;
+      float* to = a.opart + (static_cast<size_t>(it->part) * (2 * kRows) + (r0 - it->row0) + g) * kD + d;
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         if (g + c < nr) to[c * kD] = o[c];
@@ -739,148 +821,231 @@ __device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, C
   }
 }
 
-// The factors that the rows' outputs take, their log-sum-exps or partial sums.
-__device__ __forceinline__ void finish_sums(const ChunkArgs& a, const Item* it, ChunkSmem* sm, int e) {
+// The factors that this block's rows' outputs take (to both blocks), their log-sum-exps or partial sums.
+__device__ __forceinline__ void finish_sums(const ChunkArgs& a, const Item* it, ChunkSmem* sm, int rank, int e) {
   const int r = threadIdx.x - kSoftWarps * 32;
-  if (r >= kRows) return;
+  if (r >= it->nq) return;
   float f = 0.f;
   if (r < it->nr) {
-    float4 s = sm->sums[e & 1][0][r];   // m, l, sum of the rounded weights
-    const float4 more = sm->sums[e & 1][1][r];
-    s.y += more.y;
-    s.z += more.z;
+    const float m = sm->ref[e & 1][r];
+    float2 s = sm->sums[e & 1][0][r];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      const float2 more = sm->sums[e & 1][k][r];
+      s.x += more.x;
+      s.y += more.y;
+    }
     const unsigned row = it->r0 + r;
     // the output is made of rounded weights: over their own sum a few large ones' roundings cancel
-    const float ratio = s.y == 0.f ? 1.f : s.y / s.z;
+    const float ratio = s.x == 0.f ? 1.f : s.x / s.y;
     if (it->part >= 0) {
-      a.ml[static_cast<size_t>(it->part) * kRows + r] = make_float2(s.x, s.y);
+      a.ml[static_cast<size_t>(it->part) * (2 * kRows) + (it->r0 - it->row0) + r] = make_float2(m, s.x);
       f = ratio;
     } else {
       const float sink = a.sink != nullptr ? __ldg(a.sink + row % static_cast<unsigned>(a.H)) : -INFINITY;
       const float s2 = sink * kLog2e;
-      const float M = fmaxf(s.x, s2);
-      const float w = exp2f(s.x - M);
-      const float total = s.y * w + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));
+      const float M = fmaxf(m, s2);
+      const float w = exp2f(m - M);
+      const float total = s.x * w + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));
       // no key, or a sink above fp32 in base 2 (which leaves the keys nothing): out 0, lse the sink itself
-      const bool none = s.y == 0.f || s2 == INFINITY;
+      const bool none = s.x == 0.f || s2 == INFINITY;
       f = none ? 0.f : w / total * ratio;
-      if (s.y != s.y) f = s.y;
-      if (a.lse != nullptr) a.lse[row] = none ? sink : s.y != s.y ? s.y : (M + log2f(total)) * kLn2;
+      if (s.x != s.x) f = s.x;
+      if (a.lse != nullptr) a.lse[row] = none ? sink : s.x != s.x ? s.x : (M + log2f(total)) * kLn2;
     }
   }
-  sm->out_fac[r] = f;
+  float* to = &sm->out_fac[e & 1][rank * it->nq + r];
+  *to = f;
+  store_to(of_block(to, rank ^ 1), f);
 }
 
-// S of a tile: 64 rows x 64 keys, K = 512 dims and the second halves of the 64 rotated ones
+// S of a tile: 64 dims (chunk c) of the queries and the keys, with chunk 7 the second halves of its
+// rotated queries
 __device__ __forceinline__ void issue_s_chunk(uint32_t d, uint64_t dq, uint64_t dk, int c, uint32_t id) {
-  const uint64_t q = dq + c * (kChunk >> 4), k = dk + (c >> 1) * (kPair >> 4) + (c & 1) * (1024 >> 4);
-  if (c == 0) mma_set(d, q, k, id);
-  else mma_add(d, q, k, id);
+  const uint64_t q = dq + c * (kChunk >> 4), k = dk + (c >> 1) * (kKeyPart >> 4) + (c & 1) * (1024 >> 4);
+  if (c == 0) mma2_set(d, q, k, id);
+  else mma2_add(d, q, k, id);
 #pragma unroll
-  for (int x = 1; x < 4; ++x) mma_add(d, q + 2 * x, k + 2 * x, id);
+  for (int x = 1; x < 4; ++x) mma2_add(d, q + 2 * x, k + 2 * x, id);
   if (c == 7) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) mma_add(d, q + (kChunk >> 4) + 2 * x, k + 2 * x, id);
+    for (int x = 0; x < 4; ++x) mma2_add(d, q + (kChunk >> 4) + 2 * x, k + 2 * x, id);
   }
 }
 
-constexpr size_t kChunkSmemBytes = 1024 + 2 * size_t(kStage) + 9 * size_t(kChunk) + 2 * size_t(kChunk) + sizeof(ChunkSmem);
+// `rows` rows of the list from `k` on, `bytes` each of 16 (a block of dims at `image`, 256 bytes a row)
+// into shared memory: entries, raw rows, or both.
+__device__ __forceinline__ void send_for(const Item* it, uint8_t* to, const uint8_t* image, int k, int rows, uint64_t* full) {
+  const int ne = max(0, min(rows, it->seen16 - k)), nr = rows - ne;
+  if (ne > 0) bulk_g2s(to, image + static_cast<long long>(k) * 256, ne * 256, full);
+  if (nr > 0)
+    bulk_g2s(to + ne * 256, image + static_cast<long long>(it->raw0 + k + ne - it->seen16) * 256, nr * 256, full);
+}
+
+constexpr size_t kChunkSmemBytes = 1024 + 9 * size_t(kChunk) + 4 * size_t(kKeyPart) + 2 * size_t(kDimPart) + 2 * size_t(kChunk) + sizeof(ChunkSmem);
 static_assert(kChunkSmemBytes <= 227 * 1024, "one block per SM");
 
-__global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* ktile = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // 2 stages of 64 keys
-  uint8_t* qtile = ktile + 2 * kStage;                                            // 9 chunks
-  uint8_t* ptile = qtile + 9 * kChunk;                                            // 2 of 64 rows x 64 keys
+  uint8_t* qtile = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // 9 chunks (the same place in both blocks)
+  uint8_t* ktile = qtile + 9 * kChunk;       // half a tile's keys, four blocks of 128 dims
+  uint8_t* vtile = ktile + 4 * kKeyPart;     // a tile's keys, two blocks of 128 dims
+  uint8_t* ptile = vtile + 2 * kDimPart;     // this block's rows x 2 x 64 keys
   ChunkSmem* sm = reinterpret_cast<ChunkSmem*>(ptile + 2 * kChunk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = cluster_rank(), pair = blockIdx.x >> 1;
 
   if (tid == 0) {
+    const int both = rank == 0 ? 2 : 1;      // the even block hears of the odd one's copies
+    for (int m = 0; m < 4; ++m) {
+      mbar_init(&sm->k_full[m], both);
+      mbar_init(&sm->k_free[m], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      for (int m = 0; m < 4; ++m) {
-        mbar_init(&sm->full[i][m], 1);
-        mbar_init(&sm->free_[i][m], 1);
-      }
+      mbar_init(&sm->v_full[i], both);
+      mbar_init(&sm->v_free[i], 1);
       mbar_init(&sm->s_full[i], 1);
-      mbar_init(&sm->p_full[i], kSoftWarps);
+      mbar_init(&sm->moved[i], 1);
       mbar_init(&sm->l_full[i], kSoftWarps);
+      mbar_init(&sm->f_full[i], 1);
       mbar_init(&sm->item_full[i], 1);
       mbar_init(&sm->item_free[i], 1 + kSoftWarps + kOutWarps);
     }
-    mbar_init(&sm->q_full, kOutWarps);
+    mbar_init(&sm->p_full, 2 * kSoftWarps);
+    mbar_init(&sm->q_full, 2 * kOutWarps);
     mbar_init(&sm->q_free, 1);
-    mbar_init(&sm->o_free, kOutWarps);
+    mbar_init(&sm->o_free, 2 * kOutWarps);
     mbar_init(&sm->drained, 1);
     sm->abort = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(&sm->tmem, 512);
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
   grid_dep_wait();
   grid_dep_launch();
   const ChunkHead head = *a.head;
   int first = 0, last = -1;
-  if (blockIdx.x < head.blocks && head.items > 0) share_items(a, head, &first, &last);
+  if (pair < head.blocks && head.items > 0) share_items(a, head, pair, &first, &last);
   const int items = last - first + 1;
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                          // the other block's barriers are there
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
 
   if (warp == kLoadWarp) {                 // ---- row blocks and keys
     bool ok = true;
-    int g = 0, pairs = 0;                  // tiles sent for, and pairs of chunks of one more
+    int gk = 0, gv = 0, parts = 0;         // tiles sent for: keys, dims; and parts of one more (4 + of dims)
     fence_proxy_async_global();            // (the decoded rows, by another kernel's plain stores)
-    for (int e = 0; e < items && ok; ++e) {
-      Item* it = &sm->item[e & 1];
-      if (e >= 2) ok = wait_warp(sm, &sm->item_free[e & 1], ((e >> 1) - 1) & 1, a.spin);
-      if (!ok) break;
-      make_item(a, it, first + e, head.units, head.blocks);
+    auto plan = [&](int e) {
+      if (e >= 2) ok = ok && wait_warp(sm, &sm->item_free[e & 1], ((e >> 1) - 1) & 1, a.spin);
+      if (!ok) return;
+      make_item(a, &sm->item[e & 1], first + e, head.units, head.blocks, pair, rank);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->item_full[e & 1]);
-      if (lane == 0) {
-        const uint8_t* image = a.images + it->base * (2 * kD);
-        const long long stride = it->stride;
-        const int nt = it->nt, keys = it->keys, seen16 = it->seen16, raw0 = it->raw0;
-        for (int t = 0; t < nt && ok; ++t) {
-          const int k0 = (it->begin + t) * kTile, n = min(kTile, keys - k0);
-          const int ne = max(0, min(n, seen16 - k0)), nr = n - ne;   // entries, raw rows (whole 16s)
-          const uint8_t* from = image + static_cast<long long>(ne > 0 ? k0 : raw0 + k0 - seen16) * 256;
-          const int stage = g & 1;
-          uint8_t* to = ktile + stage * kStage;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            uint64_t* full = &sm->full[stage][m];
-            if (g >= 2) ok = ok && wait_bar(sm, &sm->free_[stage][m], ((g >> 1) - 1) & 1, a.spin);
-            if (ok) {
-              mbar_expect_tx(full, n * 256);
-              bulk_g2s(to + m * kPair, from + m * stride, (ne > 0 ? ne : nr) * 256, full);
-              if (ne > 0 && nr > 0)
-                bulk_g2s(to + m * kPair + ne * 256, image + m * stride + static_cast<long long>(raw0) * 256, nr * 256, full);
-              pairs = m + 1;
-            }
-          }
-          if (ok) { ++g; pairs = 0; }
+    };
+    // (one lane each)
+    auto send_keys = [&](const Item* it, int t) {
+      const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0), n2 = half_keys(n);
+      const int mine = rank == 0 ? min(n, n2) : n - min(n, n2);
+      const uint8_t* image = a.images + it->base * (2 * kD);
+#pragma unroll 1
+      for (int m = 0; m < 4 && ok; ++m) {
+        if (gk > 0) ok = wait_bar(sm, &sm->k_free[m], (gk - 1) & 1, a.spin);
+        if (!ok) break;
+        mbar_expect_tx(&sm->k_full[m], mine * 256);
+        send_for(it, ktile + m * kKeyPart, image + m * it->stride, k0 + rank * n2, mine, &sm->k_full[m]);
+        parts = m + 1;
+      }
+      if (ok) { ++gk; parts = 0; }
+    };
+    auto send_dims = [&](const Item* it, int t) {
+      const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0);
+      const uint8_t* image = a.images + it->base * (2 * kD);
+#pragma unroll 1
+      for (int j = 0; j < 2 && ok; ++j) {
+        if (gv > 0) ok = wait_bar(sm, &sm->v_free[j], (gv - 1) & 1, a.spin);
+        if (!ok) break;
+        mbar_expect_tx(&sm->v_full[j], n * 256);
+        send_for(it, vtile + j * kDimPart, image + (2 * j + rank) * it->stride, k0, n, &sm->v_full[j]);
+        parts = 4 + j + 1;
+      }
+      if (ok) { ++gv; parts = 0; }
+    };
+    if (items > 0) plan(0);
+    bool sent = false;                     // the keys of this row block's first tile have been sent for
+    for (int e = 0; e < items && ok; ++e) {
+      const Item* it = &sm->item[e & 1];
+      const int nt = it->nt;
+      if (lane == 0 && nt > 0) {
+        if (!sent) send_keys(it, 0);
+        for (int t = 0; t + 1 < nt && ok; ++t) {
+          send_keys(it, t + 1);
+          send_dims(it, t);
         }
       }
-      g = __shfl_sync(0xFFFFFFFFu, g, 0);
-      pairs = __shfl_sync(0xFFFFFFFFu, pairs, 0);
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      // the next row block's first keys before this one's last dims
+      if (ok && e + 1 < items) plan(e + 1);
+      sent = ok && e + 1 < items && sm->item[(e + 1) & 1].nt > 0;
+      if (lane == 0 && ok) {
+        if (sent && nt > 0) send_keys(&sm->item[(e + 1) & 1], 0);
+        if (nt > 0 && ok) send_dims(it, nt - 1);
+      }
+      sent = sent && nt > 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
     }
-    // copies in flight (there are none, unless a wait gave up): the last ones to each pair of chunks
+    // copies in flight (there are none, unless a wait gave up): the last ones to each place
     if (lane == 0) {
-      for (int i = 0; i < 8; ++i) {
-        const int stage = i >> 2, m = i & 3;
-        const int sent = (g + 1 - stage) / 2 + (stage == (g & 1) && m < pairs);
-        if (sent > 0) mbar_wait(&sm->full[stage][m], (sent - 1) & 1, kDefaultSpinLimit);
+      for (int m = 0; m < 4; ++m) {
+        const int n = gk + (parts < 4 && m < parts ? 1 : 0);
+        if (n > 0) mbar_wait(&sm->k_full[m], (n - 1) & 1, kDefaultSpinLimit);
       }
+      for (int j = 0; j < 2; ++j) {
+        const int n = gv + (parts > 4 + j ? 1 : 0);
+        if (n > 0) mbar_wait(&sm->v_full[j], (n - 1) & 1, kDefaultSpinLimit);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp && rank == 1) {   // ---- tells the even block of this one's copies
+    if (elect_lane()) {
+      bool ok = true;
+      int g = 0;
+      auto keys = [&](int i) {
+#pragma unroll 1
+        for (int m = 0; m < 4 && ok; ++m) {
+          ok = wait_bar(sm, &sm->k_full[m], i & 1, a.spin);
+          if (ok) arrive_at(of_block(&sm->k_full[m], 0));
+        }
+      };
+      auto dims = [&](int i) {
+#pragma unroll 1
+        for (int j = 0; j < 2 && ok; ++j) {
+          ok = wait_bar(sm, &sm->v_full[j], i & 1, a.spin);
+          if (ok) arrive_at(of_block(&sm->v_full[j], 0));
+        }
+      };
+      for (int e = 0; e < items && ok; ++e) {
+        ok = wait_bar(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
+        if (!ok) break;
+        const int nt = sm->item[e & 1].nt;
+        mbar_arrive(&sm->item_free[e & 1]);
+        if (nt > 0) keys(g);
+        for (int t = 0; t < nt && ok; ++t, ++g) {
+          if (t + 1 < nt) keys(g + 1);
+          dims(g);
+        }
+      }
+      mbar_wait(&sm->drained, 0, 2 * kDefaultSpinLimit);   // the even block's last commit has come (before this block ends)
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {           // ---- products
     if (elect_lane()) {
-      const uint32_t ids = make_idesc(1, 1, 0, 0, 64, 64);
       const uint64_t dq = smem_desc_sw128(smem_u32(qtile), 16, 1024);
       const uint64_t dk = smem_desc_sw128(smem_u32(ktile), 16, 2048);
-      const uint64_t dv = smem_desc_sw128(smem_u32(ktile), 1024, 2048);
+      const uint64_t dv = smem_desc_sw128(smem_u32(vtile), 1024, 2048);
       const uint64_t dp = smem_desc_sw128(smem_u32(ptile), 16, 1024);
       bool ok = true;
       int g = 0;
@@ -889,68 +1054,70 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         if (!ok) break;
         const Item* it = &sm->item[e & 1];
         const int nt = it->nt, keys = it->keys - it->begin * kTile;
-        const uint32_t ido = make_idesc(1, 1, 1, 0, 128, 0) | (static_cast<uint32_t>(it->nq >> 3) << 17);
+        const uint32_t ido = make_idesc(1, 1, 1, 0, 256, 0) | (static_cast<uint32_t>(it->nq >> 2) << 17);   // 2 nq columns
         ok = wait_bar(sm, &sm->q_full, e & 1, a.spin);
         tc_fence_after();
+        auto issue_s = [&](int t) {
+          const int i = g + t;
+          const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) |
+                               (static_cast<uint32_t>(half_keys(min(kTile, keys - t * kTile)) >> 2) << 17);
+          const uint32_t d = tmem + kTmemS + 64 * (i & 1);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if ((c & 1) == 0) {
+              ok = ok && wait_bar(sm, &sm->k_full[c >> 1], i & 1, a.spin);
+              tc_fence_after();
+            }
+            if (ok) issue_s_chunk(d, dq, dk, c, ids);
+            if ((c & 1) == 1) mma2_commit(&sm->k_free[c >> 1]);
+          }
+          mma2_commit(&sm->s_full[i & 1]);
+          if (t == nt - 1) mma2_commit(&sm->q_free);
+        };
         // before this row block's first O product the outputs of the one before are read (a row block
         // without tiles waits too: its own outputs would be told from those by nothing)
-        bool waited = e == 0;
         auto outputs_read = [&]() {
-          if (!waited) {
+          if (e > 0) {
             ok = ok && wait_bar(sm, &sm->o_free, (e - 1) & 1, a.spin);
             tc_fence_after();
-            waited = true;
           }
         };
         if (nt == 0) {
           outputs_read();
-          mma_commit(&sm->q_free);
+          mma2_commit(&sm->q_free);
+        } else if (ok) {
+          issue_s(0);
         }
-        for (int t = 0; t < nt && ok; t += 2) {
-          const int two = min(2, nt - t);
-          for (int u = 0; u < two && ok; ++u) {
-            const int i = g + u, stage = i & 1;
-            const uint64_t k = dk + stage * (kStage >> 4);
-            const uint32_t d = tmem + kTmemS + 64 * stage;
+        for (int t = 0; t < nt && ok; ++t) {
+          const int i = g + t;
+          if (t + 1 < nt) issue_s(t + 1);
+          if (t == 0) outputs_read();
+          const int ks = min(kTile, keys - t * kTile) >> 4;
+          ok = ok && wait_bar(sm, &sm->p_full, i & 1, a.spin);
+          if (!ok) break;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              if ((c & 1) == 0) {
-                ok = ok && wait_bar(sm, &sm->full[stage][c >> 1], (i >> 1) & 1, a.spin);
-                tc_fence_after();
-              }
-              if (ok) issue_s_chunk(d, dq, k, c, ids);
-            }
-            mma_commit(&sm->s_full[stage]);
-          }
-          if (t + two == nt) mma_commit(&sm->q_free);
-          outputs_read();
-          for (int u = 0; u < two && ok; ++u) {
-            const int i = g + u, stage = i & 1;
-            const int ks = min(kTile, keys - (t + u) * kTile) >> 4;
-            ok = ok && wait_bar(sm, &sm->p_full[stage], (i >> 1) & 1, a.spin);
-            if (!ok) break;
+          for (int j = 0; j < 2; ++j) {
+            ok = ok && wait_bar(sm, &sm->v_full[j], i & 1, a.spin);
             tc_fence_after();
-            const uint64_t v = dv + stage * (kStage >> 4), p = dp + stage * (kChunk >> 4);
+            if (!ok) break;
+            const uint64_t v = dv + j * (kDimPart >> 4);
+            const uint32_t d = tmem + j * (2 * kRows);
+            if (t == 0) mma2_set(d, v, dp, ido);
+            else mma2_add(d, v, dp, ido);
+            if (ks == 8) {
 #pragma unroll
-            for (int mb = 0; mb < 4; ++mb) {
-              const uint64_t vb = v + mb * (kPair >> 4);
-              if (t + u == 0) mma_set(tmem + mb * kRows, vb, p, ido);
-              else mma_add(tmem + mb * kRows, vb, p, ido);
-              if (ks == 4) {
-#pragma unroll
-                for (int k = 1; k < 4; ++k) mma_add(tmem + mb * kRows, vb + k * 256, p + 2 * k, ido);
-              } else {
+              for (int k = 1; k < 8; ++k) mma2_add(d, v + k * 256, dp + (k >> 2) * (kChunk >> 4) + 2 * (k & 3), ido);
+            } else {
 #pragma unroll 1
-                for (int k = 1; k < ks; ++k) mma_add(tmem + mb * kRows, vb + k * 256, p + 2 * k, ido);
-              }
-              mma_commit(&sm->free_[stage][mb]);
+              for (int k = 1; k < ks; ++k) mma2_add(d, v + k * 256, dp + (k >> 2) * (kChunk >> 4) + 2 * (k & 3), ido);
             }
+            mma2_commit(&sm->v_free[j]);
           }
-          g += two;
         }
+        g += nt;
         mbar_arrive(&sm->item_free[e & 1]);
       }
-      mma_commit(&sm->drained);   // before the tensor memory is given back (and shared memory)
+      mma2_commit(&sm->drained);   // before the tensor memory is given back (and shared memory)
       mbar_wait(&sm->drained, 0, kDefaultSpinLimit);
     }
     __syncwarp();
@@ -960,22 +1127,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       const bool there = wait_warp(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
       if (role_any<kSoftId, kSoftWarps * 32>(!there)) break;
       const Item* it = &sm->item[e & 1];
-      const int r = 16 * (warp & 3) + (lane >> 2);
-      const RowSees sees[2] = {it->sees[r], it->sees[r + 8]};
+      const int r = 32 * (warp & 1) + lane;
+      const RowSees sees = it->sees[r];
       RowState s;
       s.reset();
       const int nt = it->nt;
-      for (int t = 0; t < nt; ++t, ++g) weigh_tile(a, sm, it, ptile, tmem, g, it->begin + t, t == 0, sees, s);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          s.l[i] += __shfl_xor_sync(0xFFFFFFFFu, s.l[i], o);
-          s.hat[i] += __shfl_xor_sync(0xFFFFFFFFu, s.hat[i], o);
-        }
-        if ((lane & 3) == 0)
-          sm->sums[e & 1][warp >> 2][r + 8 * i] = make_float4(s.m[i] == -INFINITY ? -INFINITY : s.msub[i], s.l[i], s.hat[i], 0.f);
-      }
+      for (int t = 0; t < nt; ++t, ++g) weigh_tile(a, sm, it, ptile, tmem, rank, g, it->begin + t, t == 0, sees, s);
+      const int quarter = 2 * (warp >> 2) + ((warp >> 1) & 1);   // of the keys
+      if (quarter == 0) sm->ref[e & 1][r] = s.m == -INFINITY ? -INFINITY : s.msub;
+      sm->sums[e & 1][quarter][r] = make_float2(s.l, s.hat);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&sm->l_full[e & 1]);
@@ -993,7 +1153,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
       request_queries(a, it, qtile);
       rotate_queries(a, it, qtile);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->q_full);
+      if (lane == 0) arrive_at(of_block(&sm->q_full, 0));
     };
     bool there = items > 0 && item_there(0);
     if (there) queries(0);
@@ -1006,15 +1166,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         if (there) queries(e + 1);
       }
       wait_warp(sm, &sm->l_full[e & 1], (e >> 1) & 1, a.spin);
-      finish_sums(a, it, sm, e);
+      finish_sums(a, it, sm, rank, e);
       role_sync<kOutId, kOutThreads>();
-      if (it->nt > 0) wait_warp(sm, &sm->free_[(g - 1) & 1][3], ((g - 1) >> 1) & 1, a.spin);
+      if (tid == kSoftWarps * 32) arrive_release_at(of_block(&sm->f_full[e & 1], rank ^ 1));
+      wait_warp(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
+      if (it->nt > 0) wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
       tc_fence_after();
-      write_rows(a, it, sm, tmem);
+      write_rows(a, it, sm, tmem, rank, e);
       tc_fence_before();
-      role_sync<kOutId, kOutThreads>();   // (out_fac is read; this row block's sums too)
+      __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&sm->o_free);
+        arrive_at(of_block(&sm->o_free, 0));
         mbar_arrive(&sm->item_free[e & 1]);
       }
     }
@@ -1022,9 +1184,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                          // nobody writes into or reads from a block that has ended
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
 }
 
@@ -1040,18 +1203,17 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
   grid_dep_wait();
   const ChunkHead head = *a.head;
   const int share = threadIdx.x >> 6, lane = threadIdx.x & 31, d = (threadIdx.x & 63) * 8;
-  for (int x = blockIdx.x; x < head.splits * kRows; x += gridDim.x) {
-    const SplitPlan sp = a.split[x / kRows];
-    const int r = x % kRows;
+  for (int x = blockIdx.x; x < head.splits * (2 * kRows); x += gridDim.x) {
+    const SplitPlan sp = a.split[x / (2 * kRows)];
+    const int r = x % (2 * kRows);
     const ReqPlan p = a.req[request_of_item(a, sp.item)];
-    const int y = sp.item - p.item0;
-    const int g = a.head_blocks == 1 ? y : y / a.head_blocks, h0 = a.head_blocks == 1 ? 0 : (y % a.head_blocks) * a.heads_per_block;
-    const int nr = a.head_blocks == 1 ? min(p.nq - g * a.group, a.group) * a.H : min(a.heads_per_block, a.H - h0);
+    const int i0 = (sp.item - p.item0) * a.group;
+    const int nr = min(p.nq - i0, a.group) * a.H;
     if (r >= nr) continue;   // (the whole block)
-    const size_t row = static_cast<size_t>(p.q0 + g * a.group) * a.H + h0 + r;
+    const size_t row = static_cast<size_t>(p.q0 + i0) * a.H + r;
     const bool late = a.unit0[sp.item] > share_begin(head.units, head.blocks, sp.b0);
     const int parts = sp.b1 - sp.b0 + 1;
-    auto slot = [&](int k) { return (2 * static_cast<size_t>(sp.b0 + k) + (k == 0 && late)) * kRows + r; };
+    auto slot = [&](int k) { return (2 * static_cast<size_t>(sp.b0 + k) + (k == 0 && late)) * (2 * kRows) + r; };
     const float sink = a.sink != nullptr ? __ldg(a.sink + row % a.H) : -INFINITY;
     const float s2 = sink * kLog2e;
     auto weight = [&](float2 v, float M) { return v.y == 0.f ? 0.f : v.y != v.y ? v.y : exp2f(v.x - M); };
@@ -1112,18 +1274,16 @@ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // How the row blocks and the workspace follow from the sizes alone.
 struct Layout {
-  int group, head_blocks, heads_per_block, most_blocks;
+  int group, most_blocks;
   size_t head, req, unit0, split, flags, images, opart, ml, bytes;
 };
 Layout layout_of(int R, int T, int H, int64_t max_keys) {
   Layout l = {};
-  l.head_blocks = (H + kRows - 1) / kRows;
-  l.heads_per_block = (H + l.head_blocks - 1) / l.head_blocks;
-  l.group = l.head_blocks == 1 ? kRows / H : 1;
+  l.group = std::max(1, 2 * kRows / H);
   // each request's last row block may be a short one
-  const int64_t items = (static_cast<int64_t>(T) / l.group + std::min(R, T)) * l.head_blocks;
+  const int64_t items = static_cast<int64_t>(T) / l.group + std::min(R, T);
   const int64_t tiles = items * ((max_keys + kTile - 1) / kTile + 1);
-  l.most_blocks = static_cast<int>(std::min<int64_t>(kSms, std::max<int64_t>(1, (2 * tiles + kItemUnits * items) / kLeastShare)));
+  l.most_blocks = static_cast<int>(std::min<int64_t>(kPairs, std::max<int64_t>(1, (2 * tiles + kItemUnits * items) / kLeastShare)));
   const size_t keys = static_cast<size_t>(max_keys + 15) & ~size_t(15);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t x = at; at += a256(bytes); return x; };
@@ -1133,8 +1293,8 @@ Layout layout_of(int R, int T, int H, int64_t max_keys) {
   l.split = take(sizeof(SplitPlan) * l.most_blocks);
   l.flags = take(keys);
   l.images = take(keys * (2 * kD));
-  l.opart = take(2 * static_cast<size_t>(l.most_blocks) * kRows * kD * 4);
-  l.ml = take(2 * static_cast<size_t>(l.most_blocks) * kRows * 8);
+  l.opart = take(2 * static_cast<size_t>(l.most_blocks) * (2 * kRows) * kD * 4);
+  l.ml = take(2 * static_cast<size_t>(l.most_blocks) * (2 * kRows) * 8);
   l.bytes = at;
   return l;
 }
@@ -1194,8 +1354,6 @@ cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t*
   a.lse = lse;
   a.max_keys = max_keys;
   a.group = l.group;
-  a.head_blocks = l.head_blocks;
-  a.heads_per_block = l.heads_per_block;
   a.most_blocks = l.most_blocks;
   a.head = reinterpret_cast<ChunkHead*>(ws + l.head);
   a.req = reinterpret_cast<ReqPlan*>(ws + l.req);
@@ -1211,13 +1369,13 @@ cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t*
   if (e != cudaSuccess) return e;
   const int64_t decode_warps = (max_keys + kDecodeRows - 1) / kDecodeRows;
   const unsigned decode_blocks = static_cast<unsigned>(
-      std::min<int64_t>(8 * kSms, std::max<int64_t>(1, (decode_warps + kDecodeThreads / 32 - 1) / (kDecodeThreads / 32))));
+      std::min<int64_t>(16 * kPairs, std::max<int64_t>(1, (decode_warps + kDecodeThreads / 32 - 1) / (kDecodeThreads / 32))));
   e = launch_next(chunk_decode_kernel, decode_blocks, kDecodeThreads, 0, stream, nullptr, a);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> allowed;
-  e = launch_next(chunk_attn_kernel, l.most_blocks, kThreads, kChunkSmemBytes, stream, &allowed, a);
+  e = launch_next(chunk_attn_kernel, 2 * l.most_blocks, kThreads, kChunkSmemBytes, stream, &allowed, a);
   if (e != cudaSuccess || l.most_blocks == 1) return e;
-  return launch_next(chunk_join_kernel, 4 * kSms, kJoinThreads, 0, stream, nullptr, a);
+  return launch_next(chunk_join_kernel, 8 * kPairs, kJoinThreads, 0, stream, nullptr, a);
 }
 
 unsigned int take_err_chunk_attn() { return take_dev_err(); }
