@@ -313,22 +313,78 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 // the keys
 // ---------------------------------------------------------------------------
-// 16 neighbouring dims of a row (lane's) as bf16 pairs
-__device__ __forceinline__ void decode16(const cskv_paged& c, const uint8_t* row, int lane, uint32_t (&w)[8]) {
-  if (c.fmt == CSKV_FMT_BF16) {
-    const uint4* p = reinterpret_cast<const uint4*>(row) + 2 * lane;
-    const uint4 x = __ldg(p), y = __ldg(p + 1);
+constexpr int kDecodeThreads = 256;
+constexpr int kDecodeRows = 8;    // of a warp at a time: a group of the image (a request's rows are whole 16s)
+
+// The bytes of 16 neighbouring dims of a row, and their scale.
+template <int FMT>
+struct RawRow;
+template <>
+struct RawRow<CSKV_FMT_BF16> {
+  uint4 x, y;
+  __device__ __forceinline__ void load(const uint8_t* row, int lane) {
+    x = __ldg(reinterpret_cast<const uint4*>(row) + 2 * lane);
+    y = __ldg(reinterpret_cast<const uint4*>(row) + 2 * lane + 1);
+  }
+  __device__ __forceinline__ void to_bf16(uint32_t (&w)[8]) const {
     w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
     w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
-  } else if (c.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32) {
-    convert(__ldg(reinterpret_cast<const uint4*>(row) + lane), __ldg(row + kD + (lane >> 1)), w);
-  } else {
-    convert(__ldg(reinterpret_cast<const uint2*>(row) + lane), __ldg(row + kD / 2 + lane), w);
   }
-}
+};
+template <>
+struct RawRow<CSKV_FMT_FP8_E4M3_E8M0_B32> {
+  uint4 codes;
+  uint32_t scale;
+  __device__ __forceinline__ void load(const uint8_t* row, int lane) {
+    codes = __ldg(reinterpret_cast<const uint4*>(row) + lane);
+    scale = __ldg(row + kD + (lane >> 1));
+  }
+  __device__ __forceinline__ void to_bf16(uint32_t (&w)[8]) const { convert(codes, scale, w); }
+};
+template <>
+struct RawRow<CSKV_FMT_FP4_E2M1_E4M3_B16> {
+  uint2 codes;
+  uint32_t scale;
+  __device__ __forceinline__ void load(const uint8_t* row, int lane) {
+    codes = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+    scale = __ldg(row + kD / 2 + lane);
+  }
+  __device__ __forceinline__ void to_bf16(uint32_t (&w)[8]) const { convert(codes, scale, w); }
+};
 
-constexpr int kDecodeThreads = 256;
-constexpr int kDecodeRows = 16;   // of a warp at a time (a request's rows are whole 16s)
+// Eight rows (lane i < 8 has row i's address, nullptr: none) into their group of the image; returns
+// a bit for each that is not finite, whose values become 0.  All loads are on their way before the
+// first is used.
+template <int FMT>
+__device__ __forceinline__ uint32_t decode_rows(const uint8_t* mine, uint8_t* image) {
+  const int lane = threadIdx.x & 31;
+  RawRow<FMT> raw[kDecodeRows] = {};
+#pragma unroll
+  for (int i = 0; i < kDecodeRows; ++i) {
+    const uint8_t* row = reinterpret_cast<const uint8_t*>(
+        __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), i));
+    if (row != nullptr) raw[i].load(row, lane);
+  }
+  const uint32_t there = __ballot_sync(0xFFFFFFFFu, mine != nullptr);
+  uint32_t unfit = 0;
+#pragma unroll
+  for (int i = 0; i < kDecodeRows; ++i) {
+    uint32_t w[8] = {}, bad = 0;
+    if ((there >> i) & 1u) raw[i].to_bf16(w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bad |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    if (__any_sync(0xFFFFFFFFu, bad != 0u)) {   // (an exponent of all ones carries into the sign bit)
+      unfit |= 1u << i;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = 0u;
+    }
+    const int at = 2 * (lane & 3);
+    uint8_t* to = image + i * 128;
+    *reinterpret_cast<uint4*>(to + ((at ^ i) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(to + (((at + 1) ^ i) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  return unfit;
+}
 
 __global__ void __launch_bounds__(kDecodeThreads) chunk_decode_kernel(const __grid_constant__ ChunkArgs a) {
   grid_dep_wait();
@@ -353,39 +409,19 @@ __global__ void __launch_bounds__(kDecodeThreads) chunk_decode_kernel(const __gr
     const cskv_paged& c = raw ? a.rows : a.entries;
     const int k0 = raw ? first - p.entries16 : first, have = raw ? p.rows : p.entries;
     const int row_bytes = c.fmt == CSKV_FMT_BF16 ? 2 * kD : c.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32 ? kD + kD / 32 : kD / 2 + kD / 16;
-    // lane i < 16 looks row i up
+    const bool exists = lane < kDecodeRows && k0 + lane < have;
     const uint8_t* mine = nullptr;
-    if (lane < kDecodeRows && k0 + lane < have)
-      mine = paged_row(c, r, (raw ? p.row0 : 0) + static_cast<long long>(k0) + lane, row_bytes).data;
+    if (exists) mine = paged_row(c, r, (raw ? p.row0 : 0) + static_cast<long long>(k0) + lane, row_bytes).data;
     uint8_t* image = a.images + p.base * (2 * kD) + (lane >> 3) * (rows * 256) + static_cast<long long>(first) * 256 +
                      ((lane >> 2) & 1) * 1024;
-    uint32_t unfit = 0;
-#pragma unroll 4
-    for (int i = 0; i < kDecodeRows; ++i) {
-      const uint8_t* row = reinterpret_cast<const uint8_t*>(
-          __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), i));
-      uint32_t w[8] = {};
-      if (row != nullptr) {
-        decode16(c, row, lane, w);
-        uint32_t bad = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) bad |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-        if (__any_sync(0xFFFFFFFFu, bad != 0u)) {   // (an exponent of all ones carries into the sign bit)
-          unfit |= 1u << i;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = 0u;
-        }
-      }
-      const int swz = i & 7, at = 2 * (lane & 3);
-      uint8_t* to = image + (i >> 3) * 2048 + swz * 128;
-      *reinterpret_cast<uint4*>(to + ((at ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(to + (((at + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+    const uint32_t unfit = c.fmt == CSKV_FMT_BF16 ? decode_rows<CSKV_FMT_BF16>(mine, image)
+                           : c.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32 ? decode_rows<CSKV_FMT_FP8_E4M3_E8M0_B32>(mine, image)
+                                                                : decode_rows<CSKV_FMT_FP4_E2M1_E4M3_B16>(mine, image);
+    if (lane < kDecodeRows) a.flags[x + lane] = mine == nullptr ? kNone : (unfit >> lane) & 1u ? kUnfit : 0;
+    // a row that is there and cannot be used (those behind the last one are seen by nobody)
+    if (__any_sync(0xFFFFFFFFu, exists && mine == nullptr) || unfit != 0u) {
+      if (lane == 0) a.req[r].bad = 1;
     }
-    const uint32_t none = __ballot_sync(0xFFFFFFFFu, lane < kDecodeRows && mine == nullptr);
-    if (lane < kDecodeRows) a.flags[x + lane] = (none >> lane) & 1u ? kNone : (unfit >> lane) & 1u ? kUnfit : 0;
-    // rows that are there but cannot be used; those behind the last one are seen by nobody
-    const uint32_t there = k0 + kDecodeRows <= have ? 0xFFFFu : (1u << max(0, have - k0)) - 1u;
-    if (lane == 0 && ((none & there) | unfit) != 0u) a.req[r].bad = 1;
   }
 }
 
@@ -442,9 +478,13 @@ __device__ __forceinline__ void store_to(uint32_t at, float v) {
 __device__ __forceinline__ void store_to(uint32_t at, int v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
+// Says that something is done: what the products read (P and the queries in their own block's shared
+// memory, tensor memory) is ordered before it by the proxy and tcgen05 fences.  With a release at
+// cluster scope, which waits for every write of the warp, a tile took 1.8 times as long.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Hands on what was stored to the other block; wait_pair receives it.
 __device__ __forceinline__ void arrive_release_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -485,6 +525,15 @@ __device__ __forceinline__ bool wait_on(ChunkSmem* sm, uint64_t* bar, uint32_t p
 }
 __device__ __forceinline__ bool wait_bar(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
   return try_wait_long(bar, parity) || wait_on(sm, bar, parity, limit);
+}
+// For what the other block stored here (arrive_release_at); a warp.
+__device__ __forceinline__ bool wait_pair(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
+  uint32_t ok = wait_bar(sm, bar, parity, limit);
+  if (ok)   // (complete: this one returns at once)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return __all_sync(0xFFFFFFFFu, ok) != 0;
 }
 __device__ __forceinline__ bool wait_warp(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
   return __all_sync(0xFFFFFFFFu, wait_bar(sm, bar, parity, limit)) != 0;
@@ -566,9 +615,11 @@ __device__ __forceinline__ void share_items(const ChunkArgs& a, const ChunkHead&
   *last = item_of_unit(a.unit0, h.items, hi - 1);
 }
 
-// Queries into the K-major chunks of Q (64 rows apart; rows behind the last one zero).  A thread
-// rotates what it loaded itself: chunk 7 holds the first bf16 of each rotated value, chunk 8 the second.
-__device__ __forceinline__ void request_queries(const ChunkArgs& a, const Item* it, uint8_t* qtile) {
+// Queries into the K-major chunks of Q (64 rows apart; rows behind the last one zero); the output
+// warps.  The last 64 dims are then rotated in place: chunk 7 holds the first bf16 of each rotated
+// value, chunk 8 the second.  (The angles are on their way while the queries are awaited: loaded row by
+// row, they took 5,600 cycles.)
+__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item* it, uint8_t* qtile) {
   const int tid = threadIdx.x - kSoftWarps * 32;
   const uint8_t* q = a.q + static_cast<size_t>(it->r0) * kD * 2;
   const int nr = it->nr;
@@ -579,34 +630,40 @@ __device__ __forceinline__ void request_queries(const ChunkArgs& a, const Item* 
     if (r < nr) cp_async16(dst, q + static_cast<size_t>(x) * 16);
     else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
   }
-}
-__device__ __forceinline__ void rotate_queries(const ChunkArgs& a, const Item* it, uint8_t* qtile) {
-  const int tid = threadIdx.x - kSoftWarps * 32;
-  const int c = tid & 63;   // of all of the thread's pieces (kOutThreads is a multiple of 64)
-  cp_async_wait_all();
-  if (c >= 56) {
-#pragma unroll 1
-    for (int r = tid >> 6; r < kRows; r += kOutThreads / 64) {
-      uint4* hi = reinterpret_cast<uint4*>(qtile + 7 * kChunk + sw128_offset(r, c & 7));
-      uint4 lo = make_uint4(0u, 0u, 0u, 0u);
-      if (r < it->nr) {
-        const float* cs = a.q_rope + static_cast<size_t>(static_cast<unsigned>(it->r0 + r) / static_cast<unsigned>(a.H)) * 64 + (c & 7) * 8;
-        const float4 t0 = __ldg(reinterpret_cast<const float4*>(cs)), t1 = __ldg(reinterpret_cast<const float4*>(cs + 4));
-        const float co[4] = {t0.x, t0.z, t1.x, t1.z}, si[4] = {t0.y, t0.w, t1.y, t1.w};
-        uint4 v = *hi;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-        uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+  static_assert(kRows * 8 == 2 * kOutThreads, "a thread rotates 8 dims of two rows");
+  float4 cs[2][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
-          const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
-          w[k] = pack_bf16(z0, z1);
-          l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
-        }
-        *hi = v;
-      }
-      *reinterpret_cast<uint4*>(qtile + 8 * kChunk + sw128_offset(r, c & 7)) = lo;
+  for (int u = 0; u < 2; ++u) {
+    const int r = (tid >> 3) + 32 * u;
+    if (r < nr) {
+      const float4* from = reinterpret_cast<const float4*>(
+          a.q_rope + static_cast<size_t>(static_cast<unsigned>(it->r0 + r) / static_cast<unsigned>(a.H)) * 64 + (tid & 7) * 8);
+      cs[u][0] = __ldg(from);
+      cs[u][1] = __ldg(from + 1);
     }
+  }
+  cp_async_wait_all();
+  role_sync<kOutId, kOutThreads>();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = (tid >> 3) + 32 * u, c = tid & 7;
+    uint4 lo = make_uint4(0u, 0u, 0u, 0u);
+    if (r < nr) {
+      uint4* hi = reinterpret_cast<uint4*>(qtile + 7 * kChunk + sw128_offset(r, c));
+      const float co[4] = {cs[u][0].x, cs[u][0].z, cs[u][1].x, cs[u][1].z}, si[4] = {cs[u][0].y, cs[u][0].w, cs[u][1].y, cs[u][1].w};
+      uint4 v = *hi;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+      uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
+        const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
+        w[k] = pack_bf16(z0, z1);
+        l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
+      }
+      *hi = v;
+    }
+    *reinterpret_cast<uint4*>(qtile + 8 * kChunk + sw128_offset(r, c)) = lo;
   }
   fence_proxy_async_smem();
 }
@@ -729,7 +786,7 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
       *reinterpret_cast<uint4*>(ptile + (k >> 6) * kChunk + r * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4)) =
           make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   }
-  wait_warp(sm, &sm->moved[buf], (g >> 1) & 1, a.spin);
+  wait_pair(sm, &sm->moved[buf], (g >> 1) & 1, a.spin);
   if (!first) {
     const bool theirs = *reinterpret_cast<volatile int*>(&sm->flag[buf]) != 0;
 #pragma unroll 1
@@ -754,35 +811,42 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
   if (lane == 0) arrive_at(of_block(&sm->p_full, 0));
 }
 
-// O^T out, in units of 8 rows of a block of 128 dims: a thread has one dim of them, a row's 32 dims
+// O^T out, in units of 16 rows of a block of 128 dims: a thread has one dim of them, a row's 32 dims
 // of a warp are one 64-byte run.  All rows of the row block, this block's dims.
 __device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem, int rank, int e) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;
   const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const unsigned H = a.H;
-  const int sets = it->nq >> 3;   // of each half of the rows
+  const int sets = it->nq >> 4;   // of each half of the rows
 #pragma unroll 1
   for (int x = (warp - kSoftWarps) >> 2; x < 4 * sets; x += kOutWarps / 4) {
-    const int which = x / sets, j = which >> 1, u = which & 1, g = (x - which * sets) * 8;   // block of dims, half of the rows, row
+    const int which = x / sets, j = which >> 1, u = which & 1, g = (x - which * sets) * 16;   // block of dims, half of the rows, row
     const int block = 2 * j + rank;
     const int d = block * 128 + quarter * 32 + lane;
-    const int r0 = it->row0 + (u == 0 ? 0 : it->half), nr = u == 0 ? it->half : it->rows - it->half;
-    if (g >= nr) continue;
+    const int r0 = it->row0 + (u == 0 ? 0 : it->half), nr = (u == 0 ? it->half : it->rows - it->half) - g;
+    if (nr <= 0) continue;
     const bool turn = block == 3 && quarter >= 2 && it->part < 0;   // dims 448..511, turned back
-    const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
-    float2 w = make_float2(1.f, 0.f);
-    if (turn && it->one) w = __ldg(cs + static_cast<size_t>(it->t0) * 32);
-    float o[8];
+    // even lanes turn and store the pair of dims (d, d + 1) of row c, odd lanes (d - 1, d) of row c + 1
+    const int odd = lane & 1;
+    float2 w[8];
+    if (turn) {
+      const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c == 0 || !it->one) w[c] = __ldg(cs + static_cast<size_t>((r0 + g + min(2 * c + odd, nr - 1)) / H) * 32);
+        else w[c] = w[0];
+    }
+    float o[16];
     if (it->nt > 0) {
-      tmem_ld8(from + j * (2 * kRows) + u * it->nq + g, o);   // (columns behind the last row hold nothing of use)
+      tmem_ld16(from + j * (2 * kRows) + u * it->nq + g, o);   // (columns behind the last row hold nothing of use)
       tmem_wait_ld();
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) o[c] = 0.f;
+      for (int c = 0; c < 16; ++c) o[c] = 0.f;
     }
 #pragma unroll
-    for (int c = 0; c < 8; c += 4) {
+    for (int c = 0; c < 16; c += 4) {
       const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[e & 1][u * it->nq + g + c]);
       o[c] *= f.x;
       o[c + 1] *= f.y;
@@ -792,31 +856,28 @@ __device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, C
     if (it->part >= 0) {
       float* to = a.opart + (static_cast<size_t>(it->part) * (2 * kRows) + (r0 - it->row0) + g) * kD + d;
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (g + c < nr) to[c * kD] = o[c];
+      for (int c = 0; c < 16; ++c)
+        if (c < nr) to[c * kD] = o[c];
       continue;
     }
     if (turn) {
-      // even lanes turn and store the pair of dims (d, d + 1) of row c, odd lanes (d - 1, d) of row c + 1
-      const bool odd = (lane & 1) != 0;
 #pragma unroll
-      for (int c = 0; c < 8; c += 2) {
-        const int r = g + c + (odd ? 1 : 0);
-        if (!it->one) w = __ldg(cs + static_cast<size_t>((r0 + min(r, nr - 1)) / H) * 32);
+      for (int c = 0; c < 16; c += 2) {
         const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[c] : o[c + 1], 1);
         const float y0 = odd ? other : o[c], y1 = odd ? o[c + 1] : other;
-        const uint32_t v = pack_bf16(y0 * w.x + y1 * w.y, y1 * w.x - y0 * w.y);
-        if (r < nr)
-          *reinterpret_cast<uint32_t*>(a.out + ((static_cast<size_t>(r0) + r) * kD + (d & ~1)) * 2) = v;
+        const float2 t = w[c / 2];
+        const uint32_t v = pack_bf16(y0 * t.x + y1 * t.y, y1 * t.x - y0 * t.y);
+        if (c + odd < nr)
+          *reinterpret_cast<uint32_t*>(a.out + ((static_cast<size_t>(r0) + g + c + odd) * kD + (d & ~1)) * 2) = v;
       }
       continue;
     }
     uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + (static_cast<size_t>(r0) + g) * kD + d;
 #pragma unroll
-    for (int c = 0; c < 8; c += 2) {
+    for (int c = 0; c < 16; c += 2) {
       const uint32_t v = pack_bf16(o[c], o[c + 1]);
-      if (g + c < nr) to[c * kD] = static_cast<uint16_t>(v);
-      if (g + c + 1 < nr) to[(c + 1) * kD] = static_cast<uint16_t>(v >> 16);
+      if (c < nr) to[c * kD] = static_cast<uint16_t>(v);
+      if (c + 1 < nr) to[(c + 1) * kD] = static_cast<uint16_t>(v >> 16);
     }
   }
 }
@@ -1150,8 +1211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     };
     auto queries = [&](int e) {
       const Item* it = &sm->item[e & 1];
-      request_queries(a, it, qtile);
-      rotate_queries(a, it, qtile);
+      load_queries(a, it, qtile);
       __syncwarp();
       if (lane == 0) arrive_at(of_block(&sm->q_full, 0));
     };
@@ -1169,7 +1229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       finish_sums(a, it, sm, rank, e);
       role_sync<kOutId, kOutThreads>();
       if (tid == kSoftWarps * 32) arrive_release_at(of_block(&sm->f_full[e & 1], rank ^ 1));
-      wait_warp(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
+      wait_pair(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
       if (it->nt > 0) wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
       tc_fence_after();
       write_rows(a, it, sm, tmem, rank, e);
