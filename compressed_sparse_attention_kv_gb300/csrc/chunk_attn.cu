@@ -454,11 +454,11 @@ struct ChunkSmem {
   uint32_t tmem;
   int abort;
   int flag[2];                             // by tile: the other block's references moved
-  __align__(16) float fac[2][2 * kRows];   // by tile: a moved reference's factors, by columns of O
+  __align__(16) float fac[2][2][kRows];    // by tile and block: a moved reference's factors
   float top[4][kRows];                     // a tile's largest logits, of each quarter of its keys
   float ref[2][kRows];                     // of a row block: m (base 2)
   float2 sums[2][4][kRows];                // and of a quarter of its keys: l, the sum of the rounded weights
-  __align__(16) float out_fac[2][2 * kRows];   // of a row block, by columns of O
+  __align__(16) float out_fac[2][2][kRows];   // of a row block, by block
 };
 
 // Another block of the cluster's shared memory.
@@ -472,21 +472,15 @@ __device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void store_to(uint32_t at, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
-}
-__device__ __forceinline__ void store_to(uint32_t at, int v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+// 4 bytes into it, counted on its barrier (the wait for the barrier is all that they need).
+__device__ __forceinline__ void send_to(uint32_t at, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(at), "r"(v), "r"(bar) : "memory");
 }
 // Says that something is done: what the products read (P and the queries in their own block's shared
 // memory, tensor memory) is ordered before it by the proxy and tcgen05 fences.  With a release at
 // cluster scope, which waits for every write of the warp, a tile took 1.8 times as long.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Hands on what was stored to the other block; wait_pair receives it.
-__device__ __forceinline__ void arrive_release_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -525,15 +519,6 @@ __device__ __forceinline__ bool wait_on(ChunkSmem* sm, uint64_t* bar, uint32_t p
 }
 __device__ __forceinline__ bool wait_bar(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
   return try_wait_long(bar, parity) || wait_on(sm, bar, parity, limit);
-}
-// For what the other block stored here (arrive_release_at); a warp.
-__device__ __forceinline__ bool wait_pair(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
-  uint32_t ok = wait_bar(sm, bar, parity, limit);
-  if (ok)   // (complete: this one returns at once)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  return __all_sync(0xFFFFFFFFu, ok) != 0;
 }
 __device__ __forceinline__ bool wait_warp(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
   return __all_sync(0xFFFFFFFFu, wait_bar(sm, bar, parity, limit)) != 0;
@@ -704,13 +689,6 @@ __device__ __forceinline__ void mask_keys(const ChunkArgs& a, const Item* it, in
   }
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // The softmax of the pair's tile g, the row block's tile t: this thread's row and 32 keys.
 __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, const Item* it, uint8_t* ptile, uint32_t tmem,
                                            int rank, int g, int t, bool first, const RowSees& sees, RowState& s) {
@@ -742,6 +720,7 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
   float top = z[0];
 #pragma unroll
   for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j]);
+  float fac = 1.f;
   const bool moves = role_any<kSoftId, kSoftWarps * 32>(top > s.limit);
   if (moves) {   // some row's reference moves
     sm->top[2 * side + (quarter >> 1)][r] = top;
@@ -754,16 +733,15 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
     s.msub = sub;
     s.l *= f;
     s.hat *= f;
-    if (!first && side == 0 && quarter < 2 && r < it->nq) {
-      float* to = &sm->fac[buf][rank * it->nq + r];
-      *to = f;
-      store_to(of_block(to, rank ^ 1), f);
-    }
+    if (side == 0 && quarter < 2) sm->fac[buf][rank][r] = fac = f;
     role_sync<kSoftId, kSoftWarps * 32>();
   }
-  if (threadIdx.x == 0) {   // (the barriers above order the warps' factors before it)
-    store_to(of_block(&sm->flag[buf], rank ^ 1), static_cast<int>(moves));
-    arrive_release_at(of_block(&sm->moved[buf], rank ^ 1));
+  // to the other block: each row's factor, and whether there is one
+  const uint32_t theirs = of_block(&sm->moved[buf], rank ^ 1);
+  if (side == 0 && quarter < 2) send_to(of_block(&sm->fac[buf][rank][r], rank ^ 1), __float_as_uint(fac), theirs);
+  if (threadIdx.x == 0) {
+    send_to(of_block(&sm->flag[buf], rank ^ 1), moves, theirs);
+    mbar_expect_tx(&sm->moved[buf], kRows * 4 + 4);
   }
   uint32_t w[16];
 #pragma unroll
@@ -786,21 +764,21 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
       *reinterpret_cast<uint4*>(ptile + (k >> 6) * kChunk + r * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4)) =
           make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   }
-  wait_pair(sm, &sm->moved[buf], (g >> 1) & 1, a.spin);
+  wait_warp(sm, &sm->moved[buf], (g >> 1) & 1, a.spin);
   if (!first) {
-    const bool theirs = *reinterpret_cast<volatile int*>(&sm->flag[buf]) != 0;
+    const bool other = *reinterpret_cast<volatile int*>(&sm->flag[buf]) != 0;
 #pragma unroll 1
     for (int u = 0; u < 2; ++u) {
-      if (!(u == rank ? moves : theirs)) continue;
+      if (!(u == rank ? moves : other)) continue;
 #pragma unroll 1
-      for (int x = u * it->nq; x < (u + 1) * it->nq; x += 8) {   // 32 dims of block `side`, 8 rows at a time
-        float o[8];
-        const uint32_t at = tmem + tlane + side * (2 * kRows) + x;
-        tmem_ld8(at, o);
+      for (int x = 0; x < it->nq; x += 16) {   // 32 dims of block `side`, 16 rows at a time
+        float o[16];
+        const uint32_t at = tmem + tlane + side * (2 * kRows) + u * it->nq + x;
+        tmem_ld16(at, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) o[c] *= sm->fac[buf][x + c];
-        tmem_st8(at, o);
+        for (int c = 0; c < 16; ++c) o[c] *= sm->fac[buf][u][x + c];
+        tmem_st16(at, o);
       }
       tmem_wait_st();
     }
@@ -847,7 +825,7 @@ __device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, C
     }
 #pragma unroll
     for (int c = 0; c < 16; c += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[e & 1][u * it->nq + g + c]);
+      const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[e & 1][u][g + c]);
       o[c] *= f.x;
       o[c + 1] *= f.y;
       o[c + 2] *= f.z;
@@ -885,7 +863,7 @@ __device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, C
 // The factors that this block's rows' outputs take (to both blocks), their log-sum-exps or partial sums.
 __device__ __forceinline__ void finish_sums(const ChunkArgs& a, const Item* it, ChunkSmem* sm, int rank, int e) {
   const int r = threadIdx.x - kSoftWarps * 32;
-  if (r >= it->nq) return;
+  if (r >= kRows) return;
   float f = 0.f;
   if (r < it->nr) {
     const float m = sm->ref[e & 1][r];
@@ -915,9 +893,10 @@ __device__ __forceinline__ void finish_sums(const ChunkArgs& a, const Item* it, 
       if (a.lse != nullptr) a.lse[row] = none ? sink : s.x != s.x ? s.x : (M + log2f(total)) * kLn2;
     }
   }
-  float* to = &sm->out_fac[e & 1][rank * it->nq + r];
+  float* to = &sm->out_fac[e & 1][rank][r];
   *to = f;
-  store_to(of_block(to, rank ^ 1), f);
+  send_to(of_block(to, rank ^ 1), __float_as_uint(f), of_block(&sm->f_full[e & 1], rank ^ 1));
+  if (r == 0) mbar_expect_tx(&sm->f_full[e & 1], kRows * 4);
 }
 
 // S of a tile: 64 dims (chunk c) of the queries and the keys, with chunk 7 the second halves of its
@@ -1228,8 +1207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       wait_warp(sm, &sm->l_full[e & 1], (e >> 1) & 1, a.spin);
       finish_sums(a, it, sm, rank, e);
       role_sync<kOutId, kOutThreads>();
-      if (tid == kSoftWarps * 32) arrive_release_at(of_block(&sm->f_full[e & 1], rank ^ 1));
-      wait_pair(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
+      wait_warp(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
       if (it->nt > 0) wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
       tc_fence_after();
       write_rows(a, it, sm, tmem, rank, e);
