@@ -39,8 +39,9 @@
 //   warp 16      in the even block one thread issues the products, S of the next tile before O of this
 //                one, so that the softmax runs beside products; in the odd block one thread tells the
 //                even one which copies have arrived;
-//   warp 17      plans row blocks and sends for their keys (bulk copies of a block of 128 dims), as soon
-//                as the product on the same place's keys before is complete.
+//   warp 17      sends for the keys (bulk copies of a block of 128 dims), as soon as the product on the
+//                same place's keys before is complete;
+//   warp 18      plans the row blocks, two at a time.
 // A row's reference belongs to its block, its output's columns to both: when a reference moves, the
 // factors go to the other block's shared memory, and a flag for every tile says whether they did.
 // Roundings as in list_attn.cu: the rotated query as two bf16 numbers, P in bf16 over the sum of the
@@ -63,8 +64,8 @@ constexpr int kChunk = kRows * 128;       // bytes of 64 dims of the queries, of
 constexpr int kKeyPart = 64 * 256;        // bytes of 128 dims of half a tile: groups of 8 keys, each [64 dims][8 keys][128 B] twice
 constexpr int kDimPart = kTile * 256;     // of a tile
 constexpr int kSoftWarps = 8, kOutWarps = 8;
-constexpr int kMmaWarp = kSoftWarps + kOutWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = (kLoadWarp + 1) * 32;
+constexpr int kMmaWarp = kSoftWarps + kOutWarps, kLoadWarp = kMmaWarp + 1, kPlanWarp = kMmaWarp + 2;
+constexpr int kThreads = (kPlanWarp + 1) * 32;
 constexpr int kOutThreads = kOutWarps * 32;
 constexpr uint32_t kTmemS = 256;          // TMEM columns: O 0..255, S from here, 64 for each tile
 constexpr float kSlack = 8.0f;            // base 2
@@ -81,6 +82,9 @@ struct ReqPlan {
   long long base;           // its first decoded row
   int item0;                // its first row block
   int bad;                  // a row of it could not be read or is not finite
+};
+struct SharePlan {
+  int first, last;          // the row blocks of a pair's share
 };
 struct SplitPlan {
   int item, b0, b1, pad;    // a row block that pairs b0 .. b1 share
@@ -113,6 +117,7 @@ struct ChunkArgs {
   ChunkHead* head;
   ReqPlan* req;
   long long* unit0;         // [items + 1]
+  SharePlan* share;         // [most_blocks]
   SplitPlan* split;         // [most_blocks]
   uint8_t* flags;           // of every decoded row: 0, kNone, kUnfit
   uint8_t* images;          // decoded rows: of each request 4 blocks of 128 dims as they lie in a stage
@@ -214,8 +219,10 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part, lo
   return v;
 }
 
+constexpr int kPlanStaged = 4096;         // row blocks whose places are searched in shared memory
+
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
-  __shared__ long long part[32];
+  __shared__ long long part[32], staged[kPlanStaged];
   grid_dep_launch();
   const int tid = threadIdx.x;
   long long keys = 0, items = 0, total;
@@ -283,14 +290,27 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     units += total;
 #pragma unroll
     for (int u = 0; u < kPlanItems; ++u) {
-      if (e1 + u < items) a.unit0[e1 + u] = at;
+      if (e1 + u < items) {
+        a.unit0[e1 + u] = at;
+        if (e1 + u < kPlanStaged) staged[e1 + u] = at;
+      }
       at += mine[u];
     }
   }
-  if (tid == 0) a.unit0[items] = units;
+  if (tid == 0) {
+    a.unit0[items] = units;
+    if (items < kPlanStaged) staged[items] = units;
+  }
   __syncthreads();
   const int blocks = static_cast<int>(max(1ll, min(static_cast<long long>(a.most_blocks), units / kLeastShare)));
-  // row blocks that a border cuts: listed at the last border inside
+  // the row blocks of each share; those that a border cuts are listed at the last border inside
+  if (items == 0) {
+    if (tid == 0) a.share[0] = SharePlan{0, -1};
+  } else if (tid == 0) {
+    a.share[0].first = 0;
+    a.share[blocks - 1].last = static_cast<int>(items) - 1;
+  }
+  const long long* unit0 = items < kPlanStaged ? staged : a.unit0;
   int splits = 0;
   for (int b0 = 1; b0 < blocks; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -298,13 +318,15 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     int e = 0;
     if (b < blocks) {
       const long long u = share_begin(units, blocks, b);
-      e = item_of_unit(a.unit0, static_cast<int>(items), u);
-      const int tiles = (static_cast<int>(a.unit0[e + 1] - a.unit0[e]) - kItemUnits) / 2;
-      const long long end = a.unit0[e] + 2ll * (tiles - 1);   // its last tile
-      last = u > a.unit0[e] && u <= end && block_of_unit(units, blocks, end) == b;
+      e = item_of_unit(unit0, static_cast<int>(items), u);
+      const int tiles = (static_cast<int>(unit0[e + 1] - unit0[e]) - kItemUnits) / 2;
+      const long long end = unit0[e] + 2ll * (tiles - 1);   // its last tile
+      a.share[b].first = e + (end < u);                     // (its tiles are all before the border)
+      a.share[b - 1].last = e - (unit0[e] == u);
+      last = u > unit0[e] && u <= end && block_of_unit(units, blocks, end) == b;
     }
     const long long at = splits + block_scan(last, part, &total) - 1;
-    if (last) a.split[at] = SplitPlan{e, block_of_unit(units, blocks, a.unit0[e]), b, 0};
+    if (last) a.split[at] = SplitPlan{e, block_of_unit(units, blocks, unit0[e]), b, 0};
     splits += static_cast<int>(total);
   }
   if (tid == 0) *a.head = ChunkHead{static_cast<int>(items), blocks, splits, 0, units, keys};
@@ -590,16 +612,6 @@ __device__ void make_item(const ChunkArgs& a, Item* it, int e, long long units, 
   }
 }
 
-// The row blocks of a pair's share: [first, last].
-__device__ __forceinline__ void share_items(const ChunkArgs& a, const ChunkHead& h, int pair, int* first, int* last) {
-  const long long lo = share_begin(h.units, h.blocks, pair), hi = share_begin(h.units, h.blocks, pair + 1);
-  int e = item_of_unit(a.unit0, h.items, lo);
-  const int tiles = (static_cast<int>(a.unit0[e + 1] - a.unit0[e]) - kItemUnits) / 2;
-  if (a.unit0[e] + 2ll * (tiles - 1) < lo) ++e;   // its tiles are all before the border
-  *first = e;
-  *last = item_of_unit(a.unit0, h.items, hi - 1);
-}
-
 // Queries into the K-major chunks of Q (64 rows apart; rows behind the last one zero); the output
 // warps.  The last 64 dims are then rotated in place: chunk 7 holds the first bf16 of each rotated
 // value, chunk 8 the second.  (The angles are on their way while the queries are awaited: loaded row by
@@ -726,7 +738,7 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
     sm->top[2 * side + (quarter >> 1)][r] = top;
     role_sync<kSoftId, kSoftWarps * 32>();
     const float now = fmaxf(fmaxf(fmaxf(sm->top[0][r], sm->top[1][r]), fmaxf(sm->top[2][r], sm->top[3][r])), s.m);
-    const float sub = now == -INFINITY ? 0.f : now * a.scale_log2;
+    const float sub = now == -INFINITY ? 0.f : __fmul_rn(now, a.scale_log2);
     const float f = s.m == -INFINITY ? 0.f : exp2f(s.msub - sub);
     s.m = now;
     s.limit = now + a.slack;
@@ -790,73 +802,120 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
 }
 
 // O^T out, in units of 16 rows of a block of 128 dims: a thread has one dim of them, a row's 32 dims
-// of a warp are one 64-byte run.  All rows of the row block, this block's dims.
-__device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem, int rank, int e) {
+// of a warp are one 64-byte run.  All rows of the row block, this block's dims; warps 8-11 have the even
+// block's rows, 12-15 the odd one's.
+// Outputs are taken out of tensor memory as bf16 first, so that the next row block's products need not
+// wait for the stores (with stores in between: 14,000 cycles until they went on).  The last 64
+// dims are turned back on the way: even lanes have the pair of dims (d, d + 1) of row c, odd lanes (d - 1, d)
+// of row c + 1.
+struct OutPlace {
+  int row0, rows;        // the warp's rows of the [T * H] rows
+  int at;                // the first one's place in the row block
+};
+__device__ __forceinline__ OutPlace out_place(const Item* it, int u) {
+  return u == 0 ? OutPlace{it->row0, it->half, 0} : OutPlace{it->row0 + it->half, it->rows - it->half, it->half};
+}
+__device__ __forceinline__ void take_out16(const Item* it, const ChunkSmem* sm, uint32_t from, int u, int j, int g, int e,
+                                           float (&o)[16]) {
+  if (it->nt > 0) {
+    tmem_ld16(from + j * (2 * kRows) + u * it->nq + g, o);   // (columns behind the last row hold nothing of use)
+    tmem_wait_ld();
+  } else {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) o[c] = 0.f;
+  }
+#pragma unroll
+  for (int c = 0; c < 16; c += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[e & 1][u][g + c]);
+    o[c] *= f.x;
+    o[c + 1] *= f.y;
+    o[c + 2] *= f.z;
+    o[c + 3] *= f.w;
+  }
+}
+// the outputs of a whole row block; `read` is called once they are out of tensor memory
+template <class Read>
+__device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem, int rank, int e,
+                                           Read&& read) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3;
+  const int quarter = warp & 3, u = (warp - kSoftWarps) >> 2, odd = lane & 1;
   const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-  const unsigned H = a.H;
-  const int sets = it->nq >> 4;   // of each half of the rows
-#pragma unroll 1
-  for (int x = (warp - kSoftWarps) >> 2; x < 4 * sets; x += kOutWarps / 4) {
-    const int which = x / sets, j = which >> 1, u = which & 1, g = (x - which * sets) * 16;   // block of dims, half of the rows, row
-    const int block = 2 * j + rank;
-    const int d = block * 128 + quarter * 32 + lane;
-    const int r0 = it->row0 + (u == 0 ? 0 : it->half), nr = (u == 0 ? it->half : it->rows - it->half) - g;
-    if (nr <= 0) continue;
-    const bool turn = block == 3 && quarter >= 2 && it->part < 0;   // dims 448..511, turned back
-    // even lanes turn and store the pair of dims (d, d + 1) of row c, odd lanes (d - 1, d) of row c + 1
-    const int odd = lane & 1;
-    float2 w[8];
-    if (turn) {
-      const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
+  const OutPlace p = out_place(it, u);
+  const bool turns = rank == 1 && quarter >= 2;        // dims 448..511 are in its second block
+  const int d0 = rank * 128 + quarter * 32 + lane;     // of the first block; 256 more of the second
+  uint32_t hold[2][4][8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (c == 0 || !it->one) w[c] = __ldg(cs + static_cast<size_t>((r0 + g + min(2 * c + odd, nr - 1)) / H) * 32);
-        else w[c] = w[0];
-    }
-    float o[16];
-    if (it->nt > 0) {
-      tmem_ld16(from + j * (2 * kRows) + u * it->nq + g, o);   // (columns behind the last row hold nothing of use)
-      tmem_wait_ld();
-    } else {
+  for (int j = 1; j >= 0; --j) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) o[c] = 0.f;
-    }
+    for (int x = 0; x < 4; ++x) {
+      const int g = 16 * x;
+      if (g >= p.rows) continue;
+      float o[16];
+      float2 w[8];
+      const bool turn = j == 1 && turns;
+      if (turn) {
+        const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d0 + 256 - (kD - 64)) >> 1);
 #pragma unroll
-    for (int c = 0; c < 16; c += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[e & 1][u][g + c]);
-      o[c] *= f.x;
-      o[c + 1] *= f.y;
-      o[c + 2] *= f.z;
-      o[c + 3] *= f.w;
-    }
-    if (it->part >= 0) {
-      float* to = a.opart + (static_cast<size_t>(it->part) * (2 * kRows) + (r0 - it->row0) + g) * kD + d;
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (c < nr) to[c * kD] = o[c];
-      continue;
-    }
-    if (turn) {
-#pragma unroll
-      for (int c = 0; c < 16; c += 2) {
-        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[c] : o[c + 1], 1);
-        const float y0 = odd ? other : o[c], y1 = odd ? o[c + 1] : other;
-        const float2 t = w[c / 2];
-        const uint32_t v = pack_bf16(y0 * t.x + y1 * t.y, y1 * t.x - y0 * t.y);
-        if (c + odd < nr)
-          *reinterpret_cast<uint32_t*>(a.out + ((static_cast<size_t>(r0) + g + c + odd) * kD + (d & ~1)) * 2) = v;
+        for (int c = 0; c < 8; ++c)
+          if (c == 0 || !it->one)
+            w[c] = __ldg(cs + static_cast<size_t>(static_cast<unsigned>(p.row0 + min(g + 2 * c + odd, p.rows - 1)) / static_cast<unsigned>(a.H)) * 32);
+          else w[c] = w[0];
       }
-      continue;
-    }
-    uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + (static_cast<size_t>(r0) + g) * kD + d;
+      take_out16(it, sm, from, u, j, g, e, o);
 #pragma unroll
-    for (int c = 0; c < 16; c += 2) {
-      const uint32_t v = pack_bf16(o[c], o[c + 1]);
-      if (c < nr) to[c * kD] = static_cast<uint16_t>(v);
-      if (c + 1 < nr) to[(c + 1) * kD] = static_cast<uint16_t>(v >> 16);
+      for (int c = 0; c < 8; ++c) {
+        if (turn) {
+          const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[2 * c] : o[2 * c + 1], 1);
+          const float y0 = odd ? other : o[2 * c], y1 = odd ? o[2 * c + 1] : other;
+          hold[j][x][c] = pack_bf16(y0 * w[c].x + y1 * w[c].y, y1 * w[c].x - y0 * w[c].y);
+        } else {
+          hold[j][x][c] = pack_bf16(o[2 * c], o[2 * c + 1]);
+        }
+      }
     }
+  }
+  read();
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const bool turn = j == 1 && turns;
+    const int d = d0 + 256 * j;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int left = p.rows - 16 * x;
+      if (left <= 0) continue;
+      const size_t row = static_cast<size_t>(p.row0) + 16 * x;
+      if (turn) {
+        uint8_t* to = a.out + ((row + odd) * kD + (d & ~1)) * 2;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (2 * c + odd < left) *reinterpret_cast<uint32_t*>(to + c * (4 * kD)) = hold[j][x][c];
+      } else {
+        uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + row * kD + d;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (2 * c < left) to[2 * c * kD] = static_cast<uint16_t>(hold[j][x][c]);
+          if (2 * c + 1 < left) to[(2 * c + 1) * kD] = static_cast<uint16_t>(hold[j][x][c] >> 16);
+        }
+      }
+    }
+  }
+}
+// a partial output, fp32
+__device__ __forceinline__ void write_part(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem, int rank, int e) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, u = (warp - kSoftWarps) >> 2;
+  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const OutPlace p = out_place(it, u);
+  float* out = a.opart + (static_cast<size_t>(it->part) * (2 * kRows) + p.at) * kD + rank * 128 + quarter * 32 + lane;
+#pragma unroll 2
+  for (int x = 0; x < 8; ++x) {
+    const int j = x & 1, g = 8 * (x & ~1);
+    if (g >= p.rows) break;
+    float o[16];
+    take_out16(it, sm, from, u, j, g, e, o);
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (g + c < p.rows) out[(g + c) * kD + 256 * j] = o[c];
   }
 }
 
@@ -882,7 +941,7 @@ __device__ __forceinline__ void finish_sums(const ChunkArgs& a, const Item* it, 
       f = ratio;
     } else {
       const float sink = a.sink != nullptr ? __ldg(a.sink + row % static_cast<unsigned>(a.H)) : -INFINITY;
-      const float s2 = sink * kLog2e;
+      const float s2 = __fmul_rn(sink, kLog2e);   // (not part of a fused difference: s2 - M is 0 where s2 is the larger)
       const float M = fmaxf(m, s2);
       const float w = exp2f(m - M);
       const float total = s.x * w + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));
@@ -949,7 +1008,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       mbar_init(&sm->l_full[i], kSoftWarps);
       mbar_init(&sm->f_full[i], 1);
       mbar_init(&sm->item_full[i], 1);
-      mbar_init(&sm->item_free[i], 1 + kSoftWarps + kOutWarps);
+      mbar_init(&sm->item_free[i], 2 + kSoftWarps + kOutWarps);
     }
     mbar_init(&sm->p_full, 2 * kSoftWarps);
     mbar_init(&sm->q_full, 2 * kOutWarps);
@@ -966,27 +1025,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
   grid_dep_wait();
   grid_dep_launch();
   const ChunkHead head = *a.head;
-  int first = 0, last = -1;
-  if (pair < head.blocks && head.items > 0) share_items(a, head, pair, &first, &last);
-  const int items = last - first + 1;
+  const SharePlan share = pair < head.blocks ? a.share[pair] : SharePlan{0, -1};
+  const int items = share.last - share.first + 1;
   tc_fence_before();
   __syncthreads();
   cluster_sync();                          // the other block's barriers are there
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
 
-  if (warp == kLoadWarp) {                 // ---- row blocks and keys
+  if (warp == kPlanWarp) {                 // ---- row blocks
+    for (int e = 0; e < items; ++e) {
+      if (e >= 2 && !wait_warp(sm, &sm->item_free[e & 1], ((e >> 1) - 1) & 1, a.spin)) break;
+      make_item(a, &sm->item[e & 1], share.first + e, head.units, head.blocks, pair, rank);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->item_full[e & 1]);
+    }
+  } else if (warp == kLoadWarp) {          // ---- keys
+    if (elect_lane()) {
     bool ok = true;
     int gk = 0, gv = 0, parts = 0;         // tiles sent for: keys, dims; and parts of one more (4 + of dims)
     fence_proxy_async_global();            // (the decoded rows, by another kernel's plain stores)
-    auto plan = [&](int e) {
-      if (e >= 2) ok = ok && wait_warp(sm, &sm->item_free[e & 1], ((e >> 1) - 1) & 1, a.spin);
-      if (!ok) return;
-      make_item(a, &sm->item[e & 1], first + e, head.units, head.blocks, pair, rank);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->item_full[e & 1]);
-    };
-    // (one lane each)
     auto send_keys = [&](const Item* it, int t) {
       const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0), n2 = half_keys(n);
       const int mine = rank == 0 ? min(n, n2) : n - min(n, n2);
@@ -1014,31 +1072,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       }
       if (ok) { ++gv; parts = 0; }
     };
-    if (items > 0) plan(0);
     bool sent = false;                     // the keys of this row block's first tile have been sent for
     for (int e = 0; e < items && ok; ++e) {
+      if (e == 0) ok = wait_bar(sm, &sm->item_full[0], 0, a.spin);
+      if (!ok) break;
       const Item* it = &sm->item[e & 1];
       const int nt = it->nt;
-      if (lane == 0 && nt > 0) {
-        if (!sent) send_keys(it, 0);
-        for (int t = 0; t + 1 < nt && ok; ++t) {
-          send_keys(it, t + 1);
-          send_dims(it, t);
-        }
+      if (nt > 0 && !sent) send_keys(it, 0);
+      for (int t = 0; t + 1 < nt && ok; ++t) {
+        send_keys(it, t + 1);
+        send_dims(it, t);
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       // the next row block's first keys before this one's last dims
-      if (ok && e + 1 < items) plan(e + 1);
-      sent = ok && e + 1 < items && sm->item[(e + 1) & 1].nt > 0;
-      if (lane == 0 && ok) {
-        if (sent && nt > 0) send_keys(&sm->item[(e + 1) & 1], 0);
-        if (nt > 0 && ok) send_dims(it, nt - 1);
-      }
-      sent = sent && nt > 0;
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (ok && e + 1 < items) ok = wait_bar(sm, &sm->item_full[(e + 1) & 1], ((e + 1) >> 1) & 1, a.spin);
+      sent = ok && nt > 0 && e + 1 < items && sm->item[(e + 1) & 1].nt > 0;
+      if (sent) send_keys(&sm->item[(e + 1) & 1], 0);
+      if (nt > 0 && ok) send_dims(it, nt - 1);
+      mbar_arrive(&sm->item_free[e & 1]);
     }
     // copies in flight (there are none, unless a wait gave up): the last ones to each place
-    if (lane == 0) {
+    {
       for (int m = 0; m < 4; ++m) {
         const int n = gk + (parts < 4 && m < parts ? 1 : 0);
         if (n > 0) mbar_wait(&sm->k_full[m], (n - 1) & 1, kDefaultSpinLimit);
@@ -1047,6 +1100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
         const int n = gv + (parts > 4 + j ? 1 : 0);
         if (n > 0) mbar_wait(&sm->v_full[j], (n - 1) & 1, kDefaultSpinLimit);
       }
+    }
     }
     __syncwarp();
   } else if (warp == kMmaWarp && rank == 1) {   // ---- tells the even block of this one's copies
@@ -1210,13 +1264,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       wait_warp(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
       if (it->nt > 0) wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
       tc_fence_after();
-      write_rows(a, it, sm, tmem, rank, e);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        arrive_at(of_block(&sm->o_free, 0));
-        mbar_arrive(&sm->item_free[e & 1]);
+      auto outputs_read = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(of_block(&sm->o_free, 0));
+      };
+      if (it->part < 0) {
+        write_rows(a, it, sm, tmem, rank, e, outputs_read);
+      } else {
+        write_part(a, it, sm, tmem, rank, e);
+        outputs_read();
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->item_free[e & 1]);
     }
     cp_async_wait_all();
   }
@@ -1230,62 +1290,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
 }
 
 // ---------------------------------------------------------------------------
-// the join: the parts of a row in order, the sink, the rotation back.  64 threads of 8 dims, four
-// times as many, each with every fourth part, for a row.
+// the join: the parts of a row in order, the sink, the rotation back.  64 threads of 8 dims for a row;
+// where there are many parts four times as many, each with every fourth part.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kShares = 4;
+constexpr int kFewParts = 8;
 
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ float shares[kShares - 1][kD];
   grid_dep_wait();
   const ChunkHead head = *a.head;
-  const int share = threadIdx.x >> 6, lane = threadIdx.x & 31, d = (threadIdx.x & 63) * 8;
-  for (int x = blockIdx.x; x < head.splits * (2 * kRows); x += gridDim.x) {
-    const SplitPlan sp = a.split[x / (2 * kRows)];
-    const int r = x % (2 * kRows);
+  const int sub = threadIdx.x >> 6, lane = threadIdx.x & 31, d = (threadIdx.x & 63) * 8;
+  constexpr int kSets = 2 * kRows / 4;   // of four rows of a row block
+  for (int x = blockIdx.x; x < head.splits * kSets; x += gridDim.x) {
+    const SplitPlan sp = a.split[x / kSets];
     const ReqPlan p = a.req[request_of_item(a, sp.item)];
     const int i0 = (sp.item - p.item0) * a.group;
     const int nr = min(p.nq - i0, a.group) * a.H;
-    if (r >= nr) continue;   // (the whole block)
-    const size_t row = static_cast<size_t>(p.q0 + i0) * a.H + r;
     const bool late = a.unit0[sp.item] > share_begin(head.units, head.blocks, sp.b0);
     const int parts = sp.b1 - sp.b0 + 1;
-    auto slot = [&](int k) { return (2 * static_cast<size_t>(sp.b0 + k) + (k == 0 && late)) * (2 * kRows) + r; };
-    const float sink = a.sink != nullptr ? __ldg(a.sink + row % a.H) : -INFINITY;
-    const float s2 = sink * kLog2e;
-    auto weight = [&](float2 v, float M) { return v.y == 0.f ? 0.f : v.y != v.y ? v.y : exp2f(v.x - M); };
-    float M = s2, total = 0.f, o[8];
-    for (int k = lane; k < parts; k += 32) {
-      const float2 v = a.ml[slot(k)];
-      if (v.y != 0.f) M = fmaxf(M, v.x);
-    }
-    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, w));
-    for (int k = lane; k < parts; k += 32) {
-      const float2 v = a.ml[slot(k)];
-      total += v.y * weight(v, M);
-    }
-    for (int w = 16; w >= 1; w >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, w);
+    const bool few = parts <= kFewParts;
+    for (int y = 0; y < (few ? 1 : 4); ++y) {   // (the whole block)
+      const int r = (x % kSets) * 4 + (few ? sub : y), share = few ? 0 : sub;
+      const bool there = r < nr;
+      auto slot = [&](int k) { return (2 * static_cast<size_t>(sp.b0 + k) + (k == 0 && late)) * (2 * kRows) + r; };
+      auto weight = [&](float2 v, float M) { return v.y == 0.f ? 0.f : v.y != v.y ? v.y : exp2f(v.x - M); };
+      const size_t row = static_cast<size_t>(p.q0 + i0) * a.H + r;
+      const float sink = a.sink != nullptr && there ? __ldg(a.sink + row % a.H) : -INFINITY;
+      const float s2 = __fmul_rn(sink, kLog2e);   // (not part of a fused difference: s2 - M is 0 where s2 is the larger)
+      float M = s2, total = 0.f, o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+      for (int i = 0; i < 8; ++i) o[i] = 0.f;
+      if (there) {
+        if (few) {
+          for (int k = 0; k < parts; ++k) {
+            const float2 v = a.ml[slot(k)];
+            if (v.y != 0.f) M = fmaxf(M, v.x);
+          }
+        } else {
+          for (int k = lane; k < parts; k += 32) {
+            const float2 v = a.ml[slot(k)];
+            if (v.y != 0.f) M = fmaxf(M, v.x);
+          }
+          for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, w));
+          for (int k = lane; k < parts; k += 32) {
+            const float2 v = a.ml[slot(k)];
+            total += v.y * weight(v, M);
+          }
+          for (int w = 16; w >= 1; w >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, w);
+        }
 #pragma unroll 4
-    for (int k = share; k < parts; k += kShares) {
-      const float e = weight(a.ml[slot(k)], M);   // 0: a part without keys, whose output is 0
-      const float4* v = reinterpret_cast<const float4*>(a.opart + slot(k) * kD + d);
-      const float4 v0 = v[0], v1 = v[1];
-      o[0] += e * v0.x; o[1] += e * v0.y; o[2] += e * v0.z; o[3] += e * v0.w;
-      o[4] += e * v1.x; o[5] += e * v1.y; o[6] += e * v1.z; o[7] += e * v1.w;
-    }
-    if (share > 0) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) shares[share - 1][d + i] = o[i];
-    }
-    __syncthreads();
-    if (share == 0) {
-      for (int k = 0; k < kShares - 1; ++k) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += shares[k][d + i];
+        for (int k = share; k < parts; k += few ? 1 : kShares) {
+          const float2 ml = a.ml[slot(k)];
+          const float e = weight(ml, M);   // 0: a part without keys, whose output is 0
+          if (few) total += ml.y * e;
+          const float4* v = reinterpret_cast<const float4*>(a.opart + slot(k) * kD + d);
+          const float4 v0 = v[0], v1 = v[1];
+          o[0] += e * v0.x; o[1] += e * v0.y; o[2] += e * v0.z; o[3] += e * v0.w;
+          o[4] += e * v1.x; o[5] += e * v1.y; o[6] += e * v1.z; o[7] += e * v1.w;
+        }
       }
+      if (!few) {
+        if (share > 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) shares[share - 1][d + i] = o[i];
+        }
+        __syncthreads();
+        if (share == 0) {
+          for (int k = 0; k < kShares - 1; ++k) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] += shares[k][d + i];
+          }
+        }
+        __syncthreads();   // shares are used again
+      }
+      if (!there || share > 0) continue;
       const bool none = total == 0.f;   // no key that counts beside the sink
       if (s2 != -INFINITY) total += exp2f(s2 - M);
       const float inv = none ? 0.f : 1.0f / total;
@@ -1304,7 +1384,6 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
           make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
       if (a.lse != nullptr && d == 0) a.lse[row] = none ? sink : (M + log2f(total)) * kLn2;
     }
-    __syncthreads();   // shares are used again
   }
 }
 
@@ -1313,7 +1392,7 @@ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
 // How the row blocks and the workspace follow from the sizes alone.
 struct Layout {
   int group, most_blocks;
-  size_t head, req, unit0, split, flags, images, opart, ml, bytes;
+  size_t head, req, unit0, share, split, flags, images, opart, ml, bytes;
 };
 Layout layout_of(int R, int T, int H, int64_t max_keys) {
   Layout l = {};
@@ -1328,6 +1407,7 @@ Layout layout_of(int R, int T, int H, int64_t max_keys) {
   l.head = take(sizeof(ChunkHead));
   l.req = take(sizeof(ReqPlan) * static_cast<size_t>(R));
   l.unit0 = take(8 * static_cast<size_t>(items + 1));
+  l.share = take(sizeof(SharePlan) * l.most_blocks);
   l.split = take(sizeof(SplitPlan) * l.most_blocks);
   l.flags = take(keys);
   l.images = take(keys * (2 * kD));
@@ -1396,6 +1476,7 @@ cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t*
   a.head = reinterpret_cast<ChunkHead*>(ws + l.head);
   a.req = reinterpret_cast<ReqPlan*>(ws + l.req);
   a.unit0 = reinterpret_cast<long long*>(ws + l.unit0);
+  a.share = reinterpret_cast<SharePlan*>(ws + l.share);
   a.split = reinterpret_cast<SplitPlan*>(ws + l.split);
   a.flags = ws + l.flags;
   a.images = ws + l.images;
@@ -1413,7 +1494,7 @@ cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t*
   static std::atomic<uint64_t> allowed;
   e = launch_next(chunk_attn_kernel, 2 * l.most_blocks, kThreads, kChunkSmemBytes, stream, &allowed, a);
   if (e != cudaSuccess || l.most_blocks == 1) return e;
-  return launch_next(chunk_join_kernel, 8 * kPairs, kJoinThreads, 0, stream, nullptr, a);
+  return launch_next(chunk_join_kernel, 32 * l.most_blocks, kJoinThreads, 0, stream, nullptr, a);
 }
 
 unsigned int take_err_chunk_attn() { return take_dev_err(); }
