@@ -472,7 +472,7 @@ struct ChunkSmem {
   Item item[2];
   uint64_t k_full[4], k_free[4];           // keys: blocks of 128 dims
   uint64_t v_full[2], v_free[2];           // this block's dims
-  uint64_t s_full[2], moved[2], p_full, q_full, q_free, o_free, l_full[2], f_full[2], item_full[2], item_free[2], drained;
+  uint64_t s_full[2], moved[2], p_full, q_full, q_free, o_free[2], l_full[2], f_full[2], item_full[2], item_free[2], drained;
   uint32_t tmem;
   int abort;
   int flag[2];                             // by tile: the other block's references moved
@@ -801,122 +801,83 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
   if (lane == 0) arrive_at(of_block(&sm->p_full, 0));
 }
 
-// O^T out, in units of 16 rows of a block of 128 dims: a thread has one dim of them, a row's 32 dims
-// of a warp are one 64-byte run.  All rows of the row block, this block's dims; warps 8-11 have the even
-// block's rows, 12-15 the odd one's.
-// Outputs are taken out of tensor memory as bf16 first, so that the next row block's products need not
-// wait for the stores (with stores in between: 14,000 cycles until they went on).  The last 64
-// dims are turned back on the way: even lanes have the pair of dims (d, d + 1) of row c, odd lanes (d - 1, d)
-// of row c + 1.
-struct OutPlace {
-  int row0, rows;        // the warp's rows of the [T * H] rows
-  int at;                // the first one's place in the row block
-};
-__device__ __forceinline__ OutPlace out_place(const Item* it, int u) {
-  return u == 0 ? OutPlace{it->row0, it->half, 0} : OutPlace{it->row0 + it->half, it->rows - it->half, it->half};
-}
-__device__ __forceinline__ void take_out16(const Item* it, const ChunkSmem* sm, uint32_t from, int u, int j, int g, int e,
-                                           float (&o)[16]) {
-  if (it->nt > 0) {
-    tmem_ld16(from + j * (2 * kRows) + u * it->nq + g, o);   // (columns behind the last row hold nothing of use)
-    tmem_wait_ld();
-  } else {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) o[c] = 0.f;
-  }
-#pragma unroll
-  for (int c = 0; c < 16; c += 4) {
-    const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[e & 1][u][g + c]);
-    o[c] *= f.x;
-    o[c + 1] *= f.y;
-    o[c + 2] *= f.z;
-    o[c + 3] *= f.w;
-  }
-}
-// the outputs of a whole row block; `read` is called once they are out of tensor memory
+// Block j of O^T out (128 dims x all rows of the row block), 16 rows at a time: a thread has one dim, a
+// row's 32 dims of a warp are one 64-byte run; warps 8-11 have the even block's rows, 12-15 the odd one's.
+// `read` is called once the block is out of tensor memory: the next row block's products go on with
+// it while the other block is read.  Dims 448..511 are turned back on the way: even lanes have the
+// pair of dims (d, d + 1) of row c, odd lanes (d - 1, d) of row c + 1.  A partial output goes out in fp32 as
+// it is.  (Rolled: with all 64 rows unrolled the block's first outputs waited 12,000 cycles for
+// instructions.)
 template <class Read>
-__device__ __forceinline__ void write_rows(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem, int rank, int e,
-                                           Read&& read) {
+__device__ __forceinline__ void write_block(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem, int rank, int e,
+                                            int j, Read&& read) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, u = (warp - kSoftWarps) >> 2, odd = lane & 1;
-  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-  const OutPlace p = out_place(it, u);
-  const bool turns = rank == 1 && quarter >= 2;        // dims 448..511 are in its second block
-  const int d0 = rank * 128 + quarter * 32 + lane;     // of the first block; 256 more of the second
-  uint32_t hold[2][4][8];
-#pragma unroll
-  for (int j = 1; j >= 0; --j) {
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int g = 16 * x;
-      if (g >= p.rows) continue;
-      float o[16];
-      float2 w[8];
-      const bool turn = j == 1 && turns;
-      if (turn) {
-        const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d0 + 256 - (kD - 64)) >> 1);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c == 0 || !it->one)
-            w[c] = __ldg(cs + static_cast<size_t>(static_cast<unsigned>(p.row0 + min(g + 2 * c + odd, p.rows - 1)) / static_cast<unsigned>(a.H)) * 32);
-          else w[c] = w[0];
-      }
-      take_out16(it, sm, from, u, j, g, e, o);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if (turn) {
-          const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[2 * c] : o[2 * c + 1], 1);
-          const float y0 = odd ? other : o[2 * c], y1 = odd ? o[2 * c + 1] : other;
-          hold[j][x][c] = pack_bf16(y0 * w[c].x + y1 * w[c].y, y1 * w[c].x - y0 * w[c].y);
-        } else {
-          hold[j][x][c] = pack_bf16(o[2 * c], o[2 * c + 1]);
-        }
-      }
-    }
+  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + j * (2 * kRows) + u * it->nq;
+  const int at = u == 0 ? 0 : it->half, rows = u == 0 ? it->half : it->rows - it->half;   // of the row block
+  const unsigned row0 = it->row0 + at, H = a.H;
+  const int d = (2 * j + rank) * 128 + quarter * 32 + lane;
+  const bool whole = it->part < 0, turn = whole && d >= kD - 64, tiles = it->nt > 0;
+  // the angles of the thread's pair of dims for its row's query, and for the next query, on their way
+  const float2* cs = reinterpret_cast<const float2*>(a.q_rope) + ((d - (kD - 64)) >> 1);
+  const unsigned final_query = rows > 0 ? (row0 + rows - 1) / H : 0;
+  unsigned query = (row0 + odd) / H, border = (query + 1) * H;
+  float2 w = make_float2(1.f, 0.f), next = w;
+  if (turn && rows > 0) {
+    w = __ldg(cs + static_cast<size_t>(min(query, final_query)) * 32);
+    next = __ldg(cs + static_cast<size_t>(min(query + 1, final_query)) * 32);
   }
-  read();
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const bool turn = j == 1 && turns;
-    const int d = d0 + 256 * j;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int left = p.rows - 16 * x;
-      if (left <= 0) continue;
-      const size_t row = static_cast<size_t>(p.row0) + 16 * x;
-      if (turn) {
-        uint8_t* to = a.out + ((row + odd) * kD + (d & ~1)) * 2;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (2 * c + odd < left) *reinterpret_cast<uint32_t*>(to + c * (4 * kD)) = hold[j][x][c];
-      } else {
-        uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + row * kD + d;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (2 * c < left) to[2 * c * kD] = static_cast<uint16_t>(hold[j][x][c]);
-          if (2 * c + 1 < left) to[(2 * c + 1) * kD] = static_cast<uint16_t>(hold[j][x][c] >> 16);
-        }
-      }
-    }
-  }
-}
-// a partial output, fp32
-__device__ __forceinline__ void write_part(const ChunkArgs& a, const Item* it, ChunkSmem* sm, uint32_t tmem, int rank, int e) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, u = (warp - kSoftWarps) >> 2;
-  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-  const OutPlace p = out_place(it, u);
-  float* out = a.opart + (static_cast<size_t>(it->part) * (2 * kRows) + p.at) * kD + rank * 128 + quarter * 32 + lane;
-#pragma unroll 2
-  for (int x = 0; x < 8; ++x) {
-    const int j = x & 1, g = 8 * (x & ~1);
-    if (g >= p.rows) break;
+  float* part = whole ? nullptr : a.opart + (static_cast<size_t>(it->part) * (2 * kRows) + at) * kD + d;
+  uint8_t* out = a.out + (static_cast<size_t>(row0) * kD + d) * 2;
+#pragma unroll 1
+  for (int g = 0; g < rows; g += 16) {
     float o[16];
-    take_out16(it, sm, from, u, j, g, e, o);
+    if (tiles) {
+      tmem_ld16(from + g, o);   // (columns behind the last row hold nothing of use)
+      tmem_wait_ld();
+    } else {
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      if (g + c < p.rows) out[(g + c) * kD + 256 * j] = o[c];
+      for (int c = 0; c < 16; ++c) o[c] = 0.f;
+    }
+    if (g + 16 >= rows) read();
+    const int left = rows - g;
+#pragma unroll
+    for (int c = 0; c < 16; c += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&sm->out_fac[e & 1][u][g + c]);
+      o[c] *= f.x;
+      o[c + 1] *= f.y;
+      o[c + 2] *= f.z;
+      o[c + 3] *= f.w;
+    }
+    if (!whole) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        if (c < left) part[(g + c) * kD] = o[c];
+    } else if (turn) {
+      uint8_t* to = out + (static_cast<size_t>(g + odd) * kD - odd) * 2;
+#pragma unroll
+      for (int c = 0; c < 16; c += 2) {
+        while (row0 + g + c + odd >= border && query < final_query) {
+          w = next;
+          ++query;
+          border += H;
+          next = __ldg(cs + static_cast<size_t>(min(query + 1, final_query)) * 32);
+        }
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? o[c] : o[c + 1], 1);
+        const float y0 = odd ? other : o[c], y1 = odd ? o[c + 1] : other;
+        if (c + odd < left) *reinterpret_cast<uint32_t*>(to + c * (2 * kD)) = pack_bf16(y0 * w.x + y1 * w.y, y1 * w.x - y0 * w.y);
+      }
+    } else {
+      uint16_t* to = reinterpret_cast<uint16_t*>(out) + g * kD;
+#pragma unroll
+      for (int c = 0; c < 16; c += 2) {
+        const uint32_t v = pack_bf16(o[c], o[c + 1]);
+        if (c < left) to[c * kD] = static_cast<uint16_t>(v);
+        if (c + 1 < left) to[(c + 1) * kD] = static_cast<uint16_t>(v >> 16);
+      }
+    }
   }
+  if (rows == 0) read();
 }
 
 // The factors that this block's rows' outputs take (to both blocks), their log-sum-exps or partial sums.
@@ -1013,7 +974,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     mbar_init(&sm->p_full, 2 * kSoftWarps);
     mbar_init(&sm->q_full, 2 * kOutWarps);
     mbar_init(&sm->q_free, 1);
-    mbar_init(&sm->o_free, 2 * kOutWarps);
+    for (int j = 0; j < 2; ++j) mbar_init(&sm->o_free[j], 2 * kOutWarps);
     mbar_init(&sm->drained, 1);
     sm->abort = 0;
     fence_mbar_init();
@@ -1168,29 +1129,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
           mma2_commit(&sm->s_full[i & 1]);
           if (t == nt - 1) mma2_commit(&sm->q_free);
         };
-        // before this row block's first O product the outputs of the one before are read (a row block
+        // before this row block's first O products the outputs of the one before are read (a row block
         // without tiles waits too: its own outputs would be told from those by nothing)
-        auto outputs_read = [&]() {
+        auto outputs_read = [&](int j) {
           if (e > 0) {
-            ok = ok && wait_bar(sm, &sm->o_free, (e - 1) & 1, a.spin);
+            ok = ok && wait_bar(sm, &sm->o_free[j], (e - 1) & 1, a.spin);
             tc_fence_after();
           }
         };
         if (nt == 0) {
-          outputs_read();
+          outputs_read(0);
+          outputs_read(1);
           mma2_commit(&sm->q_free);
-        } else if (ok) {
-          issue_s(0);
         }
-        for (int t = 0; t < nt && ok; ++t) {
+        for (int t = -1; t < nt && ok; ++t) {   // (issue_s once: its code is long)
           const int i = g + t;
           if (t + 1 < nt) issue_s(t + 1);
-          if (t == 0) outputs_read();
+          if (t < 0) continue;
           const int ks = min(kTile, keys - t * kTile) >> 4;
           ok = ok && wait_bar(sm, &sm->p_full, i & 1, a.spin);
           if (!ok) break;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+            if (t == 0) outputs_read(j);
             ok = ok && wait_bar(sm, &sm->v_full[j], i & 1, a.spin);
             tc_fence_after();
             if (!ok) break;
@@ -1264,17 +1225,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       wait_warp(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
       if (it->nt > 0) wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
       tc_fence_after();
-      auto outputs_read = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(of_block(&sm->o_free, 0));
-      };
-      if (it->part < 0) {
-        write_rows(a, it, sm, tmem, rank, e, outputs_read);
-      } else {
-        write_part(a, it, sm, tmem, rank, e);
-        outputs_read();
-      }
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j)
+        write_block(a, it, sm, tmem, rank, e, j, [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at(of_block(&sm->o_free[j], 0));
+        });
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->item_free[e & 1]);
     }
