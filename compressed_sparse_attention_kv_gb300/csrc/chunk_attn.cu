@@ -74,6 +74,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanItems = 4;             // row blocks of a thread at a time
 constexpr int kItemUnits = 3;             // a row block's cost beside its tiles, a tile being 2
 constexpr int kLeastShare = 8;            // units of a share
+constexpr unsigned long long kDrainLimit = 1ull << 27;   // cycles that a block which gives up waits for its own copies
 
 struct ReqPlan {
   int q0, nq, len;          // its queries [q0, q0 + nq), its length
@@ -546,8 +547,8 @@ __device__ __forceinline__ bool wait_warp(ChunkSmem* sm, uint64_t* bar, uint32_t
   return __all_sync(0xFFFFFFFFu, wait_bar(sm, bar, parity, limit)) != 0;
 }
 // Named barriers of the softmax warps (1) and of the output warps (2).  They have no limit: all of
-// a role's warps take the same loops (a row block is accepted by all or by none, and after a wait
-// that gave up they go on through its tiles without waiting).
+// a role's warps take the same loops (a row block is accepted by all or by none; after a wait that gave
+// up a warp goes on through its tiles to these barriers alone).
 template <int kId, int kCount>
 __device__ __forceinline__ void role_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kCount) : "memory");
@@ -703,7 +704,7 @@ __device__ __forceinline__ void mask_keys(const ChunkArgs& a, const Item* it, in
 
 // The softmax of the pair's tile g, the row block's tile t: this thread's row and 32 keys.
 __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, const Item* it, uint8_t* ptile, uint32_t tmem,
-                                           int rank, int g, int t, bool first, const RowSees& sees, RowState& s) {
+                                           int rank, int g, int t, bool first, const RowSees& sees, RowState& s, bool& ok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, side = warp >> 2;        // lanes of tensor memory; columns 32 side .. + 31
   const int r = 32 * (quarter & 1) + lane;
@@ -712,8 +713,8 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
   const int n2 = half_keys(min(kTile, it->keys - t * kTile));
   const int c0 = 32 * side;                              // the thread's first key within its half
   const int k0 = (quarter >> 1) * n2 + c0;               // within the tile
-  const bool has = c0 < n2;
-  wait_warp(sm, &sm->s_full[buf], (g >> 1) & 1, a.spin);
+  ok = ok && wait_warp(sm, &sm->s_full[buf], (g >> 1) & 1, a.spin);
+  const bool has = ok && c0 < n2;
   tc_fence_after();
   float z[32];
   if (has) {
@@ -748,6 +749,7 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
     if (side == 0 && quarter < 2) sm->fac[buf][rank][r] = fac = f;
     role_sync<kSoftId, kSoftWarps * 32>();
   }
+  if (!ok) return;
   // to the other block: each row's factor, and whether there is one
   const uint32_t theirs = of_block(&sm->moved[buf], rank ^ 1);
   if (side == 0 && quarter < 2) send_to(of_block(&sm->fac[buf][rank][r], rank ^ 1), __float_as_uint(fac), theirs);
@@ -766,7 +768,7 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
   }
   // the O product before has read P, and its output may be rescaled
   if (g > 0) {
-    wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
+    ok = wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
     tc_fence_after();
   }
 #pragma unroll
@@ -776,7 +778,8 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
       *reinterpret_cast<uint4*>(ptile + (k >> 6) * kChunk + r * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4)) =
           make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   }
-  wait_warp(sm, &sm->moved[buf], (g >> 1) & 1, a.spin);
+  ok = ok && wait_warp(sm, &sm->moved[buf], (g >> 1) & 1, a.spin);
+  if (!ok) return;
   if (!first) {
     const bool other = *reinterpret_cast<volatile int*>(&sm->flag[buf]) != 0;
 #pragma unroll 1
@@ -1003,65 +1006,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     }
   } else if (warp == kLoadWarp) {          // ---- keys
     if (elect_lane()) {
-    bool ok = true;
-    int gk = 0, gv = 0, parts = 0;         // tiles sent for: keys, dims; and parts of one more (4 + of dims)
-    fence_proxy_async_global();            // (the decoded rows, by another kernel's plain stores)
-    auto send_keys = [&](const Item* it, int t) {
-      const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0), n2 = half_keys(n);
-      const int mine = rank == 0 ? min(n, n2) : n - min(n, n2);
-      const uint8_t* image = a.images + it->base * (2 * kD);
+      bool ok = true;
+      int gk = 0, gv = 0, parts = 0;         // tiles sent for: keys, dims; and parts of one more (4 + of dims)
+      fence_proxy_async_global();            // (the decoded rows, by another kernel's plain stores)
+      auto send_keys = [&](const Item* it, int t) {
+        const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0), n2 = half_keys(n);
+        const int mine = rank == 0 ? min(n, n2) : n - min(n, n2);
+        const uint8_t* image = a.images + it->base * (2 * kD);
 #pragma unroll 1
-      for (int m = 0; m < 4 && ok; ++m) {
-        if (gk > 0) ok = wait_bar(sm, &sm->k_free[m], (gk - 1) & 1, a.spin);
-        if (!ok) break;
-        mbar_expect_tx(&sm->k_full[m], mine * 256);
-        send_for(it, ktile + m * kKeyPart, image + m * it->stride, k0 + rank * n2, mine, &sm->k_full[m]);
-        parts = m + 1;
-      }
-      if (ok) { ++gk; parts = 0; }
-    };
-    auto send_dims = [&](const Item* it, int t) {
-      const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0);
-      const uint8_t* image = a.images + it->base * (2 * kD);
+        for (int m = 0; m < 4 && ok; ++m) {
+          if (gk > 0) ok = wait_bar(sm, &sm->k_free[m], (gk - 1) & 1, a.spin);
+          if (!ok) break;
+          mbar_expect_tx(&sm->k_full[m], mine * 256);
+          send_for(it, ktile + m * kKeyPart, image + m * it->stride, k0 + rank * n2, mine, &sm->k_full[m]);
+          parts = m + 1;
+        }
+        if (ok) { ++gk; parts = 0; }
+      };
+      auto send_dims = [&](const Item* it, int t) {
+        const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0);
+        const uint8_t* image = a.images + it->base * (2 * kD);
 #pragma unroll 1
-      for (int j = 0; j < 2 && ok; ++j) {
-        if (gv > 0) ok = wait_bar(sm, &sm->v_free[j], (gv - 1) & 1, a.spin);
+        for (int j = 0; j < 2 && ok; ++j) {
+          if (gv > 0) ok = wait_bar(sm, &sm->v_free[j], (gv - 1) & 1, a.spin);
+          if (!ok) break;
+          mbar_expect_tx(&sm->v_full[j], n * 256);
+          send_for(it, vtile + j * kDimPart, image + (2 * j + rank) * it->stride, k0, n, &sm->v_full[j]);
+          parts = 4 + j + 1;
+        }
+        if (ok) { ++gv; parts = 0; }
+      };
+      bool sent = false;                     // the keys of this row block's first tile have been sent for
+      for (int e = 0; e < items && ok; ++e) {
+        if (e == 0) ok = wait_bar(sm, &sm->item_full[0], 0, a.spin);
         if (!ok) break;
-        mbar_expect_tx(&sm->v_full[j], n * 256);
-        send_for(it, vtile + j * kDimPart, image + (2 * j + rank) * it->stride, k0, n, &sm->v_full[j]);
-        parts = 4 + j + 1;
+        const Item* it = &sm->item[e & 1];
+        const int nt = it->nt;
+        if (nt > 0 && !sent) send_keys(it, 0);
+        for (int t = 0; t + 1 < nt && ok; ++t) {
+          send_keys(it, t + 1);
+          send_dims(it, t);
+        }
+        // the next row block's first keys before this one's last dims
+        if (ok && e + 1 < items) ok = wait_bar(sm, &sm->item_full[(e + 1) & 1], ((e + 1) >> 1) & 1, a.spin);
+        sent = ok && nt > 0 && e + 1 < items && sm->item[(e + 1) & 1].nt > 0;
+        if (sent) send_keys(&sm->item[(e + 1) & 1], 0);
+        if (nt > 0 && ok) send_dims(it, nt - 1);
+        mbar_arrive(&sm->item_free[e & 1]);
       }
-      if (ok) { ++gv; parts = 0; }
-    };
-    bool sent = false;                     // the keys of this row block's first tile have been sent for
-    for (int e = 0; e < items && ok; ++e) {
-      if (e == 0) ok = wait_bar(sm, &sm->item_full[0], 0, a.spin);
-      if (!ok) break;
-      const Item* it = &sm->item[e & 1];
-      const int nt = it->nt;
-      if (nt > 0 && !sent) send_keys(it, 0);
-      for (int t = 0; t + 1 < nt && ok; ++t) {
-        send_keys(it, t + 1);
-        send_dims(it, t);
+      // copies in flight (there are none, unless a wait gave up): the last ones to each place
+      {
+        for (int m = 0; m < 4; ++m) {
+          const int n = gk + (parts < 4 && m < parts ? 1 : 0);
+          if (n > 0) mbar_wait(&sm->k_full[m], (n - 1) & 1, kDrainLimit);
+        }
+        for (int j = 0; j < 2; ++j) {
+          const int n = gv + (parts > 4 + j ? 1 : 0);
+          if (n > 0) mbar_wait(&sm->v_full[j], (n - 1) & 1, kDrainLimit);
+        }
       }
-      // the next row block's first keys before this one's last dims
-      if (ok && e + 1 < items) ok = wait_bar(sm, &sm->item_full[(e + 1) & 1], ((e + 1) >> 1) & 1, a.spin);
-      sent = ok && nt > 0 && e + 1 < items && sm->item[(e + 1) & 1].nt > 0;
-      if (sent) send_keys(&sm->item[(e + 1) & 1], 0);
-      if (nt > 0 && ok) send_dims(it, nt - 1);
-      mbar_arrive(&sm->item_free[e & 1]);
-    }
-    // copies in flight (there are none, unless a wait gave up): the last ones to each place
-    {
-      for (int m = 0; m < 4; ++m) {
-        const int n = gk + (parts < 4 && m < parts ? 1 : 0);
-        if (n > 0) mbar_wait(&sm->k_full[m], (n - 1) & 1, kDefaultSpinLimit);
-      }
-      for (int j = 0; j < 2; ++j) {
-        const int n = gv + (parts > 4 + j ? 1 : 0);
-        if (n > 0) mbar_wait(&sm->v_full[j], (n - 1) & 1, kDefaultSpinLimit);
-      }
-    }
     }
     __syncwarp();
   } else if (warp == kMmaWarp && rank == 1) {   // ---- tells the even block of this one's copies
@@ -1178,8 +1181,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     __syncwarp();
   } else if (warp < kSoftWarps) {          // ---- softmax
     int g = 0;
+    bool ok = true;
     for (int e = 0; e < items; ++e) {
-      const bool there = wait_warp(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
+      const bool there = ok && wait_warp(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
       if (role_any<kSoftId, kSoftWarps * 32>(!there)) break;
       const Item* it = &sm->item[e & 1];
       const int r = 32 * (warp & 1) + lane;
@@ -1187,7 +1191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       RowState s;
       s.reset();
       const int nt = it->nt;
-      for (int t = 0; t < nt; ++t, ++g) weigh_tile(a, sm, it, ptile, tmem, rank, g, it->begin + t, t == 0, sees, s);
+      for (int t = 0; t < nt; ++t, ++g) weigh_tile(a, sm, it, ptile, tmem, rank, g, it->begin + t, t == 0, sees, s, ok);
       const int quarter = 2 * (warp >> 2) + ((warp >> 1) & 1);   // of the keys
       if (quarter == 0) sm->ref[e & 1][r] = s.m == -INFINITY ? -INFINITY : s.msub;
       sm->sums[e & 1][quarter][r] = make_float2(s.l, s.hat);
@@ -1199,9 +1203,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     }
   } else {                                 // ---- queries and outputs
     int g = 0;
+    bool ok = true;
     auto item_there = [&](int e) {
-      const bool there = wait_warp(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
-      return !role_any<kOutId, kOutThreads>(!there);
+      ok = ok && wait_warp(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
+      return !role_any<kOutId, kOutThreads>(!ok);
     };
     auto queries = [&](int e) {
       const Item* it = &sm->item[e & 1];
@@ -1214,16 +1219,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     for (int e = 0; e < items && there; ++e) {
       const Item* it = &sm->item[e & 1];
       g += it->nt;
-      wait_warp(sm, &sm->q_free, e & 1, a.spin);   // the last S product on these queries is complete
+      ok = ok && wait_warp(sm, &sm->q_free, e & 1, a.spin);   // the last S product on these queries is complete
       if (e + 1 < items) {
         there = item_there(e + 1);
         if (there) queries(e + 1);
       }
-      wait_warp(sm, &sm->l_full[e & 1], (e >> 1) & 1, a.spin);
-      finish_sums(a, it, sm, rank, e);
+      ok = ok && wait_warp(sm, &sm->l_full[e & 1], (e >> 1) & 1, a.spin);
+      if (ok) finish_sums(a, it, sm, rank, e);
       role_sync<kOutId, kOutThreads>();
-      wait_warp(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
-      if (it->nt > 0) wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
+      ok = ok && wait_warp(sm, &sm->f_full[e & 1], (e >> 1) & 1, a.spin);   // the other rows' factors
+      if (it->nt > 0) ok = ok && wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
+      if (!ok) continue;
       tc_fence_after();
 #pragma unroll 1
       for (int j = 0; j < 2; ++j)
@@ -1419,7 +1425,7 @@ cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t*
   a.ratio = ratio;
   a.n_entries = n_entries;
   a.max_entries = max_entries;
-  a.window = window;
+  a.window = std::min(window, 1 << 30);   // (no length is more; differences stay within 32 bits)
   a.max_ctx = max_ctx;
   a.sink = sink;
   a.scale_log2 = scale * kLog2e;

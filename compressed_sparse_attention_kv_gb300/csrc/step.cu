@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kMapThreads) plan_maps_kernel(const __grid_con
 // Bound: writes, 256 bytes a position, beside about 50 instructions a pair.
 // ---------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
+constexpr int kRopeBlocks = 7;                   // of an SM: all are resident (36 registers a thread), none waits for a place
 constexpr int kRopeAtOnce = kRopeThreads / 16;   // positions of a block at a time: a thread has two pairs
 
 struct RopeArgs {
@@ -336,13 +337,15 @@ __device__ __forceinline__ float4 cos_sin_of_turns(const uint64_t (&t)[2]) {
   float part[2][3];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    q[u] = static_cast<uint32_t>((t[u] + (1ull << 61)) >> 62);
-    const int64_t r = static_cast<int64_t>(t[u] - (static_cast<uint64_t>(q[u]) << 62));   // [-2^61, 2^61)
+    const uint32_t low = static_cast<uint32_t>(t[u]);
+    uint32_t high = static_cast<uint32_t>(t[u] >> 32);
+    q[u] = (high + 0x20000000u) >> 30;
+    high -= q[u] << 30;   // what is left, signed: [-2^61, 2^61) with the low word
     // in three pieces, each a float without rounding (conversions of 64 bits run at a quarter of the
     // rate: 25.5 us instead of 16)
-    part[u][0] = static_cast<float>(static_cast<int>(r >> 46));
-    part[u][1] = float23(static_cast<uint32_t>(r >> 23) & 0x7FFFFFu);
-    part[u][2] = float23(static_cast<uint32_t>(r) & 0x7FFFFFu);
+    part[u][0] = __uint_as_float(0x4B400000u + (static_cast<int>(high) >> 14)) - 12582912.0f;
+    part[u][1] = float23(__funnelshift_l(low, high, 9) & 0x7FFFFFu);
+    part[u][2] = float23(low & 0x7FFFFFu);
   }
   const Two r2 = mul(Two{part[0][0], part[1][0]}, both(0x1p46f)), r1 = mul(Two{part[0][1], part[1][1]}, both(0x1p23f));
   const Two rh = add(r2, r1);
@@ -374,7 +377,7 @@ __device__ __forceinline__ float4 cos_sin_of_turns(const uint64_t (&t)[2]) {
   return make_float4(o[0], o[1], o[2], o[3]);
 }
 
-__global__ void __launch_bounds__(kRopeThreads) rope_cs_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_cs_kernel(const __grid_constant__ RopeArgs a) {
   const int two = threadIdx.x & 15;
   uint64_t speed[2], more[2];   // bits 2^-1 .. 2^-64 of a turn; 2^-33 .. 2^-96
   const int32_t* pos[2];
@@ -385,14 +388,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cs_kernel(const __grid_cons
     more[u] = static_cast<uint64_t>(w[1]) << 32 | w[2];
     pos[u] = a.pos + a.plan.axis[2 * two + u] * a.axis_stride;
   }
-  const long long step = static_cast<long long>(gridDim.x) * kRopeAtOnce;
-  long long i = static_cast<long long>(blockIdx.x) * kRopeAtOnce + (threadIdx.x >> 4);
+  const int step = gridDim.x * kRopeAtOnce;
+  int i = blockIdx.x * kRopeAtOnce + (threadIdx.x >> 4);
+  float4* out = reinterpret_cast<float4*>(a.out) + static_cast<long long>(i) * 16 + two;
   int next[2] = {0, 0};
   if (i < a.T) {
     next[0] = __ldg(pos[0] + i);
     next[1] = __ldg(pos[1] + i);
   }
-  for (; i < a.T; i += step) {
+  for (; i < a.T; i += step, out += static_cast<long long>(step) * 16) {
     const int now[2] = {next[0], next[1]};
     if (i + step < a.T) {
       next[0] = __ldg(pos[0] + i + step);
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_cs_kernel(const __grid_cons
       const uint32_t low = static_cast<uint32_t>(p);
       t[u] = speed[u] * low + __umulhi(low, static_cast<uint32_t>(more[u])) - (p < 0 ? more[u] : 0);
     }
-    reinterpret_cast<float4*>(a.out)[i * 16 + two] = cos_sin_of_turns(t);
+    *out = cos_sin_of_turns(t);
   }
 }
 
@@ -605,7 +609,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const NormJob& j, lo
 
 // N: heads of 512 dims a warp has at a time
 template <int N>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, N == 4 ? 3 : 1) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   const long long w = static_cast<long long>(blockIdx.x) * kNormWarps + (threadIdx.x >> 5);
   int k = 0;
   while (k + 1 < a.njobs && w >= a.first[k + 1]) ++k;
@@ -687,7 +691,7 @@ cudaError_t launch_rope_cs(const cskvs_rope_plan& plan, const int32_t* pos, int6
   a.shift = shift;
   a.T = T;
   a.out = out;
-  const int blocks = std::min((T + kRopeAtOnce - 1) / kRopeAtOnce, 152 * 8);
+  const int blocks = std::min((T + kRopeAtOnce - 1) / kRopeAtOnce, 152 * kRopeBlocks);
   rope_cs_kernel<<<blocks, kRopeThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -13,7 +13,7 @@ from test_gpu_bounded_cache import BF16, FP4, FP8, SCALE, _cache, _check, _i32, 
 
 pytestmark = pytest.mark.gpu
 
-ERR_BOUNDS = 5
+ERR_BOUNDS, ERR_TIMEOUT = 5, 4
 
 
 class Case:
@@ -125,6 +125,19 @@ def test_a_bound_of_entries_beside_the_positions():
 def test_windows_alone():
     c = Case([50, 20, 1], [300, 20, 129], 20, None, window=100, rfmt=FP8, sink=True, seed=5)
     c.check(*c.run(), pick=_some(71, 16))
+
+
+def test_chunks_longer_than_their_requests_and_endless_windows():
+    """Queries before position 0 see nothing; a window of any size reaches back to the first row."""
+    c = Case([12, 3], [12, 3], 16, 1, FP8, window=2 ** 31 - 1, seed=30)
+    c.check(*c.run())
+    out, lse = c.run(ctx_len=_i32([5, 3]))
+    assert cskv.device_status() == 0
+    assert not out[:7].any() and torch.isneginf(lse[:7]).all()
+    for i in range(7, 12):
+        # the query at position i - 7, turned by the table's row of its own
+        keys = np.concatenate([c.entries.decoded[0][:i - 6], c.rows.decoded[0][:i - 6]])
+        _check(out[i], lse[i], bounded.attend(c.q[1][i], i, keys, None, SCALE))
 
 
 def test_requests_without_queries_and_rows_behind_the_last_one():
@@ -365,6 +378,70 @@ def test_calls_that_are_refused():
                 dict(softmax_scale=0.0), dict(max_entries=-1), dict(ctx_len=None)):
         with pytest.raises(cskv.CskvError):
             cskv.chunk_attn(**dict(a, **bad))
+
+
+@pytest.mark.parametrize("new,length,H", [([300], [9000], 64), ([5], [300], 16), ([40, 1, 0, 7], [500, 60, 0, 9], 128)])
+def test_waits_that_run_out_end_the_call_and_leave_the_next_one_exact(new, length, H):
+    c = Case(new, length, H, 1, FP8, window=128, sink=True, seed=24)
+    want = c.run()
+    assert cskv.device_status() == 0
+    cskv.set_spin_limit(64)
+    try:
+        for _ in range(3):
+            c.run()
+            assert cskv.device_status() == ERR_TIMEOUT
+    finally:
+        cskv.set_spin_limit(0)
+    out, lse = c.run()
+    assert cskv.device_status() == 0
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_calls_on_two_streams_at_once():
+    """Each with a workspace of its own; the same bits as one after the other."""
+    cases = [Case([200, 30], [900, 400], 64, 1, FP8, window=64, sink=True, seed=25), Case([150], [4000], 20, 4, FP4, seed=26)]
+    args = [c.args() for c in cases]
+    want = [cskv.chunk_attn(**a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(6):
+        for k in (0, 1):
+            got[k].append(cskv.chunk_attn(**args[k], stream=streams[k]))
+    torch.cuda.synchronize()
+    assert cskv.device_status() == 0
+    for k in (0, 1):
+        for out, lse in got[k]:
+            assert torch.equal(out, want[k][0]) and torch.equal(lse, want[k][1])
+
+
+def test_the_same_as_the_calls_for_windows_and_for_single_tokens():
+    """window_attn with a window as long as the request, prefix_decode_attn without a prefix: the
+    same definition, other kernels; each within its bound of it."""
+    c = Case([40, 25], [300, 200], 16, 1, FP8, sink=True, seed=27)
+    out, lse = c.run()
+    pos1 = c.pos + 1
+    w, wl = cskv.window_attn(c.q[0].cuda(), c.entries.to_device(), _i32(pos1), 300, 0, 300, cuda(c.sink), SCALE,
+                             cuda(cskv.rope_table(c.pos)), req_of=_i32(c.req), want_lse=True)
+    for i in range(0, 65, 7):
+        ref = c.want(i)
+        _check(out[i], lse[i], ref)
+        _check(w[i], wl[i], ref)
+    c = Case([1, 1, 1], [700, 129, 5], 64, 1, FP8, sink=True, seed=28)
+    out, lse = c.run()
+    p, pl = cskv.prefix_decode_attn(c.q[0].cuda(), c.entries.to_device(), _i32(c.len), 0, 700, cuda(c.sink), SCALE,
+                                    cuda(cskv.rope_table(c.pos)), want_lse=True)
+    for i in range(3):
+        ref = c.want(i)
+        _check(out[i], lse[i], ref)
+        _check(p[i], pl[i], ref)
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 7, 33, 50, 63, 127])
+def test_heads_that_fill_a_row_block_unevenly(H):
+    """Row blocks of 128 / H queries, in two halves that part between the heads of a query."""
+    c = Case([9, 130, 2], [200, 130, 777], H, 1, FP8, window=20, rfmt=FP8, sink=True, seed=H)
+    c.check(*c.run(), pick=_some(141, 16))
 
 
 # --- a server's steps --------------------------------------------------------------------------
