@@ -15,33 +15,36 @@
 // copies' writes come on top.  Two SMs that share 128 rows and their keys read half of it:
 // 36 products of 128 x 128 x 16 (34 cycles) and 16 of 256 x 128 x 16 (69) for 128 rows on 128 keys.
 //
-// Four kernels, each started while the one before it ends:
-//   chunk_plan_kernel    the requests' key lists, the row blocks and their tiles as one line of
-//                        work, cut into equal shares;
-//   chunk_decode_kernel  every key that some query sees, once, from its paged row to bf16 in the
-//                        order that the tensor core reads (the same rows are read by hundreds of row
-//                        blocks: decoding a tile takes longer than its products);
+// Three kernels, each started while the one before it ends:
+//   chunk_prepare_kernel its first block plans: the requests' key lists, the row blocks and their tiles as one line
+//                        of work, cut into equal shares.  The others decode meanwhile: every key that some query
+//                        sees, once, from its paged row to bf16 in the order that the tensor core reads (the
+//                        same rows are read by hundreds of row blocks: decoding a tile takes longer than
+//                        its products).  (Two kernels one after the other for very many requests.)
 //   chunk_attn_kernel    one pair of blocks (a cluster) per two SMs, its share of the work;
 //   chunk_join_kernel    the row blocks that a share's border cuts in two or more.
 //
-// chunk_attn_kernel.  A row block is up to 128 rows of one request, 128 / H queries; the even block of
+// A pair of blocks.  A row block has up to 128 (query, head) rows, whole queries of a request; the even block of
 // the pair has the first half of its rows, the odd one the second.  The keys come in tiles of 128.
 //   S  = Q K^T     each block gets its own rows x 128 keys; it holds its rows of Q and half of the
 //                  tile's keys, all dims (64 KB);
 //   O^T += V^T P^T each block gets all rows x two of the four blocks of 128 dims; it holds these dims of
 //                  all the tile's keys (64 KB) and its own rows of P (16 KB).
-// The products are issued for both by the even block.  Tensor memory: O in columns 0..255 (dims as
-// lanes), the logits of two tiles behind it (rows as lanes, 64 to 127 with the second half of
-// the keys).  Roles in each block:
+// The products are issued for both by the even block.  Tensor memory: three places of outputs (a block of 128
+// dims as lanes), by turns, so that a row block's products begin while the one before is read; the logits of
+// two tiles behind them (rows as lanes, 64 to 127 with the second half of the keys).  Roles in each block:
 //   warps 0-7    softmax of a tile: a thread has one row and 32 keys; P to shared memory;
-//   warps 8-15   the next row block's queries (loaded and rotated while the last products of this one
-//                run), and the outputs;
+//   warps 8-15   the next row block's queries (loaded and rotated ahead), and the outputs;
 //   warp 16      in the even block one thread issues the products, S of the next tile before O of this
-//                one, so that the softmax runs beside products; in the odd block one thread tells the
-//                even one which copies have arrived;
+//                one, also from row block to row block, so that the softmax runs beside products; in the odd
+//                block one thread tells the even one which copies have arrived;
 //   warp 17      sends for the keys (bulk copies of a block of 128 dims), as soon as the product on the
 //                same place's keys before is complete;
 //   warp 18      plans the row blocks, two at a time.
+// Measured: two tiles take O + S + the softmax and what lies between, 5,400 cycles; the products alone are 4,660
+// of them.  What the single threads do between a barrier and the next product or copy counts in full, and
+// so does code that drops out of the instruction caches: a clock read before every wait cost 16 % (4,096
+// queries on 8,320 keys: 2.72 -> 3.3 ms), the give-up path of every wait in line 8 % of three short prompts.
 // A row's reference belongs to its block, its output's columns to both: when a reference moves, the
 // factors go to the other block's shared memory, and a flag for every tile says whether they did.
 // Roundings as in list_attn.cu: the rotated query as two bf16 numbers, P in bf16 over the sum of the
@@ -67,13 +70,21 @@ constexpr int kSoftWarps = 8, kOutWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kOutWarps, kLoadWarp = kMmaWarp + 1, kPlanWarp = kMmaWarp + 2;
 constexpr int kThreads = (kPlanWarp + 1) * 32;
 constexpr int kOutThreads = kOutWarps * 32;
-constexpr uint32_t kTmemS = 256;          // TMEM columns: O 0..255, S from here, 64 for each tile
+constexpr int kPlaces = 3;                // of outputs in tensor memory: 128 dims of a row block (128 columns)
+constexpr uint32_t kTmemS = kPlaces * 2 * kRows;   // TMEM columns: O, then S, 64 for each tile
 constexpr float kSlack = 8.0f;            // base 2
 constexpr int kPairs = 76;                // of SMs
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;         // of the plan alone
+constexpr int kPrepThreads = 256;          // of the plan beside the decoding, and of the decoding
+constexpr int kOwnReqs = 1024;             // requests whose rows every decoding block sums up itself
 constexpr int kPlanItems = 4;             // row blocks of a thread at a time
-constexpr int kItemUnits = 3;             // a row block's cost beside its tiles, a tile being 2
-constexpr int kLeastShare = 8;            // units of a share
+// A row block's cost beside its tiles, a tile being 2 (three ragged prompts, 173 row blocks: 71.6, 69.4, 67.7 and
+// 68.4 us with 2, 3, 4 and 5).
+constexpr int kItemUnits = 4;
+// Units of a share at least (5 tokens on 288 keys, 3 tiles: 18.4 us on several pairs with 4, 17.6 us on one with 8;
+// with 16 the same).
+constexpr int kLeastShare = 8;
+constexpr int kFewParts = 8;              // of a row: joined by one warp
 constexpr unsigned long long kDrainLimit = 1ull << 27;   // cycles that a block which gives up waits for its own copies
 
 struct ReqPlan {
@@ -82,16 +93,24 @@ struct ReqPlan {
   int row0, rows, rows16;   // its first decoded raw row, how many, rounded up
   long long base;           // its first decoded row
   int item0;                // its first row block
-  int bad;                  // a row of it could not be read or is not finite
+};
+struct ItemPlan {           // of a row block
+  long long unit0;          // its first unit of work
+  int req, pad;
 };
 struct SharePlan {
-  int first, last;          // the row blocks of a pair's share
+  ItemPlan plan;            // of its first row block
+  long long lo, hi;         // a pair's units [lo, hi)
+  int first, last;          // the row blocks that have some of them
 };
-struct SplitPlan {
-  int item, b0, b1, pad;    // a row block that pairs b0 .. b1 share
+struct SplitPlan {          // a row block that several pairs share
+  int row0, rows;           // its rows of [T * H]
+  int first, next;          // its first part, and its second one: each further one is two behind
+  int parts, pad[3];
 };
 struct ChunkHead {
-  int items, blocks, splits, pad;
+  int items, blocks;
+  int few, many;            // split[0 .. few): row blocks of kFewParts parts at most; split[most_blocks - many ..): of more
   long long units;          // of all row blocks
   long long keys;           // decoded rows
 };
@@ -113,14 +132,16 @@ struct ChunkArgs {
   float* lse;
   long long max_keys;
   int group;                // queries of a row block
+  int head_inv;             // 2^16 / H, rounded up: row / H is row * head_inv >> 16 for rows of a row block
   int most_blocks;          // shares at most
   // workspace
   ChunkHead* head;
   ReqPlan* req;
-  long long* unit0;         // [items + 1]
+  ItemPlan* item;           // [items + 1]; the last one ends the units
   SharePlan* share;         // [most_blocks]
   SplitPlan* split;         // [most_blocks]
   uint8_t* flags;           // of every decoded row: 0, kNone, kUnfit
+  uint8_t* bad;             // of every eight of them: whether a row that is there cannot be used
   uint8_t* images;          // decoded rows: of each request 4 blocks of 128 dims as they lie in a stage
   float* opart;             // [2 * most_blocks][2 * kRows][512]
   float2* ml;               // [2 * most_blocks][2 * kRows]: m (base 2) and l
@@ -136,18 +157,6 @@ __device__ __forceinline__ int half_keys(int n) { return up16((n + 1) / 2); }
 // ---------------------------------------------------------------------------
 // row blocks
 // ---------------------------------------------------------------------------
-// The request of row block e, by the first row blocks of the requests.
-__device__ __forceinline__ int request_of_item(const ChunkArgs& a, int e) {
-  int r = 0, n = a.R;
-  while (n > 1) {   // the last request whose first row block is not behind e
-    const int half = n / 2;
-    const bool le = a.req[r + half].item0 <= e;
-    r = le ? r + half : r;
-    n = le ? n - half : half;
-  }
-  return r;
-}
-
 // What row block e of request p sees: entries [0, seen) and decoded raw rows [lo, hi) (counted from
 // the request's first decoded one), both as lists of whole 16 rows: entries16 of them, then raw
 // rows from raw0.
@@ -176,167 +185,224 @@ __device__ __forceinline__ BlockKeys block_keys(const ChunkArgs& a, const ReqPla
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 __device__ __forceinline__ int units_of(int tiles) { return 2 * max(tiles, 1) + kItemUnits; }
 
+// a / b, most often of 32 bits (b's are below 2^31)
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
 // Shares: pair b has the units [units * b / blocks, units * (b + 1) / blocks); tile t of a row block
 // begins at its unit 2 t and belongs to the pair that has this unit.
-__device__ __forceinline__ long long share_begin(long long units, int blocks, int b) { return units * b / blocks; }
+__device__ __forceinline__ long long share_begin(long long units, int blocks, int b) { return divide(units * b, blocks); }
 __device__ __forceinline__ int block_of_unit(long long units, int blocks, long long u) {
-  return static_cast<int>(((u + 1) * blocks - 1) / units);
+  return static_cast<int>(divide((u + 1) * blocks - 1, units));
 }
 // the last row block that begins at or before unit u
-__device__ __forceinline__ int item_of_unit(const long long* unit0, int items, long long u) {
+template <class Unit0>
+__device__ __forceinline__ int item_of_unit(Unit0&& unit0, int items, long long u) {
   int e = 0, n = items;
   while (n > 1) {
     const int half = n / 2;
-    const bool le = unit0[e + half] <= u;
+    const bool le = unit0(e + half) <= u;
     e = le ? e + half : e;
     n = le ? n - half : half;
   }
   return e;
 }
 
-// Inclusive sums of a block's values; `total` gets the last one.
-__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
+// Inclusive sums of a block's pairs of values; `total` gets the last ones.
+struct Pair {
+  long long x;
+  int y;
+};
+__device__ __forceinline__ Pair block_scan(Pair v, Pair* part, Pair* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  auto warp_scan = [&](Pair& p) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xFFFFFFFFu, v, o);
-    if (lane >= o) v += x;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xFFFFFFFFu, p.x, o);
+      const int y = __shfl_up_sync(0xFFFFFFFFu, p.y, o);
+      if (lane >= o) {
+        p.x += x;
+        p.y += y;
+      }
+    }
+  };
+  warp_scan(v);
   if (lane == 31) part[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    long long x = lane < warps ? part[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    part[lane] = x;
+    Pair p = lane < warps ? part[lane] : Pair{0, 0};
+    warp_scan(p);
+    part[lane] = p;
   }
   __syncthreads();
-  if (warp > 0) v += part[warp - 1];
+  if (warp > 0) {
+    v.x += part[warp - 1].x;
+    v.y += part[warp - 1].y;
+  }
   *total = part[warps - 1];
   __syncthreads();   // part is used again
   return v;
 }
 
-constexpr int kPlanStaged = 4096;         // row blocks whose places are searched in shared memory
+// What request r has; a wrong length is told by the plan alone.
+template <bool kTell>
+__device__ __forceinline__ ReqPlan request_of(const ChunkArgs& a, int r) {
+  auto wrong = [] { if constexpr (kTell) set_err(CSKV_ERR_BOUNDS); };
+  ReqPlan p = {};
+  const int lo = a.cu_q[r], hi = a.cu_q[r + 1];
+  int len = a.ctx_len != nullptr ? a.ctx_len[r] : 0, given = a.n_entries != nullptr ? a.n_entries[r] : 0;
+  if (lo < 0 || hi < lo || hi > a.T) wrong();
+  else { p.q0 = lo; p.nq = hi - lo; }
+  if (p.nq == 0) return p;
+  if (len < 0 || len > a.max_ctx) { wrong(); len = max(0, min(len, a.max_ctx)); }
+  p.len = len;
+  if (a.has_entries) {
+    int n = a.ratio > 0 ? len / a.ratio : a.max_entries;
+    if (a.n_entries != nullptr) {
+      if (given < 0 || given > a.max_entries) { wrong(); given = max(0, min(given, a.max_entries)); }
+      n = min(n, given);
+    }
+    if (n > a.max_entries) { wrong(); n = a.max_entries; }
+    p.entries = n;
+  }
+  if (a.has_rows) {
+    p.rows = static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(p.nq) + a.window - 1));
+    p.row0 = len - p.rows;
+  }
+  p.entries16 = up16(p.entries);
+  p.rows16 = up16(p.rows);
+  return p;
+}
 
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
-  __shared__ long long part[32], staged[kPlanStaged];
-  grid_dep_launch();
+constexpr int kPlanStaged = 2048;         // row blocks whose places are searched in shared memory
+struct PlanSmem {
+  Pair part[32];
+  long long staged[kPlanStaged];
+  int item0[kOwnReqs];
+};
+
+__device__ void plan_chunks(const ChunkArgs& a, PlanSmem& sm) {
+  Pair* part = sm.part;
   const int tid = threadIdx.x;
-  long long keys = 0, items = 0, total;
-  for (int r0 = 0; r0 < a.R; r0 += kPlanThreads) {
+  long long keys = 0;
+  int items = 0;
+  Pair total;
+  for (int r0 = 0; r0 < a.R; r0 += blockDim.x) {
     const int r = r0 + tid;
     ReqPlan p = {};
-    if (r < a.R) {
-      const int lo = a.cu_q[r], hi = a.cu_q[r + 1];
-      if (lo < 0 || hi < lo || hi > a.T) set_err(CSKV_ERR_BOUNDS);
-      else { p.q0 = lo; p.nq = hi - lo; }
-      if (p.nq > 0) {
-        int len = a.ctx_len != nullptr ? a.ctx_len[r] : 0;
-        if (len < 0 || len > a.max_ctx) { set_err(CSKV_ERR_BOUNDS); len = max(0, min(len, a.max_ctx)); }
-        p.len = len;
-        if (a.has_entries) {
-          int n = a.ratio > 0 ? len / a.ratio : a.max_entries;
-          if (a.n_entries != nullptr) {
-            int m = a.n_entries[r];
-            if (m < 0 || m > a.max_entries) { set_err(CSKV_ERR_BOUNDS); m = max(0, min(m, a.max_entries)); }
-            n = min(n, m);
-          }
-          if (n > a.max_entries) { set_err(CSKV_ERR_BOUNDS); n = a.max_entries; }
-          p.entries = n;
-        }
-        if (a.has_rows) {
-          p.rows = static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(p.nq) + a.window - 1));
-          p.row0 = len - p.rows;
-        }
-        p.entries16 = up16(p.entries);
-        p.rows16 = up16(p.rows);
-      }
-    }
+    if (r < a.R) p = request_of<true>(a, r);
     const long long mine = static_cast<long long>(p.entries16) + p.rows16;
-    const long long upto = keys + block_scan(mine, part, &total);
-    keys += total;
-    p.base = upto - mine;
-    if (upto > a.max_keys && mine > 0) {   // no room
+    const int blocks = (p.nq + a.group - 1) / a.group;
+    const Pair upto = block_scan(Pair{mine, blocks}, part, &total);
+    p.base = keys + upto.x - mine;
+    p.item0 = items + upto.y - blocks;
+    if (p.base + mine > a.max_keys && mine > 0) {   // no room
       set_err(CSKV_ERR_BOUNDS);
       p.entries = p.entries16 = p.rows = p.rows16 = 0;
     }
-    const int blocks = (p.nq + a.group - 1) / a.group;
-    p.item0 = static_cast<int>(items + block_scan(blocks, part, &total) - blocks);
-    items += total;
+    keys += total.x;
+    items += total.y;
     if (r < a.R) a.req[r] = p;
+    if (r < kOwnReqs) sm.item0[r] = p.item0;
   }
   // the last request that has room ends the decoded rows
   keys = min(keys, a.max_keys);
   __syncthreads();
+  auto item0 = [&](int r) { return a.R <= kOwnReqs ? sm.item0[r] : a.req[r].item0; };
   long long units = 0;
-  for (int e0 = 0; e0 < items; e0 += kPlanThreads * kPlanItems) {
-    int mine[kPlanItems], sum = 0;
+  for (int e0 = 0; e0 < items; e0 += blockDim.x * kPlanItems) {
+    int mine[kPlanItems], req[kPlanItems], sum = 0;
     const int e1 = e0 + tid * kPlanItems;
-    int r = e1 < items ? request_of_item(a, e1) : 0;
+    int r = 0;
+    if (e1 < items) {
+      for (int n = a.R; n > 1;) {   // the last request whose first row block is not behind e1
+        const int half = n / 2;
+        const bool le = item0(r + half) <= e1;
+        r = le ? r + half : r;
+        n = le ? n - half : half;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kPlanItems; ++u) {
-      mine[u] = 0;
+      mine[u] = req[u] = 0;
       if (e1 + u < items) {
-        while (r + 1 < a.R && a.req[r + 1].item0 <= e1 + u) ++r;
+        while (r + 1 < a.R && item0(r + 1) <= e1 + u) ++r;
         const ReqPlan& p = a.req[r];
         mine[u] = units_of(tiles_of(block_keys(a, p, e1 + u - p.item0).keys));
+        req[u] = r;
       }
       sum += mine[u];
     }
-    long long at = units + block_scan(sum, part, &total) - sum;
-    units += total;
+    long long at = units + block_scan(Pair{sum, 0}, part, &total).x - sum;
+    units += total.x;
 #pragma unroll
     for (int u = 0; u < kPlanItems; ++u) {
       if (e1 + u < items) {
-        a.unit0[e1 + u] = at;
-        if (e1 + u < kPlanStaged) staged[e1 + u] = at;
+        a.item[e1 + u] = ItemPlan{at, req[u], 0};
+        if (e1 + u < kPlanStaged) sm.staged[e1 + u] = at;
       }
       at += mine[u];
     }
   }
   if (tid == 0) {
-    a.unit0[items] = units;
-    if (items < kPlanStaged) staged[items] = units;
+    a.item[items] = ItemPlan{units, 0, 0};
+    if (items < kPlanStaged) sm.staged[items] = units;
   }
   __syncthreads();
   const int blocks = static_cast<int>(max(1ll, min(static_cast<long long>(a.most_blocks), units / kLeastShare)));
   // the row blocks of each share; those that a border cuts are listed at the last border inside
   if (items == 0) {
-    if (tid == 0) a.share[0] = SharePlan{0, -1};
+    if (tid == 0) a.share[0].first = 0, a.share[0].last = -1;
   } else if (tid == 0) {
     a.share[0].first = 0;
-    a.share[blocks - 1].last = static_cast<int>(items) - 1;
+    a.share[0].plan = a.item[0];
+    a.share[0].lo = 0;
+    a.share[blocks - 1].hi = units;
+    a.share[blocks - 1].last = items - 1;
   }
-  const long long* unit0 = items < kPlanStaged ? staged : a.unit0;
-  int splits = 0;
-  for (int b0 = 1; b0 < blocks; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    bool last = false;
-    int e = 0;
-    if (b < blocks) {
-      const long long u = share_begin(units, blocks, b);
-      e = item_of_unit(unit0, static_cast<int>(items), u);
-      const int tiles = (static_cast<int>(unit0[e + 1] - unit0[e]) - kItemUnits) / 2;
-      const long long end = unit0[e] + 2ll * (tiles - 1);   // its last tile
-      a.share[b].first = e + (end < u);                     // (its tiles are all before the border)
-      a.share[b - 1].last = e - (unit0[e] == u);
-      last = u > unit0[e] && u <= end && block_of_unit(units, blocks, end) == b;
+  auto unit0 = [&](int e) { return items < kPlanStaged ? sm.staged[e] : a.item[e].unit0; };
+  static_assert(kPairs <= kPrepThreads, "a thread for each border");
+  const int b = tid + 1;
+  SplitPlan split = {};
+  if (b < blocks) {
+    const long long u = share_begin(units, blocks, b);
+    const int e = item_of_unit(unit0, items, u);
+    const long long u0 = unit0(e);
+    const int tiles = (static_cast<int>(unit0(e + 1) - u0) - kItemUnits) / 2;
+    const long long end = u0 + 2ll * (tiles - 1);   // its last tile
+    const int first = e + (end < u);                // (its tiles are all before the border)
+    a.share[b].first = first;
+    a.share[b].plan = a.item[first];
+    a.share[b].lo = u;
+    a.share[b - 1].hi = u;
+    a.share[b - 1].last = e - (u0 == u);
+    if (u > u0 && u <= end && block_of_unit(units, blocks, end) == b) {
+      const int b0 = block_of_unit(units, blocks, u0);
+      const ReqPlan& p = a.req[a.item[e].req];
+      const int i0 = (e - p.item0) * a.group;
+      split.row0 = (p.q0 + i0) * a.H;
+      split.rows = min(p.nq - i0, a.group) * a.H;
+      split.first = 2 * b0 + (u0 > share_begin(units, blocks, b0));
+      split.next = 2 * (b0 + 1);
+      split.parts = b - b0 + 1;
     }
-    const long long at = splits + block_scan(last, part, &total) - 1;
-    if (last) a.split[at] = SplitPlan{e, block_of_unit(units, blocks, unit0[e]), b, 0};
-    splits += static_cast<int>(total);
   }
-  if (tid == 0) *a.head = ChunkHead{static_cast<int>(items), blocks, splits, 0, units, keys};
+  const bool few = split.parts > 0 && split.parts <= kFewParts, many = split.parts > kFewParts;
+  const Pair at = block_scan(Pair{few, many}, part, &total);
+  if (few) a.split[at.x - 1] = split;
+  if (many) a.split[a.most_blocks - at.y] = split;
+  if (tid == 0) *a.head = ChunkHead{items, blocks, static_cast<int>(total.x), total.y, units, keys};
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
+  __shared__ PlanSmem sm;
+  grid_dep_launch();
+  plan_chunks(a, sm);
 }
 
 // ---------------------------------------------------------------------------
 // the keys
 // ---------------------------------------------------------------------------
-constexpr int kDecodeThreads = 256;
 constexpr int kDecodeRows = 8;    // of a warp at a time: a group of the image (a request's rows are whole 16s)
 
 // The bytes of 16 neighbouring dims of a row, and their scale.
@@ -376,61 +442,101 @@ struct RawRow<CSKV_FMT_FP4_E2M1_E4M3_B16> {
 };
 
 // Eight rows (lane i < 8 has row i's address, nullptr: none) into their group of the image; returns
-// a bit for each that is not finite, whose values become 0.  All loads are on their way before the
-// first is used.
+// a bit for each that is not finite, whose values become 0.  All loads (of four rows, if they are long
+// ones) are on their way before the first is used.
 template <int FMT>
 __device__ __forceinline__ uint32_t decode_rows(const uint8_t* mine, uint8_t* image) {
+  constexpr int kAtOnce = FMT == CSKV_FMT_BF16 ? kDecodeRows / 2 : kDecodeRows;
   const int lane = threadIdx.x & 31;
-  RawRow<FMT> raw[kDecodeRows] = {};
-#pragma unroll
-  for (int i = 0; i < kDecodeRows; ++i) {
-    const uint8_t* row = reinterpret_cast<const uint8_t*>(
-        __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), i));
-    if (row != nullptr) raw[i].load(row, lane);
-  }
   const uint32_t there = __ballot_sync(0xFFFFFFFFu, mine != nullptr);
   uint32_t unfit = 0;
 #pragma unroll
-  for (int i = 0; i < kDecodeRows; ++i) {
-    uint32_t w[8] = {}, bad = 0;
-    if ((there >> i) & 1u) raw[i].to_bf16(w);
+  for (int i0 = 0; i0 < kDecodeRows; i0 += kAtOnce) {
+    RawRow<FMT> raw[kAtOnce] = {};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) bad |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-    if (__any_sync(0xFFFFFFFFu, bad != 0u)) {   // (an exponent of all ones carries into the sign bit)
-      unfit |= 1u << i;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = 0u;
+    for (int i = 0; i < kAtOnce; ++i) {
+      const uint8_t* row = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), i0 + i));
+      if (row != nullptr) raw[i].load(row, lane);
     }
-    const int at = 2 * (lane & 3);
-    uint8_t* to = image + i * 128;
-    *reinterpret_cast<uint4*>(to + ((at ^ i) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(to + (((at + 1) ^ i) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      uint32_t w[8] = {}, bad = 0;
+      if ((there >> (i0 + i)) & 1u) raw[i].to_bf16(w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) bad |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+      if (__any_sync(0xFFFFFFFFu, bad != 0u)) {   // (an exponent of all ones carries into the sign bit)
+        unfit |= 1u << (i0 + i);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = 0u;
+      }
+      const int at = 2 * (lane & 3);
+      uint8_t* to = image + (i0 + i) * 128;
+      // the two pieces of 16 bytes are a sector, the second one first in every other row
+      const int o = (i0 + i) & 1 ? 4 : 0;
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + (((at ^ (i0 + i)) & ~1) << 4)), "r"(w[o]),
+                   "r"(w[o + 1]), "r"(w[o + 2]), "r"(w[o + 3]), "r"(w[4 - o]), "r"(w[5 - o]), "r"(w[6 - o]), "r"(w[7 - o])
+                   : "memory");
+    }
   }
   return unfit;
 }
 
-__global__ void __launch_bounds__(kDecodeThreads) chunk_decode_kernel(const __grid_constant__ ChunkArgs a) {
-  grid_dep_wait();
-  grid_dep_launch();
+struct ReqRows {            // of a request: its decoded rows
+  long long base;
+  int entries, rows, row0, pad;
+};
+struct DecodeSmem {
+  Pair part[32];
+  ReqRows req[kOwnReqs];
+};
+
+// Eight rows a warp, from block `block` of `blocks` on.  kOwn: the requests' places are the sums of this block itself (they
+// are made in the time that a wait for the plan would take); else the plan's.
+template <bool kOwn>
+__device__ __forceinline__ void decode_chunks(const ChunkArgs& a, DecodeSmem* sm, int block, int blocks) {
   const int lane = threadIdx.x & 31;
-  const long long keys = a.head->keys;
-  const long long warps = static_cast<long long>(gridDim.x) * (kDecodeThreads / 32);
-  for (long long x = (static_cast<long long>(blockIdx.x) * kDecodeThreads + threadIdx.x) / 32 * kDecodeRows; x < keys;
+  long long keys;
+  if constexpr (kOwn) {
+    Pair total;
+    const int each = (a.R + kPrepThreads - 1) / kPrepThreads, r0 = threadIdx.x * each;
+    long long mine = 0;
+    for (int r = r0; r < min(a.R, r0 + each); ++r) {
+      const ReqPlan p = request_of<false>(a, r);
+      sm->req[r] = ReqRows{mine, p.entries, p.rows, p.row0, 0};
+      mine += p.entries16 + p.rows16;
+    }
+    const long long before = block_scan(Pair{mine, 0}, sm->part, &total).x - mine;
+    for (int r = r0; r < min(a.R, r0 + each); ++r) {
+      ReqRows& p = sm->req[r];
+      p.base += before;
+      if (p.base + up16(p.entries) + up16(p.rows) > a.max_keys) p.entries = p.rows = 0;   // no room
+    }
+    keys = min(total.x, a.max_keys);
+    __syncthreads();
+  } else {
+    keys = a.head->keys;
+  }
+  const long long warps = static_cast<long long>(blocks) * (kPrepThreads / 32);
+  for (long long x = (static_cast<long long>(block) * kPrepThreads + threadIdx.x) / 32 * kDecodeRows; x < keys;
        x += warps * kDecodeRows) {
     int r = 0, n = a.R;
     while (n > 1) {   // the last request whose rows begin at or before x
       const int half = n / 2;
-      const bool le = a.req[r + half].base <= x;
+      const bool le = (kOwn ? sm->req[r + half].base : a.req[r + half].base) <= x;
       r = le ? r + half : r;
       n = le ? n - half : half;
     }
-    const ReqPlan p = a.req[r];
-    const long long rows = p.entries16 + p.rows16;
+    ReqRows p;
+    if constexpr (kOwn) p = sm->req[r];
+    else p = ReqRows{a.req[r].base, a.req[r].entries, a.req[r].rows, a.req[r].row0, 0};
+    const int entries16 = up16(p.entries);
+    const long long rows = entries16 + up16(p.rows);
     if (x - p.base >= rows) continue;   // no room for this request
     const int first = static_cast<int>(x - p.base);
-    const bool raw = first >= p.entries16;
+    const bool raw = first >= entries16;
     const cskv_paged& c = raw ? a.rows : a.entries;
-    const int k0 = raw ? first - p.entries16 : first, have = raw ? p.rows : p.entries;
+    const int k0 = raw ? first - entries16 : first, have = raw ? p.rows : p.entries;
     const int row_bytes = c.fmt == CSKV_FMT_BF16 ? 2 * kD : c.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32 ? kD + kD / 32 : kD / 2 + kD / 16;
     const bool exists = lane < kDecodeRows && k0 + lane < have;
     const uint8_t* mine = nullptr;
@@ -441,11 +547,29 @@ __global__ void __launch_bounds__(kDecodeThreads) chunk_decode_kernel(const __gr
                            : c.fmt == CSKV_FMT_FP8_E4M3_E8M0_B32 ? decode_rows<CSKV_FMT_FP8_E4M3_E8M0_B32>(mine, image)
                                                                 : decode_rows<CSKV_FMT_FP4_E2M1_E4M3_B16>(mine, image);
     if (lane < kDecodeRows) a.flags[x + lane] = mine == nullptr ? kNone : (unfit >> lane) & 1u ? kUnfit : 0;
-    // a row that is there and cannot be used (those behind the last one are seen by nobody)
-    if (__any_sync(0xFFFFFFFFu, exists && mine == nullptr) || unfit != 0u) {
-      if (lane == 0) a.req[r].bad = 1;
-    }
+    // (rows behind the last one are seen by nobody)
+    const bool bad = __any_sync(0xFFFFFFFFu, exists && mine == nullptr) || unfit != 0u;
+    if (lane == 0) a.bad[x / kDecodeRows] = bad;
   }
+}
+
+constexpr int kPrepBlocks = 3;    // of an SM: all are resident, so that the next kernel's blocks come as these end
+// The first block plans, the others decode.
+__global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) chunk_prepare_kernel(const __grid_constant__ ChunkArgs a) {
+  __shared__ union Smem {
+    PlanSmem plan;
+    DecodeSmem decode;
+    __device__ Smem() {}
+  } sm;
+  grid_dep_launch();
+  if (blockIdx.x == 0) plan_chunks(a, sm.plan);
+  else decode_chunks<true>(a, &sm.decode, blockIdx.x - 1, gridDim.x - 1);
+}
+
+__global__ void __launch_bounds__(kPrepThreads, kPrepBlocks) chunk_decode_kernel(const __grid_constant__ ChunkArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  decode_chunks<false>(a, nullptr, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -459,13 +583,14 @@ struct Item {
   int row0, rows, half;          // rows [row0, row0 + rows) of the [T * H] rows, the first `half` of them in the even block
   int r0, nr;                    // this block's
   int nq;                        // columns of O for a block's rows: half, rounded up to 16
-  int t0, one;                   // the first row's query; all rows are that query's
+  int t0;                        // the first row's query
   int seen16, raw0, keys;        // the list (BlockKeys); raw0 counted among all decoded rows of the request
   int begin, nt;                 // this pair's tiles
-  int plain;                     // keys below it are seen by every row
-  int bad;
   int part;                      // partial output, -1: none
   long long base, stride;        // the request's first decoded row, bytes between its blocks of dims
+  // of the softmax alone:
+  int plain;                     // keys below it are seen by every row
+  int bad;                       // a row of these tiles could not be read or is not finite
   RowSees sees[kRows];
 };
 
@@ -473,7 +598,7 @@ struct ChunkSmem {
   Item item[2];
   uint64_t k_full[4], k_free[4];           // keys: blocks of 128 dims
   uint64_t v_full[2], v_free[2];           // this block's dims
-  uint64_t s_full[2], moved[2], p_full, q_full, q_free, o_free[2], l_full[2], f_full[2], item_full[2], item_free[2], drained;
+  uint64_t s_full[2], moved[2], p_full, q_full, q_free, o_free[kPlaces], l_full[2], f_full[2], item_full[2], sees_full[2], item_free[2], drained;
   uint32_t tmem;
   int abort;
   int flag[2];                             // by tile: the other block's references moved
@@ -528,16 +653,22 @@ __device__ __forceinline__ void mma2_commit(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-__device__ __forceinline__ bool wait_on(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {   // at once
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return done != 0u;
+}
+// A wait that gives up makes every role leave its loop.
+__device__ __noinline__ bool wait_on(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
   const unsigned long long t0 = clock64();
-  while (!try_wait_long(bar, parity)) {
-    if (*reinterpret_cast<volatile int*>(&sm->abort)) return false;
-    if (clock64() - t0 > limit) {   // gave up: every role leaves its loop
-      set_err(CSKV_ERR_TIMEOUT);
+  do {
+    if (*reinterpret_cast<volatile int*>(&sm->abort) != 0 || clock64() - t0 > limit) {
       *reinterpret_cast<volatile int*>(&sm->abort) = 1;
       return false;
     }
-  }
+  } while (!try_wait_long(bar, parity));
   return true;
 }
 __device__ __forceinline__ bool wait_bar(ChunkSmem* sm, uint64_t* bar, uint32_t parity, unsigned long long limit) {
@@ -562,19 +693,44 @@ __device__ __forceinline__ bool role_any(bool p) {
 }
 constexpr int kSoftId = 1, kOutId = 2;
 
-// Row block e of this pair's share, and this block's rows of it; one warp.
-__device__ void make_item(const ChunkArgs& a, Item* it, int e, long long units, int blocks, int pair, int rank) {
+// Row block e of this pair's share, and this block's rows of it; one warp.  First what all others wait for.
+__device__ void make_item(const ChunkArgs& a, ChunkSmem* sm, int place, int e, const ItemPlan& plan, long long lo, long long hi,
+                          int pair, int rank) {
   const int lane = threadIdx.x & 31;
-  const ReqPlan p = a.req[request_of_item(a, e)];
+  Item* it = &sm->item[place];
+  const ReqPlan p = a.req[plan.req];
   const BlockKeys k = block_keys(a, p, e - p.item0);
   const int rows = (k.i1 - k.i0) * a.H, half = (rows + 1) / 2;
   const int at = rank == 0 ? 0 : half, nr = rank == 0 ? half : rows - half;   // of the row block
+  // its tiles between the share's borders
+  const int tiles = tiles_of(k.keys);
+  const int begin = static_cast<int>(min(static_cast<long long>(tiles), max(0ll, (lo - plan.unit0 + 1) / 2)));
+  const int end = static_cast<int>(min(static_cast<long long>(tiles), max(0ll, (hi - plan.unit0 + 1) / 2)));
+  const int raw_at = p.entries16 + k.raw0;
+  if (lane == 0) {
+    it->t0 = p.q0 + k.i0;
+    it->row0 = (p.q0 + k.i0) * a.H;
+    it->rows = rows;
+    it->half = half;
+    it->r0 = (p.q0 + k.i0) * a.H + at;
+    it->nr = nr;
+    it->nq = up16(half);
+    it->seen16 = k.seen16;
+    it->raw0 = raw_at;
+    it->keys = k.keys;
+    it->base = p.base;
+    it->stride = static_cast<long long>(p.entries16 + p.rows16) * 256;
+    it->begin = begin;
+    it->nt = end - begin;
+    it->part = begin > 0 || end < tiles ? 2 * pair + (plan.unit0 > lo) : -1;
+    mbar_arrive(&sm->item_full[place]);
+  }
   const int raw0 = k.raw0 + p.row0;   // position of the list's first raw row
   int least = INT32_MAX;
   for (int r = lane; r < kRows; r += 32) {
     RowSees s{0, 0, -1, 0};
     if (r < nr) {
-      const int pos1 = p.len - p.nq + k.i0 + (at + r) / a.H + 1;
+      const int pos1 = p.len - p.nq + k.i0 + ((at + r) * a.head_inv >> 16) + 1;
       s.seen = seen_entries(a, p, pos1);
       if (p.rows > 0 && pos1 > 0) {
         s.lo = k.seen16 + max(0, pos1 - a.window) - raw0;
@@ -585,86 +741,80 @@ __device__ void make_item(const ChunkArgs& a, Item* it, int e, long long units, 
     it->sees[r] = s;
   }
   least = __reduce_min_sync(0xFFFFFFFFu, least);
-  if (lane == 0) {
-    it->t0 = p.q0 + k.i0;
-    it->one = k.i1 - k.i0 == 1;
-    it->row0 = it->t0 * a.H;
-    it->rows = rows;
-    it->half = half;
-    it->r0 = it->row0 + at;
-    it->nr = nr;
-    it->nq = up16(half);
-    it->seen16 = k.seen16;
-    it->raw0 = p.entries16 + k.raw0;
-    it->keys = k.keys;
-    it->plain = least;
-    it->bad = p.bad;
-    it->base = p.base;
-    it->stride = static_cast<long long>(p.entries16 + p.rows16) * 256;
-    // its tiles between the share's borders
-    const long long u0 = a.unit0[e];
-    const int tiles = tiles_of(k.keys);
-    const long long lo = share_begin(units, blocks, pair), hi = share_begin(units, blocks, pair + 1);
-    const int begin = static_cast<int>(min(static_cast<long long>(tiles), max(0ll, (lo - u0 + 1) / 2)));
-    const int end = static_cast<int>(min(static_cast<long long>(tiles), max(0ll, (hi - u0 + 1) / 2)));
-    it->begin = begin;
-    it->nt = end - begin;
-    it->part = begin > 0 || end < tiles ? 2 * pair + (u0 > lo) : -1;
+  uint32_t bad = 0;
+  const uint8_t* groups = a.bad + p.base / kDecodeRows;
+  for (int g = begin * (kTile / kDecodeRows) + lane; g < min(end * kTile, k.keys) / kDecodeRows; g += 32) {
+    const int k0 = g * kDecodeRows;
+    bad |= groups[(k0 < k.seen16 ? k0 : raw_at + k0 - k.seen16) / kDecodeRows];
   }
+  bad = __any_sync(0xFFFFFFFFu, bad != 0u);
+  if (lane == 0) {
+    it->plain = least;
+    it->bad = bad;
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm->sees_full[place]);
 }
 
-// Queries into the K-major chunks of Q (64 rows apart; rows behind the last one zero); the output
-// warps.  The last 64 dims are then rotated in place: chunk 7 holds the first bf16 of each rotated
-// value, chunk 8 the second.  (The angles are on their way while the queries are awaited: loaded row by
-// row, they took 5,600 cycles.)
-__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item* it, uint8_t* qtile) {
-  const int tid = threadIdx.x - kSoftWarps * 32;
-  const uint8_t* q = a.q + static_cast<size_t>(it->r0) * kD * 2;
-  const int nr = it->nr;
-#pragma unroll 4
-  for (int x = tid; x < kRows * 64; x += kOutThreads) {
-    const int r = x >> 6, c = x & 63;
-    uint8_t* dst = qtile + (c >> 3) * kChunk + sw128_offset(r, c & 7);
-    if (r < nr) cp_async16(dst, q + static_cast<size_t>(x) * 16);
-    else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
-  }
-  static_assert(kRows * 8 == 2 * kOutThreads, "a thread rotates 8 dims of two rows");
+// The next row block's queries wait in the output warps' registers for the last product on this one's (loaded
+// from memory then, they took 4,000 cycles, in which nothing was multiplied): a thread has 8 dims of
+// every 64 of two rows.  Of the last 64 dims `v` has the first bf16 of each rotated value, `low` the second.
+struct NextQueries {
+  uint4 v[2][8], low[2];
+};
+__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item* it, bool any, NextQueries& n) {
+  const int tid = threadIdx.x - kSoftWarps * 32, nr = any ? it->nr : 0;
+  const uint8_t* q = a.q + (static_cast<size_t>(it->r0) + (tid >> 3)) * (2 * kD) + (tid & 7) * 16;
+  static_assert(kRows * 8 == 2 * kOutThreads, "a thread has 8 dims of two rows");
   float4 cs[2][2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = (tid >> 3) + 32 * u;
-    if (r < nr) {
-      const float4* from = reinterpret_cast<const float4*>(
-          a.q_rope + static_cast<size_t>(static_cast<unsigned>(it->r0 + r) / static_cast<unsigned>(a.H)) * 64 + (tid & 7) * 8);
+    const bool there = r < nr;
+    // (the row's query: rows of a row block are counted from its first query's first head)
+    const int query = it->t0 + ((it->r0 - it->row0 + r) * a.head_inv >> 16);
+    const float4* from = reinterpret_cast<const float4*>(a.q_rope + static_cast<size_t>(query) * 64 + (tid & 7) * 8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      n.v[u][k] = make_uint4(0u, 0u, 0u, 0u);
+      if (there) n.v[u][k] = __ldg(reinterpret_cast<const uint4*>(q + u * 32 * (2 * kD) + k * 128));
+    }
+    cs[u][0] = cs[u][1] = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (there) {
       cs[u][0] = __ldg(from);
       cs[u][1] = __ldg(from + 1);
     }
   }
-  cp_async_wait_all();
-  role_sync<kOutId, kOutThreads>();
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int r = (tid >> 3) + 32 * u, c = tid & 7;
-    uint4 lo = make_uint4(0u, 0u, 0u, 0u);
-    if (r < nr) {
-      uint4* hi = reinterpret_cast<uint4*>(qtile + 7 * kChunk + sw128_offset(r, c));
-      const float co[4] = {cs[u][0].x, cs[u][0].z, cs[u][1].x, cs[u][1].z}, si[4] = {cs[u][0].y, cs[u][0].w, cs[u][1].y, cs[u][1].w};
-      uint4 v = *hi;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-      uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+    const float co[4] = {cs[u][0].x, cs[u][0].z, cs[u][1].x, cs[u][1].z}, si[4] = {cs[u][0].y, cs[u][0].w, cs[u][1].y, cs[u][1].w};
+    uint32_t* w = reinterpret_cast<uint32_t*>(&n.v[u][7]);
+    uint32_t* l = reinterpret_cast<uint32_t*>(&n.low[u]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
-        const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
-        w[k] = pack_bf16(z0, z1);
-        l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
-      }
-      *hi = v;
+    for (int k = 0; k < 4; ++k) {
+      const float y0 = bf16lo(w[k]), y1 = bf16hi(w[k]);
+      const float z0 = y0 * co[k] - y1 * si[k], z1 = y0 * si[k] + y1 * co[k];
+      w[k] = pack_bf16(z0, z1);
+      l[k] = pack_bf16(z0 - bf16lo(w[k]), z1 - bf16hi(w[k]));
     }
-    *reinterpret_cast<uint4*>(qtile + 8 * kChunk + sw128_offset(r, c)) = lo;
+  }
+}
+// Into the K-major chunks of Q (rows behind the last one are zero).
+__device__ __forceinline__ void store_queries(const NextQueries& n, uint8_t* qtile) {
+  const int tid = threadIdx.x - kSoftWarps * 32;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint8_t* to = qtile + sw128_offset((tid >> 3) + 32 * u, tid & 7);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(to + k * kChunk) = n.v[u][k];
+    *reinterpret_cast<uint4*>(to + 8 * kChunk) = n.low[u];
   }
   fence_proxy_async_smem();
 }
+
+// The place of row block e's block j of outputs in tensor memory, of three by turns: the next row block's
+// products begin in the third one while this one's are read.
+__device__ __forceinline__ uint32_t place_of(int e, int j) { return static_cast<uint32_t>((2 * e + j) % kPlaces) * (2 * kRows); }
 
 // A softmax thread's state of its row.
 struct RowState {
@@ -676,60 +826,57 @@ struct RowState {
   }
 };
 
-// Logits of the keys k0 .. k0 + 31 that the row does not see become -inf, those of unfit rows NaN.
-__device__ __forceinline__ void mask_keys(const ChunkArgs& a, const Item* it, int k0, const RowSees& s, float (&z)[32]) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const int k = k0 + j;
-    if (!(k < s.seen || (k >= s.lo && k <= s.hi))) z[j] = -INFINITY;
-  }
+// bits [0, n)
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+// the lowest bits of four bytes
+__device__ __forceinline__ uint32_t bit_of_bytes(uint32_t x) { return ((x & 0x01010101u) * 0x01020408u) >> 24; }
+// Logits of the keys k0 .. k0 + n - 1 that the row does not see, and those behind, become -inf; says whether
+// it sees an unfit row (whose values are 0): its sum is NaN then, and with it its output.
+__device__ __forceinline__ bool mask_keys(const ChunkArgs& a, const Item* it, int k0, int n, const RowSees& s, float (&z)[32]) {
+  uint32_t seen = (low_bits(s.seen - k0) | (low_bits(s.hi + 1 - k0) & ~low_bits(s.lo - k0))) & low_bits(n), unfit = 0;
   if (it->bad) {
+    uint32_t none = 0;
 #pragma unroll 1
-    for (int j0 = 0; j0 < 32; j0 += 8) {   // eight rows' flags lie together (k0 and the list's parts are whole 8s)
-      const int k = k0 + j0;
+    for (int j = 0; j < 32; j += 8) {   // eight rows' flags lie together (k0 and the list's parts are whole 8s)
+      const int k = k0 + j;
       if (k >= it->keys) break;
       const uint8_t* at = a.flags + it->base + (k < it->seen16 ? k : it->raw0 + k - it->seen16);
       const uint2 f = *reinterpret_cast<const uint2*>(at);
-      if ((f.x | f.y) == 0u) continue;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if ((j & ~7) != j0) continue;
-        const uint32_t x = byte_of((j & 4) ? f.y : f.x, j & 3);
-        if (x == kNone) z[j] = -INFINITY;
-        if (x == kUnfit && z[j] != -INFINITY) z[j] = __int_as_float(0x7FC00000);
-      }
+      static_assert(kNone == 1 && kUnfit == 2, "a bit of each");
+      none |= (bit_of_bytes(f.x) | bit_of_bytes(f.y) << 4) << j;
+      unfit |= (bit_of_bytes(f.x >> 1) | bit_of_bytes(f.y >> 1) << 4) << j;
     }
+    seen &= ~none;
+    unfit &= seen;
   }
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (!(seen & (1u << j))) z[j] = -INFINITY;
+  return unfit != 0u;
 }
 
 // The softmax of the pair's tile g, the row block's tile t: this thread's row and 32 keys.
 __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, const Item* it, uint8_t* ptile, uint32_t tmem,
-                                           int rank, int g, int t, bool first, const RowSees& sees, RowState& s, bool& ok) {
+                                           int rank, uint32_t place, int left, int masked, int g, int t, bool first, const RowSees& sees, RowState& s, bool& ok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, side = warp >> 2;        // lanes of tensor memory; columns 32 side .. + 31
   const int r = 32 * (quarter & 1) + lane;
   const uint32_t tlane = static_cast<uint32_t>(quarter * 32) << 16;
   const int buf = g & 1;
-  const int n2 = half_keys(min(kTile, it->keys - t * kTile));
+  const int n2 = half_keys(min(kTile, left));
   const int c0 = 32 * side;                              // the thread's first key within its half
   const int k0 = (quarter >> 1) * n2 + c0;               // within the tile
   ok = ok && wait_warp(sm, &sm->s_full[buf], (g >> 1) & 1, a.spin);
-  const bool has = ok && c0 < n2;
+  const bool has = ok && c0 < n2;   // (a warp's columns may all lie behind the last key)
   tc_fence_after();
   float z[32];
   if (has) {
     tmem_ld32(tmem + kTmemS + 64 * buf + c0 + tlane, z);
     tmem_wait_ld();
-    if (n2 - c0 < 32) {   // a short tile: columns behind its last key
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (c0 + j >= n2) z[j] = -INFINITY;
-    }
-    if (t * kTile + k0 + 32 > it->plain || it->bad) mask_keys(a, it, t * kTile + k0, sees, z);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) z[j] = -INFINITY;
   }
+  bool spoilt = false;
+  if (n2 - c0 < 32 || t * kTile + k0 + 32 > masked || !has)
+    spoilt = mask_keys(a, it, t * kTile + k0, has ? n2 - c0 : 0, sees, z);
   float top = z[0];
 #pragma unroll
   for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j]);
@@ -766,6 +913,7 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
     s.l += x + y;
     s.hat += bf16lo(w[j]) + bf16hi(w[j]);
   }
+  if (spoilt) s.l = __int_as_float(0x7FC00000);
   // the O product before has read P, and its output may be rescaled
   if (g > 0) {
     ok = wait_warp(sm, &sm->v_free[1], (g - 1) & 1, a.spin);
@@ -788,7 +936,7 @@ __device__ __forceinline__ void weigh_tile(const ChunkArgs& a, ChunkSmem* sm, co
 #pragma unroll 1
       for (int x = 0; x < it->nq; x += 16) {   // 32 dims of block `side`, 16 rows at a time
         float o[16];
-        const uint32_t at = tmem + tlane + side * (2 * kRows) + u * it->nq + x;
+        const uint32_t at = tmem + tlane + place + u * it->nq + x;
         tmem_ld16(at, o);
         tmem_wait_ld();
 #pragma unroll
@@ -816,7 +964,7 @@ __device__ __forceinline__ void write_block(const ChunkArgs& a, const Item* it, 
                                             int j, Read&& read) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, u = (warp - kSoftWarps) >> 2, odd = lane & 1;
-  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + j * (2 * kRows) + u * it->nq;
+  const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + place_of(e, j) + u * it->nq;
   const int at = u == 0 ? 0 : it->half, rows = u == 0 ? it->half : it->rows - it->half;   // of the row block
   const unsigned row0 = it->row0 + at, H = a.H;
   const int d = (2 * j + rank) * 128 + quarter * 32 + lane;
@@ -936,13 +1084,90 @@ __device__ __forceinline__ void issue_s_chunk(uint32_t d, uint64_t dq, uint64_t 
   }
 }
 
-// `rows` rows of the list from `k` on, `bytes` each of 16 (a block of dims at `image`, 256 bytes a row)
-// into shared memory: entries, raw rows, or both.
-__device__ __forceinline__ void send_for(const Item* it, uint8_t* to, const uint8_t* image, int k, int rows, uint64_t* full) {
-  const int ne = max(0, min(rows, it->seen16 - k)), nr = rows - ne;
-  if (ne > 0) bulk_g2s(to, image + static_cast<long long>(k) * 256, ne * 256, full);
-  if (nr > 0)
-    bulk_g2s(to + ne * 256, image + static_cast<long long>(it->raw0 + k + ne - it->seen16) * 256, nr * 256, full);
+// What the loading thread needs of a row block, in its registers: its reads of shared memory wait behind the
+// products', and whatever it does between a place that is free and its copy is time without products.
+struct Source {
+  const uint8_t* image;     // the request's first block of dims
+  long long stride;         // to the next one
+  int seen16, raw0;         // (BlockKeys)
+  int keys, begin, nt;
+  __device__ __forceinline__ void load(const ChunkArgs& a, const Item* it) {
+    image = a.images + it->base * (2 * kD);
+    stride = it->stride;
+    seen16 = it->seen16;
+    raw0 = it->raw0;
+    keys = it->keys;
+    begin = it->begin;
+    nt = it->nt;
+  }
+};
+// `rows` rows of a list from `k` on, entries, raw rows, or both: where they lie in a block of dims (256 bytes a row).
+struct Stretch {
+  const uint8_t *entries, *raw;
+  int entry_bytes, raw_bytes;
+  __device__ __forceinline__ Stretch(const Source& s, int k, int rows, long long at) {
+    const int ne = max(0, min(rows, s.seen16 - k));
+    entry_bytes = ne * 256;
+    raw_bytes = (rows - ne) * 256;
+    entries = s.image + at + static_cast<long long>(k) * 256;
+    raw = s.image + at + static_cast<long long>(s.raw0 + k + ne - s.seen16) * 256;
+  }
+  __device__ __forceinline__ void send(uint8_t* to, uint64_t* full) const {
+    mbar_expect_tx(full, entry_bytes + raw_bytes);
+    if (entry_bytes > 0) bulk_g2s(to, entries, entry_bytes, full);
+    if (raw_bytes > 0) bulk_g2s(to + entry_bytes, raw, raw_bytes, full);
+  }
+  __device__ __forceinline__ void move(long long bytes) {
+    entries += bytes;
+    raw += bytes;
+  }
+};
+
+// The order in which a share's tiles are sent for (and told of): a tile's keys before the dims of the tile before it,
+// as the products need them, also from row block to row block; the very first tile's dims at once, as their
+// place is free.
+template <class Source, class Keys, class Dims>
+__device__ __forceinline__ void walk_tiles(const ChunkArgs& a, ChunkSmem* sm, int items, bool& ok, Source s, Keys&& keys, Dims&& dims) {
+  int e = 0, t = -1;                       // the row block, its tile
+  bool fresh = true, first = true, early = false;
+#pragma unroll 1
+  while (e < items) {
+    if (fresh) {
+      ok = wait_bar(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
+      if (!ok) break;
+      s.load(a, &sm->item[e & 1]);
+      t = -1;
+    }
+    fresh = s.nt == 0;
+    bool next = false;
+    if (!fresh) {
+      Source of = s;
+      int kt = t + 1;
+      bool send = kt < s.nt;
+      if (!send && e + 1 < items) {
+        ok = wait_bar(sm, &sm->item_full[(e + 1) & 1], ((e + 1) >> 1) & 1, a.spin);
+        if (!ok) break;
+        of.load(a, &sm->item[(e + 1) & 1]);
+        kt = 0;
+        send = next = of.nt > 0;
+      }
+      if (send) keys(of, kt);
+      if (!ok) break;
+      if (first || (t >= 0 && !early)) dims(s, max(t, 0));
+      if (!ok) break;
+      early = first;
+      first = false;
+      if (t + 1 < s.nt) {
+        ++t;
+        continue;
+      }
+      s = of;
+      t = 0;
+      fresh = !next;
+    }
+    mbar_arrive(&sm->item_free[e & 1]);
+    ++e;
+  }
 }
 
 constexpr size_t kChunkSmemBytes = 1024 + 9 * size_t(kChunk) + 4 * size_t(kKeyPart) + 2 * size_t(kDimPart) + 2 * size_t(kChunk) + sizeof(ChunkSmem);
@@ -972,12 +1197,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       mbar_init(&sm->l_full[i], kSoftWarps);
       mbar_init(&sm->f_full[i], 1);
       mbar_init(&sm->item_full[i], 1);
+      mbar_init(&sm->sees_full[i], 1);
       mbar_init(&sm->item_free[i], 2 + kSoftWarps + kOutWarps);
     }
     mbar_init(&sm->p_full, 2 * kSoftWarps);
     mbar_init(&sm->q_full, 2 * kOutWarps);
     mbar_init(&sm->q_free, 1);
-    for (int j = 0; j < 2; ++j) mbar_init(&sm->o_free[j], 2 * kOutWarps);
+    for (int j = 0; j < kPlaces; ++j) mbar_init(&sm->o_free[j], 2 * kOutWarps);
     mbar_init(&sm->drained, 1);
     sm->abort = 0;
     fence_mbar_init();
@@ -986,74 +1212,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  grid_dep_wait();
-  grid_dep_launch();
-  const ChunkHead head = *a.head;
-  const SharePlan share = pair < head.blocks ? a.share[pair] : SharePlan{0, -1};
-  const int items = share.last - share.first + 1;
   tc_fence_before();
   __syncthreads();
   cluster_sync();                          // the other block's barriers are there
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm->tmem, 0);
+  grid_dep_wait();
+  grid_dep_launch();
+  const ChunkHead head = *a.head;
+  const SharePlan share = a.share[pair];         // (there is room for every pair's; on its way beside the head)
+  const int items = pair < head.blocks ? share.last - share.first + 1 : 0;
 
   if (warp == kPlanWarp) {                 // ---- row blocks
+    ItemPlan plan = share.plan;
     for (int e = 0; e < items; ++e) {
       if (e >= 2 && !wait_warp(sm, &sm->item_free[e & 1], ((e >> 1) - 1) & 1, a.spin)) break;
-      make_item(a, &sm->item[e & 1], share.first + e, head.units, head.blocks, pair, rank);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->item_full[e & 1]);
+      if (e > 0) plan = a.item[share.first + e];
+      make_item(a, sm, e & 1, share.first + e, plan, share.lo, share.hi, pair, rank);
     }
   } else if (warp == kLoadWarp) {          // ---- keys
     if (elect_lane()) {
       bool ok = true;
       int gk = 0, gv = 0, parts = 0;         // tiles sent for: keys, dims; and parts of one more (4 + of dims)
       fence_proxy_async_global();            // (the decoded rows, by another kernel's plain stores)
-      auto send_keys = [&](const Item* it, int t) {
-        const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0), n2 = half_keys(n);
-        const int mine = rank == 0 ? min(n, n2) : n - min(n, n2);
-        const uint8_t* image = a.images + it->base * (2 * kD);
+      walk_tiles(
+          a, sm, items, ok, Source{},
+          [&](const Source& s, int t) {
+            const int k0 = (s.begin + t) * kTile, n = min(kTile, s.keys - k0), n2 = half_keys(n);
+            Stretch x(s, k0 + rank * n2, rank == 0 ? min(n, n2) : n - min(n, n2), 0);
 #pragma unroll 1
-        for (int m = 0; m < 4 && ok; ++m) {
-          if (gk > 0) ok = wait_bar(sm, &sm->k_free[m], (gk - 1) & 1, a.spin);
-          if (!ok) break;
-          mbar_expect_tx(&sm->k_full[m], mine * 256);
-          send_for(it, ktile + m * kKeyPart, image + m * it->stride, k0 + rank * n2, mine, &sm->k_full[m]);
-          parts = m + 1;
-        }
-        if (ok) { ++gk; parts = 0; }
-      };
-      auto send_dims = [&](const Item* it, int t) {
-        const int k0 = (it->begin + t) * kTile, n = min(kTile, it->keys - k0);
-        const uint8_t* image = a.images + it->base * (2 * kD);
+            for (int m = 0; m < 4; ++m) {
+              if (gk > 0) ok = wait_bar(sm, &sm->k_free[m], (gk - 1) & 1, a.spin);
+              if (!ok) return;
+              x.send(ktile + m * kKeyPart, &sm->k_full[m]);
+              x.move(s.stride);
+              parts = m + 1;
+            }
+            ++gk;
+            parts = 0;
+          },
+          [&](const Source& s, int t) {
+            const int k0 = (s.begin + t) * kTile;
+            Stretch x(s, k0, min(kTile, s.keys - k0), rank * s.stride);
 #pragma unroll 1
-        for (int j = 0; j < 2 && ok; ++j) {
-          if (gv > 0) ok = wait_bar(sm, &sm->v_free[j], (gv - 1) & 1, a.spin);
-          if (!ok) break;
-          mbar_expect_tx(&sm->v_full[j], n * 256);
-          send_for(it, vtile + j * kDimPart, image + (2 * j + rank) * it->stride, k0, n, &sm->v_full[j]);
-          parts = 4 + j + 1;
-        }
-        if (ok) { ++gv; parts = 0; }
-      };
-      bool sent = false;                     // the keys of this row block's first tile have been sent for
-      for (int e = 0; e < items && ok; ++e) {
-        if (e == 0) ok = wait_bar(sm, &sm->item_full[0], 0, a.spin);
-        if (!ok) break;
-        const Item* it = &sm->item[e & 1];
-        const int nt = it->nt;
-        if (nt > 0 && !sent) send_keys(it, 0);
-        for (int t = 0; t + 1 < nt && ok; ++t) {
-          send_keys(it, t + 1);
-          send_dims(it, t);
-        }
-        // the next row block's first keys before this one's last dims
-        if (ok && e + 1 < items) ok = wait_bar(sm, &sm->item_full[(e + 1) & 1], ((e + 1) >> 1) & 1, a.spin);
-        sent = ok && nt > 0 && e + 1 < items && sm->item[(e + 1) & 1].nt > 0;
-        if (sent) send_keys(&sm->item[(e + 1) & 1], 0);
-        if (nt > 0 && ok) send_dims(it, nt - 1);
-        mbar_arrive(&sm->item_free[e & 1]);
-      }
+            for (int j = 0; j < 2; ++j) {
+              if (gv > 0) ok = wait_bar(sm, &sm->v_free[j], (gv - 1) & 1, a.spin);
+              if (!ok) return;
+              x.send(vtile + j * kDimPart, &sm->v_full[j]);
+              x.move(2 * s.stride);
+              parts = 4 + j + 1;
+            }
+            ++gv;
+            parts = 0;
+          });
       // copies in flight (there are none, unless a wait gave up): the last ones to each place
       {
         for (int m = 0; m < 4; ++m) {
@@ -1070,32 +1281,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
   } else if (warp == kMmaWarp && rank == 1) {   // ---- tells the even block of this one's copies
     if (elect_lane()) {
       bool ok = true;
-      int g = 0;
-      auto keys = [&](int i) {
-#pragma unroll 1
-        for (int m = 0; m < 4 && ok; ++m) {
-          ok = wait_bar(sm, &sm->k_full[m], i & 1, a.spin);
-          if (ok) arrive_at(of_block(&sm->k_full[m], 0));
-        }
+      int gk = 0, gv = 0;
+      struct Count {
+        int nt;
+        __device__ __forceinline__ void load(const ChunkArgs&, const Item* it) { nt = it->nt; }
       };
-      auto dims = [&](int i) {
+      walk_tiles(
+          a, sm, items, ok, Count{},
+          [&](const Count&, int) {
 #pragma unroll 1
-        for (int j = 0; j < 2 && ok; ++j) {
-          ok = wait_bar(sm, &sm->v_full[j], i & 1, a.spin);
-          if (ok) arrive_at(of_block(&sm->v_full[j], 0));
-        }
-      };
-      for (int e = 0; e < items && ok; ++e) {
-        ok = wait_bar(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
-        if (!ok) break;
-        const int nt = sm->item[e & 1].nt;
-        mbar_arrive(&sm->item_free[e & 1]);
-        if (nt > 0) keys(g);
-        for (int t = 0; t < nt && ok; ++t, ++g) {
-          if (t + 1 < nt) keys(g + 1);
-          dims(g);
-        }
-      }
+            for (int m = 0; m < 4 && ok; ++m) {
+              ok = wait_bar(sm, &sm->k_full[m], gk & 1, a.spin);
+              if (ok) arrive_at(of_block(&sm->k_full[m], 0));
+            }
+            ++gk;
+          },
+          [&](const Count&, int) {
+#pragma unroll 1
+            for (int j = 0; j < 2 && ok; ++j) {
+              ok = wait_bar(sm, &sm->v_full[j], gv & 1, a.spin);
+              if (ok) arrive_at(of_block(&sm->v_full[j], 0));
+            }
+            ++gv;
+          });
       mbar_wait(&sm->drained, 0, 2 * kDefaultSpinLimit);   // the even block's last commit has come (before this block ends)
     }
     __syncwarp();
@@ -1105,7 +1313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       const uint64_t dk = smem_desc_sw128(smem_u32(ktile), 16, 2048);
       const uint64_t dv = smem_desc_sw128(smem_u32(vtile), 1024, 2048);
       const uint64_t dp = smem_desc_sw128(smem_u32(ptile), 16, 1024);
-      bool ok = true;
+      bool ok = true, ahead = false;         // ahead: S of this row block's first tile has been issued
       int g = 0;
       for (int e = 0; e < items && ok; ++e) {
         ok = wait_bar(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
@@ -1113,30 +1321,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
         const Item* it = &sm->item[e & 1];
         const int nt = it->nt, keys = it->keys - it->begin * kTile;
         const uint32_t ido = make_idesc(1, 1, 1, 0, 256, 0) | (static_cast<uint32_t>(it->nq >> 2) << 17);   // 2 nq columns
-        ok = wait_bar(sm, &sm->q_full, e & 1, a.spin);
-        tc_fence_after();
-        auto issue_s = [&](int t) {
-          const int i = g + t;
-          const uint32_t ids = make_idesc(1, 1, 0, 0, 128, 0) |
-                               (static_cast<uint32_t>(half_keys(min(kTile, keys - t * kTile)) >> 2) << 17);
-          const uint32_t d = tmem + kTmemS + 64 * (i & 1);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if ((c & 1) == 0) {
-              ok = ok && wait_bar(sm, &sm->k_full[c >> 1], i & 1, a.spin);
-              tc_fence_after();
-            }
-            if (ok) issue_s_chunk(d, dq, dk, c, ids);
-            if ((c & 1) == 1) mma2_commit(&sm->k_free[c >> 1]);
-          }
-          mma2_commit(&sm->s_full[i & 1]);
-          if (t == nt - 1) mma2_commit(&sm->q_free);
-        };
-        // before this row block's first O products the outputs of the one before are read (a row block
+        if (!ahead) {
+          ok = wait_bar(sm, &sm->q_full, e & 1, a.spin);
+          tc_fence_after();
+        }
+        // before this row block's first O products the outputs in their places before are read (a row block
         // without tiles waits too: its own outputs would be told from those by nothing)
         auto outputs_read = [&](int j) {
-          if (e > 0) {
-            ok = ok && wait_bar(sm, &sm->o_free[j], (e - 1) & 1, a.spin);
+          const int n = 2 * e + j;
+          if (n >= kPlaces) {
+            ok = ok && wait_bar(sm, &sm->o_free[n % kPlaces], (n / kPlaces - 1) & 1, a.spin);
             tc_fence_after();
           }
         };
@@ -1145,9 +1339,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
           outputs_read(1);
           mma2_commit(&sm->q_free);
         }
-        for (int t = -1; t < nt && ok; ++t) {   // (issue_s once: its code is long)
+        int t = ahead ? 0 : -1;
+        ahead = false;
+        for (; t < nt && ok; ++t) {
           const int i = g + t;
-          if (t + 1 < nt) issue_s(t + 1);
+          // S of the next tile before O of this one, so that the softmax runs beside products; behind the last
+          // tile that is the next row block's first one, if its queries are there before this one's weights
+          const int k = i + 1;
+          bool more = t + 1 < nt;
+          int left = keys - (t + 1) * kTile, tiles = nt - (t + 1);   // of the row block from that tile on
+          if (!more && nt > 0 && e + 1 < items) {
+            const int f = e + 1;
+            const unsigned long long t0 = clock64();
+            while (!more && !mbar_test(&sm->p_full, i & 1) && clock64() - t0 < a.spin &&
+                   !*reinterpret_cast<volatile int*>(&sm->abort)) {
+              if (mbar_test(&sm->item_full[f & 1], (f >> 1) & 1)) {
+                const Item* of = &sm->item[f & 1];
+                left = of->keys - of->begin * kTile;
+                tiles = of->nt;
+                if (tiles == 0) break;
+                more = mbar_test(&sm->q_full, f & 1);
+              }
+            }
+            tc_fence_after();
+            ahead = more;
+          }
+          if (more) {   // (here alone: its code is long)
+            const uint32_t ids =
+                make_idesc(1, 1, 0, 0, 128, 0) | (static_cast<uint32_t>(half_keys(min(kTile, left)) >> 2) << 17);
+            const uint32_t d = tmem + kTmemS + 64 * (k & 1);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              if ((c & 1) == 0) {
+                ok = ok && wait_bar(sm, &sm->k_full[c >> 1], k & 1, a.spin);
+                tc_fence_after();
+              }
+              if (ok) issue_s_chunk(d, dq, dk, c, ids);
+              if ((c & 1) == 1) mma2_commit(&sm->k_free[c >> 1]);
+            }
+            mma2_commit(&sm->s_full[k & 1]);
+            if (tiles == 1) mma2_commit(&sm->q_free);
+          }
           if (t < 0) continue;
           const int ks = min(kTile, keys - t * kTile) >> 4;
           ok = ok && wait_bar(sm, &sm->p_full, i & 1, a.spin);
@@ -1159,7 +1391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
             tc_fence_after();
             if (!ok) break;
             const uint64_t v = dv + j * (kDimPart >> 4);
-            const uint32_t d = tmem + j * (2 * kRows);
+            const uint32_t d = tmem + place_of(e, j);
             if (t == 0) mma2_set(d, v, dp, ido);
             else mma2_add(d, v, dp, ido);
             if (ks == 8) {
@@ -1183,7 +1415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     int g = 0;
     bool ok = true;
     for (int e = 0; e < items; ++e) {
-      const bool there = ok && wait_warp(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
+      const bool there = ok && wait_warp(sm, &sm->sees_full[e & 1], (e >> 1) & 1, a.spin);
       if (role_any<kSoftId, kSoftWarps * 32>(!there)) break;
       const Item* it = &sm->item[e & 1];
       const int r = 32 * (warp & 1) + lane;
@@ -1191,7 +1423,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       RowState s;
       s.reset();
       const int nt = it->nt;
-      for (int t = 0; t < nt; ++t, ++g) weigh_tile(a, sm, it, ptile, tmem, rank, g, it->begin + t, t == 0, sees, s, ok);
+      const int keys = it->keys, begin = it->begin, masked = it->bad ? 0 : it->plain;
+      const uint32_t place = place_of(e, warp >> 2);
+      for (int t = 0; t < nt; ++t, ++g)
+        weigh_tile(a, sm, it, ptile, tmem, rank, place, keys - (begin + t) * kTile, masked, g, begin + t, t == 0, sees, s, ok);
       const int quarter = 2 * (warp >> 2) + ((warp >> 1) & 1);   // of the keys
       if (quarter == 0) sm->ref[e & 1][r] = s.m == -INFINITY ? -INFINITY : s.msub;
       sm->sums[e & 1][quarter][r] = make_float2(s.l, s.hat);
@@ -1208,22 +1443,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
       ok = ok && wait_warp(sm, &sm->item_full[e & 1], (e >> 1) & 1, a.spin);
       return !role_any<kOutId, kOutThreads>(!ok);
     };
-    auto queries = [&](int e) {
-      const Item* it = &sm->item[e & 1];
-      load_queries(a, it, qtile);
-      __syncwarp();
-      if (lane == 0) arrive_at(of_block(&sm->q_full, 0));
-    };
-    bool there = items > 0 && item_there(0);
-    if (there) queries(0);
-    for (int e = 0; e < items && there; ++e) {
+    bool there = items > 0;
+    for (int e = -1; e < items && there; ++e) {   // (-1: the first queries)
+      const bool more = e + 1 < items;
+      if (more) there = item_there(e + 1);
+      NextQueries next;
+      load_queries(a, &sm->item[(e + 1) & 1], more && there, next);
+      if (e >= 0) ok = ok && wait_warp(sm, &sm->q_free, e & 1, a.spin);   // the last S product on these queries is complete
+      if (more && there && ok) {
+        store_queries(next, qtile);
+        __syncwarp();
+        if (lane == 0) arrive_at(of_block(&sm->q_full, 0));
+      }
+      if (e < 0) continue;
       const Item* it = &sm->item[e & 1];
       g += it->nt;
-      ok = ok && wait_warp(sm, &sm->q_free, e & 1, a.spin);   // the last S product on these queries is complete
-      if (e + 1 < items) {
-        there = item_there(e + 1);
-        if (there) queries(e + 1);
-      }
       ok = ok && wait_warp(sm, &sm->l_full[e & 1], (e >> 1) & 1, a.spin);
       if (ok) finish_sums(a, it, sm, rank, e);
       role_sync<kOutId, kOutThreads>();
@@ -1236,15 +1470,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
         write_block(a, it, sm, tmem, rank, e, j, [&]() {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_at(of_block(&sm->o_free[j], 0));
+          if (lane == 0) arrive_at(of_block(&sm->o_free[(2 * e + j) % kPlaces], 0));
         });
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->item_free[e & 1]);
     }
-    cp_async_wait_all();
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && sm->abort != 0) set_err(CSKV_ERR_TIMEOUT);
   cluster_sync();                          // nobody writes into or reads from a block that has ended
   if (warp == kMmaWarp) {
     tc_fence_after();
@@ -1253,100 +1487,105 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
 }
 
 // ---------------------------------------------------------------------------
-// the join: the parts of a row in order, the sink, the rotation back.  64 threads of 8 dims for a row;
-// where there are many parts four times as many, each with every fourth part.
+// the join: the parts of a row in order, the sink, the rotation back.  A lane has four dims of every 128.
+// A row of few parts is one warp's, one of more (few queries on a long cache) a block's, whose warps have every
+// eighth part.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-constexpr int kShares = 4;
-constexpr int kFewParts = 8;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
-  __shared__ float shares[kShares - 1][kD];
+__global__ void __launch_bounds__(kJoinThreads, 3) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+  __shared__ float shares[kJoinWarps - 1][kD];
   grid_dep_wait();
+  constexpr int kSets = 2 * kRows / kJoinWarps;   // of a row block, where a warp has a row
   const ChunkHead head = *a.head;
-  const int sub = threadIdx.x >> 6, lane = threadIdx.x & 31, d = (threadIdx.x & 63) * 8;
-  constexpr int kSets = 2 * kRows / 4;   // of four rows of a row block
-  for (int x = blockIdx.x; x < head.splits * kSets; x += gridDim.x) {
-    const SplitPlan sp = a.split[x / kSets];
-    const ReqPlan p = a.req[request_of_item(a, sp.item)];
-    const int i0 = (sp.item - p.item0) * a.group;
-    const int nr = min(p.nq - i0, a.group) * a.H;
-    const bool late = a.unit0[sp.item] > share_begin(head.units, head.blocks, sp.b0);
-    const int parts = sp.b1 - sp.b0 + 1;
-    const bool few = parts <= kFewParts;
-    for (int y = 0; y < (few ? 1 : 4); ++y) {   // (the whole block)
-      const int r = (x % kSets) * 4 + (few ? sub : y), share = few ? 0 : sub;
-      const bool there = r < nr;
-      auto slot = [&](int k) { return (2 * static_cast<size_t>(sp.b0 + k) + (k == 0 && late)) * (2 * kRows) + r; };
-      auto weight = [&](float2 v, float M) { return v.y == 0.f ? 0.f : v.y != v.y ? v.y : exp2f(v.x - M); };
-      const size_t row = static_cast<size_t>(p.q0 + i0) * a.H + r;
-      const float sink = a.sink != nullptr && there ? __ldg(a.sink + row % a.H) : -INFINITY;
-      const float s2 = __fmul_rn(sink, kLog2e);   // (not part of a fused difference: s2 - M is 0 where s2 is the larger)
-      float M = s2, total = 0.f, o[8];
+  SplitPlan sp = a.split[blockIdx.x / kSets];     // (there is room for as many; on its way beside the head)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int few = head.few * kSets, all = few + head.many * (2 * kRows);
+  for (int x = blockIdx.x; x < all; x += gridDim.x) {
+    const bool alone = x < few;   // (the whole block)
+    if (!alone) sp = a.split[a.most_blocks - 1 - (x - few) / (2 * kRows)];
+    else if (x >= gridDim.x) sp = a.split[x / kSets];
+    const int r = alone ? x % kSets * kJoinWarps + warp : (x - few) % (2 * kRows);
+    const int share = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;
+    if (r >= sp.rows) continue;   // (a warp alone, or the whole block)
+    auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? sp.first : sp.next + 2 * (k - 1)) * (2 * kRows) + r; };
+    auto weight = [&](float2 v, float M) { return v.y == 0.f ? 0.f : v.y != v.y ? v.y : exp2f(v.x - M); };
+    const unsigned row = sp.row0 + r;
+    const float sink = a.sink != nullptr ? __ldg(a.sink + row % static_cast<unsigned>(a.H)) : -INFINITY;
+    const float s2 = __fmul_rn(sink, kLog2e);   // (not part of a fused difference: s2 - M is 0 where s2 is the larger)
+    // the outputs of the first two parts, on their way while the weights are made
+    float4 y[2][4];
+    auto load = [&](float4 (&to)[4], int k) {
+      const float4* v = reinterpret_cast<const float4*>(a.opart + slot(k) * kD) + lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = 0.f;
-      if (there) {
-        if (few) {
-          for (int k = 0; k < parts; ++k) {
-            const float2 v = a.ml[slot(k)];
-            if (v.y != 0.f) M = fmaxf(M, v.x);
-          }
-        } else {
-          for (int k = lane; k < parts; k += 32) {
-            const float2 v = a.ml[slot(k)];
-            if (v.y != 0.f) M = fmaxf(M, v.x);
-          }
-          for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, w));
-          for (int k = lane; k < parts; k += 32) {
-            const float2 v = a.ml[slot(k)];
-            total += v.y * weight(v, M);
-          }
-          for (int w = 16; w >= 1; w >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, w);
-        }
-#pragma unroll 4
-        for (int k = share; k < parts; k += few ? 1 : kShares) {
-          const float2 ml = a.ml[slot(k)];
-          const float e = weight(ml, M);   // 0: a part without keys, whose output is 0
-          if (few) total += ml.y * e;
-          const float4* v = reinterpret_cast<const float4*>(a.opart + slot(k) * kD + d);
-          const float4 v0 = v[0], v1 = v[1];
-          o[0] += e * v0.x; o[1] += e * v0.y; o[2] += e * v0.z; o[3] += e * v0.w;
-          o[4] += e * v1.x; o[5] += e * v1.y; o[6] += e * v1.z; o[7] += e * v1.w;
-        }
-      }
-      if (!few) {
-        if (share > 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) shares[share - 1][d + i] = o[i];
-        }
-        __syncthreads();
-        if (share == 0) {
-          for (int k = 0; k < kShares - 1; ++k) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] += shares[k][d + i];
-          }
-        }
-        __syncthreads();   // shares are used again
-      }
-      if (!there || share > 0) continue;
-      const bool none = total == 0.f;   // no key that counts beside the sink
-      if (s2 != -INFINITY) total += exp2f(s2 - M);
-      const float inv = none ? 0.f : 1.0f / total;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] *= inv;
-      if (d >= kD - 64) {
-        const float* cs = a.q_rope + row / a.H * 64 + (d - (kD - 64));
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float c = cs[i], s = cs[i + 1], y0 = o[i], y1 = o[i + 1];
-          o[i] = y0 * c + y1 * s;
-          o[i + 1] = y1 * c - y0 * s;
-        }
-      }
-      *reinterpret_cast<uint4*>(a.out + (row * kD + d) * 2) =
-          make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-      if (a.lse != nullptr && d == 0) a.lse[row] = none ? sink : (M + log2f(total)) * kLn2;
+      for (int i = 0; i < 4; ++i) to[i] = k < sp.parts ? v[32 * i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(y[0], share);
+    load(y[1], share + step);
+    float M = s2, total = 0.f;
+    for (int k = lane; k < sp.parts; k += 32) {
+      const float2 v = a.ml[slot(k)];
+      if (v.y != 0.f) M = fmaxf(M, v.x);
     }
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, w));
+    float4 o[4] = {};
+    for (int k = share; k < sp.parts; k += 2 * step) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (k + u * step >= sp.parts) break;
+        const float2 ml = a.ml[slot(k + u * step)];
+        const float e = weight(ml, M);   // 0: a part without keys, whose output is 0
+        total += ml.y * e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[i].x += e * y[u][i].x;
+          o[i].y += e * y[u][i].y;
+          o[i].z += e * y[u][i].z;
+          o[i].w += e * y[u][i].w;
+        }
+        load(y[u], k + (u + 2) * step);
+      }
+    }
+    if (!alone) {
+      __shared__ float totals[kJoinWarps];
+      if (lane == 0) totals[warp] = total;
+      if (share > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(shares[share - 1])[32 * i + lane] = o[i];
+      }
+      __syncthreads();
+      if (share == 0) {
+        for (int k = 1; k < kJoinWarps; ++k) {
+          total += totals[k];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 y = reinterpret_cast<const float4*>(shares[k - 1])[32 * i + lane];
+            o[i].x += y.x;
+            o[i].y += y.y;
+            o[i].z += y.z;
+            o[i].w += y.w;
+          }
+        }
+      }
+      __syncthreads();   // shares are used again
+      if (share > 0) continue;
+    }
+    const bool none = total == 0.f;   // no key that counts beside the sink
+    if (s2 != -INFINITY) total += exp2f(s2 - M);
+    const float inv = none ? 0.f : 1.0f / total;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float4 y = make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+      if (i == 3 && lane >= 16) {   // dims 448 .. 511, back
+        const float4 w = __ldg(reinterpret_cast<const float4*>(a.q_rope + static_cast<size_t>(row / static_cast<unsigned>(a.H)) * 64) + (lane - 16));
+        y = make_float4(y.x * w.x + y.y * w.y, y.y * w.x - y.x * w.y, y.z * w.z + y.w * w.w, y.w * w.z - y.z * w.w);
+      }
+      *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(row) * kD + 128 * i + 4 * lane) * 2) =
+          make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    }
+    if (a.lse != nullptr && lane == 0) a.lse[row] = none ? sink : (M + log2f(total)) * kLn2;
   }
 }
 
@@ -1355,7 +1594,7 @@ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
 // How the row blocks and the workspace follow from the sizes alone.
 struct Layout {
   int group, most_blocks;
-  size_t head, req, unit0, share, split, flags, images, opart, ml, bytes;
+  size_t head, req, item, share, split, flags, bad, images, opart, ml, bytes;
 };
 Layout layout_of(int R, int T, int H, int64_t max_keys) {
   Layout l = {};
@@ -1369,10 +1608,11 @@ Layout layout_of(int R, int T, int H, int64_t max_keys) {
   auto take = [&](size_t bytes) { const size_t x = at; at += a256(bytes); return x; };
   l.head = take(sizeof(ChunkHead));
   l.req = take(sizeof(ReqPlan) * static_cast<size_t>(R));
-  l.unit0 = take(8 * static_cast<size_t>(items + 1));
+  l.item = take(sizeof(ItemPlan) * static_cast<size_t>(items + 1));
   l.share = take(sizeof(SharePlan) * l.most_blocks);
   l.split = take(sizeof(SplitPlan) * l.most_blocks);
   l.flags = take(keys);
+  l.bad = take(keys / kDecodeRows);
   l.images = take(keys * (2 * kD));
   l.opart = take(2 * static_cast<size_t>(l.most_blocks) * (2 * kRows) * kD * 4);
   l.ml = take(2 * static_cast<size_t>(l.most_blocks) * (2 * kRows) * 8);
@@ -1435,29 +1675,37 @@ cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t*
   a.lse = lse;
   a.max_keys = max_keys;
   a.group = l.group;
+  a.head_inv = (65535 + H) / H;
   a.most_blocks = l.most_blocks;
   a.head = reinterpret_cast<ChunkHead*>(ws + l.head);
   a.req = reinterpret_cast<ReqPlan*>(ws + l.req);
-  a.unit0 = reinterpret_cast<long long*>(ws + l.unit0);
+  a.item = reinterpret_cast<ItemPlan*>(ws + l.item);
   a.share = reinterpret_cast<SharePlan*>(ws + l.share);
   a.split = reinterpret_cast<SplitPlan*>(ws + l.split);
   a.flags = ws + l.flags;
+  a.bad = ws + l.bad;
   a.images = ws + l.images;
   a.opart = reinterpret_cast<float*>(ws + l.opart);
   a.ml = reinterpret_cast<float2*>(ws + l.ml);
   a.spin = spin_limit();
-  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   const int64_t decode_warps = (max_keys + kDecodeRows - 1) / kDecodeRows;
-  const unsigned decode_blocks = static_cast<unsigned>(
-      std::min<int64_t>(16 * kPairs, std::max<int64_t>(1, (decode_warps + kDecodeThreads / 32 - 1) / (kDecodeThreads / 32))));
-  e = launch_next(chunk_decode_kernel, decode_blocks, kDecodeThreads, 0, stream, nullptr, a);
+  const unsigned decode_blocks = static_cast<unsigned>(std::min<int64_t>(
+      2 * kPairs * kPrepBlocks - 1, std::max<int64_t>(1, (decode_warps + kPrepThreads / 32 - 1) / (kPrepThreads / 32))));
+  cudaError_t e;
+  if (R <= kOwnReqs) {
+    chunk_prepare_kernel<<<1 + decode_blocks, kPrepThreads, 0, stream>>>(a);
+    e = cudaGetLastError();
+  } else {
+    chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_next(chunk_decode_kernel, decode_blocks, kPrepThreads, 0, stream, nullptr, a);
+  }
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> allowed;
   e = launch_next(chunk_attn_kernel, 2 * l.most_blocks, kThreads, kChunkSmemBytes, stream, &allowed, a);
   if (e != cudaSuccess || l.most_blocks == 1) return e;
-  return launch_next(chunk_join_kernel, 32 * l.most_blocks, kJoinThreads, 0, stream, nullptr, a);
+  return launch_next(chunk_join_kernel, 16 * l.most_blocks, kJoinThreads, 0, stream, nullptr, a);
 }
 
 unsigned int take_err_chunk_attn() { return take_dev_err(); }

@@ -489,3 +489,24 @@ def test_a_servers_steps_from_lengths_to_attention():
                 _check(wout[i + k], wlse[i + k], bounded.attend(qv[i + k], t, rows[b][max(0, t + 1 - window):t + 1], None, SCALE))
             i += n[b]
         assert maps.new_len.tolist() == [len(r) for r in rows]
+
+
+@pytest.mark.parametrize("R", [255, 257, 1024, 1025, 2100])
+def test_many_requests(R):
+    """More requests than a block has threads, and than it sums up itself; some without new tokens, one
+    with a row that is not finite."""
+    rs = np.random.default_rng(R)
+    length = rs.integers(1, 40, R)
+    new = np.minimum(rs.choice([0, 1, 1, 2, 5], R), length)
+    new[R - 2] = 1
+    c = Case(new, length, 4, 1, FP8, window=8, seed=R)
+    pick = sorted(set(_some(len(c.req), 30, R)) | {int(c.cu[R - 2])})
+    out, lse = c.run()
+    c.check(out, lse, pick)
+    _poison(c.entries, R - 2, [0])
+    bad, bad_lse = c.run()
+    hit = np.flatnonzero(c.req == R - 2)
+    assert np.isnan(bad[hit].float().cpu().numpy()).all() and np.isnan(bad_lse[hit].cpu().numpy()).all()
+    rest = np.flatnonzero(c.req != R - 2)
+    assert torch.equal(bad[rest], out[rest]) and torch.equal(bad_lse[rest], lse[rest])
+    assert cskv.device_status() == 0
