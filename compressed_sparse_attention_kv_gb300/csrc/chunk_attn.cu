@@ -1494,7 +1494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
-__global__ void __launch_bounds__(kJoinThreads, 3) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ float shares[kJoinWarps - 1][kD];
   grid_dep_wait();
   constexpr int kSets = 2 * kRows / kJoinWarps;   // of a row block, where a warp has a row
@@ -1514,15 +1514,6 @@ __global__ void __launch_bounds__(kJoinThreads, 3) chunk_join_kernel(const __gri
     const unsigned row = sp.row0 + r;
     const float sink = a.sink != nullptr ? __ldg(a.sink + row % static_cast<unsigned>(a.H)) : -INFINITY;
     const float s2 = __fmul_rn(sink, kLog2e);   // (not part of a fused difference: s2 - M is 0 where s2 is the larger)
-    // the outputs of the first two parts, on their way while the weights are made
-    float4 y[2][4];
-    auto load = [&](float4 (&to)[4], int k) {
-      const float4* v = reinterpret_cast<const float4*>(a.opart + slot(k) * kD) + lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) to[i] = k < sp.parts ? v[32 * i] : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    load(y[0], share);
-    load(y[1], share + step);
     float M = s2, total = 0.f;
     for (int k = lane; k < sp.parts; k += 32) {
       const float2 v = a.ml[slot(k)];
@@ -1531,21 +1522,19 @@ __global__ void __launch_bounds__(kJoinThreads, 3) chunk_join_kernel(const __gri
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, w));
     float4 o[4] = {};
-    for (int k = share; k < sp.parts; k += 2 * step) {
+#pragma unroll 2
+    for (int k = share; k < sp.parts; k += step) {
+      const float2 ml = a.ml[slot(k)];
+      const float e = weight(ml, M);   // 0: a part without keys, whose output is 0
+      total += ml.y * e;
+      const float4* v = reinterpret_cast<const float4*>(a.opart + slot(k) * kD) + lane;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (k + u * step >= sp.parts) break;
-        const float2 ml = a.ml[slot(k + u * step)];
-        const float e = weight(ml, M);   // 0: a part without keys, whose output is 0
-        total += ml.y * e;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[i].x += e * y[u][i].x;
-          o[i].y += e * y[u][i].y;
-          o[i].z += e * y[u][i].z;
-          o[i].w += e * y[u][i].w;
-        }
-        load(y[u], k + (u + 2) * step);
+      for (int i = 0; i < 4; ++i) {
+        const float4 y = v[32 * i];
+        o[i].x += e * y.x;
+        o[i].y += e * y.y;
+        o[i].z += e * y.z;
+        o[i].w += e * y.w;
       }
     }
     if (!alone) {

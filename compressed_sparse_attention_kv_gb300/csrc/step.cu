@@ -18,13 +18,16 @@ namespace {
 // a page's place follows from its number alone: the k-th new page of the step is the k-th of the
 // ring, and the j-th page given back goes j places behind the ring's last one.  The two stretches
 // do not meet, so that blocks read and write the ring without waiting for one another.
-// Bound: latency (24 bytes a token).  One block does a small step in one launch; beyond
-// that one block makes the sums and a launch of many blocks the maps.
+// Bound: latency (24 bytes a token; 262,144 tokens of 512 requests take 14.8 us, their 4.5 MB 0.7).
+// One block does a small step in one launch; beyond that one block makes the sums and a launch of
+// many blocks, started meanwhile, the maps (in one launch and in two: 1 request of 1 token 5.4 and
+// 6.6 us, 64 of one 8.0 and 8.1, 64 and 1,024 tokens 9.1 and 8.7, 256 of one 16.4 and 9.5).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kMapThreads = 256;
 constexpr int kStaged = 2048;            // requests of a block's tokens that fit into shared memory
 constexpr int kMaxLen = 1 << 30;
+constexpr int kSmallStep = 256, kSmallBatch = 64;   // tokens and requests of one launch at most
 
 struct PlanRecord {        // of a request
   int tok0;                // its first token
@@ -262,7 +265,7 @@ template <bool kWhole>   // kWhole: the maps too
 __global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const __grid_constant__ PlanArgs a) {
   grid_dep_launch();
   if constexpr (kWhole) {
-    __shared__ int first_tokens[kPlanThreads];
+    __shared__ int first_tokens[kSmallBatch];
     plan_sums(a, first_tokens);
     __syncthreads();   // (the records are this block's own writes)
     const PlanHead h = *a.head;
@@ -290,7 +293,8 @@ __global__ void __launch_bounds__(kMapThreads) plan_maps_kernel(const __grid_con
 //   sin = t + (t^3 (-1/6 + t^2/120 - ...) + d),  cos = (1 - t^2/2) + (t^4 (1/24 - ...) - t d + what
 // the rounding of 1 - t^2/2 lost): Taylor polynomials to t^11 and t^12 (remainders 7e-12 and
 // 1e-12), the error below one ulp of the result.
-// Bound: writes, 256 bytes a position, beside about 50 instructions a pair.
+// Bound: instructions, about 50 for two pairs, beside 256 bytes of writes a position: 131,071 positions
+// 11.7 us (their 35 MB 5.2), with fp32 operations on two numbers at once.
 // ---------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
 constexpr int kRopeBlocks = 7;                   // of an SM: all are resident (36 registers a thread), none waits for a place
@@ -415,12 +419,21 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_cs_kernel(cons
 }
 
 // ---------------------------------------------------------------------------
-// cskvs_norm_rope
+// cskvs_norm_rope: y = x r w, r = (mean of x^2 + eps)^-1/2, the last 64 dims turned by the
+// token's angles; bf16 out, or coded into a page.  The order of the sums is that of the calls that
+// norm rows one by one, and products and sums are rounded one at a time, so that the bits
+// agree.
+// Bound: memory, one read and one write of everything: a warp keeps its heads in registers between
+// the sum and the product.  8,192 tokens of 64 heads of 512, 64 of 128 and their rows: 1.36 GB in
+// 219 us, 6.2 TB/s, 91 % of a copy; in three resident blocks an SM (two: 229 us).
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kMaxNormJobs = 4;
-constexpr long long kManyHeads = 4 * 152 * 32;   // of 512 dims
+// Heads of 512 dims from which on a warp takes four of them, so that their loads are on their way together: 8 warps
+// an SM.  With fewer, warps hide more (one and four a warp, tokens of 80 heads: 1 token 3.2 and 4.0 us, 32
+// 3.95 and 4.1, 64 5.2 and 5.0, 512 18.6 and 14.8, 4,096 158 and 112).
+constexpr long long kManyHeads = 152 * 32;
 
 struct NormJob {
   const uint8_t* x;
@@ -660,7 +673,7 @@ cudaError_t launch_plan_step(const int32_t* ctx_len, const int32_t* n_new, int B
   a.ring_slot = reinterpret_cast<long long*>(ring_slot);
   a.head = static_cast<PlanHead*>(workspace);
   a.rec = reinterpret_cast<PlanRecord*>(static_cast<uint8_t*>(workspace) + 256);
-  const bool whole = T <= 2048 && B <= kPlanThreads;
+  const bool whole = T <= kSmallStep && B <= kSmallBatch;
   if (whole) {
     plan_sums_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
     return cudaGetLastError();
@@ -702,8 +715,6 @@ cudaError_t launch_norm_rope(const cskvs_norm_job* jobs, int njobs, const float*
   a.njobs = njobs;
   a.T = T;
   a.rope_cs = rope_cs;
-  // four heads a warp where that leaves every SM its warps, else one: the loads on their way hide the
-  // memory's latency in long calls, the warps in short ones
   long long heads = 0;
   for (int i = 0; i < njobs; ++i)
     if (jobs[i].slot == nullptr) heads += static_cast<long long>(T) * jobs[i].H * jobs[i].dim / 512;

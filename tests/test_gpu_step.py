@@ -474,3 +474,33 @@ def test_norm_calls_that_are_refused():
     with pytest.raises(cskv.CskvError):
         cskv.norm_rope([dict(x=odd)])
     assert cskv.norm_rope([dict(x=x[:0])], cs[:0])[0].shape == (0, 2, 512)
+
+
+@pytest.mark.parametrize("B,T", [(64, 256), (65, 256), (64, 257), (1, 256), (63, 1)])
+def test_plans_where_one_launch_ends(B, T):
+    rs = np.random.default_rng(B + T)
+    ctx, new = rs.integers(0, 700, B), np.zeros(B, np.int64)
+    for b in rs.integers(0, B, T - T // 9):
+        new[b] += 1
+    new[new == 0] = rs.choice([0, -1], int((new == 0).sum()))
+    pages = _pages_case(rs, ctx, 1, step.pages_of(int(ctx.max() + new.max())) + 1, 9)
+    m, t, state = _run_plan(ctx, new, T, 1, 128, pages)
+    assert cskv.device_status() == 0
+    _check_plan(m, t, state, step.plan_step(ctx, new, T, 1, 128, *pages), True)
+
+
+def test_norms_of_few_and_of_many_tokens_have_the_same_bits():
+    rs = np.random.default_rng(31)
+    T, H = 90, 61
+    t, v = _values(rs, (T, H, 512))
+    small, sv = _values(rs, (T, 7, 128))
+    cs, w = _cs(rs, T), rs.uniform(0.5, 1.5, 512).astype(np.float32)
+    x, y, c = t.cuda(), small.cuda(), cuda(cs)
+    whole = None
+    for n in (T, 80, 79, 78, 77, 5, 1):
+        got = cskv.norm_rope([dict(x=x[:n], norm_w=cuda(w), rotate=True), dict(x=y[:n], norm=True, rotate=True)], c[:n])
+        if whole is None:
+            whole = got
+            assert np.array_equal(_bits(got[0]), _want_heads(v, True, w, 1e-6, cs))
+            assert np.array_equal(_bits(got[1]), _want_heads(sv, True, None, 1e-6, cs))
+        assert all(torch.equal(a, b[:n]) for a, b in zip(got, whole)), n
