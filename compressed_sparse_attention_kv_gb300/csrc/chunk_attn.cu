@@ -244,15 +244,24 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair* part, Pair* total) {
   return v;
 }
 
-// What request r has; a wrong length is told by the plan alone.
+// Whether request r's queries are none: a border outside [0, T], or before the one before it.
+__device__ __forceinline__ bool wrong_queries(const ChunkArgs& a, int lo, int hi) { return lo < 0 || hi < lo || hi > a.T; }
+
+// What request r has, nq -1 with wrong queries (one such request leaves all without any: the sum of their
+// queries is no longer bounded by T); what is wrong is told by the plan alone.
 template <bool kTell>
 __device__ __forceinline__ ReqPlan request_of(const ChunkArgs& a, int r) {
   auto wrong = [] { if constexpr (kTell) set_err(CSKV_ERR_BOUNDS); };
   ReqPlan p = {};
   const int lo = a.cu_q[r], hi = a.cu_q[r + 1];
   int len = a.ctx_len != nullptr ? a.ctx_len[r] : 0, given = a.n_entries != nullptr ? a.n_entries[r] : 0;
-  if (lo < 0 || hi < lo || hi > a.T) wrong();
-  else { p.q0 = lo; p.nq = hi - lo; }
+  if (wrong_queries(a, lo, hi)) {
+    wrong();
+    p.nq = -1;
+    return p;
+  }
+  p.q0 = lo;
+  p.nq = hi - lo;
   if (p.nq == 0) return p;
   if (len < 0 || len > a.max_ctx) { wrong(); len = max(0, min(len, a.max_ctx)); }
   p.len = len;
@@ -287,10 +296,19 @@ __device__ void plan_chunks(const ChunkArgs& a, PlanSmem& sm) {
   long long keys = 0;
   int items = 0;
   Pair total;
+  const bool once = a.R <= static_cast<int>(blockDim.x);
+  bool sound = true;
+  if (!once) {
+    bool wrong = false;
+    for (int r = tid; r < a.R; r += blockDim.x) wrong |= wrong_queries(a, a.cu_q[r], a.cu_q[r + 1]);
+    sound = __syncthreads_or(wrong) == 0;
+  }
   for (int r0 = 0; r0 < a.R; r0 += blockDim.x) {
     const int r = r0 + tid;
     ReqPlan p = {};
     if (r < a.R) p = request_of<true>(a, r);
+    if (once) sound = __syncthreads_or(p.nq < 0) == 0;
+    if (!sound) p = ReqPlan{};
     const long long mine = static_cast<long long>(p.entries16) + p.rows16;
     const int blocks = (p.nq + a.group - 1) / a.group;
     const Pair upto = block_scan(Pair{mine, blocks}, part, &total);
@@ -501,8 +519,10 @@ __device__ __forceinline__ void decode_chunks(const ChunkArgs& a, DecodeSmem* sm
     Pair total;
     const int each = (a.R + kPrepThreads - 1) / kPrepThreads, r0 = threadIdx.x * each;
     long long mine = 0;
+    bool wrong = false;
     for (int r = r0; r < min(a.R, r0 + each); ++r) {
       const ReqPlan p = request_of<false>(a, r);
+      wrong |= p.nq < 0;
       sm->req[r] = ReqRows{mine, p.entries, p.rows, p.row0, 0};
       mine += p.entries16 + p.rows16;
     }
@@ -512,8 +532,7 @@ __device__ __forceinline__ void decode_chunks(const ChunkArgs& a, DecodeSmem* sm
       p.base += before;
       if (p.base + up16(p.entries) + up16(p.rows) > a.max_keys) p.entries = p.rows = 0;   // no room
     }
-    keys = min(total.x, a.max_keys);
-    __syncthreads();
+    keys = __syncthreads_or(wrong) != 0 ? 0 : min(total.x, a.max_keys);
   } else {
     keys = a.head->keys;
   }

@@ -1,6 +1,7 @@
 // C-ABI front end of include/cskvs.h: synchronous argument checks, then launches.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/cskvs.h"
 #include "internal.h"
@@ -10,6 +11,9 @@ using namespace cskv;
 namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool words(std::initializer_list<const void*> p) {   // arrays of 32-bit numbers (or none)
+  return std::all_of(p.begin(), p.end(), [](const void* x) { return aligned(x, 4); });
+}
 
 int32_t cuda_status(cudaError_t e) { return e == cudaSuccess ? CSKV_OK : CSKV_ERR_CUDA; }
 
@@ -74,6 +78,9 @@ int32_t cskvs_plan_step(const int32_t* ctx_len, const int32_t* n_new, int32_t B,
       n_rows == nullptr)
     return CSKV_ERR_INVALID;
   if (T > 0 && (req_of == nullptr || pos1 == nullptr)) return CSKV_ERR_INVALID;
+  if (!words({ctx_len, n_new, block_table, shared_pages, free_pages, state, state_out, cu_new, new_len, first_row, n_rows,
+              req_of, pos1}) || !aligned(slot, 8) || !aligned(ring_slot, 8))
+    return CSKV_ERR_INVALID;
   if (block_table != nullptr) {
     if (max_pages < 1 || free_pages == nullptr || capacity < 1 || state == nullptr || state_out == nullptr)
       return CSKV_ERR_INVALID;
@@ -108,7 +115,8 @@ int32_t cskvs_rope_cs(const cskvs_rope_plan* plan, const int32_t* positions, int
   if (plan == nullptr || plan->axes < 1 || plan->axes > 4 || T < 0 || T > kMaxTokens) return CSKV_ERR_INVALID;
   for (int k = 0; k < 32; ++k)
     if (plan->axis[k] >= plan->axes) return CSKV_ERR_INVALID;
-  if (T > 0 && (positions == nullptr || out == nullptr || !aligned(out, 16))) return CSKV_ERR_INVALID;
+  if (T > 0 && (positions == nullptr || out == nullptr)) return CSKV_ERR_INVALID;
+  if (!words({positions}) || !aligned(out, 16)) return CSKV_ERR_INVALID;
   if (plan->axes > 1 && axis_stride < T) return CSKV_ERR_INVALID;
   return cuda_status(launch_rope_cs(*plan, positions, axis_stride, shift, T, out, static_cast<cudaStream_t>(stream)));
 }
@@ -164,6 +172,7 @@ int32_t cskvs_chunk_attn(const void* q, const int32_t* cu_q, const int32_t* ctx_
   if (R < 1 || R > kMaxReqs || T < 1 || T > kMaxQueries || H < 1 || H > 128) return CSKV_ERR_INVALID;
   if (q == nullptr || cu_q == nullptr || q_rope_cs == nullptr || out == nullptr) return CSKV_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(q_rope_cs, 16)) return CSKV_ERR_INVALID;
+  if (!words({cu_q, ctx_len, n_entries, sink, lse})) return CSKV_ERR_INVALID;
   if (entries == nullptr && rows == nullptr) return CSKV_ERR_INVALID;
   const unsigned formats = (1u << CSKV_FMT_BF16) | (1u << CSKV_FMT_FP8_E4M3_E8M0_B32) | (1u << CSKV_FMT_FP4_E2M1_E4M3_B16);
   for (const cskv_paged* c : {entries, rows})

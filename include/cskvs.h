@@ -139,7 +139,8 @@ CSKV_API int32_t cskvs_norm_rope(const cskvs_norm_job* jobs, int32_t njobs, cons
  * left as they were.  A row that no query sees never counts; no page wholly behind the
  * windows is looked up.  A key row with a value that is not finite makes the outputs of
  * the queries that see it NaN, and no others.
- * q, out: bf16 [T, H, 512]; cu_q: int32 [R + 1], from 0, not decreasing, at most T;
+ * q, out: bf16 [T, H, 512]; cu_q: int32 [R + 1], from 0, not decreasing, at most T (else no
+ * query is computed, CSKV_ERR_BOUNDS);
  * ctx_len: int32 [R], at most max_ctx_len; n_entries: int32 [R] (NULL: no such bound;
  * required with ratio 0); entries (NULL: none), rows (NULL: none; one of the two is
  * given): 512-d, BF16, FP8 or FP4, block tables [R, max_pages] or NULL (one flat array of

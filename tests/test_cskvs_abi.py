@@ -58,6 +58,9 @@ BAD_CHUNK = [{"q": None}, {"q": FAKE + 8}, {"cu": None}, {"ctx": None}, {"R": 0}
              {"max_entries": (1 << 30) + 1}, {"window": 0}, {"window": -5}, {"max_ctx": -1}, {"max_ctx": (1 << 30) + 1},
              {"scale": 0.0}, {"scale": NAN}, {"scale": INF}, {"scale": 2e38}, {"cs": None}, {"cs": FAKE + 4},
              {"out": None}, {"out": FAKE + 2}, {"max_keys": -1}, {"max_keys": (1 << 40) + 1}]
+BAD_PLAN += [{k: FAKE + 2} for k in ("ctx", "new", "table", "shared", "free", "state", "state_out", "cu", "len", "first", "rows",
+                                     "req", "pos1")] + [{"slot": FAKE + 4}, {"ring": FAKE + 4}]
+BAD_CHUNK += [{k: FAKE + 2} for k in ("cu", "ctx", "n", "sink", "lse")]
 
 
 @pytest.mark.parametrize("change", BAD_PLAN)
@@ -188,6 +191,7 @@ def test_rotation_plans_of_several_axes(lib):
     plan = p.struct
     assert lib.cskvs_rope_cs(None, FAKE, 8, 0, 8, FAKE, None) == 1
     assert lib.cskvs_rope_cs(ctypes.byref(plan), None, 8, 0, 8, FAKE, None) == 1
+    assert lib.cskvs_rope_cs(ctypes.byref(plan), FAKE + 2, 8, 0, 8, FAKE, None) == 1
     assert lib.cskvs_rope_cs(ctypes.byref(plan), FAKE, 7, 0, 8, FAKE, None) == 1       # axes overlap
     assert lib.cskvs_rope_cs(ctypes.byref(plan), FAKE, 8, 0, 8, FAKE + 8, None) == 1
     assert lib.cskvs_rope_cs(ctypes.byref(plan), FAKE, 8, 0, -1, FAKE, None) == 1

@@ -510,3 +510,20 @@ def test_many_requests(R):
     rest = np.flatnonzero(c.req != R - 2)
     assert torch.equal(bad[rest], out[rest]) and torch.equal(bad_lse[rest], lse[rest])
     assert cskv.device_status() == 0
+
+
+@pytest.mark.parametrize("R", [3, 300, 1025])
+def test_queries_that_do_not_add_up_are_left_and_reported(R):
+    """Borders that go back, again and again, below 0 or beyond T: each request alone would have all queries."""
+    c = Case([1] * R, [40] * R, 8, 1, FP8, window=16, seed=R)
+    back = np.tile([0, R], R)[:R + 1]
+    low, high, one = c.cu.copy(), c.cu.copy(), c.cu.copy()
+    low[1], high[R], one[R // 2] = -1, R + 1, one[R // 2 + 1] + 1
+    for cu in (back, low, high, one):
+        out = torch.full((R, 8, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((R, 8), 5.0, device="cuda")
+        c.run(cu_q=_i32(cu), out=out, lse=lse)
+        assert cskv.device_status() == ERR_BOUNDS
+        assert (out == 3.0).all() and (lse == 5.0).all()
+    out, lse = c.run()
+    c.check(out, lse, pick=_some(R, 9, R))
