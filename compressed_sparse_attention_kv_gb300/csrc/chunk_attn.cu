@@ -17,7 +17,8 @@
 //
 // Three kernels, each started while the one before it ends:
 //   chunk_prepare_kernel its first block plans: the requests' key lists, the row blocks and their tiles as one line
-//                        of work, cut into equal shares.  The others decode meanwhile: every key that some query
+//                        of work, cut into equal shares, or dealt out whole where that is as short.  The others
+//                        decode meanwhile: every key that some query
 //                        sees, once, from its paged row to bf16 in the order that the tensor core reads (the
 //                        same rows are read by hundreds of row blocks: decoding a tile takes longer than
 //                        its products).  (Two kernels one after the other for very many requests.)
@@ -84,6 +85,11 @@ constexpr int kItemUnits = 4;
 // Units of a share at least (5 tokens on 288 keys, 3 tiles: 18.4 us on several pairs with 4, 17.6 us on one with 8;
 // with 16 the same).
 constexpr int kLeastShare = 8;
+// Row blocks are dealt out whole, largest first, where the longest share is at most this many units longer than an equal
+// one: what cutting row blocks and joining their parts costs.  (Cut and whole: 455 row blocks, shares of 79 and at
+// most 80 units, 107 and 95 us; 13, 8 and 12: 27.4 and 24.2; 91, 23 and 36: 42.7 and 42.4; 58, 35 and 50: 54.5 and
+// 56.9; 246, 131 and 164: 132 and 143.)
+constexpr int kSplitCost = 15;
 constexpr int kFewParts = 8;              // of a row: joined by one warp
 constexpr unsigned long long kDrainLimit = 1ull << 27;   // cycles that a block which gives up waits for its own copies
 
@@ -96,7 +102,7 @@ struct ReqPlan {
 };
 struct ItemPlan {           // of a row block
   long long unit0;          // its first unit of work
-  int req, pad;
+  int req, item;            // its request; its number
 };
 struct SharePlan {
   ItemPlan plan;            // of its first row block
@@ -111,6 +117,7 @@ struct SplitPlan {          // a row block that several pairs share
 struct ChunkHead {
   int items, blocks;
   int few, many;            // split[0 .. few): row blocks of kFewParts parts at most; split[most_blocks - many ..): of more
+  int whole, pad;           // shares of whole row blocks, in `list`'s order
   long long units;          // of all row blocks
   long long keys;           // decoded rows
 };
@@ -138,6 +145,7 @@ struct ChunkArgs {
   ChunkHead* head;
   ReqPlan* req;
   ItemPlan* item;           // [items + 1]; the last one ends the units
+  ItemPlan* list;           // [items]: the row blocks share by share, where shares are of whole ones
   SharePlan* share;         // [most_blocks]
   SplitPlan* split;         // [most_blocks]
   uint8_t* flags;           // of every decoded row: 0, kNone, kUnfit
@@ -284,11 +292,69 @@ __device__ __forceinline__ ReqPlan request_of(const ChunkArgs& a, int r) {
 }
 
 constexpr int kPlanStaged = 2048;         // row blocks whose places are searched in shared memory
+constexpr int kSizes = 1024;              // sizes of row blocks that are told apart
 struct PlanSmem {
   Pair part[32];
   long long staged[kPlanStaged];
   int item0[kOwnReqs];
+  int sizes[kSizes];
+  uint16_t rank[kPlanStaged];
+  int load[kPairs];
 };
+
+// Deals the row blocks out whole, if that is no longer than equal shares with their join: largest first, to the
+// pairs in order and back again in turn (row blocks of one size in any order: every one's results are its own).
+__device__ __forceinline__ bool deal_whole(const ChunkArgs& a, PlanSmem& sm, int items, int most) {
+  const int tid = threadIdx.x, pairs = min(items, a.most_blocks), rounds = items / pairs, rest = items % pairs;
+  auto units_at = [&](int e) { return static_cast<int>(sm.staged[e + 1] - sm.staged[e]); };
+  auto pair_of = [&](int rank) { return (rank / pairs) & 1 ? pairs - 1 - rank % pairs : rank % pairs; };
+  const bool single = pairs == items;    // one for each pair: in any order
+  bool longer = false;
+  if (single) {
+    for (int e = tid; e < items; e += blockDim.x) longer |= units_at(e) > most;
+  } else {
+    for (int i = tid; i < kSizes; i += blockDim.x) sm.sizes[i] = 0;
+    for (int i = tid; i < pairs; i += blockDim.x) sm.load[i] = 0;
+    __syncthreads();
+    auto size_of = [&](int e) { return kSizes - 1 - min(units_at(e) / 2, kSizes - 1); };
+    for (int e = tid; e < items; e += blockDim.x) atomicAdd(&sm.sizes[size_of(e)], 1);
+    __syncthreads();
+    const int each = kSizes / blockDim.x;
+    int mine = 0;
+    for (int i = 0; i < each; ++i) mine += sm.sizes[tid * each + i];
+    Pair total;
+    int at = block_scan(Pair{0, mine}, sm.part, &total).y - mine;
+    for (int i = 0; i < each; ++i) {
+      const int n = sm.sizes[tid * each + i];
+      sm.sizes[tid * each + i] = at;
+      at += n;
+    }
+    __syncthreads();
+    for (int e = tid; e < items; e += blockDim.x) {
+      const int rank = atomicAdd(&sm.sizes[size_of(e)], 1);
+      sm.rank[e] = static_cast<uint16_t>(rank);
+      atomicAdd(&sm.load[pair_of(rank)], units_at(e));
+    }
+    __syncthreads();
+    longer = tid < pairs && sm.load[tid] > most;
+  }
+  if (__syncthreads_or(longer)) return false;
+  // row blocks of the pairs before: whole rounds, and those of the last one
+  auto first_of = [&](int pair) { return pair * rounds + ((rounds & 1) ? max(0, pair - (pairs - rest)) : min(pair, rest)); };
+  for (int e = tid; e < items; e += blockDim.x) {
+    const int rank = single ? e : sm.rank[e], pair = pair_of(rank), first = first_of(pair);
+    const ItemPlan plan = {0, a.item[e].req, e};
+    a.list[first + rank / pairs] = plan;
+    if (rank < pairs) {
+      a.share[pair].plan = plan;
+      a.share[pair].lo = 0;
+      a.share[pair].hi = 1ll << 40;   // (beyond every tile)
+      a.share[pair].first = first;
+      a.share[pair].last = first_of(pair + 1) - 1;
+    }
+  }
+  return true;
+}
 
 __device__ void plan_chunks(const ChunkArgs& a, PlanSmem& sm) {
   Pair* part = sm.part;
@@ -356,7 +422,7 @@ __device__ void plan_chunks(const ChunkArgs& a, PlanSmem& sm) {
 #pragma unroll
     for (int u = 0; u < kPlanItems; ++u) {
       if (e1 + u < items) {
-        a.item[e1 + u] = ItemPlan{at, req[u], 0};
+        a.item[e1 + u] = ItemPlan{at, req[u], e1 + u};
         if (e1 + u < kPlanStaged) sm.staged[e1 + u] = at;
       }
       at += mine[u];
@@ -367,6 +433,17 @@ __device__ void plan_chunks(const ChunkArgs& a, PlanSmem& sm) {
     if (items < kPlanStaged) sm.staged[items] = units;
   }
   __syncthreads();
+  // may the row blocks be dealt out whole?  A first test needs no order: as many average ones as some pair gets at least
+  bool whole = false;
+  if (items > 1 && items < kPlanStaged) {
+    const float all = static_cast<float>(units), most = fmaxf(__fdividef(all, a.most_blocks), kLeastShare) + kSplitCost;
+    whole = __fdividef(all, items) * ceilf(__fdividef(items, min(items, a.most_blocks))) <= most;
+    if (whole) whole = deal_whole(a, sm, items, static_cast<int>(most));
+  }
+  if (whole) {
+    if (tid == 0) *a.head = ChunkHead{items, min(items, a.most_blocks), 0, 0, 1, 0, units, keys};
+    return;
+  }
   const int blocks = static_cast<int>(max(1ll, min(static_cast<long long>(a.most_blocks), units / kLeastShare)));
   // the row blocks of each share; those that a border cuts are listed at the last border inside
   if (items == 0) {
@@ -409,7 +486,7 @@ __device__ void plan_chunks(const ChunkArgs& a, PlanSmem& sm) {
   const Pair at = block_scan(Pair{few, many}, part, &total);
   if (few) a.split[at.x - 1] = split;
   if (many) a.split[a.most_blocks - at.y] = split;
-  if (tid == 0) *a.head = ChunkHead{items, blocks, static_cast<int>(total.x), total.y, units, keys};
+  if (tid == 0) *a.head = ChunkHead{items, blocks, static_cast<int>(total.x), total.y, 0, 0, units, keys};
 }
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
@@ -712,13 +789,13 @@ __device__ __forceinline__ bool role_any(bool p) {
 }
 constexpr int kSoftId = 1, kOutId = 2;
 
-// Row block e of this pair's share, and this block's rows of it; one warp.  First what all others wait for.
-__device__ void make_item(const ChunkArgs& a, ChunkSmem* sm, int place, int e, const ItemPlan& plan, long long lo, long long hi,
+// A row block of this pair's share, and this block's rows of it; one warp.  First what all others wait for.
+__device__ void make_item(const ChunkArgs& a, ChunkSmem* sm, int place, const ItemPlan& plan, long long lo, long long hi,
                           int pair, int rank) {
   const int lane = threadIdx.x & 31;
   Item* it = &sm->item[place];
   const ReqPlan p = a.req[plan.req];
-  const BlockKeys k = block_keys(a, p, e - p.item0);
+  const BlockKeys k = block_keys(a, p, plan.item - p.item0);
   const int rows = (k.i1 - k.i0) * a.H, half = (rows + 1) / 2;
   const int at = rank == 0 ? 0 : half, nr = rank == 0 ? half : rows - half;   // of the row block
   // its tiles between the share's borders
@@ -1246,8 +1323,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
     ItemPlan plan = share.plan;
     for (int e = 0; e < items; ++e) {
       if (e >= 2 && !wait_warp(sm, &sm->item_free[e & 1], ((e >> 1) - 1) & 1, a.spin)) break;
-      if (e > 0) plan = a.item[share.first + e];
-      make_item(a, sm, e & 1, share.first + e, plan, share.lo, share.hi, pair, rank);
+      if (e > 0) plan = (head.whole ? a.list : a.item)[share.first + e];
+      make_item(a, sm, e & 1, plan, share.lo, share.hi, pair, rank);
     }
   } else if (warp == kLoadWarp) {          // ---- keys
     if (elect_lane()) {
@@ -1602,7 +1679,7 @@ inline size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
 // How the row blocks and the workspace follow from the sizes alone.
 struct Layout {
   int group, most_blocks;
-  size_t head, req, item, share, split, flags, bad, images, opart, ml, bytes;
+  size_t head, req, item, list, share, split, flags, bad, images, opart, ml, bytes;
 };
 Layout layout_of(int R, int T, int H, int64_t max_keys) {
   Layout l = {};
@@ -1617,6 +1694,7 @@ Layout layout_of(int R, int T, int H, int64_t max_keys) {
   l.head = take(sizeof(ChunkHead));
   l.req = take(sizeof(ReqPlan) * static_cast<size_t>(R));
   l.item = take(sizeof(ItemPlan) * static_cast<size_t>(items + 1));
+  l.list = take(sizeof(ItemPlan) * static_cast<size_t>(std::min<int64_t>(items, kPlanStaged)));
   l.share = take(sizeof(SharePlan) * l.most_blocks);
   l.split = take(sizeof(SplitPlan) * l.most_blocks);
   l.flags = take(keys);
@@ -1688,6 +1766,7 @@ cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t*
   a.head = reinterpret_cast<ChunkHead*>(ws + l.head);
   a.req = reinterpret_cast<ReqPlan*>(ws + l.req);
   a.item = reinterpret_cast<ItemPlan*>(ws + l.item);
+  a.list = reinterpret_cast<ItemPlan*>(ws + l.list);
   a.share = reinterpret_cast<SharePlan*>(ws + l.share);
   a.split = reinterpret_cast<SplitPlan*>(ws + l.split);
   a.flags = ws + l.flags;

@@ -527,3 +527,15 @@ def test_queries_that_do_not_add_up_are_left_and_reported(R):
         assert (out == 3.0).all() and (lse == 5.0).all()
     out, lse = c.run()
     c.check(out, lse, pick=_some(R, 9, R))
+
+
+@pytest.mark.parametrize("new,length,H,ratio,window", [([77], [77], 128, 1, 0), ([76], [76], 128, 1, 0), ([75, 1], [75, 900], 128, 1, 0),
+                                                       ([200, 33, 5], [200, 400, 700], 64, 1, 0), ([640], [1000], 32, 4, 128),
+                                                       ([2100, 1, 40], [2100, 300, 40], 96, 128, 128), ([1, 700], [9000, 700], 64, 1, 0)])
+def test_row_blocks_dealt_out_whole_and_cut(new, length, H, ratio, window):
+    """As many row blocks as pairs, one more, some rounds, more than are dealt out, one long one among short ones."""
+    c = Case(new, length, H, ratio, FP8, window=window, rfmt=BF16, sink=True, seed=len(new) + H)
+    out, lse = c.run()
+    c.check(out, lse, pick=sorted(set(_some(len(c.req), 14)) | {min(len(c.req) - 1, k) for k in (74, 75, 76, 77)}))
+    again, lse2 = c.run()
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
