@@ -321,7 +321,10 @@ __device__ __forceinline__ bool deal_whole(const ChunkArgs& a, PlanSmem& sm, int
     for (int i = tid; i < pairs; i += blockDim.x) sm.load[i] = 0;
     __syncthreads();
     auto size_of = [&](int e) { return kSizes - 1 - min(units_at(e) / 2, kSizes - 1); };
-    for (int e = tid; e < items; e += blockDim.x) atomicAdd(&sm.sizes[size_of(e)], 1);
+    for (int e = tid; e < items; e += blockDim.x) {
+      atomicAdd(&sm.sizes[size_of(e)], 1);
+      longer |= units_at(e) / 2 >= kSizes;   // not told apart: their order, and with it the longest share, would be any
+    }
     __syncthreads();
     const int each = kSizes / blockDim.x;
     int mine = 0;
@@ -340,7 +343,7 @@ __device__ __forceinline__ bool deal_whole(const ChunkArgs& a, PlanSmem& sm, int
       atomicAdd(&sm.load[pair_of(rank)], units_at(e));
     }
     __syncthreads();
-    longer = tid < pairs && sm.load[tid] > most;
+    longer |= tid < pairs && sm.load[tid] > most;
   }
   if (__syncthreads_or(longer)) return false;
   // row blocks of the pairs before: whole rounds, and those of the last one
@@ -846,6 +849,7 @@ __device__ void make_item(const ChunkArgs& a, ChunkSmem* sm, int place, const It
   least = __reduce_min_sync(0xFFFFFFFFu, least);
   uint32_t bad = 0;
   const uint8_t* groups = a.bad + p.base / kDecodeRows;
+#pragma unroll 4
   for (int g = begin * (kTile / kDecodeRows) + lane; g < min(end * kTile, k.keys) / kDecodeRows; g += 32) {
     const int k0 = g * kDecodeRows;
     bad |= groups[(k0 < k.seen16 ? k0 : raw_at + k0 - k.seen16) / kDecodeRows];

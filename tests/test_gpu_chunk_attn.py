@@ -539,3 +539,22 @@ def test_row_blocks_dealt_out_whole_and_cut(new, length, H, ratio, window):
     c.check(out, lse, pick=sorted(set(_some(len(c.req), 14)) | {min(len(c.req) - 1, k) for k in (74, 75, 76, 77)}))
     again, lse2 = c.run()
     assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+def test_row_blocks_of_a_thousand_tiles_and_more_in_full_rounds():
+    """Sizes beyond those that the plan tells apart: the same bits each time."""
+    n = 132000
+    c = Case([1], [n], 16, 1, FP4, seed=52)                 # its pages are every request's
+    R = 2 * 76
+    lens = n - 3 * np.arange(R)
+    entries = c.entries.to_device()
+    kw = dict(c.args(), q=c.q[0].repeat(R, 1, 1).cuda(), cu_q=_i32(np.arange(R + 1)), ctx_len=_i32(lens),
+              q_rope_cs=cuda(cskv.rope_table(lens - 1)), max_keys=int(((lens + 15) // 16 * 16).sum()),
+              entries=cskv.PagedCache(entries.pool, _i32(np.repeat(c.entries.block_table, R, 0)), FP4, 512))
+    out, lse = cskv.chunk_attn(**kw)
+    assert cskv.device_status() == 0
+    for i in (0, 77, 151):
+        _check(out[i], lse[i], bounded.attend(c.q[1][0], int(lens[i]) - 1, c.entries.decoded[0][:lens[i]], None, SCALE))
+    for _ in range(3):
+        again, lse2 = cskv.chunk_attn(**kw)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
