@@ -14,7 +14,9 @@ namespace {
 // ---------------------------------------------------------------------------
 // cskvs_plan_step.  Three prefix sums over the requests (their new tokens, the pages they need,
 // the pages they give back), then every token finds its request among the sums and every new
-// page its place in the ring of free pages.  Nothing is carried between blocks but the sums, so
+// page its place in the ring of free pages.  A request that ends gives back the ids of its row that are
+// pages: where none was left it has -1, and its row is counted before the sum of what comes back.  Nothing
+// is carried between blocks but the sums, so
 // a page's place follows from its number alone: the k-th new page of the step is the k-th of the
 // ring, and the j-th page given back goes j places behind the ring's last one.  The two stretches
 // do not meet, so that blocks read and write the ring without waiting for one another.
@@ -33,7 +35,7 @@ struct PlanRecord {        // of a request
   int tok0;                // its first token
   int ctx;                 // its length before the step
   int first, last;         // its pages before and after the step
-  int used, own;           // a request that ends: pages [own, used) are given back
+  int used, own;           // a request that ends: of its row's places [own, used) the pages are given back
   long long take, give;    // the number of its first new page, and of its first page given back
 };
 struct PlanHead {
@@ -99,10 +101,49 @@ __device__ __forceinline__ int bounded_len(int n) {
   return n < 0 ? 0 : kMaxLen;
 }
 
+// The pages among the places [own, used) of the rows of requests that end in this round: a warp reads 512 places
+// of a row at once, 16 bytes a lane; with fewer rows than warps several warps share one.
+constexpr int kCountAtOnce = 4;          // 16-byte pieces of a lane
+constexpr int kMoveAtOnce = 8;           // places of a lane
+struct Ended {
+  int thread, own, used;   // of a request that ends: its thread
+};
+__device__ __forceinline__ int pages_in(const int4& v) {
+  return 4 + (v.x >> 31) + (v.y >> 31) + (v.z >> 31) + (v.w >> 31);
+}
+__device__ void count_pages(const PlanArgs& a, int b0, const Ended* ended, int n, int* pages) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int each = max(1, warps / n), groups = warps / each, part = warp % each;
+  for (int e = warp / each; e < n; e += groups) {   // (fewer rows than warps: one each, groups >= n)
+    const Ended r = ended[e];
+    const int32_t* line = a.table + static_cast<long long>(b0 + r.thread) * a.max_pages;
+    // the places before the first 16-byte border, whole pieces, and the places behind the last one
+    const int ahead = min(r.used - r.own, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(line + r.own) & 15)) & 15) / 4);
+    const int4* piece = reinterpret_cast<const int4*>(line + r.own + ahead);
+    const int whole = (r.used - r.own - ahead) / 4, behind = r.own + ahead + 4 * whole;
+    int have = 0;
+    if (part == 0) {
+      if (lane < ahead) have += line[r.own + lane] >= 0;
+      if (behind + lane < r.used) have += line[behind + lane] >= 0;
+    }
+    for (int x = part * (32 * kCountAtOnce) + lane; x < whole; x += each * (32 * kCountAtOnce)) {
+      int4 v[kCountAtOnce];
+#pragma unroll
+      for (int u = 0; u < kCountAtOnce; ++u) v[u] = x + 32 * u < whole ? piece[x + 32 * u] : make_int4(-1, -1, -1, -1);
+#pragma unroll
+      for (int u = 0; u < kCountAtOnce; ++u) have += pages_in(v[u]);
+    }
+    have = __reduce_add_sync(0xFFFFFFFFu, have);
+    if (lane == 0) atomicAdd(&pages[r.thread], have);
+  }
+}
+
 // The sums, the lengths and the ring's new state; one block.  first_tokens (shared memory, may be
 // null): the requests' first tokens once more.
 __device__ void plan_sums(const PlanArgs& a, int* first_tokens) {
   __shared__ long long part[32];
+  __shared__ Ended ended[kPlanThreads];
+  __shared__ int pages[kPlanThreads], n_ended;
   long long tok = 0, take = 0, give = 0;   // before this round of requests
   int head = a.state != nullptr ? a.state[0] : 0, count = a.state != nullptr ? a.state[1] : 0;
   if (a.state != nullptr && (head < 0 || head >= a.capacity || count < 0 || count > a.capacity)) {
@@ -122,6 +163,8 @@ __device__ void plan_sums(const PlanArgs& a, int* first_tokens) {
       n = ends ? 0 : n;
       if (n > kMaxLen - ctx) { set_err(CSKV_ERR_BOUNDS); n = kMaxLen - ctx; }
     }
+    pages[threadIdx.x] = 0;
+    if (threadIdx.x == 0) n_ended = 0;
     long long total;
     const long long upto = tok + block_scan(n, part, &total);
     const int tok0 = static_cast<int>(min(upto - n, static_cast<long long>(a.T)));
@@ -143,9 +186,14 @@ __device__ void plan_sums(const PlanArgs& a, int* first_tokens) {
     }
     r.own = there && ends && a.shared != nullptr ? max(0, min(a.shared[b], r.used)) : 0;
     const int need = there && a.table != nullptr ? r.last - r.first : 0;
-    const int back = there && a.table != nullptr ? r.used - r.own : 0;
+    if (a.table != nullptr && r.used > r.own) ended[atomicAdd(&n_ended, 1)] = Ended{static_cast<int>(threadIdx.x), r.own, r.used};
     r.take = take + block_scan(need, part, &total) - need;
     take += total;
+    if (n_ended > 0) {   // (in any order: their counts are their own)
+      count_pages(a, b0, ended, n_ended, pages);
+      __syncthreads();
+    }
+    const int back = pages[threadIdx.x];
     r.give = give + block_scan(back, part, &total) - back;
     give += total;
     if (there) {
@@ -254,9 +302,18 @@ __device__ void plan_pages(const PlanArgs& a, const PlanHead& h, int warp, int w
     const PlanRecord r = a.rec[b];
     int32_t* line = a.table + static_cast<long long>(b) * a.max_pages;
     for (int lp = r.first + lane; lp < r.last; lp += 32) line[lp] = new_page(a, h, r.take + lp - r.first);
-    for (int lp = r.own + lane; lp < r.used; lp += 32) {
-      const long long j = r.give + lp - r.own;
-      if (j < a.capacity - h.count) *ring_place(a, h, h.count + j) = line[lp];
+    long long give = r.give;   // the number of the next page
+    for (int lp = r.own; lp < r.used; lp += 32 * kMoveAtOnce) {
+      int id[kMoveAtOnce];
+#pragma unroll
+      for (int u = 0; u < kMoveAtOnce; ++u) id[u] = lp + 32 * u + lane < r.used ? line[lp + 32 * u + lane] : -1;
+#pragma unroll
+      for (int u = 0; u < kMoveAtOnce; ++u) {
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, id[u] >= 0);
+        const long long j = give + __popc(there & ((1u << lane) - 1u));
+        if (id[u] >= 0 && j < a.capacity - h.count) *ring_place(a, h, h.count + j) = id[u];
+        give += __popc(there);
+      }
     }
   }
 }

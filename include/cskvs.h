@@ -48,10 +48,13 @@ extern "C" {
  * ring of `capacity` ids of free pages, state[0] the place of the first one, state[1] how
  * many there are.  A request that outgrows its pages gets new ones, requests in order, its
  * pages in order, from the front of the ring, written into its row of the table; where
- * none is left the table gets -1 and state_out[2] counts the missing pages.  The pages of
- * a request that ends go behind the last one, requests in order, except its first
- * shared_pages[b] (pages that are not its own; NULL: none); they can be taken from the next
- * step on.  The table's row of such a request stays as it is.  state_out, int32 [4]: the
+ * none is left the table gets -1 and state_out[2] counts the missing pages.  No later step
+ * fills such a hole: the rows of that page were not kept (their slots are -1), and the request
+ * goes on behind it; a caller that needs them ends the request and begins it again.  The
+ * pages of a request that ends go behind the last one, requests in order, except the first
+ * shared_pages[b] places of its row (pages that are not its own; NULL: none) and those that
+ * hold no page (negative ids); they can be taken from the next step on.  The table's row of
+ * such a request stays as it is.  state_out, int32 [4]: the
  * ring after the step (place, count), the missing pages, 0; it may be state itself.  Ids
  * outside the table or beyond the ring's capacity set CSKV_ERR_BOUNDS.
  * ctx_len, n_new, shared_pages: int32 [B]; cu_new: int32 [B + 1]; new_len (may be ctx_len

@@ -4,8 +4,8 @@ rotation, and which keys a chunk's queries see (oracle side).
 TEST INFRASTRUCTURE ONLY.  Python integers and numpy, from the definitions:
 
 * a request of ctx tokens that gets n more has floor((ctx + n) / ratio) rows, 64 to a page; new
-  pages come from the front of a ring of free ones, requests in order; a request that ends
-  gives its pages back behind the ring's last one;
+  pages come from the front of a ring of free ones, requests in order, and where none is left the
+  table has -1; a request that ends gives the pages that it has back behind the ring's last one;
 * pair k of the rotated dims turns by position * theta^(-2k/64) along its own axis;
 * a norm and rotation is the compressor's contract for one token (its sums, roundings and codes);
 * the query at position t sees the entries j < floor((t + 1) / ratio) and the rows
@@ -43,7 +43,7 @@ def plan_step(ctx, new, T, ratio, ring_rows=0, table=None, free=None, state=None
         if table is not None:
             if ends:
                 own = 0 if shared is None else int(shared[b])
-                given += [int(p) for p in table[b, min(own, pages_of(have // ratio)):pages_of(have // ratio)]]
+                given += [int(p) for p in table[b, min(own, pages_of(have // ratio)):pages_of(have // ratio)] if p >= 0]
             for lp in range(pages_of(first), pages_of(rows)):
                 if taken < count:
                     table[b, lp] = free[(head + taken) % len(free)]
