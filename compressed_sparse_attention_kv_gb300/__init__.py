@@ -883,9 +883,9 @@ def chunk_attn(q, cu_q, ctx_len, entries, ratio, max_entries, max_ctx_len, sink,
     [T, H, 512]) are the last tokens of request r, whose length is ctx_len[r]; the one at position
     t sees the entries j < floor((t + 1) / ratio) of `entries` (a PagedCache; ratio 0: all
     n_entries[r]; never more than n_entries[r], if given) and, with rows (a PagedCache of raw
-    rows by position), the last `window` rows up to its own.  max_keys: a tighter bound than
-    chunk_attn_max_keys (the workspace holds 1 KB for each).  Returns (out bf16 [T, H, 512], lse
-    fp32 [T, H] or None)."""
+    rows by position), the last `window` rows up to its own.  q is normed but not rotated: the call
+    turns it by q_rope_cs, and its output back.  max_keys: a tighter bound than chunk_attn_max_keys
+    (the workspace holds 1 KB for each).  Returns (out bf16 [T, H, 512], lse fp32 [T, H] or None)."""
     import torch
     T, H, dev, pq = _query(q)
     i32, f32 = torch.int32, torch.float32

@@ -7,9 +7,10 @@
  * The calls work together; nothing in between goes through the host:
  *   cskvs_plan_step   lengths -> block tables, slots, positions of the step's tokens,
  *   cskvs_rope_cs     positions -> their (cos, sin) table,
- *   cskvs_norm_rope   normed and rotated queries; normed, rotated and coded cache rows
- *                     in those slots (raw rows; cskv_compress writes entries, with
- *                     first_row as its first_entry),
+ *   cskvs_norm_rope   normed queries (not rotated: every attention call turns its own), normed
+ *                     and rotated index queries; normed, rotated and coded cache rows in
+ *                     those slots (raw rows; cskv_compress writes entries, with first_row as
+ *                     its first_entry),
  *   cskvs_chunk_attn  the new tokens' attention over all visible entries and a window.
  *
  * Every pointer is device memory unless it says host.  Arguments are checked on the
@@ -137,7 +138,8 @@ CSKV_API int32_t cskvs_norm_rope(const cskvs_norm_job* jobs, int32_t njobs, cons
  *   own; ratio 0: all n_entries[r] entries, as in attention to the states of an encoder,
  *   which are of another length), never more than n_entries[r], where that is given, and
  *   with `rows` the raw rows max(0, t - window + 1) .. t of its request.
- * One softmax with the sink, rotations, out and lse as in cskvx_window_attn; a query
+ * One softmax with the sink, rotations, out and lse as in cskvx_window_attn (q comes without
+ * its rotation, which the call does by q_rope_cs, and out goes with it undone); a query
  * without any key: out 0, lse the sink (-inf without one).  Queries from cu_q[R] on are
  * left as they were.  A row that no query sees never counts; no page wholly behind the
  * windows is looked up.  A key row with a value that is not finite makes the outputs of
