@@ -831,7 +831,8 @@ def norm_rope(jobs, rope_cs=None, stream=None):
     dicts of x (bf16 [T, H, dim], dim 128 or 512, tokens any stride apart), norm (False), norm_w
     (fp32 [dim] or None), eps (1e-6), rotate (False), and either out (bf16 [T, H, dim], None: a
     new tensor; may be x) or cache (a PagedCache of that dim, H = 1) with slot (int64 [T],
-    physical rows, < 0: skipped).  rope_cs: fp32 [T, 32, 2] (needed where a job rotates).
+    physical rows, < 0: skipped).  rope_cs: fp32 [T, 32, 2] (needed where a job rotates).  What a
+    job writes no other job of the call reads or writes.
     Returns the list of outs (None for jobs with a cache)."""
     import torch
     if not 1 <= len(jobs) <= 4:

@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <numeric>
 
 #include "../../include/cskvs.h"
 #include "internal.h"
@@ -40,6 +41,32 @@ bool cache_ok(const cskv_paged& c, int dim) {
 
 bool workspace_ok(const void* w, size_t have, size_t need) {
   return need == 0 || (w != nullptr && aligned(w, 256) && have >= need);
+}
+
+// What a norm job reads or writes: T pieces of `width` bytes, `stride` apart (at least the width).
+struct Pieces {
+  uintptr_t at;
+  int64_t stride, width;
+};
+Pieces pieces_of(const cskvs_norm_job& j, const void* at, int64_t stride) {
+  return {reinterpret_cast<uintptr_t>(at), 2 * stride, 2 * static_cast<int64_t>(j.H) * j.dim};
+}
+// Whether some piece i of a and some piece k of b share a byte: -a.width < d + i a.stride - k b.stride < b.width.
+// With equal strides exactly; else whether the whole stretches meet and some multiple of the strides' common
+// divisor lies between (pieces that pass one another in one stretch, as columns of one buffer do, do not).
+bool meet(const Pieces& a, const Pieces& b, int64_t T) {
+  using wide = __int128;
+  const wide d = static_cast<wide>(a.at) - static_cast<wide>(b.at), last = T - 1;
+  if (d + last * a.stride + a.width <= 0 || d >= last * b.stride + b.width) return false;
+  const wide step = a.stride == b.stride ? a.stride : std::gcd(a.stride, b.stride);
+  // the least m with d + m step > -a.width
+  const wide over = -a.width - d;
+  wide m = over / step - (over % step < 0) + 1;
+  if (a.stride == b.stride) {
+    m = std::max(m, -last);
+    if (m > last) return false;
+  }
+  return d + m * step < b.width;
 }
 
 // 1 / 2 pi = kInvTwoPi / 2^128
@@ -144,6 +171,16 @@ int32_t cskvs_norm_rope(const cskvs_norm_job* jobs, int32_t njobs, const float* 
     warps += static_cast<int64_t>(T) * j.H;
   }
   if (warps > (int64_t(1) << 33)) return CSKV_ERR_INVALID;   // of one launch
+  // the jobs run in any order: what one writes no other one reads or writes, and itself only in place
+  for (int32_t i = 0; i < njobs && T > 0; ++i) {
+    if (jobs[i].slot != nullptr) continue;
+    const Pieces out = pieces_of(jobs[i], jobs[i].out, jobs[i].out_stride);
+    for (int32_t k = 0; k < njobs; ++k) {
+      const cskvs_norm_job& o = jobs[k];
+      if (!(k == i && o.x == o.out) && meet(out, pieces_of(o, o.x, o.x_stride), T)) return CSKV_ERR_INVALID;
+      if (k < i && o.slot == nullptr && meet(out, pieces_of(o, o.out, o.out_stride), T)) return CSKV_ERR_INVALID;
+    }
+  }
   return cuda_status(launch_norm_rope(jobs, njobs, rope_cs, T, static_cast<cudaStream_t>(stream)));
 }
 
