@@ -857,6 +857,8 @@ def norm_rope(jobs, rope_cs=None, stream=None):
             a.slot = _take("slot", j["slot"], torch.int64, (T,), dev)
             a.cache = _cache_on("cache", cache, 0, dev)
         else:
+            if j.get("slot") is not None:
+                raise ValueError("slot needs cache")
             if out is None:
                 out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
             elif out.shape != x.shape:

@@ -100,3 +100,13 @@ def test_the_rule_of_strided_pieces_against_all_pairs(lib):
             assert refused == shared, (T, H, xs, os_, out - x)
             met, passed = met + refused, passed + (not refused)
     assert met > 500 and passed > 500
+
+
+@pytest.mark.gpu
+def test_a_slot_without_a_cache_is_refused():
+    import torch
+    import compressed_sparse_attention_kv_gb300 as cskv
+    x, slot = torch.ones((3, 1, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    for job in (dict(x=x, slot=slot), dict(x=x, slot=slot, out=torch.empty_like(x)), dict(x=x, slot=slot, cache=None)):
+        with pytest.raises(ValueError, match="slot needs cache"):
+            cskv.norm_rope([job])
