@@ -828,8 +828,8 @@ _NORM_ARRAYS = [_lib.NormJob * max(1, n) for n in range(5)]
 @_on_stream
 def norm_rope(jobs, rope_cs=None, stream=None):
     """Norms, rotation and coding of a step's queries and rows in one launch.  jobs: up to four
-    dicts of x (bf16 [T, H, dim], dim 128 or 512, tokens any stride apart), norm (False), norm_w
-    (fp32 [dim] or None), eps (1e-6), rotate (False), and either out (bf16 [T, H, dim], None: a
+    dicts of x (bf16 [T, H, dim], dim 128 or 512, tokens any stride apart), norm_w (fp32 [dim] or
+    None), norm (True with norm_w, else False), eps (1e-6), rotate (False), and either out (bf16 [T, H, dim], None: a
     new tensor; may be x) or cache (a PagedCache of that dim, H = 1) with slot (int64 [T],
     physical rows, < 0: skipped).  rope_cs: fp32 [T, 32, 2] (needed where a job rotates).  What a
     job writes no other job of the call reads or writes.
@@ -846,6 +846,8 @@ def norm_rope(jobs, rope_cs=None, stream=None):
         a.x, a.x_stride = _heads("x", x, T, dev)
         a.H, a.dim = x.shape[1], x.shape[2]
         w = j.get("norm_w")
+        if w is not None and not j.get("norm", True):
+            raise ValueError("norm_w without norm")
         a.norm, a.eps, a.rotate = bool(j.get("norm", w is not None)), j.get("eps", 1e-6), bool(j.get("rotate"))
         a.norm_w = _take("norm_w", w, torch.float32, (a.dim,), dev)
         cache, out = j.get("cache"), j.get("out")

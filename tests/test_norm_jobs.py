@@ -110,3 +110,15 @@ def test_a_slot_without_a_cache_is_refused():
     for job in (dict(x=x, slot=slot), dict(x=x, slot=slot, out=torch.empty_like(x)), dict(x=x, slot=slot, cache=None)):
         with pytest.raises(ValueError, match="slot needs cache"):
             cskv.norm_rope([job])
+
+
+@pytest.mark.gpu
+def test_norm_follows_norm_w_and_not_against_it():
+    import torch
+    import compressed_sparse_attention_kv_gb300 as cskv
+    x = torch.randn((3, 2, 512), device="cuda").to(torch.bfloat16)
+    w = torch.rand(512, device="cuda")
+    assert torch.equal(cskv.norm_rope([dict(x=x, norm_w=w)])[0], cskv.norm_rope([dict(x=x, norm_w=w, norm=True)])[0])
+    assert torch.equal(cskv.norm_rope([dict(x=x)])[0], x)
+    with pytest.raises(ValueError, match="norm_w without norm"):
+        cskv.norm_rope([dict(x=x, norm_w=w, norm=False)])
