@@ -1600,20 +1600,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) chunk_a
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
+// Blocks for a row block of few parts, a warp for each row.  The launch has as many for each share: fewer row blocks than
+// shares are cut, so that a block of the launch meets one of few parts at most, its own.
+constexpr int kJoinSets = 2 * kRows / kJoinWarps;
 
 __global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
   __shared__ float shares[kJoinWarps - 1][kD];
   grid_dep_wait();
-  constexpr int kSets = 2 * kRows / kJoinWarps;   // of a row block, where a warp has a row
   const ChunkHead head = *a.head;
-  SplitPlan sp = a.split[blockIdx.x / kSets];     // (there is room for as many; on its way beside the head)
+  SplitPlan sp = a.split[blockIdx.x / kJoinSets]; // (there is room for as many; on its way beside the head)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int few = head.few * kSets, all = few + head.many * (2 * kRows);
+  const int few = head.few * kJoinSets, all = few + head.many * (2 * kRows);
   for (int x = blockIdx.x; x < all; x += gridDim.x) {
     const bool alone = x < few;   // (the whole block)
     if (!alone) sp = a.split[a.most_blocks - 1 - (x - few) / (2 * kRows)];
-    else if (x >= gridDim.x) sp = a.split[x / kSets];
-    const int r = alone ? x % kSets * kJoinWarps + warp : (x - few) % (2 * kRows);
+    const int r = alone ? x % kJoinSets * kJoinWarps + warp : (x - few) % (2 * kRows);
     const int share = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;
     if (r >= sp.rows) continue;   // (a warp alone, or the whole block)
     auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? sp.first : sp.next + 2 * (k - 1)) * (2 * kRows) + r; };
@@ -1803,7 +1804,7 @@ cudaError_t launch_chunk_attn(const void* q, const int32_t* cu_q, const int32_t*
   static std::atomic<uint64_t> allowed;
   e = launch_next(chunk_attn_kernel, 2 * l.most_blocks, kThreads, kChunkSmemBytes, stream, &allowed, a);
   if (e != cudaSuccess || l.most_blocks == 1) return e;
-  return launch_next(chunk_join_kernel, 16 * l.most_blocks, kJoinThreads, 0, stream, nullptr, a);
+  return launch_next(chunk_join_kernel, kJoinSets * l.most_blocks, kJoinThreads, 0, stream, nullptr, a);
 }
 
 unsigned int take_err_chunk_attn() { return take_dev_err(); }
