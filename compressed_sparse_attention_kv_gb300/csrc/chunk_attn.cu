@@ -88,10 +88,12 @@ constexpr int kItemUnits = 4;
 // with 16 the same).
 constexpr int kLeastShare = 8;
 // Row blocks are dealt out whole, largest first, where the longest share is at most this many units longer than an equal
-// one: what cutting row blocks and joining their parts costs.  (Cut and whole: 455 row blocks, shares of 79 and at
-// most 80 units, 107 and 95 us; 13, 8 and 12: 27.4 and 24.2; 91, 23 and 36: 42.7 and 42.4; 58, 35 and 50: 54.5 and
-// 56.9; 246, 131 and 164: 132 and 143.)
-constexpr int kSplitCost = 15;
+// one: what cutting row blocks and joining their parts costs.  (45 calls of 2 to 640 row blocks, BF16, cut and whole: 336
+// row blocks, equal shares of 39.8 units and at most 46, 75.9 and 60.1 us; 138, 79.9 and 88: 77.7 and 76.1; 120, 44.2 and 56: 57.7
+// and 55.7; 96, 22.7 and 36: 41.3 and 41.4; 90, 22 and 36: 40.6 and 41.3; 411, 149.5 and 164: 136.1 and 142.4; 232, 61.1
+// and 80: 75.3 and 79.5.  Below 11 units' difference whole ones are shorter by up to 16 us and longer by 0.6 at most, from 14 on
+// shorter in two of 21 calls, by 2.4 at most.)
+constexpr int kSplitCost = 13;
 // Parts of a row that one warp joins; more are a block's.  (64 queries of 64 heads on 65,536 entries, two or three parts:
 // 360 us, by blocks 372; one on 262,144, seventy: 146 us, by warps 187.)
 constexpr int kFewParts = 8;
