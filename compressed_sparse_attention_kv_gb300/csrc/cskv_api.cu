@@ -172,9 +172,10 @@ bool rope_speeds(double theta, double yarn_factor, double yarn_original, double 
     auto kb = [&](double beta) {
       return kRopeDim * std::log(yarn_original / (2.0 * M_PI * beta)) / (2.0 * std::log(theta));
     };
-    const int lo = std::max(static_cast<int>(std::floor(kb(beta_fast))), 0);
-    const int hi = std::min(static_cast<int>(std::ceil(kb(beta_slow))), kPairs - 1);
-    const double span = std::max(static_cast<double>(hi - lo), 1e-3);
+    // kept in range before it becomes a whole number: a theta near 1 puts it beyond an int's
+    auto pair = [](double k) { return k > 0.0 ? std::min(k, kPairs - 1.0) : 0.0; };
+    const double lo = pair(std::floor(kb(beta_fast))), hi = pair(std::ceil(kb(beta_slow)));
+    const double span = std::max(hi - lo, 1e-3);
     for (int k = 0; k < kPairs; ++k) {
       const double ramp = std::min(std::max((k - lo) / span, 0.0), 1.0);
       f[k] = f[k] / yarn_factor * ramp + f[k] * (1.0 - ramp);
