@@ -732,9 +732,13 @@ __device__ __forceinline__ uint32_t of_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void send_to(uint32_t at, uint32_t v, uint32_t bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(at), "r"(v), "r"(bar) : "memory");
 }
-// Says that something is done: what the products read (P and the queries in their own block's shared
-// memory, tensor memory) is ordered before it by the proxy and tcgen05 fences.  With a release at
-// cluster scope, which waits for every write of the warp, a tile took 1.8 times as long.
+// Says that something is done.  Nothing that plain loads of the other block read stands behind it (those numbers
+// come by send_to): what it announces is read by the tensor core alone, P and the queries in their own
+// block's shared memory and tensor memory, behind this block's proxy and tcgen05 fences, or it frees a
+// place.  The arrival and the waits have the default scope, the block; that these fences also order what the
+// products, which the other block issues, read of this block's memory is an assumption on the
+// hardware, not a promise of the memory model.  The model's form, a release at cluster scope, waits
+// for every write of the warp: a tile took 1.8 times as long.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

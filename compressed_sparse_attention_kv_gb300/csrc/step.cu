@@ -20,10 +20,12 @@ namespace {
 // a page's place follows from its number alone: the k-th new page of the step is the k-th of the
 // ring, and the j-th page given back goes j places behind the ring's last one.  The two stretches
 // do not meet, so that blocks read and write the ring without waiting for one another.
-// Bound: latency (24 bytes a token; 262,144 tokens of 512 requests take 14.8 us, their 4.5 MB 0.7).
+// Bound: latency (24 bytes a token; 262,144 tokens of 512 requests take 14.7 us, their 4.5 MB 0.7): the chain of
+// loads, barriers and scans of one block, with which the other SMs wait.
 // One block does a small step in one launch; beyond that one block makes the sums and a launch of
-// many blocks, started meanwhile, the maps (in one launch and in two: 1 request of 1 token 5.4 and
-// 6.6 us, 64 of one 8.0 and 8.1, 64 and 1,024 tokens 9.1 and 8.7, 256 of one 16.4 and 9.5).
+// many blocks, started meanwhile, the maps (in one launch and in two: 1 request of 1 token 5.3 and
+// 6.3 us, 64 of one 7.7 and 9.2, 64 and 256 tokens 8.5 and 9.5, 64 and 1,024 9.0 and 9.5, 256 of one 15.1
+// and 10.5).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kMapThreads = 256;
@@ -102,7 +104,8 @@ __device__ __forceinline__ int bounded_len(int n) {
 }
 
 // The pages among the places [own, used) of the rows of requests that end in this round: a warp reads 512 places
-// of a row at once, 16 bytes a lane; with fewer rows than warps several warps share one.
+// of a row at once, 16 bytes a lane; with fewer rows than warps several warps share one.  (262,144 tokens of
+// 512 requests, 64 of which end with 512 places on average: 14.7 us, with 4 bytes a lane 19 to 23.)
 constexpr int kCountAtOnce = 4;          // 16-byte pieces of a lane
 constexpr int kMoveAtOnce = 8;           // places of a lane
 struct Ended {
@@ -350,11 +353,13 @@ __global__ void __launch_bounds__(kMapThreads) plan_maps_kernel(const __grid_con
 //   sin = t + (t^3 (-1/6 + t^2/120 - ...) + d),  cos = (1 - t^2/2) + (t^4 (1/24 - ...) - t d + what
 // the rounding of 1 - t^2/2 lost): Taylor polynomials to t^11 and t^12 (remainders 7e-12 and
 // 1e-12), the error below one ulp of the result.
-// Bound: instructions, about 50 for two pairs, beside 256 bytes of writes a position: 131,071 positions
-// 11.7 us (their 35 MB 5.2), with fp32 operations on two numbers at once.
+// Bound: neither memory nor issue slots.  131,071 positions take 12.0 us (their 35 MB 5.2): 58 instructions a warp
+// and position, with fp32 operations on two numbers at once, use 53 % of an SM's issue slots while it has
+// warps; at each issue as many warps wait for the arithmetic pipes (3.2) as for their positions
+// (3.0), 64 % of the warps are there, and of the 7.7 rounds of the grid the last is partly empty.
 // ---------------------------------------------------------------------------
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBlocks = 7;                   // of an SM: all are resident (36 registers a thread), none waits for a place
+constexpr int kRopeBlocks = 7;                   // of an SM: all are resident (32 registers a thread, 8 bytes of spills), none waits for a place
 constexpr int kRopeAtOnce = kRopeThreads / 16;   // positions of a block at a time: a thread has two pairs
 
 struct RopeArgs {
@@ -482,7 +487,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_cs_kernel(cons
 // agree.
 // Bound: memory, one read and one write of everything: a warp keeps its heads in registers between
 // the sum and the product.  8,192 tokens of 64 heads of 512, 64 of 128 and their rows: 1.36 GB in
-// 214 us, 6.3 TB/s, 93 % of a copy; in three resident blocks an SM (two: 228 us), with heads loaded
+// 214 us, 6.3 TB/s, 93 % of a copy; in three resident blocks an SM (two: 228 us; 80 registers, which costs 84 bytes
+// of spills a thread), with heads loaded
 // and stored as what leaves the cache first (plain: 219 us; 1,037 tokens of 20 heads 10.2 -> 8.7 us).
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;
