@@ -110,7 +110,8 @@ CSKV_API int32_t cskvs_rope_cs(const cskvs_rope_plan* plan, const int32_t* posit
  * x: heads `dim` apart, tokens x_stride apart (elements, a multiple of 8, at least H * dim);
  * out likewise with out_stride; out may be x itself (same stride).  The jobs run in no order: an
  * out that overlaps its own x otherwise, or another job's x or out, is refused (columns of one
- * buffer do not overlap), and no job's x lies in rows that the call codes.  No two tokens have
+ * buffer do not overlap; pieces of two strides in one stretch of memory are refused unless no
+ * multiples of the strides could meet), and no job's x lies in rows that the call codes.  No two tokens have
  * the same slot, nor two jobs the same row of one pool.  norm_w: fp32 [dim]; rope_cs: fp32 [T, 32, 2] (NULL: no job rotates); slot:
  * int64 [T].  dim 128 or 512, H in [1, 1024], T in [0, 2^27]; cache: any format of that dim
  * (dim 128: the index-key formats or BF16).  Alignment: x, out, norm_w, rope_cs 16 bytes.
