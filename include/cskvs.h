@@ -162,7 +162,7 @@ CSKV_API int32_t cskvs_norm_rope(const cskvs_norm_job* jobs, int32_t njobs, cons
  * is left without keys (CSKV_ERR_BOUNDS).  cskvs_chunk_attn_max_keys gives a bound that
  * always holds.  Alignment: q, out, q_rope_cs 16 bytes, workspace 256.
  * Precision as in cskvx_window_attn: the rotated query in two bf16 numbers, weights of the
- * second product in bf16 over their own sum, the rest fp32.
+ * second product in bf16 over their own sum, the rest fp32; logits up to 2^30 in magnitude.
  * ------------------------------------------------------------------------ */
 CSKV_API int64_t cskvs_chunk_attn_max_keys(int32_t R, int32_t T, int32_t max_entries, int32_t window,
                                            int32_t max_ctx_len);

@@ -21,7 +21,9 @@
  * bound is cut to it, an index outside its table or pool is skipped; both set
  * CSKV_ERR_BOUNDS on the device.  A workspace belongs to one call at a time.
  * Limits: 2^23 queries or requests of a call (65,535 requests in attn_weights and
- * evict), lengths and positions up to 2^30; softmax_scale is above 0, 1e38 at most.
+ * evict), lengths and positions up to 2^30; softmax_scale is above 0, 1e38 at most.  Logits
+ * are up to 2^30 in magnitude: above, where a rounding of fp32 is a factor of 2^64 between
+ * weights, outputs may be NaN.
  * A wait inside a kernel that runs out (cskv_set_spin_limit) ends the kernel with
  * CSKV_ERR_TIMEOUT on the device; its outputs are then not defined.
  */

@@ -51,3 +51,28 @@ def test_the_documented_step():
                 want = bounded.attend(normed[i + k], start + k, rows[b][:start + k + 1], sink_host, SCALE)
                 _check(env["out"][i + k], env["lse"][i + k], want, "token %d of request %d" % (k, b))
             i += new[b]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("length", [40, 9000])
+@pytest.mark.parametrize("logit", [1e3, 1e6, 2.0 ** 30])
+def test_logits_up_to_two_to_the_thirty(logit, length):
+    """A query that is one of its keys, +-1 in 448 dims, the logits as large as is allowed: that key alone, whole and
+    split, by both calls.  (The other products with it are sums of 448 signs, below 448 / 2: their weights are less
+    than e^-500.)"""
+    rs = np.random.default_rng(41)
+    H, hot = 3, length // 3
+    t, v = bf16_values(rs.choice([-1.0, 1.0], (length, 512)))
+    t[:, 448:] = 0                                                   # (nothing to rotate)
+    cache = cskv.PagedCache.allocate((length + 63) // 64, cskv.FMT_BF16, 512,
+                                     block_table=torch.arange((length + 63) // 64, dtype=torch.int32, device="cuda")[None])
+    cache.pool.view(torch.bfloat16).view(-1, 512)[:length] = t.cuda()
+    q = t[hot].cuda().expand(1, H, 512).contiguous()
+    cs, n = cskv.rope_cs(_i32([length - 1]), cskv.RopePlan()), _i32([length])
+    scale = logit / 448 * (1 - 2.0 ** -20)
+    for out, lse in (cskv.chunk_attn(q, _i32([0, 1]), n, cache, 1, length, length, None, scale, cs, want_lse=True),
+                     cskv.window_attn(q, cache, n, length, 0, length, None, scale, cs, want_lse=True)):
+        assert cskv.device_status() == 0
+        assert torch.equal(out, q)
+        # the logit, its product with log2(e), and back: a few roundings of fp32
+        assert float((lse.double() - logit).abs().max()) <= logit * 2.0 ** -19
